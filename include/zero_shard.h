@@ -608,6 +608,82 @@ int zero_units_slot_restore(const zero_unit_buffers_t* units_host,
                             zero_unit_buffers_t* units_dev, int32_t n_units,
                             const zero_step_result_t* dev_result, hipStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Gradient norm and clipping over a list of tensors, for gradients that are
+ * already summed: the .grad tensors of an unsharded module, fp32 gradients
+ * accumulated over micro-batches, a head's weight gradient (zero_head_grad).
+ * The norm is written as the zero_step_result_t that zero_adam_apply reads, so
+ * an accumulated fp32 gradient can go straight into the update, and
+ * zero_finalize_bf16 combines it with other ranks' shares. */
+
+enum zero_dtype { ZERO_F32 = 0, ZERO_F16 = 1, ZERO_BF16 = 2 };
+
+typedef struct zero_tensor {
+  const void* src;   /* device, numel elements, contiguous, aligned to one element */
+  void* dst;         /* device, where zero_tensors_clip writes: numel elements, aligned to one
+                        element; src itself (same dtype) or memory that does not overlap it.
+                        Not used by the norm. */
+  int64_t numel;     /* >= 0 */
+  int32_t src_dtype; /* zero_dtype */
+  int32_t dst_dtype; /* zero_dtype */
+} zero_tensor_t;
+
+/* Bytes of workspace for a list: depends on the numels alone; 0 for a bad list
+ * (negative n_tensors or numel, NULL table with n_tensors > 0). */
+size_t zero_tensors_workspace_bytes(const zero_tensor_t* tensors, int32_t n_tensors);
+
+/*
+ * zero_tensors_norm: the L2 norm over all tensors, the clip coefficient and the
+ * skip decision.  With S_i the sum of tensor i's squares (each square exact in
+ * fp64, summed in fp64 in an order fixed by the numels and types alone, so
+ * equal inputs give equal bits) and inv = 1 / loss_scale:
+ *   tensor_sq[i] = (S_i * inv) * inv
+ *   own_sq       = ((sum_i S_i) * inv) * inv;   total_sq = own_sq + other_sq
+ *   norm, clip_coef as in zero_step_result_t;   own_q = 0
+ *   overflow     = some element is inf or NaN (such elements add nothing to S)
+ *   skip         = overflow || other_overflow
+ *   tensors     host [n_tensors], read before the call returns; dst is not used
+ *   args        host; loss_scale, max_grad_norm, other_sq and other_overflow are
+ *               read, other_q must be 0
+ *   tensor_sq   device [n_tensors] fp64, 8-byte aligned, or NULL
+ *   workspace   device, >= zero_tensors_workspace_bytes, 16-byte aligned; its
+ *               content on entry does not matter
+ *   dev_result  device, 8-byte aligned; fully written
+ * n_tensors may be 0, and numels may be 0 (src is then not read).
+ * Errors: ZERO_EINVAL (a bad list, dtype or args, NULL pointers), ZERO_EALIGN,
+ * ZERO_ENOSPC (workspace), ZERO_EHIP.  Nothing is launched if a check fails.
+ */
+int zero_tensors_norm(const zero_tensor_t* tensors, int32_t n_tensors,
+                      const zero_step_args_t* args, double* tensor_sq, void* workspace,
+                      size_t ws_bytes, zero_step_result_t* dev_result, hipStream_t stream);
+
+/*
+ * zero_tensors_clip: dst = cast((src * s) * clip_coef), unless
+ * dev_result->skip (then nothing is written), with s = f32(out_scale /
+ * loss_scale); the products are fp32, each rounded once, and the cast rounds
+ * to nearest even.  out_scale = 1 gives unscaled gradients; out_scale =
+ * loss_scale keeps the loss scale on, e.g. for fp16 contribution rows that the
+ * shard step divides by it.
+ *   args        host; loss_scale is read
+ *   out_scale   > 0
+ *   dev_result  device, from zero_tensors_norm or zero_finalize_bf16
+ * Different entries must not overlap.  In place with s = clip_coef = 1 the
+ * tensor already holds the result and is left alone.
+ * Errors: as zero_tensors_norm, plus ZERO_EINVAL for out_scale or s not finite
+ * and > 0, a NULL dst, or a dst that partly overlaps its src.
+ */
+int zero_tensors_clip(const zero_tensor_t* tensors, int32_t n_tensors,
+                      const zero_step_args_t* args, double out_scale,
+                      const zero_step_result_t* dev_result, hipStream_t stream);
+
+/* zero_tensors_norm_clip: zero_tensors_norm then zero_tensors_clip on the same
+ * stream, with no host synchronisation; nothing is launched if any check of
+ * the two fails. */
+int zero_tensors_norm_clip(const zero_tensor_t* tensors, int32_t n_tensors,
+                           const zero_step_args_t* args, double out_scale, double* tensor_sq,
+                           void* workspace, size_t ws_bytes, zero_step_result_t* dev_result,
+                           hipStream_t stream);
+
 typedef struct zero_scaler {
   double scale;            /* current loss scale */
   double growth, backoff;  /* e.g. 2.0 and 0.5 */

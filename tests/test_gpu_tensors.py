@@ -1,0 +1,296 @@
+"""Gradient norm and clip over tensor lists (zero_tensors_*) on the GPU,
+against exact sums (math.fsum of exact squares) and against the same products
+in fp32 on the CPU.
+
+Tolerances.  Squares are exact in fp64.  A sum of non-negative terms whose
+longest chain of additions is L has relative error at most L * 2^-53 (to first
+order); a thread adds at most chunk / 256 squares of a chunk (64 chunks'
+worth of doubling never occurs at these sizes: 64 for 16384 elements plus one
+for the tail), 8 more in the workgroup's tree, chunks / 256 + 8 for the
+tensor, n / 256 + 8 for the list.  Below, L <= 256 for every case here, plus
+two roundings for the scaling: 258 * 2^-53 < 2^-44.  The norm's root halves
+that and rounds once.  The clip's products and casts are single IEEE
+roundings, so they must match bit for bit.
+"""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+REL = 2.0 ** -44
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+SIZES = [0, 1, 3, 7, 8, 9, 255, 2053, 16384, 16385, 300_001, 0, 64]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _lists():
+    from zero_sharded_optimizer_rank_amd.tensors import GradList
+    return GradList
+
+
+def _make(sizes, dtypes, seed=0, sigma=1e-2, shift=0):
+    """CPU values and their GPU copies, each starting `shift` elements into its buffer."""
+    g = torch.Generator().manual_seed(seed)
+    cpu, gpu = [], []
+    for i, n in enumerate(sizes):
+        dt = dtypes[i % len(dtypes)]
+        x = (torch.randn(n, generator=g) * sigma).to(dt)
+        buf = torch.full((n + 16,), 7.0, dtype=dt, device="cuda")
+        v = buf[shift:shift + n]
+        v.copy_(x)
+        cpu.append(x)
+        gpu.append(v)
+    return cpu, gpu
+
+
+def _exact_squares(cpu):
+    return [math.fsum((x.double() * x.double()).tolist()) for x in cpu]
+
+
+def _close(got, want, rel=REL):
+    assert abs(got - want) <= rel * abs(want), (got, want)
+
+
+def _coef(norm, max_norm):
+    return min(1.0, max_norm / (norm + 1e-6)) if max_norm > 0 else 1.0
+
+
+def _f32(x):
+    return float(torch.tensor(x, dtype=torch.float64).float())
+
+
+@pytest.mark.parametrize("dtypes", [[t] for t in TYPES] + [TYPES],
+                         ids=["f32", "f16", "bf16", "mixed"])
+@pytest.mark.parametrize("shift", [0, 1, 3])
+def test_norm(dtypes, shift):
+    cpu, gpu = _make(SIZES, dtypes, seed=1, shift=shift)
+    scale = 3.0
+    r = _lists()(gpu).norm(max_grad_norm=0.5, loss_scale=scale)
+    sq = _exact_squares(cpu)
+    for i, (got, s) in enumerate(zip(r.tensor_sq.tolist(), sq)):
+        _close(got, s / scale / scale)
+    total = math.fsum(sq) / scale / scale
+    _close(r.own_sq.item(), total)
+    _close(r.total_sq.item(), total)
+    _close(r.norm.item(), math.sqrt(total))
+    assert r.clip_coef.item() == _f32(_coef(r.norm.item(), 0.5))
+    assert r.overflow.item() == 0 and r.skip.item() == 0
+
+
+def test_bits_do_not_depend_on_address_or_call():
+    cpu, a = _make(SIZES, TYPES, seed=2, shift=0)
+    _, b = _make(SIZES, TYPES, seed=2, shift=5)
+    la, lb = _lists()(a), _lists()(b)
+    want = la.norm().tensor_sq.clone()
+    lb.ws.fill_(0xA5)  # the workspace's content on entry does not matter
+    for _ in range(3):
+        assert torch.equal(la.norm().tensor_sq, want)
+        assert torch.equal(lb.norm().tensor_sq, want)
+
+
+@pytest.mark.parametrize("n", [1, 136, 137, 192, 193, 500])
+def test_many_tensors(n):
+    """Lists that fill one launch's table, spill over it, and take several."""
+    sizes = [(7 * i) % 61 for i in range(n)]
+    cpu, gpu = _make(sizes, TYPES, seed=3, sigma=1.0)
+    out = [torch.empty_like(t) for t in gpu]
+    r = _lists()(gpu, out=out).norm_clip(max_grad_norm=1.0)
+    sq = _exact_squares(cpu)
+    for got, s in zip(r.tensor_sq.tolist(), sq):
+        _close(got, s)
+    _close(r.own_sq.item(), math.fsum(sq))
+    c = torch.tensor(r.clip_coef.item())
+    for x, y in zip(cpu, out):
+        assert torch.equal(y.cpu(), ((x.float() * 1.0) * c).to(y.dtype))
+
+
+@pytest.mark.parametrize("sd", TYPES)
+@pytest.mark.parametrize("dd", TYPES)
+@pytest.mark.parametrize("shift", [0, 1])
+def test_clip_matches_single_roundings(sd, dd, shift):
+    cpu, gpu = _make(SIZES, [sd], seed=4, shift=shift)
+    outs, bufs = [], []
+    for n in SIZES:
+        b = torch.full((n + 16,), 5.0, dtype=dd, device="cuda")
+        bufs.append(b)
+        outs.append(b[2 + shift:2 + shift + n])
+    r = _lists()(gpu, out=outs).norm_clip(max_grad_norm=0.25, loss_scale=7.0, out_scale=64.0)
+    c = torch.tensor(r.clip_coef.item())
+    assert c < 1
+    s = torch.tensor(_f32(64.0 / 7.0))
+    for x, y, b, n in zip(cpu, outs, bufs, SIZES):
+        assert torch.equal(y.cpu(), ((x.float() * s) * c).to(dd))
+        b = b.cpu()
+        assert (b[:2 + shift] == 5).all() and (b[2 + shift + n:] == 5).all()
+    for x, t in zip(cpu, gpu):  # sources are left as they were
+        assert torch.equal(t.cpu(), x)
+
+
+def test_clip_in_place():
+    cpu, gpu = _make(SIZES, TYPES, seed=5)
+    r = _lists()(gpu).norm_clip(max_grad_norm=0.25)
+    c = torch.tensor(r.clip_coef.item())
+    for x, t in zip(cpu, gpu):
+        assert torch.equal(t.cpu(), ((x.float() * 1.0) * c).to(x.dtype))
+    # nothing to clip: the tensors keep their bits
+    cpu, gpu = _make(SIZES, TYPES, seed=6)
+    assert _lists()(gpu).norm_clip(max_grad_norm=1e9).clip_coef.item() == 1.0
+    for x, t in zip(cpu, gpu):
+        assert torch.equal(t.cpu(), x)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("where", [(6, 0), (10, 299_999), (10, 300_000), (2, 2)])
+def test_non_finite(dtype, value, where):
+    cpu, gpu = _make(SIZES, [dtype], seed=7)
+    i, j = where
+    if j >= SIZES[i]:
+        j = SIZES[i] - 1
+    gpu[i][j] = value
+    cpu[i][j] = 0.0
+    out = [torch.full_like(t, 3.0) for t in gpu]
+    r = _lists()(gpu, out=out).norm_clip(max_grad_norm=0.25)
+    assert r.overflow.item() == 1 and r.skip.item() == 1
+    for got, s in zip(r.tensor_sq.tolist(), _exact_squares(cpu)):
+        _close(got, s)
+    assert all((o == 3.0).all() for o in out)  # a skipped step writes nothing
+
+
+def test_extreme_magnitudes():
+    """The largest and the smallest values of each type neither overflow nor vanish."""
+    for dt in TYPES:
+        info = torch.finfo(dt)
+        for v in (info.max, info.tiny, info.smallest_normal * info.eps):
+            x = torch.full((5000,), v, dtype=torch.float64).to(dt)
+            r = _lists()([x.cuda()]).norm()
+            e = float(x[0])
+            want = 5000 * (e * e)
+            assert r.overflow.item() == 0
+            if want > 0:
+                _close(r.own_sq.item(), want)
+                _close(r.norm.item(), math.sqrt(want))
+
+
+def test_empty_lists():
+    r = _lists()([], device="cuda:0").norm_clip(max_grad_norm=1.0, other_sq=9.0)
+    assert r.norm.item() == 3.0 and r.own_sq.item() == 0.0
+    z = [torch.empty(0, device="cuda") for _ in range(3)]
+    r = _lists()(z).norm_clip(max_grad_norm=1.0)
+    assert r.norm.item() == 0.0 and r.clip_coef.item() == 1.0 and r.tensor_sq.tolist() == [0.0] * 3
+
+
+def test_other_ranks_share():
+    from zero_sharded_optimizer_rank_amd import abi
+    cpu, gpu = _make(SIZES, TYPES, seed=8)
+    lst = _lists()(gpu)
+    own = lst.norm(max_grad_norm=1.0).own_sq.item()
+    r = lst.norm(max_grad_norm=1.0, other_sq=25.0)
+    _close(r.total_sq.item(), own + 25.0)
+    assert lst.norm(other_overflow=True).skip.item() == 1
+    assert r.overflow.item() == 0
+    # the exchange after the fact: zero_finalize_bf16 keeps own_sq
+    lst.norm(max_grad_norm=1.0)
+    plan = abi.zero_plan_t(0, 1, 1, 0, 0)
+    abi.zero_finalize_bf16(plan, lst.args(1.0, 1.0, other_sq=25.0), lst.res,
+                           torch.cuda.current_stream())
+    assert r.own_sq.item() == own
+    _close(r.total_sq.item(), own + 25.0)
+    assert r.clip_coef.item() == _f32(1.0 / (r.norm.item() + 1e-6))
+
+
+def test_long_tensor():
+    """Offsets past 2^32 elements: ones at the ends of a tensor of zeros."""
+    n = (1 << 32) + 12_345
+    x = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    x[0] = 2.0
+    x[1 << 32] = 3.0
+    x[n - 1] = 6.0
+    r = _lists()([x]).norm_clip(max_grad_norm=3.5)
+    assert r.own_sq.item() == 49.0 and r.norm.item() == 7.0
+    c = _f32(3.5 / (7.0 + 1e-6))
+    want = (torch.tensor([2.0, 3.0, 6.0]) * torch.tensor(c)).to(torch.bfloat16)
+    assert torch.equal(x[torch.tensor([0, 1 << 32, n - 1], device="cuda")].cpu(), want)
+    assert int(torch.count_nonzero(x[:1 << 31])) == 1
+    del x
+    torch.cuda.empty_cache()
+
+
+def test_graph_replays():
+    """Captured once, replayed on changing inputs with eager work in between."""
+    cpu, gpu = _make(SIZES, TYPES, seed=9)
+    out = [torch.empty_like(t) for t in gpu]
+    lst = _lists()(gpu, out=out)
+    lst.norm_clip(max_grad_norm=0.25)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        lst.norm_clip(max_grad_norm=0.25)
+    for k in range(4):
+        cpu, fresh = _make(SIZES, TYPES, seed=20 + k)
+        for t, f in zip(gpu, fresh):
+            t.copy_(f)
+        eager = _lists()(fresh, out=[torch.empty_like(t) for t in fresh])
+        want = eager.norm_clip(max_grad_norm=0.25)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(lst.res, eager.res)
+        assert torch.equal(lst.result.tensor_sq, want.tensor_sq)
+        for a, b in zip(out, eager.out):
+            assert torch.equal(a, b)
+
+
+def test_two_lists_on_two_streams():
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    cpu, gpu = zip(*[_make([200_003, 17, 900_001], TYPES, seed=30 + k) for k in range(2)])
+    lists = [_lists()(g) for g in gpu]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for lst, s in zip(lists, streams):
+            lst.norm(loss_scale=2.0, stream=s)
+    torch.cuda.synchronize()
+    for lst, c in zip(lists, cpu):
+        _close(lst.result.own_sq.item(), math.fsum(_exact_squares(c)) / 4.0)
+
+
+def test_accumulated_gradient_into_the_update():
+    """fp32 gradients accumulated over micro-batches go from zero_tensors_norm straight into
+    zero_adam_apply: the update equals the one after zero_reduce_check of a single row that
+    holds the same gradient (fp16-exact values, so both see equal g)."""
+    from zero_sharded_optimizer_rank_amd import abi
+    n = 70_001
+    g = torch.Generator().manual_seed(11)
+    grad16 = (torch.randn(n, generator=g) * 4).half().cuda()
+    plan, _ = abi.zero_plan([n], 1)
+    st = torch.cuda.current_stream()
+    args = abi.step_args(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1,
+                         max_grad_norm=1.0, loss_scale=1.0, step=1)
+    master0 = torch.randn(n, generator=g).cuda()
+    ends = []
+    for path in ("row", "list"):
+        master, m, v = master0.clone(), torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+        slot = torch.zeros(n, dtype=torch.float16, device="cuda")
+        if path == "row":
+            grad = torch.empty(n, device="cuda")
+            ws = torch.empty(abi.zero_workspace_bytes(plan), dtype=torch.uint8, device="cuda")
+            res = torch.zeros(abi.RESULT_BYTES, dtype=torch.uint8, device="cuda")
+            abi.zero_reduce_check(plan, 0, [grad16], args, grad, ws, ws.numel(), res, st)
+        else:
+            grad = grad16.float()
+            lst = _lists()([grad])
+            lst.norm(max_grad_norm=1.0)
+            res = lst.res
+        abi.zero_adam_apply(plan, 0, grad, master, m, v, slot, args, res, st)
+        ends.append((master, m, v, slot, res.view(torch.float32)[10].clone()))
+    assert ends[0][4].item() == ends[1][4].item() < 1.0
+    for a, b in zip(ends[0], ends[1]):
+        assert torch.equal(a, b)

@@ -20,6 +20,7 @@ ZERO_OK, ZERO_EINVAL, ZERO_EALIGN, ZERO_ENOSPC, ZERO_EHIP = 0, -1, -2, -3, -4
 ZERO_MAX_RANKS = 64
 ZERO_MAX_SHARD = 0x7FFFFFF8
 ZERO_NOALLOC_MAX_SHARD = 9 << 27
+ZERO_F32, ZERO_F16, ZERO_BF16 = 0, 1, 2
 
 
 class ZeroError(RuntimeError):
@@ -84,6 +85,11 @@ class zero_unit_buffers_t(ctypes.Structure):
                 ("master", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("param16", ctypes.c_void_p), ("shard", ctypes.c_int64),
                 ("reduce_block", ctypes.c_int64), ("adam_block", ctypes.c_int64)]
+
+
+class zero_tensor_t(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("src_dtype", ctypes.c_int32), ("dst_dtype", ctypes.c_int32)]
 
 
 class zero_offload_staging_t(ctypes.Structure):
@@ -172,6 +178,14 @@ _SIGNATURES = {
                                              _vp]),
     "zero_units_slot_restore": (ctypes.c_int, [_P(zero_unit_buffers_t), _vp, ctypes.c_int32,
                                                _vp, _vp]),
+    "zero_tensors_workspace_bytes": (ctypes.c_size_t, [_P(zero_tensor_t), ctypes.c_int32]),
+    "zero_tensors_norm": (ctypes.c_int, [_P(zero_tensor_t), ctypes.c_int32, _P(zero_step_args_t),
+                                         _vp, _vp, ctypes.c_size_t, _vp, _vp]),
+    "zero_tensors_clip": (ctypes.c_int, [_P(zero_tensor_t), ctypes.c_int32, _P(zero_step_args_t),
+                                         ctypes.c_double, _vp, _vp]),
+    "zero_tensors_norm_clip": (ctypes.c_int, [_P(zero_tensor_t), ctypes.c_int32,
+                                              _P(zero_step_args_t), ctypes.c_double, _vp, _vp,
+                                              ctypes.c_size_t, _vp, _vp]),
     "zero_scaler_update": (ctypes.c_int, [_P(zero_scaler_t), ctypes.c_int32]),
     "zero_last_error": (ctypes.c_char_p, []),
 }
@@ -476,3 +490,35 @@ def new_scaler(scale: float, growth: float = 2.0, backoff: float = 0.5, min_scal
 def zero_scaler_update(s: zero_scaler_t, skipped: bool) -> zero_scaler_t:
     _check(lib().zero_scaler_update(ctypes.byref(s), 1 if skipped else 0))
     return s
+
+
+def tensor_table(entries):
+    """Table of zero_tensor_t from (src, src_dtype, dst, dst_dtype, numel) tuples; dst may be
+    None for a list that is only measured."""
+    t = (zero_tensor_t * max(len(entries), 1))()
+    for i, (src, sd, dst, dd, numel) in enumerate(entries):
+        t[i] = zero_tensor_t(_addr(src), _addr(dst), numel, sd, dd)
+    return t
+
+
+def zero_tensors_workspace_bytes(tensors, n_tensors: int) -> int:
+    return int(lib().zero_tensors_workspace_bytes(tensors, n_tensors))
+
+
+def zero_tensors_norm(tensors, n_tensors, args, tensor_sq, workspace, ws_bytes, dev_result,
+                      stream=None):
+    _check(lib().zero_tensors_norm(tensors, n_tensors, ctypes.byref(args), _addr(tensor_sq),
+                                   _addr(workspace), ws_bytes, _addr(dev_result),
+                                   _stream(stream)))
+
+
+def zero_tensors_clip(tensors, n_tensors, args, out_scale, dev_result, stream=None):
+    _check(lib().zero_tensors_clip(tensors, n_tensors, ctypes.byref(args), out_scale,
+                                   _addr(dev_result), _stream(stream)))
+
+
+def zero_tensors_norm_clip(tensors, n_tensors, args, out_scale, tensor_sq, workspace, ws_bytes,
+                           dev_result, stream=None):
+    _check(lib().zero_tensors_norm_clip(tensors, n_tensors, ctypes.byref(args), out_scale,
+                                        _addr(tensor_sq), _addr(workspace), ws_bytes,
+                                        _addr(dev_result), _stream(stream)))

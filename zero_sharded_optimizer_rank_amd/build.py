@@ -30,6 +30,10 @@ DEVICE_FLAGS = [
     f"--offload-arch={ARCH}",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
+DEVICE_SOURCES = ("zero_kernels.hip", "zero_units.hip", "zero_noalloc.hip", "zero_tensors.hip")
+HOST_SOURCES = ("zero_host.cpp", "zero_offload.cpp", "zero_tensors.cpp")
+# host Adam of the offload form: IEEE fp32, no contraction, errno-free sqrt
+HOST_FLAGS = {"zero_offload.cpp": ["-ffp-contract=off", "-fno-math-errno", "-pthread"]}
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-I", INCLUDE, "-I", CSRC]
 
 
@@ -40,25 +44,17 @@ def _run(cmd):
 
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    kobj = os.path.join(BUILD_DIR, "zero_kernels.o")
-    uobj = os.path.join(BUILD_DIR, "zero_units.o")
-    nobj = os.path.join(BUILD_DIR, "zero_noalloc.o")
-    hobj = os.path.join(BUILD_DIR, "zero_host.o")
-    oobj = os.path.join(BUILD_DIR, "zero_offload.o")
-    _run([HIPCC, "-x", "hip", *COMMON, *FP_FLAGS, *DEVICE_FLAGS, "-c",
-          os.path.join(CSRC, "zero_kernels.hip"), "-o", kobj])
-    _run([HIPCC, "-x", "hip", *COMMON, *FP_FLAGS, *DEVICE_FLAGS, "-c",
-          os.path.join(CSRC, "zero_units.hip"), "-o", uobj])
-    _run([HIPCC, "-x", "hip", *COMMON, *FP_FLAGS, *DEVICE_FLAGS, "-c",
-          os.path.join(CSRC, "zero_noalloc.hip"), "-o", nobj])
-    _run([HIPCC, *COMMON, "-ffp-contract=off", "-c", os.path.join(CSRC, "zero_host.cpp"),
-          "-o", hobj])
-    # host Adam of the offload form: IEEE fp32, no contraction, errno-free sqrt
-    _run([HIPCC, *COMMON, "-ffp-contract=off", "-fno-math-errno", "-pthread", "-c",
-          os.path.join(CSRC, "zero_offload.cpp"), "-o", oobj])
+    objs = []
+    for src in DEVICE_SOURCES:
+        objs.append(os.path.join(BUILD_DIR, src + ".o"))
+        _run([HIPCC, "-x", "hip", *COMMON, *FP_FLAGS, *DEVICE_FLAGS, "-c",
+              os.path.join(CSRC, src), "-o", objs[-1]])
+    for src in HOST_SOURCES:
+        objs.append(os.path.join(BUILD_DIR, src + ".o"))
+        _run([HIPCC, *COMMON, *HOST_FLAGS.get(src, ["-ffp-contract=off"]), "-c",
+              os.path.join(CSRC, src), "-o", objs[-1]])
     tmp = LIB + ".tmp"
-    _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-pthread", kobj, uobj, nobj, hobj, oobj,
-          "-o", tmp])
+    _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-pthread", *objs, "-o", tmp])
     os.replace(tmp, LIB)
     # measurement-only copy kernel, in a library of its own
     tmp = CALIB_LIB + ".tmp"
@@ -106,12 +102,11 @@ def build_host_sanitized(kind: str) -> dict:
            "-fno-math-errno", "-D__HIP_PLATFORM_AMD__", "-I", "/opt/rocm/include", "-I", INCLUDE,
            "-I", CSRC, *flags]
     objs = []
-    for src in ("zero_host.cpp", "zero_offload.cpp"):
-        o = os.path.join(out, src.replace(".cpp", ".o"))
+    for src in HOST_SOURCES:
+        o = os.path.join(out, src + ".o")
         _run([*gxx, "-c", os.path.join(CSRC, src), "-o", o])
         objs.append(o)
-    kobjs = [os.path.join(BUILD_DIR, f) for f in ("zero_kernels.o", "zero_units.o",
-                                                  "zero_noalloc.o")]
+    kobjs = [os.path.join(BUILD_DIR, f + ".o") for f in DEVICE_SOURCES]
     if not all(os.path.exists(k) for k in kobjs):
         build()
     link = ["-L/opt/rocm/lib", "-Wl,-rpath,/opt/rocm/lib", "-lamdhip64"]

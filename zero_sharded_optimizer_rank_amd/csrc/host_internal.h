@@ -15,6 +15,7 @@ extern thread_local char g_err[512];
 // Record a printf-style message for zero_last_error and return `code`.
 int fail(int code, const char* fmt, ...);
 bool aligned(const void* p, uintptr_t a);
+bool overlap(const void* a, size_t na, const void* b, size_t nb);  // a byte in common
 int check_plan_rank(const zero_plan_t* plan, int32_t rank);
 int check_norm_args(const zero_step_args_t* a);
 int check_adam_args(const zero_step_args_t* a);

@@ -26,6 +26,11 @@ int fail(int code, const char* fmt, ...) {
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + nb && y < x + na;
+}
+
 // Checks shared by the device entry points.
 int check_plan_rank(const zero_plan_t* plan, int32_t rank) {
   if (!plan) return fail(ZERO_EINVAL, "plan is NULL");
@@ -296,12 +301,6 @@ int zero_reduce_adam_step(const zero_plan_t* plan, int32_t rank, const uint16_t*
   if (rc || args->other_overflow) return rc;
   return zero_adam_apply(plan, rank, grad_out, master, m, v, param16_slot, args, dev_result,
                          stream);
-}
-
-// [a, a + na) and [b, b + nb) share a byte.
-static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return x < y + nb && y < x + na;
 }
 
 // Checks of the single-pass calls: no clipping, reduce inputs, state

@@ -1,0 +1,365 @@
+// Gradient norm and clip over a list of tensors.
+//
+// Norm: S_i = sum_j x_ij^2 for every tensor, the total, its root and the clip
+// coefficient; one read of every element, so the bound is HBM.  A square of an
+// fp32 (or 16-bit) value is exact in fp64 and the sums are fp64, so neither
+// the length of the list nor the range of bf16 costs digits; the fp64 work is
+// one conversion and one fused multiply-add an element, well under what the
+// vector units do in the time the element takes to arrive.  The list travels
+// in the kernel arguments, kNormBatch tensors a launch: gradient tensors move
+// from step to step, and a table in device memory would cost a copy each time.
+//
+// The sums keep one order: chunk by chunk, thread t of a chunk's workgroup
+// takes its 16-byte pieces t, t + T, ... in turn, the workgroup's threads are
+// added in a fixed tree, a tensor's chunks and then the tensors likewise.
+// Pieces are counted from the tensor's start whatever its address, so two
+// tensors with equal values have equal sums.
+//
+// Clip: y = cast((x * s) * c), one read and one write of every element.
+#include <stddef.h>
+
+#include "tensors_internal.h"
+#include "zero_device.h"
+
+namespace zk {
+namespace {
+
+using namespace dev;
+
+constexpr int kNormThreads = 256;
+constexpr int kClipThreads = 256;
+constexpr int64_t kClipChunk = 8192;  // elements a clip workgroup takes
+// Entries that fit the 4 KiB of kernel arguments beside the other arguments.
+constexpr int kNormBatch = 192;
+constexpr int kClipBatch = 136;
+constexpr int kDtypeShift = 60;  // a numel's top bits hold the type(s)
+
+struct NormBatch {
+  const void* src[kNormBatch];
+  uint64_t numel[kNormBatch];   // | dtype << kDtypeShift
+  uint32_t first[kNormBatch];   // first chunk of the tensor within this launch
+};
+struct ClipBatch {
+  const void* src[kClipBatch];
+  void* dst[kClipBatch];
+  uint64_t numel[kClipBatch];   // | (src dtype | dst dtype << 2) << kDtypeShift
+  uint32_t first[kClipBatch];
+};
+static_assert(sizeof(NormBatch) <= 3904 && sizeof(ClipBatch) <= 3904, "kernel arguments");
+
+struct TensorRecord {
+  int64_t first;  // first chunk of the tensor in the whole list
+  int64_t chunks;
+};
+
+// 16 bytes at any element's address: global loads and stores need no more
+// than element alignment on gfx950.
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+// Pointers out of the argument table are generic; typed as global memory the
+// accesses need not wait on both memory counters.
+template <typename T>
+using gptr = __attribute__((address_space(1))) T*;
+__device__ __forceinline__ u32x4 load16(const char* p) {
+  return __builtin_nontemporal_load((gptr<const u32x4_a2>)p);
+}
+__device__ __forceinline__ void store16(u32x4 v, char* p) {
+  __builtin_nontemporal_store(v, (gptr<u32x4_a2>)p);
+}
+
+template <int D>
+__device__ __forceinline__ constexpr int per16() { return D == ZERO_F32 ? 4 : 8; }
+
+// Element e of a 16-byte piece, and one element in memory.
+template <int D>
+__device__ __forceinline__ float piece_elem(u32x4 v, int e) {
+  if constexpr (D == ZERO_F32) return __uint_as_float(v[e]);
+  else return to_f32<D == ZERO_BF16 ? Fmt::BF16 : Fmt::F16>((v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+}
+template <int D>
+__device__ __forceinline__ float load_elem(const void* p, int64_t i) {
+  if constexpr (D == ZERO_F32) return ((gptr<const float>)p)[i];
+  else return to_f32<D == ZERO_BF16 ? Fmt::BF16 : Fmt::F16>(((gptr<const uint16_t>)p)[i]);
+}
+template <int D>
+__device__ __forceinline__ void store_elem(void* p, int64_t i, float x) {
+  if constexpr (D == ZERO_F32) ((gptr<float>)p)[i] = x;
+  else ((gptr<uint16_t>)p)[i] = (uint16_t)from_f32<D == ZERO_BF16 ? Fmt::BF16 : Fmt::F16>(x);
+}
+
+// Largest i < n with first[i] <= b (n >= 1, first[0] = 0).
+__device__ __forceinline__ int find_tensor(const uint32_t* first, int n, uint32_t b) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= b) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Sum of one thread's squares over elements [0, len) of a chunk.  FINITE: inf
+// and NaN count zero and set bad.
+template <int D, bool FINITE>
+__device__ __forceinline__ double chunk_squares(const void* base, int64_t at, int64_t len,
+                                                uint32_t& bad) {
+  constexpr int E = per16<D>(), U = 4;
+  const char* p = (const char*)base + at * (D == ZERO_F32 ? 4 : 2);
+  const int64_t pieces = len / E;
+  double s = 0.0;
+  auto add = [&](float x) {
+    if constexpr (FINITE) s += sq_or_zero(x, bad);
+    else s = __builtin_fma((double)x, (double)x, s);
+  };
+  int64_t i = threadIdx.x;
+  for (; i + (U - 1) * kNormThreads < pieces; i += U * kNormThreads) {
+    u32x4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      v[u] = load16(p + 16 * (i + u * kNormThreads));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e) add(piece_elem<D>(v[u], e));
+  }
+  for (; i < pieces; i += kNormThreads) {
+    const u32x4 v = load16(p + 16 * i);
+#pragma unroll
+    for (int e = 0; e < E; ++e) add(piece_elem<D>(v, e));
+  }
+  const int64_t j = pieces * E + threadIdx.x;
+  if (j < len) add(load_elem<D>(base, at + j));
+  return s;
+}
+
+template <int D>
+__device__ __forceinline__ double chunk_sum(const void* base, int64_t at, int64_t len,
+                                            uint32_t& bad) {
+  double s = chunk_squares<D, false>(base, at, len, bad);
+  // finite elements cannot overflow fp64: a sum that is not finite has met an
+  // inf or NaN, and is taken again without them
+  if (!__builtin_isfinite(s)) s = chunk_squares<D, true>(base, at, len, bad);
+  return s;
+}
+
+__global__ __launch_bounds__(kNormThreads) void k_tensors_norm(
+    NormBatch nb, int32_t n, int32_t t0, int64_t chunk0, int64_t chunk, int32_t arm,
+    TensorRecord* __restrict__ records, Partial* __restrict__ partials,
+    uint32_t* __restrict__ ticket) {
+  const uint32_t b = blockIdx.x;
+  if (arm && b == 0 && threadIdx.x == 0) *ticket = 0u;
+  const int i = find_tensor(nb.first, n, b);
+  const int64_t numel = (int64_t)(nb.numel[i] & ((1ull << kDtypeShift) - 1));
+  const int dtype = (int)(nb.numel[i] >> kDtypeShift);
+  const int64_t c = (int64_t)(b - nb.first[i]), at = c * chunk;
+  const int64_t len = numel - at < chunk ? numel - at : chunk;
+  if (c == 0 && threadIdx.x == 0)
+    records[t0 + i] = TensorRecord{chunk0 + nb.first[i], numel ? (numel - 1) / chunk + 1 : 1};
+  uint32_t bad = 0;
+  double s;
+  if (dtype == ZERO_F32) s = chunk_sum<ZERO_F32>(nb.src[i], at, len, bad);
+  else if (dtype == ZERO_F16) s = chunk_sum<ZERO_F16>(nb.src[i], at, len, bad);
+  else s = chunk_sum<ZERO_BF16>(nb.src[i], at, len, bad);
+  block_tree<kNormThreads>(s, bad);
+  if (threadIdx.x == 0)
+    partials[chunk0 + b] = Partial{(uint64_t)__double_as_longlong(s),
+                                   (uint64_t)(bad ? 1u : 0u) << 63};
+}
+
+// Thread t's share of values t, t + T, ... of get(0..count).
+template <typename Get>
+__device__ __forceinline__ void strided_sum(int64_t count, double& x, uint32_t& bad, Get get) {
+  x = 0.0;
+  bad = 0;
+  for (int64_t j = threadIdx.x; j < count; j += kNormThreads) {
+    const Partial pt = get(j);
+    x += __longlong_as_double((long long)pt.lo);
+    bad |= (uint32_t)(pt.hi >> 63);
+  }
+}
+
+// Workgroup i sums tensor i's partials; the last one to finish (ticket) sums
+// the tensors and finalizes.
+__global__ __launch_bounds__(kNormThreads) void k_tensors_finalize(
+    const Partial* __restrict__ partials, const TensorRecord* __restrict__ records,
+    Partial* __restrict__ sums, int32_t n, double* __restrict__ tensor_sq,
+    uint32_t* __restrict__ ticket, FinalizeArgs fa, zero_step_result_t* __restrict__ res) {
+  __shared__ uint32_t s_last;
+  double x = 0.0;
+  uint32_t bad = 0;
+  if (n > 0) {
+    const TensorRecord r = records[blockIdx.x];
+    strided_sum(r.chunks, x, bad, [&](int64_t j) { return partials[r.first + j]; });
+    block_tree<kNormThreads>(x, bad);
+    if (threadIdx.x == 0) {
+      if (tensor_sq) tensor_sq[blockIdx.x] = (x * fa.inv64) * fa.inv64;
+      s_last = 1u;
+      if (n > 1) {
+        sums[blockIdx.x] = Partial{(uint64_t)__double_as_longlong(x),
+                                   (uint64_t)(bad ? 1u : 0u) << 63};
+        __threadfence();
+        s_last = atomicAdd(ticket, 1u) == (uint32_t)n - 1 ? 1u : 0u;
+      }
+    }
+    __syncthreads();
+    if (!s_last) return;
+    if (n > 1) {
+      __threadfence();
+      strided_sum(n, x, bad, [&](int64_t j) { return sums[j]; });
+      block_tree<kNormThreads>(x, bad);
+    }
+  }
+  if (threadIdx.x == 0) finalize_bf16_into(x, bad, fa, res);
+}
+
+// (x * s) * c, each product rounded to fp32.  The barrier keeps the second
+// product apart from the cast: the compiler would otherwise fold both into the
+// mixed-precision multiply, whose fp16 result skips the fp32 rounding.
+__device__ __forceinline__ float clipped(float x, float s, float c) {
+  float y = (x * s) * c;
+  asm volatile("" : "+v"(y));
+  return y;
+}
+
+// One clip workgroup's elements [at, at + len) of a tensor.
+template <int SD, int DD>
+__device__ __forceinline__ void clip_chunk(const void* src, void* dst, int64_t at, int64_t len,
+                                           float s, float c) {
+  // a piece is 8 elements: 16 bytes of a 16-bit side, two 16-byte halves of an
+  // fp32 side
+  const int64_t pieces = len >> 3;
+  const char* ps = (const char*)src + at * (SD == ZERO_F32 ? 4 : 2);
+  char* pd = (char*)dst + at * (DD == ZERO_F32 ? 4 : 2);
+  for (int64_t i = threadIdx.x; i < pieces; i += kClipThreads) {
+    float x[8];
+    if constexpr (SD == ZERO_F32) {
+      const u32x4 a = load16(ps + 32 * i);
+      const u32x4 b = load16(ps + 32 * i + 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = __uint_as_float(a[e]);
+        x[4 + e] = __uint_as_float(b[e]);
+      }
+    } else {
+      const u32x4 a = load16(ps + 16 * i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = piece_elem<SD>(a, e);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = clipped(x[e], s, c);
+    if constexpr (DD == ZERO_F32) {
+      u32x4 a, b;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a[e] = __float_as_uint(x[e]);
+        b[e] = __float_as_uint(x[4 + e]);
+      }
+      store16(a, pd + 32 * i);
+      store16(b, pd + 32 * i + 16);
+    } else {
+      constexpr Fmt F = DD == ZERO_BF16 ? Fmt::BF16 : Fmt::F16;
+      u32x4 a;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] = from_f32<F>(x[2 * e]) | (from_f32<F>(x[2 * e + 1]) << 16);
+      store16(a, pd + 16 * i);
+    }
+  }
+  const int64_t j = (pieces << 3) + threadIdx.x;
+  if (j < len) store_elem<DD>(dst, at + j, clipped(load_elem<SD>(src, at + j), s, c));
+}
+
+template <int SD>
+__device__ __forceinline__ void clip_to(int dd, const void* src, void* dst, int64_t at,
+                                        int64_t len, float s, float c) {
+  if (dd == ZERO_F32) clip_chunk<SD, ZERO_F32>(src, dst, at, len, s, c);
+  else if (dd == ZERO_F16) clip_chunk<SD, ZERO_F16>(src, dst, at, len, s, c);
+  else clip_chunk<SD, ZERO_BF16>(src, dst, at, len, s, c);
+}
+
+__global__ __launch_bounds__(kClipThreads) void k_tensors_clip(
+    ClipBatch cb, int32_t n, uint32_t b0, float s, const zero_step_result_t* __restrict__ res) {
+  if (res->skip) return;
+  const float c = res->clip_coef;
+  const uint32_t b = b0 + blockIdx.x;
+  const int i = find_tensor(cb.first, n, b);
+  const int64_t numel = (int64_t)(cb.numel[i] & ((1ull << kDtypeShift) - 1));
+  const int sd = (int)(cb.numel[i] >> kDtypeShift) & 3;
+  const int dd = (int)(cb.numel[i] >> (kDtypeShift + 2));
+  if (cb.src[i] == cb.dst[i] && s == 1.0f && c == 1.0f) return;  // in place: same type
+  const int64_t at = (int64_t)(b - cb.first[i]) * kClipChunk;
+  const int64_t len = numel - at < kClipChunk ? numel - at : kClipChunk;
+  if (len <= 0) return;
+  if (sd == ZERO_F32) clip_to<ZERO_F32>(dd, cb.src[i], cb.dst[i], at, len, s, c);
+  else if (sd == ZERO_F16) clip_to<ZERO_F16>(dd, cb.src[i], cb.dst[i], at, len, s, c);
+  else clip_to<ZERO_BF16>(dd, cb.src[i], cb.dst[i], at, len, s, c);
+}
+
+}  // namespace
+
+// Workspace: ticket | records [n] | sums [n] | partials [chunks].
+int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_sq,
+                        void* workspace, const FinalizeArgs& fa, zero_step_result_t* res,
+                        hipStream_t stream) {
+  const TensorLayout l = tensor_layout(tensors, n);
+  const int64_t chunk = kTensorChunk << l.shift;
+  uint32_t* ticket = (uint32_t*)workspace;
+  TensorRecord* records = (TensorRecord*)((char*)workspace + kTicketBytes);
+  Partial* sums = (Partial*)(records + n);
+  Partial* partials = sums + n;
+  int64_t chunk0 = 0;
+  for (int32_t t0 = 0; t0 < n; t0 += kNormBatch) {
+    const int32_t m = n - t0 < kNormBatch ? n - t0 : kNormBatch;
+    NormBatch nb;
+    int64_t blocks = 0;
+    for (int32_t i = 0; i < m; ++i) {
+      const zero_tensor_t& t = tensors[t0 + i];
+      nb.src[i] = t.src;
+      nb.numel[i] = (uint64_t)t.numel | (uint64_t)t.src_dtype << kDtypeShift;
+      nb.first[i] = (uint32_t)blocks;
+      blocks += t.numel ? (t.numel - 1) / chunk + 1 : 1;
+    }
+    hipLaunchKernelGGL(k_tensors_norm, dim3((uint32_t)blocks), dim3(kNormThreads), 0, stream, nb,
+                       m, t0, chunk0, chunk, t0 == 0 ? 1 : 0, records, partials, ticket);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return (int)e;
+    chunk0 += blocks;
+  }
+  hipLaunchKernelGGL(k_tensors_finalize, dim3(n > 0 ? (uint32_t)n : 1u), dim3(kNormThreads), 0,
+                     stream, partials, records, sums, n, tensor_sq, ticket, fa, res);
+  return (int)hipGetLastError();
+}
+
+int launch_tensors_clip(const zero_tensor_t* tensors, int32_t n, float scale,
+                        const zero_step_result_t* res, hipStream_t stream) {
+  constexpr int64_t kMaxBlocks = (int64_t)1 << 30;
+  int32_t t0 = 0;
+  while (t0 < n) {
+    ClipBatch cb;
+    int32_t m = 0;
+    int64_t blocks = 0;
+    for (; t0 + m < n && m < kClipBatch; ++m) {
+      const zero_tensor_t& t = tensors[t0 + m];
+      const int64_t nb = (t.numel + kClipChunk - 1) / kClipChunk;
+      if (m > 0 && blocks + nb > kMaxBlocks) break;
+      cb.src[m] = t.src;
+      cb.dst[m] = t.dst;
+      cb.numel[m] = (uint64_t)t.numel |
+                    (uint64_t)(t.src_dtype | t.dst_dtype << 2) << kDtypeShift;
+      cb.first[m] = (uint32_t)blocks;
+      blocks += nb;
+    }
+    if (blocks > 0) {
+      if (blocks > UINT32_MAX - kMaxBlocks) return (int)hipErrorInvalidValue;
+      for (int64_t b0 = 0; b0 < blocks; b0 += kMaxBlocks) {
+        const int64_t nb = blocks - b0 < kMaxBlocks ? blocks - b0 : kMaxBlocks;
+        hipLaunchKernelGGL(k_tensors_clip, dim3((uint32_t)nb), dim3(kClipThreads), 0, stream, cb,
+                           m, (uint32_t)b0, scale, res);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return (int)e;
+      }
+    }
+    t0 += m;
+  }
+  return (int)hipSuccess;
+}
+
+}  // namespace zk
