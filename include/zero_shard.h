@@ -684,6 +684,97 @@ int zero_tensors_norm_clip(const zero_tensor_t* tensors, int32_t n_tensors,
                            void* workspace, size_t ws_bytes, zero_step_result_t* dev_result,
                            hipStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Loss of a language-model head and its gradients: softmax cross entropy of
+ * logits = x w^T, taken in pieces of the vocabulary so that the logits are
+ * never kept.  It is where the loss scale enters that the shard step divides
+ * by: the weight's gradient is written in the 16-bit form of a contribution
+ * row, straight into the flat gradient if the caller points dw there.
+ *   l_tv = sum_h x_th w_vh;  lse_t = log sum_v exp(l_tv);  loss_t = lse_t - l_t,y(t)
+ *   c    = loss_scale / (mean ? max(valid, 1) : 1)
+ *   d_tv = c (exp(l_tv - lse_t) - [v = y(t)])
+ *   dx_t = sum_v d_tv w_v;   dw_v = sum_t d_tv x_t
+ * over the valid tokens, those with 0 <= y(t) < vocab.  A token with y(t) < 0
+ * is ignored: loss and lse 0, dx 0, no part in dw, whatever its x holds.  A
+ * label >= vocab is an error of the data: it is counted in `bad`, and the
+ * loss and every gradient become NaN, so that a step would be skipped. */
+
+#define ZERO_HEAD_MAX_TOKENS ((int64_t)1 << 20)
+#define ZERO_HEAD_MAX_VOCAB ((int64_t)1 << 30)
+#define ZERO_HEAD_MAX_HIDDEN ((int64_t)1 << 20)
+
+typedef struct zero_head {
+  int64_t tokens, hidden, vocab; /* T >= 0, H >= 1, V >= 1 */
+  const void* x;                 /* device [T, H], row t at x + t*ldx; 2-byte aligned */
+  int64_t ldx;                   /* elements between rows, >= H, <= ZERO_HEAD_MAX_HIDDEN */
+  const void* w;                 /* device [V, H], row v at w + v*ldw; 2-byte aligned */
+  int64_t ldw;                   /* as ldx; rows that start on 16-byte boundaries are read in
+                                    place, others are first laid out in the workspace */
+  const int64_t* labels;         /* device [T], 8-byte aligned */
+  int32_t dtype;                 /* of x and w: ZERO_F16 or ZERO_BF16 */
+  int32_t mean;                  /* nonzero: divide by the valid tokens */
+  double loss_scale;             /* factor on the gradients, finite and > 0 */
+} zero_head_t;
+
+typedef struct zero_head_grads {
+  void* dx;            /* device [T, H], type of x, row t at dx + t*lddx; 2-byte aligned */
+  int64_t lddx;        /* >= H */
+  void* dw;            /* device [V, H], row v at dw + v*lddw; aligned to one element */
+  int64_t lddw;        /* >= H */
+  int32_t dw_dtype;    /* type of w, or ZERO_F32 */
+  int32_t accumulate;  /* nonzero: dw += (a tied embedding, micro-batches; the sum is fp32,
+                          rounded once); zero: dw is overwritten */
+} zero_head_grads_t;
+
+/* Written to device memory by the loss. */
+typedef struct zero_loss_result {
+  double loss_sum;   /* sum of the valid tokens' losses */
+  float loss;        /* loss_sum / max(valid, 1) if mean, else loss_sum; unscaled */
+  int32_t reserved;
+  int64_t valid;     /* tokens with 0 <= label < vocab */
+  int64_t bad;       /* tokens with label >= vocab */
+} zero_loss_result_t;
+
+/* Bytes of workspace for the calls below; grad: nonzero for the calls that
+ * form gradients.  0 for a bad head.  Depends on sizes, types, strides and the
+ * alignment of w. */
+size_t zero_head_workspace_bytes(const zero_head_t* head, int32_t grad);
+
+/*
+ * zero_head_loss: the loss alone (evaluation).
+ *   token_loss  device [T] fp32, 4-byte aligned, or NULL
+ *   lse         device [T] fp32, 4-byte aligned, or NULL (zero_head_grad needs it)
+ *   workspace   device, >= zero_head_workspace_bytes(head, 0), 256-byte
+ *               aligned; its content on entry does not matter
+ *   dev_result  device, 8-byte aligned; fully written
+ * Logits and sums are fp32.  Equal inputs give equal bits.
+ * Errors: ZERO_EINVAL (sizes, strides, dtype, loss_scale, NULL pointers),
+ * ZERO_EALIGN, ZERO_ENOSPC (workspace), ZERO_EHIP.  Nothing is launched if a
+ * check fails.
+ */
+int zero_head_loss(const zero_head_t* head, float* token_loss, float* lse, void* workspace,
+                   size_t ws_bytes, zero_loss_result_t* dev_result, hipStream_t stream);
+
+/*
+ * zero_head_grad: the gradients, from the lse that zero_head_loss wrote for
+ * the same x, w and labels.  The logits are formed again, one piece of the
+ * vocabulary at a time; exp(l - lse) - [v = y] is rounded once to the type of
+ * x and w (fp16: scaled by 2^15 first, so that small probabilities stay in
+ * range), and both products accumulate in fp32 and are rounded once.
+ *   lse         device [T] fp32, 4-byte aligned
+ *   workspace   >= zero_head_workspace_bytes(head, 1)
+ * dx and dw must not overlap each other, x, w, labels or lse.
+ * Errors: as zero_head_loss.
+ */
+int zero_head_grad(const zero_head_t* head, const float* lse, const zero_head_grads_t* grads,
+                   void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/* zero_head_loss_grad: zero_head_loss then zero_head_grad on the same stream
+ * (training); lse may be NULL.  workspace >= zero_head_workspace_bytes(head, 1). */
+int zero_head_loss_grad(const zero_head_t* head, float* token_loss, float* lse,
+                        const zero_head_grads_t* grads, void* workspace, size_t ws_bytes,
+                        zero_loss_result_t* dev_result, hipStream_t stream);
+
 typedef struct zero_scaler {
   double scale;            /* current loss scale */
   double growth, backoff;  /* e.g. 2.0 and 0.5 */

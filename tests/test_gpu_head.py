@@ -1,0 +1,281 @@
+"""The head's loss and gradients (zero_head_*) on the GPU against 64-bit values,
+element by element within the bounds of tests/head_util.py."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from head_util import check, check_dw, reference  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.float16, torch.bfloat16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _inputs(T, V, H, dtype, seed=0, ignored=0.0, lean=6.0, ldx=None, ldw=None, shift=0,
+            pad=float("nan")):
+    """x, w, y on the GPU; x leans towards its label's row, so that losses spread; row padding
+    (ldx, ldw) and what lies before and after holds `pad`."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = (torch.randn(V, H, generator=g, device="cuda") * H ** -0.5)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    x = torch.randn(T, H, generator=g, device="cuda")
+    x = x + lean * torch.rand(T, 1, generator=g, device="cuda") * w[y]
+    if ignored:
+        y[torch.rand(T, generator=g, device="cuda") < ignored] = -100
+
+    def place(t, ld):
+        ld = ld or H
+        n = t.shape[0]
+        buf = torch.full((n * ld + 64,), pad, dtype=dtype, device="cuda")
+        v = buf[shift:shift + n * ld].view(n, ld)[:, :H]
+        v.copy_(t)
+        return v
+    return place(x, ldx), place(w, ldw), y
+
+
+def _head(T, V, H, dtype, **kw):
+    from zero_sharded_optimizer_rank_amd.head import LossHead
+    h = LossHead(T, H, V, dtype, **kw)
+    h.ws.fill_(0xFF)  # NaN in every format: the workspace's content must not matter
+    return h
+
+
+def _check_loss(r, ref):
+    check(r.lse, *ref["lse"], "lse")
+    check(r.token_loss, *ref["token_loss"], "token_loss")
+    want, bound = ref["loss"]
+    assert abs(r.loss.item() - want) <= bound, (r.loss.item(), want, bound)
+    assert r.valid.item() == ref["valid"] and r.bad.item() == 0
+
+
+SHAPES = [  # T, V, H
+    (1, 1, 1), (1, 2, 8), (1, 300, 64), (2, 257, 72), (17, 1000, 1600), (50, 1000, 72),
+    (63, 129, 65), (128, 128, 128), (129, 2049, 200), (256, 256, 256), (257, 513, 1001),
+    (600, 5000, 264), (1025, 777, 96), (33, 50257, 40),
+]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+@pytest.mark.parametrize("T,V,H", SHAPES)
+def test_loss_and_gradients(T, V, H, dtype):
+    x, w, y = _inputs(T, V, H, dtype, seed=T + V)
+    scale = 16.0
+    ref = reference(x, w, y, loss_scale=scale)
+    h = _head(T, V, H, dtype)
+    _check_loss(h.loss(x, w, y), ref)
+    r = h.loss_grad(x, w, y, loss_scale=scale)
+    _check_loss(r, ref)
+    check(r.dx, *ref["dx"], "dx")
+    check_dw(r.dw, ref)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+@pytest.mark.parametrize("mean", [True, False])
+@pytest.mark.parametrize("ignored", [0.3, 0.95])
+def test_ignored_tokens(dtype, mean, ignored):
+    T, V, H = 300, 700, 136
+    x, w, y = _inputs(T, V, H, dtype, seed=5, ignored=ignored)
+    x[y < 0] = float("nan")  # whatever an ignored token holds reaches no result
+    x[(y < 0).nonzero()[0, 0]] = float("inf")
+    y[(y < 0).nonzero()[1, 0]] = -1  # any negative label
+    ref = reference(x, w, y, mean=mean)
+    r = _head(T, V, H, dtype).loss_grad(x, w, y, mean=mean)
+    _check_loss(r, ref)
+    check(r.dx, *ref["dx"], "dx")
+    check_dw(r.dw, ref)
+    assert (r.dx[y < 0] == 0).all() and (r.token_loss[y < 0] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+@pytest.mark.parametrize("T", [0, 1, 300])
+def test_no_valid_token(dtype, T):
+    V, H = 300, 72
+    x, w, _ = _inputs(max(T, 1), V, H, dtype)
+    y = torch.full((T,), -100, dtype=torch.int64, device="cuda")
+    h = _head(max(T, 1), V, H, dtype)
+    r = h.loss_grad(x[:T], w, y)
+    assert r.loss.item() == 0.0 and r.loss_sum.item() == 0.0 and r.valid.item() == 0
+    assert (r.dx == 0).all() and (r.dw == 0).all() and (r.lse == 0).all()
+    r.dw.fill_(3.0)
+    h.loss_grad(x[:T], w, y, dw=r.dw, accumulate=True)
+    assert (r.dw == 3.0).all()
+    assert h.loss(x[:T], w, y).loss.item() == 0.0
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+@pytest.mark.parametrize("ldx,ldw,shift", [(80, 88, 0), (72, 75, 0), (73, 72, 0), (72, 72, 1),
+                                           (72, 72, 8), (77, 79, 3)])
+def test_strides_and_alignment(dtype, ldx, ldw, shift):
+    """Padded and misaligned rows; the padding holds NaN and reaches no result; what lies
+    around the outputs stays as it was."""
+    T, V, H = 70, 555, 72
+    x, w, y = _inputs(T, V, H, dtype, seed=9, ldx=ldx, ldw=ldw, shift=shift)
+    ref = reference(x, w, y)
+    bx = torch.full((T + 2, ldx), 7.0, dtype=dtype, device="cuda")
+    bw = torch.full((V + 2, ldw), 7.0, dtype=dtype, device="cuda")
+    r = _head(T, V, H, dtype).loss_grad(x, w, y, dx=bx[1:-1, :H], dw=bw[1:-1, :H])
+    _check_loss(r, ref)
+    check(bx[1:-1, :H], *ref["dx"], "dx")
+    check_dw(bw[1:-1, :H], ref)
+    for b in (bx, bw):
+        assert (b[0] == 7).all() and (b[-1] == 7).all() and (b[:, H:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+@pytest.mark.parametrize("out", ["same", "f32"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weight_gradient_forms(dtype, out, accumulate):
+    T, V, H = 90, 600, 104
+    x, w, y = _inputs(T, V, H, dtype, seed=3)
+    ref = reference(x, w, y, loss_scale=32.0)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    base = torch.randn(V, H, generator=g, device="cuda").to(
+        torch.float32 if out == "f32" else dtype)
+    dw = base.clone()
+    _head(T, V, H, dtype).loss_grad(x, w, y, loss_scale=32.0, dw=dw, accumulate=accumulate)
+    check_dw(dw, ref, base if accumulate else None)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+def test_several_pieces_of_the_vocabulary(dtype):
+    """Enough tokens that the vocabulary is taken in several pieces."""
+    T, V, H = 33_000, 9_001, 72
+    x, w, y = _inputs(T, V, H, dtype, seed=4, ignored=0.1)
+    ref = reference(x, w, y, loss_scale=1024.0)
+    r = _head(T, V, H, dtype).loss_grad(x, w, y, loss_scale=1024.0)
+    _check_loss(r, ref)
+    check(r.dx, *ref["dx"], "dx")
+    check_dw(r.dw, ref)
+    del ref
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+def test_separate_calls_equal_the_joint_one(dtype):
+    T, V, H = 200, 1500, 328
+    x, w, y = _inputs(T, V, H, dtype, seed=6, ignored=0.2)
+    h = _head(T, V, H, dtype)
+    r = h.loss_grad(x, w, y, loss_scale=64.0)
+    dx, dw, lse = r.dx.clone(), r.dw.clone(), r.lse.clone()
+    first = h.loss(x, w, y)
+    assert torch.equal(first.lse, lse)
+    h2 = _head(T, V, H, dtype)
+    dx2, dw2 = h2.grad(x, w, y, lse, loss_scale=64.0)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    for _ in range(3):  # equal inputs give equal bits
+        r = h.loss_grad(x, w, y, loss_scale=64.0)
+        assert torch.equal(r.dx, dx) and torch.equal(r.dw, dw) and torch.equal(r.lse, lse)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+@pytest.mark.parametrize("alone", [True, False])
+def test_bad_label_makes_the_gradients_nan(dtype, alone):
+    T, V, H = 40, 300, 72
+    x, w, y = _inputs(T, V, H, dtype, seed=7)
+    if alone:
+        y[:] = -100
+    y[3] = V
+    r = _head(T, V, H, dtype).loss_grad(x, w, y)
+    assert r.bad.item() == 1 and r.valid.item() == (0 if alone else T - 1)
+    assert r.loss.isnan() and r.loss_sum.isnan() and r.dw.isnan().all()
+    assert r.token_loss[3].isnan()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_non_finite_input_is_not_hidden(dtype, value):
+    T, V, H = 40, 300, 72
+    x, w, y = _inputs(T, V, H, dtype, seed=8)
+    x[5, 7] = value
+    r = _head(T, V, H, dtype).loss_grad(x, w, y)
+    assert r.loss.isnan() and r.token_loss[5].isnan() and r.dx[5].isnan().all()
+    assert not r.token_loss[[4, 6]].isnan().any()
+    assert r.dw.isnan().any()  # an overflow that the step's norm will find
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+def test_large_logits(dtype):
+    """Logits of hundreds: no exponential overflows, confident tokens lose next to nothing."""
+    T, V, H = 64, 400, 128
+    x, w, y = _inputs(T, V, H, dtype, seed=10, lean=400.0)
+    ref = reference(x, w, y)
+    r = _head(T, V, H, dtype).loss_grad(x, w, y)
+    _check_loss(r, ref)
+    check(r.dx, *ref["dx"], "dx")
+    check_dw(r.dw, ref)
+
+
+def test_fewer_tokens_than_the_head_holds():
+    T, V, H = 500, 300, 72
+    h = _head(T, V, H, torch.bfloat16)
+    for t in (500, 7, 256):
+        x, w, y = _inputs(t, V, H, torch.bfloat16, seed=t)
+        ref = reference(x, w, y)
+        r = h.loss_grad(x, w, y)
+        _check_loss(r, ref)
+        check(r.dx, *ref["dx"], "dx")
+        check_dw(r.dw, ref)
+
+
+def test_call_checks():
+    h = _head(8, 30, 16, torch.bfloat16)
+    x, w, y = _inputs(8, 30, 16, torch.bfloat16)
+    for bad in [
+        lambda: h.loss(x.half(), w, y), lambda: h.loss(x, w[:29], y),
+        lambda: h.loss(x[:, :8], w, y), lambda: h.loss(x, w, y.int()),
+        lambda: h.loss(x, w.cpu(), y), lambda: h.loss(x, w, y[::2]),
+        lambda: h.loss(x.t().contiguous().t(), w, y),
+        lambda: h.loss_grad(x, w, y, accumulate=True),
+        lambda: h.loss_grad(x, w, y, dw=torch.empty(30, 16, dtype=torch.float16, device="cuda")),
+        lambda: h.loss(torch.cat([x, x]), w, torch.cat([y, y])),
+        lambda: h.grad(x, w, y, y.float()[:3]),
+        lambda: _head(8, 30, 16, torch.bfloat16, grad=False).loss_grad(x, w, y),
+    ]:
+        with pytest.raises((ValueError, TypeError)):
+            bad()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+def test_graph_replays(dtype):
+    """Captured once; every replay, with eager work in between, equals the eager result; the
+    number of valid tokens changes between replays."""
+    T, V, H = 300, 2000, 264
+    x, w, y = _inputs(T, V, H, dtype, seed=11)
+    h, eager = _head(T, V, H, dtype), _head(T, V, H, dtype)
+    h.loss_grad(x, w, y, loss_scale=8.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        r = h.loss_grad(x, w, y, loss_scale=8.0)
+    for k in range(4):
+        x2, w2, y2 = _inputs(T, V, H, dtype, seed=40 + k, ignored=0.3 * k)
+        x.copy_(x2), w.copy_(w2), y.copy_(y2)
+        want = eager.loss_grad(x2, w2, y2, loss_scale=8.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(h.res, eager.res)
+        for a, b in zip(r[2:4] + r[6:], want[2:4] + want[6:]):
+            assert torch.equal(a, b)
+
+
+def test_two_heads_on_two_streams():
+    T, V, H = 260, 3000, 264
+    heads = [_head(T, V, H, torch.bfloat16) for _ in range(2)]
+    data = [_inputs(T, V, H, torch.bfloat16, seed=50 + k) for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        rs = [h.loss_grad(*d, stream=s) for h, d, s in zip(heads, data, streams)]
+    torch.cuda.synchronize()
+    for r, d in zip(rs, data):
+        ref = reference(*d)
+        _check_loss(r, ref)
+        check(r.dx, *ref["dx"], "dx")
+        check_dw(r.dw, ref)

@@ -1,0 +1,138 @@
+"""The head's loss (zero_head_*) on the CPU: argument checks, the workspace's
+size, and the 64-bit reference's gradients against differences."""
+import ctypes
+
+import pytest
+
+from zero_sharded_optimizer_rank_amd import abi
+
+torch = pytest.importorskip("torch")
+
+X, W, Y, DX, DW, WS, RES = (0x10000000 * (i + 1) for i in range(7))  # never dereferenced
+GOOD = dict(tokens=5, hidden=64, vocab=100, x=X, ldx=64, w=W, ldw=64, labels=Y,
+            dtype=abi.ZERO_BF16, mean=1, loss_scale=1.0)
+
+
+def _head(**kw):
+    a = dict(GOOD)
+    a.update(kw)
+    return abi.zero_head_t(*(a[n] for n, _ in abi.zero_head_t._fields_))
+
+
+def _grads(**kw):
+    a = dict(dx=DX, lddx=64, dw=DW, lddw=64, dw_dtype=abi.ZERO_BF16, accumulate=0)
+    a.update(kw)
+    return abi.zero_head_grads_t(*(a[n] for n, _ in abi.zero_head_grads_t._fields_))
+
+
+def _loss(head, token_loss=None, lse=None, ws=WS, n=1 << 30, res=RES):
+    abi.zero_head_loss(head, token_loss, lse, ws, n, res)
+
+
+def _grad(head=None, lse=0x90000000, grads=None, ws=WS, n=1 << 30):
+    abi.zero_head_grad(head or _head(), lse, grads or _grads(), ws, n)
+
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.mark.parametrize("call,code", [
+    (lambda: _loss(_head(tokens=-1)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(tokens=(1 << 20) + 1)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(hidden=0)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(hidden=1 << 21, ldx=1 << 21, ldw=1 << 21)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(vocab=0)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(vocab=(1 << 30) + 1)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(ldx=63)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(ldw=63)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(dtype=abi.ZERO_F32)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(loss_scale=0.0)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(loss_scale=NAN)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(loss_scale=INF)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(x=0)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(w=0)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(labels=0)), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(x=X + 1)), abi.ZERO_EALIGN),
+    (lambda: _loss(_head(w=W + 1)), abi.ZERO_EALIGN),
+    (lambda: _loss(_head(labels=Y + 4)), abi.ZERO_EALIGN),
+    (lambda: _loss(_head(), token_loss=RES + 2), abi.ZERO_EALIGN),
+    (lambda: _loss(_head(), lse=RES + 2), abi.ZERO_EALIGN),
+    (lambda: _loss(_head(), res=None), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(), res=RES + 4), abi.ZERO_EALIGN),
+    (lambda: _loss(_head(), ws=None), abi.ZERO_EINVAL),
+    (lambda: _loss(_head(), ws=WS + 128), abi.ZERO_EALIGN),
+    (lambda: _loss(_head(), n=1000), abi.ZERO_ENOSPC),
+    (lambda: _grad(lse=None), abi.ZERO_EINVAL),
+    (lambda: _grad(lse=0x90000002), abi.ZERO_EALIGN),
+    (lambda: _grad(grads=_grads(dx=0)), abi.ZERO_EINVAL),
+    (lambda: _grad(grads=_grads(dw=0)), abi.ZERO_EINVAL),
+    (lambda: _grad(grads=_grads(lddx=63)), abi.ZERO_EINVAL),
+    (lambda: _grad(grads=_grads(lddw=63)), abi.ZERO_EINVAL),
+    (lambda: _grad(grads=_grads(dw_dtype=abi.ZERO_F16)), abi.ZERO_EINVAL),
+    (lambda: _grad(grads=_grads(dw=DW + 2, dw_dtype=abi.ZERO_F32)), abi.ZERO_EALIGN),
+    (lambda: _grad(grads=_grads(dx=X)), abi.ZERO_EINVAL),
+    (lambda: _grad(grads=_grads(dw=W + 128)), abi.ZERO_EINVAL),
+    (lambda: _grad(grads=_grads(dw=DX)), abi.ZERO_EINVAL),
+    (lambda: _grad(grads=_grads(dx=Y)), abi.ZERO_EINVAL),
+    (lambda: _grad(n=1000), abi.ZERO_ENOSPC),
+])
+def test_refusals(call, code):
+    with pytest.raises(abi.ZeroError) as e:
+        call()
+    assert e.value.code == code
+    assert abi.zero_last_error()
+
+
+def test_null_structures():
+    so = abi.lib()
+    assert so.zero_head_loss(None, None, None, WS, 1 << 30, RES, None) == abi.ZERO_EINVAL
+    assert so.zero_head_grad(ctypes.byref(_head()), 0x90000000, None, WS, 1 << 30, None) == \
+        abi.ZERO_EINVAL
+    assert so.zero_head_workspace_bytes(None, 1) == 0
+    assert abi.zero_head_workspace_bytes(_head(hidden=0), True) == 0
+
+
+def test_workspace_bytes():
+    need = lambda grad, **kw: abi.zero_head_workspace_bytes(_head(**kw), grad)
+    big = dict(tokens=8192, hidden=4096, vocab=128256, ldx=4096, ldw=4096)
+    # far less than the logits (fp32 4.2 GB, 16-bit 2.1 GB)
+    assert need(False, **big) < 0.2e9
+    assert need(True, **big) < 1.0e9
+    # a w whose rows do not start on 16-byte boundaries is laid out once more
+    copy = 2 * 128256 * 4096
+    assert copy <= need(False, **dict(big, w=W + 2)) - need(False, **big) <= copy + 256
+    assert need(False, **dict(big, ldw=4097)) > copy
+
+
+@pytest.mark.parametrize("mean", [True, False])
+def test_reference_gradients_against_differences(mean):
+    from head_util import reference
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(4, 6, generator=g, dtype=torch.float64)
+    w = torch.randn(5, 6, generator=g, dtype=torch.float64)
+    y = torch.tensor([2, -100, 0, 4])
+    ref = reference(x, w, y, loss_scale=8.0, mean=mean)
+
+    def loss(x, w):
+        return reference(x, w, y, mean=mean)["loss"][0] * 8.0
+
+    h = 1e-6  # central differences: error ~ h^2 and 1e-16 / h, both under 1e-8 here
+    for name, t in (("dx", x), ("dw", w)):
+        got = torch.zeros_like(t)
+        for i in range(t.numel()):
+            a, b = t.clone(), t.clone()
+            a.view(-1)[i] += h
+            b.view(-1)[i] -= h
+            got.view(-1)[i] = (loss(*((a, w) if name == "dx" else (x, a)))
+                               - loss(*((b, w) if name == "dx" else (x, b)))) / (2 * h)
+        assert (got - ref[name][0]).abs().max() < 1e-7, name
+
+
+def test_loss_head_refusals():
+    from zero_sharded_optimizer_rank_amd.head import LossHead
+    with pytest.raises(TypeError):
+        LossHead(4, 8, 16, torch.float32)
+    with pytest.raises(ValueError):
+        LossHead(4, 8, 16, torch.float16, device="cpu")
+    with pytest.raises(ValueError):
+        LossHead(4, 0, 16, torch.float16)

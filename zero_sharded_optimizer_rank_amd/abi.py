@@ -92,12 +92,31 @@ class zero_tensor_t(ctypes.Structure):
                 ("src_dtype", ctypes.c_int32), ("dst_dtype", ctypes.c_int32)]
 
 
+class zero_head_t(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("w", ctypes.c_void_p),
+                ("ldw", ctypes.c_int64), ("labels", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("mean", ctypes.c_int32), ("loss_scale", ctypes.c_double)]
+
+
+class zero_head_grads_t(ctypes.Structure):
+    _fields_ = [("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dw", ctypes.c_void_p),
+                ("lddw", ctypes.c_int64), ("dw_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+
+class zero_loss_result_t(ctypes.Structure):
+    _fields_ = [("loss_sum", ctypes.c_double), ("loss", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("valid", ctypes.c_int64), ("bad", ctypes.c_int64)]
+
+
 class zero_offload_staging_t(ctypes.Structure):
     _fields_ = [("grad_pinned", ctypes.c_void_p), ("param16_pinned", ctypes.c_void_p),
                 ("chunk", ctypes.c_int64), ("upload_stream", ctypes.c_void_p)]
 
 
 RESULT_BYTES = ctypes.sizeof(zero_step_result_t)
+LOSS_RESULT_BYTES = ctypes.sizeof(zero_loss_result_t)
 UNIT_BUFFERS_BYTES = ctypes.sizeof(zero_unit_buffers_t)
 
 # (name, restype, argtypes) for every symbol the header declares
@@ -186,6 +205,12 @@ _SIGNATURES = {
     "zero_tensors_norm_clip": (ctypes.c_int, [_P(zero_tensor_t), ctypes.c_int32,
                                               _P(zero_step_args_t), ctypes.c_double, _vp, _vp,
                                               ctypes.c_size_t, _vp, _vp]),
+    "zero_head_workspace_bytes": (ctypes.c_size_t, [_P(zero_head_t), ctypes.c_int32]),
+    "zero_head_loss": (ctypes.c_int, [_P(zero_head_t), _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]),
+    "zero_head_grad": (ctypes.c_int, [_P(zero_head_t), _vp, _P(zero_head_grads_t), _vp,
+                                      ctypes.c_size_t, _vp]),
+    "zero_head_loss_grad": (ctypes.c_int, [_P(zero_head_t), _vp, _vp, _P(zero_head_grads_t), _vp,
+                                           ctypes.c_size_t, _vp, _vp]),
     "zero_scaler_update": (ctypes.c_int, [_P(zero_scaler_t), ctypes.c_int32]),
     "zero_last_error": (ctypes.c_char_p, []),
 }
@@ -522,3 +547,24 @@ def zero_tensors_norm_clip(tensors, n_tensors, args, out_scale, tensor_sq, works
     _check(lib().zero_tensors_norm_clip(tensors, n_tensors, ctypes.byref(args), out_scale,
                                         _addr(tensor_sq), _addr(workspace), ws_bytes,
                                         _addr(dev_result), _stream(stream)))
+
+
+def zero_head_workspace_bytes(head: zero_head_t, grad: bool) -> int:
+    return int(lib().zero_head_workspace_bytes(ctypes.byref(head), 1 if grad else 0))
+
+
+def zero_head_loss(head, token_loss, lse, workspace, ws_bytes, dev_result, stream=None):
+    _check(lib().zero_head_loss(ctypes.byref(head), _addr(token_loss), _addr(lse),
+                                _addr(workspace), ws_bytes, _addr(dev_result), _stream(stream)))
+
+
+def zero_head_grad(head, lse, grads, workspace, ws_bytes, stream=None):
+    _check(lib().zero_head_grad(ctypes.byref(head), _addr(lse), ctypes.byref(grads),
+                                _addr(workspace), ws_bytes, _stream(stream)))
+
+
+def zero_head_loss_grad(head, token_loss, lse, grads, workspace, ws_bytes, dev_result,
+                        stream=None):
+    _check(lib().zero_head_loss_grad(ctypes.byref(head), _addr(token_loss), _addr(lse),
+                                     ctypes.byref(grads), _addr(workspace), ws_bytes,
+                                     _addr(dev_result), _stream(stream)))

@@ -30,8 +30,9 @@ DEVICE_FLAGS = [
     f"--offload-arch={ARCH}",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
-DEVICE_SOURCES = ("zero_kernels.hip", "zero_units.hip", "zero_noalloc.hip", "zero_tensors.hip")
-HOST_SOURCES = ("zero_host.cpp", "zero_offload.cpp", "zero_tensors.cpp")
+DEVICE_SOURCES = ("zero_kernels.hip", "zero_units.hip", "zero_noalloc.hip", "zero_tensors.hip",
+                  "zero_head.hip")
+HOST_SOURCES = ("zero_host.cpp", "zero_offload.cpp", "zero_tensors.cpp", "zero_head.cpp")
 # host Adam of the offload form: IEEE fp32, no contraction, errno-free sqrt
 HOST_FLAGS = {"zero_offload.cpp": ["-ffp-contract=off", "-fno-math-errno", "-pthread"]}
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-I", INCLUDE, "-I", CSRC]

@@ -1,0 +1,49 @@
+// Internal interface between the host side of the head's loss (zero_head.cpp)
+// and its kernels (zero_head.hip).
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "zero_internal.h"
+#include "zero_shard.h"
+
+namespace zk {
+
+constexpr int64_t kHeadTile = 256;  // token and vocabulary rows are padded to whole tiles
+constexpr int64_t kHeadStep = 64;   // contraction elements a step stages
+
+// Where things lie in the workspace (byte offsets), and how the work is cut.
+struct HeadPlan {
+  int64_t tokens_pad;  // tokens rounded up to a tile
+  int64_t hidden_pad;  // hidden rounded up to a step: row length of the packed x (and w)
+  int64_t parts;       // softmax partials a token gets (one per kHeadPart vocabulary rows)
+  int64_t piece;       // vocabulary rows a piece of the gradient takes (whole tiles)
+  int32_t split;       // ways the hidden gradient's contraction is split
+  bool pack_w;         // w's rows do not start on 16-byte boundaries
+  // offsets
+  size_t state, sums, index, label, lse, x, w, part, picked, g, acc, total;
+};
+constexpr int64_t kHeadPart = 128;
+
+struct HeadState {  // at offset `state`
+  int32_t valid;
+  int32_t ticket;
+  int64_t bad;
+  float coef;      // c, or NaN
+  float pad;
+};
+
+HeadPlan head_plan(const zero_head_t* h, bool grad);
+
+// Launchers: arguments already validated.  Return hipSuccess or the error.
+// lse_in: NULL when the loss runs in the same call (the packed lse is then
+// already in the workspace).
+int launch_head_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse_in,
+                     const zero_head_grads_t* grads, hipStream_t stream);
+int launch_head_loss(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
+                     float* lse, zero_loss_result_t* res, hipStream_t stream);
+int launch_head_grad(const zero_head_t* h, const HeadPlan& p, void* ws,
+                     const zero_head_grads_t* grads, hipStream_t stream);
+
+}  // namespace zk
