@@ -27,7 +27,12 @@ using namespace dev;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kScanThreads = 1024;
 constexpr int kPackThreads = 256;
-constexpr int kGemmThreads = 512;
+#ifndef ZK_CFG
+#define ZK_CFG 2, 4, 4, 2
+#endif
+constexpr int kCfg[4] = {ZK_CFG};
+constexpr int kWM = kCfg[0], kWN = kCfg[1], kMI = kCfg[2], kNJ = kCfg[3];
+constexpr int kGemmThreads = 64 * kWM * kWN;
 constexpr int kJoinTokens = 64, kJoinWaves = 4;
 
 // g's scale before it is rounded: |p - [v = y]| <= 1, so 2^15 keeps fp16 in
@@ -157,12 +162,12 @@ struct LogitTile {
                                              int32_t vocab, const uint16_t* x, int32_t t0,
                                              int32_t hidden_pad, int32_t K,
                                              f32x16 (&acc)[MI][NJ]) {
-    __shared__ __attribute__((aligned(1024))) char a0[G::BM * kStep * 2], b0[G::BN * kStep * 2],
-        a1[G::BM * kStep * 2], b1[G::BN * kStep * 2];
+    __shared__ __attribute__((aligned(1024))) char s0[G::kSlotBytes], s1[G::kSlotBytes],
+      s2[G::kSlotBytes], s3[G::kSlotBytes];
     const int64_t rows = vocab - v0;
     const Operand A{w + v0 * ldw, ldw * 2, (int32_t)(rows < G::BM ? rows : G::BM), K};
     const Operand B{x + (int64_t)t0 * hidden_pad, (int64_t)hidden_pad * 2, G::BN, K};
-    G::run(A, B, K, (lds_char*)a0, (lds_char*)b0, (lds_char*)a1, (lds_char*)b1, acc);
+    G::run(A, B, K, (lds_char*)s0, (lds_char*)s1, (lds_char*)s2, (lds_char*)s3, acc);
     return true;
   }
 };
@@ -179,9 +184,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_partials(
   using L = LogitTile<T, WM, WN, MI, NJ>;
   using G = typename L::G;
   static_assert(MI * 32 == kHeadPart, "one partial a wave");
-  const int32_t t0 = blockIdx.x * G::BN;
-  const int64_t v0 = (int64_t)blockIdx.y * G::BM;
-  if (t0 >= state->valid) return;
+  int32_t mt, nt;
+  if (!tile_of(blockIdx.x, (uint32_t)((vocab + G::BM - 1) / G::BM),
+               (uint32_t)((state->valid + G::BN - 1) / G::BN), mt, nt))
+    return;
+  const int32_t t0 = nt * G::BN;
+  const int64_t v0 = (int64_t)mt * G::BM;
   f32x16 acc[MI][NJ];
   L::run(w, ldw, v0, vocab, x, t0, hidden_pad, K, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -315,16 +323,20 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_g(
     int32_t piece, uint16_t* __restrict__ g) {
   using L = LogitTile<T, WM, WN, MI, NJ>;
   using G = typename L::G;
-  const int32_t t0 = blockIdx.x * G::BN;
-  const int32_t c0 = blockIdx.y * G::BM;  // column of g
-  const int64_t v0 = piece0 + c0;
   const int32_t valid = state->valid;
-  if (t0 >= valid) return;
+  const int32_t left = vocab - piece0 < piece ? (int32_t)(vocab - piece0) : piece;
+  int32_t mt, nt;
+  if (!tile_of(blockIdx.x, (uint32_t)((left + G::BM - 1) / G::BM),
+               (uint32_t)((valid + G::BN - 1) / G::BN), mt, nt))
+    return;
+  const int32_t t0 = nt * G::BN;
+  const int32_t c0 = mt * G::BM;  // column of g
+  const int64_t v0 = piece0 + c0;
   f32x16 acc[MI][NJ];
   L::run(w, ldw, v0, vocab, x, t0, hidden_pad, K, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t cw = c0 + (wave / WN) * MI * 32;
-  const int32_t rows = (int32_t)(vocab - piece0 < piece ? vocab - piece0 : piece) - cw;
+  const int32_t rows = left - cw;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const int32_t t = t0 + (wave % WN) * NJ * 32 + j * 32 + (lane & 31);
@@ -354,22 +366,26 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_g(
 template <typename T, int WM, int WN, int MI, int NJ>
 __global__ __launch_bounds__(64 * WM * WN) void k_head_dx(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ w, int64_t ldw,
-    int32_t vocab_left, int32_t hidden_w, int32_t hidden_pad, int32_t tokens_pad, int32_t part,
-    int32_t first, const HeadState* __restrict__ state, float* __restrict__ acc_out) {
+    int32_t vocab_left, int32_t hidden_w, int32_t hidden, int32_t hidden_pad, int32_t tokens_pad,
+    int32_t split, int32_t part, int32_t first, const HeadState* __restrict__ state, float* __restrict__ acc_out) {
   using G = Gemm<T, WM, WN, MI, NJ, false, true>;
-  __shared__ __attribute__((aligned(1024))) char a0[G::BM * kStep * 2], b0[G::BN * kStep * 2],
-      a1[G::BM * kStep * 2], b1[G::BN * kStep * 2];
-  const int32_t h0 = blockIdx.x * G::BN, t0 = blockIdx.y * G::BM, k0 = blockIdx.z * part;
-  if (t0 >= state->valid) return;
+  __shared__ __attribute__((aligned(1024))) char s0[G::kSlotBytes], s1[G::kSlotBytes],
+      s2[G::kSlotBytes], s3[G::kSlotBytes];
+  const uint32_t ht = (uint32_t)((hidden + G::BN - 1) / G::BN);
+  int32_t mt, nt;
+  if (!tile_of(blockIdx.x, (uint32_t)((state->valid + G::BM - 1) / G::BM), ht * (uint32_t)split,
+               mt, nt))
+    return;
+  const int32_t h0 = nt % ht * G::BN, t0 = mt * G::BM, ks = nt / ht, k0 = ks * part;
   int32_t K = piece - k0 < part ? piece - k0 : part;
   if (K > vocab_left - k0) K = vocab_left - k0;
   // g's columns are zero from the vocabulary's end to the next tile
   const Operand A{g + (int64_t)t0 * piece + k0, (int64_t)piece * 2, G::BM, (K + 7) & ~7};
   const Operand B{w + (int64_t)k0 * ldw + h0, ldw * 2, hidden_w - h0, K};
   f32x16 acc[MI][NJ];
-  G::run(A, B, K, (lds_char*)a0, (lds_char*)b0, (lds_char*)a1, (lds_char*)b1, acc);
+  G::run(A, B, K, (lds_char*)s0, (lds_char*)s1, (lds_char*)s2, (lds_char*)s3, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float* out = acc_out + ((int64_t)blockIdx.z * tokens_pad + t0 + (wave / WN) * MI * 32) * hidden_pad;
+  float* out = acc_out + ((int64_t)ks * tokens_pad + t0 + (wave / WN) * MI * 32) * hidden_pad;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const int32_t h = h0 + (wave % WN) * NJ * 32 + j * 32 + (lane & 31);
@@ -412,15 +428,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_dw(
     int32_t hidden_pad, int32_t hidden, int32_t vocab_left, const HeadState* __restrict__ state,
     int32_t accumulate, void* __restrict__ dw, int64_t lddw) {
   using G = Gemm<T, WM, WN, MI, NJ, true, true>;
-  __shared__ __attribute__((aligned(1024))) char a0[G::BM * kStep * 2], b0[G::BN * kStep * 2],
-      a1[G::BM * kStep * 2], b1[G::BN * kStep * 2];
-  const int32_t h0 = blockIdx.x * G::BN, c0 = blockIdx.y * G::BM;
+  __shared__ __attribute__((aligned(1024))) char s0[G::kSlotBytes], s1[G::kSlotBytes],
+      s2[G::kSlotBytes], s3[G::kSlotBytes];
+  int32_t mt, nt;
+  if (!tile_of(blockIdx.x, (uint32_t)((vocab_left + G::BM - 1) / G::BM),
+               (uint32_t)((hidden + G::BN - 1) / G::BN), mt, nt))
+    return;
+  const int32_t h0 = nt * G::BN, c0 = mt * G::BM;
   const int32_t K = state->valid;
   const float c = state->coef / g_scale<T>();
   const Operand A{g + c0, (int64_t)piece * 2, piece - c0, K};
   const Operand B{x + h0, (int64_t)hidden_pad * 2, hidden_pad - h0, K};
   f32x16 acc[MI][NJ];
-  G::run(A, B, K, (lds_char*)a0, (lds_char*)b0, (lds_char*)a1, (lds_char*)b1, acc);
+  G::run(A, B, K, (lds_char*)s0, (lds_char*)s1, (lds_char*)s2, (lds_char*)s3, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const bool bad = state->bad != 0;
 #pragma unroll
@@ -478,8 +498,8 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
   const WeightView w = weight_view(h, p, ws);
   HeadState* state = at<HeadState>(ws, p.state);
   if (h->tokens > 0) {
-    hipLaunchKernelGGL((k_head_partials<T, 2, 4, 4, 2>),
-                       dim3((uint32_t)(p.tokens_pad / 256), (uint32_t)((h->vocab + 255) / 256)),
+    hipLaunchKernelGGL((k_head_partials<T, kWM, kWN, kMI, kNJ>),
+                       dim3(tile_grid(p.tokens_pad / 256, (h->vocab + 255) / 256)),
                        dim3(kGemmThreads), 0, stream, w.w, w.ld, (int32_t)h->vocab,
                        at<const uint16_t>(ws, p.x), (int32_t)p.hidden_pad, w.K,
                        (int32_t)p.tokens_pad, at<const int32_t>(ws, p.label), state,
@@ -515,25 +535,25 @@ int grad_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_gr
     const int64_t left = h->vocab - v0 < p.piece ? h->vocab - v0 : p.piece;
     const uint32_t vtiles = (uint32_t)((left + 255) / 256);
     if (h->tokens > 0) {
-      hipLaunchKernelGGL((k_head_g<T, 2, 4, 4, 2>), dim3(ttiles, vtiles), dim3(kGemmThreads), 0, stream,
+      hipLaunchKernelGGL((k_head_g<T, kWM, kWN, kMI, kNJ>), dim3(tile_grid(ttiles, vtiles)), dim3(kGemmThreads), 0, stream,
                          w.w, w.ld, (int32_t)h->vocab, x, (int32_t)p.hidden_pad, w.K,
                          at<const int32_t>(ws, p.label), at<const float>(ws, p.lse), state, v0,
                          (int32_t)p.piece, g);
       ZK_LAUNCHED();
-      hipLaunchKernelGGL((k_head_dx<T, 2, 4, 4, 2>), dim3(htiles, ttiles, (uint32_t)p.split),
+      hipLaunchKernelGGL((k_head_dx<T, kWM, kWN, kMI, kNJ>), dim3(tile_grid(htiles * p.split, ttiles)),
                          dim3(kGemmThreads), 0, stream, g, (int32_t)p.piece, w.w + v0 * w.ld, w.ld,
-                         (int32_t)left, w.width, (int32_t)p.hidden_pad, (int32_t)p.tokens_pad,
-                         part, v0 == 0 ? 1 : 0, state, acc);
+                         (int32_t)left, w.width, (int32_t)h->hidden, (int32_t)p.hidden_pad,
+                         (int32_t)p.tokens_pad, p.split, part, v0 == 0 ? 1 : 0, state, acc);
       ZK_LAUNCHED();
     }
     const size_t ew = gr->dw_dtype == ZERO_F32 ? 4 : 2;
     void* dw = (char*)gr->dw + ew * (size_t)(v0 * gr->lddw);
     if (gr->dw_dtype == ZERO_F32)
-      hipLaunchKernelGGL((k_head_dw<T, 2, 4, 4, 2, true>), dim3(htiles, vtiles), dim3(kGemmThreads), 0,
+      hipLaunchKernelGGL((k_head_dw<T, kWM, kWN, kMI, kNJ, true>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads), 0,
                          stream, g, (int32_t)p.piece, x, (int32_t)p.hidden_pad,
                          (int32_t)h->hidden, (int32_t)left, state, gr->accumulate, dw, gr->lddw);
     else
-      hipLaunchKernelGGL((k_head_dw<T, 2, 4, 4, 2, false>), dim3(htiles, vtiles), dim3(kGemmThreads), 0,
+      hipLaunchKernelGGL((k_head_dw<T, kWM, kWN, kMI, kNJ, false>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads), 0,
                          stream, g, (int32_t)p.piece, x, (int32_t)p.hidden_pad,
                          (int32_t)h->hidden, (int32_t)left, state, gr->accumulate, dw, gr->lddw);
     ZK_LAUNCHED();
