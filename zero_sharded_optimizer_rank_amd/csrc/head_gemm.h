@@ -1,4 +1,4 @@
-// Matrix-product core of the head's loss: one workgroup computes a BM x BN tile
+// Matrix-product core of the head's loss: one workgroup computes a 256 x 256 tile
 // of A B^T on gfx950's matrix cores, fp32 accumulators in registers, and hands
 // them to an epilogue.
 //
@@ -7,24 +7,26 @@
 //   cols    element (m, k) at base + k*ld + m: the tile's rows are contiguous
 // so that all three products of the loss (logits: rows x rows; dx: rows x
 // cols; dw: cols x cols) read their operands as they lie, with no transposed
-// copy.  LDS is a ring of four slots of 32 contraction elements of both
-// operands; global memory goes straight to LDS (16 bytes a lane, no
-// registers), and the lanes pick their global addresses so that the LDS image
-// is swizzled and every fragment read is free of bank conflicts:
-//   rows    64 bytes a row; 16-byte chunk c of row r lies at c ^ (r >> 2 & 3),
+// copy.  LDS holds two stages of 64 contraction elements of both operands,
+// each in three parts: the B rows, and two halves of the A rows.  Global
+// memory goes straight to LDS (16 bytes a lane, no registers), in whole
+// 128-byte lines, and the lanes pick their global addresses so that the LDS
+// image is swizzled and every fragment read is free of bank conflicts:
+//   rows    128 bytes a row; 16-byte chunk c of row r lies at c ^ (r >> 1 & 7),
 //           so that 16 consecutive rows' chunks c fill the 256 bytes the banks
 //           deliver in a cycle
-//   cols    2*BM bytes a contraction index k; 32-byte pair p lies at p ^ f(k),
-//           f(k) = 2 * ((k & 3) | (k >> 3 & 1) << 2); fragments come back
-//           transposed (ds_read_b64_tr_b16)
+//   cols    a contraction index k's elements side by side; 32-byte pair p lies
+//           at p ^ 2 * (k & 3); fragments come back transposed
+//           (ds_read_b64_tr_b16)
 //
 // Eight waves, two on each SIMD.  The second four run one phase behind the
-// first: while one wave of a SIMD reads its fragments, the other multiplies,
-// so the matrix cores do not wait for LDS or for barriers.  A slot is read in
-// two consecutive phases (by either half of the waves), and a wave refills its
-// part in its next reading phase, five or six phases before it is read again:
-// loads are issued while the other half multiplies, never in front of a
-// wave's own products, which would wait for the loads to be accepted.
+// first: while one wave of a SIMD reads fragments and issues loads, the other
+// multiplies, so the matrix cores wait neither for LDS nor for barriers, and
+// no product queues behind a load that has yet to be accepted.  A stage takes
+// a wave two rounds of (read, multiply): the first reads B and its rows of the
+// first A half (and keeps B in registers), the second its rows of the other
+// half.  A part is refilled in the round after its last reading, five or six
+// phases before it is read again.
 //
 // Lanes whose element lies outside the operand read zero (buffer bounds), so
 // ragged edges cost nothing and nothing outside the operand is touched.
@@ -85,45 +87,41 @@ struct Operand {
   int32_t k;          // contraction indexes that exist (rows: a multiple of 8)
 };
 
-constexpr int kSlot = 32;   // contraction indexes of an LDS slot
-constexpr int kSlots = 4;
+constexpr int kStage = 64;  // contraction indexes of a stage
 
-// f(k) of the cols layout, from bits 0-1 and bit 3 of k; a tile of 128 rows
-// has only 8 pairs a memory row and takes the low part.
-template <int R>
-__device__ __forceinline__ int swizzle(int k01, int k3) {
-  return (2 * (k01 | k3 << 2)) & (R / 16 - 1);
-}
+// R tile rows (columns of memory if COLS) staged by eight waves.  HALF 0 or 1:
+// R = 128 of the tile's 256 rows, local row r is row r / 64 * 128 + 64 * HALF +
+// r % 64; HALF < 0: all rows.
+template <int R, bool COLS, int HALF>
+struct Part {
+  static constexpr int kBytes = R * kStage * 2;
+  static constexpr int kLoads = kBytes / (8 * 1024);  // 1 KiB loads of a wave
+  static_assert(kLoads * 8 * 1024 == kBytes && (HALF < 0 || R == 128), "whole loads");
 
-// R tile rows staged by WAVES waves; COLS as above.
-template <int R, bool COLS, int WAVES>
-struct Stage {
-  static constexpr int kBytes = R * kSlot * 2;
-  static constexpr int kLoads = kBytes / (WAVES * 1024);  // 1 KiB wave loads of a wave and slot
-  static_assert(kLoads * WAVES * 1024 == kBytes, "whole loads");
-
-  // Issue the loads of contraction indexes [k0, k0 + 32) into lds; past the
+  // Issue the loads of contraction indexes [k0, k0 + 64) into lds; past the
   // contraction's end they read zero.
   static __device__ __forceinline__ void issue(const Operand& o, int32_t k0, lds_char* lds,
                                                int wave, int lane) {
     int32_t left = o.k - k0;
     if (left < 0) left = 0;
-    if (left > kSlot) left = kSlot;
+    if (left > kStage) left = kStage;
     left = __builtin_amdgcn_readfirstlane(left);  // uniform, kept in a scalar register
     lds += wave * kLoads * 1024;
     if constexpr (!COLS) {
       const char* p = (const char*)o.base + 2 * (int64_t)k0;
       const uint32_t bytes = left ? (uint32_t)((int64_t)(o.count - 1) * o.ld + 2 * left) : 0u;
       const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
-      const int row = wave * kLoads * 16 + (lane >> 2);
-      const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
-      const uint32_t inc = (uint32_t)(16 * o.ld);
-      const uint32_t v = (uint32_t)((int64_t)row * o.ld) + 16 * chunk;
+      int row = wave * kLoads * 8;
+      if constexpr (HALF >= 0) row = row / 64 * 128 + 64 * HALF + row % 64;
+      const int chunk = (lane & 7) ^ ((lane >> 4) & 3);
+      const uint32_t v = (uint32_t)((int64_t)(row + (lane >> 3)) * o.ld);
+      const uint32_t inc = (uint32_t)(8 * o.ld);
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
+        const int c = chunk ^ ((j & 1) << 2);  // the 8 rows of every second load have bit 3 set
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rsrc, (__attribute__((address_space(3))) void*)(lds + j * 1024), 16,
-            chunk * 8 < left ? v + j * inc : 0x80000000u, 0, 0, 0);
+            c * 8 < left ? v + j * inc + 16 * c : 0x80000000u, 0, 0, 0);
       }
     } else {
       const char* p = (const char*)o.base + (int64_t)k0 * o.ld;
@@ -133,43 +131,41 @@ struct Stage {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         const int k = (wave * kLoads + j) * kLoadRows + lane / kChunks;
-        const int q = lane % kChunks;
-        const int f = swizzle<R>(k & 3, (k >> 3) & 1);
-        const int chunk = (((q >> 1) ^ f) << 1) | (q & 1);
-        const uint32_t v = (uint32_t)((int64_t)k * o.ld) + 16 * chunk;
+        const int q = (lane % kChunks) ^ (k & 3) << 2;
+        const int col = HALF < 0 ? 16 * q : (q >> 3) * 256 + 128 * HALF + 16 * (q & 7);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rsrc, (__attribute__((address_space(3))) void*)(lds + j * 1024), 16, v, 0, 0, 0);
+            rsrc, (__attribute__((address_space(3))) void*)(lds + j * 1024), 16,
+            (uint32_t)((int64_t)k * o.ld) + col, 0, 0, 0);
       }
     }
   }
 };
 
-// Fragments of F 32-row blocks, rows r0 .. r0 + 32F of the tile, at slice s
-// (16 contraction elements) of a slot: lane l holds row l % 32, elements
+// Fragments of two 32-row blocks, local rows r0 .. r0 + 64 of a part, at slice
+// s (16 contraction elements) of a stage: lane l holds row l % 32, elements
 // (l / 32) * 8 .. + 8.
-template <int R, bool COLS, int F>
+template <int R, bool COLS>
 struct Frags {
-  int base[COLS ? F : 2];
+  int base[COLS ? 2 : 4];
   __device__ __forceinline__ Frags(int r0, int lane) {
     if constexpr (!COLS) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        base[s] = (r0 + (lane & 31)) * (kSlot * 2) +
-                  16 * ((s * 2 + (lane >> 5)) ^ ((lane >> 2) & 3));
+      for (int s = 0; s < 4; ++s)
+        base[s] = (r0 + (lane & 31)) * (kStage * 2) +
+                  16 * ((s * 2 + (lane >> 5)) ^ ((lane >> 1) & 7));
     } else {
+      const int g = lane >> 4, j = lane & 15;
+      const int k = (g >> 1) * 8 + (j >> 2);
 #pragma unroll
-      for (int i = 0; i < F; ++i) {
-        const int g = lane >> 4, j = lane & 15;
-        const int k = (g >> 1) * 8 + (j >> 2);
-        const int f = swizzle<R>(j >> 2, g >> 1);
-        const int pair = (r0 >> 4) + 2 * i + (g & 1);
-        base[i] = k * (R * 2) + ((pair ^ f) << 5) + (j & 3) * 8;
+      for (int i = 0; i < 2; ++i) {
+        const int pair = ((r0 >> 4) + 2 * i + (g & 1)) ^ 2 * (j >> 2);
+        base[i] = k * (R * 2) + (pair << 5) + (j & 3) * 8;
       }
     }
   }
   __device__ __forceinline__ s16x8 load(const lds_char* lds, int i, int s) const {
     if constexpr (!COLS) {
-      return *(const __attribute__((address_space(3))) s16x8*)(lds + base[s] + i * 32 * kSlot * 2);
+      return *(const __attribute__((address_space(3))) s16x8*)(lds + base[s] + i * 32 * kStage * 2);
     } else {
       typedef __attribute__((address_space(3))) s16x4 lds4;
       const lds_char* p = lds + base[i] + s * 16 * (R * 2);
@@ -180,90 +176,109 @@ struct Frags {
   }
 };
 
-// The tile: WM x WN waves, each MI x NJ blocks of 32 x 32.  acc[i][j][e] of
-// lane l is row wm*32*MI + 32i + 8(e/4) + 4(l/32) + e%4, column
-// wn*32*NJ + 32j + l%32.
-template <typename T, int WM, int WN, int MI, int NJ, bool ACOLS, bool BCOLS>
+// The stages' memory: separate arrays, so that the compiler does not take a
+// read of one for a reader of loads into another.
+#define ZK_GEMM_LDS                                                                       \
+  __shared__ __attribute__((aligned(1024))) char lds_a00[16384], lds_a10[16384],           \
+      lds_b0[32768], lds_a01[16384], lds_a11[16384], lds_b1[32768];                        \
+  const GemmLds lds{{(lds_char*)lds_a00, (lds_char*)lds_a10, (lds_char*)lds_b0},           \
+                    {(lds_char*)lds_a01, (lds_char*)lds_a11, (lds_char*)lds_b1}}
+struct StageLds {
+  lds_char *a0, *a1, *b;
+};
+struct GemmLds {
+  StageLds even, odd;
+};
+
+// The 256 x 256 tile: 2 x 4 waves, each 4 x 2 blocks of 32 x 32.
+// acc[i][j][e] of lane l is row wm*128 + 32i + 8(e/4) + 4(l/32) + e%4, column
+// wn*64 + 32j + l%32, wm = wave / 4, wn = wave % 4.
+template <typename T, bool ACOLS, bool BCOLS>
 struct Gemm {
-  static constexpr int BM = WM * MI * 32, BN = WN * NJ * 32, WAVES = WM * WN;
-  static constexpr int THREADS = 64 * WAVES;
-  static constexpr int kSlotBytes = (BM + BN) * kSlot * 2;
-  static constexpr int kABytes = BM * kSlot * 2;
-  static_assert(WAVES == 8, "two halves of four waves");
-  using SA = Stage<BM, ACOLS, WAVES>;
-  using SB = Stage<BN, BCOLS, WAVES>;
+  static constexpr int BM = 256, BN = 256, THREADS = 512, MI = 4, NJ = 2;
+  using A0 = Part<128, ACOLS, 0>;
+  using A1 = Part<128, ACOLS, 1>;
+  using SB = Part<256, BCOLS, -1>;
+  using FA = Frags<128, ACOLS>;
+  using FB = Frags<256, BCOLS>;
 
-  static __device__ __forceinline__ void issue(const Operand& A, const Operand& B, int32_t slot,
-                                               lds_char* lds, int wave, int lane) {
-    SA::issue(A, slot * kSlot, lds, wave, lane);
-    SB::issue(B, slot * kSlot, lds + kABytes, wave, lane);
-  }
-
-  // Slot number `slot`, in ring position `lds`; `ahead` is the position three on.
-  static __device__ __forceinline__ void phases(const Operand& A, const Operand& B, int32_t slot,
-                                                lds_char* lds, lds_char* ahead, int wave,
-                                                const Frags<BM, ACOLS, MI>& fa,
-                                                const Frags<BN, BCOLS, NJ>& fb, int lane,
-                                                f32x16 (&acc)[MI][NJ]) {
-    s16x8 ra[2][MI], rb[2][NJ];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) rb[s][j] = fb.load(lds + kABytes, j, s);
-#pragma unroll
-      for (int i = 0; i < MI; ++i) ra[s][i] = fa.load(lds, i, s);
-    }
-    issue(A, B, slot + kSlots - 1, ahead, wave, lane);
-    // this wave has read the slot, and its loads of the next one have landed
-    // (those of the two after it may be on their way)
-    static_assert(2 * (SA::kLoads + SB::kLoads) == 8, "the count below");
-    asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
+  template <int HALF>
+  static __device__ __forceinline__ void multiply(const s16x8 (&ra)[4][2], const s16x8 (&rb)[4][2],
+                                                  f32x16 (&acc)[MI][NJ]) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = mfma(T{}, ra[s][i], rb[s][j], acc[i][j]);
+        for (int j = 0; j < 2; ++j)
+          acc[2 * HALF + i][j] = mfma(T{}, ra[s][i], rb[s][j], acc[2 * HALF + i][j]);
     __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_barrier" ::: "memory");
   }
 
-  // acc = A B^T over K >= 0 contraction indexes.  s0 .. s3: the ring's slots
-  // (separate arrays, so that the compiler does not take a read of one for a
-  // reader of loads into another).  On return every wave is done with LDS.
+  // End of a reading phase: this wave has read what it came for, and its loads
+  // of the part that the next round reads have landed; the 8 issued since may
+  // be on their way.
+  static __device__ __forceinline__ void turn() {
+    static_assert(A1::kLoads + A0::kLoads + SB::kLoads == 8, "loads in flight");
+    asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  static __device__ __forceinline__ void stage(const Operand& A, const Operand& B, int32_t k0,
+                                               const StageLds& here, const StageLds& other,
+                                               int wave, int lane, const FA& fa, const FB& fb,
+                                               f32x16 (&acc)[MI][NJ]) {
+    s16x8 ra[4][2], rb[4][2];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        rb[s][i] = fb.load(here.b, i, s);
+        ra[s][i] = fa.load(here.a0, i, s);
+      }
+    A1::issue(A, k0 + kStage, other.a1, wave, lane);
+    turn();
+    multiply<0>(ra, rb, acc);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) ra[s][i] = fa.load(here.a1, i, s);
+    A0::issue(A, k0 + 2 * kStage, here.a0, wave, lane);
+    SB::issue(B, k0 + 2 * kStage, here.b, wave, lane);
+    turn();
+    multiply<1>(ra, rb, acc);
+  }
+
+  // acc = A B^T over K >= 0 contraction indexes.  On return every wave is done
+  // with LDS.
   static __device__ __forceinline__ void run(const Operand& A, const Operand& B, int32_t K,
-                                             lds_char* s0, lds_char* s1, lds_char* s2,
-                                             lds_char* s3, f32x16 (&acc)[MI][NJ]) {
+                                             const GemmLds& lds, f32x16 (&acc)[MI][NJ]) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int half = wave / 4;
-    const Frags<BM, ACOLS, MI> fa((wave / WN) * MI * 32, lane);
-    const Frags<BN, BCOLS, NJ> fb((wave % WN) * NJ * 32, lane);
+    const FA fa(wave / 4 * 64, lane);
+    const FB fb(wave % 4 * 64, lane);
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16{};
     if (K <= 0) return;
-    issue(A, B, 0, s0, wave, lane);
-    issue(A, B, 1, s1, wave, lane);
-    issue(A, B, 2, s2, wave, lane);
+    A0::issue(A, 0, lds.even.a0, wave, lane);
+    SB::issue(B, 0, lds.even.b, wave, lane);
+    A1::issue(A, 0, lds.even.a1, wave, lane);
+    A0::issue(A, kStage, lds.odd.a0, wave, lane);
+    SB::issue(B, kStage, lds.odd.b, wave, lane);
     asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
-    if (half != 0) asm volatile("s_barrier" ::: "memory");  // one phase behind
-    const int32_t n = (K + kSlot - 1) / kSlot;
-    int32_t t = 0;
-    for (; t + kSlots <= n; t += kSlots) {
-      phases(A, B, t, s0, s3, wave, fa, fb, lane, acc);
-      phases(A, B, t + 1, s1, s0, wave, fa, fb, lane, acc);
-      phases(A, B, t + 2, s2, s1, wave, fa, fb, lane, acc);
-      phases(A, B, t + 3, s3, s2, wave, fa, fb, lane, acc);
+    if (wave >= 4) asm volatile("s_barrier" ::: "memory");  // one phase behind
+    int32_t k0 = 0;
+    for (; k0 + kStage < K; k0 += 2 * kStage) {
+      stage(A, B, k0, lds.even, lds.odd, wave, lane, fa, fb, acc);
+      stage(A, B, k0 + kStage, lds.odd, lds.even, wave, lane, fa, fb, acc);
     }
-    if (t < n) phases(A, B, t, s0, s3, wave, fa, fb, lane, acc);
-    if (t + 1 < n) phases(A, B, t + 1, s1, s0, wave, fa, fb, lane, acc);
-    if (t + 2 < n) phases(A, B, t + 2, s2, s1, wave, fa, fb, lane, acc);
-    if (half == 0) asm volatile("s_barrier" ::: "memory");
+    if (k0 < K) stage(A, B, k0, lds.even, lds.odd, wave, lane, fa, fb, acc);
+    if (wave < 4) asm volatile("s_barrier" ::: "memory");
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
 };

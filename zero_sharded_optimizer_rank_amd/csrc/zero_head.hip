@@ -27,12 +27,7 @@ using namespace dev;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kScanThreads = 1024;
 constexpr int kPackThreads = 256;
-#ifndef ZK_CFG
-#define ZK_CFG 2, 4, 4, 2
-#endif
-constexpr int kCfg[4] = {ZK_CFG};
-constexpr int kWM = kCfg[0], kWN = kCfg[1], kMI = kCfg[2], kNJ = kCfg[3];
-constexpr int kGemmThreads = 64 * kWM * kWN;
+constexpr int kGemmThreads = 512;
 constexpr int kJoinTokens = 64, kJoinWaves = 4;
 
 // g's scale before it is rounded: |p - [v = y]| <= 1, so 2^15 keeps fp16 in
@@ -154,20 +149,19 @@ __global__ __launch_bounds__(kPackThreads) void k_head_zero_dx(
 // --- 2. the logits' tiles ------------------------------------------------------
 // A = w (vocabulary rows), B = packed x (token rows), both contiguous along
 // the hidden axis.
-template <typename T, int WM, int WN, int MI, int NJ>
+template <typename T>
 struct LogitTile {
-  using G = Gemm<T, WM, WN, MI, NJ, false, false>;
+  using G = Gemm<T, false, false>;
 
   static __device__ __forceinline__ bool run(const uint16_t* w, int64_t ldw, int64_t v0,
                                              int32_t vocab, const uint16_t* x, int32_t t0,
                                              int32_t hidden_pad, int32_t K,
-                                             f32x16 (&acc)[MI][NJ]) {
-    __shared__ __attribute__((aligned(1024))) char s0[G::kSlotBytes], s1[G::kSlotBytes],
-      s2[G::kSlotBytes], s3[G::kSlotBytes];
+                                             f32x16 (&acc)[G::MI][G::NJ]) {
+    ZK_GEMM_LDS;
     const int64_t rows = vocab - v0;
     const Operand A{w + v0 * ldw, ldw * 2, (int32_t)(rows < G::BM ? rows : G::BM), K};
     const Operand B{x + (int64_t)t0 * hidden_pad, (int64_t)hidden_pad * 2, G::BN, K};
-    G::run(A, B, K, (lds_char*)s0, (lds_char*)s1, (lds_char*)s2, (lds_char*)s3, acc);
+    G::run(A, B, K, lds, acc);
     return true;
   }
 };
@@ -176,28 +170,29 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 
 // Loss: (max, sum of exp(l - max)) of every token over each 128 vocabulary
 // rows, and the label's logit.
-template <typename T, int WM, int WN, int MI, int NJ>
-__global__ __launch_bounds__(64 * WM * WN) void k_head_partials(
+template <typename T>
+__global__ __launch_bounds__(kGemmThreads) void k_head_partials(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, const uint16_t* __restrict__ x,
     int32_t hidden_pad, int32_t K, int32_t tokens_pad, const int32_t* __restrict__ label,
     const HeadState* __restrict__ state, float2* __restrict__ part, float* __restrict__ picked) {
-  using L = LogitTile<T, WM, WN, MI, NJ>;
+  using L = LogitTile<T>;
   using G = typename L::G;
-  static_assert(MI * 32 == kHeadPart, "one partial a wave");
+  static_assert(G::MI * 32 == kHeadPart, "one partial a wave");
   int32_t mt, nt;
   if (!tile_of(blockIdx.x, (uint32_t)((vocab + G::BM - 1) / G::BM),
                (uint32_t)((state->valid + G::BN - 1) / G::BN), mt, nt))
     return;
   const int32_t t0 = nt * G::BN;
   const int64_t v0 = (int64_t)mt * G::BM;
+  constexpr int MI = G::MI, NJ = G::NJ;
   f32x16 acc[MI][NJ];
   L::run(w, ldw, v0, vocab, x, t0, hidden_pad, K, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t vw = v0 + (wave / WN) * MI * 32;  // the wave's first vocabulary row
+  const int64_t vw = v0 + (wave / 4) * MI * 32;  // the wave's first vocabulary row
   const int32_t rows = (int32_t)(vocab - vw < MI * 32 ? vocab - vw : MI * 32);
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int32_t t = t0 + (wave % WN) * NJ * 32 + j * 32 + (lane & 31);
+    const int32_t t = t0 + (wave % 4) * NJ * 32 + j * 32 + (lane & 31);
     const int64_t y = t < state->valid ? (int64_t)label[t] - vw : -1;
     float m = -INFINITY;
 #pragma unroll
@@ -315,13 +310,13 @@ __global__ __launch_bounds__(kPackThreads) void k_head_ignored(
 // --- 4. gradient -----------------------------------------------------------------
 // g of a piece: rows are packed tokens, columns the piece's vocabulary rows;
 // columns past the vocabulary and rows past the valid tokens are zero.
-template <typename T, int WM, int WN, int MI, int NJ>
-__global__ __launch_bounds__(64 * WM * WN) void k_head_g(
+template <typename T>
+__global__ __launch_bounds__(kGemmThreads) void k_head_g(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, const uint16_t* __restrict__ x,
     int32_t hidden_pad, int32_t K, const int32_t* __restrict__ label,
     const float* __restrict__ lse, const HeadState* __restrict__ state, int64_t piece0,
     int32_t piece, uint16_t* __restrict__ g) {
-  using L = LogitTile<T, WM, WN, MI, NJ>;
+  using L = LogitTile<T>;
   using G = typename L::G;
   const int32_t valid = state->valid;
   const int32_t left = vocab - piece0 < piece ? (int32_t)(vocab - piece0) : piece;
@@ -332,14 +327,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_g(
   const int32_t t0 = nt * G::BN;
   const int32_t c0 = mt * G::BM;  // column of g
   const int64_t v0 = piece0 + c0;
+  constexpr int MI = G::MI, NJ = G::NJ;
   f32x16 acc[MI][NJ];
   L::run(w, ldw, v0, vocab, x, t0, hidden_pad, K, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int32_t cw = c0 + (wave / WN) * MI * 32;
+  const int32_t cw = c0 + (wave / 4) * MI * 32;
   const int32_t rows = left - cw;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int32_t t = t0 + (wave % WN) * NJ * 32 + j * 32 + (lane & 31);
+    const int32_t t = t0 + (wave % 4) * NJ * 32 + j * 32 + (lane & 31);
     const bool there = t < valid;
     const float z = there ? lse[t] : 0.0f;
     const int64_t y = there ? (int64_t)label[t] - piece0 - cw : -1;
@@ -363,14 +359,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_g(
 
 // dx: A = g (token rows, contiguous along the vocabulary), B = w (contiguous
 // along the hidden axis).  Split s of the piece adds into its own fp32 block.
-template <typename T, int WM, int WN, int MI, int NJ>
-__global__ __launch_bounds__(64 * WM * WN) void k_head_dx(
+template <typename T>
+__global__ __launch_bounds__(kGemmThreads) void k_head_dx(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ w, int64_t ldw,
     int32_t vocab_left, int32_t hidden_w, int32_t hidden, int32_t hidden_pad, int32_t tokens_pad,
     int32_t split, int32_t part, int32_t first, const HeadState* __restrict__ state, float* __restrict__ acc_out) {
-  using G = Gemm<T, WM, WN, MI, NJ, false, true>;
-  __shared__ __attribute__((aligned(1024))) char s0[G::kSlotBytes], s1[G::kSlotBytes],
-      s2[G::kSlotBytes], s3[G::kSlotBytes];
+  using G = Gemm<T, false, true>;
+  ZK_GEMM_LDS;
   const uint32_t ht = (uint32_t)((hidden + G::BN - 1) / G::BN);
   int32_t mt, nt;
   if (!tile_of(blockIdx.x, (uint32_t)((state->valid + G::BM - 1) / G::BM), ht * (uint32_t)split,
@@ -382,13 +377,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_dx(
   // g's columns are zero from the vocabulary's end to the next tile
   const Operand A{g + (int64_t)t0 * piece + k0, (int64_t)piece * 2, G::BM, (K + 7) & ~7};
   const Operand B{w + (int64_t)k0 * ldw + h0, ldw * 2, hidden_w - h0, K};
+  constexpr int MI = G::MI, NJ = G::NJ;
   f32x16 acc[MI][NJ];
-  G::run(A, B, K, (lds_char*)s0, (lds_char*)s1, (lds_char*)s2, (lds_char*)s3, acc);
+  G::run(A, B, K, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float* out = acc_out + ((int64_t)ks * tokens_pad + t0 + (wave / WN) * MI * 32) * hidden_pad;
+  float* out = acc_out + ((int64_t)ks * tokens_pad + t0 + (wave / 4) * MI * 32) * hidden_pad;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int32_t h = h0 + (wave % WN) * NJ * 32 + j * 32 + (lane & 31);
+    const int32_t h = h0 + (wave % 4) * NJ * 32 + j * 32 + (lane & 31);
     if (h >= hidden_pad) continue;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -422,14 +418,13 @@ __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
 
 // dw: A = g, B = packed x, both contiguous along their rows; the contraction
 // runs over the tokens.
-template <typename T, int WM, int WN, int MI, int NJ, bool F32OUT>
-__global__ __launch_bounds__(64 * WM * WN) void k_head_dw(
+template <typename T, bool F32OUT>
+__global__ __launch_bounds__(kGemmThreads) void k_head_dw(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ x,
     int32_t hidden_pad, int32_t hidden, int32_t vocab_left, const HeadState* __restrict__ state,
     int32_t accumulate, void* __restrict__ dw, int64_t lddw) {
-  using G = Gemm<T, WM, WN, MI, NJ, true, true>;
-  __shared__ __attribute__((aligned(1024))) char s0[G::kSlotBytes], s1[G::kSlotBytes],
-      s2[G::kSlotBytes], s3[G::kSlotBytes];
+  using G = Gemm<T, true, true>;
+  ZK_GEMM_LDS;
   int32_t mt, nt;
   if (!tile_of(blockIdx.x, (uint32_t)((vocab_left + G::BM - 1) / G::BM),
                (uint32_t)((hidden + G::BN - 1) / G::BN), mt, nt))
@@ -439,20 +434,21 @@ __global__ __launch_bounds__(64 * WM * WN) void k_head_dw(
   const float c = state->coef / g_scale<T>();
   const Operand A{g + c0, (int64_t)piece * 2, piece - c0, K};
   const Operand B{x + h0, (int64_t)hidden_pad * 2, hidden_pad - h0, K};
+  constexpr int MI = G::MI, NJ = G::NJ;
   f32x16 acc[MI][NJ];
-  G::run(A, B, K, (lds_char*)s0, (lds_char*)s1, (lds_char*)s2, (lds_char*)s3, acc);
+  G::run(A, B, K, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const bool bad = state->bad != 0;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int32_t h = h0 + (wave % WN) * NJ * 32 + j * 32 + (lane & 31);
+    const int32_t h = h0 + (wave % 4) * NJ * 32 + j * 32 + (lane & 31);
     if (h >= hidden) continue;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       asm volatile("" ::: "memory");
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int32_t v = c0 + (wave / WN) * MI * 32 + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+        const int32_t v = c0 + (wave / 4) * MI * 32 + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
         if (v >= vocab_left) continue;
         const int64_t at = (int64_t)v * lddw + h;
         // bad labels alone (no valid token) still have to show
@@ -498,7 +494,7 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
   const WeightView w = weight_view(h, p, ws);
   HeadState* state = at<HeadState>(ws, p.state);
   if (h->tokens > 0) {
-    hipLaunchKernelGGL((k_head_partials<T, kWM, kWN, kMI, kNJ>),
+    hipLaunchKernelGGL(k_head_partials<T>,
                        dim3(tile_grid(p.tokens_pad / 256, (h->vocab + 255) / 256)),
                        dim3(kGemmThreads), 0, stream, w.w, w.ld, (int32_t)h->vocab,
                        at<const uint16_t>(ws, p.x), (int32_t)p.hidden_pad, w.K,
@@ -535,12 +531,12 @@ int grad_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_gr
     const int64_t left = h->vocab - v0 < p.piece ? h->vocab - v0 : p.piece;
     const uint32_t vtiles = (uint32_t)((left + 255) / 256);
     if (h->tokens > 0) {
-      hipLaunchKernelGGL((k_head_g<T, kWM, kWN, kMI, kNJ>), dim3(tile_grid(ttiles, vtiles)), dim3(kGemmThreads), 0, stream,
+      hipLaunchKernelGGL(k_head_g<T>, dim3(tile_grid(ttiles, vtiles)), dim3(kGemmThreads), 0, stream,
                          w.w, w.ld, (int32_t)h->vocab, x, (int32_t)p.hidden_pad, w.K,
                          at<const int32_t>(ws, p.label), at<const float>(ws, p.lse), state, v0,
                          (int32_t)p.piece, g);
       ZK_LAUNCHED();
-      hipLaunchKernelGGL((k_head_dx<T, kWM, kWN, kMI, kNJ>), dim3(tile_grid(htiles * p.split, ttiles)),
+      hipLaunchKernelGGL(k_head_dx<T>, dim3(tile_grid(htiles * p.split, ttiles)),
                          dim3(kGemmThreads), 0, stream, g, (int32_t)p.piece, w.w + v0 * w.ld, w.ld,
                          (int32_t)left, w.width, (int32_t)h->hidden, (int32_t)p.hidden_pad,
                          (int32_t)p.tokens_pad, p.split, part, v0 == 0 ? 1 : 0, state, acc);
@@ -549,11 +545,11 @@ int grad_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_gr
     const size_t ew = gr->dw_dtype == ZERO_F32 ? 4 : 2;
     void* dw = (char*)gr->dw + ew * (size_t)(v0 * gr->lddw);
     if (gr->dw_dtype == ZERO_F32)
-      hipLaunchKernelGGL((k_head_dw<T, kWM, kWN, kMI, kNJ, true>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads), 0,
+      hipLaunchKernelGGL((k_head_dw<T, true>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads), 0,
                          stream, g, (int32_t)p.piece, x, (int32_t)p.hidden_pad,
                          (int32_t)h->hidden, (int32_t)left, state, gr->accumulate, dw, gr->lddw);
     else
-      hipLaunchKernelGGL((k_head_dw<T, kWM, kWN, kMI, kNJ, false>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads), 0,
+      hipLaunchKernelGGL((k_head_dw<T, false>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads), 0,
                          stream, g, (int32_t)p.piece, x, (int32_t)p.hidden_pad,
                          (int32_t)h->hidden, (int32_t)left, state, gr->accumulate, dw, gr->lddw);
     ZK_LAUNCHED();
