@@ -758,7 +758,8 @@ int zero_head_loss(const zero_head_t* head, float* token_loss, float* lse, void*
 /*
  * zero_head_grad: the gradients, from the lse that zero_head_loss wrote for
  * the same x, w and labels.  The logits are formed again, one piece of the
- * vocabulary at a time; exp(l - lse) - [v = y] is rounded once to the type of
+ * vocabulary at a time (as many rows as keep the workspace's block for a piece
+ * within 1 GiB); exp(l - lse) - [v = y] is rounded once to the type of
  * x and w (fp16: scaled by 2^15 first, so that small probabilities stay in
  * range), and both products accumulate in fp32 and are rounded once.
  *   lse         device [T] fp32, 4-byte aligned
@@ -769,8 +770,13 @@ int zero_head_loss(const zero_head_t* head, float* token_loss, float* lse, void*
 int zero_head_grad(const zero_head_t* head, const float* lse, const zero_head_grads_t* grads,
                    void* workspace, size_t ws_bytes, hipStream_t stream);
 
-/* zero_head_loss_grad: zero_head_loss then zero_head_grad on the same stream
- * (training); lse may be NULL.  workspace >= zero_head_workspace_bytes(head, 1). */
+/* zero_head_loss_grad: zero_head_loss and zero_head_grad in one call
+ * (training); lse may be NULL.  workspace >= zero_head_workspace_bytes(head, 1).
+ * The loss is that of zero_head_loss bit for bit.  The gradients need fewer
+ * logits a second time: the last piece's exponentials stay where its g will be,
+ * rounded to the 16-bit type, and are multiplied by e^(max - lse) and rounded
+ * once more (the label's element alone comes from its fp32 logit), so a
+ * probability there has two roundings instead of one. */
 int zero_head_loss_grad(const zero_head_t* head, float* token_loss, float* lse,
                         const zero_head_grads_t* grads, void* workspace, size_t ws_bytes,
                         zero_loss_result_t* dev_result, hipStream_t stream);

@@ -12,7 +12,8 @@ lse        the exponentials are off by a relative eexp <= 4e + 2e |l - m| (the p
            |dlse| <= max|dl| + eexp + (V + 64) e + 4e (|lse| + |m| + 2)
 loss       |dloss| <= |dlse| + |dl at the label| + 4e (|lse| + |l|)
 p          relative r = |dl| + |dlse| + 4e + 4e |l - lse|
-g          |dg| <= u |d| + p r (1 + u) + e |d|, plus half the type's smallest step (fp16, 2^-25 after
+g          |dg| <= u |d| + p (r + u) (1 + u) + e |d|: one rounding of the difference and, where
+           the exponentials were kept, one of the probability before it; plus half the type's smallest step (fp16, 2^-25 after
            the scale of 2^15)
 dx         |g|'s error through |w|, the sum's V e (|g| |w|), the scaling 2e |dx|, the output's u |dx|
            plus half its smallest step
@@ -62,7 +63,7 @@ def reference(x, w, y, loss_scale=1.0, mean=True):
     d[rows, yk] -= 1.0
     r = dl + dlse[:, None] + 4 * E + 4 * E * (l - lse[:, None]).abs()
     floor = tiny * 2.0 ** -15 if dt == torch.float16 else tiny
-    dg = u * d.abs() + p * r * (1 + u) + E * d.abs() + floor
+    dg = u * d.abs() + p * (r + u) * (1 + u) + E * d.abs() + 2 * floor
     g = d.abs() + dg
     dxk = c * (d @ wk)
     bx = c * (dg @ wk.abs() + V * E * (g @ wk.abs())) + (2 * E + u) * dxk.abs()

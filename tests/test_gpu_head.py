@@ -145,7 +145,7 @@ def test_weight_gradient_forms(dtype, out, accumulate):
 @pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
 def test_several_pieces_of_the_vocabulary(dtype):
     """Enough tokens that the vocabulary is taken in several pieces."""
-    T, V, H = 33_000, 9_001, 72
+    T, V, H = 70_000, 9_001, 72
     x, w, y = _inputs(T, V, H, dtype, seed=4, ignored=0.1)
     ref = reference(x, w, y, loss_scale=1024.0)
     r = _head(T, V, H, dtype).loss_grad(x, w, y, loss_scale=1024.0)
@@ -157,20 +157,24 @@ def test_several_pieces_of_the_vocabulary(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
-def test_separate_calls_equal_the_joint_one(dtype):
+def test_separate_calls_and_repeated_ones(dtype):
     T, V, H = 200, 1500, 328
     x, w, y = _inputs(T, V, H, dtype, seed=6, ignored=0.2)
+    ref = reference(x, w, y, loss_scale=64.0)
     h = _head(T, V, H, dtype)
     r = h.loss_grad(x, w, y, loss_scale=64.0)
     dx, dw, lse = r.dx.clone(), r.dw.clone(), r.lse.clone()
-    first = h.loss(x, w, y)
-    assert torch.equal(first.lse, lse)
+    assert torch.equal(h.loss(x, w, y).lse, lse)
     h2 = _head(T, V, H, dtype)
     dx2, dw2 = h2.grad(x, w, y, lse, loss_scale=64.0)
-    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    check(dx2, *ref["dx"], "dx")
+    check_dw(dw2, ref)
+    dx2, dw2 = dx2.clone(), dw2.clone()
     for _ in range(3):  # equal inputs give equal bits
         r = h.loss_grad(x, w, y, loss_scale=64.0)
         assert torch.equal(r.dx, dx) and torch.equal(r.dw, dw) and torch.equal(r.lse, lse)
+        a, b = h2.grad(x, w, y, lse, loss_scale=64.0)
+        assert torch.equal(a, dx2) and torch.equal(b, dw2)
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])

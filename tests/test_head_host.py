@@ -97,7 +97,7 @@ def test_workspace_bytes():
     big = dict(tokens=8192, hidden=4096, vocab=128256, ldx=4096, ldw=4096)
     # far less than the logits (fp32 4.2 GB, 16-bit 2.1 GB)
     assert need(False, **big) < 0.2e9
-    assert need(True, **big) < 1.0e9
+    assert need(True, **big) < 1.6e9
     # a w whose rows do not start on 16-byte boundaries is laid out once more
     copy = 2 * 128256 * 4096
     assert copy <= need(False, **dict(big, w=W + 2)) - need(False, **big) <= copy + 256

@@ -19,7 +19,8 @@ struct HeadPlan {
   int64_t hidden_pad;  // hidden rounded up to a step: row length of the packed x (and w)
   int64_t parts;       // softmax partials a token gets (one per kHeadPart vocabulary rows)
   int64_t piece;       // vocabulary rows a piece of the gradient takes (whole tiles)
-  int32_t split;       // ways the hidden gradient's contraction is split
+  int64_t kept;        // first row of the last piece
+  int32_t split;       // most ways the hidden gradient's contraction is split
   bool pack_w;         // w's rows do not start on 16-byte boundaries
   // offsets
   size_t state, sums, index, label, lse, x, w, part, picked, g, acc, total;
@@ -37,13 +38,16 @@ struct HeadState {  // at offset `state`
 HeadPlan head_plan(const zero_head_t* h, bool grad);
 
 // Launchers: arguments already validated.  Return hipSuccess or the error.
-// lse_in: NULL when the loss runs in the same call (the packed lse is then
-// already in the workspace).
+// pack: lse_in is NULL when the loss runs in the same call; token_loss and lse
+// (of ignored tokens, where not NULL) and grads' dx rows of theirs are written.
+// loss: keep leaves the last piece's exponentials for the gradient; grad: kept
+// says that they are there.
 int launch_head_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse_in,
-                     const zero_head_grads_t* grads, hipStream_t stream);
+                     float* token_loss, float* lse, const zero_head_grads_t* grads,
+                     hipStream_t stream);
 int launch_head_loss(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
-                     float* lse, zero_loss_result_t* res, hipStream_t stream);
+                     float* lse, bool keep, zero_loss_result_t* res, hipStream_t stream);
 int launch_head_grad(const zero_head_t* h, const HeadPlan& p, void* ws,
-                     const zero_head_grads_t* grads, hipStream_t stream);
+                     const zero_head_grads_t* grads, bool kept, hipStream_t stream);
 
 }  // namespace zk

@@ -93,16 +93,22 @@ HeadPlan head_plan(const zero_head_t* h, bool grad) {
   p.pack_w = h->hidden % 8 != 0 || h->ldw % 8 != 0 || !aligned(h->w, 16);
   const int64_t vocab_pad = up(h->vocab, kHeadTile);
   if (grad) {
-    // a piece's gradient block stays near 256 MiB
-    int64_t piece = ((int64_t)1 << 27) / p.tokens_pad / kHeadTile * kHeadTile;
+    // a piece's block of g stays within 1 GiB: with all 128256 rows of a
+    // Llama-3 head up to 4096 tokens go in one piece, whose logits are formed
+    // once, and every further doubling of the tokens halves the piece
+    int64_t piece = ((int64_t)1 << 29) / p.tokens_pad / kHeadTile * kHeadTile;
     if (piece < 16 * kHeadTile) piece = 16 * kHeadTile;
     if (piece > vocab_pad) piece = vocab_pad;
     const int64_t pieces = (vocab_pad + piece - 1) / piece;
     p.piece = up((vocab_pad + pieces - 1) / pieces, kHeadTile);
+    p.kept = (h->vocab - 1) / p.piece * p.piece;
+    // dx: up to four rounds of the 256 CUs (how many is settled on the device,
+    // which knows the valid tokens)
     const int64_t tiles = p.tokens_pad / kHeadTile * (up(h->hidden, kHeadTile) / kHeadTile);
-    int64_t split = 512 / tiles;
+    int64_t split = (1024 + tiles - 1) / tiles;
+    if (split > 64) split = 64;
     if (split > p.piece / kHeadTile) split = p.piece / kHeadTile;
-    p.split = split < 1 ? 1 : (int32_t)split;
+    p.split = (int32_t)split;
   }
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -118,16 +124,12 @@ HeadPlan head_plan(const zero_head_t* h, bool grad) {
   p.picked = take(4 * (size_t)p.tokens_pad);
   p.x = take(2 * (size_t)p.tokens_pad * (size_t)p.hidden_pad);
   p.w = take(p.pack_w ? 2 * (size_t)h->vocab * (size_t)p.hidden_pad : 0);
-  // the loss's partials and the gradient's blocks are never alive together
-  const size_t shared = at;
   p.part = take(8 * (size_t)p.parts * (size_t)p.tokens_pad);
-  p.total = at;
   if (grad) {
-    at = shared;
     p.g = take(2 * (size_t)p.tokens_pad * (size_t)p.piece);
     p.acc = take(4 * (size_t)p.split * (size_t)p.tokens_pad * (size_t)p.hidden_pad);
-    if (at > p.total) p.total = at;
   }
+  p.total = at;
   return p;
 }
 
@@ -148,8 +150,8 @@ int zero_head_loss(const zero_head_t* head, float* token_loss, float* lse, void*
   if (!rc) rc = check_workspace(head, false, workspace, ws_bytes);
   if (rc) return rc;
   const zk::HeadPlan p = zk::head_plan(head, false);
-  int e = zk::launch_head_pack(head, p, workspace, nullptr, nullptr, stream);
-  if (!e) e = zk::launch_head_loss(head, p, workspace, token_loss, lse, dev_result, stream);
+  int e = zk::launch_head_pack(head, p, workspace, nullptr, token_loss, lse, nullptr, stream);
+  if (!e) e = zk::launch_head_loss(head, p, workspace, token_loss, lse, false, dev_result, stream);
   return hip_status(e, "head_loss launch");
 }
 
@@ -163,8 +165,8 @@ int zero_head_grad(const zero_head_t* head, const float* lse, const zero_head_gr
   if (!rc) rc = check_workspace(head, true, workspace, ws_bytes);
   if (rc) return rc;
   const zk::HeadPlan p = zk::head_plan(head, true);
-  int e = zk::launch_head_pack(head, p, workspace, lse, grads, stream);
-  if (!e) e = zk::launch_head_grad(head, p, workspace, grads, stream);
+  int e = zk::launch_head_pack(head, p, workspace, lse, nullptr, nullptr, grads, stream);
+  if (!e) e = zk::launch_head_grad(head, p, workspace, grads, false, stream);
   return hip_status(e, "head_grad launch");
 }
 
@@ -178,9 +180,9 @@ int zero_head_loss_grad(const zero_head_t* head, float* token_loss, float* lse,
   if (!rc) rc = check_workspace(head, true, workspace, ws_bytes);
   if (rc) return rc;
   const zk::HeadPlan p = zk::head_plan(head, true);
-  int e = zk::launch_head_pack(head, p, workspace, nullptr, grads, stream);
-  if (!e) e = zk::launch_head_loss(head, p, workspace, token_loss, lse, dev_result, stream);
-  if (!e) e = zk::launch_head_grad(head, p, workspace, grads, stream);
+  int e = zk::launch_head_pack(head, p, workspace, nullptr, token_loss, lse, grads, stream);
+  if (!e) e = zk::launch_head_loss(head, p, workspace, token_loss, lse, true, dev_result, stream);
+  if (!e) e = zk::launch_head_grad(head, p, workspace, grads, true, stream);
   return hip_status(e, "head_loss_grad launch");
 }
 

@@ -9,10 +9,12 @@
 //      registers; the tile leaves only (max, sum of exp) per token and 128
 //      vocabulary rows, and the label's logit;
 //   3. those partials are joined into lse and the loss;
-//   4. gradient, piece by piece: the logits again, turned into
-//      g = exp(l - lse) - [v = y] in 16 bits (the type the matrix cores
-//      multiply), then dx += g w (fp32 between pieces) and dw = g^T x.
-// All four products accumulate in fp32.
+//   4. gradient, piece by piece: g = exp(l - lse) - [v = y] in 16 bits (the
+//      type the matrix cores multiply), then dx += g w (fp32 between pieces)
+//      and dw = g^T x.  The piece that the loss formed last has its
+//      exponentials in g's block already; the logits of the others are formed
+//      again.
+// All products accumulate in fp32.
 #include <stddef.h>
 
 #include "head_gemm.h"
@@ -28,7 +30,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kScanThreads = 1024;
 constexpr int kPackThreads = 256;
 constexpr int kGemmThreads = 512;
-constexpr int kJoinTokens = 64, kJoinWaves = 4;
+constexpr int kJoinTokens = 64, kJoinWaves = 16, kJoinBatch = 8;
 
 // g's scale before it is rounded: |p - [v = y]| <= 1, so 2^15 keeps fp16 in
 // range and p down to 2^-29 normal; bf16 has fp32's exponents.
@@ -107,13 +109,28 @@ __device__ __forceinline__ u32x4 take8(const uint16_t* p, int64_t n, bool whole1
   return v;
 }
 
-// Packed x: workgroup r copies valid token index[r], zero-padded; rows from
-// the valid count to the next whole tile are zero.
+// Workgroup r: packed row r copies valid token index[r], zero-padded (rows from
+// the valid count to the next whole tile are zero); and if token r takes no
+// part, its loss, lse and dx are written.
 __global__ __launch_bounds__(kPackThreads) void k_head_pack_x(
-    const uint16_t* __restrict__ x, int64_t ldx, int32_t hidden, int32_t hidden_pad,
+    const uint16_t* __restrict__ x, int64_t ldx, int32_t tokens, int32_t hidden,
+    int32_t hidden_pad, int32_t vocab, const int64_t* __restrict__ labels,
     const int32_t* __restrict__ index, const HeadState* __restrict__ state,
-    uint16_t* __restrict__ out) {
+    uint16_t* __restrict__ out, float* __restrict__ token_loss, float* __restrict__ lse,
+    uint16_t* __restrict__ dx, int64_t lddx) {
   const int32_t r = blockIdx.x, valid = state->valid;
+  if (r < tokens) {
+    const int64_t y = labels[r];
+    if (y < 0 || y >= vocab) {
+      if (threadIdx.x == 0) {
+        const float v = y < 0 ? 0.0f : __builtin_nanf("");
+        if (token_loss) token_loss[r] = v;
+        if (lse) lse[r] = v;
+      }
+      if (dx)
+        for (int32_t h = threadIdx.x; h < hidden; h += kPackThreads) dx[r * lddx + h] = 0;
+    }
+  }
   if (r >= (valid + kHeadTile - 1) / kHeadTile * kHeadTile) return;
   u32x4* o = (u32x4*)(out + (int64_t)r * hidden_pad);
   const uint16_t* p = r < valid ? x + (int64_t)index[r] * ldx : nullptr;
@@ -135,15 +152,6 @@ __global__ __launch_bounds__(kPackThreads) void k_head_pack_w(
   const bool whole16 = ((uintptr_t)p & 15) == 0;
   for (int32_t c = threadIdx.x; c < hidden_pad / 8; c += kPackThreads)
     o[c] = take8(p + 8 * c, hidden - 8 * c, whole16);
-}
-
-// dx of the tokens that take no part.
-__global__ __launch_bounds__(kPackThreads) void k_head_zero_dx(
-    const int64_t* __restrict__ labels, int32_t vocab, int32_t hidden, uint16_t* __restrict__ dx,
-    int64_t lddx) {
-  const int64_t t = blockIdx.x;
-  if (labels[t] >= 0 && labels[t] < vocab) return;
-  for (int32_t h = threadIdx.x; h < hidden; h += kPackThreads) dx[t * lddx + h] = 0;
 }
 
 // --- 2. the logits' tiles ------------------------------------------------------
@@ -168,13 +176,23 @@ struct LogitTile {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Four consecutive vocabulary rows of a token into g's type.
+template <typename T>
+__device__ __forceinline__ u32x2 narrow4(float a, float b, float c, float d) {
+  return u32x2{narrow<T>(a) | narrow<T>(b) << 16, narrow<T>(c) | narrow<T>(d) << 16};
+}
+
 // Loss: (max, sum of exp(l - max)) of every token over each 128 vocabulary
-// rows, and the label's logit.
+// rows, and the label's logit.  Where the gradient follows in the same call,
+// the exponentials of the piece of the vocabulary that starts at `kept` stay
+// in g's block (rounded to 16 bits): k_head_rescale turns them into g without
+// forming those logits again.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, const uint16_t* __restrict__ x,
     int32_t hidden_pad, int32_t K, int32_t tokens_pad, const int32_t* __restrict__ label,
-    const HeadState* __restrict__ state, float2* __restrict__ part, float* __restrict__ picked) {
+    const HeadState* __restrict__ state, float2* __restrict__ part, float* __restrict__ picked,
+    int64_t kept, int32_t piece, uint16_t* __restrict__ g) {
   using L = LogitTile<T>;
   using G = typename L::G;
   static_assert(G::MI * 32 == kHeadPart, "one partial a wave");
@@ -194,25 +212,36 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
   for (int j = 0; j < NJ; ++j) {
     const int32_t t = t0 + (wave % 4) * NJ * 32 + j * 32 + (lane & 31);
     const int64_t y = t < state->valid ? (int64_t)label[t] - vw : -1;
+    const int r0 = 4 * (lane >> 5);  // element (i, e) is row r0 + 32i + 8(e/4) + e%4
+    if (rows < MI * 32) {  // the vocabulary ends here
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (r0 + 32 * i + 8 * (e >> 2) + (e & 3) >= rows) acc[i][j][e] = -INFINITY;
+    }
+    if (__any(y >= 0 && y < MI * 32)) {  // some token's label is here
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (r0 + 32 * i + 8 * (e >> 2) + (e & 3) == y) picked[t] = acc[i][j][e];
+    }
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int r = 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-        float l = acc[i][j][e];
-        if (r >= rows) l = -INFINITY;
-        acc[i][j][e] = l;
-        m = fmaxf(m, l);
-        if (r == y) picked[t] = l;
-      }
+      for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[i][j][e]);
     m = fmaxf(m, __shfl_xor(m, 32));
     float s = 0.0f;
     if (m > -INFINITY) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s += exp2_fast((acc[i][j][e] - m) * kLog2e);
+        for (int e = 0; e < 16; ++e) {
+          acc[i][j][e] = exp2_fast((acc[i][j][e] - m) * kLog2e);
+          s += acc[i][j][e];
+        }
     }
     // a row of NaN alone has max -inf: it must not pass for an empty one
     if (!(m > -INFINITY)) {
@@ -221,6 +250,20 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           if (acc[i][j][e] != acc[i][j][e]) s = acc[i][j][e];
+    }
+    if (g && vw >= kept) {
+      // rows past the vocabulary and rows of NaN alone: whatever is kept here
+      // k_head_rescale replaces, or multiplies by NaN
+      uint16_t* o = g + (int64_t)t * piece + (vw - kept) + 4 * (lane >> 5);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& v = acc[i][j];
+          *(u32x2*)(o + 32 * i + 8 * q) =
+              narrow4<T>(v[4 * q] * g_scale<T>(), v[4 * q + 1] * g_scale<T>(),
+                         v[4 * q + 2] * g_scale<T>(), v[4 * q + 3] * g_scale<T>());
+        }
     }
     s += __shfl_xor(s, 32);
     if (lane < 32) part[(vw / kHeadPart) * tokens_pad + t] = float2{m, s};
@@ -252,9 +295,15 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
   double loss = 0.0;
   if (r < valid) {
     float m = -INFINITY, s = 0.0f;
-    for (int32_t p = wave; p < parts; p += kJoinWaves) {
-      const float2 q = part[(int64_t)p * tokens_pad + r];
-      join(m, s, q.x, q.y);
+    for (int32_t p = wave; p < parts; p += kJoinWaves * kJoinBatch) {
+      float2 q[kJoinBatch];
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) {
+        q[k] = float2{-INFINITY, 0.0f};
+        if (p + k * kJoinWaves < parts) q[k] = part[(int64_t)(p + k * kJoinWaves) * tokens_pad + r];
+      }
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) join(m, s, q[k].x, q[k].y);
     }
     s_m[wave][lane] = m;
     s_s[wave][lane] = s;
@@ -294,19 +343,6 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
   }
 }
 
-// Loss and lse of the tokens that take no part.
-__global__ __launch_bounds__(kPackThreads) void k_head_ignored(
-    const int64_t* __restrict__ labels, int32_t tokens, int32_t vocab, float* __restrict__ token_loss,
-    float* __restrict__ lse) {
-  const int32_t t = blockIdx.x * kPackThreads + threadIdx.x;
-  if (t >= tokens) return;
-  const int64_t y = labels[t];
-  if (y >= 0 && y < vocab) return;
-  const float v = y < 0 ? 0.0f : __builtin_nanf("");
-  if (token_loss) token_loss[t] = v;
-  if (lse) lse[t] = v;
-}
-
 // --- 4. gradient -----------------------------------------------------------------
 // g of a piece: rows are packed tokens, columns the piece's vocabulary rows;
 // columns past the vocabulary and rows past the valid tokens are zero.
@@ -339,22 +375,94 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_g(
     const bool there = t < valid;
     const float z = there ? lse[t] : 0.0f;
     const int64_t y = there ? (int64_t)label[t] - piece0 - cw : -1;
+    const int r0 = 4 * (lane >> 5);  // element (i, e) is row r0 + 32i + 8(e/4) + e%4
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = exp2_fast((acc[i][j][e] - z) * kLog2e);
+    if (__any(y >= 0 && y < MI * 32)) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (r0 + 32 * i + 8 * (e >> 2) + (e & 3) == y) acc[i][j][e] -= 1.0f;
+    }
+    if (rows < MI * 32 || !__all(there)) {  // the vocabulary's or the tokens' end
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (!there || r0 + 32 * i + 8 * (e >> 2) + (e & 3) >= rows) acc[i][j][e] = 0.0f;
+    }
+    uint16_t* o = g + (int64_t)t * piece + cw + r0;
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int r = 32 * i + 8 * q + 4 * (lane >> 5);
-        uint32_t b[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float p = exp2_fast((acc[i][j][4 * q + e] - z) * kLog2e);
-          if (r + e == y) p -= 1.0f;
-          if (!there || r + e >= rows) p = 0.0f;
-          b[e] = narrow<T>(p * g_scale<T>());
-        }
-        *(u32x2*)(g + (int64_t)t * piece + cw + r) = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
+        const f32x16& v = acc[i][j];
+        *(u32x2*)(o + 32 * i + 8 * q) =
+            narrow4<T>(v[4 * q] * g_scale<T>(), v[4 * q + 1] * g_scale<T>(),
+                       v[4 * q + 2] * g_scale<T>(), v[4 * q + 3] * g_scale<T>());
       }
   }
+}
+
+// g of the piece whose exponentials were kept: e^(l - m) e^(m - lse) - [v = y],
+// m the maximum of the 128 vocabulary rows.  The label's element is formed
+// from its fp32 logit: there 1 is subtracted, and the rounding of the kept
+// value would show.  A workgroup takes 8 tokens (one line of partials) and
+// kRescaleCols columns.
+constexpr int kRescaleCols = 1024;
+template <typename T>
+__global__ __launch_bounds__(256) void k_head_rescale(
+    uint16_t* __restrict__ g, int32_t piece, int32_t left, const float2* __restrict__ part,
+    int32_t part0, int32_t tokens_pad, const int32_t* __restrict__ label, int64_t piece0,
+    const float* __restrict__ lse, const float* __restrict__ picked,
+    const HeadState* __restrict__ state) {
+  const int32_t valid = state->valid;
+  const int32_t t = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (t >= (valid + kHeadTile - 1) / kHeadTile * kHeadTile) return;
+  const bool there = t < valid;
+  const float z = there ? lse[t] : 0.0f;
+  const int64_t y = there ? (int64_t)label[t] - piece0 : -1;
+  const int32_t c1 = (int32_t)(blockIdx.x + 1) * kRescaleCols;
+  for (int32_t c = blockIdx.x * kRescaleCols + (threadIdx.x & 31) * 8; c < c1 && c < piece;
+       c += 256) {
+    if (c >= (left + kHeadTile - 1) / kHeadTile * kHeadTile) return;
+    u32x4* o = (u32x4*)(g + (int64_t)t * piece + c);
+    u32x4 v = {0, 0, 0, 0};
+    if (there && c < left) {
+      const float f =
+          exp2_fast((part[(int64_t)(part0 + c / kHeadPart) * tokens_pad + t].x - z) * kLog2e);
+      v = *o;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float p = widen<T>((v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) * f;
+        if (c + e == y) p = (exp2_fast((picked[t] - z) * kLog2e) - 1.0f) * g_scale<T>();
+        if (c + e >= left) p = 0.0f;
+        const uint32_t b = narrow<T>(p);
+        v[e >> 1] = e & 1 ? (v[e >> 1] & 0xFFFFu) | b << 16 : (v[e >> 1] & 0xFFFF0000u) | b;
+      }
+    }
+    *o = v;
+  }
+}
+
+// Ways to split dx's contraction: the fewest whose tiles come close to filling
+// whole rounds of the 256 CUs (a token count that leaves 208 tiles would
+// idle a fifth of the chip; eight times as many tiles, a twentieth).
+constexpr int32_t kCus = 256;
+__device__ __forceinline__ int32_t dx_split(int32_t tiles, int32_t most) {
+  int32_t best = 1;
+  float cost = 1e30f;
+  for (int32_t s = 1; s <= most; ++s) {
+    const float c = (float)((tiles * s + kCus - 1) / kCus) / (float)s;
+    if (c < 0.97f * cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
 }
 
 // dx: A = g (token rows, contiguous along the vocabulary), B = w (contiguous
@@ -363,14 +471,15 @@ template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_dx(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ w, int64_t ldw,
     int32_t vocab_left, int32_t hidden_w, int32_t hidden, int32_t hidden_pad, int32_t tokens_pad,
-    int32_t split, int32_t part, int32_t first, const HeadState* __restrict__ state, float* __restrict__ acc_out) {
+    int32_t most, int32_t first, const HeadState* __restrict__ state, float* __restrict__ acc_out) {
   using G = Gemm<T, false, true>;
   ZK_GEMM_LDS;
   const uint32_t ht = (uint32_t)((hidden + G::BN - 1) / G::BN);
+  const uint32_t tt = (uint32_t)((state->valid + G::BM - 1) / G::BM);
+  const int32_t split = dx_split((int32_t)(ht * tt), most);
+  const int32_t part = (piece / split + kStage - 1) / kStage * kStage;
   int32_t mt, nt;
-  if (!tile_of(blockIdx.x, (uint32_t)((state->valid + G::BM - 1) / G::BM), ht * (uint32_t)split,
-               mt, nt))
-    return;
+  if (!tile_of(blockIdx.x, tt, ht * (uint32_t)split, mt, nt)) return;
   const int32_t h0 = nt % ht * G::BN, t0 = mt * G::BM, ks = nt / ht, k0 = ks * part;
   int32_t K = piece - k0 < part ? piece - k0 : part;
   if (K > vocab_left - k0) K = vocab_left - k0;
@@ -399,21 +508,25 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dx(
   }
 }
 
-// dx from the splits' sums.
+// dx from the splits' sums, four columns a thread.
 template <typename T>
 __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
-    const float* __restrict__ acc, int32_t split, int32_t tokens_pad, int32_t hidden_pad,
+    const float* __restrict__ acc, int32_t most, int32_t tokens_pad, int32_t hidden_pad,
     int32_t hidden, const int32_t* __restrict__ index, const HeadState* __restrict__ state,
     uint16_t* __restrict__ dx, int64_t lddx) {
-  const int32_t r = blockIdx.x;
-  if (r >= state->valid) return;
+  const int32_t r = blockIdx.y, valid = state->valid;
+  const int32_t h = (blockIdx.x * kPackThreads + threadIdx.x) * 4;
+  if (r >= valid || h >= hidden) return;
+  const int32_t split = dx_split(
+      (int32_t)((valid + kHeadTile - 1) / kHeadTile * ((hidden + kHeadTile - 1) / kHeadTile)), most);
   const float c = state->coef / g_scale<T>();
-  uint16_t* o = dx + (int64_t)index[r] * lddx;
-  for (int32_t h = threadIdx.x; h < hidden; h += kPackThreads) {
-    float s = 0.0f;
-    for (int32_t k = 0; k < split; ++k) s += acc[((int64_t)k * tokens_pad + r) * hidden_pad + h];
-    o[h] = (uint16_t)narrow<T>(s * c);
-  }
+  const float* p = acc + (int64_t)r * hidden_pad + h;
+  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int32_t k = 0; k < split; ++k) s += *(const f32x4*)(p + (int64_t)k * tokens_pad * hidden_pad);
+  uint16_t* o = dx + (int64_t)index[r] * lddx + h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (h + e < hidden) o[e] = (uint16_t)narrow<T>(s[e] * c);
 }
 
 // dw: A = g, B = packed x, both contiguous along their rows; the contraction
@@ -488,9 +601,11 @@ WeightView weight_view(const zero_head_t* h, const HeadPlan& p, void* ws) {
   return {(const uint16_t*)h->w, h->ldw, (int32_t)h->hidden, (int32_t)h->hidden};
 }
 
+// kept: the vocabulary row from which the exponentials stay in g's block, or
+// none if the loss stands alone.
 template <typename T>
 int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss, float* lse,
-           zero_loss_result_t* res, hipStream_t stream) {
+           bool keep, zero_loss_result_t* res, hipStream_t stream) {
   const WeightView w = weight_view(h, p, ws);
   HeadState* state = at<HeadState>(ws, p.state);
   if (h->tokens > 0) {
@@ -499,14 +614,9 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
                        dim3(kGemmThreads), 0, stream, w.w, w.ld, (int32_t)h->vocab,
                        at<const uint16_t>(ws, p.x), (int32_t)p.hidden_pad, w.K,
                        (int32_t)p.tokens_pad, at<const int32_t>(ws, p.label), state,
-                       at<float2>(ws, p.part), at<float>(ws, p.picked));
+                       at<float2>(ws, p.part), at<float>(ws, p.picked), p.kept,
+                       (int32_t)p.piece, keep ? at<uint16_t>(ws, p.g) : nullptr);
     ZK_LAUNCHED();
-    if (token_loss || lse) {
-      hipLaunchKernelGGL(k_head_ignored, dim3((uint32_t)((h->tokens + kPackThreads - 1) / kPackThreads)),
-                         dim3(kPackThreads), 0, stream, h->labels, (int32_t)h->tokens,
-                         (int32_t)h->vocab, token_loss, lse);
-      ZK_LAUNCHED();
-    }
   }
   hipLaunchKernelGGL(k_head_join, dim3((uint32_t)(p.tokens_pad / kJoinTokens)),
                      dim3(64 * kJoinWaves), 0, stream, at<const float2>(ws, p.part),
@@ -517,47 +627,69 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
   return (int)hipGetLastError();
 }
 
+// One piece of the vocabulary, from row v0: g, then its share of dx and its dw.
 template <typename T>
-int grad_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_grads_t* gr,
-           hipStream_t stream) {
+int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_grads_t* gr,
+            int64_t v0, bool have, bool first, hipStream_t stream) {
   const WeightView w = weight_view(h, p, ws);
   HeadState* state = at<HeadState>(ws, p.state);
-  const uint32_t htiles = (uint32_t)((h->hidden + 255) / 256), ttiles = (uint32_t)(p.tokens_pad / 256);
+  const uint32_t htiles = (uint32_t)((h->hidden + 255) / 256);
+  const uint32_t ttiles = (uint32_t)(p.tokens_pad / 256);
   uint16_t* g = at<uint16_t>(ws, p.g);
-  float* acc = at<float>(ws, p.acc);
   const uint16_t* x = at<const uint16_t>(ws, p.x);
-  const int32_t part = (int32_t)((p.piece / p.split + kHeadStep - 1) / kHeadStep * kHeadStep);
-  for (int64_t v0 = 0; v0 < h->vocab; v0 += p.piece) {
-    const int64_t left = h->vocab - v0 < p.piece ? h->vocab - v0 : p.piece;
-    const uint32_t vtiles = (uint32_t)((left + 255) / 256);
-    if (h->tokens > 0) {
-      hipLaunchKernelGGL(k_head_g<T>, dim3(tile_grid(ttiles, vtiles)), dim3(kGemmThreads), 0, stream,
-                         w.w, w.ld, (int32_t)h->vocab, x, (int32_t)p.hidden_pad, w.K,
-                         at<const int32_t>(ws, p.label), at<const float>(ws, p.lse), state, v0,
-                         (int32_t)p.piece, g);
-      ZK_LAUNCHED();
-      hipLaunchKernelGGL(k_head_dx<T>, dim3(tile_grid(htiles * p.split, ttiles)),
-                         dim3(kGemmThreads), 0, stream, g, (int32_t)p.piece, w.w + v0 * w.ld, w.ld,
-                         (int32_t)left, w.width, (int32_t)h->hidden, (int32_t)p.hidden_pad,
-                         (int32_t)p.tokens_pad, p.split, part, v0 == 0 ? 1 : 0, state, acc);
-      ZK_LAUNCHED();
-    }
-    const size_t ew = gr->dw_dtype == ZERO_F32 ? 4 : 2;
-    void* dw = (char*)gr->dw + ew * (size_t)(v0 * gr->lddw);
-    if (gr->dw_dtype == ZERO_F32)
-      hipLaunchKernelGGL((k_head_dw<T, true>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads), 0,
-                         stream, g, (int32_t)p.piece, x, (int32_t)p.hidden_pad,
-                         (int32_t)h->hidden, (int32_t)left, state, gr->accumulate, dw, gr->lddw);
+  const int64_t left = h->vocab - v0 < p.piece ? h->vocab - v0 : p.piece;
+  const uint32_t vtiles = (uint32_t)((left + 255) / 256);
+  const int32_t* label = at<const int32_t>(ws, p.label);
+  const float* lse = at<const float>(ws, p.lse);
+  if (h->tokens > 0) {
+    if (have)
+      hipLaunchKernelGGL(k_head_rescale<T>,
+                         dim3((uint32_t)((left + kRescaleCols - 1) / kRescaleCols),
+                              (uint32_t)(p.tokens_pad / 8)),
+                         dim3(256), 0, stream, g, (int32_t)p.piece, (int32_t)left,
+                         at<const float2>(ws, p.part), (int32_t)(v0 / kHeadPart),
+                         (int32_t)p.tokens_pad, label, v0, lse, at<const float>(ws, p.picked),
+                         state);
     else
-      hipLaunchKernelGGL((k_head_dw<T, false>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads), 0,
-                         stream, g, (int32_t)p.piece, x, (int32_t)p.hidden_pad,
-                         (int32_t)h->hidden, (int32_t)left, state, gr->accumulate, dw, gr->lddw);
+      hipLaunchKernelGGL(k_head_g<T>, dim3(tile_grid(ttiles, vtiles)), dim3(kGemmThreads), 0,
+                         stream, w.w, w.ld, (int32_t)h->vocab, x, (int32_t)p.hidden_pad, w.K,
+                         label, lse, state, v0, (int32_t)p.piece, g);
+    ZK_LAUNCHED();
+    hipLaunchKernelGGL(k_head_dx<T>, dim3(tile_grid(htiles * p.split, ttiles)),
+                       dim3(kGemmThreads), 0, stream, g, (int32_t)p.piece, w.w + v0 * w.ld, w.ld,
+                       (int32_t)left, w.width, (int32_t)h->hidden, (int32_t)p.hidden_pad,
+                       (int32_t)p.tokens_pad, p.split, first ? 1 : 0, state,
+                       at<float>(ws, p.acc));
     ZK_LAUNCHED();
   }
+  const size_t ew = gr->dw_dtype == ZERO_F32 ? 4 : 2;
+  void* dw = (char*)gr->dw + ew * (size_t)(v0 * gr->lddw);
+  if (gr->dw_dtype == ZERO_F32)
+    hipLaunchKernelGGL((k_head_dw<T, true>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads),
+                       0, stream, g, (int32_t)p.piece, x, (int32_t)p.hidden_pad,
+                       (int32_t)h->hidden, (int32_t)left, state, gr->accumulate, dw, gr->lddw);
+  else
+    hipLaunchKernelGGL((k_head_dw<T, false>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads),
+                       0, stream, g, (int32_t)p.piece, x, (int32_t)p.hidden_pad,
+                       (int32_t)h->hidden, (int32_t)left, state, gr->accumulate, dw, gr->lddw);
+  return (int)hipGetLastError();
+}
+
+template <typename T>
+int grad_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_grads_t* gr,
+           bool kept, hipStream_t stream) {
+  // the kept piece lies in g's block: it goes first
+  int e = piece_t<T>(h, p, ws, gr, p.kept, kept, true, stream);
+  for (int64_t v0 = 0; !e && v0 < p.kept; v0 += p.piece)
+    e = piece_t<T>(h, p, ws, gr, v0, false, false, stream);
+  if (e) return e;
   if (h->tokens > 0)
-    hipLaunchKernelGGL((k_head_dx_out<T>), dim3((uint32_t)h->tokens), dim3(kPackThreads), 0,
-                       stream, acc, p.split, (int32_t)p.tokens_pad, (int32_t)p.hidden_pad,
-                       (int32_t)h->hidden, at<const int32_t>(ws, p.index), state,
+    hipLaunchKernelGGL((k_head_dx_out<T>),
+                       dim3((uint32_t)((h->hidden + 4 * kPackThreads - 1) / (4 * kPackThreads)),
+                            (uint32_t)h->tokens),
+                       dim3(kPackThreads), 0, stream, at<const float>(ws, p.acc), p.split,
+                       (int32_t)p.tokens_pad, (int32_t)p.hidden_pad, (int32_t)h->hidden,
+                       at<const int32_t>(ws, p.index), at<HeadState>(ws, p.state),
                        (uint16_t*)gr->dx, gr->lddx);
   return (int)hipGetLastError();
 }
@@ -565,7 +697,8 @@ int grad_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_gr
 }  // namespace
 
 int launch_head_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse_in,
-                     const zero_head_grads_t* gr, hipStream_t stream) {
+                     float* token_loss, float* lse, const zero_head_grads_t* gr,
+                     hipStream_t stream) {
   HeadState* state = at<HeadState>(ws, p.state);
   hipLaunchKernelGGL(k_head_scan, dim3(1), dim3(kScanThreads), 0, stream, h->labels,
                      (int32_t)h->tokens, (int32_t)h->vocab, h->loss_scale, h->mean, lse_in,
@@ -574,15 +707,11 @@ int launch_head_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const fl
   ZK_LAUNCHED();
   if (h->tokens > 0) {
     hipLaunchKernelGGL(k_head_pack_x, dim3((uint32_t)p.tokens_pad), dim3(kPackThreads), 0, stream,
-                       (const uint16_t*)h->x, h->ldx, (int32_t)h->hidden, (int32_t)p.hidden_pad,
-                       at<const int32_t>(ws, p.index), state, at<uint16_t>(ws, p.x));
+                       (const uint16_t*)h->x, h->ldx, (int32_t)h->tokens, (int32_t)h->hidden,
+                       (int32_t)p.hidden_pad, (int32_t)h->vocab, h->labels,
+                       at<const int32_t>(ws, p.index), state, at<uint16_t>(ws, p.x), token_loss,
+                       lse, gr ? (uint16_t*)gr->dx : nullptr, gr ? gr->lddx : 0);
     ZK_LAUNCHED();
-    if (gr) {
-      hipLaunchKernelGGL(k_head_zero_dx, dim3((uint32_t)h->tokens), dim3(kPackThreads), 0, stream,
-                         h->labels, (int32_t)h->vocab, (int32_t)h->hidden, (uint16_t*)gr->dx,
-                         gr->lddx);
-      ZK_LAUNCHED();
-    }
   }
   if (p.pack_w) {
     hipLaunchKernelGGL(k_head_pack_w, dim3((uint32_t)h->vocab), dim3(kPackThreads), 0, stream,
@@ -594,15 +723,15 @@ int launch_head_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const fl
 }
 
 int launch_head_loss(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
-                     float* lse, zero_loss_result_t* res, hipStream_t stream) {
-  return h->dtype == ZERO_BF16 ? loss_t<BF16>(h, p, ws, token_loss, lse, res, stream)
-                               : loss_t<FP16>(h, p, ws, token_loss, lse, res, stream);
+                     float* lse, bool keep, zero_loss_result_t* res, hipStream_t stream) {
+  return h->dtype == ZERO_BF16 ? loss_t<BF16>(h, p, ws, token_loss, lse, keep, res, stream)
+                               : loss_t<FP16>(h, p, ws, token_loss, lse, keep, res, stream);
 }
 
 int launch_head_grad(const zero_head_t* h, const HeadPlan& p, void* ws,
-                     const zero_head_grads_t* gr, hipStream_t stream) {
-  return h->dtype == ZERO_BF16 ? grad_t<BF16>(h, p, ws, gr, stream)
-                               : grad_t<FP16>(h, p, ws, gr, stream);
+                     const zero_head_grads_t* gr, bool kept, hipStream_t stream) {
+  return h->dtype == ZERO_BF16 ? grad_t<BF16>(h, p, ws, gr, kept, stream)
+                               : grad_t<FP16>(h, p, ws, gr, kept, stream);
 }
 
 }  // namespace zk
