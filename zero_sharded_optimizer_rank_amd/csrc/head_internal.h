@@ -21,11 +21,15 @@ struct HeadPlan {
   int64_t piece;       // vocabulary rows a piece of the gradient takes (whole tiles)
   int64_t kept;        // first row of the last piece
   int32_t split;       // most ways the hidden gradient's contraction is split
+  bool few;            // gradient of at most kFewTokens tokens: g in two parts
   bool pack_w;         // w's rows do not start on 16-byte boundaries
   // offsets
-  size_t state, sums, index, label, lse, x, w, part, picked, g, acc, total;
+  size_t state, sums, index, label, lse, x, w, part, picked, g, logits, acc, total;
 };
 constexpr int64_t kHeadPart = 128;
+// With this few tokens g is kept in two 16-bit parts: rows t and kFewTokens + t
+// of the one tile of tokens.
+constexpr int32_t kFewTokens = 64;
 
 struct HeadState {  // at offset `state`
   int32_t valid;

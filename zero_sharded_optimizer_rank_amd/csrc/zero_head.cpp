@@ -101,6 +101,7 @@ HeadPlan head_plan(const zero_head_t* h, bool grad) {
     if (piece > vocab_pad) piece = vocab_pad;
     const int64_t pieces = (vocab_pad + piece - 1) / piece;
     p.piece = up((vocab_pad + pieces - 1) / pieces, kHeadTile);
+    p.few = h->tokens <= kFewTokens && pieces == 1;
     p.kept = (h->vocab - 1) / p.piece * p.piece;
     // dx: up to four rounds of the 256 CUs (how many is settled on the device,
     // which knows the valid tokens)
@@ -127,6 +128,7 @@ HeadPlan head_plan(const zero_head_t* h, bool grad) {
   p.part = take(8 * (size_t)p.parts * (size_t)p.tokens_pad);
   if (grad) {
     p.g = take(2 * (size_t)p.tokens_pad * (size_t)p.piece);
+    p.logits = take(p.few ? 4 * (size_t)kFewTokens * (size_t)p.piece : 0);
     p.acc = take(4 * (size_t)p.split * (size_t)p.tokens_pad * (size_t)p.hidden_pad);
   }
   p.total = at;

@@ -11,8 +11,11 @@
 //   3. those partials are joined into lse and the loss;
 //   4. gradient, piece by piece: g = exp(l - lse) - [v = y] in 16 bits (the
 //      type the matrix cores multiply), then dx += g w (fp32 between pieces)
-//      and dw = g^T x.  The piece that the loss formed last has its
-//      exponentials in g's block already; the logits of the others are formed
+//      and dw = g^T x.  With up to 64 tokens, whose few large elements of g
+//      would show their rounding in the results, g is kept as the sum of two
+//      16-bit parts, which lie in rows of the tile that would be idle.  The
+//      piece that the loss formed last has its
+//      exponentials (or logits) in the workspace already; the logits of the others are formed
 //      again.
 // All products accumulate in fp32.
 #include <stddef.h>
@@ -110,14 +113,15 @@ __device__ __forceinline__ u32x4 take8(const uint16_t* p, int64_t n, bool whole1
 }
 
 // Workgroup r: packed row r copies valid token index[r], zero-padded (rows from
-// the valid count to the next whole tile are zero); and if token r takes no
-// part, its loss, lse and dx are written.
+// the valid count to the next whole tile are zero; with few tokens, rows
+// kFewTokens on hold them a second time); and if token r takes no part, its
+// loss, lse and dx are written.
 __global__ __launch_bounds__(kPackThreads) void k_head_pack_x(
     const uint16_t* __restrict__ x, int64_t ldx, int32_t tokens, int32_t hidden,
     int32_t hidden_pad, int32_t vocab, const int64_t* __restrict__ labels,
     const int32_t* __restrict__ index, const HeadState* __restrict__ state,
-    uint16_t* __restrict__ out, float* __restrict__ token_loss, float* __restrict__ lse,
-    uint16_t* __restrict__ dx, int64_t lddx) {
+    uint16_t* __restrict__ out, int32_t few, float* __restrict__ token_loss,
+    float* __restrict__ lse, uint16_t* __restrict__ dx, int64_t lddx) {
   const int32_t r = blockIdx.x, valid = state->valid;
   if (r < tokens) {
     const int64_t y = labels[r];
@@ -133,7 +137,8 @@ __global__ __launch_bounds__(kPackThreads) void k_head_pack_x(
   }
   if (r >= (valid + kHeadTile - 1) / kHeadTile * kHeadTile) return;
   u32x4* o = (u32x4*)(out + (int64_t)r * hidden_pad);
-  const uint16_t* p = r < valid ? x + (int64_t)index[r] * ldx : nullptr;
+  const int32_t q = few && r >= kFewTokens ? r - kFewTokens : r;
+  const uint16_t* p = q < valid ? x + (int64_t)index[q] * ldx : nullptr;
   const bool whole16 = ((uintptr_t)p & 15) == 0;
   for (int32_t c = threadIdx.x; c < hidden_pad / 8; c += kPackThreads) {
     u32x4 v = {0, 0, 0, 0};
@@ -182,17 +187,24 @@ __device__ __forceinline__ u32x2 narrow4(float a, float b, float c, float d) {
   return u32x2{narrow<T>(a) | narrow<T>(b) << 16, narrow<T>(c) | narrow<T>(d) << 16};
 }
 
+// What the 16-bit value of x leaves.
+template <typename T>
+__device__ __forceinline__ float second(float x) { return x - widen<T>(narrow<T>(x)); }
+
 // Loss: (max, sum of exp(l - max)) of every token over each 128 vocabulary
-// rows, and the label's logit.  Where the gradient follows in the same call,
-// the exponentials of the piece of the vocabulary that starts at `kept` stay
-// in g's block (rounded to 16 bits): k_head_rescale turns them into g without
-// forming those logits again.
+// rows, the label's row left out, and the label's logit: a confident token's
+// loss is log(1 + the others' sum), whose digits a sum that held the label's 1
+// would have lost.  Where the gradient follows in the same call, the
+// exponentials of the piece of the vocabulary that starts at `kept` stay in
+// g's block (rounded to 16 bits), or with few tokens the fp32 logits in
+// `logits`: k_head_rescale turns them into g without forming those logits
+// again.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, const uint16_t* __restrict__ x,
     int32_t hidden_pad, int32_t K, int32_t tokens_pad, const int32_t* __restrict__ label,
     const HeadState* __restrict__ state, float2* __restrict__ part, float* __restrict__ picked,
-    int64_t kept, int32_t piece, uint16_t* __restrict__ g) {
+    int64_t kept, int32_t piece, uint16_t* __restrict__ g, float* __restrict__ logits) {
   using L = LogitTile<T>;
   using G = typename L::G;
   static_assert(G::MI * 32 == kHeadPart, "one partial a wave");
@@ -225,7 +237,20 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
       for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (r0 + 32 * i + 8 * (e >> 2) + (e & 3) == y) picked[t] = acc[i][j][e];
+          if (r0 + 32 * i + 8 * (e >> 2) + (e & 3) == y) {
+            picked[t] = acc[i][j][e];
+            acc[i][j][e] = -INFINITY;
+          }
+    }
+    if (logits && t < kFewTokens) {
+      float* o = logits + (int64_t)t * piece + vw + r0;
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& v = acc[i][j];
+          *(f32x4*)(o + 32 * i + 8 * q) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        }
     }
     float m = -INFINITY;
 #pragma unroll
@@ -312,12 +337,15 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
   if (wave == 0 && r < valid) {
     float m = s_m[0][lane], s = s_s[0][lane];
     for (int k = 1; k < kJoinWaves; ++k) join(m, s, s_m[k][lane], s_s[k][lane]);
-    const float l = m + __logf(s);
-    const float d = (m - picked[r]) + __logf(s);
+    // with o the others' sum over the label's exponential: log(1 + o)
+    const double y = picked[r], gap = (double)m - y;
+    double d = gap > 0.0 ? gap + log((double)s + exp(-gap)) : log1p((double)s * exp(gap));
+    if (!(gap == gap) || y == INFINITY) d = __builtin_nan("");
+    const float l = (float)(y + d);
     lse[r] = l;
     if (lse_out) lse_out[index[r]] = l;
-    if (token_loss) token_loss[index[r]] = d;
-    loss = d;
+    if (token_loss) token_loss[index[r]] = (float)d;
+    loss = (float)d;
   }
   if (wave == 0) {
     for (int off = 32; off > 0; off >>= 1) loss += __shfl_xor(loss, off);
@@ -351,7 +379,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_g(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, const uint16_t* __restrict__ x,
     int32_t hidden_pad, int32_t K, const int32_t* __restrict__ label,
     const float* __restrict__ lse, const HeadState* __restrict__ state, int64_t piece0,
-    int32_t piece, uint16_t* __restrict__ g) {
+    int32_t piece, int32_t few, uint16_t* __restrict__ g) {
   using L = LogitTile<T>;
   using G = typename L::G;
   const int32_t valid = state->valid;
@@ -395,14 +423,18 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_g(
           if (!there || r0 + 32 * i + 8 * (e >> 2) + (e & 3) >= rows) acc[i][j][e] = 0.0f;
     }
     uint16_t* o = g + (int64_t)t * piece + cw + r0;
+    if (few && t >= kFewTokens) continue;  // those rows hold the others' second parts
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const f32x16& v = acc[i][j];
-        *(u32x2*)(o + 32 * i + 8 * q) =
-            narrow4<T>(v[4 * q] * g_scale<T>(), v[4 * q + 1] * g_scale<T>(),
-                       v[4 * q + 2] * g_scale<T>(), v[4 * q + 3] * g_scale<T>());
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e] * g_scale<T>();
+        *(u32x2*)(o + 32 * i + 8 * q) = narrow4<T>(v[0], v[1], v[2], v[3]);
+        if (few)
+          *(u32x2*)(o + (int64_t)kFewTokens * piece + 32 * i + 8 * q) =
+              narrow4<T>(second<T>(v[0]), second<T>(v[1]), second<T>(v[2]), second<T>(v[3]));
       }
   }
 }
@@ -465,6 +497,37 @@ __device__ __forceinline__ int32_t dx_split(int32_t tiles, int32_t most) {
   return best;
 }
 
+// The same from the fp32 logits of few tokens, in two 16-bit parts.  Workgroup:
+// 8 tokens, kRescaleCols columns.
+template <typename T>
+__global__ __launch_bounds__(256) void k_head_rescale_few(
+    const float* __restrict__ logits, uint16_t* __restrict__ g, int32_t piece, int32_t vocab,
+    const int32_t* __restrict__ label, const float* __restrict__ lse,
+    const float* __restrict__ picked, const HeadState* __restrict__ state) {
+  const int32_t t = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const bool there = t < state->valid;
+  const float z = there ? lse[t] : 0.0f;
+  const int32_t y = there ? label[t] : -1;
+  const int32_t c1 = (int32_t)(blockIdx.x + 1) * kRescaleCols;
+  for (int32_t c = blockIdx.x * kRescaleCols + (threadIdx.x & 31) * 4; c < c1 && c < piece;
+       c += 128) {
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (there) {
+      const f32x4 l = *(const f32x4*)(logits + (int64_t)t * piece + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = exp2_fast((l[e] - z) * kLog2e) * g_scale<T>();
+        if (c + e == y) v[e] = (exp2_fast((picked[t] - z) * kLog2e) - 1.0f) * g_scale<T>();
+        if (c + e >= vocab) v[e] = 0.0f;
+      }
+    }
+    uint16_t* o = g + (int64_t)t * piece + c;
+    *(u32x2*)o = narrow4<T>(v[0], v[1], v[2], v[3]);
+    *(u32x2*)(o + (int64_t)kFewTokens * piece) =
+        narrow4<T>(second<T>(v[0]), second<T>(v[1]), second<T>(v[2]), second<T>(v[3]));
+  }
+}
+
 // dx: A = g (token rows, contiguous along the vocabulary), B = w (contiguous
 // along the hidden axis).  Split s of the piece adds into its own fp32 block.
 template <typename T>
@@ -512,8 +575,8 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dx(
 template <typename T>
 __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
     const float* __restrict__ acc, int32_t most, int32_t tokens_pad, int32_t hidden_pad,
-    int32_t hidden, const int32_t* __restrict__ index, const HeadState* __restrict__ state,
-    uint16_t* __restrict__ dx, int64_t lddx) {
+    int32_t hidden, int32_t few, const int32_t* __restrict__ index,
+    const HeadState* __restrict__ state, uint16_t* __restrict__ dx, int64_t lddx) {
   const int32_t r = blockIdx.y, valid = state->valid;
   const int32_t h = (blockIdx.x * kPackThreads + threadIdx.x) * 4;
   if (r >= valid || h >= hidden) return;
@@ -522,7 +585,10 @@ __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
   const float c = state->coef / g_scale<T>();
   const float* p = acc + (int64_t)r * hidden_pad + h;
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int32_t k = 0; k < split; ++k) s += *(const f32x4*)(p + (int64_t)k * tokens_pad * hidden_pad);
+  for (int32_t k = 0; k < split; ++k, p += (int64_t)tokens_pad * hidden_pad) {
+    s += *(const f32x4*)p;
+    if (few) s += *(const f32x4*)(p + (int64_t)kFewTokens * hidden_pad);
+  }
   uint16_t* o = dx + (int64_t)index[r] * lddx + h;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
@@ -535,7 +601,7 @@ template <typename T, bool F32OUT>
 __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ x,
     int32_t hidden_pad, int32_t hidden, int32_t vocab_left, const HeadState* __restrict__ state,
-    int32_t accumulate, void* __restrict__ dw, int64_t lddw) {
+    int32_t few, int32_t accumulate, void* __restrict__ dw, int64_t lddw) {
   using G = Gemm<T, true, true>;
   ZK_GEMM_LDS;
   int32_t mt, nt;
@@ -543,7 +609,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
                (uint32_t)((hidden + G::BN - 1) / G::BN), mt, nt))
     return;
   const int32_t h0 = nt * G::BN, c0 = mt * G::BM;
-  const int32_t K = state->valid;
+  const int32_t K = few && state->valid ? 2 * kFewTokens : state->valid;
   const float c = state->coef / g_scale<T>();
   const Operand A{g + c0, (int64_t)piece * 2, piece - c0, K};
   const Operand B{x + h0, (int64_t)hidden_pad * 2, hidden_pad - h0, K};
@@ -615,7 +681,8 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
                        at<const uint16_t>(ws, p.x), (int32_t)p.hidden_pad, w.K,
                        (int32_t)p.tokens_pad, at<const int32_t>(ws, p.label), state,
                        at<float2>(ws, p.part), at<float>(ws, p.picked), p.kept,
-                       (int32_t)p.piece, keep ? at<uint16_t>(ws, p.g) : nullptr);
+                       (int32_t)p.piece, keep && !p.few ? at<uint16_t>(ws, p.g) : nullptr,
+                       keep && p.few ? at<float>(ws, p.logits) : nullptr);
     ZK_LAUNCHED();
   }
   hipLaunchKernelGGL(k_head_join, dim3((uint32_t)(p.tokens_pad / kJoinTokens)),
@@ -642,7 +709,13 @@ int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
   const int32_t* label = at<const int32_t>(ws, p.label);
   const float* lse = at<const float>(ws, p.lse);
   if (h->tokens > 0) {
-    if (have)
+    if (have && p.few)
+      hipLaunchKernelGGL(k_head_rescale_few<T>,
+                         dim3((uint32_t)((p.piece + kRescaleCols - 1) / kRescaleCols),
+                              kFewTokens / 8),
+                         dim3(256), 0, stream, at<const float>(ws, p.logits), g, (int32_t)p.piece,
+                         (int32_t)h->vocab, label, lse, at<const float>(ws, p.picked), state);
+    else if (have)
       hipLaunchKernelGGL(k_head_rescale<T>,
                          dim3((uint32_t)((left + kRescaleCols - 1) / kRescaleCols),
                               (uint32_t)(p.tokens_pad / 8)),
@@ -653,7 +726,7 @@ int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
     else
       hipLaunchKernelGGL(k_head_g<T>, dim3(tile_grid(ttiles, vtiles)), dim3(kGemmThreads), 0,
                          stream, w.w, w.ld, (int32_t)h->vocab, x, (int32_t)p.hidden_pad, w.K,
-                         label, lse, state, v0, (int32_t)p.piece, g);
+                         label, lse, state, v0, (int32_t)p.piece, p.few ? 1 : 0, g);
     ZK_LAUNCHED();
     hipLaunchKernelGGL(k_head_dx<T>, dim3(tile_grid(htiles * p.split, ttiles)),
                        dim3(kGemmThreads), 0, stream, g, (int32_t)p.piece, w.w + v0 * w.ld, w.ld,
@@ -667,11 +740,13 @@ int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
   if (gr->dw_dtype == ZERO_F32)
     hipLaunchKernelGGL((k_head_dw<T, true>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads),
                        0, stream, g, (int32_t)p.piece, x, (int32_t)p.hidden_pad,
-                       (int32_t)h->hidden, (int32_t)left, state, gr->accumulate, dw, gr->lddw);
+                       (int32_t)h->hidden, (int32_t)left, state, p.few ? 1 : 0, gr->accumulate, dw,
+                       gr->lddw);
   else
     hipLaunchKernelGGL((k_head_dw<T, false>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads),
                        0, stream, g, (int32_t)p.piece, x, (int32_t)p.hidden_pad,
-                       (int32_t)h->hidden, (int32_t)left, state, gr->accumulate, dw, gr->lddw);
+                       (int32_t)h->hidden, (int32_t)left, state, p.few ? 1 : 0, gr->accumulate, dw,
+                       gr->lddw);
   return (int)hipGetLastError();
 }
 
@@ -688,7 +763,7 @@ int grad_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_gr
                        dim3((uint32_t)((h->hidden + 4 * kPackThreads - 1) / (4 * kPackThreads)),
                             (uint32_t)h->tokens),
                        dim3(kPackThreads), 0, stream, at<const float>(ws, p.acc), p.split,
-                       (int32_t)p.tokens_pad, (int32_t)p.hidden_pad, (int32_t)h->hidden,
+                       (int32_t)p.tokens_pad, (int32_t)p.hidden_pad, (int32_t)h->hidden, p.few ? 1 : 0,
                        at<const int32_t>(ws, p.index), at<HeadState>(ws, p.state),
                        (uint16_t*)gr->dx, gr->lddx);
   return (int)hipGetLastError();
@@ -709,8 +784,8 @@ int launch_head_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const fl
     hipLaunchKernelGGL(k_head_pack_x, dim3((uint32_t)p.tokens_pad), dim3(kPackThreads), 0, stream,
                        (const uint16_t*)h->x, h->ldx, (int32_t)h->tokens, (int32_t)h->hidden,
                        (int32_t)p.hidden_pad, (int32_t)h->vocab, h->labels,
-                       at<const int32_t>(ws, p.index), state, at<uint16_t>(ws, p.x), token_loss,
-                       lse, gr ? (uint16_t*)gr->dx : nullptr, gr ? gr->lddx : 0);
+                       at<const int32_t>(ws, p.index), state, at<uint16_t>(ws, p.x), p.few ? 1 : 0,
+                       token_loss, lse, gr ? (uint16_t*)gr->dx : nullptr, gr ? gr->lddx : 0);
     ZK_LAUNCHED();
   }
   if (p.pack_w) {
