@@ -38,6 +38,8 @@
 namespace zk {
 namespace dev {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -279,7 +281,56 @@ struct Gemm {
     }
     if (k0 < K) stage(A, B, k0, lds.even, lds.odd, wave, lane, fa, fb, acc);
     if (wave < 4) asm volatile("s_barrier" ::: "memory");
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // loads past the contraction's end (zeros) may still be on their way
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+
+  // The tile in 16 bits through LDS, so that it leaves in whole lines: pack(a,
+  // b, c, d) narrows four values that follow one another along the rows,
+  // store(col, row, v) gets eight of them (16 bytes) of a tile column, 32
+  // lanes side by side.  A column's 16-byte chunk c lies at c ^ (col % 32).
+  // Call after run, by all waves.
+  template <typename Pack, typename Store>
+  static __device__ __forceinline__ void transposed(const GemmLds& lds, const f32x16 (&acc)[MI][NJ],
+                                                    Pack pack, Store store) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 31, hi = lane >> 5;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      lds_char* p = columns(lds, wave % 4 * 2 + j) + r * 512 + hi * 8;
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& v = acc[i][j];
+          *(__attribute__((address_space(3))) u32x2*)(p + (((wave / 4 * 16 + 4 * i + q) ^ r) << 4)) =
+              pack(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+    }
+    __syncthreads();
+    const lds_char* p = columns(lds, wave);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int col = 2 * k + hi;
+      store(wave * 32 + col, r * 8,
+            *(const __attribute__((address_space(3))) u32x4*)(p + col * 512 + ((r ^ col) << 4)));
+    }
+  }
+
+ private:
+  // 16 KiB of LDS for 32 of the tile's columns.
+  static __device__ __forceinline__ lds_char* columns(const GemmLds& l, int block) {
+    switch (block) {
+      case 0: return l.even.a0;
+      case 1: return l.even.a1;
+      case 2: return l.odd.a0;
+      case 3: return l.odd.a1;
+      case 4: return l.even.b;
+      case 5: return l.even.b + 16384;
+      case 6: return l.odd.b;
+      default: return l.odd.b + 16384;
+    }
   }
 };
 

@@ -166,16 +166,14 @@ template <typename T>
 struct LogitTile {
   using G = Gemm<T, false, false>;
 
-  static __device__ __forceinline__ bool run(const uint16_t* w, int64_t ldw, int64_t v0,
+  static __device__ __forceinline__ void run(const uint16_t* w, int64_t ldw, int64_t v0,
                                              int32_t vocab, const uint16_t* x, int32_t t0,
-                                             int32_t hidden_pad, int32_t K,
+                                             int32_t hidden_pad, int32_t K, const GemmLds& lds,
                                              f32x16 (&acc)[G::MI][G::NJ]) {
-    ZK_GEMM_LDS;
     const int64_t rows = vocab - v0;
     const Operand A{w + v0 * ldw, ldw * 2, (int32_t)(rows < G::BM ? rows : G::BM), K};
     const Operand B{x + (int64_t)t0 * hidden_pad, (int64_t)hidden_pad * 2, G::BN, K};
     G::run(A, B, K, lds, acc);
-    return true;
   }
 };
 
@@ -216,7 +214,8 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
   const int64_t v0 = (int64_t)mt * G::BM;
   constexpr int MI = G::MI, NJ = G::NJ;
   f32x16 acc[MI][NJ];
-  L::run(w, ldw, v0, vocab, x, t0, hidden_pad, K, acc);
+  ZK_GEMM_LDS;
+  L::run(w, ldw, v0, vocab, x, t0, hidden_pad, K, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t vw = v0 + (wave / 4) * MI * 32;  // the wave's first vocabulary row
   const int32_t rows = (int32_t)(vocab - vw < MI * 32 ? vocab - vw : MI * 32);
@@ -276,22 +275,20 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
         for (int e = 0; e < 16; ++e)
           if (acc[i][j][e] != acc[i][j][e]) s = acc[i][j][e];
     }
-    if (g && vw >= kept) {
-      // rows past the vocabulary and rows of NaN alone: whatever is kept here
-      // k_head_rescale replaces, or multiplies by NaN
-      uint16_t* o = g + (int64_t)t * piece + (vw - kept) + 4 * (lane >> 5);
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16& v = acc[i][j];
-          *(u32x2*)(o + 32 * i + 8 * q) =
-              narrow4<T>(v[4 * q] * g_scale<T>(), v[4 * q + 1] * g_scale<T>(),
-                         v[4 * q + 2] * g_scale<T>(), v[4 * q + 3] * g_scale<T>());
-        }
-    }
     s += __shfl_xor(s, 32);
     if (lane < 32) part[(vw / kHeadPart) * tokens_pad + t] = float2{m, s};
+  }
+  if (g && v0 >= kept) {
+    // rows past the vocabulary, and of NaN alone: whatever is kept here
+    // k_head_rescale replaces, or multiplies by NaN
+    constexpr float S = g_scale<T>();
+    G::transposed(lds, acc,
+                  [](float a, float b, float c, float d) {
+                    return narrow4<T>(a * S, b * S, c * S, d * S);
+                  },
+                  [&](int col, int row, u32x4 v) {
+                    *(u32x4*)(g + (int64_t)(t0 + col) * piece + (v0 - kept) + row) = v;
+                  });
   }
 }
 
@@ -393,7 +390,8 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_g(
   const int64_t v0 = piece0 + c0;
   constexpr int MI = G::MI, NJ = G::NJ;
   f32x16 acc[MI][NJ];
-  L::run(w, ldw, v0, vocab, x, t0, hidden_pad, K, acc);
+  ZK_GEMM_LDS;
+  L::run(w, ldw, v0, vocab, x, t0, hidden_pad, K, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t cw = c0 + (wave / 4) * MI * 32;
   const int32_t rows = left - cw;
@@ -422,21 +420,30 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_g(
         for (int e = 0; e < 16; ++e)
           if (!there || r0 + 32 * i + 8 * (e >> 2) + (e & 3) >= rows) acc[i][j][e] = 0.0f;
     }
-    uint16_t* o = g + (int64_t)t * piece + cw + r0;
-    if (few && t >= kFewTokens) continue;  // those rows hold the others' second parts
+    if (few && t < kFewTokens) {
+      uint16_t* o = g + (int64_t)t * piece + cw + r0;
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float v[4];
+        for (int q = 0; q < 4; ++q) {
+          float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e] * g_scale<T>();
-        *(u32x2*)(o + 32 * i + 8 * q) = narrow4<T>(v[0], v[1], v[2], v[3]);
-        if (few)
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e] * g_scale<T>();
+          *(u32x2*)(o + 32 * i + 8 * q) = narrow4<T>(v[0], v[1], v[2], v[3]);
           *(u32x2*)(o + (int64_t)kFewTokens * piece + 32 * i + 8 * q) =
               narrow4<T>(second<T>(v[0]), second<T>(v[1]), second<T>(v[2]), second<T>(v[3]));
-      }
+        }
+    }
   }
+  if (few) return;
+  constexpr float S = g_scale<T>();
+  G::transposed(lds, acc,
+                [](float a, float b, float c, float d) {
+                  return narrow4<T>(a * S, b * S, c * S, d * S);
+                },
+                [&](int col, int row, u32x4 v) {
+                  *(u32x4*)(g + (int64_t)(t0 + col) * piece + c0 + row) = v;
+                });
 }
 
 // g of the piece whose exponentials were kept: e^(l - m) e^(m - lse) - [v = y],
@@ -595,8 +602,9 @@ __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
     if (h + e < hidden) o[e] = (uint16_t)narrow<T>(s[e] * c);
 }
 
-// dw: A = g, B = packed x, both contiguous along their rows; the contraction
-// runs over the tokens.
+// dw: A = packed x (rows of the tile: hidden columns), B = g (vocabulary
+// rows), both contiguous along their rows; the contraction runs over the
+// tokens.
 template <typename T, bool F32OUT>
 __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ x,
@@ -605,40 +613,73 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
   using G = Gemm<T, true, true>;
   ZK_GEMM_LDS;
   int32_t mt, nt;
-  if (!tile_of(blockIdx.x, (uint32_t)((vocab_left + G::BM - 1) / G::BM),
-               (uint32_t)((hidden + G::BN - 1) / G::BN), mt, nt))
+  if (!tile_of(blockIdx.x, (uint32_t)((vocab_left + G::BN - 1) / G::BN),
+               (uint32_t)((hidden + G::BM - 1) / G::BM), mt, nt))
     return;
-  const int32_t h0 = nt * G::BN, c0 = mt * G::BM;
+  const int32_t h0 = nt * G::BM, c0 = mt * G::BN;
   const int32_t K = few && state->valid ? 2 * kFewTokens : state->valid;
   const float c = state->coef / g_scale<T>();
-  const Operand A{g + c0, (int64_t)piece * 2, piece - c0, K};
-  const Operand B{x + h0, (int64_t)hidden_pad * 2, hidden_pad - h0, K};
+  const Operand A{x + h0, (int64_t)hidden_pad * 2, hidden_pad - h0, K};
+  const Operand B{g + c0, (int64_t)piece * 2, piece - c0, K};
   constexpr int MI = G::MI, NJ = G::NJ;
   f32x16 acc[MI][NJ];
   G::run(A, B, K, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const bool bad = state->bad != 0;
+  if (state->bad) {  // bad labels alone (no valid token) still have to show: c is NaN
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16{} + c;
+  }
+  if (!F32OUT && !accumulate) {
+    uint16_t* out = (uint16_t*)dw;
+    G::transposed(lds, acc,
+                  [c](float p, float q, float r, float s) {
+                    return narrow4<T>(p * c, q * c, r * c, s * c);
+                  },
+                  [&](int col, int row, u32x4 d) {
+                    const int32_t v = c0 + col, h = h0 + row;
+                    if (v >= vocab_left || h >= hidden) return;
+                    uint16_t* o = out + (int64_t)v * lddw + h;
+                    if (h + 8 <= hidden && ((uintptr_t)o & 15) == 0) {
+                      *(u32x4*)o = d;
+                    } else {
+#pragma unroll
+                      for (int e = 0; e < 8; ++e)
+                        if (h + e < hidden) o[e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
+                    }
+                  });
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int32_t h = h0 + (wave % 4) * NJ * 32 + j * 32 + (lane & 31);
-    if (h >= hidden) continue;
+    const int32_t v = c0 + wave % 4 * 64 + j * 32 + (lane & 31);
+    if (v >= vocab_left) continue;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       asm volatile("" ::: "memory");
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int32_t v = c0 + (wave / 4) * MI * 32 + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-        if (v >= vocab_left) continue;
+      for (int q = 0; q < 4; ++q) {
+        const int32_t h = h0 + wave / 4 * 128 + 32 * i + 8 * q + 4 * (lane >> 5);
         const int64_t at = (int64_t)v * lddw + h;
-        // bad labels alone (no valid token) still have to show
-        float d = bad ? c : acc[i][j][e] * c;
+        f32x4 d;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = acc[i][j][4 * q + e] * c;
         if constexpr (F32OUT) {
           float* o = (float*)dw + at;
-          *o = accumulate ? *o + d : d;
+          if (h + 4 <= hidden && ((uintptr_t)o & 15) == 0) {
+            if (accumulate) d = *(const f32x4*)o + d;
+            *(f32x4*)o = d;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (h + e < hidden) o[e] = accumulate ? o[e] + d[e] : d[e];
+          }
         } else {
           uint16_t* o = (uint16_t*)dw + at;
-          if (accumulate) d += widen<T>(*o);
-          *o = (uint16_t)narrow<T>(d);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (h + e < hidden) o[e] = (uint16_t)narrow<T>(widen<T>(o[e]) + d[e]);
         }
       }
     }
