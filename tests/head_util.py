@@ -6,12 +6,13 @@ e = 2^-23 bounds one fp32 operation (the matrix cores may truncate), a length-n
 fp32 sum of terms a_i is off by at most n e sum |a_i|.
 
 logits     |dl| <= H e (|x| |w|^T)                (16-bit products are exact in fp32)
-lse        the exponentials are off by a relative eexp <= 4e + 2e |l - m| (the product with
-           log2 e, the argument's subtraction and the instruction, whose error is one step),
+lse        the exponentials are off by a relative eexp <= 4e + 2e |l - m| + e/8 |l| (one
+           multiply-add with log2 e in fp32, which is off by 1.34e-8 < e/8 of itself, and the
+           instruction, whose error is one step),
            their sums by (V + 64) e and the logarithm by 4e (|lse| + |m| + 2):
            |dlse| <= max|dl| + eexp + (V + 64) e + 4e (|lse| + |m| + 2)
 loss       |dloss| <= |dlse| + |dl at the label| + 4e (|lse| + |l|)
-p          relative r = |dl| + |dlse| + 4e + 4e |l - lse|
+p          relative r = |dl| + |dlse| + 4e + 4e |l - lse| + e (|l| + |lse|)
 g          |dg| <= u |d| + p (r + u) (1 + u) + e |d|: one rounding of the difference and, where
            the exponentials were kept, one of the probability before it; plus half the type's smallest step (fp16, 2^-25 after
            the scale of 2^15)
@@ -43,7 +44,7 @@ def reference(x, w, y, loss_scale=1.0, mean=True):
         m = l.amax(1)
         lse = torch.logsumexp(l, 1)
         far = (l - m[:, None]).abs()
-        eexp = ((4 * E + 2 * E * far) * torch.exp(l - lse[:, None])).sum(1)
+        eexp = ((4 * E + 2 * E * far + E / 8 * l.abs()) * torch.exp(l - lse[:, None])).sum(1)
         dlse = dl.amax(1) + eexp + (V + 64) * E + 4 * E * (lse.abs() + m.abs() + 2)
     else:
         lse = dlse = torch.zeros(0, dtype=torch.float64, device=x.device)
@@ -61,7 +62,8 @@ def reference(x, w, y, loss_scale=1.0, mean=True):
     p = torch.exp(l - lse[:, None])
     d = p.clone()
     d[rows, yk] -= 1.0
-    r = dl + dlse[:, None] + 4 * E + 4 * E * (l - lse[:, None]).abs()
+    r = dl + dlse[:, None] + 4 * E + 4 * E * (l - lse[:, None]).abs() \
+        + E * (l.abs() + lse.abs()[:, None])
     floor = tiny * 2.0 ** -15 if dt == torch.float16 else tiny
     dg = u * d.abs() + p * (r + u) * (1 + u) + E * d.abs() + 2 * floor
     g = d.abs() + dg

@@ -16,7 +16,7 @@
 //           so that 16 consecutive rows' chunks c fill the 256 bytes the banks
 //           deliver in a cycle
 //   cols    a contraction index k's elements side by side; 32-byte pair p lies
-//           at p ^ 2 * (k & 3); fragments come back transposed
+//           at p ^ (2 * (k & 3) + (k >> 3 & 1)); fragments come back transposed
 //           (ds_read_b64_tr_b16)
 //
 // Eight waves, two on each SIMD.  The second four run one phase behind the
@@ -27,6 +27,12 @@
 // first A half (and keeps B in registers), the second its rows of the other
 // half.  A part is refilled in the round after its last reading, five or six
 // phases before it is read again.
+//
+// The products are 16 x 16 x 32.  On full tiles the chip runs at its power
+// limit, not at its issue limit: 32 x 32 x 16 products need 6% fewer cycles but
+// held the clock at 1.54 GHz where these run at 1.70 (logits of 7373 x 128256 x
+// 4096: 5.99 against 5.77 ms), since they move twice the accumulator bits for
+// the same multiplications.
 //
 // Lanes whose element lies outside the operand read zero (buffer bounds), so
 // ragged edges cost nothing and nothing outside the operand is touched.
@@ -40,7 +46,7 @@ namespace dev {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -50,12 +56,12 @@ typedef __attribute__((address_space(3))) char lds_char;
 struct BF16 {};
 struct FP16 {};
 
-__device__ __forceinline__ f32x16 mfma(BF16, s16x8 a, s16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+__device__ __forceinline__ f32x4 mfma(BF16, s16x8 a, s16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x16 mfma(FP16, s16x8 a, s16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+__device__ __forceinline__ f32x4 mfma(FP16, s16x8 a, s16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                 __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
@@ -133,7 +139,7 @@ struct Part {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         const int k = (wave * kLoads + j) * kLoadRows + lane / kChunks;
-        const int q = (lane % kChunks) ^ (k & 3) << 2;
+        const int q = (lane % kChunks) ^ ((k & 3) << 2 | (k >> 3 & 1) << 1);
         const int col = HALF < 0 ? 16 * q : (q >> 3) * 256 + 128 * HALF + 16 * (q & 7);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rsrc, (__attribute__((address_space(3))) void*)(lds + j * 1024), 16,
@@ -143,34 +149,31 @@ struct Part {
   }
 };
 
-// Fragments of two 32-row blocks, local rows r0 .. r0 + 64 of a part, at slice
-// s (16 contraction elements) of a stage: lane l holds row l % 32, elements
-// (l / 32) * 8 .. + 8.
+// Fragments of four 16-row blocks, local rows r0 .. r0 + 64 of a part, at slice
+// s (32 contraction elements) of a stage: lane l holds row l % 16, elements
+// (l / 16) * 8 .. + 8.
 template <int R, bool COLS>
 struct Frags {
-  int base[COLS ? 2 : 4];
+  int base[COLS ? 4 : 2];
   __device__ __forceinline__ Frags(int r0, int lane) {
+    const int g = lane >> 4, j = lane & 15;
     if constexpr (!COLS) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        base[s] = (r0 + (lane & 31)) * (kStage * 2) +
-                  16 * ((s * 2 + (lane >> 5)) ^ ((lane >> 1) & 7));
+      for (int s = 0; s < 2; ++s)
+        base[s] = (r0 + j) * (kStage * 2) + 16 * ((s * 4 + g) ^ (j >> 1));
     } else {
-      const int g = lane >> 4, j = lane & 15;
-      const int k = (g >> 1) * 8 + (j >> 2);
+      const int k = g * 8 + (j >> 2), f = (j >> 2) << 1 | (g & 1);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int pair = ((r0 >> 4) + 2 * i + (g & 1)) ^ 2 * (j >> 2);
-        base[i] = k * (R * 2) + (pair << 5) + (j & 3) * 8;
-      }
+      for (int i = 0; i < 4; ++i)
+        base[i] = k * (R * 2) + ((((r0 >> 4) + i) ^ f) << 5) + (j & 3) * 8;
     }
   }
   __device__ __forceinline__ s16x8 load(const lds_char* lds, int i, int s) const {
     if constexpr (!COLS) {
-      return *(const __attribute__((address_space(3))) s16x8*)(lds + base[s] + i * 32 * kStage * 2);
+      return *(const __attribute__((address_space(3))) s16x8*)(lds + base[s] + i * 16 * kStage * 2);
     } else {
       typedef __attribute__((address_space(3))) s16x4 lds4;
-      const lds_char* p = lds + base[i] + s * 16 * (R * 2);
+      const lds_char* p = lds + base[i] + s * 32 * (R * 2);
       const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
       const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 4 * (R * 2)));
       return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -192,12 +195,12 @@ struct GemmLds {
   StageLds even, odd;
 };
 
-// The 256 x 256 tile: 2 x 4 waves, each 4 x 2 blocks of 32 x 32.
-// acc[i][j][e] of lane l is row wm*128 + 32i + 8(e/4) + 4(l/32) + e%4, column
-// wn*64 + 32j + l%32, wm = wave / 4, wn = wave % 4.
+// The 256 x 256 tile: 2 x 4 waves, each 8 x 4 blocks of 16 x 16.
+// acc[i][j][e] of lane l is row wm*128 + 16i + 4(l/16) + e, column wn*64 + 16j
+// + l%16, wm = wave / 4, wn = wave % 4.
 template <typename T, bool ACOLS, bool BCOLS>
 struct Gemm {
-  static constexpr int BM = 256, BN = 256, THREADS = 512, MI = 4, NJ = 2;
+  static constexpr int BM = 256, BN = 256, THREADS = 512, MI = 8, NJ = 4;
   using A0 = Part<128, ACOLS, 0>;
   using A1 = Part<128, ACOLS, 1>;
   using SB = Part<256, BCOLS, -1>;
@@ -205,16 +208,16 @@ struct Gemm {
   using FB = Frags<256, BCOLS>;
 
   template <int HALF>
-  static __device__ __forceinline__ void multiply(const s16x8 (&ra)[4][2], const s16x8 (&rb)[4][2],
-                                                  f32x16 (&acc)[MI][NJ]) {
+  static __device__ __forceinline__ void multiply(const s16x8 (&ra)[2][4], const s16x8 (&rb)[2][4],
+                                                  f32x4 (&acc)[MI][NJ]) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[2 * HALF + i][j] = mfma(T{}, ra[s][i], rb[s][j], acc[2 * HALF + i][j]);
+        for (int j = 0; j < 4; ++j)
+          acc[4 * HALF + i][j] = mfma(T{}, ra[s][i], rb[s][j], acc[4 * HALF + i][j]);
     __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_barrier" ::: "memory");
@@ -232,12 +235,12 @@ struct Gemm {
   static __device__ __forceinline__ void stage(const Operand& A, const Operand& B, int32_t k0,
                                                const StageLds& here, const StageLds& other,
                                                int wave, int lane, const FA& fa, const FB& fb,
-                                               f32x16 (&acc)[MI][NJ]) {
-    s16x8 ra[4][2], rb[4][2];
+                                               f32x4 (&acc)[MI][NJ]) {
+    s16x8 ra[2][4], rb[2][4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         rb[s][i] = fb.load(here.b, i, s);
         ra[s][i] = fa.load(here.a0, i, s);
       }
@@ -245,9 +248,9 @@ struct Gemm {
     turn();
     multiply<0>(ra, rb, acc);
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) ra[s][i] = fa.load(here.a1, i, s);
+      for (int i = 0; i < 4; ++i) ra[s][i] = fa.load(here.a1, i, s);
     A0::issue(A, k0 + 2 * kStage, here.a0, wave, lane);
     SB::issue(B, k0 + 2 * kStage, here.b, wave, lane);
     turn();
@@ -257,7 +260,7 @@ struct Gemm {
   // acc = A B^T over K >= 0 contraction indexes.  On return every wave is done
   // with LDS.
   static __device__ __forceinline__ void run(const Operand& A, const Operand& B, int32_t K,
-                                             const GemmLds& lds, f32x16 (&acc)[MI][NJ]) {
+                                             const GemmLds& lds, f32x4 (&acc)[MI][NJ]) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const FA fa(wave / 4 * 64, lane);
@@ -265,7 +268,7 @@ struct Gemm {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16{};
+      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{};
     if (K <= 0) return;
     A0::issue(A, 0, lds.even.a0, wave, lane);
     SB::issue(B, 0, lds.even.b, wave, lane);
@@ -291,24 +294,24 @@ struct Gemm {
   // lanes side by side.  A column's 16-byte chunk c lies at c ^ (col % 32).
   // Call after run, by all waves.
   template <typename Pack, typename Store>
-  static __device__ __forceinline__ void transposed(const GemmLds& lds, const f32x16 (&acc)[MI][NJ],
+  static __device__ __forceinline__ void transposed(const GemmLds& lds, const f32x4 (&acc)[MI][NJ],
                                                     Pack pack, Store store) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 31, hi = lane >> 5;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      lds_char* p = columns(lds, wave % 4 * 2 + j) + r * 512 + hi * 8;
+      const int col = j % 2 * 16 + (lane & 15);
+      lds_char* p = columns(lds, wave % 4 * 2 + j / 2) + col * 512 + (lane >> 4 & 1) * 8;
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16& v = acc[i][j];
-          *(__attribute__((address_space(3))) u32x2*)(p + (((wave / 4 * 16 + 4 * i + q) ^ r) << 4)) =
-              pack(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        }
+      for (int i = 0; i < MI; ++i) {
+        const f32x4& v = acc[i][j];
+        const int chunk = wave / 4 * 16 + 2 * i + (lane >> 5);
+        *(__attribute__((address_space(3))) u32x2*)(p + ((chunk ^ col) << 4)) =
+            pack(v[0], v[1], v[2], v[3]);
+      }
     }
     __syncthreads();
+    const int r = lane & 31, hi = lane >> 5;
     const lds_char* p = columns(lds, wave);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {

@@ -24,7 +24,7 @@ struct HeadPlan {
   bool few;            // gradient of at most kFewTokens tokens: g in two parts
   bool pack_w;         // w's rows do not start on 16-byte boundaries
   // offsets
-  size_t state, sums, index, label, lse, x, w, part, picked, g, logits, acc, total;
+  size_t state, sums, index, label, lse, loss, x, w, part, picked, g, logits, acc, total;
 };
 constexpr int64_t kHeadPart = 128;
 // With this few tokens g is kept in two 16-bit parts: rows t and kFewTokens + t

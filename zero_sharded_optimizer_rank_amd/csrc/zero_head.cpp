@@ -122,6 +122,7 @@ HeadPlan head_plan(const zero_head_t* h, bool grad) {
   p.index = take(4 * (size_t)p.tokens_pad);
   p.label = take(4 * (size_t)p.tokens_pad);
   p.lse = take(4 * (size_t)p.tokens_pad);
+  p.loss = take(4 * (size_t)p.tokens_pad);
   p.picked = take(4 * (size_t)p.tokens_pad);
   p.x = take(2 * (size_t)p.tokens_pad * (size_t)p.hidden_pad);
   p.w = take(p.pack_w ? 2 * (size_t)h->vocab * (size_t)p.hidden_pad : 0);

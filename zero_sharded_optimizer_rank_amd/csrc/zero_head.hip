@@ -38,11 +38,14 @@ constexpr int kJoinTokens = 64, kJoinWaves = 16, kJoinBatch = 8;
 // g's scale before it is rounded: |p - [v = y]| <= 1, so 2^15 keeps fp16 in
 // range and p down to 2^-29 normal; bf16 has fp32's exponents.
 template <typename T>
-__device__ __forceinline__ constexpr float g_scale();
+__host__ __device__ constexpr float g_scale();
 template <>
-__device__ __forceinline__ constexpr float g_scale<BF16>() { return 1.0f; }
+__host__ __device__ constexpr float g_scale<BF16>() { return 1.0f; }
 template <>
-__device__ __forceinline__ constexpr float g_scale<FP16>() { return 32768.0f; }
+__host__ __device__ constexpr float g_scale<FP16>() { return 32768.0f; }
+
+template <typename T>
+__device__ __forceinline__ constexpr float g_log2() { return g_scale<T>() == 1.0f ? 0.0f : 15.0f; }
 
 template <typename T>
 __device__ __forceinline__ uint32_t narrow(float x);
@@ -169,7 +172,7 @@ struct LogitTile {
   static __device__ __forceinline__ void run(const uint16_t* w, int64_t ldw, int64_t v0,
                                              int32_t vocab, const uint16_t* x, int32_t t0,
                                              int32_t hidden_pad, int32_t K, const GemmLds& lds,
-                                             f32x16 (&acc)[G::MI][G::NJ]) {
+                                             f32x4 (&acc)[G::MI][G::NJ]) {
     const int64_t rows = vocab - v0;
     const Operand A{w + v0 * ldw, ldw * 2, (int32_t)(rows < G::BM ? rows : G::BM), K};
     const Operand B{x + (int64_t)t0 * hidden_pad, (int64_t)hidden_pad * 2, G::BN, K};
@@ -189,8 +192,8 @@ __device__ __forceinline__ u32x2 narrow4(float a, float b, float c, float d) {
 template <typename T>
 __device__ __forceinline__ float second(float x) { return x - widen<T>(narrow<T>(x)); }
 
-// Loss: (max, sum of exp(l - max)) of every token over each 128 vocabulary
-// rows, the label's row left out, and the label's logit: a confident token's
+// Loss: (m, g_scale sum of 2^(l log2 e - m)) of every token over each 128
+// vocabulary rows, m the largest l log2 e rounded up, the label's row left out, and the label's logit: a confident token's
 // loss is log(1 + the others' sum), whose digits a sum that held the label's 1
 // would have lost.  Where the gradient follows in the same call, the
 // exponentials of the piece of the vocabulary that starts at `kept` stay in
@@ -205,7 +208,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
     int64_t kept, int32_t piece, uint16_t* __restrict__ g, float* __restrict__ logits) {
   using L = LogitTile<T>;
   using G = typename L::G;
-  static_assert(G::MI * 32 == kHeadPart, "one partial a wave");
+  static_assert(G::MI * 16 == kHeadPart, "one partial a wave");
   int32_t mt, nt;
   if (!tile_of(blockIdx.x, (uint32_t)((vocab + G::BM - 1) / G::BM),
                (uint32_t)((state->valid + G::BN - 1) / G::BN), mt, nt))
@@ -213,79 +216,69 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
   const int32_t t0 = nt * G::BN;
   const int64_t v0 = (int64_t)mt * G::BM;
   constexpr int MI = G::MI, NJ = G::NJ;
-  f32x16 acc[MI][NJ];
+  f32x4 acc[MI][NJ];
   ZK_GEMM_LDS;
   L::run(w, ldw, v0, vocab, x, t0, hidden_pad, K, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t vw = v0 + (wave / 4) * MI * 32;  // the wave's first vocabulary row
-  const int32_t rows = (int32_t)(vocab - vw < MI * 32 ? vocab - vw : MI * 32);
+  const int64_t vw = v0 + (wave / 4) * kHeadPart;  // the wave's first vocabulary row
+  const int32_t rows = (int32_t)(vocab - vw < kHeadPart ? vocab - vw : kHeadPart);
+  const int r0 = 4 * (lane >> 4);  // element (i, e) is row r0 + 16i + e
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int32_t t = t0 + (wave % 4) * NJ * 32 + j * 32 + (lane & 31);
+    const int32_t t = t0 + (wave % 4) * 64 + j * 16 + (lane & 15);
     const int64_t y = t < state->valid ? (int64_t)label[t] - vw : -1;
-    const int r0 = 4 * (lane >> 5);  // element (i, e) is row r0 + 32i + 8(e/4) + e%4
-    if (rows < MI * 32) {  // the vocabulary ends here
+    if (rows < kHeadPart) {  // the vocabulary ends here
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (r0 + 32 * i + 8 * (e >> 2) + (e & 3) >= rows) acc[i][j][e] = -INFINITY;
+        for (int e = 0; e < 4; ++e)
+          if (r0 + 16 * i + e >= rows) acc[i][j][e] = -INFINITY;
     }
-    if (__any(y >= 0 && y < MI * 32)) {  // some token's label is here
+    // the element of this lane that is the label's, if one is
+    const bool mine = y >= 0 && y < kHeadPart && ((int32_t)y >> 2 & 3) == lane >> 4;
+    const int want = mine ? ((int32_t)y >> 4) * 4 + ((int32_t)y & 3) : -1;
+    if (__any(mine)) {
+      float p = 0.0f;
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (r0 + 32 * i + 8 * (e >> 2) + (e & 3) == y) {
-            picked[t] = acc[i][j][e];
-            acc[i][j][e] = -INFINITY;
-          }
+        for (int e = 0; e < 4; ++e) {
+          const bool hit = want == 4 * i + e;
+          p = hit ? acc[i][j][e] : p;
+          acc[i][j][e] = hit ? -INFINITY : acc[i][j][e];
+        }
+      if (mine) picked[t] = p;
     }
     if (logits && t < kFewTokens) {
-      float* o = logits + (int64_t)t * piece + vw + r0;
 #pragma unroll
       for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16& v = acc[i][j];
-          *(f32x4*)(o + 32 * i + 8 * q) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-        }
+        *(f32x4*)(logits + (int64_t)t * piece + vw + r0 + 16 * i) = acc[i][j];
     }
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[i][j][e]);
-    m = fmaxf(m, __shfl_xor(m, 32));
+      for (int e = 0; e < 4; ++e) m = __builtin_elementwise_maximum(m, acc[i][j][e]);
+    m = __builtin_elementwise_maximum(m, __shfl_xor(m, 16));  // NaN if one is
+    m = __builtin_elementwise_maximum(m, __shfl_xor(m, 32));
+    // in base 2, rounded up to a whole number, so that taking it off is exact;
+    // one multiply-add and one exponential a value; rows that are -inf alone give 0
+    m = __builtin_ceilf(m * kLog2e);
+    const float shift = (m == -INFINITY ? 0.0f : -m) + g_log2<T>();
     float s = 0.0f;
-    if (m > -INFINITY) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          acc[i][j][e] = exp2_fast((acc[i][j][e] - m) * kLog2e);
-          s += acc[i][j][e];
-        }
-    }
-    // a row of NaN alone has max -inf: it must not pass for an empty one
-    if (!(m > -INFINITY)) {
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (acc[i][j][e] != acc[i][j][e]) s = acc[i][j][e];
-    }
+      for (int e = 0; e < 4; ++e) {
+        acc[i][j][e] = exp2_fast(__builtin_fmaf(acc[i][j][e], kLog2e, shift));
+        s += acc[i][j][e];
+      }
+    s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
-    if (lane < 32) part[(vw / kHeadPart) * tokens_pad + t] = float2{m, s};
+    if (lane < 16) part[(vw / kHeadPart) * tokens_pad + t] = float2{m, s};
   }
   if (g && v0 >= kept) {
-    // rows past the vocabulary, and of NaN alone: whatever is kept here
-    // k_head_rescale replaces, or multiplies by NaN
-    constexpr float S = g_scale<T>();
-    G::transposed(lds, acc,
-                  [](float a, float b, float c, float d) {
-                    return narrow4<T>(a * S, b * S, c * S, d * S);
-                  },
+    G::transposed(lds, acc, narrow4<T>,
                   [&](int col, int row, u32x4 v) {
                     *(u32x4*)(g + (int64_t)(t0 + col) * piece + (v0 - kept) + row) = v;
                   });
@@ -293,12 +286,11 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
 }
 
 // --- 3. join -------------------------------------------------------------------
+// (m, s) stands for s 2^m.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
-  const float n = fmaxf(m, m2);
-  if (n > -INFINITY)
-    s = s * exp2_fast((m - n) * kLog2e) + s2 * exp2_fast((m2 - n) * kLog2e);
-  else
-    s = s + s2;  // both empty, or NaN
+  const float n = __builtin_elementwise_maximum(m, m2);
+  if (n == -INFINITY) return;  // both empty: s = s2 = 0
+  s = s * exp2_fast(m - n) + s2 * exp2_fast(m2 - n);
   m = n;
 }
 
@@ -307,8 +299,8 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
     const float2* __restrict__ part, int32_t parts, int32_t tokens_pad,
     const float* __restrict__ picked, const int32_t* __restrict__ index, float* __restrict__ lse,
-    float* __restrict__ token_loss, float* __restrict__ lse_out, double* __restrict__ sums,
-    int32_t mean, HeadState* __restrict__ state, zero_loss_result_t* __restrict__ res) {
+    float* __restrict__ loss_c, float* __restrict__ token_loss, float* __restrict__ lse_out, double* __restrict__ sums,
+    double scale, int32_t mean, HeadState* __restrict__ state, zero_loss_result_t* __restrict__ res) {
   __shared__ float s_m[kJoinWaves][64], s_s[kJoinWaves][64];
   __shared__ uint32_t s_last;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -335,13 +327,14 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
     float m = s_m[0][lane], s = s_s[0][lane];
     for (int k = 1; k < kJoinWaves; ++k) join(m, s, s_m[k][lane], s_s[k][lane]);
     // with o the others' sum over the label's exponential: log(1 + o)
-    const double y = picked[r], gap = (double)m - y;
-    double d = gap > 0.0 ? gap + log((double)s + exp(-gap)) : log1p((double)s * exp(gap));
+    const double y = picked[r], gap = (double)m / (double)kLog2e - y, sum = (double)s * scale;
+    double d = gap > 0.0 ? gap + log(sum + exp(-gap)) : log1p(sum * exp(gap));
     if (!(gap == gap) || y == INFINITY) d = __builtin_nan("");
     const float l = (float)(y + d);
     lse[r] = l;
     if (lse_out) lse_out[index[r]] = l;
     if (token_loss) token_loss[index[r]] = (float)d;
+    loss_c[r] = (float)d;
     loss = (float)d;
   }
   if (wave == 0) {
@@ -389,74 +382,68 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_g(
   const int32_t c0 = mt * G::BM;  // column of g
   const int64_t v0 = piece0 + c0;
   constexpr int MI = G::MI, NJ = G::NJ;
-  f32x16 acc[MI][NJ];
+  f32x4 acc[MI][NJ];
   ZK_GEMM_LDS;
   L::run(w, ldw, v0, vocab, x, t0, hidden_pad, K, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int32_t cw = c0 + (wave / 4) * MI * 32;
+  const int32_t cw = c0 + (wave / 4) * kHeadPart;
   const int32_t rows = left - cw;
+  const int r0 = 4 * (lane >> 4);  // element (i, e) is row r0 + 16i + e
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int32_t t = t0 + (wave % 4) * NJ * 32 + j * 32 + (lane & 31);
+    const int32_t t = t0 + (wave % 4) * 64 + j * 16 + (lane & 15);
     const bool there = t < valid;
     const float z = there ? lse[t] : 0.0f;
     const int64_t y = there ? (int64_t)label[t] - piece0 - cw : -1;
-    const int r0 = 4 * (lane >> 5);  // element (i, e) is row r0 + 32i + 8(e/4) + e%4
+    const bool mine = y >= 0 && y < kHeadPart && ((int32_t)y >> 2 & 3) == lane >> 4;
+    const int want = mine ? ((int32_t)y >> 4) * 4 + ((int32_t)y & 3) : -1;
+    const float shift = g_log2<T>() - z * kLog2e;
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = exp2_fast((acc[i][j][e] - z) * kLog2e);
-    if (__any(y >= 0 && y < MI * 32)) {
+      for (int e = 0; e < 4; ++e)
+        acc[i][j][e] = exp2_fast(__builtin_fmaf(acc[i][j][e], kLog2e, shift));
+    if (__any(mine)) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (r0 + 32 * i + 8 * (e >> 2) + (e & 3) == y) acc[i][j][e] -= 1.0f;
+        for (int e = 0; e < 4; ++e) acc[i][j][e] -= want == 4 * i + e ? g_scale<T>() : 0.0f;
     }
-    if (rows < MI * 32 || !__all(there)) {  // the vocabulary's or the tokens' end
+    if (rows < kHeadPart || !__all(there)) {  // the vocabulary's or the tokens' end
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (!there || r0 + 32 * i + 8 * (e >> 2) + (e & 3) >= rows) acc[i][j][e] = 0.0f;
+        for (int e = 0; e < 4; ++e)
+          if (!there || r0 + 16 * i + e >= rows) acc[i][j][e] = 0.0f;
     }
     if (few && t < kFewTokens) {
       uint16_t* o = g + (int64_t)t * piece + cw + r0;
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e] * g_scale<T>();
-          *(u32x2*)(o + 32 * i + 8 * q) = narrow4<T>(v[0], v[1], v[2], v[3]);
-          *(u32x2*)(o + (int64_t)kFewTokens * piece + 32 * i + 8 * q) =
-              narrow4<T>(second<T>(v[0]), second<T>(v[1]), second<T>(v[2]), second<T>(v[3]));
-        }
+      for (int i = 0; i < MI; ++i) {
+        const f32x4& v = acc[i][j];
+        *(u32x2*)(o + 16 * i) = narrow4<T>(v[0], v[1], v[2], v[3]);
+        *(u32x2*)(o + (int64_t)kFewTokens * piece + 16 * i) =
+            narrow4<T>(second<T>(v[0]), second<T>(v[1]), second<T>(v[2]), second<T>(v[3]));
+      }
     }
   }
   if (few) return;
-  constexpr float S = g_scale<T>();
-  G::transposed(lds, acc,
-                [](float a, float b, float c, float d) {
-                  return narrow4<T>(a * S, b * S, c * S, d * S);
-                },
+  G::transposed(lds, acc, narrow4<T>,
                 [&](int col, int row, u32x4 v) {
                   *(u32x4*)(g + (int64_t)(t0 + col) * piece + c0 + row) = v;
                 });
 }
 
-// g of the piece whose exponentials were kept: e^(l - m) e^(m - lse) - [v = y],
-// m the maximum of the 128 vocabulary rows.  The label's element is formed
-// from its fp32 logit: there 1 is subtracted, and the rounding of the kept
-// value would show.  A workgroup takes 8 tokens (one line of partials) and
+// g of the piece whose exponentials were kept: 2^(l log2 e - m) 2^(m - lse log2
+// e) - [v = y], m the reference of the 128 vocabulary rows.  The label's element is
+// e^-loss - 1.  A workgroup takes 8 tokens (one line of partials) and
 // kRescaleCols columns.
 constexpr int kRescaleCols = 1024;
 template <typename T>
 __global__ __launch_bounds__(256) void k_head_rescale(
     uint16_t* __restrict__ g, int32_t piece, int32_t left, const float2* __restrict__ part,
     int32_t part0, int32_t tokens_pad, const int32_t* __restrict__ label, int64_t piece0,
-    const float* __restrict__ lse, const float* __restrict__ picked,
+    const float* __restrict__ lse, const float* __restrict__ loss,
     const HeadState* __restrict__ state) {
   const int32_t valid = state->valid;
   const int32_t t = blockIdx.y * 8 + (threadIdx.x >> 5);
@@ -471,13 +458,13 @@ __global__ __launch_bounds__(256) void k_head_rescale(
     u32x4* o = (u32x4*)(g + (int64_t)t * piece + c);
     u32x4 v = {0, 0, 0, 0};
     if (there && c < left) {
-      const float f =
-          exp2_fast((part[(int64_t)(part0 + c / kHeadPart) * tokens_pad + t].x - z) * kLog2e);
+      const float f = exp2_fast(__builtin_fmaf(
+          -z, kLog2e, part[(int64_t)(part0 + c / kHeadPart) * tokens_pad + t].x));
       v = *o;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float p = widen<T>((v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) * f;
-        if (c + e == y) p = (exp2_fast((picked[t] - z) * kLog2e) - 1.0f) * g_scale<T>();
+        if (c + e == y) p = expm1f(-loss[t]) * g_scale<T>();
         if (c + e >= left) p = 0.0f;
         const uint32_t b = narrow<T>(p);
         v[e >> 1] = e & 1 ? (v[e >> 1] & 0xFFFFu) | b << 16 : (v[e >> 1] & 0xFFFF0000u) | b;
@@ -510,7 +497,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_head_rescale_few(
     const float* __restrict__ logits, uint16_t* __restrict__ g, int32_t piece, int32_t vocab,
     const int32_t* __restrict__ label, const float* __restrict__ lse,
-    const float* __restrict__ picked, const HeadState* __restrict__ state) {
+    const float* __restrict__ loss, const HeadState* __restrict__ state) {
   const int32_t t = blockIdx.y * 8 + (threadIdx.x >> 5);
   const bool there = t < state->valid;
   const float z = there ? lse[t] : 0.0f;
@@ -524,7 +511,7 @@ __global__ __launch_bounds__(256) void k_head_rescale_few(
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         v[e] = exp2_fast((l[e] - z) * kLog2e) * g_scale<T>();
-        if (c + e == y) v[e] = (exp2_fast((picked[t] - z) * kLog2e) - 1.0f) * g_scale<T>();
+        if (c + e == y) v[e] = expm1f(-loss[t]) * g_scale<T>();
         if (c + e >= vocab) v[e] = 0.0f;
       }
     }
@@ -535,45 +522,43 @@ __global__ __launch_bounds__(256) void k_head_rescale_few(
   }
 }
 
-// dx: A = g (token rows, contiguous along the vocabulary), B = w (contiguous
-// along the hidden axis).  Split s of the piece adds into its own fp32 block.
+// dx: A = w (rows of the tile: hidden columns, contiguous along them), B = g
+// (token rows, contiguous along the vocabulary).  Split s of the piece adds
+// into its own fp32 block.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_dx(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ w, int64_t ldw,
     int32_t vocab_left, int32_t hidden_w, int32_t hidden, int32_t hidden_pad, int32_t tokens_pad,
     int32_t most, int32_t first, const HeadState* __restrict__ state, float* __restrict__ acc_out) {
-  using G = Gemm<T, false, true>;
+  using G = Gemm<T, true, false>;
   ZK_GEMM_LDS;
-  const uint32_t ht = (uint32_t)((hidden + G::BN - 1) / G::BN);
-  const uint32_t tt = (uint32_t)((state->valid + G::BM - 1) / G::BM);
+  const uint32_t ht = (uint32_t)((hidden + G::BM - 1) / G::BM);
+  const uint32_t tt = (uint32_t)((state->valid + G::BN - 1) / G::BN);
   const int32_t split = dx_split((int32_t)(ht * tt), most);
   const int32_t part = (piece / split + kStage - 1) / kStage * kStage;
   int32_t mt, nt;
   if (!tile_of(blockIdx.x, tt, ht * (uint32_t)split, mt, nt)) return;
-  const int32_t h0 = nt % ht * G::BN, t0 = mt * G::BM, ks = nt / ht, k0 = ks * part;
+  const int32_t h0 = nt % ht * G::BM, t0 = mt * G::BN, ks = nt / ht, k0 = ks * part;
   int32_t K = piece - k0 < part ? piece - k0 : part;
   if (K > vocab_left - k0) K = vocab_left - k0;
   // g's columns are zero from the vocabulary's end to the next tile
-  const Operand A{g + (int64_t)t0 * piece + k0, (int64_t)piece * 2, G::BM, (K + 7) & ~7};
-  const Operand B{w + (int64_t)k0 * ldw + h0, ldw * 2, hidden_w - h0, K};
+  const Operand A{w + (int64_t)k0 * ldw + h0, ldw * 2, hidden_w - h0, K};
+  const Operand B{g + (int64_t)t0 * piece + k0, (int64_t)piece * 2, G::BN, (K + 7) & ~7};
   constexpr int MI = G::MI, NJ = G::NJ;
-  f32x16 acc[MI][NJ];
+  f32x4 acc[MI][NJ];
   G::run(A, B, K, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float* out = acc_out + ((int64_t)ks * tokens_pad + t0 + (wave / 4) * MI * 32) * hidden_pad;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int32_t h = h0 + (wave % 4) * NJ * 32 + j * 32 + (lane & 31);
-    if (h >= hidden_pad) continue;
+    const int32_t t = t0 + (wave % 4) * 64 + j * 16 + (lane & 15);
+    float* out = acc_out + ((int64_t)ks * tokens_pad + t) * hidden_pad;
+    asm volatile("" ::: "memory");
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      asm volatile("" ::: "memory");
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int r = 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-        float* o = out + (int64_t)r * hidden_pad + h;
-        *o = first ? acc[i][j][e] : *o + acc[i][j][e];
-      }
+      const int32_t h = h0 + wave / 4 * 128 + 16 * i + 4 * (lane >> 4);
+      if (h >= hidden_pad) continue;
+      f32x4* o = (f32x4*)(out + h);
+      *o = first ? acc[i][j] : *o + acc[i][j];
     }
   }
 }
@@ -622,14 +607,14 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
   const Operand A{x + h0, (int64_t)hidden_pad * 2, hidden_pad - h0, K};
   const Operand B{g + c0, (int64_t)piece * 2, piece - c0, K};
   constexpr int MI = G::MI, NJ = G::NJ;
-  f32x16 acc[MI][NJ];
+  f32x4 acc[MI][NJ];
   G::run(A, B, K, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (state->bad) {  // bad labels alone (no valid token) still have to show: c is NaN
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16{} + c;
+      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{} + c;
   }
   if (!F32OUT && !accumulate) {
     uint16_t* out = (uint16_t*)dw;
@@ -653,34 +638,29 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int32_t v = c0 + wave % 4 * 64 + j * 32 + (lane & 31);
+    const int32_t v = c0 + wave % 4 * 64 + j * 16 + (lane & 15);
     if (v >= vocab_left) continue;
+    asm volatile("" ::: "memory");
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      asm volatile("" ::: "memory");
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int32_t h = h0 + wave / 4 * 128 + 32 * i + 8 * q + 4 * (lane >> 5);
-        const int64_t at = (int64_t)v * lddw + h;
-        f32x4 d;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[e] = acc[i][j][4 * q + e] * c;
-        if constexpr (F32OUT) {
-          float* o = (float*)dw + at;
-          if (h + 4 <= hidden && ((uintptr_t)o & 15) == 0) {
-            if (accumulate) d = *(const f32x4*)o + d;
-            *(f32x4*)o = d;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (h + e < hidden) o[e] = accumulate ? o[e] + d[e] : d[e];
-          }
+      const int32_t h = h0 + wave / 4 * 128 + 16 * i + 4 * (lane >> 4);
+      const int64_t at = (int64_t)v * lddw + h;
+      f32x4 d = acc[i][j] * c;
+      if constexpr (F32OUT) {
+        float* o = (float*)dw + at;
+        if (h + 4 <= hidden && ((uintptr_t)o & 15) == 0) {
+          if (accumulate) d = *(const f32x4*)o + d;
+          *(f32x4*)o = d;
         } else {
-          uint16_t* o = (uint16_t*)dw + at;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (h + e < hidden) o[e] = (uint16_t)narrow<T>(widen<T>(o[e]) + d[e]);
+            if (h + e < hidden) o[e] = accumulate ? o[e] + d[e] : d[e];
         }
+      } else {
+        uint16_t* o = (uint16_t*)dw + at;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (h + e < hidden) o[e] = (uint16_t)narrow<T>(widen<T>(o[e]) + d[e]);
       }
     }
   }
@@ -730,8 +710,8 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
                      dim3(64 * kJoinWaves), 0, stream, at<const float2>(ws, p.part),
                      (int32_t)(((h->vocab + 255) / 256) * 2), (int32_t)p.tokens_pad,
                      at<const float>(ws, p.picked), at<const int32_t>(ws, p.index),
-                     at<float>(ws, p.lse), token_loss, lse, at<double>(ws, p.sums), h->mean, state,
-                     res);
+                     at<float>(ws, p.lse), at<float>(ws, p.loss), token_loss, lse,
+                     at<double>(ws, p.sums), 1.0 / (double)g_scale<T>(), h->mean, state, res);
   return (int)hipGetLastError();
 }
 
@@ -755,15 +735,14 @@ int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
                          dim3((uint32_t)((p.piece + kRescaleCols - 1) / kRescaleCols),
                               kFewTokens / 8),
                          dim3(256), 0, stream, at<const float>(ws, p.logits), g, (int32_t)p.piece,
-                         (int32_t)h->vocab, label, lse, at<const float>(ws, p.picked), state);
+                         (int32_t)h->vocab, label, lse, at<const float>(ws, p.loss), state);
     else if (have)
       hipLaunchKernelGGL(k_head_rescale<T>,
                          dim3((uint32_t)((left + kRescaleCols - 1) / kRescaleCols),
                               (uint32_t)(p.tokens_pad / 8)),
                          dim3(256), 0, stream, g, (int32_t)p.piece, (int32_t)left,
                          at<const float2>(ws, p.part), (int32_t)(v0 / kHeadPart),
-                         (int32_t)p.tokens_pad, label, v0, lse, at<const float>(ws, p.picked),
-                         state);
+                         (int32_t)p.tokens_pad, label, v0, lse, at<const float>(ws, p.loss), state);
     else
       hipLaunchKernelGGL(k_head_g<T>, dim3(tile_grid(ttiles, vtiles)), dim3(kGemmThreads), 0,
                          stream, w.w, w.ld, (int32_t)h->vocab, x, (int32_t)p.hidden_pad, w.K,
