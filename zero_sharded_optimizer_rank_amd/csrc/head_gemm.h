@@ -89,7 +89,8 @@ __device__ __forceinline__ bool tile_of(uint32_t block, uint32_t nm, uint32_t nn
 // One operand of a tile.
 struct Operand {
   const void* base;   // element (0, 0) of the tile
-  int64_t ld;         // bytes between rows (rows) or contraction indexes (cols)
+  int32_t ld;         // bytes between rows (rows) or contraction indexes (cols); at most 2^22,
+                      // so that offsets within a tile fit 32 bits
   int32_t count;      // rows of the tile that exist (rows), or columns from base to
                       // the end of a memory row (cols); multiples of 8 along memory
   int32_t k;          // contraction indexes that exist (rows: a multiple of 8)
@@ -117,13 +118,12 @@ struct Part {
     lds += wave * kLoads * 1024;
     if constexpr (!COLS) {
       const char* p = (const char*)o.base + 2 * (int64_t)k0;
-      const uint32_t bytes = left ? (uint32_t)((int64_t)(o.count - 1) * o.ld + 2 * left) : 0u;
-      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
+      const int32_t bytes = left > 0 ? (o.count - 1) * o.ld + 2 * left : 0;
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00020000);
       int row = wave * kLoads * 8;
       if constexpr (HALF >= 0) row = row / 64 * 128 + 64 * HALF + row % 64;
       const int chunk = (lane & 7) ^ ((lane >> 4) & 3);
-      const uint32_t v = (uint32_t)((int64_t)(row + (lane >> 3)) * o.ld);
-      const uint32_t inc = (uint32_t)(8 * o.ld);
+      const uint32_t v = (uint32_t)((row + (lane >> 3)) * o.ld), inc = 8u * (uint32_t)o.ld;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         const int c = chunk ^ ((j & 1) << 2);  // the 8 rows of every second load have bit 3 set
@@ -133,8 +133,8 @@ struct Part {
       }
     } else {
       const char* p = (const char*)o.base + (int64_t)k0 * o.ld;
-      const uint32_t bytes = left ? (uint32_t)((int64_t)(left - 1) * o.ld + 2 * (int64_t)o.count) : 0u;
-      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
+      const int32_t bytes = left > 0 ? (left - 1) * o.ld + 2 * o.count : 0;
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00020000);
       constexpr int kRowBytes = R * 2, kChunks = kRowBytes / 16, kLoadRows = 1024 / kRowBytes;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
@@ -143,7 +143,7 @@ struct Part {
         const int col = HALF < 0 ? 16 * q : (q >> 3) * 256 + 128 * HALF + 16 * (q & 7);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rsrc, (__attribute__((address_space(3))) void*)(lds + j * 1024), 16,
-            (uint32_t)((int64_t)k * o.ld) + col, 0, 0, 0);
+            (uint32_t)(k * o.ld + col), 0, 0, 0);
       }
     }
   }

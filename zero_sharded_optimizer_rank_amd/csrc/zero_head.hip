@@ -174,8 +174,8 @@ struct LogitTile {
                                              int32_t hidden_pad, int32_t K, const GemmLds& lds,
                                              f32x4 (&acc)[G::MI][G::NJ]) {
     const int64_t rows = vocab - v0;
-    const Operand A{w + v0 * ldw, ldw * 2, (int32_t)(rows < G::BM ? rows : G::BM), K};
-    const Operand B{x + (int64_t)t0 * hidden_pad, (int64_t)hidden_pad * 2, G::BN, K};
+    const Operand A{w + v0 * ldw, (int32_t)ldw * 2, (int32_t)(rows < G::BM ? rows : G::BM), K};
+    const Operand B{x + (int64_t)t0 * hidden_pad, hidden_pad * 2, G::BN, K};
     G::run(A, B, K, lds, acc);
   }
 };
@@ -542,8 +542,8 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dx(
   int32_t K = piece - k0 < part ? piece - k0 : part;
   if (K > vocab_left - k0) K = vocab_left - k0;
   // g's columns are zero from the vocabulary's end to the next tile
-  const Operand A{w + (int64_t)k0 * ldw + h0, ldw * 2, hidden_w - h0, K};
-  const Operand B{g + (int64_t)t0 * piece + k0, (int64_t)piece * 2, G::BN, (K + 7) & ~7};
+  const Operand A{w + (int64_t)k0 * ldw + h0, (int32_t)ldw * 2, hidden_w - h0, K};
+  const Operand B{g + (int64_t)t0 * piece + k0, piece * 2, G::BN, (K + 7) & ~7};
   constexpr int MI = G::MI, NJ = G::NJ;
   f32x4 acc[MI][NJ];
   G::run(A, B, K, lds, acc);
@@ -604,8 +604,8 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
   const int32_t h0 = nt * G::BM, c0 = mt * G::BN;
   const int32_t K = few && state->valid ? 2 * kFewTokens : state->valid;
   const float c = state->coef / g_scale<T>();
-  const Operand A{x + h0, (int64_t)hidden_pad * 2, hidden_pad - h0, K};
-  const Operand B{g + c0, (int64_t)piece * 2, piece - c0, K};
+  const Operand A{x + h0, hidden_pad * 2, hidden_pad - h0, K};
+  const Operand B{g + c0, piece * 2, piece - c0, K};
   constexpr int MI = G::MI, NJ = G::NJ;
   f32x4 acc[MI][NJ];
   G::run(A, B, K, lds, acc);
