@@ -31,7 +31,7 @@ DEVICE_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
 DEVICE_SOURCES = ("zero_kernels.hip", "zero_units.hip", "zero_noalloc.hip", "zero_tensors.hip",
-                  "zero_head.hip")
+                  "zero_head.hip", "zero_head_few.hip")
 HOST_SOURCES = ("zero_host.cpp", "zero_offload.cpp", "zero_tensors.cpp", "zero_head.cpp")
 # host Adam of the offload form: IEEE fp32, no contraction, errno-free sqrt
 HOST_FLAGS = {"zero_offload.cpp": ["-ffp-contract=off", "-fno-math-errno", "-pthread"]}

@@ -21,14 +21,13 @@ struct HeadPlan {
   int64_t piece;       // vocabulary rows a piece of the gradient takes (whole tiles)
   int64_t kept;        // first row of the last piece
   int32_t split;       // most ways the hidden gradient's contraction is split
-  bool few;            // gradient of at most kFewTokens tokens: g in two parts
+  bool few;            // at most kFewTokens tokens (see zero_head_few.hip)
   bool pack_w;         // w's rows do not start on 16-byte boundaries
   // offsets
-  size_t state, sums, index, label, lse, loss, x, w, part, picked, g, logits, acc, total;
+  size_t state, sums, index, label, lse, loss, x, xt, w, part, picked, g, logits,
+      acc, total;
 };
 constexpr int64_t kHeadPart = 128;
-// With this few tokens g is kept in two 16-bit parts: rows t and kFewTokens + t
-// of the one tile of tokens.
 constexpr int32_t kFewTokens = 64;
 
 struct HeadState {  // at offset `state`
@@ -53,5 +52,15 @@ int launch_head_loss(const zero_head_t* h, const HeadPlan& p, void* ws, float* t
                      float* lse, bool keep, zero_loss_result_t* res, hipStream_t stream);
 int launch_head_grad(const zero_head_t* h, const HeadPlan& p, void* ws,
                      const zero_head_grads_t* grads, bool kept, hipStream_t stream);
+
+// The same steps for few tokens: pack, logits (keep: also stored), gradients
+// (have: the logits are there).
+int launch_few_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse_in,
+                    float* token_loss, float* lse, const zero_head_grads_t* grads,
+                    hipStream_t stream);
+int launch_few_logits(const zero_head_t* h, const HeadPlan& p, void* ws, bool keep,
+                      hipStream_t stream);
+int launch_few_grads(const zero_head_t* h, const HeadPlan& p, void* ws,
+                     const zero_head_grads_t* grads, bool have, hipStream_t stream);
 
 }  // namespace zk

@@ -13,6 +13,10 @@ using namespace zk::host;
 namespace {
 
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+int64_t clamp(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
+// Largest vocabulary of the form for few tokens, which keeps their fp32 logits
+// for the gradient (256 bytes a vocabulary row: 512 MiB).
+constexpr int64_t kFewVocab = (int64_t)1 << 21;
 
 bool good_sizes(const zero_head_t* h) {
   return h->tokens >= 0 && h->tokens <= ZERO_HEAD_MAX_TOKENS && h->hidden >= 1 &&
@@ -87,50 +91,52 @@ namespace zk {
 
 HeadPlan head_plan(const zero_head_t* h, bool grad) {
   HeadPlan p{};
-  p.tokens_pad = up(h->tokens > 0 ? h->tokens : 1, kHeadTile);
   p.hidden_pad = up(h->hidden, kHeadStep);
-  p.parts = up(h->vocab, kHeadTile) / kHeadPart;
-  p.pack_w = h->hidden % 8 != 0 || h->ldw % 8 != 0 || !aligned(h->w, 16);
+  p.few = h->tokens <= kFewTokens && h->vocab <= kFewVocab;
+  p.tokens_pad = p.few ? kFewTokens : up(h->tokens, kHeadTile);
+  p.pack_w = !p.few && (h->hidden % 8 != 0 || h->ldw % 8 != 0 || !aligned(h->w, 16));
   const int64_t vocab_pad = up(h->vocab, kHeadTile);
-  if (grad) {
+  p.parts = vocab_pad / kHeadPart;
+  const int64_t htiles = up(h->hidden, kHeadTile) / kHeadTile;
+  if (grad && p.few) {
+    // dx: two rounds of the 256 CUs' workgroups (two a CU fit), of at least two stages each
+    p.split = (int32_t)clamp((512 + htiles - 1) / htiles, 1, up(h->vocab, 128) / 128);
+  } else if (grad) {
     // a piece's block of g stays within 1 GiB: with all 128256 rows of a
     // Llama-3 head up to 4096 tokens go in one piece, whose logits are formed
     // once, and every further doubling of the tokens halves the piece
     int64_t piece = ((int64_t)1 << 29) / p.tokens_pad / kHeadTile * kHeadTile;
-    if (piece < 16 * kHeadTile) piece = 16 * kHeadTile;
-    if (piece > vocab_pad) piece = vocab_pad;
+    piece = clamp(piece, 16 * kHeadTile, vocab_pad);
     const int64_t pieces = (vocab_pad + piece - 1) / piece;
     p.piece = up((vocab_pad + pieces - 1) / pieces, kHeadTile);
-    p.few = h->tokens <= kFewTokens && pieces == 1;
     p.kept = (h->vocab - 1) / p.piece * p.piece;
     // dx: up to four rounds of the 256 CUs (how many is settled on the device,
     // which knows the valid tokens)
-    const int64_t tiles = p.tokens_pad / kHeadTile * (up(h->hidden, kHeadTile) / kHeadTile);
-    int64_t split = (1024 + tiles - 1) / tiles;
-    if (split > 64) split = 64;
-    if (split > p.piece / kHeadTile) split = p.piece / kHeadTile;
-    p.split = (int32_t)split;
+    const int64_t tiles = p.tokens_pad / kHeadTile * htiles;
+    p.split = (int32_t)clamp((1024 + tiles - 1) / tiles, 1,
+                             p.piece / kHeadTile < 64 ? p.piece / kHeadTile : 64);
   }
   size_t at = 0;
-  auto take = [&](size_t bytes) {
+  auto take = [&](int64_t bytes) {
     const size_t o = at;
-    at += (bytes + 255) / 256 * 256;
+    at += (size_t)(bytes + 255) / 256 * 256;
     return o;
   };
   p.state = take(sizeof(HeadState));
-  p.sums = take(8 * (size_t)(p.tokens_pad / 64));
-  p.index = take(4 * (size_t)p.tokens_pad);
-  p.label = take(4 * (size_t)p.tokens_pad);
-  p.lse = take(4 * (size_t)p.tokens_pad);
-  p.loss = take(4 * (size_t)p.tokens_pad);
-  p.picked = take(4 * (size_t)p.tokens_pad);
-  p.x = take(2 * (size_t)p.tokens_pad * (size_t)p.hidden_pad);
-  p.w = take(p.pack_w ? 2 * (size_t)h->vocab * (size_t)p.hidden_pad : 0);
-  p.part = take(8 * (size_t)p.parts * (size_t)p.tokens_pad);
+  p.sums = take(8 * (p.tokens_pad / 64));
+  p.index = take(4 * p.tokens_pad);
+  p.label = take(4 * p.tokens_pad);
+  p.lse = take(4 * p.tokens_pad);
+  p.loss = take(4 * p.tokens_pad);
+  p.picked = take(4 * p.tokens_pad);
+  p.x = take(2 * p.tokens_pad * p.hidden_pad);
+  p.xt = take(grad && p.few ? 2 * p.tokens_pad * p.hidden_pad : 0);
+  p.w = take(p.pack_w ? 2 * h->vocab * p.hidden_pad : 0);
+  p.part = take(8 * p.parts * p.tokens_pad);
   if (grad) {
-    p.g = take(2 * (size_t)p.tokens_pad * (size_t)p.piece);
-    p.logits = take(p.few ? 4 * (size_t)kFewTokens * (size_t)p.piece : 0);
-    p.acc = take(4 * (size_t)p.split * (size_t)p.tokens_pad * (size_t)p.hidden_pad);
+    p.g = take(2 * p.tokens_pad * p.piece);
+    p.logits = take(p.few ? 4 * kFewTokens * h->vocab : 0);
+    p.acc = take(4 * p.split * p.tokens_pad * p.hidden_pad);
   }
   p.total = at;
   return p;

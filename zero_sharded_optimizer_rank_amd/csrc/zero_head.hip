@@ -11,54 +11,23 @@
 //   3. those partials are joined into lse and the loss;
 //   4. gradient, piece by piece: g = exp(l - lse) - [v = y] in 16 bits (the
 //      type the matrix cores multiply), then dx += g w (fp32 between pieces)
-//      and dw = g^T x.  With up to 64 tokens, whose few large elements of g
-//      would show their rounding in the results, g is kept as the sum of two
-//      16-bit parts, which lie in rows of the tile that would be idle.  The
-//      piece that the loss formed last has its
-//      exponentials (or logits) in the workspace already; the logits of the others are formed
+//      and dw = g^T x.  The piece that the loss formed last has its
+//      exponentials in g's block already; the logits of the others are formed
 //      again.
 // All products accumulate in fp32.
 #include <stddef.h>
 
-#include "head_gemm.h"
-#include "head_internal.h"
-#include "zero_device.h"
+#include "head_device.h"
 
 namespace zk {
 namespace {
 
 using namespace dev;
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kScanThreads = 1024;
 constexpr int kPackThreads = 256;
 constexpr int kGemmThreads = 512;
 constexpr int kJoinTokens = 64, kJoinWaves = 16, kJoinBatch = 8;
-
-// g's scale before it is rounded: |p - [v = y]| <= 1, so 2^15 keeps fp16 in
-// range and p down to 2^-29 normal; bf16 has fp32's exponents.
-template <typename T>
-__host__ __device__ constexpr float g_scale();
-template <>
-__host__ __device__ constexpr float g_scale<BF16>() { return 1.0f; }
-template <>
-__host__ __device__ constexpr float g_scale<FP16>() { return 32768.0f; }
-
-template <typename T>
-__device__ __forceinline__ constexpr float g_log2() { return g_scale<T>() == 1.0f ? 0.0f : 15.0f; }
-
-template <typename T>
-__device__ __forceinline__ uint32_t narrow(float x);
-template <>
-__device__ __forceinline__ uint32_t narrow<BF16>(float x) { return f2bf(x); }
-template <>
-__device__ __forceinline__ uint32_t narrow<FP16>(float x) { return f2h(x); }
-template <typename T>
-__device__ __forceinline__ float widen(uint32_t b);
-template <>
-__device__ __forceinline__ float widen<BF16>(uint32_t b) { return bf2f(b); }
-template <>
-__device__ __forceinline__ float widen<FP16>(uint32_t b) { return h2f(b); }
 
 // --- 1. scan and pack --------------------------------------------------------
 // One workgroup: the valid tokens in order.  index[r] is packed row r's token;
@@ -105,26 +74,15 @@ __global__ __launch_bounds__(kScanThreads) void k_head_scan(
   }
 }
 
-// Eight elements from p, of which the first n exist.
-__device__ __forceinline__ u32x4 take8(const uint16_t* p, int64_t n, bool whole16) {
-  if (whole16 && n >= 8) return *(const u32x4*)p;
-  u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < n) v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
-  return v;
-}
-
 // Workgroup r: packed row r copies valid token index[r], zero-padded (rows from
-// the valid count to the next whole tile are zero; with few tokens, rows
-// kFewTokens on hold them a second time); and if token r takes no part, its
-// loss, lse and dx are written.
+// the valid count to the next whole tile are zero); and if token r takes no
+// part, its loss, lse and dx are written.
 __global__ __launch_bounds__(kPackThreads) void k_head_pack_x(
     const uint16_t* __restrict__ x, int64_t ldx, int32_t tokens, int32_t hidden,
     int32_t hidden_pad, int32_t vocab, const int64_t* __restrict__ labels,
     const int32_t* __restrict__ index, const HeadState* __restrict__ state,
-    uint16_t* __restrict__ out, int32_t few, float* __restrict__ token_loss,
-    float* __restrict__ lse, uint16_t* __restrict__ dx, int64_t lddx) {
+    uint16_t* __restrict__ out, float* __restrict__ token_loss, float* __restrict__ lse,
+    uint16_t* __restrict__ dx, int64_t lddx) {
   const int32_t r = blockIdx.x, valid = state->valid;
   if (r < tokens) {
     const int64_t y = labels[r];
@@ -140,8 +98,7 @@ __global__ __launch_bounds__(kPackThreads) void k_head_pack_x(
   }
   if (r >= (valid + kHeadTile - 1) / kHeadTile * kHeadTile) return;
   u32x4* o = (u32x4*)(out + (int64_t)r * hidden_pad);
-  const int32_t q = few && r >= kFewTokens ? r - kFewTokens : r;
-  const uint16_t* p = q < valid ? x + (int64_t)index[q] * ldx : nullptr;
+  const uint16_t* p = r < valid ? x + (int64_t)index[r] * ldx : nullptr;
   const bool whole16 = ((uintptr_t)p & 15) == 0;
   for (int32_t c = threadIdx.x; c < hidden_pad / 8; c += kPackThreads) {
     u32x4 v = {0, 0, 0, 0};
@@ -180,32 +137,19 @@ struct LogitTile {
   }
 };
 
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// Four consecutive vocabulary rows of a token into g's type.
-template <typename T>
-__device__ __forceinline__ u32x2 narrow4(float a, float b, float c, float d) {
-  return u32x2{narrow<T>(a) | narrow<T>(b) << 16, narrow<T>(c) | narrow<T>(d) << 16};
-}
-
-// What the 16-bit value of x leaves.
-template <typename T>
-__device__ __forceinline__ float second(float x) { return x - widen<T>(narrow<T>(x)); }
-
 // Loss: (m, g_scale sum of 2^(l log2 e - m)) of every token over each 128
 // vocabulary rows, m the largest l log2 e rounded up, the label's row left out, and the label's logit: a confident token's
 // loss is log(1 + the others' sum), whose digits a sum that held the label's 1
 // would have lost.  Where the gradient follows in the same call, the
 // exponentials of the piece of the vocabulary that starts at `kept` stay in
-// g's block (rounded to 16 bits), or with few tokens the fp32 logits in
-// `logits`: k_head_rescale turns them into g without forming those logits
-// again.
+// g's block (rounded to 16 bits): k_head_rescale turns them into g without
+// forming those logits again.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, const uint16_t* __restrict__ x,
     int32_t hidden_pad, int32_t K, int32_t tokens_pad, const int32_t* __restrict__ label,
     const HeadState* __restrict__ state, float2* __restrict__ part, float* __restrict__ picked,
-    int64_t kept, int32_t piece, uint16_t* __restrict__ g, float* __restrict__ logits) {
+    int64_t kept, int32_t piece, uint16_t* __restrict__ g) {
   using L = LogitTile<T>;
   using G = typename L::G;
   static_assert(G::MI * 16 == kHeadPart, "one partial a wave");
@@ -249,11 +193,6 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
         }
       if (mine) picked[t] = p;
     }
-    if (logits && t < kFewTokens) {
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-        *(f32x4*)(logits + (int64_t)t * piece + vw + r0 + 16 * i) = acc[i][j];
-    }
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -286,14 +225,6 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
 }
 
 // --- 3. join -------------------------------------------------------------------
-// (m, s) stands for s 2^m.
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
-  const float n = __builtin_elementwise_maximum(m, m2);
-  if (n == -INFINITY) return;  // both empty: s = s2 = 0
-  s = s * exp2_fast(m - n) + s2 * exp2_fast(m2 - n);
-  m = n;
-}
-
 // Workgroup b joins the partials of 64 packed rows, kJoinWaves waves sharing
 // the vocabulary; the last workgroup to finish sums the losses.
 __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
@@ -369,7 +300,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_g(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, const uint16_t* __restrict__ x,
     int32_t hidden_pad, int32_t K, const int32_t* __restrict__ label,
     const float* __restrict__ lse, const HeadState* __restrict__ state, int64_t piece0,
-    int32_t piece, int32_t few, uint16_t* __restrict__ g) {
+    int32_t piece, uint16_t* __restrict__ g) {
   using L = LogitTile<T>;
   using G = typename L::G;
   const int32_t valid = state->valid;
@@ -416,18 +347,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_g(
         for (int e = 0; e < 4; ++e)
           if (!there || r0 + 16 * i + e >= rows) acc[i][j][e] = 0.0f;
     }
-    if (few && t < kFewTokens) {
-      uint16_t* o = g + (int64_t)t * piece + cw + r0;
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const f32x4& v = acc[i][j];
-        *(u32x2*)(o + 16 * i) = narrow4<T>(v[0], v[1], v[2], v[3]);
-        *(u32x2*)(o + (int64_t)kFewTokens * piece + 16 * i) =
-            narrow4<T>(second<T>(v[0]), second<T>(v[1]), second<T>(v[2]), second<T>(v[3]));
-      }
-    }
   }
-  if (few) return;
   G::transposed(lds, acc, narrow4<T>,
                 [&](int col, int row, u32x4 v) {
                   *(u32x4*)(g + (int64_t)(t0 + col) * piece + c0 + row) = v;
@@ -491,37 +411,6 @@ __device__ __forceinline__ int32_t dx_split(int32_t tiles, int32_t most) {
   return best;
 }
 
-// The same from the fp32 logits of few tokens, in two 16-bit parts.  Workgroup:
-// 8 tokens, kRescaleCols columns.
-template <typename T>
-__global__ __launch_bounds__(256) void k_head_rescale_few(
-    const float* __restrict__ logits, uint16_t* __restrict__ g, int32_t piece, int32_t vocab,
-    const int32_t* __restrict__ label, const float* __restrict__ lse,
-    const float* __restrict__ loss, const HeadState* __restrict__ state) {
-  const int32_t t = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const bool there = t < state->valid;
-  const float z = there ? lse[t] : 0.0f;
-  const int32_t y = there ? label[t] : -1;
-  const int32_t c1 = (int32_t)(blockIdx.x + 1) * kRescaleCols;
-  for (int32_t c = blockIdx.x * kRescaleCols + (threadIdx.x & 31) * 4; c < c1 && c < piece;
-       c += 128) {
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (there) {
-      const f32x4 l = *(const f32x4*)(logits + (int64_t)t * piece + c);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = exp2_fast((l[e] - z) * kLog2e) * g_scale<T>();
-        if (c + e == y) v[e] = expm1f(-loss[t]) * g_scale<T>();
-        if (c + e >= vocab) v[e] = 0.0f;
-      }
-    }
-    uint16_t* o = g + (int64_t)t * piece + c;
-    *(u32x2*)o = narrow4<T>(v[0], v[1], v[2], v[3]);
-    *(u32x2*)(o + (int64_t)kFewTokens * piece) =
-        narrow4<T>(second<T>(v[0]), second<T>(v[1]), second<T>(v[2]), second<T>(v[3]));
-  }
-}
-
 // dx: A = w (rows of the tile: hidden columns, contiguous along them), B = g
 // (token rows, contiguous along the vocabulary).  Split s of the piece adds
 // into its own fp32 block.
@@ -567,8 +456,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dx(
 template <typename T>
 __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
     const float* __restrict__ acc, int32_t most, int32_t tokens_pad, int32_t hidden_pad,
-    int32_t hidden, int32_t few, const int32_t* __restrict__ index,
-    const HeadState* __restrict__ state, uint16_t* __restrict__ dx, int64_t lddx) {
+    int32_t hidden, const int32_t* __restrict__ index, const HeadState* __restrict__ state, uint16_t* __restrict__ dx, int64_t lddx) {
   const int32_t r = blockIdx.y, valid = state->valid;
   const int32_t h = (blockIdx.x * kPackThreads + threadIdx.x) * 4;
   if (r >= valid || h >= hidden) return;
@@ -577,10 +465,8 @@ __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
   const float c = state->coef / g_scale<T>();
   const float* p = acc + (int64_t)r * hidden_pad + h;
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int32_t k = 0; k < split; ++k, p += (int64_t)tokens_pad * hidden_pad) {
+  for (int32_t k = 0; k < split; ++k, p += (int64_t)tokens_pad * hidden_pad)
     s += *(const f32x4*)p;
-    if (few) s += *(const f32x4*)(p + (int64_t)kFewTokens * hidden_pad);
-  }
   uint16_t* o = dx + (int64_t)index[r] * lddx + h;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
@@ -594,7 +480,7 @@ template <typename T, bool F32OUT>
 __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ x,
     int32_t hidden_pad, int32_t hidden, int32_t vocab_left, const HeadState* __restrict__ state,
-    int32_t few, int32_t accumulate, void* __restrict__ dw, int64_t lddw) {
+    int32_t accumulate, void* __restrict__ dw, int64_t lddw) {
   using G = Gemm<T, true, true>;
   ZK_GEMM_LDS;
   int32_t mt, nt;
@@ -602,7 +488,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
                (uint32_t)((hidden + G::BM - 1) / G::BM), mt, nt))
     return;
   const int32_t h0 = nt * G::BM, c0 = mt * G::BN;
-  const int32_t K = few && state->valid ? 2 * kFewTokens : state->valid;
+  const int32_t K = state->valid;
   const float c = state->coef / g_scale<T>();
   const Operand A{x + h0, hidden_pad * 2, hidden_pad - h0, K};
   const Operand B{g + c0, piece * 2, piece - c0, K};
@@ -610,12 +496,6 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
   f32x4 acc[MI][NJ];
   G::run(A, B, K, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (state->bad) {  // bad labels alone (no valid token) still have to show: c is NaN
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{} + c;
-  }
   if (!F32OUT && !accumulate) {
     uint16_t* out = (uint16_t*)dw;
     G::transposed(lds, acc,
@@ -666,28 +546,6 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
   }
 }
 
-template <typename P>
-P* at(void* ws, size_t off) { return (P*)((char*)ws + off); }
-
-#define ZK_LAUNCHED()                              \
-  do {                                             \
-    const hipError_t e_ = hipGetLastError();       \
-    if (e_ != hipSuccess) return (int)e_;          \
-  } while (0)
-
-struct WeightView {
-  const uint16_t* w;
-  int64_t ld;       // elements
-  int32_t K;        // contraction length of the logits
-  int32_t width;    // columns a row holds
-};
-WeightView weight_view(const zero_head_t* h, const HeadPlan& p, void* ws) {
-  if (p.pack_w)
-    return {at<const uint16_t>(ws, p.w), p.hidden_pad, (int32_t)p.hidden_pad,
-            (int32_t)p.hidden_pad};
-  return {(const uint16_t*)h->w, h->ldw, (int32_t)h->hidden, (int32_t)h->hidden};
-}
-
 // kept: the vocabulary row from which the exponentials stay in g's block, or
 // none if the loss stands alone.
 template <typename T>
@@ -695,20 +553,23 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
            bool keep, zero_loss_result_t* res, hipStream_t stream) {
   const WeightView w = weight_view(h, p, ws);
   HeadState* state = at<HeadState>(ws, p.state);
-  if (h->tokens > 0) {
+  const int64_t tile = p.few ? kHeadPart : kHeadTile;  // vocabulary rows a workgroup takes
+  if (p.few) {
+    const int e = launch_few_logits(h, p, ws, keep, stream);
+    if (e) return e;
+  } else if (h->tokens > 0) {
     hipLaunchKernelGGL(k_head_partials<T>,
                        dim3(tile_grid(p.tokens_pad / 256, (h->vocab + 255) / 256)),
                        dim3(kGemmThreads), 0, stream, w.w, w.ld, (int32_t)h->vocab,
                        at<const uint16_t>(ws, p.x), (int32_t)p.hidden_pad, w.K,
                        (int32_t)p.tokens_pad, at<const int32_t>(ws, p.label), state,
                        at<float2>(ws, p.part), at<float>(ws, p.picked), p.kept,
-                       (int32_t)p.piece, keep && !p.few ? at<uint16_t>(ws, p.g) : nullptr,
-                       keep && p.few ? at<float>(ws, p.logits) : nullptr);
+                       (int32_t)p.piece, keep ? at<uint16_t>(ws, p.g) : nullptr);
     ZK_LAUNCHED();
   }
   hipLaunchKernelGGL(k_head_join, dim3((uint32_t)(p.tokens_pad / kJoinTokens)),
                      dim3(64 * kJoinWaves), 0, stream, at<const float2>(ws, p.part),
-                     (int32_t)(((h->vocab + 255) / 256) * 2), (int32_t)p.tokens_pad,
+                     (int32_t)((h->vocab + tile - 1) / tile * tile / kHeadPart), (int32_t)p.tokens_pad,
                      at<const float>(ws, p.picked), at<const int32_t>(ws, p.index),
                      at<float>(ws, p.lse), at<float>(ws, p.loss), token_loss, lse,
                      at<double>(ws, p.sums), 1.0 / (double)g_scale<T>(), h->mean, state, res);
@@ -730,13 +591,7 @@ int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
   const int32_t* label = at<const int32_t>(ws, p.label);
   const float* lse = at<const float>(ws, p.lse);
   if (h->tokens > 0) {
-    if (have && p.few)
-      hipLaunchKernelGGL(k_head_rescale_few<T>,
-                         dim3((uint32_t)((p.piece + kRescaleCols - 1) / kRescaleCols),
-                              kFewTokens / 8),
-                         dim3(256), 0, stream, at<const float>(ws, p.logits), g, (int32_t)p.piece,
-                         (int32_t)h->vocab, label, lse, at<const float>(ws, p.loss), state);
-    else if (have)
+    if (have)
       hipLaunchKernelGGL(k_head_rescale<T>,
                          dim3((uint32_t)((left + kRescaleCols - 1) / kRescaleCols),
                               (uint32_t)(p.tokens_pad / 8)),
@@ -746,7 +601,7 @@ int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
     else
       hipLaunchKernelGGL(k_head_g<T>, dim3(tile_grid(ttiles, vtiles)), dim3(kGemmThreads), 0,
                          stream, w.w, w.ld, (int32_t)h->vocab, x, (int32_t)p.hidden_pad, w.K,
-                         label, lse, state, v0, (int32_t)p.piece, p.few ? 1 : 0, g);
+                         label, lse, state, v0, (int32_t)p.piece, g);
     ZK_LAUNCHED();
     hipLaunchKernelGGL(k_head_dx<T>, dim3(tile_grid(htiles * p.split, ttiles)),
                        dim3(kGemmThreads), 0, stream, g, (int32_t)p.piece, w.w + v0 * w.ld, w.ld,
@@ -760,13 +615,11 @@ int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
   if (gr->dw_dtype == ZERO_F32)
     hipLaunchKernelGGL((k_head_dw<T, true>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads),
                        0, stream, g, (int32_t)p.piece, x, (int32_t)p.hidden_pad,
-                       (int32_t)h->hidden, (int32_t)left, state, p.few ? 1 : 0, gr->accumulate, dw,
-                       gr->lddw);
+                       (int32_t)h->hidden, (int32_t)left, state, gr->accumulate, dw, gr->lddw);
   else
     hipLaunchKernelGGL((k_head_dw<T, false>), dim3(tile_grid(htiles, vtiles)), dim3(kGemmThreads),
                        0, stream, g, (int32_t)p.piece, x, (int32_t)p.hidden_pad,
-                       (int32_t)h->hidden, (int32_t)left, state, p.few ? 1 : 0, gr->accumulate, dw,
-                       gr->lddw);
+                       (int32_t)h->hidden, (int32_t)left, state, gr->accumulate, dw, gr->lddw);
   return (int)hipGetLastError();
 }
 
@@ -783,7 +636,7 @@ int grad_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_gr
                        dim3((uint32_t)((h->hidden + 4 * kPackThreads - 1) / (4 * kPackThreads)),
                             (uint32_t)h->tokens),
                        dim3(kPackThreads), 0, stream, at<const float>(ws, p.acc), p.split,
-                       (int32_t)p.tokens_pad, (int32_t)p.hidden_pad, (int32_t)h->hidden, p.few ? 1 : 0,
+                       (int32_t)p.tokens_pad, (int32_t)p.hidden_pad, (int32_t)h->hidden,
                        at<const int32_t>(ws, p.index), at<HeadState>(ws, p.state),
                        (uint16_t*)gr->dx, gr->lddx);
   return (int)hipGetLastError();
@@ -794,6 +647,7 @@ int grad_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_gr
 int launch_head_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse_in,
                      float* token_loss, float* lse, const zero_head_grads_t* gr,
                      hipStream_t stream) {
+  if (p.few) return launch_few_pack(h, p, ws, lse_in, token_loss, lse, gr, stream);
   HeadState* state = at<HeadState>(ws, p.state);
   hipLaunchKernelGGL(k_head_scan, dim3(1), dim3(kScanThreads), 0, stream, h->labels,
                      (int32_t)h->tokens, (int32_t)h->vocab, h->loss_scale, h->mean, lse_in,
@@ -804,8 +658,8 @@ int launch_head_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const fl
     hipLaunchKernelGGL(k_head_pack_x, dim3((uint32_t)p.tokens_pad), dim3(kPackThreads), 0, stream,
                        (const uint16_t*)h->x, h->ldx, (int32_t)h->tokens, (int32_t)h->hidden,
                        (int32_t)p.hidden_pad, (int32_t)h->vocab, h->labels,
-                       at<const int32_t>(ws, p.index), state, at<uint16_t>(ws, p.x), p.few ? 1 : 0,
-                       token_loss, lse, gr ? (uint16_t*)gr->dx : nullptr, gr ? gr->lddx : 0);
+                       at<const int32_t>(ws, p.index), state, at<uint16_t>(ws, p.x), token_loss,
+                       lse, gr ? (uint16_t*)gr->dx : nullptr, gr ? gr->lddx : 0);
     ZK_LAUNCHED();
   }
   if (p.pack_w) {
@@ -825,6 +679,7 @@ int launch_head_loss(const zero_head_t* h, const HeadPlan& p, void* ws, float* t
 
 int launch_head_grad(const zero_head_t* h, const HeadPlan& p, void* ws,
                      const zero_head_grads_t* gr, bool kept, hipStream_t stream) {
+  if (p.few) return launch_few_grads(h, p, ws, gr, kept, stream);
   return h->dtype == ZERO_BF16 ? grad_t<BF16>(h, p, ws, gr, kept, stream)
                                : grad_t<FP16>(h, p, ws, gr, kept, stream);
 }

@@ -1,0 +1,609 @@
+// The head's loss and gradients for up to 64 tokens (short prompts, single
+// tokens).
+//
+// With so few tokens every product is bound by w: the logits and dx read it
+// once each, dw writes as much; the arithmetic (128 operations a weight) is an
+// eighth of what the matrix cores do in that time.  So w is never staged for
+// reuse: the logits take it from memory straight into fragments, each wave its
+// own 32 vocabulary rows, with no barrier in the loop; and since the few large
+// elements of g would show a 16-bit rounding in the results, g is taken as the
+// sum of two 16-bit values, at twice the products.  The fp32 logits of the
+// tokens stay in the workspace (256 bytes a vocabulary row), token-contiguous.
+// w's rows may start anywhere; nothing is laid out again.
+//
+//   k_few_pack    valid tokens in order, x and its transpose
+//   k_few_logits  logits, and the partial softmax of 128 vocabulary rows
+//   (join)        as with many tokens
+//   k_few_grads   dw tiles, and dx's partial sums over runs of the vocabulary
+//   k_few_dx      those sums joined
+#include <stddef.h>
+
+#include "head_device.h"
+
+namespace zk {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads4 = 256;  // four waves
+constexpr int kT = kFewTokens;  // 64
+
+// 16 bytes at any element's address.
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+
+// Elements [k, k + 8) of a row of n elements; those past its end are zero.
+__device__ __forceinline__ s16x8 row8(const uint16_t* row, int32_t k, int32_t n) {
+  u32x4 v = {0, 0, 0, 0};
+  if (k + 8 <= n) {
+    v = *(const u32x4_a2*)(row + k);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k + e < n) v[e >> 1] |= (uint32_t)row[k + e] << (16 * (e & 1));
+  }
+  return __builtin_bit_cast(s16x8, v);
+}
+
+// Workgroup r: packed row r of x (zero past the valid tokens) and column r of
+// its transpose; what token r, if it takes no part, gets.  Every wave finds
+// the valid tokens by itself: there are at most 64.
+__global__ __launch_bounds__(kThreads4) void k_few_pack(
+    const int64_t* __restrict__ labels, int32_t tokens, int32_t vocab, double loss_scale,
+    int32_t mean, const float* __restrict__ lse_in, const uint16_t* __restrict__ x, int64_t ldx,
+    int32_t hidden, int32_t hidden_pad, int32_t* __restrict__ index, int32_t* __restrict__ label,
+    float* __restrict__ lse, HeadState* __restrict__ state, uint16_t* __restrict__ xp,
+    uint16_t* __restrict__ xt, float* __restrict__ token_loss, float* __restrict__ lse_out,
+    uint16_t* __restrict__ dx, int64_t lddx) {
+  const int lane = threadIdx.x & 63;
+  const int32_t r = blockIdx.x;
+  const int64_t y = lane < tokens ? labels[lane] : -1;
+  const uint64_t ok = __ballot(y >= 0 && y < vocab), bad = __ballot(y >= vocab);
+  const int32_t valid = __popcll(ok);
+  if (r == 0 && threadIdx.x < 64) {
+    if (ok >> lane & 1) {
+      const int32_t at = __popcll(ok & ((1ull << lane) - 1));
+      index[at] = lane;
+      label[at] = (int32_t)y;
+      if (lse_in) lse[at] = lse_in[lane];
+    }
+    if (lane == 0) {
+      double c = loss_scale;
+      if (mean) c /= valid > 0 ? (double)valid : 1.0;
+      state->valid = valid;
+      state->ticket = 0;
+      state->bad = __popcll(bad);
+      state->coef = bad ? __builtin_nanf("") : (float)c;
+    }
+  }
+  if (r < tokens && !(ok >> r & 1)) {
+    if (threadIdx.x == 0) {
+      const float v = bad >> r & 1 ? __builtin_nanf("") : 0.0f;
+      if (token_loss) token_loss[r] = v;
+      if (lse_out) lse_out[r] = v;
+    }
+    if (dx)
+      for (int32_t h = threadIdx.x; h < hidden; h += kThreads4) dx[r * lddx + h] = 0;
+  }
+  int32_t src = -1;  // the r-th valid token
+  uint64_t m = ok;
+  for (int32_t i = 0; m; ++i, m &= m - 1)
+    if (i == r) src = __ffsll((unsigned long long)m) - 1;
+  for (int32_t c = threadIdx.x; c < hidden_pad / 8; c += kThreads4) {
+    s16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (src >= 0) v = row8(x + src * ldx, 8 * c, hidden);
+    *(s16x8*)(xp + (int64_t)r * hidden_pad + 8 * c) = v;
+    if (xt)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) xt[(int64_t)(8 * c + e) * kT + r] = (uint16_t)v[e];
+  }
+}
+
+// Logits of 128 vocabulary rows, 32 a wave: A = w from memory straight into
+// fragments, two steps of 64 hidden columns (8 KiB a wave) on their way; B =
+// packed x through LDS, 128 columns at a time, since all four waves read it.
+// Three waves a SIMD with two steps ahead read w of 128256 x 4096 at 5.9 TB/s
+// (179 us) and of 50257 x 1600, which the last-level cache holds, in 33 us; two
+// waves with three steps 217 and 40 us, three with three (spilled) 315 and 65;
+// non-temporal loads lose 3 and 12 us.
+constexpr int kAhead = 2, kXTile = 128;
+template <typename T>
+__global__ __launch_bounds__(kThreads4) __attribute__((amdgpu_waves_per_eu(3, 3))) void
+k_few_logits(
+    const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, int32_t hidden,
+    const uint16_t* __restrict__ x, int32_t hidden_pad, const int32_t* __restrict__ label,
+    const HeadState* __restrict__ state, float2* __restrict__ part, float* __restrict__ picked,
+    float* __restrict__ logits) {
+  __shared__ float s_m[4][kT], s_s[4][kT];
+  // [64 tokens][128 columns]: 16-byte chunk c of row r lies at c ^ (r & 15)
+  __shared__ __attribute__((aligned(1024))) char lx[2][kT * kXTile * 2];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, q = lane & 15;
+  const int64_t v0 = (int64_t)blockIdx.x * kHeadPart + wave * 32;
+  const uint16_t* wr[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t v = v0 + 16 * i + q;
+    wr[i] = w + (v < vocab ? v : vocab - 1) * ldw;  // rows past the end are masked below
+  }
+  f32x4 acc[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
+  s16x8 a[kAhead + 1][2][2], xr[4];
+  auto fetch_w = [&](s16x8 (&d)[2][2], int32_t step) {
+    const int32_t k0 = step * kStage;
+    if (k0 + kStage <= hidden) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          d[s][i] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(wr[i] + k0 + 32 * s + 8 * g));
+    } else {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) d[s][i] = row8(wr[i], k0 + 32 * s + 8 * g, hidden);
+    }
+  };
+  // thread: chunk threadIdx % 16 of rows threadIdx / 16 + 16 k
+  const int xc = threadIdx.x & 15, xrow = threadIdx.x >> 4;
+  auto fetch_x = [&](int32_t tile) {
+    const int32_t c = tile * kXTile + 8 * xc;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      xr[k] = c < hidden_pad ? *(const s16x8*)(x + (int64_t)(xrow + 16 * k) * hidden_pad + c)
+                             : s16x8{};
+  };
+  auto store_x = [&](char* d) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *(s16x8*)(d + (xrow + 16 * k) * 256 + ((xc ^ xrow) << 4)) = xr[k];
+  };
+  auto use = [&](const s16x8 (&d)[2][2], const char* l, int half) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const s16x8 b = *(const s16x8*)(l + (16 * j + q) * 256 + (((8 * half + 4 * s + g) ^ q) << 4));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[i][j] = mfma(T{}, d[s][i], b, acc[i][j]);
+      }
+  };
+  const int32_t tiles = (hidden_pad + 2 * kXTile - 1) / (2 * kXTile) * 2;  // whole pairs; zeros past the end
+  fetch_x(0);
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) fetch_w(a[k], k);
+  store_x(lx[0]);
+  fetch_x(1);
+  for (int32_t t = 0; t < tiles; t += 2) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // tile t + h is in LDS, and the buffer of the one before is free
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      store_x(lx[1 - h]);
+      fetch_x(t + h + 2);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int now = 2 * h + k;  // step 2t + now
+        fetch_w(a[(now + kAhead) & 3], 2 * t + now + kAhead);
+        use(a[now], lx[h], k);
+      }
+    }
+  }
+  const int32_t rows = (int32_t)(vocab - v0 < 32 ? vocab - v0 : 32);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int32_t t = 16 * j + q;
+    const int64_t y = t < state->valid ? (int64_t)label[t] - v0 : -1;
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 16 * i + 4 * g + e;
+        float l = acc[i][j][e];
+        if (r >= rows) l = -INFINITY;
+        if (logits && r < rows) logits[(v0 + r) * kT + t] = l;
+        if (r == y) {
+          picked[t] = l;
+          l = -INFINITY;
+        }
+        acc[i][j][e] = l;
+        m = __builtin_elementwise_maximum(m, l);
+      }
+    m = __builtin_elementwise_maximum(m, __shfl_xor(m, 16));
+    m = __builtin_elementwise_maximum(m, __shfl_xor(m, 32));
+    m = __builtin_ceilf(m * kLog2e);
+    const float shift = (m == -INFINITY ? 0.0f : -m) + g_log2<T>();
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s += exp2_fast(__builtin_fmaf(acc[i][j][e], kLog2e, shift));
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lane < 16) {
+      s_m[wave][t] = m;
+      s_s[wave][t] = s;
+    }
+  }
+  __syncthreads();
+  if (wave == 0) {
+    float m = s_m[0][lane], s = s_s[0][lane];
+#pragma unroll
+    for (int k = 1; k < 4; ++k) join(m, s, s_m[k][lane], s_s[k][lane]);
+    part[(int64_t)blockIdx.x * kT + lane] = float2{m, s};
+  }
+}
+
+// A token's side of g: its lse in base 2 less g's scale, its label, and the
+// label's element e^-loss - 1 (with the loss of the same call, which keeps the
+// digits of a small one, or from lse).
+struct Token {
+  float shift, dy;
+  int32_t y;
+};
+template <typename T>
+__device__ __forceinline__ Token token_of(int32_t t, int32_t valid, const int32_t* label,
+                                          const float* lse, const float* loss,
+                                          const float* picked) {
+  Token k{-INFINITY, 0.0f, -1};
+  if (t < valid) {
+    k.shift = g_log2<T>() - lse[t] * kLog2e;
+    k.dy = expm1f(loss ? -loss[t] : picked[t] - lse[t]) * g_scale<T>();
+    k.y = label[t];
+  }
+  return k;
+}
+template <typename T>
+__device__ __forceinline__ float g_of(float l, int32_t v, int32_t vocab, const Token& k) {
+  if (k.shift == -INFINITY || v >= vocab) return 0.0f;  // no token, no row
+  return v == k.y ? k.dy : exp2_fast(__builtin_fmaf(l, kLog2e, k.shift));
+}
+
+// Eight values into their two 16-bit parts.
+template <typename T>
+__device__ __forceinline__ void two_parts(const float (&v)[8], s16x8& hi, s16x8& lo) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    hi[e] = (short)narrow<T>(v[e]);
+    lo[e] = (short)narrow<T>(v[e] - widen<T>((uint16_t)hi[e]));
+  }
+}
+
+struct FewGrad {
+  const float* logits;
+  const uint16_t* w;
+  int64_t ldw;
+  const uint16_t* xt;
+  const int32_t* label;
+  const float *lse, *loss, *picked;
+  const HeadState* state;
+  float* acc;       // dx's partial sums [split][64][hidden_pad]
+  void* dw;
+  int64_t lddw;
+  int32_t vocab, hidden, hidden_pad;
+  int32_t dw_blocks, dw_cols;       // workgroups of dw: 64 rows times dw_cols hidden columns
+  int32_t split, run;               // dx: vocabulary rows a split takes (whole stages)
+  int32_t accumulate;
+};
+
+// dw of 64 vocabulary rows and dw_cols hidden columns: A = x^T (rows: hidden),
+// B = g (rows: vocabulary), contraction over the 64 tokens.  A wave takes 64
+// columns at a time; its g stays in registers.
+template <typename T, bool F32OUT>
+__device__ __forceinline__ void few_dw(const FewGrad& f, char* lds, int32_t block) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, q = lane & 15;
+  const int32_t vblocks = (f.vocab + 63) / 64;
+  const int32_t v0 = block % vblocks * 64, h1 = (block / vblocks + 1) * f.dw_cols;
+  const float c = f.state->coef / g_scale<T>();
+  const int32_t valid = f.state->valid;
+  s16x8 hi[2][4], lo[2][4];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    float v[4][8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int32_t row = v0 + 16 * j + q;
+      const f32x4* p = (const f32x4*)(f.logits + (int64_t)(row < f.vocab ? row : 0) * kT + 32 * s + 8 * g);
+      const f32x4 a = p[0], b = p[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[j][e] = a[e];
+        v[j][4 + e] = b[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const Token k = token_of<T>(32 * s + 8 * g + e, valid, f.label, f.lse, f.loss, f.picked);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j][e] = g_of<T>(v[j][e], v0 + 16 * j + q, f.vocab, k);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) two_parts<T>(v[j], hi[s][j], lo[s][j]);
+  }
+  char* mine = lds + wave * 8192;  // 64 rows of 64 columns in 16 bits
+  for (int32_t h0 = h1 - f.dw_cols + wave * 64; h0 < h1 && h0 < f.hidden; h0 += 256) {
+    f32x4 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint16_t* p = f.xt + (int64_t)(h0 + 16 * i + q) * kT + 8 * g;
+      const s16x8 a0 = *(const s16x8*)p, a1 = *(const s16x8*)(p + 32);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+        d = mfma(T{}, a0, lo[0][j], d);
+        d = mfma(T{}, a1, lo[1][j], d);
+        d = mfma(T{}, a0, hi[0][j], d);
+        acc[i][j] = mfma(T{}, a1, hi[1][j], d) * c;
+      }
+    }
+    if (!F32OUT && !f.accumulate) {
+      // through this wave's own LDS (in order within a wave), so that the rows
+      // leave in 128-byte pieces; 16-byte chunk k of row r lies at k ^ (r & 7)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4& d = acc[i][j];
+          const int r = 16 * j + q, k = 2 * i + (g >> 1);
+          *(u32x2*)(mine + r * 128 + ((k ^ (r & 7)) << 4) + (g & 1) * 8) =
+              narrow4<T>(d[0], d[1], d[2], d[3]);
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = 8 * k + (lane >> 3);
+        const u32x4 d = *(const u32x4*)(mine + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        const int32_t v = v0 + r, h = h0 + (lane & 7) * 8;
+        if (v >= f.vocab || h >= f.hidden) continue;
+        uint16_t* o = (uint16_t*)f.dw + (int64_t)v * f.lddw + h;
+        if (h + 8 <= f.hidden) {
+          *(u32x4_a2*)o = d;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (h + e < f.hidden) o[e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int32_t v = v0 + 16 * j + q;
+        if (v >= f.vocab) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int32_t h = h0 + 16 * i + 4 * g + e;
+            if (h >= f.hidden) continue;
+            const int64_t at = (int64_t)v * f.lddw + h;
+            if constexpr (F32OUT) {
+              float* o = (float*)f.dw + at;
+              *o = f.accumulate ? *o + acc[i][j][e] : acc[i][j][e];
+            } else {
+              uint16_t* o = (uint16_t*)f.dw + at;
+              *o = (uint16_t)narrow<T>(widen<T>(*o) + acc[i][j][e]);
+            }
+          }
+      }
+    }
+  }
+}
+
+// dx's partial sums of 256 hidden columns over one run of the vocabulary, 64
+// rows at a time: A = w (columns of memory, staged in LDS), B = g, which the
+// workgroup forms in LDS from the logits.  The next rows of w and of the
+// logits are on their way while these are multiplied.
+template <typename T>
+__device__ __forceinline__ void few_dx(const FewGrad& f, char* lds, int32_t block) {
+  using FA = Frags<256, true>;
+  using FB = Frags<64, false>;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t htiles = (f.hidden + 255) / 256;
+  const int32_t h0 = block % htiles * 256, ks = block / htiles;
+  const int32_t va = ks * f.run, vb = va + f.run < f.vocab ? va + f.run : f.vocab;
+  const Token tok = token_of<T>(lane, f.state->valid, f.label, f.lse, f.loss, f.picked);
+  lds_char* lw = (lds_char*)lds;             // w: [64 rows][256 columns], pairs swizzled
+  lds_char* lg = (lds_char*)(lds + 32768);   // g: two parts of [64 tokens][64 rows]
+  const FA fa(wave * 64, lane);
+  const FB fb(0, lane);
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
+  s16x8 nw[8];
+  float nl[16];
+  auto fetch = [&](int32_t v0) {  // w: rows 8k + wave*2 + lane/32
+    const uint16_t* p = f.w + (v0 + wave * 2 + (lane >> 5)) * f.ldw + h0;
+    const float* l = f.logits + (int64_t)(v0 + wave * 16) * kT + lane;
+    if (v0 + kStage <= vb && h0 + 256 <= f.hidden) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        nw[k] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(p + 8 * k * f.ldw + (lane & 31) * 8));
+#pragma unroll
+      for (int e = 0; e < 16; ++e) nl[e] = l[e * kT];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        nw[k] = s16x8{};
+        if (v0 + 8 * k + wave * 2 + (lane >> 5) < vb)
+          nw[k] = row8(p + 8 * k * f.ldw, (lane & 31) * 8, f.hidden - h0);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) nl[e] = v0 + wave * 16 + e < vb ? l[e * kT] : 0.0f;
+    }
+  };
+  if (va < vb) fetch(va);
+  for (int32_t v0 = va; v0 < vb; v0 += kStage) {
+    __syncthreads();  // the last rows have been multiplied
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = 8 * k + wave * 2 + (lane >> 5);
+      const int c = (lane & 31) ^ ((r & 3) << 2 | (r >> 3 & 1) << 1);
+      *(__attribute__((address_space(3))) s16x8*)(lw + r * 512 + c * 16) = nw[k];
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = g_of<T>(nl[8 * p + e], v0 + wave * 16 + 8 * p + e, vb, tok);
+      s16x8 hi, lo;
+      two_parts<T>(v, hi, lo);
+      lds_char* o = lg + lane * 128 + (((2 * wave + p) ^ (lane >> 1 & 7)) << 4);
+      *(__attribute__((address_space(3))) s16x8*)o = hi;
+      *(__attribute__((address_space(3))) s16x8*)(o + 8192) = lo;
+    }
+    if (v0 + kStage < vb) fetch(v0 + kStage);
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      s16x8 a[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = fa.load(lw, i, s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const s16x8 hi = fb.load(lg, j, s), lo = fb.load(lg + 8192, j, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[i][j] = mfma(T{}, a[i], lo, acc[i][j]);
+          acc[i][j] = mfma(T{}, a[i], hi, acc[i][j]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int32_t h = h0 + wave * 64 + 16 * i + 4 * (lane >> 4);
+      if (h < f.hidden_pad)
+        *(f32x4*)(f.acc + ((int64_t)ks * kT + 16 * j + (lane & 15)) * f.hidden_pad + h) = acc[i][j];
+    }
+}
+
+// Workgroups of dx first: they run longest.
+template <typename T, bool F32OUT>
+__global__ __launch_bounds__(kThreads4) void k_few_grads(FewGrad f, int32_t dx_blocks) {
+  __shared__ __attribute__((aligned(1024))) char lds[49152];
+  if ((int32_t)blockIdx.x < dx_blocks) few_dx<T>(f, lds, blockIdx.x);
+  else few_dw<T, F32OUT>(f, lds, blockIdx.x - dx_blocks);
+}
+
+// dx: the splits' sums, 64 lanes of four columns, four waves sharing the splits.
+template <typename T>
+__global__ __launch_bounds__(kThreads4) void k_few_dx(
+    const float* __restrict__ acc, int32_t split, int32_t hidden_pad, int32_t hidden,
+    const int32_t* __restrict__ index, const HeadState* __restrict__ state,
+    uint16_t* __restrict__ dx, int64_t lddx) {
+  __shared__ f32x4 s_sum[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t r = blockIdx.y, h = (blockIdx.x * 64 + lane) * 4;
+  if (r >= state->valid) return;
+  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (h < hidden) {
+    const float* p = acc + (int64_t)r * hidden_pad + h;
+#pragma unroll 8
+    for (int32_t k = wave; k < split; k += 4) s += *(const f32x4*)(p + (int64_t)k * kT * hidden_pad);
+  }
+  s_sum[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || h >= hidden) return;
+  s = (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
+  const float c = state->coef / g_scale<T>();
+  uint16_t* o = dx + (int64_t)index[r] * lddx + h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (h + e < hidden) o[e] = (uint16_t)narrow<T>(s[e] * c);
+}
+
+template <typename T>
+int logits_t(const zero_head_t* h, const HeadPlan& p, void* ws, bool keep, hipStream_t stream) {
+  hipLaunchKernelGGL(k_few_logits<T>, dim3((uint32_t)((h->vocab + kHeadPart - 1) / kHeadPart)),
+                     dim3(kThreads4), 0, stream, (const uint16_t*)h->w, h->ldw, (int32_t)h->vocab,
+                     (int32_t)h->hidden, at<const uint16_t>(ws, p.x), (int32_t)p.hidden_pad,
+                     at<const int32_t>(ws, p.label), at<HeadState>(ws, p.state),
+                     at<float2>(ws, p.part), at<float>(ws, p.picked),
+                     keep ? at<float>(ws, p.logits) : nullptr);
+  return (int)hipGetLastError();
+}
+
+template <typename T>
+int grads_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_grads_t* gr,
+            bool have, hipStream_t stream) {
+  if (!have && h->tokens > 0) {
+    const int e = logits_t<T>(h, p, ws, true, stream);
+    if (e) return e;
+  }
+  FewGrad f{};
+  f.logits = at<const float>(ws, p.logits);
+  f.w = (const uint16_t*)h->w;
+  f.ldw = h->ldw;
+  f.xt = at<const uint16_t>(ws, p.xt);
+  f.label = at<const int32_t>(ws, p.label);
+  f.lse = at<const float>(ws, p.lse);
+  f.loss = have ? at<const float>(ws, p.loss) : nullptr;
+  f.picked = at<const float>(ws, p.picked);
+  f.state = at<const HeadState>(ws, p.state);
+  f.acc = at<float>(ws, p.acc);
+  f.dw = gr->dw;
+  f.lddw = gr->lddw;
+  f.vocab = (int32_t)h->vocab;
+  f.hidden = (int32_t)h->hidden;
+  f.hidden_pad = (int32_t)p.hidden_pad;
+  f.accumulate = gr->accumulate;
+  const int32_t vblocks = (f.vocab + 63) / 64, htiles = (f.hidden + 255) / 256;
+  // dw: all columns by one workgroup (g is formed once) unless that leaves CUs idle
+  int32_t parts = (1024 + vblocks - 1) / vblocks;
+  if (parts > htiles) parts = htiles;
+  f.dw_cols = (htiles + parts - 1) / parts * 256;
+  f.dw_blocks = vblocks * ((f.hidden + f.dw_cols - 1) / f.dw_cols);
+  f.split = p.split;
+  f.run = (int32_t)(((h->vocab + p.split - 1) / p.split + kStage - 1) / kStage * kStage);
+  const int32_t dx_blocks = h->tokens > 0 ? htiles * f.split : 0;
+  if (gr->dw_dtype == ZERO_F32)
+    hipLaunchKernelGGL((k_few_grads<T, true>), dim3((uint32_t)(dx_blocks + f.dw_blocks)),
+                       dim3(kThreads4), 0, stream, f, dx_blocks);
+  else
+    hipLaunchKernelGGL((k_few_grads<T, false>), dim3((uint32_t)(dx_blocks + f.dw_blocks)),
+                       dim3(kThreads4), 0, stream, f, dx_blocks);
+  ZK_LAUNCHED();
+  if (h->tokens > 0)
+    hipLaunchKernelGGL(k_few_dx<T>, dim3((uint32_t)htiles, (uint32_t)h->tokens), dim3(kThreads4), 0,
+                       stream, f.acc, f.split, f.hidden_pad, f.hidden,
+                       at<const int32_t>(ws, p.index), f.state, (uint16_t*)gr->dx, gr->lddx);
+  return (int)hipGetLastError();
+}
+
+}  // namespace
+
+int launch_few_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse_in,
+                    float* token_loss, float* lse, const zero_head_grads_t* gr,
+                    hipStream_t stream) {
+  hipLaunchKernelGGL(k_few_pack, dim3(kT), dim3(kThreads4), 0, stream, h->labels,
+                     (int32_t)h->tokens, (int32_t)h->vocab, h->loss_scale, h->mean, lse_in,
+                     (const uint16_t*)h->x, h->ldx, (int32_t)h->hidden, (int32_t)p.hidden_pad,
+                     at<int32_t>(ws, p.index), at<int32_t>(ws, p.label), at<float>(ws, p.lse),
+                     at<HeadState>(ws, p.state), at<uint16_t>(ws, p.x),
+                     gr ? at<uint16_t>(ws, p.xt) : nullptr, token_loss, lse,
+                     gr ? (uint16_t*)gr->dx : nullptr, gr ? gr->lddx : 0);
+  return (int)hipGetLastError();
+}
+
+int launch_few_logits(const zero_head_t* h, const HeadPlan& p, void* ws, bool keep,
+                      hipStream_t stream) {
+  return h->dtype == ZERO_BF16 ? logits_t<BF16>(h, p, ws, keep, stream)
+                               : logits_t<FP16>(h, p, ws, keep, stream);
+}
+
+int launch_few_grads(const zero_head_t* h, const HeadPlan& p, void* ws,
+                     const zero_head_grads_t* gr, bool have, hipStream_t stream) {
+  return h->dtype == ZERO_BF16 ? grads_t<BF16>(h, p, ws, gr, have, stream)
+                               : grads_t<FP16>(h, p, ws, gr, have, stream);
+}
+
+}  // namespace zk
