@@ -99,15 +99,15 @@ __global__ __launch_bounds__(kThreads4) void k_few_pack(
 }
 
 // Logits of 128 vocabulary rows, 32 a wave: A = w from memory straight into
-// fragments, two steps of 64 hidden columns (8 KiB a wave) on their way; B =
-// packed x through LDS, 128 columns at a time, since all four waves read it.
-// Three waves a SIMD with two steps ahead read w of 128256 x 4096 at 5.9 TB/s
-// (179 us) and of 50257 x 1600, which the last-level cache holds, in 33 us; two
-// waves with three steps 217 and 40 us, three with three (spilled) 315 and 65;
-// non-temporal loads lose 3 and 12 us.
-constexpr int kAhead = 2, kXTile = 128;
+// fragments, 128 hidden columns (8 KiB a wave) on their way while the last ones
+// are multiplied; B = packed x through LDS, since all four waves read it.
+// Workgroups start at different columns: rows of 4096 columns lie a power of
+// two apart, and all workgroups at the same column would ask the same memory
+// channels (128256 x 4096: 183 us, 5.7 TB/s, against 237 us).  Two waves a SIMD:
+// three were slower (205 us), as were more columns ahead.
+constexpr int kXTile = 128;
 template <typename T>
-__global__ __launch_bounds__(kThreads4) __attribute__((amdgpu_waves_per_eu(3, 3))) void
+__global__ __launch_bounds__(kThreads4) __attribute__((amdgpu_waves_per_eu(2, 2))) void
 k_few_logits(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, int32_t hidden,
     const uint16_t* __restrict__ x, int32_t hidden_pad, const int32_t* __restrict__ label,
@@ -118,32 +118,59 @@ k_few_logits(
   __shared__ __attribute__((aligned(1024))) char lx[2][kT * kXTile * 2];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, q = lane & 15;
   const int64_t v0 = (int64_t)blockIdx.x * kHeadPart + wave * 32;
-  const uint16_t* wr[2];
+  // A load covers 8 rows' whole 128-byte lines: lanes of q < 8 take the first
+  // half of row q % 8's, the others the second.  The fragments want lane q to
+  // hold row q: two loads of 8 rows each trade halves (lines() below).
+  const uint16_t* wr[2][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t v = v0 + 16 * i + q;
-    wr[i] = w + (v < vocab ? v : vocab - 1) * ldw;  // rows past the end are masked below
-  }
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int64_t v = v0 + 16 * i + 8 * r + (q & 7);
+      wr[i][r] = w + (v < vocab ? v : vocab - 1) * ldw;  // rows past the end are masked below
+    }
+  const int32_t wk = 8 * (4 * (q >> 3) + g);
   f32x4 acc[2][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
-  s16x8 a[kAhead + 1][2][2], xr[4];
-  auto fetch_w = [&](s16x8 (&d)[2][2], int32_t step) {
-    const int32_t k0 = step * kStage;
-    if (k0 + kStage <= hidden) {
+  // a[buffer][i][line][rows 0-7 or 8-15]
+  s16x8 a[2][2][2][2], xr[4];
+  auto fetch_w = [&](s16x8 (&d)[2][2][2], int32_t tile) {
+    const int32_t k0 = tile * kXTile + wk;
+    if ((tile + 1) * kXTile <= hidden) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          d[s][i] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(wr[i] + k0 + 32 * s + 8 * g));
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int l = 0; l < 2; ++l)
+            d[i][l][r] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(wr[i][r] + k0 + 64 * l));
     } else {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) d[s][i] = row8(wr[i], k0 + 32 * s + 8 * g, hidden);
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int l = 0; l < 2; ++l) d[i][l][r] = row8(wr[i][r], k0 + 64 * l, hidden);
     }
+  };
+  // the fragments of a line's two halves: lane q < 8 holds row q of its own
+  // first load and gets row q's second half from lane q + 8, and so on
+  auto lines = [&](const s16x8 (&d)[2], s16x8 (&f)[2]) {
+    const u32x4 lo = __builtin_bit_cast(u32x4, d[0]), hi = __builtin_bit_cast(u32x4, d[1]);
+    const bool first = q < 8;
+    u32x4 x, y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t give = first ? hi[e] : lo[e];
+      const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, false);
+      x[e] = first ? lo[e] : got;
+      y[e] = first ? got : hi[e];
+    }
+    f[0] = __builtin_bit_cast(s16x8, x);
+    f[1] = __builtin_bit_cast(s16x8, y);
   };
   // thread: chunk threadIdx % 16 of rows threadIdx / 16 + 16 k
   const int xc = threadIdx.x & 15, xrow = threadIdx.x >> 4;
@@ -159,35 +186,42 @@ k_few_logits(
     for (int k = 0; k < 4; ++k)
       *(s16x8*)(d + (xrow + 16 * k) * 256 + ((xc ^ xrow) << 4)) = xr[k];
   };
-  auto use = [&](const s16x8 (&d)[2][2], const char* l, int half) {
+  auto use = [&](const s16x8 (&d)[2][2][2], const char* l) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int n = 0; n < 2; ++n) {
+      s16x8 f[2][2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const s16x8 b = *(const s16x8*)(l + (16 * j + q) * 256 + (((8 * half + 4 * s + g) ^ q) << 4));
+      for (int i = 0; i < 2; ++i) lines(d[i][n], f[i]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) acc[i][j] = mfma(T{}, d[s][i], b, acc[i][j]);
-      }
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const s16x8 b = *(const s16x8*)(l + (16 * j + q) * 256 + (((8 * n + 4 * s + g) ^ q) << 4));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) acc[i][j] = mfma(T{}, f[i][s], b, acc[i][j]);
+        }
+    }
   };
   const int32_t tiles = (hidden_pad + 2 * kXTile - 1) / (2 * kXTile) * 2;  // whole pairs; zeros past the end
-  fetch_x(0);
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k) fetch_w(a[k], k);
+  const int32_t from = (int32_t)(blockIdx.x / kXcds) % tiles;  // the XCD's workgroups in turn
+  auto tile = [&](int32_t t) {  // t <= tiles + 1
+    t += from;
+    if (t >= tiles) t -= tiles;
+    return t >= tiles ? t - tiles : t;
+  };
+  fetch_x(tile(0));
+  fetch_w(a[0], tile(0));
   store_x(lx[0]);
-  fetch_x(1);
+  fetch_x(tile(1));
   for (int32_t t = 0; t < tiles; t += 2) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       // tile t + h is in LDS, and the buffer of the one before is free
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      fetch_w(a[1 - h], tile(t + h + 1));
       store_x(lx[1 - h]);
-      fetch_x(t + h + 2);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int now = 2 * h + k;  // step 2t + now
-        fetch_w(a[(now + kAhead) & 3], 2 * t + now + kAhead);
-        use(a[now], lx[h], k);
-      }
+      fetch_x(tile(t + h + 2));
+      use(a[h], lx[h]);
     }
   }
   const int32_t rows = (int32_t)(vocab - v0 < 32 ? vocab - v0 : 32);
