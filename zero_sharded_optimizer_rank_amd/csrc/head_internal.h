@@ -24,7 +24,7 @@ struct HeadPlan {
   bool few;            // at most kFewTokens tokens (see zero_head_few.hip)
   bool pack_w;         // w's rows do not start on 16-byte boundaries
   // offsets
-  size_t state, sums, index, label, lse, loss, x, xt, w, part, picked, g, logits,
+  size_t state, sums, index, label, lse, dy, x, xt, w, part, picked, g, logits,
       acc, total;
 };
 constexpr int64_t kHeadPart = 128;

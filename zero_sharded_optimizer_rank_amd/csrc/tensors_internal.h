@@ -20,6 +20,7 @@ constexpr int64_t kTensorPartials = 16384;
 struct TensorLayout {
   int32_t shift;       // s above
   int64_t chunks;      // over all tensors; an empty tensor has one
+  int64_t longest;     // most chunks of one tensor
 };
 TensorLayout tensor_layout(const zero_tensor_t* tensors, int32_t n);
 size_t tensors_workspace_bytes(const zero_tensor_t* tensors, int32_t n);

@@ -123,11 +123,11 @@ HeadPlan head_plan(const zero_head_t* h, bool grad) {
     return o;
   };
   p.state = take(sizeof(HeadState));
-  p.sums = take(8 * (p.tokens_pad / 64));
+  p.sums = take(8 * (p.tokens_pad / 16));
   p.index = take(4 * p.tokens_pad);
   p.label = take(4 * p.tokens_pad);
   p.lse = take(4 * p.tokens_pad);
-  p.loss = take(4 * p.tokens_pad);
+  p.dy = take(4 * p.tokens_pad);
   p.picked = take(4 * p.tokens_pad);
   p.x = take(2 * p.tokens_pad * p.hidden_pad);
   p.xt = take(grad && p.few ? 2 * p.tokens_pad * p.hidden_pad : 0);

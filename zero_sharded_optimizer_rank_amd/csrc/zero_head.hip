@@ -27,7 +27,7 @@ using namespace dev;
 constexpr int kScanThreads = 1024;
 constexpr int kPackThreads = 256;
 constexpr int kGemmThreads = 512;
-constexpr int kJoinTokens = 64, kJoinWaves = 16, kJoinBatch = 8;
+constexpr int kJoinTokens = 16, kJoinWaves = 16, kJoinBatch = 8;
 
 // --- 1. scan and pack --------------------------------------------------------
 // One workgroup: the valid tokens in order.  index[r] is packed row r's token;
@@ -225,37 +225,51 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
 }
 
 // --- 3. join -------------------------------------------------------------------
-// Workgroup b joins the partials of 64 packed rows, kJoinWaves waves sharing
-// the vocabulary; the last workgroup to finish sums the losses.
+// Workgroup b joins the partials of 16 packed rows (a line of partials), 64
+// strips of the vocabulary side by side; the last workgroup to finish sums the
+// losses.
 __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
     const float2* __restrict__ part, int32_t parts, int32_t tokens_pad,
     const float* __restrict__ picked, const int32_t* __restrict__ index, float* __restrict__ lse,
-    float* __restrict__ loss_c, float* __restrict__ token_loss, float* __restrict__ lse_out, double* __restrict__ sums,
-    double scale, int32_t mean, HeadState* __restrict__ state, zero_loss_result_t* __restrict__ res) {
-  __shared__ float s_m[kJoinWaves][64], s_s[kJoinWaves][64];
+    float* __restrict__ dy, float* __restrict__ token_loss, float* __restrict__ lse_out,
+    double* __restrict__ sums, double scale, int32_t mean, HeadState* __restrict__ state,
+    zero_loss_result_t* __restrict__ res) {
+  constexpr int kStrips = 4 * kJoinWaves;
+  __shared__ float s_m[kJoinWaves][kJoinTokens], s_s[kJoinWaves][kJoinTokens];
   __shared__ uint32_t s_last;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t valid = state->valid;
-  const int32_t r = blockIdx.x * kJoinTokens + lane;
+  const int32_t r = blockIdx.x * kJoinTokens + (lane & 15);
   double loss = 0.0;
+  float m = -INFINITY, s = 0.0f;
   if (r < valid) {
-    float m = -INFINITY, s = 0.0f;
-    for (int32_t p = wave; p < parts; p += kJoinWaves * kJoinBatch) {
+    for (int32_t p = threadIdx.x >> 4; p < parts; p += kStrips * kJoinBatch) {
       float2 q[kJoinBatch];
 #pragma unroll
       for (int k = 0; k < kJoinBatch; ++k) {
         q[k] = float2{-INFINITY, 0.0f};
-        if (p + k * kJoinWaves < parts) q[k] = part[(int64_t)(p + k * kJoinWaves) * tokens_pad + r];
+        if (p + k * kStrips < parts) q[k] = part[(int64_t)(p + k * kStrips) * tokens_pad + r];
       }
 #pragma unroll
       for (int k = 0; k < kJoinBatch; ++k) join(m, s, q[k].x, q[k].y);
     }
+  }
+#pragma unroll
+  for (int off = 16; off < 64; off <<= 1) {
+    const float m2 = __shfl_xor(m, off), s2 = __shfl_xor(s, off);
+    // both sides join in the same order, so that all lanes agree
+    const bool low = !(lane & off);
+    float a = low ? m : m2, b = low ? s : s2;
+    join(a, b, low ? m2 : m, low ? s2 : s);
+    m = a;
+    s = b;
+  }
+  if (lane < kJoinTokens) {
     s_m[wave][lane] = m;
     s_s[wave][lane] = s;
   }
   __syncthreads();
-  if (wave == 0 && r < valid) {
-    float m = s_m[0][lane], s = s_s[0][lane];
+  if (wave == 0 && lane < kJoinTokens && r < valid) {
     for (int k = 1; k < kJoinWaves; ++k) join(m, s, s_m[k][lane], s_s[k][lane]);
     // with o the others' sum over the label's exponential: log(1 + o)
     const double y = picked[r], gap = (double)m / (double)kLog2e - y, sum = (double)s * scale;
@@ -265,11 +279,11 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
     lse[r] = l;
     if (lse_out) lse_out[index[r]] = l;
     if (token_loss) token_loss[index[r]] = (float)d;
-    loss_c[r] = (float)d;
+    dy[r] = (float)expm1(-d);
     loss = (float)d;
   }
   if (wave == 0) {
-    for (int off = 32; off > 0; off >>= 1) loss += __shfl_xor(loss, off);
+    for (int off = 8; off > 0; off >>= 1) loss += __shfl_xor(loss, off);
     if (lane == 0) {
       sums[blockIdx.x] = loss;
       __threadfence();
@@ -363,7 +377,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_head_rescale(
     uint16_t* __restrict__ g, int32_t piece, int32_t left, const float2* __restrict__ part,
     int32_t part0, int32_t tokens_pad, const int32_t* __restrict__ label, int64_t piece0,
-    const float* __restrict__ lse, const float* __restrict__ loss,
+    const float* __restrict__ lse, const float* __restrict__ dy,
     const HeadState* __restrict__ state) {
   const int32_t valid = state->valid;
   const int32_t t = blockIdx.y * 8 + (threadIdx.x >> 5);
@@ -384,7 +398,7 @@ __global__ __launch_bounds__(256) void k_head_rescale(
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float p = widen<T>((v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) * f;
-        if (c + e == y) p = expm1f(-loss[t]) * g_scale<T>();
+        if (c + e == y) p = dy[t] * g_scale<T>();
         if (c + e >= left) p = 0.0f;
         const uint32_t b = narrow<T>(p);
         v[e >> 1] = e & 1 ? (v[e >> 1] & 0xFFFFu) | b << 16 : (v[e >> 1] & 0xFFFF0000u) | b;
@@ -571,7 +585,7 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
                      dim3(64 * kJoinWaves), 0, stream, at<const float2>(ws, p.part),
                      (int32_t)((h->vocab + tile - 1) / tile * tile / kHeadPart), (int32_t)p.tokens_pad,
                      at<const float>(ws, p.picked), at<const int32_t>(ws, p.index),
-                     at<float>(ws, p.lse), at<float>(ws, p.loss), token_loss, lse,
+                     at<float>(ws, p.lse), at<float>(ws, p.dy), token_loss, lse,
                      at<double>(ws, p.sums), 1.0 / (double)g_scale<T>(), h->mean, state, res);
   return (int)hipGetLastError();
 }
@@ -597,7 +611,7 @@ int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
                               (uint32_t)(p.tokens_pad / 8)),
                          dim3(256), 0, stream, g, (int32_t)p.piece, (int32_t)left,
                          at<const float2>(ws, p.part), (int32_t)(v0 / kHeadPart),
-                         (int32_t)p.tokens_pad, label, v0, lse, at<const float>(ws, p.loss), state);
+                         (int32_t)p.tokens_pad, label, v0, lse, at<const float>(ws, p.dy), state);
     else
       hipLaunchKernelGGL(k_head_g<T>, dim3(tile_grid(ttiles, vtiles)), dim3(kGemmThreads), 0,
                          stream, w.w, w.ld, (int32_t)h->vocab, x, (int32_t)p.hidden_pad, w.K,

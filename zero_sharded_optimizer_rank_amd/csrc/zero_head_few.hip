@@ -36,7 +36,7 @@ __device__ __forceinline__ s16x8 row8(const uint16_t* row, int32_t k, int32_t n)
   u32x4 v = {0, 0, 0, 0};
   if (k + 8 <= n) {
     v = *(const u32x4_a2*)(row + k);
-  } else {
+  } else if (k < n) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (k + e < n) v[e >> 1] |= (uint32_t)row[k + e] << (16 * (e & 1));
@@ -271,29 +271,18 @@ k_few_logits(
   }
 }
 
-// A token's side of g: its lse in base 2 less g's scale, its label, and the
-// label's element e^-loss - 1 (with the loss of the same call, which keeps the
-// digits of a small one, or from lse).
-struct Token {
-  float shift, dy;
-  int32_t y;
+// The tokens' side of g, in LDS: g's scale less the lse, in base 2 (-inf: no
+// token), the label's row, and its element e^-loss - 1 (from the loss of the
+// same call, which keeps a small one's digits, or from lse).
+struct Tokens {
+  float shift[kT], dy[kT];
+  int32_t y[kT];
 };
 template <typename T>
-__device__ __forceinline__ Token token_of(int32_t t, int32_t valid, const int32_t* label,
-                                          const float* lse, const float* loss,
-                                          const float* picked) {
-  Token k{-INFINITY, 0.0f, -1};
-  if (t < valid) {
-    k.shift = g_log2<T>() - lse[t] * kLog2e;
-    k.dy = expm1f(loss ? -loss[t] : picked[t] - lse[t]) * g_scale<T>();
-    k.y = label[t];
-  }
-  return k;
-}
-template <typename T>
-__device__ __forceinline__ float g_of(float l, int32_t v, int32_t vocab, const Token& k) {
-  if (k.shift == -INFINITY || v >= vocab) return 0.0f;  // no token, no row
-  return v == k.y ? k.dy : exp2_fast(__builtin_fmaf(l, kLog2e, k.shift));
+__device__ __forceinline__ float g_of(float l, int32_t v, int32_t vocab, float shift, float dy,
+                                      int32_t y) {
+  if (shift == -INFINITY || v >= vocab) return 0.0f;  // no token, no row
+  return v == y ? dy : exp2_fast(__builtin_fmaf(l, kLog2e, shift));
 }
 
 // Eight values into their two 16-bit parts.
@@ -312,7 +301,7 @@ struct FewGrad {
   int64_t ldw;
   const uint16_t* xt;
   const int32_t* label;
-  const float *lse, *loss, *picked;
+  const float *lse, *dy, *picked;  // dy: e^-loss - 1, or NULL
   const HeadState* state;
   float* acc;       // dx's partial sums [split][64][hidden_pad]
   void* dw;
@@ -323,16 +312,28 @@ struct FewGrad {
   int32_t accumulate;
 };
 
+template <typename T>
+__device__ __forceinline__ void load_tokens(const FewGrad& f, Tokens& k) {
+  const int t = threadIdx.x;
+  if (t < kT) {
+    const bool there = t < f.state->valid;
+    const float z = there ? f.lse[t] : 0.0f;
+    k.shift[t] = there ? g_log2<T>() - z * kLog2e : -INFINITY;
+    k.dy[t] = there ? (f.dy ? f.dy[t] : expm1f(f.picked[t] - z)) * g_scale<T>() : 0.0f;
+    k.y[t] = there ? f.label[t] : -1;
+  }
+  __syncthreads();
+}
+
 // dw of 64 vocabulary rows and dw_cols hidden columns: A = x^T (rows: hidden),
 // B = g (rows: vocabulary), contraction over the 64 tokens.  A wave takes 64
 // columns at a time; its g stays in registers.
 template <typename T, bool F32OUT>
-__device__ __forceinline__ void few_dw(const FewGrad& f, char* lds, int32_t block) {
+__device__ __forceinline__ void few_dw(const FewGrad& f, const Tokens& tok, char* lds, int32_t block) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, q = lane & 15;
   const int32_t vblocks = (f.vocab + 63) / 64;
   const int32_t v0 = block % vblocks * 64, h1 = (block / vblocks + 1) * f.dw_cols;
   const float c = f.state->coef / g_scale<T>();
-  const int32_t valid = f.state->valid;
   s16x8 hi[2][4], lo[2][4];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -350,9 +351,12 @@ __device__ __forceinline__ void few_dw(const FewGrad& f, char* lds, int32_t bloc
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const Token k = token_of<T>(32 * s + 8 * g + e, valid, f.label, f.lse, f.loss, f.picked);
+      const int t = 32 * s + 8 * g + e;
+      const float shift = tok.shift[t], dy = tok.dy[t];
+      const int32_t y = tok.y[t];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j][e] = g_of<T>(v[j][e], v0 + 16 * j + q, f.vocab, k);
+      for (int j = 0; j < 4; ++j)
+        v[j][e] = g_of<T>(v[j][e], v0 + 16 * j + q, f.vocab, shift, dy, y);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) two_parts<T>(v[j], hi[s][j], lo[s][j]);
@@ -432,14 +436,15 @@ __device__ __forceinline__ void few_dw(const FewGrad& f, char* lds, int32_t bloc
 // workgroup forms in LDS from the logits.  The next rows of w and of the
 // logits are on their way while these are multiplied.
 template <typename T>
-__device__ __forceinline__ void few_dx(const FewGrad& f, char* lds, int32_t block) {
+__device__ __forceinline__ void few_dx(const FewGrad& f, const Tokens& tok, char* lds, int32_t block) {
   using FA = Frags<256, true>;
   using FB = Frags<64, false>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t htiles = (f.hidden + 255) / 256;
   const int32_t h0 = block % htiles * 256, ks = block / htiles;
   const int32_t va = ks * f.run, vb = va + f.run < f.vocab ? va + f.run : f.vocab;
-  const Token tok = token_of<T>(lane, f.state->valid, f.label, f.lse, f.loss, f.picked);
+  const float shift = tok.shift[lane], dy = tok.dy[lane];
+  const int32_t y = tok.y[lane];
   lds_char* lw = (lds_char*)lds;             // w: [64 rows][256 columns], pairs swizzled
   lds_char* lg = (lds_char*)(lds + 32768);   // g: two parts of [64 tokens][64 rows]
   const FA fa(wave * 64, lane);
@@ -485,7 +490,7 @@ __device__ __forceinline__ void few_dx(const FewGrad& f, char* lds, int32_t bloc
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        v[e] = g_of<T>(nl[8 * p + e], v0 + wave * 16 + 8 * p + e, vb, tok);
+        v[e] = g_of<T>(nl[8 * p + e], v0 + wave * 16 + 8 * p + e, vb, shift, dy, y);
       s16x8 hi, lo;
       two_parts<T>(v, hi, lo);
       lds_char* o = lg + lane * 128 + (((2 * wave + p) ^ (lane >> 1 & 7)) << 4);
@@ -524,8 +529,10 @@ __device__ __forceinline__ void few_dx(const FewGrad& f, char* lds, int32_t bloc
 template <typename T, bool F32OUT>
 __global__ __launch_bounds__(kThreads4) void k_few_grads(FewGrad f, int32_t dx_blocks) {
   __shared__ __attribute__((aligned(1024))) char lds[49152];
-  if ((int32_t)blockIdx.x < dx_blocks) few_dx<T>(f, lds, blockIdx.x);
-  else few_dw<T, F32OUT>(f, lds, blockIdx.x - dx_blocks);
+  __shared__ Tokens tok;
+  load_tokens<T>(f, tok);
+  if ((int32_t)blockIdx.x < dx_blocks) few_dx<T>(f, tok, lds, blockIdx.x);
+  else few_dw<T, F32OUT>(f, tok, lds, blockIdx.x - dx_blocks);
 }
 
 // dx: the splits' sums, 64 lanes of four columns, four waves sharing the splits.
@@ -580,7 +587,7 @@ int grads_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
   f.xt = at<const uint16_t>(ws, p.xt);
   f.label = at<const int32_t>(ws, p.label);
   f.lse = at<const float>(ws, p.lse);
-  f.loss = have ? at<const float>(ws, p.loss) : nullptr;
+  f.dy = have ? at<const float>(ws, p.dy) : nullptr;
   f.picked = at<const float>(ws, p.picked);
   f.state = at<const HeadState>(ws, p.state);
   f.acc = at<float>(ws, p.acc);

@@ -90,11 +90,14 @@ TensorLayout tensor_layout(const zero_tensor_t* t, int32_t n) {
   int64_t total = 0;
   for (int32_t i = 0; i < n; ++i)
     total = t[i].numel > INT64_MAX - total ? INT64_MAX : total + t[i].numel;
-  TensorLayout l{0, 0};
+  TensorLayout l{0, 0, 0};
   while ((total >> l.shift) > kTensorChunk * kTensorPartials) ++l.shift;
   const int64_t chunk = kTensorChunk << l.shift;
-  for (int32_t i = 0; i < n; ++i)
-    l.chunks += t[i].numel ? (t[i].numel - 1) / chunk + 1 : 1;
+  for (int32_t i = 0; i < n; ++i) {
+    const int64_t c = t[i].numel ? (t[i].numel - 1) / chunk + 1 : 1;
+    l.chunks += c;
+    if (c > l.longest) l.longest = c;
+  }
   return l;
 }
 

@@ -165,20 +165,24 @@ __global__ __launch_bounds__(kNormThreads) void k_tensors_norm(
                                    (uint64_t)(bad ? 1u : 0u) << 63};
 }
 
-// Thread t's share of values t, t + T, ... of get(0..count).
+// Values first, first + step, ... of get(0..count).
 template <typename Get>
-__device__ __forceinline__ void strided_sum(int64_t count, double& x, uint32_t& bad, Get get) {
+__device__ __forceinline__ void strided_sum(int64_t first, int64_t step, int64_t count, double& x,
+                                            uint32_t& bad, Get get) {
   x = 0.0;
   bad = 0;
-  for (int64_t j = threadIdx.x; j < count; j += kNormThreads) {
+  for (int64_t j = first; j < count; j += step) {
     const Partial pt = get(j);
     x += __longlong_as_double((long long)pt.lo);
     bad |= (uint32_t)(pt.hi >> 63);
   }
 }
 
-// Workgroup i sums tensor i's partials; the last one to finish (ticket) sums
-// the tensors and finalizes.
+// Each G threads sum one tensor's partials (G = 1, a wave or the workgroup: the
+// launcher picks by the longest tensor, so that short tensors do not take a
+// workgroup each); the last workgroup to finish (ticket) sums the tensors and
+// finalizes.
+template <int G>
 __global__ __launch_bounds__(kNormThreads) void k_tensors_finalize(
     const Partial* __restrict__ partials, const TensorRecord* __restrict__ records,
     Partial* __restrict__ sums, int32_t n, double* __restrict__ tensor_sq,
@@ -186,27 +190,34 @@ __global__ __launch_bounds__(kNormThreads) void k_tensors_finalize(
   __shared__ uint32_t s_last;
   double x = 0.0;
   uint32_t bad = 0;
-  if (n > 0) {
-    const TensorRecord r = records[blockIdx.x];
-    strided_sum(r.chunks, x, bad, [&](int64_t j) { return partials[r.first + j]; });
-    block_tree<kNormThreads>(x, bad);
-    if (threadIdx.x == 0) {
-      if (tensor_sq) tensor_sq[blockIdx.x] = (x * fa.inv64) * fa.inv64;
-      s_last = 1u;
-      if (n > 1) {
-        sums[blockIdx.x] = Partial{(uint64_t)__double_as_longlong(x),
-                                   (uint64_t)(bad ? 1u : 0u) << 63};
-        __threadfence();
-        s_last = atomicAdd(ticket, 1u) == (uint32_t)n - 1 ? 1u : 0u;
-      }
+  const int32_t i = (int32_t)(blockIdx.x * (kNormThreads / G) + threadIdx.x / G);
+  if (i < n) {
+    const TensorRecord r = records[i];
+    strided_sum(threadIdx.x % G, G, r.chunks, x, bad, [&](int64_t j) { return partials[r.first + j]; });
+  }
+  if constexpr (G == 64) {
+    for (unsigned int d = 1; d < 64; d <<= 1) {
+      x += __longlong_as_double((long long)shfl_down_bits((uint64_t)__double_as_longlong(x), d));
+      bad |= (uint32_t)__shfl_xor((int)bad, (int)d);
     }
+  } else if constexpr (G == kNormThreads) {
+    block_tree<kNormThreads>(x, bad);
+  }
+  if (i < n && threadIdx.x % G == 0) {
+    if (tensor_sq) tensor_sq[i] = (x * fa.inv64) * fa.inv64;
+    if (n > 1)
+      sums[i] = Partial{(uint64_t)__double_as_longlong(x), (uint64_t)(bad ? 1u : 0u) << 63};
+  }
+  if (n > 1) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0)
+      s_last = gridDim.x == 1 || atomicAdd(ticket, 1u) == gridDim.x - 1 ? 1u : 0u;
     __syncthreads();
     if (!s_last) return;
-    if (n > 1) {
-      __threadfence();
-      strided_sum(n, x, bad, [&](int64_t j) { return sums[j]; });
-      block_tree<kNormThreads>(x, bad);
-    }
+    __threadfence();
+    strided_sum(threadIdx.x, kNormThreads, n, x, bad, [&](int64_t j) { return sums[j]; });
+    block_tree<kNormThreads>(x, bad);
   }
   if (threadIdx.x == 0) finalize_bf16_into(x, bad, fa, res);
 }
@@ -323,8 +334,16 @@ int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_
     if (e != hipSuccess) return (int)e;
     chunk0 += blocks;
   }
-  hipLaunchKernelGGL(k_tensors_finalize, dim3(n > 0 ? (uint32_t)n : 1u), dim3(kNormThreads), 0,
-                     stream, partials, records, sums, n, tensor_sq, ticket, fa, res);
+  auto finalize = [&](auto kernel, int group) {
+    const int64_t blocks = ((int64_t)n * group + kNormThreads - 1) / kNormThreads;
+    hipLaunchKernelGGL(kernel, dim3(blocks > 0 ? (uint32_t)blocks : 1u), dim3(kNormThreads), 0,
+                       stream, partials, records, sums, n, tensor_sq, ticket, fa, res);
+  };
+  // a thread takes up to 4 partials in turn, a wave 16 a lane; 290 one-chunk
+  // tensors take 5 us by threads, 12 us by workgroups (and their ticket)
+  if (l.longest <= 4) finalize(k_tensors_finalize<1>, 1);
+  else if (l.longest <= 1024) finalize(k_tensors_finalize<64>, 64);
+  else finalize(k_tensors_finalize<kNormThreads>, kNormThreads);
   return (int)hipGetLastError();
 }
 

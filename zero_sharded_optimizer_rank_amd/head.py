@@ -11,6 +11,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import abi
+from .tensors import on_device, stream_of
 
 DTYPES = {torch.float16: abi.ZERO_F16, torch.bfloat16: abi.ZERO_BF16}
 
@@ -45,6 +46,8 @@ class LossHead:
         self.device = torch.device(device)
         if self.device.type != "cuda":
             raise ValueError(f"device {self.device} is not a GPU")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self.tokens, self.hidden, self.vocab, self.dtype = tokens, hidden, vocab, dtype
         self.has_grad = grad
         head = abi.zero_head_t(tokens, hidden, vocab, 0, hidden, 0, hidden, 0, DTYPES[dtype], 1,
@@ -92,26 +95,24 @@ class LossHead:
                                loss_scale)
 
     def _workspace(self, head, grad):
-        # rows of w that do not start on 16-byte boundaries take a copy in the workspace
-        need = abi.zero_head_workspace_bytes(head, grad)
-        if need > self.ws.numel():
-            self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        # rows of w that do not start on 16-byte boundaries may take a copy in the workspace
+        if (head.w | head.ldw * 2 | self.hidden * 2) % 16:
+            need = abi.zero_head_workspace_bytes(head, grad)
+            if need > self.ws.numel():
+                self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         return self.ws
 
     def _result(self, t, **kw):
         return HeadLoss(self._loss, self._loss_sum, self._token_loss[:t], self._lse[:t],
                         self._valid, self._bad, **kw)
 
-    def _stream(self, stream):
-        return torch.cuda.current_stream(self.device) if stream is None else stream
-
     def loss(self, x, w, labels, mean: bool = True, stream=None) -> HeadLoss:
         """The loss alone."""
         head = self._head(x, w, labels, mean, 1.0)
-        with torch.cuda.device(self.device):
+        with on_device(self.device):
             ws = self._workspace(head, False)
             abi.zero_head_loss(head, self._token_loss, self._lse, ws, ws.numel(), self.res,
-                               self._stream(stream))
+                               stream_of(self.device, stream))
         return self._result(head.tokens)
 
     def _grads(self, t, dx, dw, accumulate):
@@ -140,10 +141,10 @@ class LossHead:
         accumulate adds to dw."""
         head = self._head(x, w, labels, mean, loss_scale)
         dx, dw, grads = self._grads(head.tokens, dx, dw, accumulate)
-        with torch.cuda.device(self.device):
+        with on_device(self.device):
             ws = self._workspace(head, True)
             abi.zero_head_loss_grad(head, self._token_loss, self._lse, grads, ws, ws.numel(),
-                                    self.res, self._stream(stream))
+                                    self.res, stream_of(self.device, stream))
         return self._result(head.tokens, dx=dx, dw=dw)
 
     def grad(self, x, w, labels, lse, mean: bool = True, loss_scale: float = 1.0, dx=None,
@@ -156,7 +157,7 @@ class LossHead:
                 or lse.numel() != head.tokens:
             raise ValueError(f"lse must be a contiguous float32 vector of {head.tokens}")
         dx, dw, grads = self._grads(head.tokens, dx, dw, accumulate)
-        with torch.cuda.device(self.device):
+        with on_device(self.device):
             ws = self._workspace(head, True)
-            abi.zero_head_grad(head, lse, grads, ws, ws.numel(), self._stream(stream))
+            abi.zero_head_grad(head, lse, grads, ws, ws.numel(), stream_of(self.device, stream))
         return dx, dw

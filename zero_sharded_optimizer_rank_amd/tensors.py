@@ -6,6 +6,7 @@ list, its workspace and its results; the tensors stay the caller's.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -25,6 +26,19 @@ class GradNorm(NamedTuple):
     own_sq: torch.Tensor      # 0-dim float64: this list's squared norm, unscaled
     total_sq: torch.Tensor    # 0-dim float64: with the other ranks'
     tensor_sq: torch.Tensor   # [n] float64: each tensor's squared norm, unscaled
+
+
+_HERE = contextlib.nullcontext()
+
+
+def on_device(device):
+    """A guard that makes `device` the current one; nothing to do where it is."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def stream_of(device, stream) -> int:
+    """The handle of the given stream, or of the device's current one."""
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
 
 def _check_tensor(t, what: str, device) -> None:
@@ -59,6 +73,8 @@ class GradList:
             device = self.tensors[0].device
         else:
             device = torch.device("cuda", torch.cuda.current_device())
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
         self.device = device
         entries = []
         for i, (t, o) in enumerate(zip(self.tensors, self.out)):
@@ -75,6 +91,8 @@ class GradList:
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self.res = torch.zeros(abi.RESULT_BYTES, dtype=torch.uint8, device=device)
         sq = torch.zeros(self.n, dtype=torch.float64, device=device)
+        # addresses, resolved once
+        self._sq, self._ws, self._res = sq.data_ptr(), self.ws.data_ptr(), self.res.data_ptr()
         d, f, w = (self.res.view(t) for t in (torch.float64, torch.float32, torch.int32))
         self.result = GradNorm(norm=d[4], clip_coef=f[10], overflow=w[11], skip=w[12],
                                own_sq=d[2], total_sq=d[3], tensor_sq=sq)
@@ -85,34 +103,36 @@ class GradList:
                              max_grad_norm=max_grad_norm, loss_scale=loss_scale, step=1,
                              other_sq=other_sq, other_overflow=other_overflow)
 
-    def _stream(self, stream):
-        return torch.cuda.current_stream(self.device) if stream is None else stream
+    def _on(self, stream):
+        return on_device(self.device), stream_of(self.device, stream)
 
     def norm(self, max_grad_norm: float = 0.0, loss_scale: float = 1.0, other_sq: float = 0.0,
              other_overflow: bool = False, stream=None) -> GradNorm:
         """The norm of the tensors divided by loss_scale, the coefficient that clips it to
         max_grad_norm (<= 0: 1) and the skip decision."""
-        with torch.cuda.device(self.device):
+        guard, stream = self._on(stream)
+        with guard:
             abi.zero_tensors_norm(self.table, self.n,
                                   self.args(max_grad_norm, loss_scale, other_sq, other_overflow),
-                                  self.result.tensor_sq, self.ws, self.ws_bytes, self.res,
-                                  self._stream(stream))
+                                  self._sq, self._ws, self.ws_bytes, self._res, stream)
         return self.result
 
     def clip(self, loss_scale: float = 1.0, out_scale: float = 1.0, stream=None) -> None:
         """out = tensor / loss_scale * out_scale * clip_coef of the last norm; nothing is
         written if that norm found inf or NaN."""
-        with torch.cuda.device(self.device):
+        guard, stream = self._on(stream)
+        with guard:
             abi.zero_tensors_clip(self.table, self.n, self.args(0.0, loss_scale), out_scale,
-                                  self.res, self._stream(stream))
+                                  self._res, stream)
 
     def norm_clip(self, max_grad_norm: float, loss_scale: float = 1.0, out_scale: float = 1.0,
                   other_sq: float = 0.0, other_overflow: bool = False, stream=None) -> GradNorm:
         """``norm`` then ``clip``, enqueued together."""
-        with torch.cuda.device(self.device):
+        guard, stream = self._on(stream)
+        with guard:
             abi.zero_tensors_norm_clip(self.table, self.n,
                                        self.args(max_grad_norm, loss_scale, other_sq,
                                                  other_overflow),
-                                       out_scale, self.result.tensor_sq, self.ws, self.ws_bytes,
-                                       self.res, self._stream(stream))
+                                       out_scale, self._sq, self._ws, self.ws_bytes, self._res,
+                                       stream)
         return self.result
