@@ -15,7 +15,7 @@ namespace zk {
 // the list at kTensorPartials chunks (each tensor's last, short one aside): few
 // enough for one workgroup per tensor to sum, many enough to fill the chip.
 constexpr int64_t kTensorChunk = 16384;
-constexpr int64_t kTensorPartials = 16384;
+constexpr int64_t kTensorPartials = 32768;
 
 struct TensorLayout {
   int32_t shift;       // s above

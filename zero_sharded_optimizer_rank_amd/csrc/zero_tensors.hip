@@ -171,6 +171,7 @@ __device__ __forceinline__ void strided_sum(int64_t first, int64_t step, int64_t
                                             uint32_t& bad, Get get) {
   x = 0.0;
   bad = 0;
+#pragma unroll 8
   for (int64_t j = first; j < count; j += step) {
     const Partial pt = get(j);
     x += __longlong_as_double((long long)pt.lo);
@@ -183,14 +184,17 @@ __device__ __forceinline__ void strided_sum(int64_t first, int64_t step, int64_t
 // workgroup each); the last workgroup to finish (ticket) sums the tensors and
 // finalizes.
 template <int G>
-__global__ __launch_bounds__(kNormThreads) void k_tensors_finalize(
+constexpr int kFinalThreads = G > kNormThreads ? G : kNormThreads;
+template <int G>
+__global__ __launch_bounds__(kFinalThreads<G>) void k_tensors_finalize(
     const Partial* __restrict__ partials, const TensorRecord* __restrict__ records,
     Partial* __restrict__ sums, int32_t n, double* __restrict__ tensor_sq,
     uint32_t* __restrict__ ticket, FinalizeArgs fa, zero_step_result_t* __restrict__ res) {
+  constexpr int TB = kFinalThreads<G>;
   __shared__ uint32_t s_last;
   double x = 0.0;
   uint32_t bad = 0;
-  const int32_t i = (int32_t)(blockIdx.x * (kNormThreads / G) + threadIdx.x / G);
+  const int32_t i = (int32_t)(blockIdx.x * (TB / G) + threadIdx.x / G);
   if (i < n) {
     const TensorRecord r = records[i];
     strided_sum(threadIdx.x % G, G, r.chunks, x, bad, [&](int64_t j) { return partials[r.first + j]; });
@@ -200,8 +204,8 @@ __global__ __launch_bounds__(kNormThreads) void k_tensors_finalize(
       x += __longlong_as_double((long long)shfl_down_bits((uint64_t)__double_as_longlong(x), d));
       bad |= (uint32_t)__shfl_xor((int)bad, (int)d);
     }
-  } else if constexpr (G == kNormThreads) {
-    block_tree<kNormThreads>(x, bad);
+  } else if constexpr (G == TB) {
+    block_tree<TB>(x, bad);
   }
   if (i < n && threadIdx.x % G == 0) {
     if (tensor_sq) tensor_sq[i] = (x * fa.inv64) * fa.inv64;
@@ -216,8 +220,8 @@ __global__ __launch_bounds__(kNormThreads) void k_tensors_finalize(
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    strided_sum(threadIdx.x, kNormThreads, n, x, bad, [&](int64_t j) { return sums[j]; });
-    block_tree<kNormThreads>(x, bad);
+    strided_sum(threadIdx.x, TB, n, x, bad, [&](int64_t j) { return sums[j]; });
+    block_tree<TB>(x, bad);
   }
   if (threadIdx.x == 0) finalize_bf16_into(x, bad, fa, res);
 }
@@ -287,10 +291,10 @@ __device__ __forceinline__ void clip_to(int dd, const void* src, void* dst, int6
 }
 
 __global__ __launch_bounds__(kClipThreads) void k_tensors_clip(
-    ClipBatch cb, int32_t n, uint32_t b0, float s, const zero_step_result_t* __restrict__ res) {
+    ClipBatch cb, int32_t n, uint32_t last, float s, const zero_step_result_t* __restrict__ res) {
   if (res->skip) return;
   const float c = res->clip_coef;
-  const uint32_t b = b0 + blockIdx.x;
+  const uint32_t b = last - blockIdx.x;
   const int i = find_tensor(cb.first, n, b);
   const int64_t numel = (int64_t)(cb.numel[i] & ((1ull << kDtypeShift) - 1));
   const int sd = (int)(cb.numel[i] >> kDtypeShift) & 3;
@@ -317,8 +321,12 @@ int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_
   Partial* sums = (Partial*)(records + n);
   Partial* partials = sums + n;
   int64_t chunk0 = 0;
-  for (int32_t t0 = 0; t0 < n; t0 += kNormBatch) {
-    const int32_t m = n - t0 < kNormBatch ? n - t0 : kNormBatch;
+  // as few launches as the table allows, of equally many tensors: a short last
+  // launch would leave CUs idle
+  const int32_t launches = (n + kNormBatch - 1) / kNormBatch;
+  const int32_t batch = launches ? (n + launches - 1) / launches : 1;
+  for (int32_t t0 = 0; t0 < n; t0 += batch) {
+    const int32_t m = n - t0 < batch ? n - t0 : batch;
     NormBatch nb;
     int64_t blocks = 0;
     for (int32_t i = 0; i < m; ++i) {
@@ -334,49 +342,54 @@ int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_
     if (e != hipSuccess) return (int)e;
     chunk0 += blocks;
   }
-  auto finalize = [&](auto kernel, int group) {
-    const int64_t blocks = ((int64_t)n * group + kNormThreads - 1) / kNormThreads;
-    hipLaunchKernelGGL(kernel, dim3(blocks > 0 ? (uint32_t)blocks : 1u), dim3(kNormThreads), 0,
-                       stream, partials, records, sums, n, tensor_sq, ticket, fa, res);
+  auto finalize = [&](auto kernel, int group, int threads) {
+    const int64_t blocks = ((int64_t)n * group + threads - 1) / threads;
+    hipLaunchKernelGGL(kernel, dim3(blocks > 0 ? (uint32_t)blocks : 1u), dim3(threads), 0, stream,
+                       partials, records, sums, n, tensor_sq, ticket, fa, res);
   };
-  // a thread takes up to 4 partials in turn, a wave 16 a lane; 290 one-chunk
+  // a thread takes up to 4 partials in turn, a wave 32 a lane; 290 one-chunk
   // tensors take 5 us by threads, 12 us by workgroups (and their ticket)
-  if (l.longest <= 4) finalize(k_tensors_finalize<1>, 1);
-  else if (l.longest <= 1024) finalize(k_tensors_finalize<64>, 64);
-  else finalize(k_tensors_finalize<kNormThreads>, kNormThreads);
+  if (l.longest <= 4) finalize(k_tensors_finalize<1>, 1, kNormThreads);
+  else if (l.longest <= 2048) finalize(k_tensors_finalize<64>, 64, kNormThreads);
+  else finalize(k_tensors_finalize<1024>, 1024, 1024);
   return (int)hipGetLastError();
 }
 
+// The list is gone through backwards: what the norm has read last may still
+// lie in the last-level cache.
 int launch_tensors_clip(const zero_tensor_t* tensors, int32_t n, float scale,
                         const zero_step_result_t* res, hipStream_t stream) {
-  constexpr int64_t kMaxBlocks = (int64_t)1 << 30;
-  int32_t t0 = 0;
-  while (t0 < n) {
+  constexpr int64_t kMaxBlocks = (int64_t)1 << 30;  // of one launch
+  const int32_t launches = (n + kClipBatch - 1) / kClipBatch;
+  const int32_t batch = launches ? (n + launches - 1) / launches : 1;
+  for (int32_t t1 = n; t1 > 0;) {
     ClipBatch cb;
-    int32_t m = 0;
+    int32_t t0 = t1;
     int64_t blocks = 0;
-    for (; t0 + m < n && m < kClipBatch; ++m) {
-      const zero_tensor_t& t = tensors[t0 + m];
-      const int64_t nb = (t.numel + kClipChunk - 1) / kClipChunk;
-      if (m > 0 && blocks + nb > kMaxBlocks) break;
-      cb.src[m] = t.src;
-      cb.dst[m] = t.dst;
-      cb.numel[m] = (uint64_t)t.numel |
-                    (uint64_t)(t.src_dtype | t.dst_dtype << 2) << kDtypeShift;
-      cb.first[m] = (uint32_t)blocks;
+    while (t0 > 0 && t1 - t0 < batch) {
+      const int64_t nb = (tensors[t0 - 1].numel + kClipChunk - 1) / kClipChunk;
+      if (nb > UINT32_MAX - kMaxBlocks) return (int)hipErrorInvalidValue;
+      if (t0 < t1 && blocks + nb > kMaxBlocks) break;
+      --t0;
       blocks += nb;
     }
-    if (blocks > 0) {
-      if (blocks > UINT32_MAX - kMaxBlocks) return (int)hipErrorInvalidValue;
-      for (int64_t b0 = 0; b0 < blocks; b0 += kMaxBlocks) {
-        const int64_t nb = blocks - b0 < kMaxBlocks ? blocks - b0 : kMaxBlocks;
-        hipLaunchKernelGGL(k_tensors_clip, dim3((uint32_t)nb), dim3(kClipThreads), 0, stream, cb,
-                           m, (uint32_t)b0, scale, res);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return (int)e;
-      }
+    uint32_t first = 0;
+    for (int32_t m = 0; m < t1 - t0; ++m) {
+      const zero_tensor_t& t = tensors[t0 + m];
+      cb.src[m] = t.src;
+      cb.dst[m] = t.dst;
+      cb.numel[m] = (uint64_t)t.numel | (uint64_t)(t.src_dtype | t.dst_dtype << 2) << kDtypeShift;
+      cb.first[m] = first;
+      first += (uint32_t)((t.numel + kClipChunk - 1) / kClipChunk);
     }
-    t0 += m;
+    for (int64_t b1 = blocks; b1 > 0; b1 -= kMaxBlocks) {
+      hipLaunchKernelGGL(k_tensors_clip, dim3((uint32_t)(b1 < kMaxBlocks ? b1 : kMaxBlocks)),
+                         dim3(kClipThreads), 0, stream, cb, t1 - t0, (uint32_t)(b1 - 1), scale,
+                         res);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return (int)e;
+    }
+    t1 = t0;
   }
   return (int)hipSuccess;
 }
