@@ -272,10 +272,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
   if (wave == 0 && lane < kJoinTokens && r < valid) {
     for (int k = 1; k < kJoinWaves; ++k) join(m, s, s_m[k][lane], s_s[k][lane]);
     // with o the others' sum over the label's exponential: log(1 + o)
-    const double y = picked[r], gap = (double)m / (double)kLog2e - y, sum = (double)s * scale;
-    double d = gap > 0.0 ? gap + log(sum + exp(-gap)) : log1p(sum * exp(gap));
+    const double y = picked[r], top = (double)m / (double)kLog2e, gap = top - y;
+    const double sum = (double)s * scale;
+    const double more = gap > 0.0 ? log(sum + exp(-gap)) : log1p(sum * exp(gap));
+    double d = gap > 0.0 ? gap + more : more;
     if (!(gap == gap) || y == INFINITY) d = __builtin_nan("");
-    const float l = (float)(y + d);
+    // a label at -inf: the loss is infinite, the others' lse is not
+    const float l = (float)(y == -INFINITY && d == d ? top + more : y + d);
     lse[r] = l;
     if (lse_out) lse_out[index[r]] = l;
     if (token_loss) token_loss[index[r]] = (float)d;
