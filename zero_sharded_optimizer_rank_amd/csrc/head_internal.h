@@ -53,12 +53,11 @@ int launch_head_loss(const zero_head_t* h, const HeadPlan& p, void* ws, float* t
 int launch_head_grad(const zero_head_t* h, const HeadPlan& p, void* ws,
                      const zero_head_grads_t* grads, bool kept, hipStream_t stream);
 
-// The same steps for few tokens: pack, logits (keep: also stored), gradients
-// (have: the logits are there).
-int launch_few_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse_in,
-                    float* token_loss, float* lse, const zero_head_grads_t* grads,
-                    hipStream_t stream);
-int launch_few_logits(const zero_head_t* h, const HeadPlan& p, void* ws, bool keep,
+// The same for few tokens: pack() and the logits' partial softmax in one launch
+// (the logits stay in the workspace if gradients follow), and the gradients
+// (have: the loss ran in the same call).
+int launch_few_logits(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse_in,
+                      float* token_loss, float* lse, const zero_head_grads_t* grads,
                       hipStream_t stream);
 int launch_few_grads(const zero_head_t* h, const HeadPlan& p, void* ws,
                      const zero_head_grads_t* grads, bool have, hipStream_t stream);

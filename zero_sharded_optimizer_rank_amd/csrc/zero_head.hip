@@ -138,9 +138,9 @@ struct LogitTile {
 };
 
 // Loss: (m, g_scale sum of 2^(l log2 e - m)) of every token over each 128
-// vocabulary rows, m the largest l log2 e rounded up, the label's row left out, and the label's logit: a confident token's
-// loss is log(1 + the others' sum), whose digits a sum that held the label's 1
-// would have lost.  Where the gradient follows in the same call, the
+// vocabulary rows, m the largest l log2 e rounded up, the label's row left out,
+// and the label's logit: a confident token's loss is log(1 + the others' sum),
+// whose digits a sum that held the label's 1 would have lost.  Where the gradient follows in the same call, the
 // exponentials of the piece of the vocabulary that starts at `kept` stay in
 // g's block (rounded to 16 bits): k_head_rescale turns them into g without
 // forming those logits again.
@@ -473,7 +473,8 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dx(
 template <typename T>
 __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
     const float* __restrict__ acc, int32_t most, int32_t tokens_pad, int32_t hidden_pad,
-    int32_t hidden, const int32_t* __restrict__ index, const HeadState* __restrict__ state, uint16_t* __restrict__ dx, int64_t lddx) {
+    int32_t hidden, const int32_t* __restrict__ index, const HeadState* __restrict__ state,
+    uint16_t* __restrict__ dx, int64_t lddx) {
   const int32_t r = blockIdx.y, valid = state->valid;
   const int32_t h = (blockIdx.x * kPackThreads + threadIdx.x) * 4;
   if (r >= valid || h >= hidden) return;
@@ -571,10 +572,7 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
   const WeightView w = weight_view(h, p, ws);
   HeadState* state = at<HeadState>(ws, p.state);
   const int64_t tile = p.few ? kHeadPart : kHeadTile;  // vocabulary rows a workgroup takes
-  if (p.few) {
-    const int e = launch_few_logits(h, p, ws, keep, stream);
-    if (e) return e;
-  } else if (h->tokens > 0) {
+  if (!p.few && h->tokens > 0) {
     hipLaunchKernelGGL(k_head_partials<T>,
                        dim3(tile_grid(p.tokens_pad / 256, (h->vocab + 255) / 256)),
                        dim3(kGemmThreads), 0, stream, w.w, w.ld, (int32_t)h->vocab,
@@ -584,9 +582,11 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
                        (int32_t)p.piece, keep ? at<uint16_t>(ws, p.g) : nullptr);
     ZK_LAUNCHED();
   }
-  hipLaunchKernelGGL(k_head_join, dim3((uint32_t)(p.tokens_pad / kJoinTokens)),
+  const int64_t joins = h->tokens > 0 ? (h->tokens + kJoinTokens - 1) / kJoinTokens : 1;
+  hipLaunchKernelGGL(k_head_join, dim3((uint32_t)joins),
                      dim3(64 * kJoinWaves), 0, stream, at<const float2>(ws, p.part),
-                     (int32_t)((h->vocab + tile - 1) / tile * tile / kHeadPart), (int32_t)p.tokens_pad,
+                     (int32_t)((h->vocab + tile - 1) / tile * tile / kHeadPart),
+                     (int32_t)p.tokens_pad,
                      at<const float>(ws, p.picked), at<const int32_t>(ws, p.index),
                      at<float>(ws, p.lse), at<float>(ws, p.dy), token_loss, lse,
                      at<double>(ws, p.sums), 1.0 / (double)g_scale<T>(), h->mean, state, res);
@@ -664,7 +664,7 @@ int grad_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_gr
 int launch_head_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse_in,
                      float* token_loss, float* lse, const zero_head_grads_t* gr,
                      hipStream_t stream) {
-  if (p.few) return launch_few_pack(h, p, ws, lse_in, token_loss, lse, gr, stream);
+  if (p.few) return launch_few_logits(h, p, ws, lse_in, token_loss, lse, gr, stream);
   HeadState* state = at<HeadState>(ws, p.state);
   hipLaunchKernelGGL(k_head_scan, dim3(1), dim3(kScanThreads), 0, stream, h->labels,
                      (int32_t)h->tokens, (int32_t)h->vocab, h->loss_scale, h->mean, lse_in,

@@ -11,8 +11,10 @@
 // tokens stay in the workspace (256 bytes a vocabulary row), token-contiguous.
 // w's rows may start anywhere; nothing is laid out again.
 //
-//   k_few_pack    valid tokens in order, x and its transpose
-//   k_few_logits  logits, and the partial softmax of 128 vocabulary rows
+//   k_few_logits  logits, and the partial softmax of 128 vocabulary rows; a few
+//                 workgroups of the same launch put the valid tokens in order
+//                 and transpose x for the gradients (a launch of their own in
+//                 front cost 5 us of 50)
 //   (join)        as with many tokens
 //   k_few_grads   dw tiles, and dx's partial sums over runs of the vocabulary
 //   k_few_dx      those sums joined
@@ -44,57 +46,74 @@ __device__ __forceinline__ s16x8 row8(const uint16_t* row, int32_t k, int32_t n)
   return __builtin_bit_cast(s16x8, v);
 }
 
-// Workgroup r: packed row r of x (zero past the valid tokens) and column r of
-// its transpose; what token r, if it takes no part, gets.  Every wave finds
-// the valid tokens by itself: there are at most 64.
-__global__ __launch_bounds__(kThreads4) void k_few_pack(
-    const int64_t* __restrict__ labels, int32_t tokens, int32_t vocab, double loss_scale,
-    int32_t mean, const float* __restrict__ lse_in, const uint16_t* __restrict__ x, int64_t ldx,
-    int32_t hidden, int32_t hidden_pad, int32_t* __restrict__ index, int32_t* __restrict__ label,
-    float* __restrict__ lse, HeadState* __restrict__ state, uint16_t* __restrict__ xp,
-    uint16_t* __restrict__ xt, float* __restrict__ token_loss, float* __restrict__ lse_out,
-    uint16_t* __restrict__ dx, int64_t lddx) {
+struct FewLogits {
+  const int64_t* labels;
+  const uint16_t *x, *w;
+  int64_t ldx, ldw, lddx;
+  double loss_scale;
+  int32_t tokens, vocab, hidden, hidden_pad, mean;
+  int32_t packs;          // workgroups that take pack() instead of logits
+  const float* lse_in;    // or NULL
+  float *token_loss, *lse_out;  // or NULL
+  uint16_t *xt, *dx;      // NULL: no gradients
+  // in the workspace
+  int32_t *index, *label;
+  float* lse;
+  HeadState* state;
+  float2* part;
+  float *picked, *logits; // logits: NULL if no gradients follow
+};
+
+// The valid tokens in order: lane i of `ok` takes place popcount(ok below i).
+__device__ __forceinline__ int32_t place(uint64_t ok, int lane) {
+  return __popcll(ok & ((1ull << lane) - 1));
+}
+
+// Workgroup b of f.packs: what every token that takes no part gets, x's
+// transpose for the gradients (column r: the r-th valid token, zero past the
+// last), and, b = 0, the packed tokens' indices and labels.
+__device__ __forceinline__ void pack(const FewLogits& f) {
   const int lane = threadIdx.x & 63;
-  const int32_t r = blockIdx.x;
-  const int64_t y = lane < tokens ? labels[lane] : -1;
-  const uint64_t ok = __ballot(y >= 0 && y < vocab), bad = __ballot(y >= vocab);
+  const int64_t y = lane < f.tokens ? f.labels[lane] : -1;
+  const uint64_t ok = __ballot(y >= 0 && y < f.vocab), bad = __ballot(y >= f.vocab);
   const int32_t valid = __popcll(ok);
-  if (r == 0 && threadIdx.x < 64) {
+  if (blockIdx.x == 0 && threadIdx.x < 64) {
     if (ok >> lane & 1) {
-      const int32_t at = __popcll(ok & ((1ull << lane) - 1));
-      index[at] = lane;
-      label[at] = (int32_t)y;
-      if (lse_in) lse[at] = lse_in[lane];
+      const int32_t at = place(ok, lane);
+      f.index[at] = lane;
+      f.label[at] = (int32_t)y;
+      if (f.lse_in) f.lse[at] = f.lse_in[lane];
     }
     if (lane == 0) {
-      double c = loss_scale;
-      if (mean) c /= valid > 0 ? (double)valid : 1.0;
-      state->valid = valid;
-      state->ticket = 0;
-      state->bad = __popcll(bad);
-      state->coef = bad ? __builtin_nanf("") : (float)c;
+      double c = f.loss_scale;
+      if (f.mean) c /= valid > 0 ? (double)valid : 1.0;
+      f.state->valid = valid;
+      f.state->ticket = 0;
+      f.state->bad = __popcll(bad);
+      f.state->coef = bad ? __builtin_nanf("") : (float)c;
     }
   }
-  if (r < tokens && !(ok >> r & 1)) {
-    if (threadIdx.x == 0) {
-      const float v = bad >> r & 1 ? __builtin_nanf("") : 0.0f;
-      if (token_loss) token_loss[r] = v;
-      if (lse_out) lse_out[r] = v;
+  for (int32_t r = blockIdx.x; r < kT; r += f.packs) {
+    if (r < f.tokens && !(ok >> r & 1)) {
+      if (threadIdx.x == 0) {
+        const float v = bad >> r & 1 ? __builtin_nanf("") : 0.0f;
+        if (f.token_loss) f.token_loss[r] = v;
+        if (f.lse_out) f.lse_out[r] = v;
+      }
+      if (f.dx)
+        for (int32_t h = threadIdx.x; h < f.hidden; h += kThreads4) f.dx[r * f.lddx + h] = 0;
     }
-    if (dx)
-      for (int32_t h = threadIdx.x; h < hidden; h += kThreads4) dx[r * lddx + h] = 0;
-  }
-  int32_t src = -1;  // the r-th valid token
-  uint64_t m = ok;
-  for (int32_t i = 0; m; ++i, m &= m - 1)
-    if (i == r) src = __ffsll((unsigned long long)m) - 1;
-  for (int32_t c = threadIdx.x; c < hidden_pad / 8; c += kThreads4) {
-    s16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (src >= 0) v = row8(x + src * ldx, 8 * c, hidden);
-    *(s16x8*)(xp + (int64_t)r * hidden_pad + 8 * c) = v;
-    if (xt)
+    if (!f.xt) continue;
+    int32_t src = -1;  // the r-th valid token
+    uint64_t m = ok;
+    for (int32_t i = 0; m; ++i, m &= m - 1)
+      if (i == r) src = __ffsll((unsigned long long)m) - 1;
+    for (int32_t c = threadIdx.x; c < f.hidden_pad / 8; c += kThreads4) {
+      s16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (src >= 0) v = row8(f.x + src * f.ldx, 8 * c, f.hidden);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) xt[(int64_t)(8 * c + e) * kT + r] = (uint16_t)v[e];
+      for (int e = 0; e < 8; ++e) f.xt[(int64_t)(8 * c + e) * kT + r] = (uint16_t)v[e];
+    }
   }
 }
 
@@ -104,20 +123,21 @@ __global__ __launch_bounds__(kThreads4) void k_few_pack(
 // Workgroups start at different columns: rows of 4096 columns lie a power of
 // two apart, and all workgroups at the same column would ask the same memory
 // channels (128256 x 4096: 183 us, 5.7 TB/s, against 237 us).  Two waves a SIMD:
-// three were slower (205 us), as were more columns ahead.
+// three were slower (205 us), as were more columns ahead.  Only as many 16-token
+// columns as there may be tokens are multiplied (37 tokens, 50257 x 1600: 38 -> 35 us).
 constexpr int kXTile = 128;
-template <typename T>
+template <typename T, int NJ>
 __global__ __launch_bounds__(kThreads4) __attribute__((amdgpu_waves_per_eu(2, 2))) void
-k_few_logits(
-    const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, int32_t hidden,
-    const uint16_t* __restrict__ x, int32_t hidden_pad, const int32_t* __restrict__ label,
-    const HeadState* __restrict__ state, float2* __restrict__ part, float* __restrict__ picked,
-    float* __restrict__ logits) {
-  __shared__ float s_m[4][kT], s_s[4][kT];
-  // [64 tokens][128 columns]: 16-byte chunk c of row r lies at c ^ (r & 15)
-  __shared__ __attribute__((aligned(1024))) char lx[2][kT * kXTile * 2];
+k_few_logits(const FewLogits f) {
+  constexpr int kTokens = 16 * NJ;
+  __shared__ int32_t s_src[kT], s_y[kT];
+  __shared__ float s_m[4][kTokens], s_s[4][kTokens];
+  // [tokens][128 columns]: 16-byte chunk c of row r lies at c ^ (r & 15)
+  __shared__ __attribute__((aligned(1024))) char lx[2][kTokens * kXTile * 2];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, q = lane & 15;
-  const int64_t v0 = (int64_t)blockIdx.x * kHeadPart + wave * 32;
+  if ((int32_t)blockIdx.x < f.packs) return pack(f);
+  const int32_t vocab = f.vocab, hidden = f.hidden, block = (int32_t)blockIdx.x - f.packs;
+  const int64_t v0 = (int64_t)block * kHeadPart + wave * 32;
   // A load covers 8 rows' whole 128-byte lines: lanes of q < 8 take the first
   // half of row q % 8's, the others the second.  The fragments want lane q to
   // hold row q: two loads of 8 rows each trade halves (lines() below).
@@ -127,16 +147,16 @@ k_few_logits(
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int64_t v = v0 + 16 * i + 8 * r + (q & 7);
-      wr[i][r] = w + (v < vocab ? v : vocab - 1) * ldw;  // rows past the end are masked below
+      wr[i][r] = f.w + (v < vocab ? v : vocab - 1) * f.ldw;  // rows past the end are masked below
     }
   const int32_t wk = 8 * (4 * (q >> 3) + g);
-  f32x4 acc[2][4];
+  f32x4 acc[2][NJ];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{};
   // a[buffer][i][line][rows 0-7 or 8-15]
-  s16x8 a[2][2][2][2], xr[4];
+  s16x8 a[2][2][2][2], xr[NJ];
   auto fetch_w = [&](s16x8 (&d)[2][2][2], int32_t tile) {
     const int32_t k0 = tile * kXTile + wk;
     if ((tile + 1) * kXTile <= hidden) {
@@ -165,7 +185,8 @@ k_few_logits(
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t give = first ? hi[e] : lo[e];
-      const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, false);
+      const uint32_t got =
+          (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, false);
       x[e] = first ? lo[e] : got;
       y[e] = first ? got : hi[e];
     }
@@ -174,16 +195,20 @@ k_few_logits(
   };
   // thread: chunk threadIdx % 16 of rows threadIdx / 16 + 16 k
   const int xc = threadIdx.x & 15, xrow = threadIdx.x >> 4;
+  const uint16_t* xp[NJ];
   auto fetch_x = [&](int32_t tile) {
     const int32_t c = tile * kXTile + 8 * xc;
+    if ((tile + 1) * kXTile <= hidden) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      xr[k] = c < hidden_pad ? *(const s16x8*)(x + (int64_t)(xrow + 16 * k) * hidden_pad + c)
-                             : s16x8{};
+      for (int k = 0; k < NJ; ++k) xr[k] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(xp[k] + c));
+    } else {
+#pragma unroll
+      for (int k = 0; k < NJ; ++k) xr[k] = row8(xp[k], c, hidden);
+    }
   };
   auto store_x = [&](char* d) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < NJ; ++k)
       *(s16x8*)(d + (xrow + 16 * k) * 256 + ((xc ^ xrow) << 4)) = xr[k];
   };
   auto use = [&](const s16x8 (&d)[2][2][2], const char* l) {
@@ -195,40 +220,63 @@ k_few_logits(
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const s16x8 b = *(const s16x8*)(l + (16 * j + q) * 256 + (((8 * n + 4 * s + g) ^ q) << 4));
+        for (int j = 0; j < NJ; ++j) {
+          const s16x8 b =
+              *(const s16x8*)(l + (16 * j + q) * 256 + (((8 * n + 4 * s + g) ^ q) << 4));
 #pragma unroll
           for (int i = 0; i < 2; ++i) acc[i][j] = mfma(T{}, f[i][s], b, acc[i][j]);
         }
     }
   };
-  const int32_t tiles = (hidden_pad + 2 * kXTile - 1) / (2 * kXTile) * 2;  // whole pairs; zeros past the end
+  // whole pairs; zeros past the end
+  const int32_t tiles = (hidden + 2 * kXTile - 1) / (2 * kXTile) * 2;
   const int32_t from = (int32_t)(blockIdx.x / kXcds) % tiles;  // the XCD's workgroups in turn
-  auto tile = [&](int32_t t) {  // t <= tiles + 1
-    t += from;
-    if (t >= tiles) t -= tiles;
-    return t >= tiles ? t - tiles : t;
-  };
-  fetch_x(tile(0));
+  auto tile = [&](int32_t t) { return t + from < tiles ? t + from : t + from - tiles; };
   fetch_w(a[0], tile(0));
+  // the packed tokens: where their rows of x are, and their labels
+  const int64_t own = lane < f.tokens ? f.labels[lane] : -1;
+  const uint64_t ok = __ballot(own >= 0 && own < vocab);
+  const int32_t valid = __popcll(ok);
+  if (valid == 0) return;
+  if (wave == 0) {
+    if (lane >= valid) {
+      s_src[lane] = 0;  // any row: what its columns hold reaches no result
+      s_y[lane] = -1;
+    }
+    if (ok >> lane & 1) {
+      s_src[place(ok, lane)] = lane;
+      s_y[place(ok, lane)] = (int32_t)own;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < NJ; ++k) xp[k] = f.x + s_src[xrow + 16 * k] * f.ldx;
+  fetch_x(tile(0));
   store_x(lx[0]);
   fetch_x(tile(1));
-  for (int32_t t = 0; t < tiles; t += 2) {
+  // tile t is in LDS, and the buffer of the one before is free
+  auto turn = [&] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+  for (int32_t t = 0; t < tiles - 2; t += 2) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      // tile t + h is in LDS, and the buffer of the one before is free
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      turn();
       fetch_w(a[1 - h], tile(t + h + 1));
       store_x(lx[1 - h]);
       fetch_x(tile(t + h + 2));
       use(a[h], lx[h]);
     }
   }
+  turn();
+  fetch_w(a[1], tile(tiles - 1));
+  store_x(lx[1]);
+  use(a[0], lx[0]);
+  turn();
+  use(a[1], lx[1]);
   const int32_t rows = (int32_t)(vocab - v0 < 32 ? vocab - v0 : 32);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < NJ; ++j) {
     const int32_t t = 16 * j + q;
-    const int64_t y = t < state->valid ? (int64_t)label[t] - v0 : -1;
+    const int64_t y = s_y[t] >= 0 ? s_y[t] - v0 : -1;
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -237,9 +285,9 @@ k_few_logits(
         const int r = 16 * i + 4 * g + e;
         float l = acc[i][j][e];
         if (r >= rows) l = -INFINITY;
-        if (logits && r < rows) logits[(v0 + r) * kT + t] = l;
+        if (f.logits && r < rows) f.logits[(v0 + r) * kT + t] = l;
         if (r == y) {
-          picked[t] = l;
+          f.picked[t] = l;
           l = -INFINITY;
         }
         acc[i][j][e] = l;
@@ -263,11 +311,11 @@ k_few_logits(
     }
   }
   __syncthreads();
-  if (wave == 0) {
+  if (wave == 0 && lane < kTokens) {
     float m = s_m[0][lane], s = s_s[0][lane];
 #pragma unroll
     for (int k = 1; k < 4; ++k) join(m, s, s_m[k][lane], s_s[k][lane]);
-    part[(int64_t)blockIdx.x * kT + lane] = float2{m, s};
+    f.part[(int64_t)block * kT + lane] = float2{m, s};
   }
 }
 
@@ -329,7 +377,8 @@ __device__ __forceinline__ void load_tokens(const FewGrad& f, Tokens& k) {
 // B = g (rows: vocabulary), contraction over the 64 tokens.  A wave takes 64
 // columns at a time; its g stays in registers.
 template <typename T, bool F32OUT>
-__device__ __forceinline__ void few_dw(const FewGrad& f, const Tokens& tok, char* lds, int32_t block) {
+__device__ __forceinline__ void few_dw(const FewGrad& f, const Tokens& tok, char* lds,
+                                       int32_t block) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, q = lane & 15;
   const int32_t vblocks = (f.vocab + 63) / 64;
   const int32_t v0 = block % vblocks * 64, h1 = (block / vblocks + 1) * f.dw_cols;
@@ -341,7 +390,8 @@ __device__ __forceinline__ void few_dw(const FewGrad& f, const Tokens& tok, char
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int32_t row = v0 + 16 * j + q;
-      const f32x4* p = (const f32x4*)(f.logits + (int64_t)(row < f.vocab ? row : 0) * kT + 32 * s + 8 * g);
+      const f32x4* p =
+          (const f32x4*)(f.logits + (int64_t)(row < f.vocab ? row : 0) * kT + 32 * s + 8 * g);
       const f32x4 a = p[0], b = p[1];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -436,7 +486,8 @@ __device__ __forceinline__ void few_dw(const FewGrad& f, const Tokens& tok, char
 // workgroup forms in LDS from the logits.  The next rows of w and of the
 // logits are on their way while these are multiplied.
 template <typename T>
-__device__ __forceinline__ void few_dx(const FewGrad& f, const Tokens& tok, char* lds, int32_t block) {
+__device__ __forceinline__ void few_dx(const FewGrad& f, const Tokens& tok, char* lds,
+                                       int32_t block) {
   using FA = Frags<256, true>;
   using FB = Frags<64, false>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -563,23 +614,49 @@ __global__ __launch_bounds__(kThreads4) void k_few_dx(
 }
 
 template <typename T>
-int logits_t(const zero_head_t* h, const HeadPlan& p, void* ws, bool keep, hipStream_t stream) {
-  hipLaunchKernelGGL(k_few_logits<T>, dim3((uint32_t)((h->vocab + kHeadPart - 1) / kHeadPart)),
-                     dim3(kThreads4), 0, stream, (const uint16_t*)h->w, h->ldw, (int32_t)h->vocab,
-                     (int32_t)h->hidden, at<const uint16_t>(ws, p.x), (int32_t)p.hidden_pad,
-                     at<const int32_t>(ws, p.label), at<HeadState>(ws, p.state),
-                     at<float2>(ws, p.part), at<float>(ws, p.picked),
-                     keep ? at<float>(ws, p.logits) : nullptr);
+int logits_t(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse_in,
+             float* token_loss, float* lse, const zero_head_grads_t* gr, hipStream_t stream) {
+  FewLogits f{};
+  f.labels = h->labels;
+  f.x = (const uint16_t*)h->x;
+  f.w = (const uint16_t*)h->w;
+  f.ldx = h->ldx;
+  f.ldw = h->ldw;
+  f.loss_scale = h->loss_scale;
+  f.tokens = (int32_t)h->tokens;
+  f.vocab = (int32_t)h->vocab;
+  f.hidden = (int32_t)h->hidden;
+  f.hidden_pad = (int32_t)p.hidden_pad;
+  f.mean = h->mean;
+  f.packs = gr ? kT : 1;
+  f.lse_in = lse_in;
+  f.token_loss = token_loss;
+  f.lse_out = lse;
+  if (gr) {
+    f.xt = at<uint16_t>(ws, p.xt);
+    f.dx = (uint16_t*)gr->dx;
+    f.lddx = gr->lddx;
+    f.logits = at<float>(ws, p.logits);
+  }
+  f.index = at<int32_t>(ws, p.index);
+  f.label = at<int32_t>(ws, p.label);
+  f.lse = at<float>(ws, p.lse);
+  f.state = at<HeadState>(ws, p.state);
+  f.part = at<float2>(ws, p.part);
+  f.picked = at<float>(ws, p.picked);
+  const int columns = (int)((h->tokens + 15) / 16);
+  const auto kernel = columns <= 1   ? k_few_logits<T, 1>
+                      : columns == 2 ? k_few_logits<T, 2>
+                      : columns == 3 ? k_few_logits<T, 3>
+                                     : k_few_logits<T, 4>;
+  hipLaunchKernelGGL(kernel, dim3((uint32_t)(f.packs + (h->vocab + kHeadPart - 1) / kHeadPart)),
+                     dim3(kThreads4), 0, stream, f);
   return (int)hipGetLastError();
 }
 
 template <typename T>
 int grads_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_grads_t* gr,
             bool have, hipStream_t stream) {
-  if (!have && h->tokens > 0) {
-    const int e = logits_t<T>(h, p, ws, true, stream);
-    if (e) return e;
-  }
   FewGrad f{};
   f.logits = at<const float>(ws, p.logits);
   f.w = (const uint16_t*)h->w;
@@ -622,23 +699,11 @@ int grads_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
 
 }  // namespace
 
-int launch_few_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse_in,
-                    float* token_loss, float* lse, const zero_head_grads_t* gr,
-                    hipStream_t stream) {
-  hipLaunchKernelGGL(k_few_pack, dim3(kT), dim3(kThreads4), 0, stream, h->labels,
-                     (int32_t)h->tokens, (int32_t)h->vocab, h->loss_scale, h->mean, lse_in,
-                     (const uint16_t*)h->x, h->ldx, (int32_t)h->hidden, (int32_t)p.hidden_pad,
-                     at<int32_t>(ws, p.index), at<int32_t>(ws, p.label), at<float>(ws, p.lse),
-                     at<HeadState>(ws, p.state), at<uint16_t>(ws, p.x),
-                     gr ? at<uint16_t>(ws, p.xt) : nullptr, token_loss, lse,
-                     gr ? (uint16_t*)gr->dx : nullptr, gr ? gr->lddx : 0);
-  return (int)hipGetLastError();
-}
-
-int launch_few_logits(const zero_head_t* h, const HeadPlan& p, void* ws, bool keep,
+int launch_few_logits(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse_in,
+                      float* token_loss, float* lse, const zero_head_grads_t* gr,
                       hipStream_t stream) {
-  return h->dtype == ZERO_BF16 ? logits_t<BF16>(h, p, ws, keep, stream)
-                               : logits_t<FP16>(h, p, ws, keep, stream);
+  return h->dtype == ZERO_BF16 ? logits_t<BF16>(h, p, ws, lse_in, token_loss, lse, gr, stream)
+                               : logits_t<FP16>(h, p, ws, lse_in, token_loss, lse, gr, stream);
 }
 
 int launch_few_grads(const zero_head_t* h, const HeadPlan& p, void* ws,
