@@ -702,6 +702,9 @@ int zero_tensors_norm_clip(const zero_tensor_t* tensors, int32_t n_tensors,
 #define ZERO_HEAD_MAX_TOKENS ((int64_t)1 << 20)
 #define ZERO_HEAD_MAX_VOCAB ((int64_t)1 << 30)
 #define ZERO_HEAD_MAX_HIDDEN ((int64_t)1 << 20)
+/* ceil(T / 256) * ceil(V / 256) is less than this: a million tokens take a
+ * vocabulary of up to half a million rows in one call */
+#define ZERO_HEAD_MAX_TILES ((int64_t)1 << 23)
 
 typedef struct zero_head {
   int64_t tokens, hidden, vocab; /* T >= 0, H >= 1, V >= 1 */

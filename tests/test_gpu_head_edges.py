@@ -267,3 +267,12 @@ def test_tokens_past_32_bits():
     check(dw, want_dw, (rel + n * E) * terms_dw + E * want_dw.abs(), "dw")
     del x, r
     torch.cuda.empty_cache()
+
+
+def test_long_vocabulary_laid_out_again():
+    """Rows of w that start anywhere, more of them than one launch has workgroups."""
+    T, V, H, dtype = 70, 2 ** 20 + 300, 24, torch.bfloat16
+    x, w, y = _inputs(T, V, H, dtype, seed=18, ldw=25)
+    y[-1] = V - 1
+    _all(_head(T, V, H, dtype).loss_grad(x, w, y), reference(x, w, y))
+    torch.cuda.empty_cache()

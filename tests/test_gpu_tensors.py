@@ -294,3 +294,69 @@ def test_accumulated_gradient_into_the_update():
     assert ends[0][4].item() == ends[1][4].item() < 1.0
     for a, b in zip(ends[0], ends[1]):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n,longest", [(195, 1), (196, 1), (390, 1), (391, 40_000), (1024, 3),
+                                       (1024, 65_536), (1024, 65_537), (1025, 3), (1500, 20_000)])
+def test_many_short_tensors(n, longest):
+    """Around the lists that their last launch finishes: tensors of up to four chunks, up to
+    1024 of them."""
+    sizes = [(11 * i) % 53 for i in range(n)]
+    sizes[n // 2] = longest
+    cpu, gpu = _make(sizes, TYPES, seed=31, sigma=1.0)
+    lst = _lists()(gpu)
+    lst.ws.fill_(0xFF)  # its content must not matter
+    sq = _exact_squares(cpu)
+    for k in range(3):
+        r = lst.norm(max_grad_norm=1.0, loss_scale=2.0)
+        for got, s in zip(r.tensor_sq.tolist(), sq):
+            _close(got, s / 4.0)
+        _close(r.own_sq.item(), math.fsum(sq) / 4.0)
+        assert r.skip.item() == r.overflow.item() == 0
+    for where in (0, 3, n // 2, n - 1):
+        if sizes[where]:
+            gpu[where][sizes[where] - 1] = float("nan")
+            r = lst.norm(max_grad_norm=1.0)
+            assert r.skip.item() == r.overflow.item() == 1
+            gpu[where][sizes[where] - 1] = 1.0
+            assert lst.norm(max_grad_norm=1.0).skip.item() == 0
+
+
+def test_many_short_tensors_replayed():
+    sizes = [(11 * i) % 53 for i in range(400)]
+    cpu, gpu = _make(sizes, TYPES, seed=32)
+    lst = _lists()(gpu)
+    lst.norm_clip(max_grad_norm=0.25)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        lst.norm_clip(max_grad_norm=0.25)
+    for k in range(4):
+        _, fresh = _make(sizes, TYPES, seed=40 + k)
+        for t, f in zip(gpu, fresh):
+            t.copy_(f)
+        eager = _lists()(fresh)
+        want = eager.norm_clip(max_grad_norm=0.25)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(lst.res, eager.res)
+        assert torch.equal(lst.result.tensor_sq, want.tensor_sq)
+        for a, b in zip(gpu, fresh):
+            assert torch.equal(a, b)
+
+
+def test_more_workgroups_than_a_launch_has():
+    """A tensor that the clip takes several launches for (2^35 elements a launch)."""
+    torch.cuda.empty_cache()
+    n = (1 << 35) + 4096 * 3 + 5
+    x = torch.empty(n, dtype=torch.bfloat16, device="cuda")
+    x.fill_(0.5)
+    r = _lists()([x]).norm_clip(max_grad_norm=2.0 ** 14)
+    assert r.own_sq.item() == n / 4.0  # every partial sum is exact
+    want = (torch.tensor(0.5) * torch.tensor(r.clip_coef.item())).to(torch.bfloat16)
+    assert want < 0.5
+    for s in range(0, n, 1 << 32):
+        assert bool((x[s:s + (1 << 32)] == want.item()).all())
+    del x
+    torch.cuda.empty_cache()

@@ -136,3 +136,17 @@ def test_loss_head_refusals():
         LossHead(4, 8, 16, torch.float16, device="cpu")
     with pytest.raises(ValueError):
         LossHead(4, 0, 16, torch.float16)
+
+
+def test_tiles_of_one_launch():
+    """The logits' tiles fit one launch, or the call is refused."""
+    ok = dict(tokens=1 << 20, hidden=8, ldx=8, ldw=8)
+    limit = 2 ** 23 // (2 ** 20 // 256) * 256
+    assert abi.zero_head_workspace_bytes(_head(vocab=limit - 256, **ok), False) > 0
+    for vocab in (limit - 255, limit, 1 << 30):
+        assert abi.zero_head_workspace_bytes(_head(vocab=vocab, **ok), False) == 0
+        with pytest.raises(abi.ZeroError) as e:
+            _loss(_head(vocab=vocab, **ok), n=1 << 62)
+        assert e.value.code == abi.ZERO_EINVAL
+    assert abi.zero_head_workspace_bytes(
+        _head(vocab=1 << 30, tokens=65, hidden=8, ldx=8, ldw=8), False) > 0

@@ -99,3 +99,20 @@ def test_grad_list_refusals_on_the_host():
         GradList([3.0], device=dev)
     with pytest.raises(ValueError, match="outputs for"):
         GradList([torch.zeros(3)], out=[], device=dev)
+
+
+def test_entries_that_share_memory():
+    torch = pytest.importorskip("torch")
+    from zero_sharded_optimizer_rank_amd.tensors import _check_apart
+    b = torch.zeros(100)
+    a, c, d = b[:40], b[40:60], b[60:]
+    empty = b[10:10]
+    _check_apart([a, c, d, empty, empty], [a, c, d, empty, empty])
+    _check_apart([a, c], [torch.zeros(40), torch.zeros(20)])
+    for tensors, out in (([a, a], [a, a]),                    # twice, in place
+                         ([a, c, b[:1]], [a, c, b[:1]]),
+                         ([a, c], [d, d[:20]]),               # outputs over each other
+                         ([a, c], [c, a]),                    # outputs over other inputs
+                         ([b[:90], c], [torch.zeros(90), torch.zeros(20)])):
+        with pytest.raises(ValueError, match="share memory"):
+            _check_apart(tensors, out)

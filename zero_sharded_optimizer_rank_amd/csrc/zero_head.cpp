@@ -9,6 +9,7 @@
 #include "zero_shard.h"
 
 using namespace zk::host;
+using zk::kHeadTile;
 
 namespace {
 
@@ -22,7 +23,10 @@ bool good_sizes(const zero_head_t* h) {
   return h->tokens >= 0 && h->tokens <= ZERO_HEAD_MAX_TOKENS && h->hidden >= 1 &&
          h->hidden <= ZERO_HEAD_MAX_HIDDEN && h->vocab >= 1 && h->vocab <= ZERO_HEAD_MAX_VOCAB &&
          h->ldx >= h->hidden && h->ldx <= ZERO_HEAD_MAX_HIDDEN && h->ldw >= h->hidden &&
-         h->ldw <= ZERO_HEAD_MAX_HIDDEN && (h->dtype == ZERO_F16 || h->dtype == ZERO_BF16);
+         h->ldw <= ZERO_HEAD_MAX_HIDDEN && (h->dtype == ZERO_F16 || h->dtype == ZERO_BF16) &&
+         // one launch takes all tiles of the logits, 512 threads each, of at most 2^32 - 1
+         up(h->tokens, kHeadTile) / kHeadTile * (up(h->vocab, kHeadTile) / kHeadTile) <
+             ZERO_HEAD_MAX_TILES;
 }
 
 int check_head(const zero_head_t* h) {

@@ -108,15 +108,17 @@ __global__ __launch_bounds__(kPackThreads) void k_head_pack_x(
 }
 
 // Packed w, for rows that do not start on 16-byte boundaries.
+constexpr uint32_t kPackRows = 1 << 20;  // workgroups at most: a launch holds 2^32 threads
 __global__ __launch_bounds__(kPackThreads) void k_head_pack_w(
-    const uint16_t* __restrict__ w, int64_t ldw, int32_t hidden, int32_t hidden_pad,
-    uint16_t* __restrict__ out) {
-  const int64_t v = blockIdx.x;
-  u32x4* o = (u32x4*)(out + v * hidden_pad);
-  const uint16_t* p = w + v * ldw;
-  const bool whole16 = ((uintptr_t)p & 15) == 0;
-  for (int32_t c = threadIdx.x; c < hidden_pad / 8; c += kPackThreads)
-    o[c] = take8(p + 8 * c, hidden - 8 * c, whole16);
+    const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, int32_t hidden,
+    int32_t hidden_pad, uint16_t* __restrict__ out) {
+  for (int64_t v = blockIdx.x; v < vocab; v += gridDim.x) {
+    u32x4* o = (u32x4*)(out + v * hidden_pad);
+    const uint16_t* p = w + v * ldw;
+    const bool whole16 = ((uintptr_t)p & 15) == 0;
+    for (int32_t c = threadIdx.x; c < hidden_pad / 8; c += kPackThreads)
+      o[c] = take8(p + 8 * c, hidden - 8 * c, whole16);
+  }
 }
 
 // --- 2. the logits' tiles ------------------------------------------------------
@@ -140,8 +142,8 @@ struct LogitTile {
 // Loss: (m, g_scale sum of 2^(l log2 e - m)) of every token over each 128
 // vocabulary rows, m the largest l log2 e rounded up, the label's row left out,
 // and the label's logit: a confident token's loss is log(1 + the others' sum),
-// whose digits a sum that held the label's 1 would have lost.  Where the gradient follows in the same call, the
-// exponentials of the piece of the vocabulary that starts at `kept` stay in
+// whose digits a sum that held the label's 1 would have lost.  Where the
+// gradient follows in the same call, the exponentials of the piece of the vocabulary that starts at `kept` stay in
 // g's block (rounded to 16 bits): k_head_rescale turns them into g without
 // forming those logits again.
 template <typename T>
@@ -479,7 +481,8 @@ __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
   const int32_t h = (blockIdx.x * kPackThreads + threadIdx.x) * 4;
   if (r >= valid || h >= hidden) return;
   const int32_t split = dx_split(
-      (int32_t)((valid + kHeadTile - 1) / kHeadTile * ((hidden + kHeadTile - 1) / kHeadTile)), most);
+      (int32_t)((valid + kHeadTile - 1) / kHeadTile * ((hidden + kHeadTile - 1) / kHeadTile)),
+      most);
   const float c = state->coef / g_scale<T>();
   const float* p = acc + (int64_t)r * hidden_pad + h;
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -680,9 +683,10 @@ int launch_head_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const fl
     ZK_LAUNCHED();
   }
   if (p.pack_w) {
-    hipLaunchKernelGGL(k_head_pack_w, dim3((uint32_t)h->vocab), dim3(kPackThreads), 0, stream,
-                       (const uint16_t*)h->w, h->ldw, (int32_t)h->hidden, (int32_t)p.hidden_pad,
-                       at<uint16_t>(ws, p.w));
+    const uint32_t rows = h->vocab < kPackRows ? (uint32_t)h->vocab : kPackRows;
+    hipLaunchKernelGGL(k_head_pack_w, dim3(rows), dim3(kPackThreads), 0, stream,
+                       (const uint16_t*)h->w, h->ldw, (int32_t)h->vocab, (int32_t)h->hidden,
+                       (int32_t)p.hidden_pad, at<uint16_t>(ws, p.w));
     ZK_LAUNCHED();
   }
   return (int)hipSuccess;

@@ -33,8 +33,8 @@ constexpr int kClipThreads = 256;
 // fp16 1.67 / 1.63 / 1.57 ms).
 constexpr int64_t kClipChunk = 4096;
 // Entries that fit the 4 KiB of kernel arguments beside the other arguments.
-constexpr int kNormBatch = 192;
-constexpr int kClipBatch = 136;
+constexpr int kNormBatch = 195;
+constexpr int kClipBatch = 139;
 constexpr int kDtypeShift = 60;  // a numel's top bits hold the type(s)
 
 struct NormBatch {
@@ -78,7 +78,8 @@ __device__ __forceinline__ constexpr int per16() { return D == ZERO_F32 ? 4 : 8;
 template <int D>
 __device__ __forceinline__ float piece_elem(u32x4 v, int e) {
   if constexpr (D == ZERO_F32) return __uint_as_float(v[e]);
-  else return to_f32<D == ZERO_BF16 ? Fmt::BF16 : Fmt::F16>((v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+  else
+    return to_f32<D == ZERO_BF16 ? Fmt::BF16 : Fmt::F16>((v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
 }
 template <int D>
 __device__ __forceinline__ float load_elem(const void* p, int64_t i) {
@@ -147,10 +148,29 @@ __device__ __forceinline__ double chunk_sum(const void* base, int64_t at, int64_
   return s;
 }
 
+// Values first, first + step, ... of get(0..count).
+template <typename Get>
+__device__ __forceinline__ void strided_sum(int64_t first, int64_t step, int64_t count, double& x,
+                                            uint32_t& bad, Get get) {
+  x = 0.0;
+  bad = 0;
+#pragma unroll 8
+  for (int64_t j = first; j < count; j += step) {
+    const Partial pt = get(j);
+    x += __longlong_as_double((long long)pt.lo);
+    bad |= (uint32_t)(pt.hi >> 63);
+  }
+}
+
+// FINISH: the list's last launch, of few short tensors: its last workgroup does
+// what k_tensors_finalize<1> would, in its order.
+template <bool FINISH>
 __global__ __launch_bounds__(kNormThreads) void k_tensors_norm(
     NormBatch nb, int32_t n, int32_t t0, int64_t chunk0, int64_t chunk, int64_t again, int32_t arm,
-    TensorRecord* __restrict__ records, Partial* __restrict__ partials,
-    uint32_t* __restrict__ ticket) {
+    int32_t all, TensorRecord* __restrict__ records, Partial* __restrict__ partials,
+    uint32_t* __restrict__ ticket, double* __restrict__ tensor_sq, FinalizeArgs fa,
+    zero_step_result_t* __restrict__ res) {
+  __shared__ uint32_t s_last;
   const uint32_t b = blockIdx.x;
   if (arm && b == 0 && threadIdx.x == 0) *ticket = 0u;
   const int i = find_tensor(nb.first, n, b);
@@ -170,19 +190,27 @@ __global__ __launch_bounds__(kNormThreads) void k_tensors_norm(
   if (threadIdx.x == 0)
     partials[chunk0 + b] = Partial{(uint64_t)__double_as_longlong(s),
                                    (uint64_t)(bad ? 1u : 0u) << 63};
-}
-
-// Values first, first + step, ... of get(0..count).
-template <typename Get>
-__device__ __forceinline__ void strided_sum(int64_t first, int64_t step, int64_t count, double& x,
-                                            uint32_t& bad, Get get) {
-  x = 0.0;
-  bad = 0;
-#pragma unroll 8
-  for (int64_t j = first; j < count; j += step) {
-    const Partial pt = get(j);
-    x += __longlong_as_double((long long)pt.lo);
-    bad |= (uint32_t)(pt.hi >> 63);
+  if constexpr (FINISH) {
+    if (threadIdx.x == 0) {
+      __threadfence();  // the workgroup's record and partial, before the ticket
+      s_last = atomicAdd(ticket, 1u) == gridDim.x - 1 ? 1u : 0u;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    s = 0.0;
+    bad = 0;
+    for (int32_t t = threadIdx.x; t < all; t += kNormThreads) {
+      const TensorRecord r = records[t];
+      double x;
+      uint32_t inf;
+      strided_sum(0, 1, r.chunks, x, inf, [&](int64_t j) { return partials[r.first + j]; });
+      if (tensor_sq) tensor_sq[t] = (x * fa.inv64) * fa.inv64;
+      s += x;
+      bad |= inf;
+    }
+    block_tree<kNormThreads>(s, bad);
+    if (threadIdx.x == 0) finalize_bf16_into(s, bad, fa, res);
   }
 }
 
@@ -349,6 +377,9 @@ int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_
   // launch would leave CUs idle
   const int32_t launches = (n + kNormBatch - 1) / kNormBatch;
   const int32_t batch = launches ? (n + launches - 1) / launches : 1;
+  // The last launch's last workgroup can finish a list of few short tensors,
+  // where launches are what costs; the first has set its ticket.
+  const bool fused = launches > 1 && n <= 4 * kNormThreads && l.longest <= 4;
   for (int32_t t0 = 0; t0 < n; t0 += batch) {
     const int32_t m = n - t0 < batch ? n - t0 : batch;
     NormBatch nb;
@@ -360,12 +391,15 @@ int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_
       nb.first[i] = (uint32_t)blocks;
       blocks += t.numel ? (t.numel - 1) / chunk + 1 : 1;
     }
-    hipLaunchKernelGGL(k_tensors_norm, dim3((uint32_t)blocks), dim3(kNormThreads), 0, stream, nb,
-                       m, t0, chunk0, chunk, again, t0 == 0 ? 1 : 0, records, partials, ticket);
+    const bool last = fused && t0 + batch >= n;
+    hipLaunchKernelGGL(last ? k_tensors_norm<true> : k_tensors_norm<false>, dim3((uint32_t)blocks),
+                       dim3(kNormThreads), 0, stream, nb, m, t0, chunk0, chunk, again,
+                       t0 == 0 ? 1 : 0, n, records, partials, ticket, tensor_sq, fa, res);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
     chunk0 += blocks;
   }
+  if (fused) return (int)hipSuccess;
   auto finalize = [&](auto kernel, int group, int threads) {
     const int64_t blocks = ((int64_t)n * group + threads - 1) / threads;
     hipLaunchKernelGGL(kernel, dim3(blocks > 0 ? (uint32_t)blocks : 1u), dim3(threads), 0, stream,
@@ -383,7 +417,7 @@ int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_
 // lie in the last-level cache.
 int launch_tensors_clip(const zero_tensor_t* tensors, int32_t n, float scale,
                         const zero_step_result_t* res, hipStream_t stream) {
-  constexpr int64_t kMaxBlocks = (int64_t)1 << 30;  // of one launch
+  constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // of one launch: 2^31 threads
   const int32_t launches = (n + kClipBatch - 1) / kClipBatch;
   const int32_t batch = launches ? (n + launches - 1) / launches : 1;
   for (int32_t t1 = n; t1 > 0;) {

@@ -52,6 +52,21 @@ def _check_tensor(t, what: str, device) -> None:
         raise ValueError(f"{what} is not contiguous")
 
 
+def _check_apart(tensors, out) -> None:
+    """No tensor or output may share memory with another entry's."""
+    spans = []
+    for i, (t, o) in enumerate(zip(tensors, out)):
+        for x in (t,) if o is t else (t, o):
+            if x.numel():
+                spans.append((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), i))
+    reach, owner = 0, -1
+    for start, end, i in sorted(spans):
+        if start < reach and i != owner:  # an entry's own pair is checked by the library
+            raise ValueError(f"tensors {min(i, owner)} and {max(i, owner)} share memory")
+        if end > reach:
+            reach, owner = end, i
+
+
 class GradList:
     """A list of gradient tensors on one GPU, and where its clipped copies go.
 
@@ -85,6 +100,7 @@ class GradList:
                     raise ValueError(f"output {i} has {o.numel()} elements, its tensor "
                                      f"{t.numel()}")
             entries.append((t, DTYPES[t.dtype], o, DTYPES[o.dtype], t.numel()))
+        _check_apart(self.tensors, self.out)
         self.n = len(entries)
         self.table = abi.tensor_table(entries)
         self.ws_bytes = abi.zero_tensors_workspace_bytes(self.table, self.n)
