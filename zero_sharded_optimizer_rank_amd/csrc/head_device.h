@@ -57,6 +57,8 @@ __device__ __forceinline__ u32x4 take8(const uint16_t* p, int64_t n, bool whole1
   return v;
 }
 
+// Eight bytes at any element's address.
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 
 // (m, s) stands for s 2^m.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {

@@ -20,7 +20,7 @@ struct HeadPlan {
   int64_t parts;       // softmax partials a token gets (one per kHeadPart vocabulary rows)
   int64_t piece;       // vocabulary rows a piece of the gradient takes (whole tiles)
   int64_t kept;        // first row of the last piece
-  int32_t split;       // most ways the hidden gradient's contraction is split
+  int32_t split;       // most ways the hidden gradient's contraction is split (at most 64)
   bool few;            // at most kFewTokens tokens (see zero_head_few.hip)
   bool pack_w;         // w's rows do not start on 16-byte boundaries
   // offsets
@@ -35,7 +35,7 @@ struct HeadState {  // at offset `state`
   int32_t ticket;
   int64_t bad;
   float coef;      // c, or NaN
-  float pad;
+  int32_t split;   // ways dx's contraction is split (not for few tokens)
 };
 
 HeadPlan head_plan(const zero_head_t* h, bool grad);

@@ -30,12 +30,32 @@ constexpr int kGemmThreads = 512;
 constexpr int kJoinTokens = 16, kJoinWaves = 16, kJoinBatch = 8;
 
 // --- 1. scan and pack --------------------------------------------------------
+// Ways to split dx's contraction: the fewest whose tiles come close to filling
+// whole rounds of the 256 CUs (a token count that leaves 208 tiles would
+// idle a fifth of the chip; eight times as many tiles, a twentieth).  One wave;
+// lane l weighs l + 1 ways.
+constexpr int32_t kCus = 256;
+__device__ __forceinline__ int32_t dx_split(int32_t tiles, int32_t most, int lane) {
+  const float c = (float)((tiles * (lane + 1) + kCus - 1) / kCus) / (float)(lane + 1);
+  int32_t best = 1;
+  float cost = __shfl(c, 0);
+  for (int32_t s = 2; s <= most; ++s) {
+    const float cs = __shfl(c, s - 1);
+    if (cs < 0.97f * cost) {
+      cost = cs;
+      best = s;
+    }
+  }
+  return best;
+}
+
 // One workgroup: the valid tokens in order.  index[r] is packed row r's token;
 // label and (for the gradient alone) lse likewise.
 __global__ __launch_bounds__(kScanThreads) void k_head_scan(
     const int64_t* __restrict__ labels, int32_t tokens, int32_t vocab, double loss_scale,
-    int32_t mean, const float* __restrict__ lse_in, int32_t* __restrict__ index,
-    int32_t* __restrict__ label, float* __restrict__ lse, HeadState* __restrict__ state) {
+    int32_t mean, int32_t htiles, int32_t most, const float* __restrict__ lse_in,
+    int32_t* __restrict__ index, int32_t* __restrict__ label, float* __restrict__ lse,
+    HeadState* __restrict__ state) {
   __shared__ int32_t s_count[kScanThreads / 64];
   __shared__ int32_t s_bad;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -64,7 +84,11 @@ __global__ __launch_bounds__(kScanThreads) void k_head_scan(
     at += total;
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
+  if (wave != 0) return;
+  const int32_t ttiles = (int32_t)((at + kHeadTile - 1) / kHeadTile);
+  const int32_t split = dx_split(ttiles * htiles, most, lane);
+  if (lane == 0) {
+    state->split = split;
     double c = loss_scale;
     if (mean) c /= at > 0 ? (double)at : 1.0;
     state->valid = at;
@@ -413,23 +437,6 @@ __global__ __launch_bounds__(256) void k_head_rescale(
   }
 }
 
-// Ways to split dx's contraction: the fewest whose tiles come close to filling
-// whole rounds of the 256 CUs (a token count that leaves 208 tiles would
-// idle a fifth of the chip; eight times as many tiles, a twentieth).
-constexpr int32_t kCus = 256;
-__device__ __forceinline__ int32_t dx_split(int32_t tiles, int32_t most) {
-  int32_t best = 1;
-  float cost = 1e30f;
-  for (int32_t s = 1; s <= most; ++s) {
-    const float c = (float)((tiles * s + kCus - 1) / kCus) / (float)s;
-    if (c < 0.97f * cost) {
-      cost = c;
-      best = s;
-    }
-  }
-  return best;
-}
-
 // dx: A = w (rows of the tile: hidden columns, contiguous along them), B = g
 // (token rows, contiguous along the vocabulary).  Split s of the piece adds
 // into its own fp32 block.
@@ -437,12 +444,12 @@ template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_dx(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ w, int64_t ldw,
     int32_t vocab_left, int32_t hidden_w, int32_t hidden, int32_t hidden_pad, int32_t tokens_pad,
-    int32_t most, int32_t first, const HeadState* __restrict__ state, float* __restrict__ acc_out) {
+    int32_t first, const HeadState* __restrict__ state, float* __restrict__ acc_out) {
   using G = Gemm<T, true, false>;
   ZK_GEMM_LDS;
   const uint32_t ht = (uint32_t)((hidden + G::BM - 1) / G::BM);
   const uint32_t tt = (uint32_t)((state->valid + G::BN - 1) / G::BN);
-  const int32_t split = dx_split((int32_t)(ht * tt), most);
+  const int32_t split = state->split;
   const int32_t part = (piece / split + kStage - 1) / kStage * kStage;
   int32_t mt, nt;
   if (!tile_of(blockIdx.x, tt, ht * (uint32_t)split, mt, nt)) return;
@@ -474,24 +481,28 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dx(
 // dx from the splits' sums, four columns a thread.
 template <typename T>
 __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
-    const float* __restrict__ acc, int32_t most, int32_t tokens_pad, int32_t hidden_pad,
+    const float* __restrict__ acc, int32_t tokens_pad, int32_t hidden_pad,
     int32_t hidden, const int32_t* __restrict__ index, const HeadState* __restrict__ state,
     uint16_t* __restrict__ dx, int64_t lddx) {
   const int32_t r = blockIdx.y, valid = state->valid;
   const int32_t h = (blockIdx.x * kPackThreads + threadIdx.x) * 4;
   if (r >= valid || h >= hidden) return;
-  const int32_t split = dx_split(
-      (int32_t)((valid + kHeadTile - 1) / kHeadTile * ((hidden + kHeadTile - 1) / kHeadTile)),
-      most);
+  const int32_t split = state->split;
   const float c = state->coef / g_scale<T>();
   const float* p = acc + (int64_t)r * hidden_pad + h;
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int32_t k = 0; k < split; ++k, p += (int64_t)tokens_pad * hidden_pad)
-    s += *(const f32x4*)p;
+#pragma unroll 4
+  for (int32_t k = 0; k < split; ++k)
+    s += *(const f32x4*)(p + (int64_t)k * tokens_pad * hidden_pad);
   uint16_t* o = dx + (int64_t)index[r] * lddx + h;
+  s *= c;
+  if (h + 4 <= hidden) {
+    *(u32x2_a2*)o = narrow4<T>(s[0], s[1], s[2], s[3]);
+  } else {
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (h + e < hidden) o[e] = (uint16_t)narrow<T>(s[e] * c);
+    for (int e = 0; e < 4; ++e)
+      if (h + e < hidden) o[e] = (uint16_t)narrow<T>(s[e]);
+  }
 }
 
 // dw: A = packed x (rows of the tile: hidden columns), B = g (vocabulary
@@ -626,7 +637,7 @@ int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
     hipLaunchKernelGGL(k_head_dx<T>, dim3(tile_grid(htiles * p.split, ttiles)),
                        dim3(kGemmThreads), 0, stream, g, (int32_t)p.piece, w.w + v0 * w.ld, w.ld,
                        (int32_t)left, w.width, (int32_t)h->hidden, (int32_t)p.hidden_pad,
-                       (int32_t)p.tokens_pad, p.split, first ? 1 : 0, state,
+                       (int32_t)p.tokens_pad, first ? 1 : 0, state,
                        at<float>(ws, p.acc));
     ZK_LAUNCHED();
   }
@@ -655,7 +666,7 @@ int grad_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_gr
     hipLaunchKernelGGL((k_head_dx_out<T>),
                        dim3((uint32_t)((h->hidden + 4 * kPackThreads - 1) / (4 * kPackThreads)),
                             (uint32_t)h->tokens),
-                       dim3(kPackThreads), 0, stream, at<const float>(ws, p.acc), p.split,
+                       dim3(kPackThreads), 0, stream, at<const float>(ws, p.acc),
                        (int32_t)p.tokens_pad, (int32_t)p.hidden_pad, (int32_t)h->hidden,
                        at<const int32_t>(ws, p.index), at<HeadState>(ws, p.state),
                        (uint16_t*)gr->dx, gr->lddx);
@@ -670,7 +681,8 @@ int launch_head_pack(const zero_head_t* h, const HeadPlan& p, void* ws, const fl
   if (p.few) return launch_few_logits(h, p, ws, lse_in, token_loss, lse, gr, stream);
   HeadState* state = at<HeadState>(ws, p.state);
   hipLaunchKernelGGL(k_head_scan, dim3(1), dim3(kScanThreads), 0, stream, h->labels,
-                     (int32_t)h->tokens, (int32_t)h->vocab, h->loss_scale, h->mean, lse_in,
+                     (int32_t)h->tokens, (int32_t)h->vocab, h->loss_scale, h->mean,
+                     (int32_t)((h->hidden + kHeadTile - 1) / kHeadTile), p.split, lse_in,
                      at<int32_t>(ws, p.index), at<int32_t>(ws, p.label), at<float>(ws, p.lse),
                      state);
   ZK_LAUNCHED();

@@ -600,7 +600,8 @@ __global__ __launch_bounds__(kThreads4) void k_few_dx(
   if (h < hidden) {
     const float* p = acc + (int64_t)r * hidden_pad + h;
 #pragma unroll 8
-    for (int32_t k = wave; k < split; k += 4) s += *(const f32x4*)(p + (int64_t)k * kT * hidden_pad);
+    for (int32_t k = wave; k < split; k += 4)
+      s += *(const f32x4*)(p + (int64_t)k * kT * hidden_pad);
   }
   s_sum[wave][lane] = s;
   __syncthreads();
