@@ -276,3 +276,21 @@ def test_long_vocabulary_laid_out_again():
     y[-1] = V - 1
     _all(_head(T, V, H, dtype).loss_grad(x, w, y), reference(x, w, y))
     torch.cuda.empty_cache()
+
+
+def test_workspace_grows_on_another_stream():
+    """A w that has to be laid out again, after calls on a stream of the caller's."""
+    T, V, H, dtype = 100, 900, 264, torch.bfloat16
+    x, w, y = _inputs(T, V, H, dtype, seed=19)
+    _, odd, _ = _inputs(T, V, H, dtype, seed=19, ldw=265)
+    ref = reference(x, w, y)
+    h = _head(T, V, H, dtype)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    small = h.ws.numel()
+    for m in (w, odd, w):
+        r = h.loss_grad(x, m, y, stream=s)
+        torch.empty(small, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    torch.cuda.synchronize()
+    assert h.ws.numel() > small
+    _all(r, ref)

@@ -360,3 +360,15 @@ def test_more_workgroups_than_a_launch_has():
         assert bool((x[s:s + (1 << 32)] == want.item()).all())
     del x
     torch.cuda.empty_cache()
+
+
+def test_clip_needs_a_norm():
+    _, gpu = _make([100, 3], TYPES, seed=50)
+    lst = _lists()(gpu)
+    with pytest.raises(RuntimeError):
+        lst.clip()
+    lst.norm(max_grad_norm=0.01)
+    lst.clip()
+    assert abs(math.sqrt(sum((t.double() ** 2).sum().item() for t in gpu)) - 0.01) < 1e-4
+    with pytest.raises(ValueError):
+        _lists()([gpu[0], gpu[0]])

@@ -50,7 +50,8 @@ __device__ __forceinline__ int32_t dx_split(int32_t tiles, int32_t most, int lan
 }
 
 // One workgroup: the valid tokens in order.  index[r] is packed row r's token;
-// label and (for the gradient alone) lse likewise.
+// label and (for the gradient alone) lse likewise.  Bound by latency: 5 us for
+// up to 2048 tokens, 12 us for 8192.
 __global__ __launch_bounds__(kScanThreads) void k_head_scan(
     const int64_t* __restrict__ labels, int32_t tokens, int32_t vocab, double loss_scale,
     int32_t mean, int32_t htiles, int32_t most, const float* __restrict__ lse_in,
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(kScanThreads) void k_head_scan(
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (threadIdx.x == 0) s_bad = 0;
   __syncthreads();
-  int32_t at = 0;  // valid tokens before this round
+  int32_t at = 0;  // valid tokens before these
   for (int32_t t0 = 0; t0 < tokens; t0 += kScanThreads) {
     const int32_t t = t0 + threadIdx.x;
     const int64_t y = t < tokens ? labels[t] : -1;
@@ -100,7 +101,8 @@ __global__ __launch_bounds__(kScanThreads) void k_head_scan(
 
 // Workgroup r: packed row r copies valid token index[r], zero-padded (rows from
 // the valid count to the next whole tile are zero); and if token r takes no
-// part, its loss, lse and dx are written.
+// part, its loss, lse and dx are written.  Bound by memory: 8192 x 4096, 22 us
+// (5.6 TB/s).
 __global__ __launch_bounds__(kPackThreads) void k_head_pack_x(
     const uint16_t* __restrict__ x, int64_t ldx, int32_t tokens, int32_t hidden,
     int32_t hidden_pad, int32_t vocab, const int64_t* __restrict__ labels,
@@ -167,9 +169,13 @@ struct LogitTile {
 // vocabulary rows, m the largest l log2 e rounded up, the label's row left out,
 // and the label's logit: a confident token's loss is log(1 + the others' sum),
 // whose digits a sum that held the label's 1 would have lost.  Where the
-// gradient follows in the same call, the exponentials of the piece of the vocabulary that starts at `kept` stay in
-// g's block (rounded to 16 bits): k_head_rescale turns them into g without
-// forming those logits again.
+// gradient follows in the same call, the exponentials of the piece of the
+// vocabulary that starts at `kept` stay in g's block (rounded to 16 bits):
+// k_head_rescale turns them into g without forming those logits again.
+// Bound by the matrix cores (busy 75 to 80%, at the chip's power limit): 7373 x
+// 128256 x 4096, bf16, 5.4 ms (1430 TFLOP/s); with the exponentials stored, 3277
+// tokens 2.64 ms (1300).  1024 x 50257 x 1600, fp16, 0.19 ms (870): 788 tiles on
+// 256 CUs, four rounds for three.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, const uint16_t* __restrict__ x,
@@ -253,7 +259,9 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
 // --- 3. join -------------------------------------------------------------------
 // Workgroup b joins the partials of 16 packed rows (a line of partials), 64
 // strips of the vocabulary side by side; the last workgroup to finish sums the
-// losses.
+// losses.  Sums, logarithm and exponential are fp64 from here: few values, and a
+// confident token's loss would lose digits in fp32.  Bound by latency: 3277
+// tokens x 1002 partials 20 us, 37 x 393 7 us.
 __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
     const float2* __restrict__ part, int32_t parts, int32_t tokens_pad,
     const float* __restrict__ picked, const int32_t* __restrict__ index, float* __restrict__ lse,
@@ -337,7 +345,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
 
 // --- 4. gradient -----------------------------------------------------------------
 // g of a piece: rows are packed tokens, columns the piece's vocabulary rows;
-// columns past the vocabulary and rows past the valid tokens are zero.
+// columns past the vocabulary and rows past the valid tokens are zero.  Rounded
+// once to 16 bits, the type the matrix cores multiply (dx and dw keep 32-bit
+// sums).  Bound as k_head_partials.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_g(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, const uint16_t* __restrict__ x,
@@ -399,47 +409,67 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_g(
 
 // g of the piece whose exponentials were kept: 2^(l log2 e - m) 2^(m - lse log2
 // e) - [v = y], m the reference of the 128 vocabulary rows.  The label's element is
-// e^-loss - 1.  A workgroup takes 8 tokens (one line of partials) and
-// kRescaleCols columns.
-constexpr int kRescaleCols = 1024;
+// e^-loss - 1.  A workgroup takes 8 tokens (half a line of partials), a wave
+// each, and kRescaleCols columns, all of them loaded before the first is used.
+// Bound by memory: 3277 x 128256, @@RS@@.
+constexpr int kRescaleCols = 2048, kRescaleWaves = 8, kRescaleLoads = kRescaleCols / 512;
 template <typename T>
-__global__ __launch_bounds__(256) void k_head_rescale(
+__global__ __launch_bounds__(64 * kRescaleWaves) void k_head_rescale(
     uint16_t* __restrict__ g, int32_t piece, int32_t left, const float2* __restrict__ part,
     int32_t part0, int32_t tokens_pad, const int32_t* __restrict__ label, int64_t piece0,
     const float* __restrict__ lse, const float* __restrict__ dy,
     const HeadState* __restrict__ state) {
   const int32_t valid = state->valid;
-  const int32_t t = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int32_t t = blockIdx.y * kRescaleWaves + (threadIdx.x >> 6);
   if (t >= (valid + kHeadTile - 1) / kHeadTile * kHeadTile) return;
-  const bool there = t < valid;
-  const float z = there ? lse[t] : 0.0f;
-  const int64_t y = there ? (int64_t)label[t] - piece0 : -1;
-  const int32_t c1 = (int32_t)(blockIdx.x + 1) * kRescaleCols;
-  for (int32_t c = blockIdx.x * kRescaleCols + (threadIdx.x & 31) * 8; c < c1 && c < piece;
-       c += 256) {
-    if (c >= (left + kHeadTile - 1) / kHeadTile * kHeadTile) return;
-    u32x4* o = (u32x4*)(g + (int64_t)t * piece + c);
-    u32x4 v = {0, 0, 0, 0};
-    if (there && c < left) {
-      const float f = exp2_fast(__builtin_fmaf(
-          -z, kLog2e, part[(int64_t)(part0 + c / kHeadPart) * tokens_pad + t].x));
-      v = *o;
+  const int32_t first = (int32_t)blockIdx.x * kRescaleCols, c0 = first + (threadIdx.x & 63) * 8;
+  const int32_t end = (left + kHeadTile - 1) / kHeadTile * kHeadTile;  // at most piece
+  u32x4* o = (u32x4*)(g + (int64_t)t * piece + c0);
+  if (t >= valid) {
+#pragma unroll
+    for (int k = 0; k < kRescaleLoads; ++k)
+      if (c0 + 512 * k < end) o[64 * k] = u32x4{0, 0, 0, 0};
+    return;
+  }
+  u32x4 v[kRescaleLoads];
+  float f[kRescaleLoads];
+#pragma unroll
+  for (int k = 0; k < kRescaleLoads; ++k) {
+    const int32_t c = c0 + 512 * k;
+    v[k] = u32x4{0, 0, 0, 0};
+    f[k] = 0.0f;
+    if (c < left) {
+      v[k] = o[64 * k];
+      f[k] = part[(int64_t)(part0 + c / kHeadPart) * tokens_pad + t].x;
+    }
+  }
+  const float z = lse[t];
+  const int64_t y = (int64_t)label[t] - piece0;
+  const bool plain = first + kRescaleCols <= left && (y < first || y >= first + kRescaleCols);
+#pragma unroll
+  for (int k = 0; k < kRescaleLoads; ++k) {
+    const int32_t c = c0 + 512 * k;
+    const float s = exp2_fast(__builtin_fmaf(-z, kLog2e, f[k]));
+    float p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = widen<T>((v[k][e >> 1] >> (16 * (e & 1))) & 0xFFFFu) * s;
+    if (!plain) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float p = widen<T>((v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) * f;
-        if (c + e == y) p = dy[t] * g_scale<T>();
-        if (c + e >= left) p = 0.0f;
-        const uint32_t b = narrow<T>(p);
-        v[e >> 1] = e & 1 ? (v[e >> 1] & 0xFFFFu) | b << 16 : (v[e >> 1] & 0xFFFF0000u) | b;
+        if (c + e == y) p[e] = dy[t] * g_scale<T>();
+        if (c + e >= left) p[e] = 0.0f;
       }
+      if (c >= end) continue;
     }
-    *o = v;
+    const u32x2 a = narrow4<T>(p[0], p[1], p[2], p[3]), b = narrow4<T>(p[4], p[5], p[6], p[7]);
+    o[64 * k] = u32x4{a[0], a[1], b[0], b[1]};
   }
 }
 
 // dx: A = w (rows of the tile: hidden columns, contiguous along them), B = g
 // (token rows, contiguous along the vocabulary).  Split s of the piece adds
-// into its own fp32 block.
+// into its own fp32 block.  Bound by the matrix cores: 3277 x 128256 x 4096,
+// bf16, 2.76 ms (1250 TFLOP/s); 1024 x 50257 x 1600, fp16, 0.17 ms (945).
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_dx(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ w, int64_t ldw,
@@ -478,7 +508,8 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dx(
   }
 }
 
-// dx from the splits' sums, four columns a thread.
+// dx from the splits' sums, four columns a thread.  Bound by memory: 2047 x 8192
+// 24 us (4.1 TB/s); 1024 x 1600 of nine splits 17 us.
 template <typename T>
 __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
     const float* __restrict__ acc, int32_t tokens_pad, int32_t hidden_pad,
@@ -507,7 +538,8 @@ __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
 
 // dw: A = packed x (rows of the tile: hidden columns), B = g (vocabulary
 // rows), both contiguous along their rows; the contraction runs over the
-// tokens.
+// tokens.  Bound by the matrix cores: 3277 x 128256 x 4096, bf16, 2.58 ms (1330
+// TFLOP/s); 2047 x 32000 x 8192 0.88 ms (1220).
 template <typename T, bool F32OUT>
 __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ x,
@@ -625,8 +657,8 @@ int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
     if (have)
       hipLaunchKernelGGL(k_head_rescale<T>,
                          dim3((uint32_t)((left + kRescaleCols - 1) / kRescaleCols),
-                              (uint32_t)(p.tokens_pad / 8)),
-                         dim3(256), 0, stream, g, (int32_t)p.piece, (int32_t)left,
+                              (uint32_t)(p.tokens_pad / kRescaleWaves)),
+                         dim3(64 * kRescaleWaves), 0, stream, g, (int32_t)p.piece, (int32_t)left,
                          at<const float2>(ws, p.part), (int32_t)(v0 / kHeadPart),
                          (int32_t)p.tokens_pad, label, v0, lse, at<const float>(ws, p.dy), state);
     else

