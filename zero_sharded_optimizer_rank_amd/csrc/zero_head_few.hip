@@ -20,6 +20,8 @@
 //   k_few_dx      those sums joined
 #include <stddef.h>
 
+#include <type_traits>
+
 #include "head_device.h"
 
 namespace zk {
@@ -126,7 +128,7 @@ __device__ __forceinline__ void pack(const FewLogits& f) {
 // three were slower (205 us), as were more columns ahead.  Only as many 16-token
 // columns as there may be tokens are multiplied (37 tokens, 50257 x 1600: 38 -> 35 us).
 constexpr int kXTile = 128;
-template <typename T, int NJ>
+template <typename T, int NJ, bool WHOLE>
 __global__ __launch_bounds__(kThreads4) __attribute__((amdgpu_waves_per_eu(2, 2))) void
 k_few_logits(const FewLogits f) {
   constexpr int kTokens = 16 * NJ;
@@ -159,7 +161,17 @@ k_few_logits(const FewLogits f) {
   s16x8 a[2][2][2][2], xr[NJ];
   auto fetch_w = [&](s16x8 (&d)[2][2][2], int32_t tile) {
     const int32_t k0 = tile * kXTile + wk;
-    if ((tile + 1) * kXTile <= hidden) {
+    if constexpr (WHOLE) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int l = 0; l < 2; ++l) {
+            const int32_t k = k0 + 64 * l < hidden ? k0 + 64 * l : 0;  // use() takes these out
+            d[i][l][r] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(wr[i][r] + k));
+          }
+    } else if ((tile + 1) * kXTile <= hidden) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -198,7 +210,11 @@ k_few_logits(const FewLogits f) {
   const uint16_t* xp[NJ];
   auto fetch_x = [&](int32_t tile) {
     const int32_t c = tile * kXTile + 8 * xc;
-    if ((tile + 1) * kXTile <= hidden) {
+    if constexpr (WHOLE) {
+#pragma unroll
+      for (int k = 0; k < NJ; ++k)
+        xr[k] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(xp[k] + (c < hidden ? c : 0)));
+    } else if ((tile + 1) * kXTile <= hidden) {
 #pragma unroll
       for (int k = 0; k < NJ; ++k) xr[k] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(xp[k] + c));
     } else {
@@ -206,12 +222,22 @@ k_few_logits(const FewLogits f) {
       for (int k = 0; k < NJ; ++k) xr[k] = row8(xp[k], c, hidden);
     }
   };
-  auto store_x = [&](char* d) {
+  auto store_x = [&](char* d, int32_t tile) {
+    const bool in = !WHOLE || tile * kXTile + 8 * xc < hidden;
 #pragma unroll
     for (int k = 0; k < NJ; ++k)
-      *(s16x8*)(d + (xrow + 16 * k) * 256 + ((xc ^ xrow) << 4)) = xr[k];
+      *(s16x8*)(d + (xrow + 16 * k) * 256 + ((xc ^ xrow) << 4)) = in ? xr[k] : s16x8{};
   };
-  auto use = [&](const s16x8 (&d)[2][2][2], const char* l) {
+  auto use = [&](s16x8 (&d)[2][2][2], const char* l, int32_t tile) {
+    if (WHOLE && (tile + 1) * kXTile > hidden) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (tile * kXTile + wk + 64 * n >= hidden) d[i][n][r] = s16x8{};
+    }
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       s16x8 f[2][2];
@@ -252,7 +278,7 @@ k_few_logits(const FewLogits f) {
 #pragma unroll
   for (int k = 0; k < NJ; ++k) xp[k] = f.x + s_src[xrow + 16 * k] * f.ldx;
   fetch_x(tile(0));
-  store_x(lx[0]);
+  store_x(lx[0], tile(0));
   fetch_x(tile(1));
   // tile t is in LDS, and the buffer of the one before is free
   auto turn = [&] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
@@ -261,17 +287,17 @@ k_few_logits(const FewLogits f) {
     for (int h = 0; h < 2; ++h) {
       turn();
       fetch_w(a[1 - h], tile(t + h + 1));
-      store_x(lx[1 - h]);
+      store_x(lx[1 - h], tile(t + h + 1));
       fetch_x(tile(t + h + 2));
-      use(a[h], lx[h]);
+      use(a[h], lx[h], tile(t + h));
     }
   }
   turn();
   fetch_w(a[1], tile(tiles - 1));
-  store_x(lx[1]);
-  use(a[0], lx[0]);
+  store_x(lx[1], tile(tiles - 1));
+  use(a[0], lx[0], tile(tiles - 2));
   turn();
-  use(a[1], lx[1]);
+  use(a[1], lx[1], tile(tiles - 1));
   const int32_t rows = (int32_t)(vocab - v0 < 32 ? vocab - v0 : 32);
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
@@ -485,7 +511,7 @@ __device__ __forceinline__ void few_dw(const FewGrad& f, const Tokens& tok, char
 // rows at a time: A = w (columns of memory, staged in LDS), B = g, which the
 // workgroup forms in LDS from the logits.  The next rows of w and of the
 // logits are on their way while these are multiplied.
-template <typename T>
+template <typename T, bool WHOLE>
 __device__ __forceinline__ void few_dx(const FewGrad& f, const Tokens& tok, char* lds,
                                        int32_t block) {
   using FA = Frags<256, true>;
@@ -510,7 +536,20 @@ __device__ __forceinline__ void few_dx(const FewGrad& f, const Tokens& tok, char
   auto fetch = [&](int32_t v0) {  // w: rows 8k + wave*2 + lane/32
     const uint16_t* p = f.w + (v0 + wave * 2 + (lane >> 5)) * f.ldw + h0;
     const float* l = f.logits + (int64_t)(v0 + wave * 16) * kT + lane;
-    if (v0 + kStage <= vb && h0 + 256 <= f.hidden) {
+    if constexpr (WHOLE) {
+      const int32_t c = h0 + (lane & 31) * 8 < f.hidden ? h0 + (lane & 31) * 8 : 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int32_t v = v0 + 8 * k + wave * 2 + (lane >> 5);
+        nw[k] = __builtin_bit_cast(
+            s16x8, *(const u32x4_a2*)(f.w + (int64_t)(v < f.vocab ? v : f.vocab - 1) * f.ldw + c));
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int32_t v = v0 + wave * 16 + e;
+        nl[e] = f.logits[(int64_t)(v < f.vocab ? v : f.vocab - 1) * kT + lane];
+      }
+    } else if (v0 + kStage <= vb && h0 + 256 <= f.hidden) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         nw[k] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(p + 8 * k * f.ldw + (lane & 31) * 8));
@@ -577,12 +616,12 @@ __device__ __forceinline__ void few_dx(const FewGrad& f, const Tokens& tok, char
 }
 
 // Workgroups of dx first: they run longest.
-template <typename T, bool F32OUT>
+template <typename T, bool F32OUT, bool WHOLE>
 __global__ __launch_bounds__(kThreads4) void k_few_grads(FewGrad f, int32_t dx_blocks) {
   __shared__ __attribute__((aligned(1024))) char lds[49152];
   __shared__ Tokens tok;
   load_tokens<T>(f, tok);
-  if ((int32_t)blockIdx.x < dx_blocks) few_dx<T>(f, tok, lds, blockIdx.x);
+  if ((int32_t)blockIdx.x < dx_blocks) few_dx<T, WHOLE>(f, tok, lds, blockIdx.x);
   else few_dw<T, F32OUT>(f, tok, lds, blockIdx.x - dx_blocks);
 }
 
@@ -646,10 +685,14 @@ int logits_t(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse
   f.part = at<float2>(ws, p.part);
   f.picked = at<float>(ws, p.picked);
   const int columns = (int)((h->tokens + 15) / 16);
-  const auto kernel = columns <= 1   ? k_few_logits<T, 1>
-                      : columns == 2 ? k_few_logits<T, 2>
-                      : columns == 3 ? k_few_logits<T, 3>
-                                     : k_few_logits<T, 4>;
+  const auto pick = [&](auto whole) {
+    constexpr bool W = decltype(whole)::value;
+    return columns <= 1   ? k_few_logits<T, 1, W>
+           : columns == 2 ? k_few_logits<T, 2, W>
+           : columns == 3 ? k_few_logits<T, 3, W>
+                          : k_few_logits<T, 4, W>;
+  };
+  const auto kernel = h->hidden % 8 == 0 ? pick(std::true_type{}) : pick(std::false_type{});
   hipLaunchKernelGGL(kernel, dim3((uint32_t)(f.packs + (h->vocab + kHeadPart - 1) / kHeadPart)),
                      dim3(kThreads4), 0, stream, f);
   return (int)hipGetLastError();
@@ -684,12 +727,12 @@ int grads_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
   f.split = p.split;
   f.run = (int32_t)(((h->vocab + p.split - 1) / p.split + kStage - 1) / kStage * kStage);
   const int32_t dx_blocks = h->tokens > 0 ? htiles * f.split : 0;
-  if (gr->dw_dtype == ZERO_F32)
-    hipLaunchKernelGGL((k_few_grads<T, true>), dim3((uint32_t)(dx_blocks + f.dw_blocks)),
-                       dim3(kThreads4), 0, stream, f, dx_blocks);
-  else
-    hipLaunchKernelGGL((k_few_grads<T, false>), dim3((uint32_t)(dx_blocks + f.dw_blocks)),
-                       dim3(kThreads4), 0, stream, f, dx_blocks);
+  const bool f32 = gr->dw_dtype == ZERO_F32;
+  const auto kernel = h->hidden % 8 == 0
+                          ? (f32 ? k_few_grads<T, true, true> : k_few_grads<T, false, true>)
+                          : (f32 ? k_few_grads<T, true, false> : k_few_grads<T, false, false>);
+  hipLaunchKernelGGL(kernel, dim3((uint32_t)(dx_blocks + f.dw_blocks)), dim3(kThreads4), 0, stream,
+                     f, dx_blocks);
   ZK_LAUNCHED();
   if (h->tokens > 0)
     hipLaunchKernelGGL(k_few_dx<T>, dim3((uint32_t)htiles, (uint32_t)h->tokens), dim3(kThreads4), 0,
