@@ -411,7 +411,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_g(
 // e) - [v = y], m the reference of the 128 vocabulary rows.  The label's element is
 // e^-loss - 1.  A workgroup takes 8 tokens (half a line of partials), a wave
 // each, and kRescaleCols columns, all of them loaded before the first is used.
-// Bound by memory: 3277 x 128256, @@RS@@.
+// Bound by memory: 3277 x 128256, 0.29 ms (5.9 TB/s).
 constexpr int kRescaleCols = 2048, kRescaleWaves = 8, kRescaleLoads = kRescaleCols / 512;
 template <typename T>
 __global__ __launch_bounds__(64 * kRescaleWaves) void k_head_rescale(

@@ -122,11 +122,21 @@ __device__ __forceinline__ void pack(const FewLogits& f) {
 // Logits of 128 vocabulary rows, 32 a wave: A = w from memory straight into
 // fragments, 128 hidden columns (8 KiB a wave) on their way while the last ones
 // are multiplied; B = packed x through LDS, since all four waves read it.
+// Bound by memory: 128256 x 4096, one token 168 us (6.2 TB/s), 64 tokens 190
+// (5.5); 50257 x 1600, 37 tokens 35 us (4.6).
+//
 // Workgroups start at different columns: rows of 4096 columns lie a power of
 // two apart, and all workgroups at the same column would ask the same memory
-// channels (128256 x 4096: 183 us, 5.7 TB/s, against 237 us).  Two waves a SIMD:
-// three were slower (205 us), as were more columns ahead.  Only as many 16-token
-// columns as there may be tokens are multiplied (37 tokens, 50257 x 1600: 38 -> 35 us).
+// channels (64 tokens: 183 against 237 us).  Two waves a SIMD and one set of
+// columns on its way: three waves were slower (202 against 190 us), three sets
+// too (206).  Only as many 16-token columns as there may be tokens are
+// multiplied (37 tokens, 50257 x 1600: 38 -> 35 us).
+//
+// WHOLE: rows are whole 16-byte pieces (hidden % 8 == 0).  A piece past the
+// row's end is then loaded from its start and taken out later, without a branch
+// around any load: with branches the compiler waits for the newest loads where
+// they join (37 tokens, 50257 x 1600: 37.4 against 34.8 us; dx of 50 tokens,
+// 1000 x 72, 10.2 against 6.4).
 constexpr int kXTile = 128;
 template <typename T, int NJ, bool WHOLE>
 __global__ __launch_bounds__(kThreads4) __attribute__((amdgpu_waves_per_eu(2, 2))) void
@@ -615,7 +625,8 @@ __device__ __forceinline__ void few_dx(const FewGrad& f, const Tokens& tok, char
     }
 }
 
-// Workgroups of dx first: they run longest.
+// Workgroups of dx first: they run longest.  Bound by memory: 64 tokens, 128256 x
+// 4096, 415 us (w read, dw written: 5.1 TB/s).
 template <typename T, bool F32OUT, bool WHOLE>
 __global__ __launch_bounds__(kThreads4) void k_few_grads(FewGrad f, int32_t dx_blocks) {
   __shared__ __attribute__((aligned(1024))) char lds[49152];
