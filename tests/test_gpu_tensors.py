@@ -372,3 +372,30 @@ def test_clip_needs_a_norm():
     assert abs(math.sqrt(sum((t.double() ** 2).sum().item() for t in gpu)) - 0.01) < 1e-4
     with pytest.raises(ValueError):
         _lists()([gpu[0], gpu[0]])
+
+
+@pytest.mark.parametrize("sizes", [[1], [0, 5, 0], [16384 * 4] * 3, [16384 * 5, 3, 70_000],
+                                   [16384 * 256 - 1], [16384 * 255, 1], [16384 * 256, 1],
+                                   [100] * 139, [100] * 140, [16384] * 64 + [1] * 75, [0, 0]])
+def test_norm_and_clip_in_one_call_equal_the_two_calls(sizes):
+    """Around the lists whose clip finishes the norm: the same bits as norm, then clip."""
+    for bad in (False, True):
+        if bad and not any(sizes):
+            continue
+        _, a = _make(sizes, TYPES, seed=33)
+        _, b = _make(sizes, TYPES, seed=33)
+        if bad:
+            k = max(range(len(sizes)), key=lambda i: sizes[i])
+            a[k][sizes[k] // 2] = b[k][sizes[k] // 2] = float("inf")
+        one, two = _lists()(a), _lists()(b)
+        one.ws.fill_(0xFF)
+        one.res.fill_(0xFF)
+        for other in (0.0, 9.0):
+            r = one.norm_clip(max_grad_norm=0.01, loss_scale=4.0, other_sq=other)
+            want = two.norm(max_grad_norm=0.01, loss_scale=4.0, other_sq=other)
+            two.clip(loss_scale=4.0)
+            assert torch.equal(one.res, two.res)
+            assert torch.equal(r.tensor_sq, want.tensor_sq)
+            assert r.skip.item() == bad
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)

@@ -26,11 +26,13 @@ TensorLayout tensor_layout(const zero_tensor_t* tensors, int32_t n);
 size_t tensors_workspace_bytes(const zero_tensor_t* tensors, int32_t n);
 
 // Launchers: arguments already validated.  Return hipSuccess or the error.
-// clip: a clip of the same list follows (see launch_tensors_clip's order).
 int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_sq,
-                        void* workspace, bool clip, const FinalizeArgs& fa,
-                        zero_step_result_t* res, hipStream_t stream);
+                        void* workspace, const FinalizeArgs& fa, zero_step_result_t* res,
+                        hipStream_t stream);
 int launch_tensors_clip(const zero_tensor_t* tensors, int32_t n, float scale,
                         const zero_step_result_t* res, hipStream_t stream);
+int launch_tensors_norm_clip(const zero_tensor_t* tensors, int32_t n, double* tensor_sq,
+                             void* workspace, const FinalizeArgs& fa, float scale,
+                             zero_step_result_t* res, hipStream_t stream);
 
 }  // namespace zk

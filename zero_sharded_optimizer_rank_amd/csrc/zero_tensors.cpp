@@ -123,7 +123,7 @@ int zero_tensors_norm(const zero_tensor_t* tensors, int32_t n_tensors,
   g_err[0] = 0;
   const int rc = check_norm(tensors, n_tensors, args, tensor_sq, workspace, ws_bytes, dev_result);
   if (rc) return rc;
-  return hip_status(zk::launch_tensors_norm(tensors, n_tensors, tensor_sq, workspace, false,
+  return hip_status(zk::launch_tensors_norm(tensors, n_tensors, tensor_sq, workspace,
                                             norm_finalize_args(args), dev_result, stream),
                     "tensors_norm launch");
 }
@@ -148,14 +148,11 @@ int zero_tensors_norm_clip(const zero_tensor_t* tensors, int32_t n_tensors,
   int rc = check_norm(tensors, n_tensors, args, tensor_sq, workspace, ws_bytes, dev_result);
   if (!rc) rc = check_clip(tensors, n_tensors, args, out_scale, dev_result);
   if (rc) return rc;
-  rc = hip_status(zk::launch_tensors_norm(tensors, n_tensors, tensor_sq, workspace, true,
-                                          norm_finalize_args(args), dev_result, stream),
-                  "tensors_norm launch");
-  if (rc) return rc;
-  return hip_status(zk::launch_tensors_clip(tensors, n_tensors,
-                                            (float)(out_scale / args->loss_scale),
-                                            dev_result, stream),
-                    "tensors_clip launch");
+  return hip_status(zk::launch_tensors_norm_clip(tensors, n_tensors, tensor_sq, workspace,
+                                                 norm_finalize_args(args),
+                                                 (float)(out_scale / args->loss_scale),
+                                                 dev_result, stream),
+                    "tensors_norm_clip launch");
 }
 
 }  // extern "C"

@@ -38,6 +38,8 @@ constexpr int64_t kClipChunk = 4096;
 // Entries that fit the 4 KiB of kernel arguments beside the other arguments.
 constexpr int kNormBatch = 195;
 constexpr int kClipBatch = 139;
+// Partials of a tensor that one thread adds in turn.
+constexpr int64_t kAlone = 4;
 constexpr int kDtypeShift = 60;  // a numel's top bits hold the type(s)
 
 struct NormBatch {
@@ -329,10 +331,63 @@ __device__ __forceinline__ void clip_to(int dd, const void* src, void* dst, int6
   else clip_chunk<SD, ZERO_BF16>(src, dst, at, len, s, c);
 }
 
+// What a clip that finishes the norm by itself needs (all: tensors of the list).
+struct Finish {
+  const Partial* partials;
+  const TensorRecord* records;
+  double* tensor_sq;
+  FinalizeArgs fa;
+};
+
+// The sums of k_tensors_finalize, in its order (WIDE: <64>, else <1>), by every
+// workgroup for itself: n at most kClipThreads tensors of few partials in all.
+template <bool WIDE>
+__device__ __forceinline__ void finish_norm(const Finish& f, int32_t n, zero_step_result_t* res) {
+  __shared__ double s_x[kClipThreads];
+  __shared__ uint32_t s_bad[kClipThreads];
+  double x = 0.0;
+  uint32_t bad = 0;
+  const int32_t t = (int32_t)threadIdx.x;
+  if constexpr (WIDE) {
+    for (int32_t i = t >> 6; i < n; i += kClipThreads / 64) {
+      const TensorRecord r = f.records[i];
+      strided_sum(t & 63, 64, r.chunks, x, bad, [&](int64_t j) { return f.partials[r.first + j]; });
+      for (unsigned int d = 1; d < 64; d <<= 1) {
+        x += __longlong_as_double((long long)shfl_down_bits((uint64_t)__double_as_longlong(x), d));
+        bad |= (uint32_t)__shfl_xor((int)bad, (int)d);
+      }
+      if ((t & 63) == 0) {
+        s_x[i] = x;
+        s_bad[i] = bad;
+      }
+    }
+    __syncthreads();
+    x = t < n ? s_x[t] : 0.0;
+    bad = t < n ? s_bad[t] : 0u;
+  } else if (t < n) {
+    const TensorRecord r = f.records[t];
+    strided_sum(0, 1, r.chunks, x, bad, [&](int64_t j) { return f.partials[r.first + j]; });
+  }
+  if (blockIdx.x == 0 && t < n && f.tensor_sq)
+    f.tensor_sq[t] = (x * f.fa.inv64) * f.fa.inv64;
+  block_tree<kClipThreads>(x, bad);
+  if (t == 0) finalize_bf16_into(x, bad, f.fa, res);
+}
+
+enum { kClipAlone, kClipFinish, kClipFinishWide };
+template <int MODE>
 __global__ __launch_bounds__(kClipThreads) void k_tensors_clip(
-    ClipBatch cb, int32_t n, uint32_t last, float s, const zero_step_result_t* __restrict__ res) {
-  if (res->skip) return;
-  const float c = res->clip_coef;
+    ClipBatch cb, int32_t n, uint32_t last, float s, Finish f,
+    zero_step_result_t* __restrict__ res) {
+  __shared__ zero_step_result_t s_res;
+  if constexpr (MODE != kClipAlone) {
+    finish_norm<MODE == kClipFinishWide>(f, n, &s_res);
+    __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *res = s_res;
+  }
+  const zero_step_result_t* got = MODE == kClipAlone ? res : &s_res;
+  if (got->skip) return;
+  const float c = got->clip_coef;
   const uint32_t b = last - blockIdx.x;
   const int i = find_tensor(cb.first, n, b);
   const int64_t numel = (int64_t)(cb.numel[i] & ((1ull << kDtypeShift) - 1));
@@ -349,11 +404,13 @@ __global__ __launch_bounds__(kClipThreads) void k_tensors_clip(
 
 }  // namespace
 
-// Workspace: ticket | records [n] | sums [n] | partials [chunks].
-int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_sq,
-                        void* workspace, bool clip, const FinalizeArgs& fa,
-                        zero_step_result_t* res, hipStream_t stream) {
-  const TensorLayout l = tensor_layout(tensors, n);
+namespace {
+
+// Workspace: ticket | records [n] | sums [n] | partials [chunks].  clip: a clip
+// of the list follows; finish: and that clip finalizes.
+int norm_launches(const zero_tensor_t* tensors, int32_t n, const TensorLayout& l,
+                  double* tensor_sq, void* workspace, bool clip, bool finish,
+                  const FinalizeArgs& fa, zero_step_result_t* res, hipStream_t stream) {
   const int64_t chunk = kTensorChunk << l.shift;
   uint32_t* ticket = (uint32_t*)workspace;
   TensorRecord* records = (TensorRecord*)((char*)workspace + kTicketBytes);
@@ -382,7 +439,7 @@ int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_
   const int32_t batch = launches ? (n + launches - 1) / launches : 1;
   // The last launch's last workgroup can finish a list of few short tensors,
   // where launches are what costs; the first has set its ticket.
-  const bool fused = launches > 1 && n <= 4 * kNormThreads && l.longest <= 4;
+  const bool fused = launches > 1 && n <= 4 * kNormThreads && l.longest <= kAlone;
   for (int32_t t0 = 0; t0 < n; t0 += batch) {
     const int32_t m = n - t0 < batch ? n - t0 : batch;
     NormBatch nb;
@@ -402,15 +459,15 @@ int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_
     if (e != hipSuccess) return (int)e;
     chunk0 += blocks;
   }
-  if (fused) return (int)hipSuccess;
+  if (fused || finish) return (int)hipSuccess;
   auto finalize = [&](auto kernel, int group, int threads) {
     const int64_t blocks = ((int64_t)n * group + threads - 1) / threads;
     hipLaunchKernelGGL(kernel, dim3(blocks > 0 ? (uint32_t)blocks : 1u), dim3(threads), 0, stream,
                        partials, records, sums, n, tensor_sq, ticket, fa, res);
   };
-  // a thread takes up to 4 partials in turn, a wave 32 a lane; 290 one-chunk
+  // a thread takes up to kAlone partials in turn, a wave 32 a lane; 290 one-chunk
   // tensors take 5 us by threads, 12 us by workgroups (and their ticket)
-  if (l.longest <= 4) finalize(k_tensors_finalize<1>, 1, kNormThreads);
+  if (l.longest <= kAlone) finalize(k_tensors_finalize<1>, 1, kNormThreads);
   else if (l.longest <= 2048) finalize(k_tensors_finalize<64>, 64, kNormThreads);
   else finalize(k_tensors_finalize<1024>, 1024, 1024);
   return (int)hipGetLastError();
@@ -418,8 +475,11 @@ int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_
 
 // The list is gone through backwards: what the norm has read last may still
 // lie in the last-level cache.
-int launch_tensors_clip(const zero_tensor_t* tensors, int32_t n, float scale,
-                        const zero_step_result_t* res, hipStream_t stream) {
+int clip_launches(const zero_tensor_t* tensors, int32_t n, float scale, int mode, const Finish& f,
+                  zero_step_result_t* res, hipStream_t stream) {
+  const auto kernel = mode == kClipAlone    ? k_tensors_clip<kClipAlone>
+                      : mode == kClipFinish ? k_tensors_clip<kClipFinish>
+                                            : k_tensors_clip<kClipFinishWide>;
   constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // of one launch: 2^31 threads
   const int32_t launches = (n + kClipBatch - 1) / kClipBatch;
   const int32_t batch = launches ? (n + launches - 1) / launches : 1;
@@ -444,8 +504,8 @@ int launch_tensors_clip(const zero_tensor_t* tensors, int32_t n, float scale,
       first += (uint32_t)((t.numel + kClipChunk - 1) / kClipChunk);
     }
     for (int64_t b1 = blocks; b1 > 0; b1 -= kMaxBlocks) {
-      hipLaunchKernelGGL(k_tensors_clip, dim3((uint32_t)(b1 < kMaxBlocks ? b1 : kMaxBlocks)),
-                         dim3(kClipThreads), 0, stream, cb, t1 - t0, (uint32_t)(b1 - 1), scale,
+      hipLaunchKernelGGL(kernel, dim3((uint32_t)(b1 < kMaxBlocks ? b1 : kMaxBlocks)),
+                         dim3(kClipThreads), 0, stream, cb, t1 - t0, (uint32_t)(b1 - 1), scale, f,
                          res);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return (int)e;
@@ -453,6 +513,42 @@ int launch_tensors_clip(const zero_tensor_t* tensors, int32_t n, float scale,
     t1 = t0;
   }
   return (int)hipSuccess;
+}
+
+}  // namespace
+
+int launch_tensors_norm(const zero_tensor_t* tensors, int32_t n, double* tensor_sq,
+                        void* workspace, const FinalizeArgs& fa, zero_step_result_t* res,
+                        hipStream_t stream) {
+  return norm_launches(tensors, n, tensor_layout(tensors, n), tensor_sq, workspace, false, false,
+                       fa, res, stream);
+}
+
+int launch_tensors_clip(const zero_tensor_t* tensors, int32_t n, float scale,
+                        const zero_step_result_t* res, hipStream_t stream) {
+  return clip_launches(tensors, n, scale, kClipAlone, Finish{}, (zero_step_result_t*)res, stream);
+}
+
+// A small list's clip, of one launch, finishes the norm itself: a launch less
+// costs more there than every workgroup's few loads (3 tensors, 1.0 M elements:
+// 15.7 -> 11.8 us a call).
+int launch_tensors_norm_clip(const zero_tensor_t* tensors, int32_t n, double* tensor_sq,
+                             void* workspace, const FinalizeArgs& fa, float scale,
+                             zero_step_result_t* res, hipStream_t stream) {
+  const TensorLayout l = tensor_layout(tensors, n);
+  constexpr int64_t kFinishChunks = 256;
+  bool any = false;
+  for (int32_t i = 0; i < n && !any; ++i) any = tensors[i].numel > 0;
+  const bool finish = any && n <= kClipBatch && l.chunks <= kFinishChunks;
+  static_assert(kClipBatch <= kClipThreads, "a thread for every tensor");
+  const int e = norm_launches(tensors, n, l, tensor_sq, workspace, true, finish, fa, res, stream);
+  if (e) return e;
+  if (!finish)
+    return clip_launches(tensors, n, scale, kClipAlone, Finish{}, res, stream);
+  const TensorRecord* records = (const TensorRecord*)((char*)workspace + kTicketBytes);
+  const Finish f{(const Partial*)(records + n) + n, records, tensor_sq, fa};
+  return clip_launches(tensors, n, scale, l.longest <= kAlone ? kClipFinish : kClipFinishWide, f,
+                       res, stream);
 }
 
 }  // namespace zk
