@@ -750,7 +750,8 @@ size_t zero_head_workspace_bytes(const zero_head_t* head, int32_t grad);
  *   workspace   device, >= zero_head_workspace_bytes(head, 0), 256-byte
  *               aligned; its content on entry does not matter
  *   dev_result  device, 8-byte aligned; fully written
- * Logits and sums are fp32.  Equal inputs give equal bits.
+ * Logits and sums are fp32 (up to 64 tokens, the label's logit is fp64).  Equal
+ * inputs give equal bits.
  * Errors: ZERO_EINVAL (sizes, strides, dtype, loss_scale, NULL pointers),
  * ZERO_EALIGN, ZERO_ENOSPC (workspace), ZERO_EHIP.  Nothing is launched if a
  * check fails.

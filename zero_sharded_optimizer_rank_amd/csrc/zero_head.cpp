@@ -132,7 +132,7 @@ HeadPlan head_plan(const zero_head_t* h, bool grad) {
   p.label = take(4 * p.tokens_pad);
   p.lse = take(4 * p.tokens_pad);
   p.dy = take(4 * p.tokens_pad);
-  p.picked = take(4 * p.tokens_pad);
+  p.picked = take(8 * p.tokens_pad);
   p.x = take(p.few ? 0 : 2 * p.tokens_pad * p.hidden_pad);
   p.xt = take(grad && p.few ? 2 * p.tokens_pad * p.hidden_pad : 0);
   p.w = take(p.pack_w ? 2 * h->vocab * p.hidden_pad : 0);

@@ -180,7 +180,7 @@ template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, const uint16_t* __restrict__ x,
     int32_t hidden_pad, int32_t K, int32_t tokens_pad, const int32_t* __restrict__ label,
-    const HeadState* __restrict__ state, float2* __restrict__ part, float* __restrict__ picked,
+    const HeadState* __restrict__ state, float2* __restrict__ part, double* __restrict__ picked,
     int64_t kept, int32_t piece, uint16_t* __restrict__ g) {
   using L = LogitTile<T>;
   using G = typename L::G;
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
 // tokens x 1002 partials 20 us, 37 x 393 7 us.
 __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
     const float2* __restrict__ part, int32_t parts, int32_t tokens_pad,
-    const float* __restrict__ picked, const int32_t* __restrict__ index, float* __restrict__ lse,
+    const double* __restrict__ picked, const int32_t* __restrict__ index, float* __restrict__ lse,
     float* __restrict__ dy, float* __restrict__ token_loss, float* __restrict__ lse_out,
     double* __restrict__ sums, double scale, int32_t mean, HeadState* __restrict__ state,
     zero_loss_result_t* __restrict__ res) {
@@ -624,7 +624,7 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
                        dim3(kGemmThreads), 0, stream, w.w, w.ld, (int32_t)h->vocab,
                        at<const uint16_t>(ws, p.x), (int32_t)p.hidden_pad, w.K,
                        (int32_t)p.tokens_pad, at<const int32_t>(ws, p.label), state,
-                       at<float2>(ws, p.part), at<float>(ws, p.picked), p.kept,
+                       at<float2>(ws, p.part), at<double>(ws, p.picked), p.kept,
                        (int32_t)p.piece, keep ? at<uint16_t>(ws, p.g) : nullptr);
     ZK_LAUNCHED();
   }
@@ -633,7 +633,7 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
                      dim3(64 * kJoinWaves), 0, stream, at<const float2>(ws, p.part),
                      (int32_t)((h->vocab + tile - 1) / tile * tile / kHeadPart),
                      (int32_t)p.tokens_pad,
-                     at<const float>(ws, p.picked), at<const int32_t>(ws, p.index),
+                     at<const double>(ws, p.picked), at<const int32_t>(ws, p.index),
                      at<float>(ws, p.lse), at<float>(ws, p.dy), token_loss, lse,
                      at<double>(ws, p.sums), 1.0 / (double)g_scale<T>(), h->mean, state, res);
   return (int)hipGetLastError();

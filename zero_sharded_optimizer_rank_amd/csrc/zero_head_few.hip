@@ -54,7 +54,6 @@ struct FewLogits {
   int64_t ldx, ldw, lddx;
   double loss_scale;
   int32_t tokens, vocab, hidden, hidden_pad, mean;
-  int32_t packs;          // workgroups that take pack() instead of logits
   const float* lse_in;    // or NULL
   float *token_loss, *lse_out;  // or NULL
   uint16_t *xt, *dx;      // NULL: no gradients
@@ -63,7 +62,8 @@ struct FewLogits {
   float* lse;
   HeadState* state;
   float2* part;
-  float *picked, *logits; // logits: NULL if no gradients follow
+  double* picked;
+  float* logits;          // NULL if no gradients follow
 };
 
 // The valid tokens in order: lane i of `ok` takes place popcount(ok below i).
@@ -71,15 +71,20 @@ __device__ __forceinline__ int32_t place(uint64_t ok, int lane) {
   return __popcll(ok & ((1ull << lane) - 1));
 }
 
-// Workgroup b of f.packs: what every token that takes no part gets, x's
-// transpose for the gradients (column r: the r-th valid token, zero past the
-// last), and, b = 0, the packed tokens' indices and labels.
+// Workgroups of a launch that take pack() instead of logits.
+constexpr int32_t kPacks = kT;
+
+// Workgroup r of kPacks: what token r gets if it takes no part; of the r-th
+// valid token the label's logit, in fp64 (its rounding to fp32 would be the
+// largest error of a short prompt's loss), and x's transpose for the gradients
+// (column r, zero past the last); r = 0, the packed tokens' indices and labels.
+template <typename T>
 __device__ __forceinline__ void pack(const FewLogits& f) {
   const int lane = threadIdx.x & 63;
   const int64_t y = lane < f.tokens ? f.labels[lane] : -1;
   const uint64_t ok = __ballot(y >= 0 && y < f.vocab), bad = __ballot(y >= f.vocab);
-  const int32_t valid = __popcll(ok);
-  if (blockIdx.x == 0 && threadIdx.x < 64) {
+  const int32_t valid = __popcll(ok), r = (int32_t)blockIdx.x;
+  if (r == 0 && threadIdx.x < 64) {
     if (ok >> lane & 1) {
       const int32_t at = place(ok, lane);
       f.index[at] = lane;
@@ -95,28 +100,39 @@ __device__ __forceinline__ void pack(const FewLogits& f) {
       f.state->coef = bad ? __builtin_nanf("") : (float)c;
     }
   }
-  for (int32_t r = blockIdx.x; r < kT; r += f.packs) {
-    if (r < f.tokens && !(ok >> r & 1)) {
-      if (threadIdx.x == 0) {
-        const float v = bad >> r & 1 ? __builtin_nanf("") : 0.0f;
-        if (f.token_loss) f.token_loss[r] = v;
-        if (f.lse_out) f.lse_out[r] = v;
-      }
-      if (f.dx)
-        for (int32_t h = threadIdx.x; h < f.hidden; h += kThreads4) f.dx[r * f.lddx + h] = 0;
+  if (r < f.tokens && !(ok >> r & 1)) {
+    if (threadIdx.x == 0) {
+      const float v = bad >> r & 1 ? __builtin_nanf("") : 0.0f;
+      if (f.token_loss) f.token_loss[r] = v;
+      if (f.lse_out) f.lse_out[r] = v;
     }
-    if (!f.xt) continue;
-    int32_t src = -1;  // the r-th valid token
-    uint64_t m = ok;
-    for (int32_t i = 0; m; ++i, m &= m - 1)
-      if (i == r) src = __ffsll((unsigned long long)m) - 1;
-    for (int32_t c = threadIdx.x; c < f.hidden_pad / 8; c += kThreads4) {
-      s16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (src >= 0) v = row8(f.x + src * f.ldx, 8 * c, f.hidden);
+    if (f.dx)
+      for (int32_t h = threadIdx.x; h < f.hidden; h += kThreads4) f.dx[r * f.lddx + h] = 0;
+  }
+  if (r >= valid && !f.xt) return;
+  int32_t src = -1;  // the r-th valid token
+  uint64_t m = ok;
+  for (int32_t i = 0; m; ++i, m &= m - 1)
+    if (i == r) src = __ffsll((unsigned long long)m) - 1;
+  const uint16_t* w = f.w + (src >= 0 ? __shfl(y, src) : 0) * f.ldw;
+  double dot = 0.0;
+  for (int32_t c = threadIdx.x; c < f.hidden_pad / 8; c += kThreads4) {
+    s16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (src >= 0) {
+      v = row8(f.x + src * f.ldx, 8 * c, f.hidden);
+      const s16x8 u = row8(w, 8 * c, f.hidden);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        dot = __builtin_fma((double)widen<T>((uint16_t)v[e]), (double)widen<T>((uint16_t)u[e]),
+                            dot);
+    }
+    if (f.xt)
 #pragma unroll
       for (int e = 0; e < 8; ++e) f.xt[(int64_t)(8 * c + e) * kT + r] = (uint16_t)v[e];
-    }
   }
+  uint32_t none = 0;
+  block_tree<kThreads4>(dot, none);
+  if (threadIdx.x == 0 && r < valid) f.picked[r] = dot;
 }
 
 // Logits of 128 vocabulary rows, 32 a wave: A = w from memory straight into
@@ -147,8 +163,8 @@ k_few_logits(const FewLogits f) {
   // [tokens][128 columns]: 16-byte chunk c of row r lies at c ^ (r & 15)
   __shared__ __attribute__((aligned(1024))) char lx[2][kTokens * kXTile * 2];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, q = lane & 15;
-  if ((int32_t)blockIdx.x < f.packs) return pack(f);
-  const int32_t vocab = f.vocab, hidden = f.hidden, block = (int32_t)blockIdx.x - f.packs;
+  if ((int32_t)blockIdx.x < kPacks) return pack<T>(f);
+  const int32_t vocab = f.vocab, hidden = f.hidden, block = (int32_t)blockIdx.x - kPacks;
   const int64_t v0 = (int64_t)block * kHeadPart + wave * 32;
   // A load covers 8 rows' whole 128-byte lines: lanes of q < 8 take the first
   // half of row q % 8's, the others the second.  The fragments want lane q to
@@ -322,10 +338,7 @@ k_few_logits(const FewLogits f) {
         float l = acc[i][j][e];
         if (r >= rows) l = -INFINITY;
         if (f.logits && r < rows) f.logits[(v0 + r) * kT + t] = l;
-        if (r == y) {
-          f.picked[t] = l;
-          l = -INFINITY;
-        }
+        if (r == y) l = -INFINITY;  // pack() has it
         acc[i][j][e] = l;
         m = __builtin_elementwise_maximum(m, l);
       }
@@ -385,7 +398,8 @@ struct FewGrad {
   int64_t ldw;
   const uint16_t* xt;
   const int32_t* label;
-  const float *lse, *dy, *picked;  // dy: e^-loss - 1, or NULL
+  const float *lse, *dy;  // dy: e^-loss - 1, or NULL
+  const double* picked;
   const HeadState* state;
   float* acc;       // dx's partial sums [split][64][hidden_pad]
   void* dw;
@@ -403,7 +417,7 @@ __device__ __forceinline__ void load_tokens(const FewGrad& f, Tokens& k) {
     const bool there = t < f.state->valid;
     const float z = there ? f.lse[t] : 0.0f;
     k.shift[t] = there ? g_log2<T>() - z * kLog2e : -INFINITY;
-    k.dy[t] = there ? (f.dy ? f.dy[t] : expm1f(f.picked[t] - z)) * g_scale<T>() : 0.0f;
+    k.dy[t] = there ? (f.dy ? f.dy[t] : expm1f((float)(f.picked[t] - (double)z))) * g_scale<T>() : 0.0f;
     k.y[t] = there ? f.label[t] : -1;
   }
   __syncthreads();
@@ -679,7 +693,6 @@ int logits_t(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse
   f.hidden = (int32_t)h->hidden;
   f.hidden_pad = (int32_t)p.hidden_pad;
   f.mean = h->mean;
-  f.packs = gr ? kT : 1;
   f.lse_in = lse_in;
   f.token_loss = token_loss;
   f.lse_out = lse;
@@ -694,7 +707,7 @@ int logits_t(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse
   f.lse = at<float>(ws, p.lse);
   f.state = at<HeadState>(ws, p.state);
   f.part = at<float2>(ws, p.part);
-  f.picked = at<float>(ws, p.picked);
+  f.picked = at<double>(ws, p.picked);
   const int columns = (int)((h->tokens + 15) / 16);
   const auto pick = [&](auto whole) {
     constexpr bool W = decltype(whole)::value;
@@ -704,7 +717,7 @@ int logits_t(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse
                           : k_few_logits<T, 4, W>;
   };
   const auto kernel = h->hidden % 8 == 0 ? pick(std::true_type{}) : pick(std::false_type{});
-  hipLaunchKernelGGL(kernel, dim3((uint32_t)(f.packs + (h->vocab + kHeadPart - 1) / kHeadPart)),
+  hipLaunchKernelGGL(kernel, dim3((uint32_t)(kPacks + (h->vocab + kHeadPart - 1) / kHeadPart)),
                      dim3(kThreads4), 0, stream, f);
   return (int)hipGetLastError();
 }
@@ -720,7 +733,7 @@ int grads_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
   f.label = at<const int32_t>(ws, p.label);
   f.lse = at<const float>(ws, p.lse);
   f.dy = have ? at<const float>(ws, p.dy) : nullptr;
-  f.picked = at<const float>(ws, p.picked);
+  f.picked = at<const double>(ws, p.picked);
   f.state = at<const HeadState>(ws, p.state);
   f.acc = at<float>(ws, p.acc);
   f.dw = gr->dw;
