@@ -47,9 +47,15 @@ __device__ __forceinline__ u32x2 narrow4(float a, float b, float c, float d) {
 template <typename T>
 __device__ __forceinline__ float second(float x) { return x - widen<T>(narrow<T>(x)); }
 
+// 16 and 8 bytes at any element's address: global loads and stores need no more
+// than element alignment on gfx950.
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+
 // Eight elements from p, of which the first n exist.
-__device__ __forceinline__ u32x4 take8(const uint16_t* p, int64_t n, bool whole16) {
-  if (whole16 && n >= 8) return *(const u32x4*)p;
+__device__ __forceinline__ u32x4 take8(const uint16_t* p, int64_t n) {
+  if (n >= 8) return *(const u32x4_a2*)p;
   u32x4 v = {0, 0, 0, 0};
 #pragma unroll
   for (int e = 0; e < 8; ++e)
@@ -57,8 +63,15 @@ __device__ __forceinline__ u32x4 take8(const uint16_t* p, int64_t n, bool whole1
   return v;
 }
 
-// Eight bytes at any element's address.
-typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+// Without its first n (1 to 7) elements; zeros follow the others.
+__device__ __forceinline__ s16x8 drop_first(s16x8 v, int n) {
+  typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+  u64x2 q = __builtin_bit_cast(u64x2, v);
+  if (n >= 4) q = u64x2{q[1], 0};
+  const int bits = 16 * (n & 3);
+  if (bits) q = u64x2{q[0] >> bits | q[1] << (64 - bits), q[1] >> bits};
+  return __builtin_bit_cast(s16x8, q);
+}
 
 // (m, s) stands for s 2^m.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {

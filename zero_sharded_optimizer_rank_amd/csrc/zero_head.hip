@@ -125,10 +125,9 @@ __global__ __launch_bounds__(kPackThreads) void k_head_pack_x(
   if (r >= (valid + kHeadTile - 1) / kHeadTile * kHeadTile) return;
   u32x4* o = (u32x4*)(out + (int64_t)r * hidden_pad);
   const uint16_t* p = r < valid ? x + (int64_t)index[r] * ldx : nullptr;
-  const bool whole16 = ((uintptr_t)p & 15) == 0;
   for (int32_t c = threadIdx.x; c < hidden_pad / 8; c += kPackThreads) {
     u32x4 v = {0, 0, 0, 0};
-    if (p) v = take8(p + 8 * c, hidden - 8 * c, whole16);
+    if (p) v = take8(p + 8 * c, hidden - 8 * c);
     o[c] = v;
   }
 }
@@ -141,9 +140,8 @@ __global__ __launch_bounds__(kPackThreads) void k_head_pack_w(
   for (int64_t v = blockIdx.x; v < vocab; v += gridDim.x) {
     u32x4* o = (u32x4*)(out + v * hidden_pad);
     const uint16_t* p = w + v * ldw;
-    const bool whole16 = ((uintptr_t)p & 15) == 0;
     for (int32_t c = threadIdx.x; c < hidden_pad / 8; c += kPackThreads)
-      o[c] = take8(p + 8 * c, hidden - 8 * c, whole16);
+      o[c] = take8(p + 8 * c, hidden - 8 * c);
   }
 }
 
@@ -570,8 +568,8 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
                     const int32_t v = c0 + col, h = h0 + row;
                     if (v >= vocab_left || h >= hidden) return;
                     uint16_t* o = out + (int64_t)v * lddw + h;
-                    if (h + 8 <= hidden && ((uintptr_t)o & 15) == 0) {
-                      *(u32x4*)o = d;
+                    if (h + 8 <= hidden) {
+                      *(u32x4_a2*)o = d;
                     } else {
 #pragma unroll
                       for (int e = 0; e < 8; ++e)
@@ -592,9 +590,9 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
       f32x4 d = acc[i][j] * c;
       if constexpr (F32OUT) {
         float* o = (float*)dw + at;
-        if (h + 4 <= hidden && ((uintptr_t)o & 15) == 0) {
-          if (accumulate) d = *(const f32x4*)o + d;
-          *(f32x4*)o = d;
+        if (h + 4 <= hidden) {
+          if (accumulate) d = *(const f32x4_a4*)o + d;
+          *(f32x4_a4*)o = d;
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -602,9 +600,15 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
         }
       } else {
         uint16_t* o = (uint16_t*)dw + at;
+        if (h + 4 <= hidden) {
+          const u32x2 q = *(const u32x2_a2*)o;
+          *(u32x2_a2*)o = narrow4<T>(widen<T>(q[0] & 0xFFFFu) + d[0], widen<T>(q[0] >> 16) + d[1],
+                                     widen<T>(q[1] & 0xFFFFu) + d[2], widen<T>(q[1] >> 16) + d[3]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (h + e < hidden) o[e] = (uint16_t)narrow<T>(widen<T>(o[e]) + d[e]);
+          for (int e = 0; e < 4; ++e)
+            if (h + e < hidden) o[e] = (uint16_t)narrow<T>(widen<T>(o[e]) + d[e]);
+        }
       }
     }
   }

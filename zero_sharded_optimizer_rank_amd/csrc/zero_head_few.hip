@@ -32,9 +32,6 @@ using namespace dev;
 constexpr int kThreads4 = 256;  // four waves
 constexpr int kT = kFewTokens;  // 64
 
-// 16 bytes at any element's address.
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-
 // Elements [k, k + 8) of a row of n elements; those past its end are zero.
 __device__ __forceinline__ s16x8 row8(const uint16_t* row, int32_t k, int32_t n) {
   u32x4 v = {0, 0, 0, 0};
@@ -148,13 +145,13 @@ __device__ __forceinline__ void pack(const FewLogits& f) {
 // too (206).  Only as many 16-token columns as there may be tokens are
 // multiplied (37 tokens, 50257 x 1600: 38 -> 35 us).
 //
-// WHOLE: rows are whole 16-byte pieces (hidden % 8 == 0).  A piece past the
-// row's end is then loaded from its start and taken out later, without a branch
-// around any load: with branches the compiler waits for the newest loads where
-// they join (37 tokens, 50257 x 1600: 37.4 against 34.8 us; dx of 50 tokens,
-// 1000 x 72, 10.2 against 6.4).
+// LONG: rows of eight elements or more.  A piece that passes the row's end is
+// then loaded from the row's last eight elements, and what does not belong to
+// it is taken out later, without a branch around any load: with branches the
+// compiler waits for the newest loads where they join (37 tokens, 50257 x 1600:
+// 37.4 against 34.8 us; dx of 50 tokens, 1000 x 72, 10.2 against 6.4).
 constexpr int kXTile = 128;
-template <typename T, int NJ, bool WHOLE>
+template <typename T, int NJ, bool LONG>
 __global__ __launch_bounds__(kThreads4) __attribute__((amdgpu_waves_per_eu(2, 2))) void
 k_few_logits(const FewLogits f) {
   constexpr int kTokens = 16 * NJ;
@@ -165,6 +162,7 @@ k_few_logits(const FewLogits f) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, q = lane & 15;
   if ((int32_t)blockIdx.x < kPacks) return pack<T>(f);
   const int32_t vocab = f.vocab, hidden = f.hidden, block = (int32_t)blockIdx.x - kPacks;
+  const int beyond = (8 - hidden % 8) % 8;
   const int64_t v0 = (int64_t)block * kHeadPart + wave * 32;
   // A load covers 8 rows' whole 128-byte lines: lanes of q < 8 take the first
   // half of row q % 8's, the others the second.  The fragments want lane q to
@@ -183,18 +181,25 @@ k_few_logits(const FewLogits f) {
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{};
+  // LONG: where to load the piece at column k from, and the piece that the row
+  // holds (beyond: the columns of the row's end that lie past it)
+  auto inside = [&](int32_t k) { return k + 8 <= hidden ? k : hidden - 8; };
+  auto held = [&](s16x8 v, int32_t k) {
+    if (k >= hidden) return s16x8{};
+    return k + 8 > hidden ? drop_first(v, beyond) : v;
+  };
   // a[buffer][i][line][rows 0-7 or 8-15]
   s16x8 a[2][2][2][2], xr[NJ];
   auto fetch_w = [&](s16x8 (&d)[2][2][2], int32_t tile) {
     const int32_t k0 = tile * kXTile + wk;
-    if constexpr (WHOLE) {
+    if constexpr (LONG) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int l = 0; l < 2; ++l) {
-            const int32_t k = k0 + 64 * l < hidden ? k0 + 64 * l : 0;  // use() takes these out
+            const int32_t k = inside(k0 + 64 * l);
             d[i][l][r] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(wr[i][r] + k));
           }
     } else if ((tile + 1) * kXTile <= hidden) {
@@ -236,10 +241,10 @@ k_few_logits(const FewLogits f) {
   const uint16_t* xp[NJ];
   auto fetch_x = [&](int32_t tile) {
     const int32_t c = tile * kXTile + 8 * xc;
-    if constexpr (WHOLE) {
+    if constexpr (LONG) {
 #pragma unroll
       for (int k = 0; k < NJ; ++k)
-        xr[k] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(xp[k] + (c < hidden ? c : 0)));
+        xr[k] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(xp[k] + inside(c)));
     } else if ((tile + 1) * kXTile <= hidden) {
 #pragma unroll
       for (int k = 0; k < NJ; ++k) xr[k] = __builtin_bit_cast(s16x8, *(const u32x4_a2*)(xp[k] + c));
@@ -249,20 +254,23 @@ k_few_logits(const FewLogits f) {
     }
   };
   auto store_x = [&](char* d, int32_t tile) {
-    const bool in = !WHOLE || tile * kXTile + 8 * xc < hidden;
+    if (LONG && (tile + 1) * kXTile > hidden) {
+#pragma unroll
+      for (int k = 0; k < NJ; ++k) xr[k] = held(xr[k], tile * kXTile + 8 * xc);
+    }
 #pragma unroll
     for (int k = 0; k < NJ; ++k)
-      *(s16x8*)(d + (xrow + 16 * k) * 256 + ((xc ^ xrow) << 4)) = in ? xr[k] : s16x8{};
+      *(s16x8*)(d + (xrow + 16 * k) * 256 + ((xc ^ xrow) << 4)) = xr[k];
   };
   auto use = [&](s16x8 (&d)[2][2][2], const char* l, int32_t tile) {
-    if (WHOLE && (tile + 1) * kXTile > hidden) {
+    if (LONG && (tile + 1) * kXTile > hidden) {
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            if (tile * kXTile + wk + 64 * n >= hidden) d[i][n][r] = s16x8{};
+            d[i][n][r] = held(d[i][n][r], tile * kXTile + wk + 64 * n);
     }
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
@@ -417,7 +425,9 @@ __device__ __forceinline__ void load_tokens(const FewGrad& f, Tokens& k) {
     const bool there = t < f.state->valid;
     const float z = there ? f.lse[t] : 0.0f;
     k.shift[t] = there ? g_log2<T>() - z * kLog2e : -INFINITY;
-    k.dy[t] = there ? (f.dy ? f.dy[t] : expm1f((float)(f.picked[t] - (double)z))) * g_scale<T>() : 0.0f;
+    const float dy =
+        there ? (f.dy ? f.dy[t] : expm1f((float)(f.picked[t] - (double)z))) : 0.0f;
+    k.dy[t] = dy * g_scale<T>();
     k.y[t] = there ? f.label[t] : -1;
   }
   __syncthreads();
@@ -512,20 +522,27 @@ __device__ __forceinline__ void few_dw(const FewGrad& f, const Tokens& tok, char
         const int32_t v = v0 + 16 * j + q;
         if (v >= f.vocab) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int32_t h = h0 + 16 * i + 4 * g + e;
-            if (h >= f.hidden) continue;
-            const int64_t at = (int64_t)v * f.lddw + h;
-            if constexpr (F32OUT) {
-              float* o = (float*)f.dw + at;
-              *o = f.accumulate ? *o + acc[i][j][e] : acc[i][j][e];
+        for (int i = 0; i < 4; ++i) {
+          const int32_t h = h0 + 16 * i + 4 * g;
+          const int64_t at = (int64_t)v * f.lddw + h;
+          f32x4 d = acc[i][j];
+          if constexpr (F32OUT) {
+            float* o = (float*)f.dw + at;
+            if (h + 4 <= f.hidden) {
+              if (f.accumulate) d = *(const f32x4_a4*)o + d;
+              *(f32x4_a4*)o = d;
             } else {
-              uint16_t* o = (uint16_t*)f.dw + at;
-              *o = (uint16_t)narrow<T>(widen<T>(*o) + acc[i][j][e]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (h + e < f.hidden) o[e] = f.accumulate ? o[e] + d[e] : d[e];
             }
+          } else {
+            uint16_t* o = (uint16_t*)f.dw + at;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (h + e < f.hidden) o[e] = (uint16_t)narrow<T>(widen<T>(o[e]) + d[e]);
           }
+        }
       }
     }
   }
@@ -535,7 +552,7 @@ __device__ __forceinline__ void few_dw(const FewGrad& f, const Tokens& tok, char
 // rows at a time: A = w (columns of memory, staged in LDS), B = g, which the
 // workgroup forms in LDS from the logits.  The next rows of w and of the
 // logits are on their way while these are multiplied.
-template <typename T, bool WHOLE>
+template <typename T, bool LONG>
 __device__ __forceinline__ void few_dx(const FewGrad& f, const Tokens& tok, char* lds,
                                        int32_t block) {
   using FA = Frags<256, true>;
@@ -557,11 +574,13 @@ __device__ __forceinline__ void few_dx(const FewGrad& f, const Tokens& tok, char
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
   s16x8 nw[8];
   float nl[16];
+  const int32_t column = h0 + (lane & 31) * 8;
+  const int beyond = (8 - f.hidden % 8) % 8;  // of a row's last piece
   auto fetch = [&](int32_t v0) {  // w: rows 8k + wave*2 + lane/32
     const uint16_t* p = f.w + (v0 + wave * 2 + (lane >> 5)) * f.ldw + h0;
     const float* l = f.logits + (int64_t)(v0 + wave * 16) * kT + lane;
-    if constexpr (WHOLE) {
-      const int32_t c = h0 + (lane & 31) * 8 < f.hidden ? h0 + (lane & 31) * 8 : 0;
+    if constexpr (LONG) {
+      const int32_t c = column + 8 <= f.hidden ? column : f.hidden - 8;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int32_t v = v0 + 8 * k + wave * 2 + (lane >> 5);
@@ -597,6 +616,9 @@ __device__ __forceinline__ void few_dx(const FewGrad& f, const Tokens& tok, char
     for (int k = 0; k < 8; ++k) {
       const int r = 8 * k + wave * 2 + (lane >> 5);
       const int c = (lane & 31) ^ ((r & 3) << 2 | (r >> 3 & 1) << 1);
+      // what columns past the row's end hold reaches no column of dx
+      if (LONG && beyond && column < f.hidden && column + 8 > f.hidden)
+        nw[k] = drop_first(nw[k], beyond);
       *(__attribute__((address_space(3))) s16x8*)(lw + r * 512 + c * 16) = nw[k];
     }
 #pragma unroll
@@ -641,12 +663,12 @@ __device__ __forceinline__ void few_dx(const FewGrad& f, const Tokens& tok, char
 
 // Workgroups of dx first: they run longest.  Bound by memory: 64 tokens, 128256 x
 // 4096, 415 us (w read, dw written: 5.1 TB/s).
-template <typename T, bool F32OUT, bool WHOLE>
+template <typename T, bool F32OUT, bool LONG>
 __global__ __launch_bounds__(kThreads4) void k_few_grads(FewGrad f, int32_t dx_blocks) {
   __shared__ __attribute__((aligned(1024))) char lds[49152];
   __shared__ Tokens tok;
   load_tokens<T>(f, tok);
-  if ((int32_t)blockIdx.x < dx_blocks) few_dx<T, WHOLE>(f, tok, lds, blockIdx.x);
+  if ((int32_t)blockIdx.x < dx_blocks) few_dx<T, LONG>(f, tok, lds, blockIdx.x);
   else few_dw<T, F32OUT>(f, tok, lds, blockIdx.x - dx_blocks);
 }
 
@@ -716,7 +738,7 @@ int logits_t(const zero_head_t* h, const HeadPlan& p, void* ws, const float* lse
            : columns == 3 ? k_few_logits<T, 3, W>
                           : k_few_logits<T, 4, W>;
   };
-  const auto kernel = h->hidden % 8 == 0 ? pick(std::true_type{}) : pick(std::false_type{});
+  const auto kernel = h->hidden >= 8 ? pick(std::true_type{}) : pick(std::false_type{});
   hipLaunchKernelGGL(kernel, dim3((uint32_t)(kPacks + (h->vocab + kHeadPart - 1) / kHeadPart)),
                      dim3(kThreads4), 0, stream, f);
   return (int)hipGetLastError();
@@ -752,7 +774,7 @@ int grads_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
   f.run = (int32_t)(((h->vocab + p.split - 1) / p.split + kStage - 1) / kStage * kStage);
   const int32_t dx_blocks = h->tokens > 0 ? htiles * f.split : 0;
   const bool f32 = gr->dw_dtype == ZERO_F32;
-  const auto kernel = h->hidden % 8 == 0
+  const auto kernel = h->hidden >= 8
                           ? (f32 ? k_few_grads<T, true, true> : k_few_grads<T, false, true>)
                           : (f32 ? k_few_grads<T, true, false> : k_few_grads<T, false, false>);
   hipLaunchKernelGGL(kernel, dim3((uint32_t)(dx_blocks + f.dw_blocks)), dim3(kThreads4), 0, stream,
