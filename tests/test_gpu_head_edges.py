@@ -294,3 +294,22 @@ def test_workspace_grows_on_another_stream():
     torch.cuda.synchronize()
     assert h.ws.numel() > small
     _all(r, ref)
+
+
+@pytest.mark.parametrize("V", [50, 2 ** 21 + 1])
+def test_empty_batch(V):
+    """No tokens at all, on both sides of the length where few tokens leave their own form."""
+    H, dtype = 8, torch.bfloat16
+    w = torch.ones(V, H, dtype=dtype, device="cuda")
+    x = torch.empty(0, H, dtype=dtype, device="cuda")
+    y = torch.empty(0, dtype=torch.int64, device="cuda")
+    h = _head(0, V, H, dtype)
+    r = h.loss(x, w, y)
+    assert r.loss.item() == 0.0 and r.valid.item() == 0 and r.bad.item() == 0
+    r = h.loss_grad(x, w, y)
+    assert r.loss.item() == 0.0 and (r.dw == 0).all()
+    r.dw.fill_(3.0)
+    h.loss_grad(x, w, y, dw=r.dw, accumulate=True)
+    assert (r.dw == 3.0).all()
+    _, dw = h.grad(x, w, y, torch.empty(0, device="cuda"))
+    assert (dw == 0).all()

@@ -150,3 +150,12 @@ def test_tiles_of_one_launch():
         assert e.value.code == abi.ZERO_EINVAL
     assert abi.zero_head_workspace_bytes(
         _head(vocab=1 << 30, tokens=65, hidden=8, ldx=8, ldw=8), False) > 0
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("vocab", [100, 1 << 21, (1 << 21) + 1, 1 << 30])
+def test_workspace_of_an_empty_batch(grad, vocab):
+    """No token needs the room of one: the join writes its sum whatever the count."""
+    need = [abi.zero_head_workspace_bytes(_head(tokens=t, hidden=8, vocab=vocab, ldx=8, ldw=8),
+                                          grad) for t in (0, 1)]
+    assert need[0] == need[1] > 0

@@ -97,7 +97,8 @@ HeadPlan head_plan(const zero_head_t* h, bool grad) {
   HeadPlan p{};
   p.hidden_pad = up(h->hidden, kHeadStep);
   p.few = h->tokens <= kFewTokens && h->vocab <= kFewVocab;
-  p.tokens_pad = p.few ? kFewTokens : up(h->tokens, kHeadTile);
+  // an empty batch has its join, and its dw to clear: a tile's room at least
+  p.tokens_pad = p.few ? kFewTokens : up(h->tokens > 0 ? h->tokens : 1, kHeadTile);
   p.pack_w = !p.few && (h->hidden % 8 != 0 || h->ldw % 8 != 0 || !aligned(h->w, 16));
   const int64_t vocab_pad = up(h->vocab, kHeadTile);
   p.parts = vocab_pad / kHeadPart;
