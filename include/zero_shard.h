@@ -738,9 +738,9 @@ typedef struct zero_loss_result {
   int64_t bad;       /* tokens with label >= vocab */
 } zero_loss_result_t;
 
-/* Bytes of workspace for the calls below; grad: nonzero for the calls that
- * form gradients.  0 for a bad head.  Depends on sizes, types, strides and the
- * alignment of w. */
+/* Bytes of workspace for the calls below with up to head->tokens tokens; grad:
+ * nonzero for the calls that form gradients.  0 for a bad head.  Depends on
+ * sizes, types, strides and the alignment of w. */
 size_t zero_head_workspace_bytes(const zero_head_t* head, int32_t grad);
 
 /*

@@ -313,3 +313,19 @@ def test_empty_batch(V):
     assert (r.dw == 3.0).all()
     _, dw = h.grad(x, w, y, torch.empty(0, device="cuda"))
     assert (dw == 0).all()
+
+
+@pytest.mark.parametrize("T,fewer,V,H", [
+    (4608, (4352, 4096, 4097, 64), 128256, 64),  # g's piece: one to 4096 tokens, then two
+    (2048, (1792, 1), 32000, 8192),              # dx's splits: 1024 tiles, 896 twice over
+])
+def test_smaller_batches_of_a_large_head(T, fewer, V, H):
+    """Counts whose room for g or for dx's sums is larger than that of more tokens."""
+    dtype = torch.bfloat16
+    h = _head(T, V, H, dtype)
+    for t in (T,) + fewer:
+        x, w, y = _inputs(t, V, H, dtype, seed=t)
+        ref = reference(x, w, y)
+        _all(h.loss_grad(x, w, y), ref)
+        del ref
+        torch.cuda.empty_cache()

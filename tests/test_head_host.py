@@ -159,3 +159,42 @@ def test_workspace_of_an_empty_batch(grad, vocab):
     need = [abi.zero_head_workspace_bytes(_head(tokens=t, hidden=8, vocab=vocab, ldx=8, ldw=8),
                                           grad) for t in (0, 1)]
     assert need[0] == need[1] > 0
+
+
+SHAPES = [(4096, 128256), (1600, 50257), (8192, 32000), (3, 39070), (72, 9001), (64, 700),
+          (8, (1 << 21) + 1)]
+
+
+@pytest.mark.parametrize("hidden,vocab", SHAPES)
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("w", [W, W + 2])
+def test_workspace_holds_every_smaller_batch(hidden, vocab, grad, w):
+    """A head for T tokens takes batches of 0 to T: the plan changes at 64 tokens and by
+    the tile of 256, and its room for g and dx's sums does not grow with each."""
+    counts = [0, 1, 64, 65] + [256 * k + d for k in range(1, 160) for d in (0, 1)]
+    most = 0
+    for t in counts:
+        need = abi.zero_head_workspace_bytes(
+            _head(tokens=t, hidden=hidden, vocab=vocab, ldx=hidden, w=w, ldw=hidden), grad)
+        assert need >= most, (t, need, most)
+        most = need
+
+
+@pytest.mark.parametrize("hidden,vocab,most,fewer", [
+    (4096, 128256, 5000, 4096), (4096, 128256, 16384, 12000), (1600, 50257, 12000, 10496),
+    (8192, 32000, 2048, 1792), (4096, 128256, 5000, 64)])
+@pytest.mark.parametrize("grad", [False, True])
+def test_smaller_batches_are_not_refused(hidden, vocab, most, fewer, grad):
+    """What a call of `fewer` tokens asks for (a refusal names it) is there in the workspace of
+    a head for `most`."""
+    size = dict(hidden=hidden, vocab=vocab, ldx=hidden, ldw=hidden)
+    far = [1 << (40 + k) for k in range(4)]  # apart for any of these sizes
+    head = _head(tokens=fewer, x=far[0], w=far[1], **size)
+    with pytest.raises(abi.ZeroError) as e:
+        if grad:
+            _grad(head, grads=_grads(dx=far[2], lddx=hidden, dw=far[3], lddw=hidden), n=1)
+        else:
+            _loss(head, n=1)
+    assert e.value.code == abi.ZERO_ENOSPC
+    need = int(str(e.value).split("<")[1])
+    assert 0 < need <= abi.zero_head_workspace_bytes(_head(tokens=most, **size), grad)

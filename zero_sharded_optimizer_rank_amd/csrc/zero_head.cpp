@@ -153,7 +153,19 @@ extern "C" {
 
 size_t zero_head_workspace_bytes(const zero_head_t* head, int32_t grad) {
   if (!head || !good_sizes(head)) return 0;
-  return zk::head_plan(head, grad != 0).total;
+  // A batch of fewer tokens can need more: a piece of g shrinks where the
+  // vocabulary takes one piece more, and dx's splits are whole.  The plan
+  // changes by the tile, and at kFewTokens.
+  zero_head_t h = *head;
+  size_t need = 0;
+  const auto count = [&](int64_t tokens) {
+    h.tokens = tokens < head->tokens ? tokens : head->tokens;
+    const size_t n = zk::head_plan(&h, grad != 0).total;
+    if (n > need) need = n;
+  };
+  count(zk::kFewTokens);
+  for (int64_t t = 0; t < head->tokens; t += kHeadTile) count(t + kHeadTile);
+  return need;
 }
 
 int zero_head_loss(const zero_head_t* head, float* token_loss, float* lse, void* workspace,
