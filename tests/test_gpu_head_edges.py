@@ -329,3 +329,36 @@ def test_smaller_batches_of_a_large_head(T, fewer, V, H):
         _all(h.loss_grad(x, w, y), ref)
         del ref
         torch.cuda.empty_cache()
+
+
+def test_captured_call_keeps_its_workspace():
+    """A graph is captured, then a w that has to be laid out again makes the head's workspace
+    grow: replays still have the memory that they were captured with to themselves."""
+    T, V, H, dtype = 200, 900, 264, torch.bfloat16
+    x, w, y = _inputs(T, V, H, dtype, seed=20)
+    _, odd, _ = _inputs(T, V, H, dtype, seed=20, ldw=265)
+    ref = reference(x, w, y)
+    h = _head(T, V, H, dtype)
+    h.loss_grad(x, w, y)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        r = h.loss_grad(x, w, y)
+    old = h.ws.data_ptr(), h.ws.numel()
+    _all(h.loss_grad(x[:50], odd, y[:50]), reference(x[:50], w, y[:50]))
+    assert h.ws.numel() == old[1]  # a few tokens read w in place
+    _all(h.loss_grad(x[:70], odd, y[:70]), reference(x[:70], w, y[:70]))
+    grown = h.ws.data_ptr()
+    assert grown != old[0]
+    others = [torch.full((old[1],), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for o in others:
+        assert o.data_ptr() + o.numel() <= old[0] or o.data_ptr() >= old[0] + old[1]
+    for _ in range(3):
+        r.dx.zero_(), r.dw.zero_()
+        graph.replay()
+        _all(r, ref)
+        _all(h.loss_grad(x, odd, y), ref)  # the larger batch: no further growth
+        assert h.ws.data_ptr() == grown
+        torch.cuda.synchronize()
+    assert all((o == 0xA5).all() for o in others)

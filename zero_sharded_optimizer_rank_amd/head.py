@@ -37,6 +37,7 @@ class LossHead:
     label ignores its token.  grad=False keeps the smaller workspace of the loss alone.  Calls
     run on the given stream (default: the current stream of the device), which has to wait for
     the stream that the head was made on, as for any tensor, and must not overlap on one head.
+    The head has to outlive its calls and the graphs that hold them.
     """
 
     def __init__(self, tokens: int, hidden: int, vocab: int, dtype: torch.dtype, device="cuda:0",
@@ -96,13 +97,15 @@ class LossHead:
 
     def _workspace(self, head, grad, stream):
         # rows of w that do not start on 16-byte boundaries may take a copy in the workspace
-        if (head.w | head.ldw * 2 | self.hidden * 2) % 16:
-            need = abi.zero_head_workspace_bytes(head, grad)
-            if need > self.ws.numel():
-                # earlier calls may have run on another stream than the allocating one; this
-                # call's stream is behind them
-                self.ws.record_stream(stream or torch.cuda.current_stream(self.device))
-                self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        if (head.w | head.ldw * 2 | self.hidden * 2) % 16 \
+                and abi.zero_head_workspace_bytes(head, grad) > self.ws.numel():
+            # grown once, for every later call; a graph captured before holds the old one's
+            # address, so that stays too
+            full = abi.zero_head_t.from_buffer_copy(head)
+            full.tokens = self.tokens
+            self._first_ws = self.ws
+            self.ws = torch.empty(abi.zero_head_workspace_bytes(full, self.has_grad),
+                                  dtype=torch.uint8, device=self.device)
         return self.ws
 
     def _result(self, t, **kw):
