@@ -37,7 +37,7 @@ class LossHead:
     label ignores its token.  grad=False keeps the smaller workspace of the loss alone.  Calls
     run on the given stream (default: the current stream of the device), which has to wait for
     the stream that the head was made on, as for any tensor, and must not overlap on one head.
-    The head has to outlive its calls and the graphs that hold them.
+    The head has to outlive the work of its calls, and the graphs that hold them.
     """
 
     def __init__(self, tokens: int, hidden: int, vocab: int, dtype: torch.dtype, device="cuda:0",
@@ -104,8 +104,9 @@ class LossHead:
             full = abi.zero_head_t.from_buffer_copy(head)
             full.tokens = self.tokens
             self._first_ws = self.ws
-            self.ws = torch.empty(abi.zero_head_workspace_bytes(full, self.has_grad),
-                                  dtype=torch.uint8, device=self.device)
+            with torch.cuda.stream(stream):  # the memory is the call's stream's from the start
+                self.ws = torch.empty(abi.zero_head_workspace_bytes(full, self.has_grad),
+                                      dtype=torch.uint8, device=self.device)
         return self.ws
 
     def _result(self, t, **kw):
@@ -121,7 +122,7 @@ class LossHead:
                                stream_of(self.device, stream))
         return self._result(head.tokens)
 
-    def _grads(self, t, dx, dw, accumulate):
+    def _grads(self, t, dx, dw, accumulate, stream):
         if not self.has_grad:
             raise ValueError("the head was made with grad=False")
         if dx is None:
@@ -130,8 +131,9 @@ class LossHead:
             if accumulate:
                 raise ValueError("accumulate needs a dw to add to")
             if self._dw is None:
-                self._dw = torch.empty(self.vocab, self.hidden, dtype=self.dtype,
-                                       device=self.device)
+                with torch.cuda.stream(stream):  # as a grown workspace
+                    self._dw = torch.empty(self.vocab, self.hidden, dtype=self.dtype,
+                                           device=self.device)
             dw = self._dw
         lddx, lddw = self._matrix(dx, t, "dx"), self._matrix(dw, self.vocab, "dw")
         if dx.dtype != self.dtype or dw.dtype not in (self.dtype, torch.float32):
@@ -146,7 +148,7 @@ class LossHead:
         (dw in the head's type or float32, e.g. the weight's part of a flat contribution row);
         accumulate adds to dw."""
         head = self._head(x, w, labels, mean, loss_scale)
-        dx, dw, grads = self._grads(head.tokens, dx, dw, accumulate)
+        dx, dw, grads = self._grads(head.tokens, dx, dw, accumulate, stream)
         with on_device(self.device):
             ws = self._workspace(head, True, stream)
             abi.zero_head_loss_grad(head, self._token_loss, self._lse, grads, ws, ws.numel(),
@@ -162,7 +164,7 @@ class LossHead:
                 or lse.device != self.device or not lse.is_contiguous() \
                 or lse.numel() != head.tokens:
             raise ValueError(f"lse must be a contiguous float32 vector of {head.tokens}")
-        dx, dw, grads = self._grads(head.tokens, dx, dw, accumulate)
+        dx, dw, grads = self._grads(head.tokens, dx, dw, accumulate, stream)
         with on_device(self.device):
             ws = self._workspace(head, True, stream)
             abi.zero_head_grad(head, lse, grads, ws, ws.numel(), stream_of(self.device, stream))
