@@ -399,3 +399,27 @@ def test_norm_and_clip_in_one_call_equal_the_two_calls(sizes):
             assert r.skip.item() == bad
             for x, y in zip(a, b):
                 assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("refused", [
+    lambda lst: lst.norm(loss_scale=0.0), lambda lst: lst.norm(max_grad_norm=float("nan")),
+    lambda lst: lst.norm_clip(1.0, loss_scale=float("inf")),
+    lambda lst: lst.norm_clip(1.0, out_scale=0.0)])
+def test_a_refused_norm_is_none(refused):
+    """clip finds no coefficient after a norm that was refused, and changes nothing."""
+    from zero_sharded_optimizer_rank_amd import abi
+    cpu, gpu = _make([100, 3], TYPES, seed=51)
+    lst = _lists()(gpu)
+    with pytest.raises(abi.ZeroError):
+        refused(lst)
+    with pytest.raises(RuntimeError):
+        lst.clip()
+    for x, t in zip(cpu, gpu):
+        assert torch.equal(t.cpu(), x)
+    lst.norm(max_grad_norm=0.01)
+    with pytest.raises(abi.ZeroError):
+        refused(lst)  # the last norm's result still stands
+    lst.clip()
+    for x, t in zip(cpu, gpu):
+        c = lst.result.clip_coef.cpu()
+        assert torch.equal(t.cpu(), (x.float() * c).to(x.dtype))

@@ -128,12 +128,12 @@ class GradList:
              other_overflow: bool = False, stream=None) -> GradNorm:
         """The norm of the tensors divided by loss_scale, the coefficient that clips it to
         max_grad_norm (<= 0: 1) and the skip decision."""
-        self._normed = True
         guard, stream = self._on(stream)
         with guard:
             abi.zero_tensors_norm(self.table, self.n,
                                   self.args(max_grad_norm, loss_scale, other_sq, other_overflow),
                                   self._sq, self._ws, self.ws_bytes, self._res, stream)
+        self._normed = True
         return self.result
 
     def clip(self, loss_scale: float = 1.0, out_scale: float = 1.0, stream=None) -> None:
@@ -149,7 +149,6 @@ class GradList:
     def norm_clip(self, max_grad_norm: float, loss_scale: float = 1.0, out_scale: float = 1.0,
                   other_sq: float = 0.0, other_overflow: bool = False, stream=None) -> GradNorm:
         """``norm`` then ``clip``, enqueued together."""
-        self._normed = True
         guard, stream = self._on(stream)
         with guard:
             abi.zero_tensors_norm_clip(self.table, self.n,
@@ -157,4 +156,5 @@ class GradList:
                                                  other_overflow),
                                        out_scale, self._sq, self._ws, self.ws_bytes, self._res,
                                        stream)
+        self._normed = True
         return self.result
