@@ -423,3 +423,20 @@ def test_a_refused_norm_is_none(refused):
     for x, t in zip(cpu, gpu):
         c = lst.result.clip_coef.cpu()
         assert torch.equal(t.cpu(), (x.float() * c).to(x.dtype))
+
+
+@pytest.mark.parametrize("n,longest", [(1025, 3), (5000, 7), (300, 90_000), (20, 16384 * 2100)])
+def test_every_workgroups_sums_reach_the_last(n, longest):
+    """Lists whose tensors' sums come from many workgroups, by threads, waves and workgroups:
+    whole numbers, so that every sum is exact; what an earlier call left is NaN."""
+    sizes = [1 + i % 7 for i in range(n)]
+    sizes[n // 3] = longest
+    flat = torch.empty(sum(sizes), device="cuda")
+    lst = _lists()(list(torch.split(flat, sizes)))
+    want = torch.tensor(sizes, dtype=torch.float64)
+    for k in range(1, 31):
+        flat.fill_(float(k))
+        lst.ws.fill_(0xFF)
+        r = lst.norm()
+        assert r.own_sq.item() == k * k * sum(sizes) and r.overflow.item() == 0
+        assert torch.equal(r.tensor_sq.cpu(), k * k * want)
