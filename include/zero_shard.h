@@ -697,7 +697,8 @@ int zero_tensors_norm_clip(const zero_tensor_t* tensors, int32_t n_tensors,
  * over the valid tokens, those with 0 <= y(t) < vocab.  A token with y(t) < 0
  * is ignored: loss and lse 0, dx 0, no part in dw, whatever its x holds.  A
  * label >= vocab is an error of the data: it is counted in `bad`, and the
- * loss and every gradient become NaN, so that a step would be skipped. */
+ * loss, its token's loss and lse, dw and dx of every token that is not ignored
+ * become NaN, so that a step would be skipped. */
 
 #define ZERO_HEAD_MAX_TOKENS ((int64_t)1 << 20)
 #define ZERO_HEAD_MAX_VOCAB ((int64_t)1 << 30)

@@ -392,3 +392,23 @@ def test_buffers_made_in_a_call_are_its_streams():
         assert all(b <= lo or a >= hi for lo, hi in given_back)
     torch.cuda.synchronize()
     _all(r, ref)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+@pytest.mark.parametrize("T", [1, 30, 130])
+@pytest.mark.parametrize("alone", [True, False])
+def test_a_bad_label_reaches_every_gradient(dtype, T, alone):
+    """NaN in dw and in dx of the bad token and of every valid one; ignored tokens stay 0.
+    With one call, and with the gradients alone."""
+    V, H = 300, 72
+    x, w, y = _inputs(T, V, H, dtype, seed=22)
+    y[1::3] = -100
+    if alone:
+        y[:] = -100
+    y[0] = V
+    h = _head(T, V, H, dtype)
+    r = h.loss_grad(x, w, y)
+    apart = h.grad(x, w, y, r.lse, dx=torch.zeros_like(r.dx), dw=torch.zeros_like(r.dw))
+    for dx, dw in ((r.dx, r.dw), apart):
+        assert dw.isnan().all() and dx[y >= 0].isnan().all() and (dx[y < 0] == 0).all()
+    assert r.lse[0].isnan() and r.token_loss[0].isnan() and r.loss.isnan()

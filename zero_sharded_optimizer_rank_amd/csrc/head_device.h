@@ -37,6 +37,8 @@ __device__ __forceinline__ float widen<BF16>(uint32_t b) { return bf2f(b); }
 template <>
 __device__ __forceinline__ float widen<FP16>(uint32_t b) { return h2f(b); }
 
+constexpr uint16_t kNan16 = 0x7FFF;  // NaN in either type
+
 // Four consecutive vocabulary rows of a token into g's type.
 template <typename T>
 __device__ __forceinline__ u32x2 narrow4(float a, float b, float c, float d) {

@@ -119,7 +119,8 @@ __global__ __launch_bounds__(kPackThreads) void k_head_pack_x(
         if (lse) lse[r] = v;
       }
       if (dx)
-        for (int32_t h = threadIdx.x; h < hidden; h += kPackThreads) dx[r * lddx + h] = 0;
+        for (int32_t h = threadIdx.x; h < hidden; h += kPackThreads)
+          dx[r * lddx + h] = y < 0 ? 0 : kNan16;
     }
   }
   if (r >= (valid + kHeadTile - 1) / kHeadTile * kHeadTile) return;

@@ -104,7 +104,8 @@ __device__ __forceinline__ void pack(const FewLogits& f) {
       if (f.lse_out) f.lse_out[r] = v;
     }
     if (f.dx)
-      for (int32_t h = threadIdx.x; h < f.hidden; h += kThreads4) f.dx[r * f.lddx + h] = 0;
+      for (int32_t h = threadIdx.x; h < f.hidden; h += kThreads4)
+        f.dx[r * f.lddx + h] = bad >> r & 1 ? kNan16 : 0;
   }
   if (r >= valid && !f.xt) return;
   int32_t src = -1;  // the r-th valid token
