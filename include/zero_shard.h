@@ -767,7 +767,9 @@ int zero_head_loss(const zero_head_t* head, float* token_loss, float* lse, void*
  * within 1 GiB); exp(l - lse) - [v = y] is rounded once to the type of
  * x and w (fp16: scaled by 2^15 first, so that small probabilities stay in
  * range; up to 64 tokens: to the sum of two such values), and both products
- * accumulate in fp32 and are rounded once.
+ * accumulate in fp32 and are rounded once.  The label's element of a token that
+ * is nearly certain takes over the rounding of its fp32 lse, a few |lse| 2^-24;
+ * zero_head_loss_grad forms it from the loss instead and keeps its digits.
  *   lse         device [T] fp32, 4-byte aligned
  *   workspace   >= zero_head_workspace_bytes(head, 1)
  * dx and dw must not overlap each other, x, w, labels or lse.
@@ -781,9 +783,9 @@ int zero_head_grad(const zero_head_t* head, const float* lse, const zero_head_gr
  * The loss is that of zero_head_loss bit for bit.  The gradients need fewer
  * logits a second time: the last piece's exponentials stay where its g will be,
  * rounded to the 16-bit type, and are multiplied by e^(max - lse) and rounded
- * once more (the label's element alone comes from its fp32 logit), so a
- * probability there has two roundings instead of one; up to 64 tokens keep
- * their fp32 logits instead. */
+ * once more, so a probability there has two roundings instead of one; up to 64
+ * tokens keep their fp32 logits instead.  The label's element is e^-loss - 1 in
+ * every piece. */
 int zero_head_loss_grad(const zero_head_t* head, float* token_loss, float* lse,
                         const zero_head_grads_t* grads, void* workspace, size_t ws_bytes,
                         zero_loss_result_t* dev_result, hipStream_t stream);

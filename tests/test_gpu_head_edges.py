@@ -412,3 +412,43 @@ def test_a_bad_label_reaches_every_gradient(dtype, T, alone):
     for dx, dw in ((r.dx, r.dw), apart):
         assert dw.isnan().all() and dx[y >= 0].isnan().all() and (dx[y < 0] == 0).all()
     assert r.lse[0].isnan() and r.token_loss[0].isnan() and r.loss.isnan()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f16", "bf16"])
+@pytest.mark.parametrize("label", [5, 128255])
+def test_confident_tokens_in_every_piece(dtype, label):
+    """Two pieces of the vocabulary, every token nearly certain of a label in the first or the
+    last: the label's element of g, alone in column 0 of dx (w is 0 there but for the label's
+    row, x is 0), keeps its digits.
+
+    dx[t, 0] = c (e^-loss - 1), c a power of two.  With o the others' sum over the label's
+    exponential, loss = log(1 + o) is off by as much, relatively, as o: the two logits' errors
+    dl, 300 e for the exponentials (at most 4e + 2e |l - m| + e/8 |l| < 100 e at |l| < 40) and
+    their sums (34 additions, then 33 joins of at most 4 roundings); g is rounded once (u).  The
+    gradient alone takes its lse in fp32: 8 |lse| 2^-24 of the element, absolutely, on top."""
+    T, V, H = 4352, 128256, 64
+    g = torch.Generator(device="cuda").manual_seed(23)
+    w = torch.randn(V, H, generator=g, device="cuda") * H ** -0.5
+    w[:, 0] = 0.0
+    w[label] /= w[label].norm()
+    x = w[label] * (torch.rand(T, 1, generator=g, device="cuda") * 12.0 + 20.0)
+    w[label, 0] = 1.0
+    x, w = x.to(dtype), w.to(dtype)
+    y = torch.full((T,), label, device="cuda")
+    l = x.double() @ w.double().t()
+    assert float(l.abs().max()) < 40
+    dl = 2 * H * E * float((x.double().abs() @ w.double().abs().t()).max())
+    lse = torch.logsumexp(l, 1)
+    loss = lse - l[:, label]
+    del l
+    assert loss.min() < 3e-5 and loss.max() < 1.0
+    c = 1024.0
+    want = c * torch.expm1(-loss)
+    u = torch.finfo(dtype).eps / 2
+    bound = 1.01 * (u + dl + 300 * E) * want.abs()
+    h = _head(T, V, H, dtype)
+    r = h.loss_grad(x, w, y, mean=False, loss_scale=c)
+    check(r.dx[:, 0], want, bound, "label's element")
+    dx, _ = h.grad(x, w, y, r.lse.clone(), mean=False, loss_scale=c)
+    check(dx[:, 0], want, bound + c * 4 * E * lse.abs(), "label's element, lse alone")
+    torch.cuda.empty_cache()

@@ -346,13 +346,16 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
 // g of a piece: rows are packed tokens, columns the piece's vocabulary rows;
 // columns past the vocabulary and rows past the valid tokens are zero.  Rounded
 // once to 16 bits, the type the matrix cores multiply (dx and dw keep 32-bit
-// sums).  Bound as k_head_partials.
+// sums).  The label's element is e^-loss - 1 (dy) where the loss ran in the same
+// call; from the lse alone (dy NULL) a confident token's loses the digits that
+// the fp32 lse has lost.  Bound as k_head_partials.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_g(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, const uint16_t* __restrict__ x,
     int32_t hidden_pad, int32_t K, const int32_t* __restrict__ label,
-    const float* __restrict__ lse, const HeadState* __restrict__ state, int64_t piece0,
-    int32_t piece, uint16_t* __restrict__ g) {
+    const float* __restrict__ lse, const float* __restrict__ dy,
+    const HeadState* __restrict__ state, int64_t piece0, int32_t piece,
+    uint16_t* __restrict__ g) {
   using L = LogitTile<T>;
   using G = typename L::G;
   const int32_t valid = state->valid;
@@ -387,10 +390,14 @@ __global__ __launch_bounds__(kGemmThreads) void k_head_g(
       for (int e = 0; e < 4; ++e)
         acc[i][j][e] = exp2_fast(__builtin_fmaf(acc[i][j][e], kLog2e, shift));
     if (__any(mine)) {
+      const float at = dy && mine ? dy[t] * g_scale<T>() : 0.0f;
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] -= want == 4 * i + e ? g_scale<T>() : 0.0f;
+        for (int e = 0; e < 4; ++e) {
+          const float p = dy ? at : acc[i][j][e] - g_scale<T>();
+          acc[i][j][e] = want == 4 * i + e ? p : acc[i][j][e];
+        }
     }
     if (rows < kHeadPart || !__all(there)) {  // the vocabulary's or the tokens' end
 #pragma unroll
@@ -645,9 +652,11 @@ int loss_t(const zero_head_t* h, const HeadPlan& p, void* ws, float* token_loss,
 }
 
 // One piece of the vocabulary, from row v0: g, then its share of dx and its dw.
+// loss_ran: in the same call; its exponentials of the first piece (the last
+// of the vocabulary) lie in g's block.
 template <typename T>
 int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_grads_t* gr,
-            int64_t v0, bool have, bool first, hipStream_t stream) {
+            int64_t v0, bool loss_ran, bool first, hipStream_t stream) {
   const WeightView w = weight_view(h, p, ws);
   HeadState* state = at<HeadState>(ws, p.state);
   const uint32_t htiles = (uint32_t)((h->hidden + 255) / 256);
@@ -659,7 +668,7 @@ int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
   const int32_t* label = at<const int32_t>(ws, p.label);
   const float* lse = at<const float>(ws, p.lse);
   if (h->tokens > 0) {
-    if (have)
+    if (loss_ran && first)
       hipLaunchKernelGGL(k_head_rescale<T>,
                          dim3((uint32_t)((left + kRescaleCols - 1) / kRescaleCols),
                               (uint32_t)(p.tokens_pad / kRescaleWaves)),
@@ -669,7 +678,8 @@ int piece_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_g
     else
       hipLaunchKernelGGL(k_head_g<T>, dim3(tile_grid(ttiles, vtiles)), dim3(kGemmThreads), 0,
                          stream, w.w, w.ld, (int32_t)h->vocab, x, (int32_t)p.hidden_pad, w.K,
-                         label, lse, state, v0, (int32_t)p.piece, g);
+                         label, lse, loss_ran ? at<const float>(ws, p.dy) : nullptr, state, v0,
+                         (int32_t)p.piece, g);
     ZK_LAUNCHED();
     hipLaunchKernelGGL(k_head_dx<T>, dim3(tile_grid(htiles * p.split, ttiles)),
                        dim3(kGemmThreads), 0, stream, g, (int32_t)p.piece, w.w + v0 * w.ld, w.ld,
@@ -697,7 +707,7 @@ int grad_t(const zero_head_t* h, const HeadPlan& p, void* ws, const zero_head_gr
   // the kept piece lies in g's block: it goes first
   int e = piece_t<T>(h, p, ws, gr, p.kept, kept, true, stream);
   for (int64_t v0 = 0; !e && v0 < p.kept; v0 += p.piece)
-    e = piece_t<T>(h, p, ws, gr, v0, false, false, stream);
+    e = piece_t<T>(h, p, ws, gr, v0, kept, false, stream);
   if (e) return e;
   if (h->tokens > 0)
     hipLaunchKernelGGL((k_head_dx_out<T>),
