@@ -101,6 +101,16 @@ def test_grad_list_refusals_on_the_host():
         GradList([torch.zeros(3)], out=[], device=dev)
 
 
+@pytest.mark.parametrize("device", ["cpu", "cpu:0", "meta"])
+@pytest.mark.parametrize("tensors", [0, 1])
+def test_grad_list_is_on_a_gpu(device, tensors):
+    """An empty list too: its kernels write the list's own results."""
+    torch = pytest.importorskip("torch")
+    from zero_sharded_optimizer_rank_amd.tensors import GradList
+    with pytest.raises(ValueError, match="not a GPU"):
+        GradList([torch.zeros(3, device=device)] * tensors, device=device)
+
+
 def test_entries_that_share_memory():
     torch = pytest.importorskip("torch")
     from zero_sharded_optimizer_rank_amd.tensors import _check_apart

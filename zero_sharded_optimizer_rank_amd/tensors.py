@@ -91,6 +91,8 @@ class GradList:
             device = torch.device("cuda", torch.cuda.current_device())
         if device.type == "cuda" and device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
+        if device.type != "cuda":
+            raise ValueError(f"device {device} is not a GPU")
         self.device = device
         entries = []
         for i, (t, o) in enumerate(zip(self.tensors, self.out)):
