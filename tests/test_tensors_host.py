@@ -126,3 +126,13 @@ def test_entries_that_share_memory():
                          ([b[:90], c], [torch.zeros(90), torch.zeros(20)])):
         with pytest.raises(ValueError, match="share memory"):
             _check_apart(tensors, out)
+
+
+def test_stream_of_another_device():
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+    from zero_sharded_optimizer_rank_amd.tensors import stream_of
+    here = SimpleNamespace(device_index=1, cuda_stream=77)
+    assert stream_of(torch.device("cuda", 1), here) == 77
+    with pytest.raises(ValueError, match="the stream is on cuda:1"):
+        stream_of(torch.device("cuda", 0), here)

@@ -116,10 +116,11 @@ class LossHead:
     def loss(self, x, w, labels, mean: bool = True, stream=None) -> HeadLoss:
         """The loss alone."""
         head = self._head(x, w, labels, mean, 1.0)
+        handle = stream_of(self.device, stream)
         with on_device(self.device):
             ws = self._workspace(head, False, stream)
             abi.zero_head_loss(head, self._token_loss, self._lse, ws, ws.numel(), self.res,
-                               stream_of(self.device, stream))
+                               handle)
         return self._result(head.tokens)
 
     def _grads(self, t, dx, dw, accumulate, stream):
@@ -148,11 +149,12 @@ class LossHead:
         (dw in the head's type or float32, e.g. the weight's part of a flat contribution row);
         accumulate adds to dw."""
         head = self._head(x, w, labels, mean, loss_scale)
+        handle = stream_of(self.device, stream)
         dx, dw, grads = self._grads(head.tokens, dx, dw, accumulate, stream)
         with on_device(self.device):
             ws = self._workspace(head, True, stream)
             abi.zero_head_loss_grad(head, self._token_loss, self._lse, grads, ws, ws.numel(),
-                                    self.res, stream_of(self.device, stream))
+                                    self.res, handle)
         return self._result(head.tokens, dx=dx, dw=dw)
 
     def grad(self, x, w, labels, lse, mean: bool = True, loss_scale: float = 1.0, dx=None,
@@ -164,8 +166,9 @@ class LossHead:
                 or lse.device != self.device or not lse.is_contiguous() \
                 or lse.numel() != head.tokens:
             raise ValueError(f"lse must be a contiguous float32 vector of {head.tokens}")
+        handle = stream_of(self.device, stream)
         dx, dw, grads = self._grads(head.tokens, dx, dw, accumulate, stream)
         with on_device(self.device):
             ws = self._workspace(head, True, stream)
-            abi.zero_head_grad(head, lse, grads, ws, ws.numel(), stream_of(self.device, stream))
+            abi.zero_head_grad(head, lse, grads, ws, ws.numel(), handle)
         return dx, dw

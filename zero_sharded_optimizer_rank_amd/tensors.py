@@ -38,7 +38,11 @@ def on_device(device):
 
 def stream_of(device, stream) -> int:
     """The handle of the given stream, or of the device's current one."""
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device_index != device.index:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the call on {device}")
+    return stream.cuda_stream
 
 
 def _check_tensor(t, what: str, device) -> None:
