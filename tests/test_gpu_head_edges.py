@@ -452,3 +452,12 @@ def test_confident_tokens_in_every_piece(dtype, label):
     dx, _ = h.grad(x, w, y, r.lse.clone(), mean=False, loss_scale=c)
     check(dx[:, 0], want, bound + c * 4 * E * lse.abs(), "label's element, lse alone")
     torch.cuda.empty_cache()
+
+
+def test_last_token_of_a_long_sequence():
+    """x [1, H] out of a sequence of hidden states, whose stride is far past a row's."""
+    S, V, H, dtype = 1100, 500, 1024, torch.bfloat16
+    x, w, y = _inputs(S, V, H, dtype, seed=24)
+    last = x.reshape(1, S, H)[:, -1]
+    assert last.stride(0) > 1 << 20
+    _all(_head(1, V, H, dtype).loss_grad(last, w, y[-1:]), reference(last, w, y[-1:]))

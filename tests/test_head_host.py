@@ -198,3 +198,16 @@ def test_smaller_batches_are_not_refused(hidden, vocab, most, fewer, grad):
     assert e.value.code == abi.ZERO_ENOSPC
     need = int(str(e.value).split("<")[1])
     assert 0 < need <= abi.zero_head_workspace_bytes(_head(tokens=most, **size), grad)
+
+
+def test_one_row_of_a_far_strided_tensor():
+    """The stride of a single row means nothing: the last token of one long sequence."""
+    from zero_sharded_optimizer_rank_amd.head import LossHead
+    h = LossHead.__new__(LossHead)
+    h.hidden, h.device = 8, torch.device("cpu")
+    for far in (8, 1 << 21, 3):
+        assert h._matrix(torch.zeros(8).as_strided((1, 8), (far, 1)), 1, "x") == 8
+    assert h._matrix(torch.zeros(0, 8), 0, "x") == 8
+    assert h._matrix(torch.zeros(24).as_strided((2, 8), (16, 1)), 2, "x") == 16
+    with pytest.raises(ValueError, match="overlap"):
+        h._matrix(torch.zeros(24).as_strided((2, 8), (3, 1)), 2, "x")

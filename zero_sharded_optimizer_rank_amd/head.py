@@ -33,11 +33,12 @@ class LossHead:
     """Softmax cross entropy of x @ w.T against labels, for up to ``tokens`` tokens.
 
     dtype: torch.float16 or torch.bfloat16, the type of x [T, hidden] and w [vocab, hidden];
-    rows may be strided, elements of a row must be adjacent.  labels: int64 [T]; a negative
-    label ignores its token.  grad=False keeps the smaller workspace of the loss alone.  Calls
-    run on the given stream (default: the current stream of the device), which has to wait for
-    the stream that the head was made on, as for any tensor, and must not overlap on one head.
-    The head has to outlive the work of its calls, and the graphs that hold them.
+    rows may be strided (up to 2^20 elements apart), elements of a row must be adjacent.
+    labels: int64 [T]; a negative label ignores its token.  grad=False keeps the smaller
+    workspace of the loss alone.  Calls run on the given stream (default: the current stream of
+    the device), which has to wait for the stream that the head was made on, as for any tensor,
+    and must not overlap on one head.  The head has to outlive the work of its calls, and the
+    graphs that hold them.
     """
 
     def __init__(self, tokens: int, hidden: int, vocab: int, dtype: torch.dtype, device="cuda:0",
@@ -74,7 +75,7 @@ class LossHead:
             raise ValueError(f"{what} is on {t.device}, the head on {self.device}")
         if self.hidden > 1 and t.stride(1) != 1:
             raise ValueError(f"the elements of a row of {what} must be adjacent")
-        ld = t.stride(0) if rows > 1 else max(t.stride(0), self.hidden)
+        ld = t.stride(0) if rows > 1 else self.hidden  # one row has no next
         if ld < self.hidden:
             raise ValueError(f"the rows of {what} overlap")
         return ld
