@@ -686,10 +686,12 @@ int zero_tensors_norm_clip(const zero_tensor_t* tensors, int32_t n_tensors,
 
 /* ------------------------------------------------------------------------ */
 /* Loss of a language-model head and its gradients: softmax cross entropy of
- * logits = x w^T, taken in pieces of the vocabulary so that the logits are
- * never kept.  It is where the loss scale enters that the shard step divides
- * by: the weight's gradient is written in the 16-bit form of a contribution
- * row, straight into the flat gradient if the caller points dw there.
+ * logits = x w^T.  The loss takes the logits in tiles and keeps none of them;
+ * the gradients take the vocabulary in pieces and keep one piece's exponentials
+ * in 16 bits at a time (up to 64 tokens: their fp32 logits).  It is where the
+ * loss scale enters that the shard step divides by: the weight's gradient is
+ * written in the 16-bit form of a contribution row, straight into the flat
+ * gradient if the caller points dw there.
  *   l_tv = sum_h x_th w_vh;  lse_t = log sum_v exp(l_tv);  loss_t = lse_t - l_t,y(t)
  *   c    = loss_scale / (mean ? max(valid, 1) : 1)
  *   d_tv = c (exp(l_tv - lse_t) - [v = y(t)])
@@ -763,8 +765,9 @@ int zero_head_loss(const zero_head_t* head, float* token_loss, float* lse, void*
 /*
  * zero_head_grad: the gradients, from the lse that zero_head_loss wrote for
  * the same x, w and labels.  The logits are formed again, one piece of the
- * vocabulary at a time (as many rows as keep the workspace's block for a piece
- * within 1 GiB); exp(l - lse) - [v = y] is rounded once to the type of
+ * vocabulary at a time (as many rows as keep the workspace's block for a piece,
+ * 2 bytes a row and token, within 1 GiB, but 4096 rows at least, which above
+ * 131072 tokens take more); exp(l - lse) - [v = y] is rounded once to the type of
  * x and w (fp16: scaled by 2^15 first, so that small probabilities stay in
  * range; up to 64 tokens: to the sum of two such values), and both products
  * accumulate in fp32 and are rounded once.  The label's element of a token that

@@ -109,7 +109,8 @@ HeadPlan head_plan(const zero_head_t* h, bool grad) {
   } else if (grad) {
     // a piece's block of g stays within 1 GiB: with all 128256 rows of a
     // Llama-3 head up to 4096 tokens go in one piece, whose logits are formed
-    // once, and every further doubling of the tokens halves the piece
+    // once, and every further doubling of the tokens halves the piece, down to
+    // 16 tiles of rows (131072 tokens), whose products still fill the CUs
     int64_t piece = ((int64_t)1 << 29) / p.tokens_pad / kHeadTile * kHeadTile;
     piece = clamp(piece, 16 * kHeadTile, vocab_pad);
     const int64_t pieces = (vocab_pad + piece - 1) / piece;

@@ -172,8 +172,8 @@ struct LogitTile {
 // vocabulary that starts at `kept` stay in g's block (rounded to 16 bits):
 // k_head_rescale turns them into g without forming those logits again.
 // Bound by the matrix cores (busy 75 to 80%, at the chip's power limit): 7373 x
-// 128256 x 4096, bf16, 5.4 ms (1430 TFLOP/s); with the exponentials stored, 3277
-// tokens 2.64 ms (1300).  1024 x 50257 x 1600, fp16, 0.19 ms (870): 788 tiles on
+// 128256 x 4096, bf16, 5.5 ms (1410 TFLOP/s); with the exponentials stored, 3277
+// tokens 2.62 ms (1320).  1024 x 50257 x 1600, fp16, 0.206 ms (800): 788 tiles on
 // 256 CUs, four rounds for three.
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_partials(
@@ -348,7 +348,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(
 // once to 16 bits, the type the matrix cores multiply (dx and dw keep 32-bit
 // sums).  The label's element is e^-loss - 1 (dy) where the loss ran in the same
 // call; from the lse alone (dy NULL) a confident token's loses the digits that
-// the fp32 lse has lost.  Bound as k_head_partials.
+// the fp32 lse has lost.  Bound as k_head_partials: 4096 x 128256 x 4096, bf16,
+// 3.18 ms (1350 TFLOP/s).
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_g(
     const uint16_t* __restrict__ w, int64_t ldw, int32_t vocab, const uint16_t* __restrict__ x,
@@ -475,7 +476,7 @@ __global__ __launch_bounds__(64 * kRescaleWaves) void k_head_rescale(
 // dx: A = w (rows of the tile: hidden columns, contiguous along them), B = g
 // (token rows, contiguous along the vocabulary).  Split s of the piece adds
 // into its own fp32 block.  Bound by the matrix cores: 3277 x 128256 x 4096,
-// bf16, 2.76 ms (1250 TFLOP/s); 1024 x 50257 x 1600, fp16, 0.17 ms (945).
+// bf16, 2.75 ms (1250 TFLOP/s); 1024 x 50257 x 1600, fp16, 0.166 ms (990).
 template <typename T>
 __global__ __launch_bounds__(kGemmThreads) void k_head_dx(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ w, int64_t ldw,
@@ -544,8 +545,11 @@ __global__ __launch_bounds__(kPackThreads) void k_head_dx_out(
 
 // dw: A = packed x (rows of the tile: hidden columns), B = g (vocabulary
 // rows), both contiguous along their rows; the contraction runs over the
-// tokens.  Bound by the matrix cores: 3277 x 128256 x 4096, bf16, 2.58 ms (1330
-// TFLOP/s); 2047 x 32000 x 8192 0.88 ms (1220).
+// tokens.  Bound by the matrix cores: 3277 x 128256 x 4096, bf16, 2.56 ms (1340
+// TFLOP/s); 2047 x 32000 x 8192 0.94 ms (1140).  Only a 16-bit dw that is
+// overwritten leaves through LDS in whole lines; the others go out from the
+// registers, 8 or 16 bytes of 16 rows at a time: 4096 x 128256 x 4096, bf16 3.2 ms,
+// bf16 accumulated 3.6, fp32 3.4, fp32 accumulated 3.7.
 template <typename T, bool F32OUT>
 __global__ __launch_bounds__(kGemmThreads) void k_head_dw(
     const uint16_t* __restrict__ g, int32_t piece, const uint16_t* __restrict__ x,

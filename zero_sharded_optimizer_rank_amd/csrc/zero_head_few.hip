@@ -137,7 +137,8 @@ __device__ __forceinline__ void pack(const FewLogits& f) {
 // fragments, 128 hidden columns (8 KiB a wave) on their way while the last ones
 // are multiplied; B = packed x through LDS, since all four waves read it.
 // Bound by memory: 128256 x 4096, one token 168 us (6.2 TB/s), 64 tokens 190
-// (5.5); 50257 x 1600, 37 tokens 35 us (4.6).
+// (5.5); 50257 x 1600, 37 tokens 35 us (4.6).  Behind a call that has written a dw
+// of 1 GB, whose lines are still on their way out, 64 tokens take 270 us.
 //
 // Workgroups start at different columns: rows of 4096 columns lie a power of
 // two apart, and all workgroups at the same column would ask the same memory
@@ -663,7 +664,9 @@ __device__ __forceinline__ void few_dx(const FewGrad& f, const Tokens& tok, char
 }
 
 // Workgroups of dx first: they run longest.  Bound by memory: 64 tokens, 128256 x
-// 4096, 415 us (w read, dw written: 5.1 TB/s).
+// 4096, 440 to 500 us (w read, dw written: 4.2 to 4.8 TB/s), and 8 tokens hardly
+// less, since all of this is 64 tokens wide.  A dw in fp32 0.75 ms, accumulated
+// 1.24 ms; in 16 bits accumulated, element by element, 2.1 ms.
 template <typename T, bool F32OUT, bool LONG>
 __global__ __launch_bounds__(kThreads4) void k_few_grads(FewGrad f, int32_t dx_blocks) {
   __shared__ __attribute__((aligned(1024))) char lds[49152];

@@ -8,8 +8,8 @@
 // vector units do in the time the element takes to arrive.  The list travels
 // in the kernel arguments, kNormBatch tensors a launch: gradient tensors move
 // from step to step, and a table in device memory would cost a copy each time.
-// 4.02 GB in one fp32 tensor 577 us (6.96 TB/s), 3.12 GB in 582 fp16 tensors 460
-// us (6.8).
+// 4.02 GB in one fp32 tensor 580 us (6.9 TB/s), 3.12 GB in 582 fp16 tensors, three
+// launches, 470 us (6.6).
 //
 // The sums keep one order: chunk by chunk, thread t of a chunk's workgroup
 // takes its 16-byte pieces t, t + T, ... in turn, the workgroup's threads are
@@ -533,9 +533,12 @@ int launch_tensors_clip(const zero_tensor_t* tensors, int32_t n, float scale,
   return clip_launches(tensors, n, scale, kClipAlone, Finish{}, (zero_step_result_t*)res, stream);
 }
 
-// A small list's clip, of one launch, finishes the norm itself: a launch less
-// costs more there than every workgroup's few loads (3 tensors, 1.0 M elements:
-// 15.7 -> 11.8 us a call).
+// A small list's clip, of one launch, finishes the norm itself: up to
+// kFinishChunks chunks the launch that this saves costs more than every
+// workgroup's loads of all partials (a call, fp32 to fp16, finished apart against
+// in the clip: 1 tensor of 64 chunks 13.3 / 10.0 us, 9 of 192 16.3 / 14.3, 64
+// of 256 18.1 / 15.2, 139 of 256 18.5 / 15.8; beyond, 64 of 320 21.2 / 35.2, 9 of
+// 512 23.2 / 25.5, 139 of 1024 41 / 143).
 int launch_tensors_norm_clip(const zero_tensor_t* tensors, int32_t n, double* tensor_sq,
                              void* workspace, const FinalizeArgs& fa, float scale,
                              zero_step_result_t* res, hipStream_t stream) {

@@ -2,7 +2,9 @@
 
 PyTorch supplies the memory and the stream; the work runs in libzero_shard.so
 (zero_head_loss, zero_head_grad).  A ``LossHead`` holds the workspace and the
-outputs for up to ``tokens`` tokens; the logits are never kept.
+outputs for up to ``tokens`` tokens.  The loss keeps no logits; the gradients keep
+those of one piece of the vocabulary at a time, in 16 bits and at most 1 GiB up to
+131072 tokens.
 """
 from __future__ import annotations
 

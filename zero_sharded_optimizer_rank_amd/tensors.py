@@ -76,9 +76,11 @@ class GradList:
 
     tensors: contiguous float32 / float16 / bfloat16 tensors, mixed as they come; out: tensors
     of the same sizes (any of the three types) that ``clip`` writes, or None to clip in place.
-    Different tensors must not share memory.  Calls run on the given stream (default: the
-    current stream of the list's device), which has to wait for the stream that the list was
-    made on, as for any tensor; calls on one list must not overlap.
+    Different tensors must not share memory.  The list is made for these tensors where they lie
+    (1.6 us a tensor): gradients that a step makes anew, or whose memory is exchanged, need a
+    new list.  Calls run on the given stream (default: the current stream of the list's device),
+    which has to wait for the stream that the list was made on, as for any tensor; calls on one
+    list must not overlap.  The list has to outlive their work, and the graphs that hold them.
     """
 
     def __init__(self, tensors: Sequence[torch.Tensor],
