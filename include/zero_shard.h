@@ -685,6 +685,98 @@ int zero_tensors_norm_clip(const zero_tensor_t* tensors, int32_t n_tensors,
                            hipStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* AdamW over a list of tensors in one launch, for parameters that are not laid
+ * out as a flat shard: each tensor with its own weight decay and learning-rate
+ * factor, moments in 32 bits or in 8.  Clip coefficient and skip come from
+ * zero_tensors_norm. */
+
+/* Elements of 8-bit moments that share an exponent. */
+#define ZERO_ADAM_BLOCK 128
+
+typedef struct zero_adam_tensor {
+  const void* grad;     /* device [numel], contiguous, aligned to one element */
+  float* master;        /* device [numel], in place, 4-byte aligned */
+  void* m;              /* moments, in place, 4-byte aligned: fp32 [numel], or 8-bit codes */
+  void* v;              /*   [numel]; all zero bytes are zero moments in both forms */
+  uint8_t* m_exp;       /* 8-bit moments: device [ceil(numel / ZERO_ADAM_BLOCK)], in place; */
+  uint8_t* v_exp;       /*   else not used */
+  void* param;          /* device [numel], written, aligned to one element; or NULL */
+  int64_t numel;        /* >= 0 */
+  double weight_decay;  /* decoupled */
+  double lr_scale;      /* >= 0, on the call's lr (weight decay included) */
+  int32_t grad_dtype;   /* zero_dtype */
+  int32_t param_dtype;  /* zero_dtype */
+  int32_t moment_bits;  /* 32 or 8 */
+  int32_t reserved;
+} zero_adam_tensor_t;
+
+/* A prepared list; filled by zero_tensors_adam_prepare, not changed by others. */
+typedef struct zero_adam_list {
+  void* table;       /* device, the caller's */
+  int64_t blocks;    /* workgroups of a step */
+  int64_t elements;  /* sum of the numels, each rounded up to ZERO_ADAM_BLOCK */
+  int32_t n_tensors;
+  int32_t reserved;
+} zero_adam_list_t;
+
+/* Bytes of a list's table; 0 for a negative n_tensors. */
+size_t zero_adam_table_bytes(int32_t n_tensors);
+
+/*
+ * zero_tensors_adam_prepare: check a list and write its table on `stream`.  The
+ * calls below read the tensors where they lay then: a tensor that moves needs a
+ * new table.  Different entries must not overlap, nor anything that is written
+ * overlap the table.
+ *   tensors  host [n_tensors], read before the call returns
+ *   table    device, >= zero_adam_table_bytes(n_tensors), 8-byte aligned; must stay
+ *            as written while steps use it
+ *   list     host, filled on success
+ * Errors: ZERO_EINVAL (sizes, dtypes, moment_bits, weight_decay, lr_scale, NULL
+ * pointers, buffers of one entry that overlap, more than 2^42 elements),
+ * ZERO_EALIGN, ZERO_ENOSPC (table), ZERO_EHIP.
+ */
+int zero_tensors_adam_prepare(const zero_adam_tensor_t* tensors, int32_t n_tensors, void* table,
+                              size_t table_bytes, zero_adam_list_t* list, hipStream_t stream);
+
+/*
+ * zero_tensors_adam: one AdamW step of every tensor, unless dev_result->skip (then
+ * nothing is written).  Per element, one rounding per operation:
+ *   gc = (g * s) * c;  then the sequence of zero_adam_apply with lr * lr_scale
+ * and the tensor's weight decay, s = f32(1 / loss_scale), c = clip_coef;
+ * param = the new master, rounded to nearest even.  beta^t is pow(beta, t).
+ *   args        host; lr, betas, eps, step and loss_scale are read (weight_decay is
+ *               the tensors')
+ *   seed        of the 8-bit moments' rounding: give every step its own
+ *   dev_result  device, from zero_tensors_norm or zero_finalize_bf16; NULL: c = 1, no skip
+ * 8-bit moments.  A block of ZERO_ADAM_BLOCK elements has one byte E, the largest
+ * biased fp32 exponent in it (after rounding).  An element's fp32 pattern without
+ * sign, cut to its upper 11 bits (exponent and 3 fraction bits), less 8 max(E - K +
+ * 1, 0), is its code: for v, K = 32, 8 bits; for m, K = 16, 7 bits below the sign.
+ * Code 0 is zero.  Smaller values become 0 (m) or, if not zero, code 1 (v).  The cut
+ * adds 16 u + 8 to the pattern first, u 16 random bits: with mix a 32-bit hash, i the
+ * element and t the tensor's place in the list,
+ *   r = mix(mix(mix(mix(seed) + t) + (i >> 12)) + (i & 4095)), u = r & 0xFFFF for m,
+ *   r >> 16 for v;
+ *   mix(x): x ^= x >> 16; x *= 0x7FEB352D; x ^= x >> 15; x *= 0x846CA68B; x ^= x >> 16
+ * The parameter is updated from the moments before they are rounded.
+ * Errors: ZERO_EINVAL (a list not prepared, args as zero_adam_apply), ZERO_EALIGN,
+ * ZERO_EHIP.
+ */
+int zero_tensors_adam(const zero_adam_list_t* list, const zero_step_args_t* args, uint32_t seed,
+                      const zero_step_result_t* dev_result, hipStream_t stream);
+
+/*
+ * zero_tensors_adam_moments: the values of a list's 8-bit moments, tensor i's from
+ * element sum over j < i of numel_j rounded up to ZERO_ADAM_BLOCK; what lies between
+ * the tensors, and the places of tensors with 32-bit moments, is left as it is.
+ *   m, v   device [list->elements], aligned to one element
+ *   dtype  ZERO_F32 or ZERO_BF16 (both hold the values exactly)
+ * Errors: ZERO_EINVAL (also for m, v that overlap), ZERO_EALIGN, ZERO_EHIP.
+ */
+int zero_tensors_adam_moments(const zero_adam_list_t* list, void* m, void* v, int32_t dtype,
+                              hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Loss of a language-model head and its gradients: softmax cross entropy of
  * logits = x w^T.  The loss takes the logits in tiles and keeps none of them;
  * the gradients take the vocabulary in pieces and keep one piece's exponentials

@@ -21,6 +21,7 @@ ZERO_MAX_RANKS = 64
 ZERO_MAX_SHARD = 0x7FFFFFF8
 ZERO_NOALLOC_MAX_SHARD = 9 << 27
 ZERO_F32, ZERO_F16, ZERO_BF16 = 0, 1, 2
+ZERO_ADAM_BLOCK = 128
 
 
 class ZeroError(RuntimeError):
@@ -90,6 +91,21 @@ class zero_unit_buffers_t(ctypes.Structure):
 class zero_tensor_t(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
                 ("src_dtype", ctypes.c_int32), ("dst_dtype", ctypes.c_int32)]
+
+
+class zero_adam_tensor_t(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("master", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("param", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("weight_decay", ctypes.c_double), ("lr_scale", ctypes.c_double),
+                ("grad_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("moment_bits", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class zero_adam_list_t(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("blocks", ctypes.c_int64),
+                ("elements", ctypes.c_int64), ("n_tensors", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class zero_head_t(ctypes.Structure):
@@ -205,6 +221,13 @@ _SIGNATURES = {
     "zero_tensors_norm_clip": (ctypes.c_int, [_P(zero_tensor_t), ctypes.c_int32,
                                               _P(zero_step_args_t), ctypes.c_double, _vp, _vp,
                                               ctypes.c_size_t, _vp, _vp]),
+    "zero_adam_table_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
+    "zero_tensors_adam_prepare": (ctypes.c_int, [_P(zero_adam_tensor_t), ctypes.c_int32, _vp,
+                                                 ctypes.c_size_t, _P(zero_adam_list_t), _vp]),
+    "zero_tensors_adam": (ctypes.c_int, [_P(zero_adam_list_t), _P(zero_step_args_t),
+                                         ctypes.c_uint32, _vp, _vp]),
+    "zero_tensors_adam_moments": (ctypes.c_int, [_P(zero_adam_list_t), _vp, _vp, ctypes.c_int32,
+                                                 _vp]),
     "zero_head_workspace_bytes": (ctypes.c_size_t, [_P(zero_head_t), ctypes.c_int32]),
     "zero_head_loss": (ctypes.c_int, [_P(zero_head_t), _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]),
     "zero_head_grad": (ctypes.c_int, [_P(zero_head_t), _vp, _P(zero_head_grads_t), _vp,
@@ -547,6 +570,40 @@ def zero_tensors_norm_clip(tensors, n_tensors, args, out_scale, tensor_sq, works
     _check(lib().zero_tensors_norm_clip(tensors, n_tensors, ctypes.byref(args), out_scale,
                                         _addr(tensor_sq), _addr(workspace), ws_bytes,
                                         _addr(dev_result), _stream(stream)))
+
+
+def adam_table(entries):
+    """Table of zero_adam_tensor_t from dicts of its fields (buffers as addresses or tensors)."""
+    t = (zero_adam_tensor_t * max(len(entries), 1))()
+    for i, e in enumerate(entries):
+        t[i] = zero_adam_tensor_t(
+            _addr(e["grad"]), _addr(e["master"]), _addr(e["m"]), _addr(e["v"]),
+            _addr(e.get("m_exp")), _addr(e.get("v_exp")), _addr(e.get("param")), e["numel"],
+            e.get("weight_decay", 0.0), e.get("lr_scale", 1.0), e["grad_dtype"],
+            e.get("param_dtype", ZERO_F32), e["moment_bits"], 0)
+    return t
+
+
+def zero_adam_table_bytes(n_tensors: int) -> int:
+    return int(lib().zero_adam_table_bytes(n_tensors))
+
+
+def zero_tensors_adam_prepare(tensors, n_tensors, table, table_bytes, stream=None
+                              ) -> zero_adam_list_t:
+    out = zero_adam_list_t()
+    _check(lib().zero_tensors_adam_prepare(tensors, n_tensors, _addr(table), table_bytes,
+                                           ctypes.byref(out), _stream(stream)))
+    return out
+
+
+def zero_tensors_adam(adam_list, args, seed, dev_result=None, stream=None):
+    _check(lib().zero_tensors_adam(ctypes.byref(adam_list), ctypes.byref(args), seed,
+                                   _addr(dev_result), _stream(stream)))
+
+
+def zero_tensors_adam_moments(adam_list, m, v, dtype, stream=None):
+    _check(lib().zero_tensors_adam_moments(ctypes.byref(adam_list), _addr(m), _addr(v), dtype,
+                                           _stream(stream)))
 
 
 def zero_head_workspace_bytes(head: zero_head_t, grad: bool) -> int:
