@@ -885,6 +885,95 @@ int zero_head_loss_grad(const zero_head_t* head, float* token_loss, float* lse,
                         const zero_head_grads_t* grads, void* workspace, size_t ws_bytes,
                         zero_loss_result_t* dev_result, hipStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Gated feed-forward block and its gradients: the largest weights of a
+ * transformer block, whose gradients go on to zero_tensors_norm and _adam.
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) u,  y = h Wd^T
+ *   dh = dy Wd,  du = dh act(g),  dg = dh u act'(g)
+ *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h
+ * Sums are fp32.  h, dg and du are rounded once to the 16-bit type (the matrix cores
+ * multiply it), g and u where they are kept for the gradients; in fp16 what passes
+ * 65504 becomes infinite.  Gradients carry whatever loss scale dy carries.  Equal
+ * inputs give equal bits. */
+
+enum zero_act {
+  ZERO_ACT_SILU = 0,      /* g / (1 + e^-g) */
+  ZERO_ACT_GELU = 1,      /* g (1 + erf(g / sqrt 2)) / 2 */
+  ZERO_ACT_GELU_TANH = 2, /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+  ZERO_ACT_RELU = 3       /* max(g, 0); slope 0 at 0 */
+};
+
+#define ZERO_FFN_MAX_TOKENS ((int64_t)1 << 20)
+#define ZERO_FFN_MAX_WIDTH ((int64_t)1 << 20) /* hidden, inner, elements between rows */
+/* ceil(T / 256) * ceil(F / 128), and 3 * ceil(F / 256) * ceil(H / 256), are less than this */
+#define ZERO_FFN_MAX_TILES ((int64_t)1 << 23)
+
+typedef struct zero_ffn {
+  int64_t tokens, hidden, inner;  /* T >= 0, H >= 1, F >= 1 */
+  const void* x;                  /* device [T, H], row t at x + t*ldx; 2-byte aligned */
+  int64_t ldx;                    /* elements between rows, >= H */
+  const void* w_gate;             /* device [F, H], as x */
+  int64_t ld_gate;
+  const void* w_up;               /* device [F, H], as x */
+  int64_t ld_up;
+  const void* w_down;             /* device [H, F], as x */
+  int64_t ld_down;                /* >= F */
+  int32_t dtype;                  /* ZERO_F16 or ZERO_BF16, of all matrices */
+  int32_t act;                    /* zero_act */
+} zero_ffn_t;
+
+/* What the gradients need of the forward pass: g and u in 16 bits. */
+typedef struct zero_ffn_saved {
+  void* gate;  /* device [T, F rounded up to 8], 16-byte aligned */
+  void* up;    /* the same */
+  int64_t ld;  /* elements between rows, a multiple of 8, >= F rounded up to 8 */
+} zero_ffn_saved_t;
+
+typedef struct zero_ffn_grads {
+  const void* dy;       /* device [T, H], as x */
+  int64_t lddy;
+  void* dx;             /* device [T, H], 2-byte aligned, or NULL: not wanted */
+  int64_t lddx;
+  void* dw_gate;        /* device [F, H], aligned to one element, or NULL */
+  int64_t lddw_gate;
+  void* dw_up;          /* device [F, H], or NULL */
+  int64_t lddw_up;
+  void* dw_down;        /* device [H, F], or NULL */
+  int64_t lddw_down;
+  int32_t dw_dtype;     /* of the three: dtype, or ZERO_F32 */
+  int32_t accumulate;   /* nonzero: they are added to (in fp32, rounded once) */
+} zero_ffn_grads_t;
+
+/* Bytes of workspace for the calls below with up to ffn->tokens tokens; grads: NULL for
+ * zero_ffn_forward.  0 for bad sizes.  Depends on sizes, types, strides and alignment:
+ * rows that do not start on 16-byte boundaries, or whose length is no multiple of 8, are
+ * laid out in the workspace first (but not by a forward pass of up to 64 tokens). */
+size_t zero_ffn_workspace_bytes(const zero_ffn_t* ffn, const zero_ffn_grads_t* grads);
+
+/*
+ * zero_ffn_forward: y.
+ *   y          device [T, H], type of x, row t at y + t*ldy; 2-byte aligned
+ *   saved      host, or NULL: g and u are kept there
+ *   workspace  device, >= zero_ffn_workspace_bytes(ffn, NULL), 256-byte aligned; its
+ *              content on entry does not matter
+ * T = 0 does nothing.
+ * Errors: ZERO_EINVAL (sizes, strides, dtype, act, NULL pointers, outputs that overlap
+ * one another or an input), ZERO_EALIGN, ZERO_ENOSPC (workspace), ZERO_EHIP.  Nothing is
+ * launched if a check fails.
+ */
+int zero_ffn_forward(const zero_ffn_t* ffn, void* y, int64_t ldy, const zero_ffn_saved_t* saved,
+                     void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * zero_ffn_backward: the gradients, from what zero_ffn_forward kept for the same inputs.
+ *   workspace  device, >= zero_ffn_workspace_bytes(ffn, grads), as above
+ * T = 0 clears the weights' gradients (or, accumulated, leaves them).
+ * Errors: as zero_ffn_forward, plus ZERO_EINVAL for dw_dtype.
+ */
+int zero_ffn_backward(const zero_ffn_t* ffn, const zero_ffn_saved_t* saved,
+                      const zero_ffn_grads_t* grads, void* workspace, size_t ws_bytes,
+                      hipStream_t stream);
+
 typedef struct zero_scaler {
   double scale;            /* current loss scale */
   double growth, backoff;  /* e.g. 2.0 and 0.5 */

@@ -22,6 +22,7 @@ ZERO_MAX_SHARD = 0x7FFFFFF8
 ZERO_NOALLOC_MAX_SHARD = 9 << 27
 ZERO_F32, ZERO_F16, ZERO_BF16 = 0, 1, 2
 ZERO_ADAM_BLOCK = 128
+ZERO_ACT_SILU, ZERO_ACT_GELU, ZERO_ACT_GELU_TANH, ZERO_ACT_RELU = 0, 1, 2, 3
 
 
 class ZeroError(RuntimeError):
@@ -126,6 +127,27 @@ class zero_loss_result_t(ctypes.Structure):
                 ("reserved", ctypes.c_int32), ("valid", ctypes.c_int64), ("bad", ctypes.c_int64)]
 
 
+class zero_ffn_t(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("inner", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("w_gate", ctypes.c_void_p),
+                ("ld_gate", ctypes.c_int64), ("w_up", ctypes.c_void_p), ("ld_up", ctypes.c_int64),
+                ("w_down", ctypes.c_void_p), ("ld_down", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+class zero_ffn_saved_t(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+
+
+class zero_ffn_grads_t(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("dx", ctypes.c_void_p),
+                ("lddx", ctypes.c_int64), ("dw_gate", ctypes.c_void_p),
+                ("lddw_gate", ctypes.c_int64), ("dw_up", ctypes.c_void_p),
+                ("lddw_up", ctypes.c_int64), ("dw_down", ctypes.c_void_p),
+                ("lddw_down", ctypes.c_int64), ("dw_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+
 class zero_offload_staging_t(ctypes.Structure):
     _fields_ = [("grad_pinned", ctypes.c_void_p), ("param16_pinned", ctypes.c_void_p),
                 ("chunk", ctypes.c_int64), ("upload_stream", ctypes.c_void_p)]
@@ -228,6 +250,11 @@ _SIGNATURES = {
                                          ctypes.c_uint32, _vp, _vp]),
     "zero_tensors_adam_moments": (ctypes.c_int, [_P(zero_adam_list_t), _vp, _vp, ctypes.c_int32,
                                                  _vp]),
+    "zero_ffn_workspace_bytes": (ctypes.c_size_t, [_P(zero_ffn_t), _P(zero_ffn_grads_t)]),
+    "zero_ffn_forward": (ctypes.c_int, [_P(zero_ffn_t), _vp, ctypes.c_int64,
+                                        _P(zero_ffn_saved_t), _vp, ctypes.c_size_t, _vp]),
+    "zero_ffn_backward": (ctypes.c_int, [_P(zero_ffn_t), _P(zero_ffn_saved_t),
+                                         _P(zero_ffn_grads_t), _vp, ctypes.c_size_t, _vp]),
     "zero_head_workspace_bytes": (ctypes.c_size_t, [_P(zero_head_t), ctypes.c_int32]),
     "zero_head_loss": (ctypes.c_int, [_P(zero_head_t), _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]),
     "zero_head_grad": (ctypes.c_int, [_P(zero_head_t), _vp, _P(zero_head_grads_t), _vp,
@@ -625,3 +652,21 @@ def zero_head_loss_grad(head, token_loss, lse, grads, workspace, ws_bytes, dev_r
     _check(lib().zero_head_loss_grad(ctypes.byref(head), _addr(token_loss), _addr(lse),
                                      ctypes.byref(grads), _addr(workspace), ws_bytes,
                                      _addr(dev_result), _stream(stream)))
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def zero_ffn_workspace_bytes(ffn: zero_ffn_t, grads=None) -> int:
+    return int(lib().zero_ffn_workspace_bytes(ctypes.byref(ffn), _ref(grads)))
+
+
+def zero_ffn_forward(ffn, y, ldy, saved, workspace, ws_bytes, stream=None):
+    _check(lib().zero_ffn_forward(ctypes.byref(ffn), _addr(y), ldy, _ref(saved),
+                                  _addr(workspace), ws_bytes, _stream(stream)))
+
+
+def zero_ffn_backward(ffn, saved, grads, workspace, ws_bytes, stream=None):
+    _check(lib().zero_ffn_backward(ctypes.byref(ffn), _ref(saved), _ref(grads),
+                                   _addr(workspace), ws_bytes, _stream(stream)))

@@ -31,9 +31,10 @@ DEVICE_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
 DEVICE_SOURCES = ("zero_kernels.hip", "zero_units.hip", "zero_noalloc.hip", "zero_tensors.hip",
-                  "zero_head.hip", "zero_head_few.hip", "zero_adam.hip")
+                  "zero_head.hip", "zero_head_few.hip", "zero_adam.hip",
+                  "zero_ffn.hip", "zero_ffn_few.hip")
 HOST_SOURCES = ("zero_host.cpp", "zero_offload.cpp", "zero_tensors.cpp", "zero_head.cpp",
-                "zero_adam.cpp")
+                "zero_adam.cpp", "zero_ffn.cpp")
 # host Adam of the offload form: IEEE fp32, no contraction, errno-free sqrt
 HOST_FLAGS = {"zero_offload.cpp": ["-ffp-contract=off", "-fno-math-errno", "-pthread"]}
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-I", INCLUDE, "-I", CSRC]

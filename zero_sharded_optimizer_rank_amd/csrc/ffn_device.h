@@ -1,0 +1,77 @@
+// Device helpers shared by the feed-forward block's kernels (zero_ffn.hip,
+// zero_ffn_few.hip): the activations.
+#pragma once
+
+#include "ffn_internal.h"
+#include "head_device.h"
+
+namespace zk {
+namespace dev {
+
+template <int A>
+struct Act {};
+
+// fn(Act<act>), one branch for the whole wave.
+template <typename Fn>
+__device__ __forceinline__ void with_act(int32_t act, Fn fn) {
+  switch (act) {
+    case ZERO_ACT_SILU: return fn(Act<ZERO_ACT_SILU>{});
+    case ZERO_ACT_GELU: return fn(Act<ZERO_ACT_GELU>{});
+    case ZERO_ACT_GELU_TANH: return fn(Act<ZERO_ACT_GELU_TANH>{});
+    default: return fn(Act<ZERO_ACT_RELU>{});
+  }
+}
+
+// 1 / (1 + e^-x): exponential and reciprocal of one unit in the last place each.
+__device__ __forceinline__ float logistic(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + exp2_fast(-kLog2e * x));
+}
+
+// The normal distribution's function and its density.  With z = |g| / sqrt 2 and t =
+// 1 / (1 + z / 2), e^(z^2) erfc(z) / t is smooth on 0 < t <= 1; the polynomial was
+// fitted to it (least largest relative error, 4.3e-8 for z up to 10), so that
+// the function keeps its digits where it is small: 3e-7 in fp32.
+__device__ __forceinline__ float normal(float g, float& density) {
+  const float z = 0.70710678118654752f * __builtin_fabsf(g);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, z, 1.0f));
+  constexpr float k[9] = {0.28208643f, 0.28237531f, 0.24310374f,  0.20268694f, -0.026625827f,
+                          0.27806741f, -0.48720014f, 0.28457508f, -0.059068985f};
+  float r = k[8];
+#pragma unroll
+  for (int i = 7; i >= 0; --i) r = __builtin_fmaf(r, t, k[i]);
+  const float e = exp2_fast(-kLog2e * z * z), tail = 0.5f * t * r * e;
+  density = 0.3989422804014327f * e;
+  return g > 0.0f ? 1.0f - tail : tail;
+}
+
+// act(g), and its slope.  (1 + tanh z) / 2 is the logistic function of 2z.
+constexpr float kGeluTanh = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+template <int A>
+__device__ __forceinline__ float activated(Act<A>, float g, float& slope) {
+  if constexpr (A == ZERO_ACT_SILU) {
+    const float s = logistic(g), a = g * s;
+    slope = s + a * (1.0f - s);
+    return a;
+  } else if constexpr (A == ZERO_ACT_GELU) {
+    float density;
+    const float c = normal(g, density);
+    slope = c + g * density;
+    return g * c;
+  } else if constexpr (A == ZERO_ACT_GELU_TANH) {
+    const float q = 0.044715f * g * g;
+    const float s = logistic(kGeluTanh * (g + g * q)), a = g * s;
+    slope = s + a * (1.0f - s) * (kGeluTanh * (1.0f + 3.0f * q));
+    return a;
+  } else {
+    slope = g > 0.0f ? 1.0f : 0.0f;
+    return g < 0.0f ? 0.0f : g;  // a NaN stays one
+  }
+}
+template <int A>
+__device__ __forceinline__ float activated(Act<A> a, float g) {
+  float slope;
+  return activated(a, g, slope);
+}
+
+}  // namespace dev
+}  // namespace zk

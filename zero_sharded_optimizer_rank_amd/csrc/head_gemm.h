@@ -195,17 +195,47 @@ struct GemmLds {
   StageLds even, odd;
 };
 
+// Where a contraction's parts come from.  A source hands out the operand of a
+// part at contraction index k, and may move k to that operand's own counting.
+struct OneProduct {  // A B^T
+  Operand A, B;
+  __device__ __forceinline__ const Operand& a0(int32_t&) const { return A; }
+  __device__ __forceinline__ const Operand& a1(int32_t&) const { return A; }
+  __device__ __forceinline__ const Operand& b(int32_t&) const { return B; }
+};
+
 // The 256 x 256 tile: 2 x 4 waves, each 8 x 4 blocks of 16 x 16.
 // acc[i][j][e] of lane l is row wm*128 + 16i + 4(l/16) + e, column wn*64 + 16j
 // + l%16, wm = wave / 4, wn = wave % 4.
-template <typename T, bool ACOLS, bool BCOLS>
+// PAIR: two products of 128 rows with one B; acc[i][j] is row wm*64 + 16i +
+// 4(l/16) + e of the first, acc[4 + i][j] that of the second (i < 4).
+template <typename T, bool ACOLS, bool BCOLS, bool PAIR = false>
 struct Gemm {
   static constexpr int BM = 256, BN = 256, THREADS = 512, MI = 8, NJ = 4;
-  using A0 = Part<128, ACOLS, 0>;
-  using A1 = Part<128, ACOLS, 1>;
+  using A0 = Part<128, ACOLS, PAIR ? -1 : 0>;
+  using A1 = Part<128, ACOLS, PAIR ? -1 : 1>;
   using SB = Part<256, BCOLS, -1>;
   using FA = Frags<128, ACOLS>;
   using FB = Frags<256, BCOLS>;
+
+  template <typename S>
+  static __device__ __forceinline__ void issue_a0(const S& s, int32_t k, lds_char* lds, int wave,
+                                                  int lane) {
+    const Operand& o = s.a0(k);
+    A0::issue(o, k, lds, wave, lane);
+  }
+  template <typename S>
+  static __device__ __forceinline__ void issue_a1(const S& s, int32_t k, lds_char* lds, int wave,
+                                                  int lane) {
+    const Operand& o = s.a1(k);
+    A1::issue(o, k, lds, wave, lane);
+  }
+  template <typename S>
+  static __device__ __forceinline__ void issue_b(const S& s, int32_t k, lds_char* lds, int wave,
+                                                 int lane) {
+    const Operand& o = s.b(k);
+    SB::issue(o, k, lds, wave, lane);
+  }
 
   template <int HALF>
   static __device__ __forceinline__ void multiply(const s16x8 (&ra)[2][4], const s16x8 (&rb)[2][4],
@@ -232,10 +262,10 @@ struct Gemm {
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  static __device__ __forceinline__ void stage(const Operand& A, const Operand& B, int32_t k0,
-                                               const StageLds& here, const StageLds& other,
-                                               int wave, int lane, const FA& fa, const FB& fb,
-                                               f32x4 (&acc)[MI][NJ]) {
+  template <typename S>
+  static __device__ __forceinline__ void stage(const S& src, int32_t k0, const StageLds& here,
+                                               const StageLds& other, int wave, int lane,
+                                               const FA& fa, const FB& fb, f32x4 (&acc)[MI][NJ]) {
     s16x8 ra[2][4], rb[2][4];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
@@ -244,15 +274,15 @@ struct Gemm {
         rb[s][i] = fb.load(here.b, i, s);
         ra[s][i] = fa.load(here.a0, i, s);
       }
-    A1::issue(A, k0 + kStage, other.a1, wave, lane);
+    issue_a1(src, k0 + kStage, other.a1, wave, lane);
     turn();
     multiply<0>(ra, rb, acc);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int i = 0; i < 4; ++i) ra[s][i] = fa.load(here.a1, i, s);
-    A0::issue(A, k0 + 2 * kStage, here.a0, wave, lane);
-    SB::issue(B, k0 + 2 * kStage, here.b, wave, lane);
+    issue_a0(src, k0 + 2 * kStage, here.a0, wave, lane);
+    issue_b(src, k0 + 2 * kStage, here.b, wave, lane);
     turn();
     multiply<1>(ra, rb, acc);
   }
@@ -261,6 +291,11 @@ struct Gemm {
   // with LDS.
   static __device__ __forceinline__ void run(const Operand& A, const Operand& B, int32_t K,
                                              const GemmLds& lds, f32x4 (&acc)[MI][NJ]) {
+    run(OneProduct{A, B}, K, lds, acc);
+  }
+  template <typename S>
+  static __device__ __forceinline__ void run(const S& src, int32_t K, const GemmLds& lds,
+                                             f32x4 (&acc)[MI][NJ]) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const FA fa(wave / 4 * 64, lane);
@@ -270,19 +305,19 @@ struct Gemm {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{};
     if (K <= 0) return;
-    A0::issue(A, 0, lds.even.a0, wave, lane);
-    SB::issue(B, 0, lds.even.b, wave, lane);
-    A1::issue(A, 0, lds.even.a1, wave, lane);
-    A0::issue(A, kStage, lds.odd.a0, wave, lane);
-    SB::issue(B, kStage, lds.odd.b, wave, lane);
+    issue_a0(src, 0, lds.even.a0, wave, lane);
+    issue_b(src, 0, lds.even.b, wave, lane);
+    issue_a1(src, 0, lds.even.a1, wave, lane);
+    issue_a0(src, kStage, lds.odd.a0, wave, lane);
+    issue_b(src, kStage, lds.odd.b, wave, lane);
     asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
     if (wave >= 4) asm volatile("s_barrier" ::: "memory");  // one phase behind
     int32_t k0 = 0;
     for (; k0 + kStage < K; k0 += 2 * kStage) {
-      stage(A, B, k0, lds.even, lds.odd, wave, lane, fa, fb, acc);
-      stage(A, B, k0 + kStage, lds.odd, lds.even, wave, lane, fa, fb, acc);
+      stage(src, k0, lds.even, lds.odd, wave, lane, fa, fb, acc);
+      stage(src, k0 + kStage, lds.odd, lds.even, wave, lane, fa, fb, acc);
     }
-    if (k0 < K) stage(A, B, k0, lds.even, lds.odd, wave, lane, fa, fb, acc);
+    if (k0 < K) stage(src, k0, lds.even, lds.odd, wave, lane, fa, fb, acc);
     if (wave < 4) asm volatile("s_barrier" ::: "memory");
     // loads past the contraction's end (zeros) may still be on their way
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
@@ -296,21 +331,37 @@ struct Gemm {
   template <typename Pack, typename Store>
   static __device__ __forceinline__ void transposed(const GemmLds& lds, const f32x4 (&acc)[MI][NJ],
                                                     Pack pack, Store store) {
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int col = j % 2 * 16 + (lane & 15);
-      lds_char* p = columns(lds, wave % 4 * 2 + j / 2) + col * 512 + (lane >> 4 & 1) * 8;
+      lds_char* p = column(lds, j);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const f32x4& v = acc[i][j];
-        const int chunk = wave / 4 * 16 + 2 * i + (lane >> 5);
-        *(__attribute__((address_space(3))) u32x2*)(p + ((chunk ^ col) << 4)) =
-            pack(v[0], v[1], v[2], v[3]);
+        put(p, i, j, pack(v[0], v[1], v[2], v[3]));
       }
     }
     __syncthreads();
+    take(lds, store);
+  }
+  // Its two halves: block column j's place, one block's four values, and the
+  // way out (between the two, and before LDS is written again, a barrier).
+  static __device__ __forceinline__ lds_char* column(const GemmLds& lds, int j) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = j % 2 * 16 + (lane & 15);
+    return columns(lds, wave % 4 * 2 + j / 2) + col * 512 + (lane >> 4 & 1) * 8;
+  }
+  static __device__ __forceinline__ void put(lds_char* p, int i, int j, u32x2 v) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = j % 2 * 16 + (lane & 15);
+    const int chunk = wave / 4 * 16 + 2 * i + (lane >> 5);
+    *(__attribute__((address_space(3))) u32x2*)(p + ((chunk ^ col) << 4)) = v;
+  }
+  template <typename Store>
+  static __device__ __forceinline__ void take(const GemmLds& lds, Store store) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 31, hi = lane >> 5;
     const lds_char* p = columns(lds, wave);
 #pragma unroll
@@ -318,6 +369,30 @@ struct Gemm {
       const int col = 2 * k + hi;
       store(wave * 32 + col, r * 8,
             *(const __attribute__((address_space(3))) u32x4*)(p + col * 512 + ((r ^ col) << 4)));
+    }
+  }
+  // PAIR: what both products make, 128 rows (i < 4) in 16 bits; a column takes
+  // 256 bytes, its chunk c at c ^ (col % 16), and 16 lanes.
+  static __device__ __forceinline__ void put_half(const GemmLds& lds, int i, int j, u32x2 v) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = j % 2 * 16 + (lane & 15);
+    const int chunk = wave / 4 * 8 + 2 * i + (lane >> 5);
+    lds_char* p = columns(lds, wave % 4 * 2 + j / 2) + col * 256 + (lane >> 4 & 1) * 8;
+    *(__attribute__((address_space(3))) u32x2*)(p + ((chunk ^ (col & 15)) << 4)) = v;
+  }
+  template <typename Store>
+  static __device__ __forceinline__ void take_half(const GemmLds& lds, Store store) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15;
+    const lds_char* p = columns(lds, wave);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int col = 4 * k + (lane >> 4);
+      store(wave * 32 + col, r * 8,
+            *(const __attribute__((address_space(3))) u32x4*)(p + col * 256 +
+                                                              ((r ^ (col & 15)) << 4)));
     }
   }
 

@@ -1,0 +1,238 @@
+// Host side of the gated feed-forward block: argument checks and the workspace
+// plan.
+#include <stdint.h>
+
+#include <hip/hip_runtime_api.h>
+
+#include "ffn_internal.h"
+#include "host_internal.h"
+#include "zero_shard.h"
+
+using namespace zk::host;
+
+namespace {
+
+int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+int64_t tiles(int64_t x, int64_t tile) { return (x + tile - 1) / tile; }
+
+bool good_ld(int64_t ld, int64_t width) { return ld >= width && ld <= ZERO_FFN_MAX_WIDTH; }
+
+bool good_sizes(const zero_ffn_t* f) {
+  return f->tokens >= 0 && f->tokens <= ZERO_FFN_MAX_TOKENS && f->hidden >= 1 &&
+         f->hidden <= ZERO_FFN_MAX_WIDTH && f->inner >= 1 && f->inner <= ZERO_FFN_MAX_WIDTH &&
+         good_ld(f->ldx, f->hidden) && good_ld(f->ld_gate, f->hidden) &&
+         good_ld(f->ld_up, f->hidden) && good_ld(f->ld_down, f->inner) &&
+         (f->dtype == ZERO_F16 || f->dtype == ZERO_BF16) && f->act >= ZERO_ACT_SILU &&
+         f->act <= ZERO_ACT_RELU &&
+         // tiles of one launch, 512 threads each, of at most 2^32 - 1
+         tiles(f->tokens, 256) * tiles(f->inner, 128) < ZERO_FFN_MAX_TILES &&
+         tiles(f->tokens, 256) * tiles(f->hidden, 256) < ZERO_FFN_MAX_TILES &&
+         3 * tiles(f->inner, 256) * tiles(f->hidden, 256) < ZERO_FFN_MAX_TILES;
+}
+
+int check_ffn(const zero_ffn_t* f) {
+  if (!f) return fail(ZERO_EINVAL, "ffn is NULL");
+  if (!good_sizes(f))
+    return fail(ZERO_EINVAL, "ffn sizes: tokens %lld hidden %lld inner %lld ld %lld %lld %lld %lld "
+                "dtype %d act %d", (long long)f->tokens, (long long)f->hidden,
+                (long long)f->inner, (long long)f->ldx, (long long)f->ld_gate,
+                (long long)f->ld_up, (long long)f->ld_down, f->dtype, f->act);
+  if (!f->w_gate || !f->w_up || !f->w_down || (f->tokens > 0 && !f->x))
+    return fail(ZERO_EINVAL, "x or a weight is NULL");
+  if (!aligned(f->x, 2) || !aligned(f->w_gate, 2) || !aligned(f->w_up, 2) ||
+      !aligned(f->w_down, 2))
+    return fail(ZERO_EALIGN, "x and the weights must be 2-byte aligned");
+  return ZERO_OK;
+}
+
+int check_saved(const zero_ffn_t* f, const zero_ffn_saved_t* s) {
+  if (s->ld < up(f->inner, 8) || s->ld % 8 || s->ld > ZERO_FFN_MAX_WIDTH)
+    return fail(ZERO_EINVAL, "rows of gate and up %lld apart", (long long)s->ld);
+  if (f->tokens > 0 && (!s->gate || !s->up)) return fail(ZERO_EINVAL, "gate or up is NULL");
+  if (!aligned(s->gate, 16) || !aligned(s->up, 16))
+    return fail(ZERO_EALIGN, "gate and up must be 16-byte aligned");
+  return ZERO_OK;
+}
+
+struct Range {
+  const void* p;
+  size_t n;
+  const char* name;
+};
+Range matrix(const void* p, int64_t rows, int64_t ld, int64_t cols, size_t elem, const char* name) {
+  return {p, p && rows > 0 ? elem * (size_t)((rows - 1) * ld + cols) : 0, name};
+}
+
+// No output over another output, an input or the workspace.
+int check_apart(const Range* out, int n_out, const Range* in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (out[i].n && out[j].n && overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+        return fail(ZERO_EINVAL, "%s overlaps %s", out[i].name, out[j].name);
+    for (int j = 0; j < n_in; ++j)
+      if (out[i].n && in[j].n && overlap(out[i].p, out[i].n, in[j].p, in[j].n))
+        return fail(ZERO_EINVAL, "%s overlaps %s", out[i].name, in[j].name);
+  }
+  return ZERO_OK;
+}
+
+int check_workspace(size_t need, const void* ws, size_t ws_bytes) {
+  if (!ws) return fail(ZERO_EINVAL, "workspace is NULL");
+  if (!aligned(ws, 256)) return fail(ZERO_EALIGN, "workspace not 256-byte aligned");
+  if (ws_bytes < need) return fail(ZERO_ENOSPC, "workspace %zu bytes < %zu", ws_bytes, need);
+  return ZERO_OK;
+}
+
+// Rows that 16-byte loads do not fit.
+bool ragged(const void* p, int64_t ld, int64_t width) {
+  return width % 8 != 0 || ld % 8 != 0 || !aligned(p, 16);
+}
+
+// Ways to split a contraction whose output has few tiles: up to one round of
+// the 256 CUs, of at least four stages each.
+int32_t split_of(int64_t out_tiles, int64_t k) {
+  const int64_t stages = tiles(k, zk::kFfnStep);
+  int64_t s = 256 / (out_tiles > 0 ? out_tiles : 1);
+  if (s > stages / 4) s = stages / 4;
+  return (int32_t)(s < 1 ? 1 : s);
+}
+
+}  // namespace
+
+namespace zk {
+
+FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
+  FfnPlan p{};
+  const int64_t T = f->tokens, H = f->hidden, F = f->inner;
+  p.hidden_pad = up(H, 8);
+  p.inner_pad = up(F, 8);
+  p.few = !g && T <= kFfnFew;
+  if (!p.few) {
+    p.pack_x = ragged(f->x, f->ldx, H);
+    p.pack_gate = ragged(f->w_gate, f->ld_gate, H);
+    p.pack_up = ragged(f->w_up, f->ld_up, H);
+    p.pack_down = ragged(f->w_down, f->ld_down, F);
+    p.pack_dy = g && ragged(g->dy, g->lddy, H);
+  }
+  const int64_t out_tiles = tiles(T, kFfnTile) * tiles(H, kFfnTile);
+  p.split_y = p.split_dx = 1;
+  if (!p.few && !g) p.split_y = split_of(out_tiles, F);
+  if (g) p.split_dx = split_of(out_tiles, 2 * F);
+  size_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t o = at;
+    at += (size_t)(bytes + 255) / 256 * 256;
+    return o;
+  };
+  p.x = take(p.pack_x ? 2 * T * p.hidden_pad : 0);
+  p.w_gate = take(p.pack_gate ? 2 * F * p.hidden_pad : 0);
+  p.w_up = take(p.pack_up ? 2 * F * p.hidden_pad : 0);
+  p.w_down = take(p.pack_down ? 2 * H * p.inner_pad : 0);
+  p.dy = take(p.pack_dy ? 2 * T * p.hidden_pad : 0);
+  p.h = take(2 * T * p.inner_pad);
+  if (g) {
+    p.dg = take(2 * T * p.inner_pad);
+    p.du = take(2 * T * p.inner_pad);
+  }
+  const int32_t split = g ? p.split_dx : p.split_y;
+  p.acc = take(split > 1 ? 4 * split * up(T, kFfnTile) * up(H, kFfnTile) : 0);
+  p.total = at > 0 ? at : 256;
+  return p;
+}
+
+}  // namespace zk
+
+extern "C" {
+
+size_t zero_ffn_workspace_bytes(const zero_ffn_t* ffn, const zero_ffn_grads_t* grads) {
+  if (!ffn || !good_sizes(ffn) || (grads && !good_ld(grads->lddy, ffn->hidden))) return 0;
+  // a batch of fewer tokens may be split more ways; the plan changes by the tile
+  zero_ffn_t f = *ffn;
+  size_t need = 0;
+  const auto count = [&](int64_t tokens) {
+    f.tokens = tokens < ffn->tokens ? tokens : ffn->tokens;
+    const size_t n = zk::ffn_plan(&f, grads).total;
+    if (n > need) need = n;
+  };
+  count(zk::kFfnFew);
+  for (int64_t t = 0; t < ffn->tokens; t += zk::kFfnTile) count(t + zk::kFfnTile);
+  return need;
+}
+
+int zero_ffn_forward(const zero_ffn_t* ffn, void* y, int64_t ldy, const zero_ffn_saved_t* saved,
+                     void* workspace, size_t ws_bytes, hipStream_t stream) {
+  g_err[0] = 0;
+  int rc = check_ffn(ffn);
+  if (rc) return rc;
+  const int64_t T = ffn->tokens, H = ffn->hidden, F = ffn->inner;
+  if (T > 0 && !y) return fail(ZERO_EINVAL, "y is NULL");
+  if (!good_ld(ldy, H)) return fail(ZERO_EINVAL, "ldy %lld", (long long)ldy);
+  if (!aligned(y, 2)) return fail(ZERO_EALIGN, "y must be 2-byte aligned");
+  if (saved) rc = check_saved(ffn, saved);
+  if (rc) return rc;
+  const zk::FfnPlan p = zk::ffn_plan(ffn, nullptr);
+  rc = check_workspace(p.total, workspace, ws_bytes);
+  if (rc) return rc;
+  const int64_t Fp = p.inner_pad;
+  const Range out[4] = {matrix(y, T, ldy, H, 2, "y"),
+                        matrix(saved ? saved->gate : nullptr, T, saved ? saved->ld : 0, Fp, 2,
+                               "gate"),
+                        matrix(saved ? saved->up : nullptr, T, saved ? saved->ld : 0, Fp, 2, "up"),
+                        {workspace, p.total, "workspace"}};
+  const Range in[4] = {matrix(ffn->x, T, ffn->ldx, H, 2, "x"),
+                       matrix(ffn->w_gate, F, ffn->ld_gate, H, 2, "w_gate"),
+                       matrix(ffn->w_up, F, ffn->ld_up, H, 2, "w_up"),
+                       matrix(ffn->w_down, H, ffn->ld_down, F, 2, "w_down")};
+  rc = check_apart(out, 4, in, 4);
+  if (rc || T == 0) return rc;
+  const int e = p.few ? zk::launch_ffn_few(ffn, p, workspace, y, ldy, saved, stream)
+                      : zk::launch_ffn_forward(ffn, p, workspace, y, ldy, saved, stream);
+  return hip_status(e, "ffn_forward launch");
+}
+
+int zero_ffn_backward(const zero_ffn_t* ffn, const zero_ffn_saved_t* saved,
+                      const zero_ffn_grads_t* g, void* workspace, size_t ws_bytes,
+                      hipStream_t stream) {
+  g_err[0] = 0;
+  int rc = check_ffn(ffn);
+  if (rc) return rc;
+  const int64_t T = ffn->tokens, H = ffn->hidden, F = ffn->inner;
+  if (!saved || !g) return fail(ZERO_EINVAL, "saved or grads is NULL");
+  rc = check_saved(ffn, saved);
+  if (rc) return rc;
+  if (g->dw_dtype != ffn->dtype && g->dw_dtype != ZERO_F32)
+    return fail(ZERO_EINVAL, "dw_dtype %d: the type of the weights or fp32", g->dw_dtype);
+  if (T > 0 && !g->dy) return fail(ZERO_EINVAL, "dy is NULL");
+  if (!good_ld(g->lddy, H) || (g->dx && !good_ld(g->lddx, H)) ||
+      (g->dw_gate && !good_ld(g->lddw_gate, H)) || (g->dw_up && !good_ld(g->lddw_up, H)) ||
+      (g->dw_down && !good_ld(g->lddw_down, F)))
+    return fail(ZERO_EINVAL, "rows of the gradients %lld %lld %lld %lld %lld apart",
+                (long long)g->lddy, (long long)g->lddx, (long long)g->lddw_gate,
+                (long long)g->lddw_up, (long long)g->lddw_down);
+  const size_t ew = g->dw_dtype == ZERO_F32 ? 4 : 2;
+  if (!aligned(g->dy, 2) || !aligned(g->dx, 2) || !aligned(g->dw_gate, ew) ||
+      !aligned(g->dw_up, ew) || !aligned(g->dw_down, ew))
+    return fail(ZERO_EALIGN, "gradients must be aligned to their elements");
+  const zk::FfnPlan p = zk::ffn_plan(ffn, g);
+  rc = check_workspace(p.total, workspace, ws_bytes);
+  if (rc) return rc;
+  const int64_t Fp = p.inner_pad;
+  const Range out[5] = {matrix(g->dx, T, g->lddx, H, 2, "dx"),
+                        matrix(g->dw_gate, F, g->lddw_gate, H, ew, "dw_gate"),
+                        matrix(g->dw_up, F, g->lddw_up, H, ew, "dw_up"),
+                        matrix(g->dw_down, H, g->lddw_down, F, ew, "dw_down"),
+                        {workspace, p.total, "workspace"}};
+  const Range in[7] = {matrix(ffn->x, T, ffn->ldx, H, 2, "x"),
+                       matrix(ffn->w_gate, F, ffn->ld_gate, H, 2, "w_gate"),
+                       matrix(ffn->w_up, F, ffn->ld_up, H, 2, "w_up"),
+                       matrix(ffn->w_down, H, ffn->ld_down, F, 2, "w_down"),
+                       matrix(g->dy, T, g->lddy, H, 2, "dy"),
+                       matrix(saved->gate, T, saved->ld, Fp, 2, "gate"),
+                       matrix(saved->up, T, saved->ld, Fp, 2, "up")};
+  rc = check_apart(out, 5, in, 7);
+  if (rc) return rc;
+  return hip_status(zk::launch_ffn_backward(ffn, p, workspace, saved, g, stream),
+                    "ffn_backward launch");
+}
+
+}  // extern "C"
