@@ -713,7 +713,8 @@ typedef struct zero_adam_tensor {
 /* A prepared list; filled by zero_tensors_adam_prepare, not changed by others. */
 typedef struct zero_adam_list {
   void* table;       /* device, the caller's */
-  int64_t blocks;    /* workgroups of a step */
+  int64_t blocks32;  /* workgroups of a step: tensors with 32-bit moments, */
+  int64_t blocks8;   /*   and with 8-bit ones */
   int64_t elements;  /* sum of the numels, each rounded up to ZERO_ADAM_BLOCK */
   int32_t n_tensors;
   int32_t reserved;
@@ -732,7 +733,7 @@ size_t zero_adam_table_bytes(int32_t n_tensors);
  *            as written while steps use it
  *   list     host, filled on success
  * Errors: ZERO_EINVAL (sizes, dtypes, moment_bits, weight_decay, lr_scale, NULL
- * pointers, buffers of one entry that overlap, more than 2^42 elements),
+ * pointers, buffers of one entry that overlap, more than 2^39 elements),
  * ZERO_EALIGN, ZERO_ENOSPC (table), ZERO_EHIP.
  */
 int zero_tensors_adam_prepare(const zero_adam_tensor_t* tensors, int32_t n_tensors, void* table,
@@ -758,7 +759,9 @@ int zero_tensors_adam_prepare(const zero_adam_tensor_t* tensors, int32_t n_tenso
  *   r = mix(mix(mix(mix(seed) + t) + (i >> 12)) + (i & 4095)), u = r & 0xFFFF for m,
  *   r >> 16 for v;
  *   mix(x): x ^= x >> 16; x *= 0x7FEB352D; x ^= x >> 15; x *= 0x846CA68B; x ^= x >> 16
- * The parameter is updated from the moments before they are rounded.
+ * The parameter is updated from the moments before they are rounded; there, where the
+ * moments keep 3 bits, the root and the two quotients are those of the instructions (one
+ * unit in the last place each, the first quotient as a product with the reciprocal).
  * Errors: ZERO_EINVAL (a list not prepared, args as zero_adam_apply), ZERO_EALIGN,
  * ZERO_EHIP.
  */

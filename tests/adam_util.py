@@ -76,14 +76,19 @@ def update32(g, p, m, v, s):
     return p, m, v
 
 
-def update64(g, p, m, v, s):
+def update64(g, p, m, v, s, bits=32):
     """The same in fp64 with the fp32 scalars, and how far each fp32 result can be off.
 
     Roundings (each at most E relative to its result): gc two; m the products b1 m (one) and
     (1-b1) gc (one more than gc's two) and their sum; v's terms are positive, gc^2 carries twice
     gc's two and one, its product one, the sum one, under 8 E in all; the root halves that and
     adds one, the division and the sum with eps one each, under 7 E; the division, the product,
-    then p's product and the difference.  1.01 covers the second order."""
+    then p's product and the difference.  1.01 covers the second order.
+
+    With 8-bit moments the root and the reciprocals are off by one unit in the last place (2 E):
+    the root 4 E + 2 E, the product with the rounded 1 / root two more (and one for this
+    reference's own rounded root), the sum with eps one, the reciprocal 2 E, its product and
+    the next one each: 14 E."""
     s = {k: np.float64(x) for k, x in s.items()}
     g, p, m, v = (np.asarray(x, dtype=np.float64) for x in (g, p, m, v))
     gc = g * s["scale"] * s["c"]
@@ -93,7 +98,7 @@ def update64(g, p, m, v, s):
     dv = 8 * E * v1
     den = np.sqrt(v1) / s["root"] + s["eps"]
     u = m1 / den * s["step_size"]
-    du = np.abs(u) * 9 * E + dm / den * s["step_size"]
+    du = np.abs(u) * (9 if bits == 32 else 14) * E + dm / den * s["step_size"]
     p1 = p * s["decay"] - u
     dp = E * (np.abs(p * s["decay"]) + np.abs(p1)) + du
     return (p1, m1, v1), tuple(1.01 * d for d in (dp, dm, dv))

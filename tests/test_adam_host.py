@@ -30,7 +30,7 @@ def _prepare(entries, n=None, table=TABLE, table_bytes=1 << 20):
                                   table, table_bytes)
 
 
-LIST = abi.zero_adam_list_t(TABLE, 1, 128, 1, 0)
+LIST = abi.zero_adam_list_t(TABLE, 0, 1, 128, 1, 0)
 
 
 def _step(adam_list=LIST, args=None, res=None):
@@ -47,7 +47,7 @@ def _read(m=BASE, v=BASE + STEP, dtype=abi.ZERO_F32, adam_list=LIST):
     (lambda: _prepare([_entry()], table=TABLE + 4), abi.ZERO_EALIGN),
     (lambda: _prepare([_entry()], table_bytes=32), abi.ZERO_ENOSPC),
     (lambda: _prepare([_entry(numel=-1)]), abi.ZERO_EINVAL),
-    (lambda: _prepare([_entry(numel=(1 << 42) + 1)]), abi.ZERO_EINVAL),
+    (lambda: _prepare([_entry(numel=(1 << 39) + 1)]), abi.ZERO_EINVAL),
     (lambda: _prepare([_entry(grad_dtype=3)]), abi.ZERO_EINVAL),
     (lambda: _prepare([_entry(param_dtype=-1)]), abi.ZERO_EINVAL),
     (lambda: _prepare([_entry(moment_bits=16)]), abi.ZERO_EINVAL),
@@ -68,7 +68,7 @@ def _read(m=BASE, v=BASE + STEP, dtype=abi.ZERO_F32, adam_list=LIST):
     (lambda: _prepare([_entry(v=BASE + 2 * STEP + 96)]), abi.ZERO_EINVAL),   # over m's last codes
     (lambda: _prepare([_entry(), _entry(m_exp=BASE + 5 * STEP)]), abi.ZERO_EINVAL),
     (lambda: _step(abi.zero_adam_list_t()), abi.ZERO_EINVAL),
-    (lambda: _step(abi.zero_adam_list_t(TABLE, 1 << 33, 1, 1, 0)), abi.ZERO_EINVAL),
+    (lambda: _step(abi.zero_adam_list_t(TABLE, 1 << 33, 0, 1, 1, 0)), abi.ZERO_EINVAL),
     (lambda: _step(args=_args(lr=-1.0)), abi.ZERO_EINVAL),
     (lambda: _step(args=_args(beta1=1.0)), abi.ZERO_EINVAL),
     (lambda: _step(args=_args(step=0)), abi.ZERO_EINVAL),

@@ -1,7 +1,7 @@
 """AdamW over tensor lists (zero_tensors_adam) on the GPU: against the same fp32 operations on
 the CPU, bit for bit, 8-bit moments and their random rounding included; against 64-bit values
-within the bounds of adam_util.update64 (the roundings counted there); and against the shard
-update (zero_adam_apply)."""
+within the bounds of adam_util.update64 (the roundings counted there; the parameters of 8-bit
+moments go by it alone); and against the shard update (zero_adam_apply)."""
 import math
 
 import numpy as np
@@ -102,8 +102,12 @@ class Run:
     def expect(self, coef=1.0, **kw):
         """The CPU side takes the step; codes and exponents stay in self.codes."""
         seed = kw.get("seed", kw["step"])
-        self.codes = []
+        self.codes, self.near = [], []
         for i, n in enumerate(self.sizes):
+            if self.bits == 8:
+                want, far = au.update64(self.g[i], self.p[i], self.m[i], self.v[i],
+                                        self.scalars(i, coef, **kw), bits=8)
+                self.near.append((want[0], far[0]))
             self.p[i], m, v = au.update32(self.g[i], self.p[i], self.m[i], self.v[i],
                                           self.scalars(i, coef, **kw))
             if self.bits == 8:
@@ -118,6 +122,10 @@ class Run:
         m, v = self.list.moments()
         for i, n in enumerate(self.sizes):
             at = self.state.offsets[i]
+            if self.bits == 8:
+                want, far = self.near[i]
+                self.p[i] = self.masters[i].cpu().numpy()  # the next step goes on from here
+                assert (np.abs(self.p[i].astype(np.float64) - want) <= far).all(), f"master {i}"
             assert _same(self.masters[i], self.p[i]), f"master {i}"
             assert _same(m[at:at + n].float(), self.m[i]), f"m {i}"
             assert _same(v[at:at + n].float(), self.v[i]), f"v {i}"
@@ -207,7 +215,7 @@ def test_within_the_roundings_of_64_bits(bits):
     g, p, m, v = (x[0].copy() for x in (r.g, r.p, r.m, r.v))
     kw = dict(lr=1e-3, step=20, loss_scale=7.0)
     r.list.step(**kw)
-    want, far = au.update64(g, p, m, v, r.scalars(0, **kw))
+    want, far = au.update64(g, p, m, v, r.scalars(0, **kw), bits)
     assert (np.abs(r.masters[0].double().cpu().numpy() - want[0]) <= far[0]).all()
     got = [t[:50_000].double().cpu().numpy() for t in r.list.moments()]
     for x, y, d, octaves in zip(got, want[1:], far[1:], (16, 32)):
@@ -265,6 +273,20 @@ def test_seeds_and_tensors_round_apart():
         same = f * f + (1 - f) * (1 - f)
         far = 5 * math.sqrt(same * (1 - same) / x.numel())
         assert abs((x == y).float().mean().item() - same) < far
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_small_roots_without_eps(bits):
+    """eps = 0 and v down to the smallest fp32: the first step is lr in every element that moves
+    (v below 2^-149 is zero, and m / 0 infinite, in fp32 too)."""
+    AdamList, AdamState = _mods()
+    g = torch.from_numpy(np.exp2(np.linspace(-64, 40, 500)).astype(np.float32)).cuda()
+    w = torch.zeros_like(g)
+    AdamList([g], [w], AdamState([500], bits=bits)).step(lr=2.0 ** -10, eps=0.0, step=1,
+                                                         beta2=0.5)
+    # v = g^2 / 2 from 2^-129, of which fp32 keeps 20 bits at least: 2^-21 of it, half of that
+    # in the root, and 14 E < 2^-20
+    assert ((w.double() + 2.0 ** -10).abs() <= 2.0 ** -10 * (2.0 ** -22 + 2.0 ** -20)).all()
 
 
 def test_wide_blocks():
@@ -425,7 +447,11 @@ def test_offsets_past_32_bits(bits):
     off = state.offsets[1]
     for at, x in zip(windows, data):
         p1, m1, v1 = au.update32(x, zero, zero, zero, s)
-        assert _same(w[at:at + k], p1)
+        if bits == 32:
+            assert _same(w[at:at + k], p1)
+        else:
+            want, far = au.update64(x, zero, zero, zero, s, bits)
+            assert (np.abs(w[at:at + k].double().cpu().numpy() - want[0]) <= far[0]).all()
         if bits == 8:
             r = au.random_bits(77, 1, at, k)
             m1 = au.decode(*au.encode(m1, r & np.uint32(0xFFFF), 16, 7), 16, 7)

@@ -141,6 +141,9 @@ class AdamList:
             self.list = abi.zero_tensors_adam_prepare(abi.adam_table(entries), n, self.table, size,
                                                       stream_of(device, None))
         self._read = None
+        # filled by each step: making it anew would take a third of a short list's time
+        self._args = abi.step_args(lr=0.0, beta1=0.0, beta2=0.0, eps=0.0, weight_decay=0.0,
+                                   max_grad_norm=0.0, loss_scale=1.0, step=1)
 
     def step(self, *, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
              step: int, loss_scale: float = 1.0, norm: Optional[GradList] = None,
@@ -157,8 +160,9 @@ class AdamList:
             if not norm._normed:
                 raise RuntimeError("the clip coefficient comes from a norm of that list")
             result = norm._res
-        args = abi.step_args(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=0.0,
-                             max_grad_norm=0.0, loss_scale=loss_scale, step=step)
+        args = self._args
+        args.lr, args.beta1, args.beta2, args.eps = lr, beta1, beta2, eps
+        args.loss_scale, args.step = loss_scale, step
         seed = (step if seed is None else seed) & 0xFFFFFFFF
         handle = stream_of(self.device, stream)
         with on_device(self.device):

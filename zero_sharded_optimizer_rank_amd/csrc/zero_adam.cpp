@@ -14,8 +14,7 @@ namespace {
 
 bool known(int32_t dtype) { return dtype == ZERO_F32 || dtype == ZERO_F16 || dtype == ZERO_BF16; }
 size_t elem_bytes(int32_t dtype) { return dtype == ZERO_F32 ? 4 : 2; }
-// Elements of a list: its workgroups are counted in 32 bits.
-constexpr int64_t kMostElements = (int64_t)1 << 42;
+constexpr int64_t kMostElements = (int64_t)1 << 39;  // workgroups are counted in 32 bits
 
 int check_tensor(const zero_adam_tensor_t& t, int32_t i) {
   if (t.numel < 0 || t.numel > kMostElements)
@@ -58,7 +57,8 @@ int check_tensor(const zero_adam_tensor_t& t, int32_t i) {
 
 int check_list(const zero_adam_list_t* l) {
   if (!l) return fail(ZERO_EINVAL, "list is NULL");
-  if (!l->table || l->n_tensors < 0 || l->blocks < 0 || l->blocks > UINT32_MAX)
+  if (!l->table || l->n_tensors < 0 || l->blocks32 < 0 || l->blocks32 > UINT32_MAX ||
+      l->blocks8 < 0 || l->blocks8 > UINT32_MAX)
     return fail(ZERO_EINVAL, "list was not prepared");
   return ZERO_OK;
 }
@@ -69,7 +69,7 @@ extern "C" {
 
 size_t zero_adam_table_bytes(int32_t n_tensors) {
   if (n_tensors < 0) return 0;
-  return (sizeof(zk::AdamEntry) + sizeof(uint32_t)) * (size_t)(n_tensors > 0 ? n_tensors : 1);
+  return (sizeof(zk::AdamEntry) + 2 * sizeof(uint32_t)) * (size_t)(n_tensors > 0 ? n_tensors : 1);
 }
 
 int zero_tensors_adam_prepare(const zero_adam_tensor_t* tensors, int32_t n_tensors, void* table,
@@ -79,21 +79,23 @@ int zero_tensors_adam_prepare(const zero_adam_tensor_t* tensors, int32_t n_tenso
   if (!list) return fail(ZERO_EINVAL, "list is NULL");
   if (!table) return fail(ZERO_EINVAL, "table is NULL");
   if (!aligned(table, 8)) return fail(ZERO_EALIGN, "table not 8-byte aligned");
-  int64_t total = 0, blocks = 0, elements = 0;
+  int64_t total = 0, blocks[2] = {0, 0}, elements = 0;
   for (int32_t i = 0; i < n_tensors; ++i) {
     const int rc = check_tensor(tensors[i], i);
     if (rc) return rc;
     total += tensors[i].numel;
     if (total > kMostElements) return fail(ZERO_EINVAL, "too many elements");
-    blocks += zk::adam_blocks(tensors[i].numel);
+    const bool small = tensors[i].moment_bits == 8;
+    blocks[small] += zk::adam_blocks(tensors[i].numel, small);
     elements += (tensors[i].numel + ZERO_ADAM_BLOCK - 1) / ZERO_ADAM_BLOCK * ZERO_ADAM_BLOCK;
   }
-  if (blocks > UINT32_MAX) return fail(ZERO_EINVAL, "too many elements");
+  if (blocks[0] > UINT32_MAX || blocks[1] > UINT32_MAX)
+    return fail(ZERO_EINVAL, "too many elements");
   const size_t need = zero_adam_table_bytes(n_tensors);
   if (table_bytes < need) return fail(ZERO_ENOSPC, "table %zu bytes < %zu", table_bytes, need);
   const int e = zk::launch_adam_table(tensors, n_tensors, table, stream);
   if (e) return hip_status(e, "adam table launch");
-  *list = zero_adam_list_t{table, blocks, elements, n_tensors, 0};
+  *list = zero_adam_list_t{table, blocks[0], blocks[1], elements, n_tensors, 0};
   return ZERO_OK;
 }
 
@@ -116,6 +118,7 @@ int zero_tensors_adam(const zero_adam_list_t* list, const zero_step_args_t* args
   s.omb2 = (float)(1.0 - args->beta2);
   s.eps = (float)args->eps;
   s.sqrt_bc2 = (float)sqrt(c2);
+  s.inv_root = (float)(0x1p-12 / sqrt(c2));
   s.scale = scale;
   s.key = seed;
   s.step_size = args->lr / c1;
