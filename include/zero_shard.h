@@ -895,8 +895,8 @@ int zero_head_loss_grad(const zero_head_t* head, float* token_loss, float* lse,
  *   dh = dy Wd,  du = dh act(g),  dg = dh u act'(g)
  *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h
  * Sums are fp32.  h, dg and du are rounded once to the 16-bit type (the matrix cores
- * multiply it), g and u where they are kept for the gradients; in fp16 what passes
- * 65504 becomes infinite.  Gradients carry whatever loss scale dy carries.  Equal
+ * multiply it), and so are act(g) and u act'(g), which are kept for the gradients; in
+ * fp16 what passes 65504 becomes infinite.  Gradients carry whatever loss scale dy carries.  Equal
  * inputs give equal bits. */
 
 enum zero_act {
@@ -925,11 +925,13 @@ typedef struct zero_ffn {
   int32_t act;                    /* zero_act */
 } zero_ffn_t;
 
-/* What the gradients need of the forward pass: g and u in 16 bits. */
+/* What the gradients need of the forward pass, in 16 bits: formed there from the fp32
+ * sums, so that the backward pass has two products an element left to do. */
 typedef struct zero_ffn_saved {
-  void* gate;  /* device [T, F rounded up to 8], 16-byte aligned */
-  void* up;    /* the same */
-  int64_t ld;  /* elements between rows, a multiple of 8, >= F rounded up to 8 */
+  void* act;    /* act(g): device [T, F rounded up to 8], 16-byte aligned */
+  void* slope;  /* u act'(g): the same */
+  void* h;      /* the same */
+  int64_t ld;   /* elements between rows, a multiple of 8, >= F rounded up to 8 */
 } zero_ffn_saved_t;
 
 typedef struct zero_ffn_grads {
@@ -956,7 +958,7 @@ size_t zero_ffn_workspace_bytes(const zero_ffn_t* ffn, const zero_ffn_grads_t* g
 /*
  * zero_ffn_forward: y.
  *   y          device [T, H], type of x, row t at y + t*ldy; 2-byte aligned
- *   saved      host, or NULL: g and u are kept there
+ *   saved      host, or NULL: what the gradients need is kept there
  *   workspace  device, >= zero_ffn_workspace_bytes(ffn, NULL), 256-byte aligned; its
  *              content on entry does not matter
  * T = 0 does nothing.

@@ -6,21 +6,20 @@ step, e = 2^-23 bounds one fp32 operation (the matrix cores may truncate); a len
 terms a_i is off by at most n e sum |a_i|.
 
 g          bg = H e (|x| |Wg|^T) (16-bit products are exact in fp32); u's likewise bu
-kept       g and u rounded once: sg = bg + u (|g| + bg) + tiny, su likewise
 a          all slopes are at most 1.2: 1.2 times g's error, and the evaluation: the exponential's
            argument is formed in a few operations, each off by e of itself, of size at most
            2 (|g| + g^2 + |g|^3) for every activation, and some 16 operations follow:
            ea = |a| e (16 + 8 (|g| + g^2 + |g|^3)) + 1e-30 (underflow)
 slope      second derivatives are at most 1: g's error, and es = e (1 + |g|) (16 + 8 (|g| + g^2 +
            |g|^3)) (1 + |slope|); relu: wrong by 1 where g is within its error of 0
-h          forward: errors of a and u through the product, one fp32 operation, one rounding;
-           backward: the same from the kept g and u
+h          errors of a and u through the product, one fp32 operation, one rounding
+kept       a and b = u slope with their errors, one rounding each
 y          h's error through |Wd|, F e (|h| |Wd|^T), one rounding
 dh         H e (|dy| |Wd|), not rounded
-du, dg     products of dh with a, u and slope, an operation each, one rounding
+du, dg     products of dh with the kept a and b, one operation, one rounding
 dx         their errors through the weights, 2 F e of the absolute sums, one rounding
 dw         errors of dg, du, h through |x| and |dy|, T e of the absolute sums, then the output's
-All first order; relative errors up to 3 u appear in products of three, so a factor 1.05 covers
+All first order; relative errors of a few u appear in products of two, so a factor 1.05 covers
 the products of errors.
 """
 import math
@@ -61,30 +60,29 @@ def reference(x, wg, wu, wd, name, dy=None):
     size = 16 + 8 * (r + r ** 2 + r ** 3)
     ea = a.abs() * E * size + 1e-30
 
-    def product(dg, dv):  # h's error from g's and u's, rounded
-        da = 1.2 * dg + ea
-        d = da * v.abs() + a.abs() * dv + E * (a * v).abs()
-        return d + u * ((a * v).abs() + d) + tiny, da
+    da = 1.2 * bg + ea
     h = a * v
-    dh_, _ = product(bg, bv)
+    bh = da * v.abs() + a.abs() * bv + E * h.abs()
+    bh = bh + u * (h.abs() + bh) + tiny
     y = h @ D.t()
-    by = dh_ @ D.abs().t() + F * E * ((h.abs() + dh_) @ D.abs().t())
+    by = bh @ D.abs().t() + F * E * ((h.abs() + bh) @ D.abs().t())
     out = {"u": u, "tiny": tiny, "y": (y, 1.05 * (by + u * y.abs()) + tiny)}
     if dy is None:
         return out
-    sg, sv = bg + u * (g.abs() + bg) + tiny, bv + u * (v.abs() + bv) + tiny
-    dhk, da = product(sg, sv)
+    es = bg + E * (1 + r) * size * (1 + slope.abs())
+    if name == "relu":
+        es = (r <= bg).double()
+    b = v * slope
+    db = bv * slope.abs() + v.abs() * es + E * b.abs()
+    sa, sb = da + u * (a.abs() + da) + tiny, db + u * (b.abs() + db) + tiny
     Y = dy.double()
     dh = Y @ D
     bdh = H * E * (Y.abs() @ D.abs())
     du = dh * a
-    bdu = bdh * a.abs() + dh.abs() * da + E * du.abs()
+    bdu = bdh * a.abs() + dh.abs() * sa + E * du.abs()
     bdu = 1.05 * (bdu + u * du.abs()) + tiny
-    es = sg + E * (1 + r) * size * (1 + slope.abs())
-    if name == "relu":
-        es = (r <= sg).double()
-    dg = dh * v * slope
-    bdg = bdh * (v * slope).abs() + dh.abs() * (sv * slope.abs() + v.abs() * es) + 2 * E * dg.abs()
+    dg = dh * b
+    bdg = bdh * b.abs() + dh.abs() * sb + E * dg.abs()
     bdg = 1.05 * (bdg + u * dg.abs()) + tiny
     dx = dg @ G + du @ U
     ag, au = dg.abs() + bdg, du.abs() + bdu
@@ -93,7 +91,7 @@ def reference(x, wg, wu, wd, name, dy=None):
     n = max(T, 1) * E
     out["dw_gate"] = (dg.t() @ X, 1.05 * (bdg.t() @ X.abs() + n * (ag.t() @ X.abs())))
     out["dw_up"] = (du.t() @ X, 1.05 * (bdu.t() @ X.abs() + n * (au.t() @ X.abs())))
-    out["dw_down"] = (Y.t() @ h, 1.05 * (Y.abs().t() @ dhk + n * (Y.abs().t() @ (h.abs() + dhk))))
+    out["dw_down"] = (Y.t() @ h, 1.05 * (Y.abs().t() @ bh + n * (Y.abs().t() @ (h.abs() + bh))))
     return out
 
 

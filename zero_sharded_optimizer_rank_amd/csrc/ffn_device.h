@@ -8,6 +8,16 @@
 namespace zk {
 namespace dev {
 
+// Where h goes, and what is kept for the gradients (or NULL): act(g) and u act'(g).
+struct Kept {
+  uint16_t *h, *act, *slope;
+  int64_t ld;  // between their rows
+};
+inline Kept kept(const FfnPlan& p, void* ws, const zero_ffn_saved_t* s) {
+  if (s) return Kept{(uint16_t*)s->h, (uint16_t*)s->act, (uint16_t*)s->slope, s->ld};
+  return Kept{at<uint16_t>(ws, p.h), nullptr, nullptr, p.inner_pad};
+}
+
 template <int A>
 struct Act {};
 
@@ -67,11 +77,5 @@ __device__ __forceinline__ float activated(Act<A>, float g, float& slope) {
     return g < 0.0f ? 0.0f : g;  // a NaN stays one
   }
 }
-template <int A>
-__device__ __forceinline__ float activated(Act<A> a, float g) {
-  float slope;
-  return activated(a, g, slope);
-}
-
 }  // namespace dev
 }  // namespace zk

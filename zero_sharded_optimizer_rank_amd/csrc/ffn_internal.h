@@ -13,6 +13,7 @@ namespace zk {
 constexpr int64_t kFfnTile = 256;
 constexpr int64_t kFfnStep = 64;   // contraction elements a step stages
 constexpr int32_t kFfnFew = 64;    // most tokens of the form that streams the weights
+constexpr int kFewTile = 128;      // columns of a wave's step there: two lines of a row
 
 // Where things lie in the workspace (byte offsets), and how the work is cut.
 struct FfnPlan {
@@ -20,6 +21,8 @@ struct FfnPlan {
   bool few;
   bool pack_x, pack_gate, pack_up, pack_down, pack_dy;  // rows that no 16-byte loads fit
   int32_t split_y, split_dx;      // ways the contractions over the inner axis are split
+  int32_t few_sets_in, few_sets_out;  // few: sets of rows of a workgroup, 2 or 4; 1: x is
+                                      // not shared
   // offsets
   size_t x, w_gate, w_up, w_down, dy, h, dg, du, acc, total;
 };

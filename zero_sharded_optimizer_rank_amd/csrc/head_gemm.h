@@ -372,21 +372,24 @@ struct Gemm {
     }
   }
   // PAIR: what both products make, 128 rows (i < 4) in 16 bits; a column takes
-  // 256 bytes, its chunk c at c ^ (col % 16), and 16 lanes.
-  static __device__ __forceinline__ void put_half(const GemmLds& lds, int i, int j, u32x2 v) {
+  // 256 bytes, its chunk c at c ^ (col % 16), and 16 lanes.  There is room for two
+  // such tiles (region 0 and 1).
+  static __device__ __forceinline__ void put_half(const GemmLds& lds, int region, int i, int j,
+                                                  u32x2 v) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = j % 2 * 16 + (lane & 15);
     const int chunk = wave / 4 * 8 + 2 * i + (lane >> 5);
-    lds_char* p = columns(lds, wave % 4 * 2 + j / 2) + col * 256 + (lane >> 4 & 1) * 8;
+    lds_char* p =
+        columns(lds, wave % 4 * 2 + j / 2) + region * 8192 + col * 256 + (lane >> 4 & 1) * 8;
     *(__attribute__((address_space(3))) u32x2*)(p + ((chunk ^ (col & 15)) << 4)) = v;
   }
   template <typename Store>
-  static __device__ __forceinline__ void take_half(const GemmLds& lds, Store store) {
+  static __device__ __forceinline__ void take_half(const GemmLds& lds, int region, Store store) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15;
-    const lds_char* p = columns(lds, wave);
+    const lds_char* p = columns(lds, wave) + region * 8192;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int col = 4 * k + (lane >> 4);

@@ -47,10 +47,11 @@ int check_ffn(const zero_ffn_t* f) {
 
 int check_saved(const zero_ffn_t* f, const zero_ffn_saved_t* s) {
   if (s->ld < up(f->inner, 8) || s->ld % 8 || s->ld > ZERO_FFN_MAX_WIDTH)
-    return fail(ZERO_EINVAL, "rows of gate and up %lld apart", (long long)s->ld);
-  if (f->tokens > 0 && (!s->gate || !s->up)) return fail(ZERO_EINVAL, "gate or up is NULL");
-  if (!aligned(s->gate, 16) || !aligned(s->up, 16))
-    return fail(ZERO_EALIGN, "gate and up must be 16-byte aligned");
+    return fail(ZERO_EINVAL, "rows of act, slope and h %lld apart", (long long)s->ld);
+  if (f->tokens > 0 && (!s->act || !s->slope || !s->h))
+    return fail(ZERO_EINVAL, "act, slope or h is NULL");
+  if (!aligned(s->act, 16) || !aligned(s->slope, 16) || !aligned(s->h, 16))
+    return fail(ZERO_EALIGN, "act, slope and h must be 16-byte aligned");
   return ZERO_OK;
 }
 
@@ -88,6 +89,9 @@ bool ragged(const void* p, int64_t ld, int64_t width) {
   return width % 8 != 0 || ld % 8 != 0 || !aligned(p, 16);
 }
 
+// Workgroups of few tokens' first product that are enough for the 256 CUs.
+constexpr int64_t kFewGroups = 192;
+
 // Ways to split a contraction whose output has few tiles: up to one round of
 // the 256 CUs, of at least four stages each.
 int32_t split_of(int64_t out_tiles, int64_t k) {
@@ -95,6 +99,16 @@ int32_t split_of(int64_t out_tiles, int64_t k) {
   int64_t s = 256 / (out_tiles > 0 ? out_tiles : 1);
   if (s > stages / 4) s = stages / 4;
   return (int32_t)(s < 1 ? 1 : s);
+}
+// Ways where other tiles share the launch: no part longer than three quarters of
+// what a CU gets of the whole (in stages; the others fill up behind), or than
+// split_of has it.
+int32_t split_beside(int64_t out_tiles, int64_t k, int64_t other_stages) {
+  const int64_t stages = tiles(k, zk::kFfnStep);
+  const int64_t each = (out_tiles * stages + other_stages) / 256 * 3 / 4;
+  int64_t s = tiles(stages, each > 4 ? each : 4);
+  const int32_t most = split_of(out_tiles, k);
+  return (int32_t)(s < most ? s : most);
 }
 
 }  // namespace
@@ -106,7 +120,7 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
   const int64_t T = f->tokens, H = f->hidden, F = f->inner;
   p.hidden_pad = up(H, 8);
   p.inner_pad = up(F, 8);
-  p.few = !g && T <= kFfnFew;
+  p.few = !g && T <= kFfnFew && H >= 8 && F >= 8;  // whole 16-byte loads
   if (!p.few) {
     p.pack_x = ragged(f->x, f->ldx, H);
     p.pack_gate = ragged(f->w_gate, f->ld_gate, H);
@@ -117,7 +131,21 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
   const int64_t out_tiles = tiles(T, kFfnTile) * tiles(H, kFfnTile);
   p.split_y = p.split_dx = 1;
   if (!p.few && !g) p.split_y = split_of(out_tiles, F);
-  if (g) p.split_dx = split_of(out_tiles, 2 * F);
+  if (p.few) {
+    p.few_sets_in = T <= 8 ? 1 : tiles(F, 64) >= kFewGroups ? 4 : 2;
+    p.few_sets_out = T <= 8 ? 1 : H >= 2048 ? 4 : 2;
+    if (p.few_sets_out > 1) {
+      const int64_t blocks = tiles(H, 32 * p.few_sets_out), steps = tiles(F, kFewTile);
+      const int64_t most = steps * p.few_sets_out / (2 * 8);  // two steps a slice at least
+      int64_t s = 256 / blocks;
+      if (s > most) s = most;
+      p.split_y = (int32_t)(s < 1 ? 1 : s);
+    }
+  }
+  if (g) {
+    const int64_t dw = tiles(F, kFfnTile) * tiles(H, kFfnTile) * tiles(T, kFfnStep);
+    p.split_dx = split_beside(out_tiles, 2 * F, (g->dw_gate ? dw : 0) + (g->dw_up ? dw : 0));
+  }
   size_t at = 0;
   auto take = [&](int64_t bytes) {
     const size_t o = at;
@@ -129,13 +157,14 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
   p.w_up = take(p.pack_up ? 2 * F * p.hidden_pad : 0);
   p.w_down = take(p.pack_down ? 2 * H * p.inner_pad : 0);
   p.dy = take(p.pack_dy ? 2 * T * p.hidden_pad : 0);
-  p.h = take(2 * T * p.inner_pad);
+  p.h = take(g ? 0 : 2 * T * p.inner_pad);
   if (g) {
     p.dg = take(2 * T * p.inner_pad);
     p.du = take(2 * T * p.inner_pad);
   }
   const int32_t split = g ? p.split_dx : p.split_y;
-  p.acc = take(split > 1 ? 4 * split * up(T, kFfnTile) * up(H, kFfnTile) : 0);
+  const int64_t row = p.few ? 1 : kFfnTile, col = p.few ? 8 : kFfnTile;
+  p.acc = take(split > 1 ? 4 * split * up(T, row) * up(H, col) : 0);
   p.total = at > 0 ? at : 256;
   return p;
 }
@@ -146,15 +175,21 @@ extern "C" {
 
 size_t zero_ffn_workspace_bytes(const zero_ffn_t* ffn, const zero_ffn_grads_t* grads) {
   if (!ffn || !good_sizes(ffn) || (grads && !good_ld(grads->lddy, ffn->hidden))) return 0;
-  // a batch of fewer tokens may be split more ways; the plan changes by the tile
+  // a batch of fewer tokens, or a call for fewer gradients, may be split more ways: at
+  // most split_of's; the plan changes by the tile
   zero_ffn_t f = *ffn;
+  zero_ffn_grads_t only;
+  if (grads) {
+    only = *grads;
+    only.dw_gate = only.dw_up = nullptr;
+  }
   size_t need = 0;
   const auto count = [&](int64_t tokens) {
     f.tokens = tokens < ffn->tokens ? tokens : ffn->tokens;
-    const size_t n = zk::ffn_plan(&f, grads).total;
+    const size_t n = zk::ffn_plan(&f, grads ? &only : nullptr).total;
     if (n > need) need = n;
   };
-  count(zk::kFfnFew);
+  for (int64_t t = 1; t <= zk::kFfnFew; ++t) count(t);
   for (int64_t t = 0; t < ffn->tokens; t += zk::kFfnTile) count(t + zk::kFfnTile);
   return need;
 }
@@ -174,16 +209,15 @@ int zero_ffn_forward(const zero_ffn_t* ffn, void* y, int64_t ldy, const zero_ffn
   rc = check_workspace(p.total, workspace, ws_bytes);
   if (rc) return rc;
   const int64_t Fp = p.inner_pad;
-  const Range out[4] = {matrix(y, T, ldy, H, 2, "y"),
-                        matrix(saved ? saved->gate : nullptr, T, saved ? saved->ld : 0, Fp, 2,
-                               "gate"),
-                        matrix(saved ? saved->up : nullptr, T, saved ? saved->ld : 0, Fp, 2, "up"),
-                        {workspace, p.total, "workspace"}};
+  const zero_ffn_saved_t none = {nullptr, nullptr, nullptr, 0}, *s = saved ? saved : &none;
+  const Range out[5] = {matrix(y, T, ldy, H, 2, "y"), matrix(s->act, T, s->ld, Fp, 2, "act"),
+                        matrix(s->slope, T, s->ld, Fp, 2, "slope"),
+                        matrix(s->h, T, s->ld, Fp, 2, "h"), {workspace, p.total, "workspace"}};
   const Range in[4] = {matrix(ffn->x, T, ffn->ldx, H, 2, "x"),
                        matrix(ffn->w_gate, F, ffn->ld_gate, H, 2, "w_gate"),
                        matrix(ffn->w_up, F, ffn->ld_up, H, 2, "w_up"),
                        matrix(ffn->w_down, H, ffn->ld_down, F, 2, "w_down")};
-  rc = check_apart(out, 4, in, 4);
+  rc = check_apart(out, 5, in, 4);
   if (rc || T == 0) return rc;
   const int e = p.few ? zk::launch_ffn_few(ffn, p, workspace, y, ldy, saved, stream)
                       : zk::launch_ffn_forward(ffn, p, workspace, y, ldy, saved, stream);
@@ -222,14 +256,15 @@ int zero_ffn_backward(const zero_ffn_t* ffn, const zero_ffn_saved_t* saved,
                         matrix(g->dw_up, F, g->lddw_up, H, ew, "dw_up"),
                         matrix(g->dw_down, H, g->lddw_down, F, ew, "dw_down"),
                         {workspace, p.total, "workspace"}};
-  const Range in[7] = {matrix(ffn->x, T, ffn->ldx, H, 2, "x"),
+  const Range in[8] = {matrix(ffn->x, T, ffn->ldx, H, 2, "x"),
                        matrix(ffn->w_gate, F, ffn->ld_gate, H, 2, "w_gate"),
                        matrix(ffn->w_up, F, ffn->ld_up, H, 2, "w_up"),
                        matrix(ffn->w_down, H, ffn->ld_down, F, 2, "w_down"),
                        matrix(g->dy, T, g->lddy, H, 2, "dy"),
-                       matrix(saved->gate, T, saved->ld, Fp, 2, "gate"),
-                       matrix(saved->up, T, saved->ld, Fp, 2, "up")};
-  rc = check_apart(out, 5, in, 7);
+                       matrix(saved->act, T, saved->ld, Fp, 2, "act"),
+                       matrix(saved->slope, T, saved->ld, Fp, 2, "slope"),
+                       matrix(saved->h, T, saved->ld, Fp, 2, "h")};
+  rc = check_apart(out, 5, in, 8);
   if (rc) return rc;
   return hip_status(zk::launch_ffn_backward(ffn, p, workspace, saved, g, stream),
                     "ffn_backward launch");

@@ -1,15 +1,15 @@
 // Gated feed-forward block and its gradients on the matrix cores (see
 // zero_ffn_t in zero_shard.h for the formulas).
 //
-//   forward   k_ffn_in    both projections of a tile at once, activation and
-//                         product on the fp32 sums: h leaves in 16 bits
-//             k_ffn_out   y = h Wd^T
-//   backward  k_ffn_dh    dh = dy Wd, whose tile becomes dg, du (and h again, from
-//                         the kept g and u) before it leaves
-//             k_ffn_dw    the three weights' gradients in one launch
-//             k_ffn_out   dx = dg Wg + du Wu, one contraction over both
-// All products are 256 x 256 tiles of head_gemm.h with fp32 sums; every operand
-// is read as it lies.
+//   forward   k_ffn_in     both projections of a tile at once, activation and
+//                          product on the fp32 sums: h leaves in 16 bits, and for
+//                          the gradients act(g) and u act'(g)
+//             k_ffn_out    y = h Wd^T
+//   backward  k_ffn_back1  dh = dy Wd, whose tiles leave as dg and du; dWd = dy^T h
+//             k_ffn_back2  dx = dg Wg + du Wu, one contraction over both; dWg, dWu
+// What does not wait for one another shares a launch, so that the tiles of one
+// fill the CUs that the last round of the other leaves idle.  All products are 256
+// x 256 tiles of head_gemm.h with fp32 sums; every operand is read as it lies.
 #include <stddef.h>
 
 #include "ffn_device.h"
@@ -72,14 +72,12 @@ struct PairProduct {
 };
 
 // A tile: 128 inner columns of both projections, 256 tokens, so that a lane holds g
-// and u of the same element.
-template <typename T>
+// and u of the same element.  What the gradients need is formed here, from the fp32
+// sums, so that the backward pass has two products an element left to do.
+template <typename T, int ACT, bool SAVE>
 __global__ __launch_bounds__(kGemmThreads) void k_ffn_in(Matrix x, Matrix w_gate, Matrix w_up,
                                                          int32_t tokens, int32_t inner,
-                                                         int32_t inner_pad, int32_t act,
-                                                         uint16_t* __restrict__ h,
-                                                         uint16_t* __restrict__ gate,
-                                                         uint16_t* __restrict__ up, int64_t ld) {
+                                                         int32_t inner_pad, Kept to) {
   using G = Gemm<T, false, false, true>;
   ZK_GEMM_LDS;
   int32_t mt, nt;
@@ -91,31 +89,49 @@ __global__ __launch_bounds__(kGemmThreads) void k_ffn_in(Matrix x, Matrix w_gate
                         by_rows(x, t0, tokens, 256)};
   f32x4 acc[G::MI][G::NJ];
   G::run(src, x.width, lds, acc);
-  if (gate) {
-    G::transposed(lds, acc, narrow4<T>, [&](int col, int row, u32x4 v) {
-      // rows: 64 of g, 64 of u, and again
-      const int32_t t = t0 + col, f = f0 + row / 128 * 64 + row % 64;
-      if (t < tokens && f < inner_pad)
-        *(u32x4*)((row & 64 ? up : gate) + (int64_t)t * ld + f) = v;
+  auto leave = [&](uint16_t* out, int region) {
+    G::take_half(lds, region, [&](int col, int row, u32x4 v) {
+      const int32_t t = t0 + col, f = f0 + row;
+      if (t < tokens && f < inner_pad) *(u32x4*)(out + (int64_t)t * to.ld + f) = v;
     });
+  };
+#pragma unroll
+  for (int j = 0; j < G::NJ; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f32x4 a, b, h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float u = acc[4 + i][j][e];
+        float slope;
+        a[e] = activated(Act<ACT>{}, acc[i][j][e], slope);
+        b[e] = u * slope;
+        h[e] = a[e] * u;
+      }
+      G::put_half(lds, 0, i, j, narrow4<T>(h[0], h[1], h[2], h[3]));
+      if constexpr (SAVE) {
+        G::put_half(lds, 1, i, j, narrow4<T>(a[0], a[1], a[2], a[3]));
+        u32x2 v = narrow4<T>(b[0], b[1], b[2], b[3]);
+        // narrowed here, into a sum's registers, and not where it leaves
+        asm volatile("" : "+v"(v));
+        acc[i][j][0] = __uint_as_float(v[0]);
+        acc[i][j][1] = __uint_as_float(v[1]);
+      }
+    }
+  __syncthreads();
+  leave(to.h, 0);
+  if constexpr (SAVE) {
+    leave(to.act, 1);
     __syncthreads();
-  }
-  with_act(act, [&](auto a) {
 #pragma unroll
     for (int j = 0; j < G::NJ; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f32x4 v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = activated(a, acc[i][j][e]) * acc[4 + i][j][e];
-        G::put_half(lds, i, j, narrow4<T>(v[0], v[1], v[2], v[3]));
-      }
-  });
-  __syncthreads();
-  G::take_half(lds, [&](int col, int row, u32x4 v) {
-    const int32_t t = t0 + col, f = f0 + row;
-    if (t < tokens && f < inner_pad) *(u32x4*)(h + (int64_t)t * inner_pad + f) = v;
-  });
+      for (int i = 0; i < 4; ++i)
+        G::put_half(lds, 0, i, j,
+                    u32x2{__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1])});
+    __syncthreads();
+    leave(to.slope, 0);
+  }
 }
 
 // --- y and dx --------------------------------------------------------------------
@@ -143,41 +159,43 @@ struct Products {
   __device__ __forceinline__ const Operand& b(int32_t& k) const { return pick(k, B1, B2); }
 };
 
+struct OutArgs {
+  Matrix a1, a2, b1, b2;
+  int32_t tokens, hidden, inner, split;
+  int64_t acc_rows;   // of a split's sums
+  int32_t acc_ld;
+  float* acc;         // split > 1
+  uint16_t* out;      // split = 1
+  int64_t ldo;
+};
+
 template <typename T, bool DX>
-__global__ __launch_bounds__(kGemmThreads) void k_ffn_out(Matrix a1, Matrix a2, Matrix b1,
-                                                          Matrix b2, int32_t tokens,
-                                                          int32_t hidden, int32_t inner,
-                                                          int32_t split, int64_t acc_rows,
-                                                          int32_t acc_ld,
-                                                          float* __restrict__ acc_out,
-                                                          uint16_t* __restrict__ out,
-                                                          int64_t ldo) {
+__device__ __forceinline__ void out_tile(uint32_t block, const OutArgs& o, const GemmLds& lds) {
   using G = Gemm<T, DX, false>;
-  ZK_GEMM_LDS;
-  const uint32_t ht = (uint32_t)((hidden + 255) / 256);
+  const uint32_t ht = (uint32_t)((o.hidden + 255) / 256);
   int32_t mt, nt;
-  if (!tile_of(blockIdx.x, (uint32_t)((tokens + 255) / 256), ht * (uint32_t)split, mt, nt)) return;
+  if (!tile_of(block, (uint32_t)((o.tokens + 255) / 256), ht * (uint32_t)o.split, mt, nt)) return;
   const int32_t h0 = (int32_t)((uint32_t)nt % ht) * 256, t0 = mt * 256;
   const int32_t part = (int32_t)((uint32_t)nt / ht);
-  const int32_t stages = (inner + kStage - 1) / kStage, all = DX ? 2 * stages : stages;
-  const int32_t s0 = (int32_t)((int64_t)all * part / split);
-  const int32_t s1 = (int32_t)((int64_t)all * (part + 1) / split);
+  const int32_t stages = (o.inner + kStage - 1) / kStage, all = DX ? 2 * stages : stages;
+  const int32_t s0 = (int32_t)((int64_t)all * part / o.split);
+  const int32_t s1 = (int32_t)((int64_t)all * (part + 1) / o.split);
   Products<DX> src;
-  src.A1 = DX ? by_cols(a1, h0, inner) : by_rows(a1, h0, hidden, 256);
-  src.B1 = by_rows(b1, t0, tokens, 256);
+  src.A1 = DX ? by_cols(o.a1, h0, o.inner) : by_rows(o.a1, h0, o.hidden, 256);
+  src.B1 = by_rows(o.b1, t0, o.tokens, 256);
   if constexpr (DX) {
-    src.A2 = by_cols(a2, h0, inner);
-    src.B2 = by_rows(b2, t0, tokens, 256);
+    src.A2 = by_cols(o.a2, h0, o.inner);
+    src.B2 = by_rows(o.b2, t0, o.tokens, 256);
   }
   src.k0 = s0 * kStage;
   src.k1 = stages * kStage;
   src.end = s1 * kStage;
   f32x4 acc[G::MI][G::NJ];
   G::run(src, (s1 - s0) * kStage, lds, acc);
-  if (split == 1) {
+  if (o.split == 1) {
     G::transposed(lds, acc, narrow4<T>, [&](int col, int row, u32x4 v) {
       const int32_t t = t0 + col, c = h0 + row;
-      if (t < tokens && c < hidden) store_row(out + (int64_t)t * ldo, c, hidden, v);
+      if (t < o.tokens && c < o.hidden) store_row(o.out + (int64_t)t * o.ldo, c, o.hidden, v);
     });
     return;
   }
@@ -185,12 +203,18 @@ __global__ __launch_bounds__(kGemmThreads) void k_ffn_out(Matrix a1, Matrix a2, 
 #pragma unroll
   for (int j = 0; j < G::NJ; ++j) {
     const int32_t t = t0 + (wave % 4) * 64 + j * 16 + (lane & 15);
-    float* o = acc_out + ((int64_t)part * acc_rows + t) * acc_ld;
+    float* p = o.acc + ((int64_t)part * o.acc_rows + t) * o.acc_ld;
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int i = 0; i < G::MI; ++i)
-      *(f32x4*)(o + h0 + wave / 4 * 128 + 16 * i + 4 * (lane >> 4)) = acc[i][j];
+      *(f32x4*)(p + h0 + wave / 4 * 128 + 16 * i + 4 * (lane >> 4)) = acc[i][j];
   }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kGemmThreads) void k_ffn_out(OutArgs o) {
+  ZK_GEMM_LDS;
+  out_tile<T, false>(blockIdx.x, o, lds);
 }
 
 // The splits' sums, four columns a thread.
@@ -219,114 +243,100 @@ __global__ __launch_bounds__(kPackThreads) void k_ffn_join(const float* __restri
 }
 
 // --- backward --------------------------------------------------------------------
-// A tile of dh: A = Wd by its columns (inner), B = dy by its rows.  Each lane reads
-// g and u of its elements, and the tile leaves as h, dg and du.
-template <typename T, int ACT>
-__global__ __launch_bounds__(kGemmThreads) void k_ffn_dh(Matrix w_down, Matrix dy, int32_t tokens,
-                                                         int32_t hidden, int32_t inner,
-                                                         int32_t inner_pad,
-                                                         const uint16_t* __restrict__ gate,
-                                                         const uint16_t* __restrict__ up,
-                                                         int64_t ld, uint16_t* __restrict__ h,
-                                                         uint16_t* __restrict__ dg,
-                                                         uint16_t* __restrict__ du) {
+struct DhArgs {
+  Matrix w_down, dy;
+  int32_t tokens, hidden, inner, inner_pad;
+  const uint16_t *act, *slope;  // rows ld apart
+  int64_t ld;
+  uint16_t *dg, *du;            // rows inner_pad apart
+};
+
+// A tile of dh: A = Wd by its columns (inner), B = dy by its rows; it leaves as dg =
+// dh (u act'(g)) and du = dh act(g).  Lane by lane those lie as the sums do, eight
+// bytes each; the next column's are on their way while one is multiplied.
+template <typename T>
+__device__ __forceinline__ void dh_tile(uint32_t block, const DhArgs& a, const GemmLds& lds) {
   using G = Gemm<T, true, false>;
-  ZK_GEMM_LDS;
   int32_t mt, nt;
-  if (!tile_of(blockIdx.x, (uint32_t)((inner + 255) / 256), (uint32_t)((tokens + 255) / 256), mt,
+  if (!tile_of(block, (uint32_t)((a.inner + 255) / 256), (uint32_t)((a.tokens + 255) / 256), mt,
                nt))
     return;
   const int32_t f0 = mt * 256, t0 = nt * 256;
   f32x4 acc[G::MI][G::NJ];
-  G::run(by_cols(w_down, f0, hidden), by_rows(dy, t0, tokens, 256), hidden, lds, acc);
+  G::run(by_cols(a.w_down, f0, a.hidden), by_rows(a.dy, t0, a.tokens, 256), a.hidden, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int j = 0; j < G::NJ; ++j) {
+  u32x2 av[2][G::MI], bv[2][G::MI];
+  auto fetch = [&](int j) {  // what lies past the operands is not stored
     const int32_t t = t0 + (wave % 4) * 64 + j * 16 + (lane & 15);
-    const int64_t row = (int64_t)(t < tokens ? t : tokens - 1) * ld;
-    lds_char* p = G::column(lds, j);
-    // 16 loads at a time: more would not fit beside the sums (what lies past the
-    // operands is not stored)
-    u32x2 gv[G::MI], uv[G::MI];
+    const int64_t row = (int64_t)(t < a.tokens ? t : a.tokens - 1) * a.ld;
 #pragma unroll
     for (int i = 0; i < G::MI; ++i) {
       const int32_t f = f0 + wave / 4 * 128 + 16 * i + 4 * (lane >> 4);
-      gv[i] = *(const u32x2*)(gate + row + (f < inner_pad ? f : 0));
-      uv[i] = *(const u32x2*)(up + row + (f < inner_pad ? f : 0));
+      const int64_t at = row + (f < a.inner_pad ? f : 0);
+      av[j & 1][i] = *(const u32x2*)(a.act + at);
+      bv[j & 1][i] = *(const u32x2*)(a.slope + at);
     }
+  };
+  fetch(0);
 #pragma unroll
-    for (int i = 0; i < G::MI; ++i) {
-      f32x4 hh, x, y;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float g = widen<T>((gv[i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-        const float u = widen<T>((uv[i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-        float slope;
-        const float v = activated(Act<ACT>{}, g, slope);
-        hh[e] = v * u;
-        x[e] = acc[i][j][e] * u * slope;
-        y[e] = acc[i][j][e] * v;
-      }
-      G::put(p, i, j, narrow4<T>(hh[0], hh[1], hh[2], hh[3]));
-      u32x2 xs = narrow4<T>(x[0], x[1], x[2], x[3]), ys = narrow4<T>(y[0], y[1], y[2], y[3]);
-      // narrowed here, into the sums' registers, and not where they leave
-      asm volatile("" : "+v"(xs), "+v"(ys));
-      acc[i][j] = f32x4{__uint_as_float(xs[0]), __uint_as_float(xs[1]), __uint_as_float(ys[0]),
-                        __uint_as_float(ys[1])};
-    }
+  for (int j = 0; j < G::NJ; ++j) {
+    if (j + 1 < G::NJ) fetch(j + 1);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
+    lds_char* p = G::column(lds, j);
+#pragma unroll
+    for (int i = 0; i < G::MI; ++i) {
+      f32x4 x, y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = acc[i][j][e] * widen<T>((bv[j & 1][i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+        y[e] = acc[i][j][e] * widen<T>((av[j & 1][i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+      }
+      G::put(p, i, j, narrow4<T>(x[0], x[1], x[2], x[3]));
+      u32x2 v = narrow4<T>(y[0], y[1], y[2], y[3]);
+      // narrowed here, into a sum's registers, and not where it leaves
+      asm volatile("" : "+v"(v));
+      acc[i][j][0] = __uint_as_float(v[0]);
+      acc[i][j][1] = __uint_as_float(v[1]);
+    }
   }
   auto leave = [&](uint16_t* out) {
     __syncthreads();
     G::take(lds, [&](int col, int row, u32x4 v) {
       const int32_t t = t0 + col, f = f0 + row;
-      if (t < tokens && f < inner_pad) *(u32x4*)(out + (int64_t)t * inner_pad + f) = v;
+      if (t < a.tokens && f < a.inner_pad) *(u32x4*)(out + (int64_t)t * a.inner_pad + f) = v;
     });
-    __syncthreads();
   };
-  leave(h);
+  leave(a.dg);
+  __syncthreads();
 #pragma unroll
-  for (int d = 0; d < 2; ++d) {
+  for (int j = 0; j < G::NJ; ++j) {
+    lds_char* p = G::column(lds, j);
 #pragma unroll
-    for (int j = 0; j < G::NJ; ++j) {
-      lds_char* p = G::column(lds, j);
-#pragma unroll
-      for (int i = 0; i < G::MI; ++i)
-        G::put(p, i, j, u32x2{__float_as_uint(acc[i][j][2 * d]),
-                              __float_as_uint(acc[i][j][2 * d + 1])});
-    }
-    leave(d == 0 ? dg : du);
+    for (int i = 0; i < G::MI; ++i)
+      G::put(p, i, j, u32x2{__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1])});
   }
+  leave(a.du);
 }
 
 // One weight's gradient [n, m] = B^T A: row j is column j of B against the columns
 // of A, over the tokens.
 struct WeightGrad {
   Matrix a, b;
-  int32_t m, n;
-  uint32_t first;  // workgroup of its first tile
-  void* out;       // NULL: not wanted
+  int32_t m, n, tokens, accumulate;
+  uint32_t first;  // its first workgroup
+  void* out;
   int64_t ld;
-};
-struct WeightGrads {
-  WeightGrad w[3];
 };
 
 template <typename T, bool F32OUT>
-__global__ __launch_bounds__(kGemmThreads) void k_ffn_dw(WeightGrads all, int32_t tokens,
-                                                         int32_t accumulate) {
+__device__ __forceinline__ void dw_tile(uint32_t block, const WeightGrad& w, const GemmLds& lds) {
   using G = Gemm<T, true, true>;
-  ZK_GEMM_LDS;
-  const int which = blockIdx.x >= all.w[2].first ? 2 : blockIdx.x >= all.w[1].first ? 1 : 0;
-  const WeightGrad w = all.w[which];
   int32_t mt, nt;
-  if (!tile_of(blockIdx.x - w.first, (uint32_t)((w.n + 255) / 256), (uint32_t)((w.m + 255) / 256),
-               nt, mt))
-    return;
-  const int32_t m0 = mt * 256, n0 = nt * 256;
+  if (!tile_of(block, (uint32_t)((w.n + 255) / 256), (uint32_t)((w.m + 255) / 256), nt, mt)) return;
+  const int32_t m0 = mt * 256, n0 = nt * 256, accumulate = w.accumulate;
   f32x4 acc[G::MI][G::NJ];
-  G::run(by_cols(w.a, m0, tokens), by_cols(w.b, n0, tokens), tokens, lds, acc);
+  G::run(by_cols(w.a, m0, w.tokens), by_cols(w.b, n0, w.tokens), w.tokens, lds, acc);
   if (!F32OUT && !accumulate) {
     uint16_t* out = (uint16_t*)w.out;
     G::transposed(lds, acc, narrow4<T>, [&](int col, int row, u32x4 v) {
@@ -372,6 +382,27 @@ __global__ __launch_bounds__(kGemmThreads) void k_ffn_dw(WeightGrads all, int32_
   }
 }
 
+// Workgroups from w.first on take dWd, those before dh: whichever has the longer
+// contraction comes first.
+template <typename T, bool F32OUT>
+__global__ __launch_bounds__(kGemmThreads) void k_ffn_back1(DhArgs d, uint32_t dh_first,
+                                                            WeightGrad w) {
+  ZK_GEMM_LDS;
+  const bool weight = w.first > dh_first ? blockIdx.x >= w.first : blockIdx.x < dh_first;
+  if (weight) dw_tile<T, F32OUT>(blockIdx.x - w.first, w, lds);
+  else dh_tile<T>(blockIdx.x - dh_first, d, lds);
+}
+
+// dx first, then dWg and dWu.
+template <typename T, bool F32OUT>
+__global__ __launch_bounds__(kGemmThreads) void k_ffn_back2(OutArgs o, WeightGrad g,
+                                                            WeightGrad u) {
+  ZK_GEMM_LDS;
+  if (blockIdx.x < g.first) return out_tile<T, true>(blockIdx.x, o, lds);
+  const WeightGrad w = blockIdx.x < u.first ? g : u;
+  dw_tile<T, F32OUT>(blockIdx.x - w.first, w, lds);
+}
+
 // --- launches ----------------------------------------------------------------------
 // The matrix as the kernels read it: in place, or laid out in the workspace.
 int view(const void* src, int64_t ld, int64_t rows, int64_t cols, bool pack, void* ws, size_t at_,
@@ -390,27 +421,37 @@ int view(const void* src, int64_t ld, int64_t rows, int64_t cols, bool pack, voi
   return (int)hipGetLastError();
 }
 
-template <typename T, bool DX>
-int out_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, Matrix a1, Matrix a2, Matrix b1,
-          Matrix b2, int32_t split, void* out, int64_t ldo, hipStream_t stream) {
+OutArgs out_args(const zero_ffn_t* f, const FfnPlan& p, void* ws, Matrix a1, Matrix a2, Matrix b1,
+                 Matrix b2, int32_t split, void* out, int64_t ldo) {
   const int64_t ht = (f->hidden + 255) / 256, tt = (f->tokens + 255) / 256;
-  hipLaunchKernelGGL((k_ffn_out<T, DX>), dim3(tile_grid(tt, ht * split)), dim3(kGemmThreads), 0,
-                     stream, a1, a2, b1, b2, (int32_t)f->tokens, (int32_t)f->hidden,
-                     (int32_t)f->inner, split, tt * 256, (int32_t)(ht * 256),
-                     at<float>(ws, p.acc), (uint16_t*)out, ldo);
-  ZK_LAUNCHED();
-  if (split == 1) return (int)hipSuccess;
+  return OutArgs{a1, a2, b1, b2, (int32_t)f->tokens, (int32_t)f->hidden, (int32_t)f->inner, split,
+                 tt * 256, (int32_t)(ht * 256), at<float>(ws, p.acc), (uint16_t*)out, ldo};
+}
+uint32_t out_blocks(const OutArgs& o) {
+  return tile_grid((o.tokens + 255) / 256, (int64_t)((o.hidden + 255) / 256) * o.split);
+}
+
+template <typename T>
+int join_t(const OutArgs& o, hipStream_t stream) {
+  if (o.split == 1) return (int)hipSuccess;
   const int64_t cols = 4 * kPackThreads, most = 65535;
-  for (int64_t t0 = 0; t0 < f->tokens; t0 += most) {
-    const int64_t n = f->tokens - t0 < most ? f->tokens - t0 : most;
+  for (int64_t t0 = 0; t0 < o.tokens; t0 += most) {
+    const int64_t n = o.tokens - t0 < most ? o.tokens - t0 : most;
     hipLaunchKernelGGL((k_ffn_join<T>),
-                       dim3((uint32_t)((f->hidden + cols - 1) / cols), (uint32_t)n),
-                       dim3(kPackThreads), 0, stream,
-                       at<const float>(ws, p.acc) + t0 * ht * 256, split, tt * 256,
-                       (int32_t)(ht * 256), (int32_t)f->hidden, (uint16_t*)out + t0 * ldo, ldo);
+                       dim3((uint32_t)((o.hidden + cols - 1) / cols), (uint32_t)n),
+                       dim3(kPackThreads), 0, stream, o.acc + t0 * o.acc_ld, o.split, o.acc_rows,
+                       o.acc_ld, o.hidden, o.out + t0 * o.ldo, o.ldo);
     ZK_LAUNCHED();
   }
   return (int)hipSuccess;
+}
+
+template <typename T, bool SAVE>
+auto in_kernel(int32_t act) {
+  return act == ZERO_ACT_SILU        ? k_ffn_in<T, ZERO_ACT_SILU, SAVE>
+         : act == ZERO_ACT_GELU      ? k_ffn_in<T, ZERO_ACT_GELU, SAVE>
+         : act == ZERO_ACT_GELU_TANH ? k_ffn_in<T, ZERO_ACT_GELU_TANH, SAVE>
+                                     : k_ffn_in<T, ZERO_ACT_RELU, SAVE>;
 }
 
 template <typename T>
@@ -423,17 +464,19 @@ int forward_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, void* y, int64_t 
   if (!e) e = view(f->w_up, f->ld_up, F, H, p.pack_up, ws, p.w_up, stream, wu);
   if (!e) e = view(f->w_down, f->ld_down, H, F, p.pack_down, ws, p.w_down, stream, wd);
   if (e) return e;
-  uint16_t* h = at<uint16_t>(ws, p.h);
-  hipLaunchKernelGGL((k_ffn_in<T>), dim3(tile_grid((F + 127) / 128, (T_ + 255) / 256)),
-                     dim3(kGemmThreads), 0, stream, x, wg, wu, (int32_t)T_, (int32_t)F,
-                     (int32_t)p.inner_pad, f->act, h, saved ? (uint16_t*)saved->gate : nullptr,
-                     saved ? (uint16_t*)saved->up : nullptr, saved ? saved->ld : 0);
+  const Kept to = kept(p, ws, saved);
+  hipLaunchKernelGGL((saved ? in_kernel<T, true>(f->act) : in_kernel<T, false>(f->act)),
+                     dim3(tile_grid((F + 127) / 128, (T_ + 255) / 256)), dim3(kGemmThreads), 0,
+                     stream, x, wg, wu, (int32_t)T_, (int32_t)F, (int32_t)p.inner_pad, to);
   ZK_LAUNCHED();
-  const Matrix hm{h, (int32_t)p.inner_pad, (int32_t)p.inner_pad};
-  return out_t<T, false>(f, p, ws, wd, wd, hm, hm, p.split_y, y, ldy, stream);
+  const Matrix h{to.h, (int32_t)to.ld, (int32_t)p.inner_pad};
+  const OutArgs o = out_args(f, p, ws, wd, wd, h, h, p.split_y, y, ldy);
+  hipLaunchKernelGGL((k_ffn_out<T>), dim3(out_blocks(o)), dim3(kGemmThreads), 0, stream, o);
+  ZK_LAUNCHED();
+  return join_t<T>(o, stream);
 }
 
-template <typename T>
+template <typename T, bool F32OUT>
 int backward_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, const zero_ffn_saved_t* saved,
                const zero_ffn_grads_t* g, hipStream_t stream) {
   Matrix x, wg{}, wu{}, wd, dy;
@@ -445,44 +488,47 @@ int backward_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, const zero_ffn_s
   if (!e) e = view(g->dy, g->lddy, T_, H, p.pack_dy, ws, p.dy, stream, dy);
   if (e) return e;
   const int32_t Fp = (int32_t)p.inner_pad;
-  const Matrix h{at<uint16_t>(ws, p.h), Fp, Fp}, dg{at<uint16_t>(ws, p.dg), Fp, Fp},
-      du{at<uint16_t>(ws, p.du), Fp, Fp};
-  const int64_t ftiles = (F + 255) / 256, htiles = (H + 255) / 256, ttiles = (T_ + 255) / 256;
-  if (T_ > 0) {
-    const auto dh = f->act == ZERO_ACT_SILU        ? k_ffn_dh<T, ZERO_ACT_SILU>
-                    : f->act == ZERO_ACT_GELU      ? k_ffn_dh<T, ZERO_ACT_GELU>
-                    : f->act == ZERO_ACT_GELU_TANH ? k_ffn_dh<T, ZERO_ACT_GELU_TANH>
-                                                   : k_ffn_dh<T, ZERO_ACT_RELU>;
-    hipLaunchKernelGGL(dh, dim3(tile_grid(ftiles, ttiles)), dim3(kGemmThreads), 0, stream, wd, dy,
-                       (int32_t)T_, (int32_t)H, (int32_t)F, Fp, (const uint16_t*)saved->gate,
-                       (const uint16_t*)saved->up, saved->ld, (uint16_t*)h.p, (uint16_t*)dg.p,
-                       (uint16_t*)du.p);
+  const Matrix h{(const uint16_t*)saved->h, (int32_t)saved->ld, Fp};
+  const Matrix dg{at<uint16_t>(ws, p.dg), Fp, Fp}, du{at<uint16_t>(ws, p.du), Fp, Fp};
+  const uint32_t dw_blocks = tile_grid((F + 255) / 256, (H + 255) / 256);
+  // tokens 0: nothing but weights' gradients to clear
+  const bool weights = T_ > 0 || !g->accumulate;
+  WeightGrad down{h, dy, (int32_t)F, (int32_t)H, (int32_t)T_, g->accumulate, 0, g->dw_down,
+                  g->lddw_down};
+  WeightGrad gate{x, dg, (int32_t)H, (int32_t)F, (int32_t)T_, g->accumulate, 0, g->dw_gate,
+                  g->lddw_gate};
+  WeightGrad up{x, du, (int32_t)H, (int32_t)F, (int32_t)T_, g->accumulate, 0, g->dw_up,
+                g->lddw_up};
+  const DhArgs dh{wd, dy, (int32_t)T_, (int32_t)H, (int32_t)F, Fp, (const uint16_t*)saved->act,
+                  (const uint16_t*)saved->slope, saved->ld, (uint16_t*)dg.p, (uint16_t*)du.p};
+  const bool through = T_ > 0 && (g->dx || g->dw_gate || g->dw_up);
+  const uint32_t dh_blocks = through ? tile_grid((F + 255) / 256, (T_ + 255) / 256) : 0;
+  const uint32_t down_blocks = weights && down.out ? dw_blocks : 0;
+  if (dh_blocks + down_blocks) {
+    const bool dh_first = through && H >= T_;
+    down.first = dh_first ? dh_blocks : 0;
+    hipLaunchKernelGGL((k_ffn_back1<T, F32OUT>), dim3(dh_blocks + down_blocks), dim3(kGemmThreads),
+                       0, stream, dh, dh_first ? 0 : down_blocks, down);
     ZK_LAUNCHED();
   }
-  if (T_ > 0 || !g->accumulate) {
-    WeightGrads all;
-    all.w[0] = WeightGrad{x, dg, (int32_t)H, (int32_t)F, 0, g->dw_gate, g->lddw_gate};
-    all.w[1] = WeightGrad{x, du, (int32_t)H, (int32_t)F, 0, g->dw_up, g->lddw_up};
-    all.w[2] = WeightGrad{h, dy, (int32_t)F, (int32_t)H, 0, g->dw_down, g->lddw_down};
-    uint32_t blocks = 0;
-    const uint32_t each = tile_grid(ftiles, htiles);
-    for (WeightGrad& w : all.w) {
-      w.first = blocks;
-      if (w.out) blocks += each;
-    }
-    // one that is not wanted has no workgroups: the next one starts where it does
-    if (blocks) {
-      if (g->dw_dtype == ZERO_F32)
-        hipLaunchKernelGGL((k_ffn_dw<T, true>), dim3(blocks), dim3(kGemmThreads), 0, stream, all,
-                           (int32_t)T_, g->accumulate);
-      else
-        hipLaunchKernelGGL((k_ffn_dw<T, false>), dim3(blocks), dim3(kGemmThreads), 0, stream, all,
-                           (int32_t)T_, g->accumulate);
-      ZK_LAUNCHED();
-    }
+  const OutArgs o = out_args(f, p, ws, wg, wu, dg, du, p.split_dx, g->dx, g->lddx);
+  const bool dx = g->dx && T_ > 0;
+  gate.first = dx ? out_blocks(o) : 0;
+  up.first = gate.first + (weights && gate.out ? dw_blocks : 0);
+  const uint32_t blocks = up.first + (weights && up.out ? dw_blocks : 0);
+  if (blocks) {
+    hipLaunchKernelGGL((k_ffn_back2<T, F32OUT>), dim3(blocks), dim3(kGemmThreads), 0, stream, o,
+                       gate, up);
+    ZK_LAUNCHED();
   }
-  if (!g->dx || T_ == 0) return (int)hipSuccess;
-  return out_t<T, true>(f, p, ws, wg, wu, dg, du, p.split_dx, g->dx, g->lddx, stream);
+  return dx ? join_t<T>(o, stream) : (int)hipSuccess;
+}
+
+template <typename T>
+int backward_o(const zero_ffn_t* f, const FfnPlan& p, void* ws, const zero_ffn_saved_t* saved,
+               const zero_ffn_grads_t* g, hipStream_t stream) {
+  return g->dw_dtype == ZERO_F32 ? backward_t<T, true>(f, p, ws, saved, g, stream)
+                                 : backward_t<T, false>(f, p, ws, saved, g, stream);
 }
 
 }  // namespace
@@ -496,8 +542,8 @@ int launch_ffn_forward(const zero_ffn_t* f, const FfnPlan& p, void* ws, void* y,
 int launch_ffn_backward(const zero_ffn_t* f, const FfnPlan& p, void* ws,
                         const zero_ffn_saved_t* saved, const zero_ffn_grads_t* g,
                         hipStream_t stream) {
-  return f->dtype == ZERO_BF16 ? backward_t<BF16>(f, p, ws, saved, g, stream)
-                               : backward_t<FP16>(f, p, ws, saved, g, stream);
+  return f->dtype == ZERO_BF16 ? backward_o<BF16>(f, p, ws, saved, g, stream)
+                               : backward_o<FP16>(f, p, ws, saved, g, stream);
 }
 
 }  // namespace zk

@@ -2,13 +2,18 @@
 // short prompts).
 //
 // Both products are bound by the weights, which are read once: 128 operations a
-// weight at 64 tokens.  So no weight is staged: a wave takes 16 rows' pieces
-// from memory straight into fragments, 128 columns at a time, the next ones on
-// their way while the last are multiplied; x (and h) come from the L2 the same
-// way.  A workgroup has 16 rows (of both projections: 16 + 16) and its waves
-// share the contraction, so that a projection of 4096 x 14336 gives 3584 waves;
-// their sums are joined through LDS in a fixed order, where the activation and
-// the rounding are.  Rows may start anywhere.
+// weight at 64 tokens.  So no weight is staged: a wave takes 32 rows' pieces (16
+// of each projection) from memory straight into fragments, 128 columns at a time,
+// the next ones on their way while the last are multiplied.  Rows may start anywhere.
+//   up to 8 tokens  k_ffn_direct  the waves of a workgroup share the contraction
+//   more            k_ffn_shared  x (and h) go through LDS, and waves of the same columns
+//                                 share them: fetched by each wave from the L2 they
+//                                 would be twice the weights' bytes at 64 tokens (4096
+//                                 x 14336: 184 us a pass, so 87).  Eight waves are R
+//                                 sets of rows by 8 / R slices of the contraction,
+//                                 joined through LDS in a fixed order; the second
+//                                 product's, whose rows are few, is also split over
+//                                 workgroups (k_ffn_few_join)
 #include <stddef.h>
 
 #include "ffn_device.h"
@@ -18,132 +23,155 @@ namespace {
 
 using namespace dev;
 
-constexpr int kTile = 128;  // columns of a wave's step: two whole 128-byte lines a row
+constexpr int kWaves = 8;
 
 struct Few {
-  const uint16_t *w0, *w1;  // gate and up, or down
+  const uint16_t *w0, *w1;  // PAIR: gate and up; else w0
   int64_t ldw0, ldw1;
   const uint16_t* x;        // [tokens, k]
   int64_t ldx;
-  int32_t rows, k, tokens, act;
-  uint16_t* out;            // [tokens, rows], rows ldo apart
+  int32_t rows, k, tokens, act, split;
+  Kept to;                  // PAIR
+  int32_t pad;              // PAIR: columns of h; those past the rows are zero
+  uint16_t* out;            // else, split = 1: [tokens, rows], rows ldo apart
   int64_t ldo;
-  uint16_t *gate, *up;      // or NULL
-  int64_t lds;
-  int32_t pad;              // PAIR: columns of h, gate and up; those past the rows are zero
+  float* acc;               // else: [split][tokens][pad]
 };
 
-// Elements [c, c + 8) of a row of n < 8 elements.
-__device__ __forceinline__ s16x8 short_row(const uint16_t* row, int32_t c, int32_t n) {
-  return __builtin_bit_cast(s16x8, take8(row + c, c < n ? n - c : 0));
+// The piece [c, c + 8) of a row of k >= 8 elements.  One that passes the row's end is
+// loaded from the row's last eight elements, without a branch around the load, and
+// what does not belong to it is taken out before it is used (held8; beyond: (8 - k %
+// 8) % 8).
+__device__ __forceinline__ s16x8 row8(const uint16_t* row, int32_t c, int32_t k) {
+  return __builtin_bit_cast(s16x8, *(const u32x4_a2*)(row + (c + 8 <= k ? c : k - 8)));
+}
+__device__ __forceinline__ s16x8 held8(s16x8 v, int32_t c, int32_t k, int beyond) {
+  if (c >= k) return s16x8{};
+  return c + 8 > k ? drop_first(v, beyond) : v;
 }
 
-template <typename T, int NJ, int WAVES, bool PAIR, bool LONG>
+// A load covers 8 rows' whole 128-byte lines: lanes with q = lane % 16 < 8 take the
+// first half of row q % 8's, the others the second; a fragment wants lane q to hold
+// row q, so two loads of 8 rows trade halves.
+__device__ __forceinline__ void fragments(const s16x8 (&d)[2], s16x8 (&f)[2], bool first) {
+  const u32x4 lo = __builtin_bit_cast(u32x4, d[0]), hi = __builtin_bit_cast(u32x4, d[1]);
+  u32x4 u, v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t give = first ? hi[e] : lo[e];
+    const uint32_t got =
+        (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, false);
+    u[e] = first ? lo[e] : got;
+    v[e] = first ? got : hi[e];
+  }
+  f[0] = __builtin_bit_cast(s16x8, u);
+  f[1] = __builtin_bit_cast(s16x8, v);
+}
+
+// Both projections' sums of four rows r .. of token t: h, and what is kept.  Rows
+// past the last give zeros.
+template <typename T, typename A>
+__device__ __forceinline__ void leave_pair(const Few& a, A act, f32x4 g, f32x4 u, int32_t t,
+                                           int32_t r) {
+  f32x4 h, v, b;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float slope;
+    v[e] = activated(act, g[e], slope);
+    b[e] = u[e] * slope;
+    h[e] = v[e] * u[e];
+    if (r + e >= a.rows) h[e] = v[e] = b[e] = 0.0f;
+  }
+  if (t >= a.tokens || r >= a.pad) return;
+  const int64_t at = t * a.to.ld + r;
+  *(u32x2*)(a.to.h + at) = narrow4<T>(h[0], h[1], h[2], h[3]);
+  if (a.to.act) {
+    *(u32x2*)(a.to.act + at) = narrow4<T>(v[0], v[1], v[2], v[3]);
+    *(u32x2*)(a.to.slope + at) = narrow4<T>(b[0], b[1], b[2], b[3]);
+  }
+}
+// Four columns of an output row that holds n.
+template <typename T>
+__device__ __forceinline__ void leave4(uint16_t* row, int32_t r, int32_t n, f32x4 s) {
+  const u32x2 v = narrow4<T>(s[0], s[1], s[2], s[3]);
+  if (r + 4 <= n) {
+    *(u32x2_a2*)(row + r) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (r + e < n) row[r + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
+// Up to 8 tokens: 16 rows a workgroup (of both projections: 16 + 16), whose waves share
+// the contraction; x comes from the L2 straight into fragments.  More than two waves a
+// SIMD were slower (one token, 4096 x 14336: two or three 70, four 86 us a forward pass),
+// and so were 8 waves for the first product (74).
+template <typename T, int WAVES, bool PAIR>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(2, 2))) void
-k_ffn_few(const Few a) {
+k_ffn_direct(const Few a) {
   constexpr int NI = PAIR ? 2 : 1;
-  static_assert(NJ <= WAVES, "a thread for every quad");
-  __shared__ f32x4 s_sum[WAVES][NI * NJ][64];
+  __shared__ f32x4 s_sum[WAVES][NI][64];
   const int lane = threadIdx.x & 63, g = lane >> 4, q = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t r0 = (int32_t)blockIdx.x * 16, k = a.k;
-  // A load covers 8 rows' whole 128-byte lines: lanes of q < 8 take the first half
-  // of row q % 8's, the others the second; the fragments want lane q to hold row q,
-  // so two loads of 8 rows trade halves (fragments()).
   const uint16_t* wr[NI][2];
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int32_t r = r0 + 8 * h + (q & 7);
-      wr[i][h] = (i ? a.w1 : a.w0) + (int64_t)(r < a.rows ? r : a.rows - 1) * (i ? a.ldw1 : a.ldw0);
+      const int64_t at = r < a.rows ? r : a.rows - 1;
+      wr[i][h] = i ? a.w1 + at * a.ldw1 : a.w0 + at * a.ldw0;
     }
-  const uint16_t* xr[NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int32_t t = 16 * j + q;
-    xr[j] = a.x + (int64_t)(t < a.tokens ? t : a.tokens - 1) * a.ldx;
-  }
+  const uint16_t* xr = a.x + (int64_t)(q < a.tokens ? q : a.tokens - 1) * a.ldx;
   const int32_t wk = 8 * (4 * (q >> 3) + g);
   const int beyond = (8 - k % 8) % 8;
-  // A piece that passes the row's end is loaded from the row's last eight elements;
-  // what does not belong to it is taken out before it is used.
-  auto inside = [&](int32_t c) { return c + 8 <= k ? c : k - 8; };
-  auto load = [&](const uint16_t* row, int32_t c) {
-    if constexpr (LONG) return __builtin_bit_cast(s16x8, *(const u32x4_a2*)(row + inside(c)));
-    else return short_row(row, c, k);
-  };
-  auto held = [&](s16x8 v, int32_t c) {
-    if (c >= k) return s16x8{};
-    return LONG && c + 8 > k ? drop_first(v, beyond) : v;
-  };
-  f32x4 acc[NI][NJ];
+  f32x4 acc[NI];
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{};
+  for (int i = 0; i < NI; ++i) acc[i] = f32x4{};
   struct Step {
     s16x8 w[NI][2][2];  // [line][rows 0-7 or 8-15]
-    s16x8 x[4][NJ];
+    s16x8 x[4];
   };
   auto fetch = [&](Step& d, int32_t tile) {
-    const int32_t c = tile * kTile;
+    const int32_t c = tile * kFewTile;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int l = 0; l < 2; ++l)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) d.w[i][l][h] = load(wr[i][h], c + 64 * l + wk);
+        for (int h = 0; h < 2; ++h) d.w[i][l][h] = row8(wr[i][h], c + 64 * l + wk, k);
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) d.x[s][j] = load(xr[j], c + 32 * s + 8 * g);
-  };
-  auto fragments = [&](const s16x8 (&d)[2], s16x8 (&f)[2]) {
-    const u32x4 lo = __builtin_bit_cast(u32x4, d[0]), hi = __builtin_bit_cast(u32x4, d[1]);
-    const bool first = q < 8;
-    u32x4 u, v;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t give = first ? hi[e] : lo[e];
-      const uint32_t got =
-          (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, false);
-      u[e] = first ? lo[e] : got;
-      v[e] = first ? got : hi[e];
-    }
-    f[0] = __builtin_bit_cast(s16x8, u);
-    f[1] = __builtin_bit_cast(s16x8, v);
+    for (int s = 0; s < 4; ++s) d.x[s] = row8(xr, c + 32 * s + 8 * g, k);
   };
   auto use = [&](Step& d, int32_t tile) {
-    const int32_t c = tile * kTile;
-    if (c + kTile > k) {
+    const int32_t c = tile * kFewTile;
+    if (c + kFewTile > k) {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int l = 0; l < 2; ++l)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) d.w[i][l][h] = held(d.w[i][l][h], c + 64 * l + wk);
+          for (int h = 0; h < 2; ++h)
+            d.w[i][l][h] = held8(d.w[i][l][h], c + 64 * l + wk, k, beyond);
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) d.x[s][j] = held(d.x[s][j], c + 32 * s + 8 * g);
+      for (int s = 0; s < 4; ++s) d.x[s] = held8(d.x[s], c + 32 * s + 8 * g, k, beyond);
     }
 #pragma unroll
     for (int l = 0; l < 2; ++l)
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         s16x8 f[2];
-        fragments(d.w[i][l], f);
+        fragments(d.w[i][l], f, q < 8);
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) acc[i][j] = mfma(T{}, f[s], d.x[2 * l + s][j], acc[i][j]);
+        for (int s = 0; s < 2; ++s) acc[i] = mfma(T{}, f[s], d.x[2 * l + s], acc[i]);
       }
   };
   // The wave's steps: every WAVES-th, from another place in each workgroup, since rows
   // of a power of two columns would all ask the same memory channels.  What is
   // fetched past the last one is the last one again, from the cache.
-  const int32_t tiles = (k + kTile - 1) / kTile;
+  const int32_t tiles = (k + kFewTile - 1) / kFewTile;
   const int32_t count = wave < tiles ? (tiles - wave + WAVES - 1) / WAVES : 0;
   if (count > 0) {
     const int32_t from = (int32_t)(blockIdx.x / kXcds) % count;
@@ -161,68 +189,244 @@ k_ffn_few(const Few a) {
     }
   }
 #pragma unroll
+  for (int i = 0; i < NI; ++i) s_sum[wave][i][lane] = acc[i];
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) s_sum[wave][i * NJ + j][lane] = acc[i][j];
-  __syncthreads();
-  if (wave >= NJ) return;
-  const int32_t t = 16 * wave + q, r = r0 + 4 * g;
-  f32x4 sum[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    sum[i] = s_sum[0][i * NJ + wave][lane];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) sum[i] += s_sum[w][i * NJ + wave][lane];
-  }
-  if (t >= a.tokens) return;
+    for (int w = 1; w < WAVES; ++w) acc[i] += s_sum[w][i][lane];
+  const int32_t r = r0 + 4 * g;
   if constexpr (PAIR) {
-    if (r >= a.pad) return;
-    f32x4 h;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (r + e >= a.rows) sum[0][e] = sum[1][e] = 0.0f;
-    with_act(a.act, [&](auto act) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = activated(act, sum[0][e]) * sum[1][e];
-    });
-    *(u32x2*)(a.out + t * a.ldo + r) = narrow4<T>(h[0], h[1], h[2], h[3]);
-    if (a.gate) {
-      *(u32x2*)(a.gate + t * a.lds + r) = narrow4<T>(sum[0][0], sum[0][1], sum[0][2], sum[0][3]);
-      *(u32x2*)(a.up + t * a.lds + r) = narrow4<T>(sum[1][0], sum[1][1], sum[1][2], sum[1][3]);
-    }
-  } else {
-    uint16_t* o = a.out + t * a.ldo + r;
-    const u32x2 v = narrow4<T>(sum[0][0], sum[0][1], sum[0][2], sum[0][3]);
-    if (r + 4 <= a.rows) {
-      *(u32x2_a2*)o = v;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (r + e < a.rows) o[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-    }
+    with_act(a.act, [&](auto act) { leave_pair<T>(a, act, acc[0], acc[1], q, r); });
+  } else if (q < a.tokens && r < a.rows) {
+    leave4<T>(a.out + q * a.ldo, r, a.rows, acc[0]);
   }
 }
 
-template <typename T, int NJ, int WAVES, bool PAIR>
-int few_k(const Few& a, hipStream_t stream) {
-  const dim3 grid((uint32_t)((a.rows + 15) / 16)), block(64 * WAVES);
-  if (a.k >= 8)
-    hipLaunchKernelGGL((k_ffn_few<T, NJ, WAVES, PAIR, true>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((k_ffn_few<T, NJ, WAVES, PAIR, false>), grid, block, 0, stream, a);
+// More tokens: x goes through LDS.
+template <typename T, int NJ, int R, bool PAIR>
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))) void
+k_ffn_shared(const Few a) {
+  constexpr int NI = 2, S = kWaves / R, XLOADS = 4 * NJ / R > 0 ? 4 * NJ / R : 1;
+  constexpr int kTileBytes = 16 * NJ * 2 * kFewTile, kSums = NI * NJ * 1024;
+  constexpr int kLds = 2 * S * kTileBytes > (S - 1) * R * kSums ? 2 * S * kTileBytes
+                                                               : (S - 1) * R * kSums;
+  __shared__ __attribute__((aligned(1024))) char lds[kLds];
+  const int lane = threadIdx.x & 63, g = lane >> 4, q = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int set = wave % R, slice = wave / R;
+  const int32_t k = a.k;
+  const int32_t block = (int32_t)(blockIdx.x / (uint32_t)a.split);
+  const int32_t part = (int32_t)(blockIdx.x % (uint32_t)a.split);
+  const int32_t r0 = (block * R + set) * (PAIR ? 16 : 16 * NI);
+  const uint16_t* wr[NI][2];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int32_t r = r0 + (PAIR ? 0 : 16 * i) + 8 * h + (q & 7);
+      const int64_t at = r < a.rows ? r : a.rows - 1;
+      wr[i][h] = PAIR && i ? a.w1 + at * a.ldw1 : a.w0 + at * a.ldw0;
+    }
+  const int32_t wk = 8 * (4 * (q >> 3) + g);
+  // x: thread of a slice's sets loads chunk % 16 of rows / 16
+  const int xt = set * 64 + lane, xc = xt & 15;
+  const uint16_t* xr[XLOADS];
+#pragma unroll
+  for (int n = 0; n < XLOADS; ++n) {
+    const int32_t t = (xt >> 4) + 4 * R * n;
+    xr[n] = a.x + (int64_t)(t < a.tokens ? t : a.tokens - 1) * a.ldx;
+  }
+  const bool stores_x = 4 * R <= 16 * NJ || (xt >> 4) < 16 * NJ;
+  char* const lx = lds + slice * 2 * kTileBytes;
+  const int beyond = (8 - k % 8) % 8;
+  auto load = [&](const uint16_t* row, int32_t c) { return row8(row, c, k); };
+  auto held = [&](s16x8 v, int32_t c) { return held8(v, c, k, beyond); };
+  f32x4 acc[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{};
+  // [rows][line][rows 0-7 or 8-15]
+  s16x8 w[2][NI][2][2], xs[XLOADS];
+  auto fetch_w = [&](s16x8 (&d)[NI][2][2], int32_t tile) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int l = 0; l < 2; ++l)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) d[i][l][h] = load(wr[i][h], tile * kFewTile + 64 * l + wk);
+  };
+  auto fetch_x = [&](int32_t tile) {
+#pragma unroll
+    for (int n = 0; n < XLOADS; ++n) xs[n] = load(xr[n], tile * kFewTile + 8 * xc);
+  };
+  auto store_x = [&](char* d, int32_t tile) {
+    if ((tile + 1) * kFewTile > k) {
+#pragma unroll
+      for (int n = 0; n < XLOADS; ++n) xs[n] = held(xs[n], tile * kFewTile + 8 * xc);
+    }
+#pragma unroll
+    for (int n = 0; n < XLOADS; ++n) {
+      const int row = (xt >> 4) + 4 * R * n;
+      if (stores_x) *(s16x8*)(d + row * 256 + ((xc ^ (row & 15)) << 4)) = xs[n];
+    }
+  };
+  auto use = [&](s16x8 (&d)[NI][2][2], const char* l, int32_t tile) {
+    if ((tile + 1) * kFewTile > k) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            d[i][n][h] = held(d[i][n][h], tile * kFewTile + 64 * n + wk);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      s16x8 f[NI][2];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) fragments(d[i][n], f[i], q < 8);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const s16x8 b =
+              *(const s16x8*)(l + (16 * j + q) * 256 + (((8 * n + 4 * s + g) ^ q) << 4));
+#pragma unroll
+          for (int i = 0; i < NI; ++i) acc[i][j] = mfma(T{}, f[i][s], b, acc[i][j]);
+        }
+    }
+  };
+  // The part's steps are dealt to the slices in turn, and taken from another place in
+  // each workgroup, since rows of a power of two columns would all ask the same memory
+  // channels.
+  const int32_t tiles = (k + kFewTile - 1) / kFewTile;
+  const int32_t first = (int32_t)((int64_t)tiles * part / a.split);
+  const int32_t own = (int32_t)((int64_t)tiles * (part + 1) / a.split) - first;
+  const int32_t steps = (own + S - 1) / S;
+  const int32_t from = (int32_t)(blockIdx.x / kXcds) % steps;
+  auto place = [&](int32_t t) {  // of step t, within the part
+    t = (t < steps ? t : steps - 1) + from;
+    return (t < steps ? t : t - steps) * S + slice;
+  };
+  // a slice without a tile in the last step loads another one again and skips it
+  auto tile = [&](int32_t t) {
+    const int32_t p = place(t);
+    return first + (p < own ? p : own - 1);
+  };
+  // the buffer of the step before last is free, the next one's is written
+  auto turn = [&] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+  fetch_w(w[0], tile(0));
+  fetch_x(tile(0));
+  store_x(lx, tile(0));
+  fetch_x(tile(1));
+  for (int32_t t = 0; t < steps; t += 2) {
+    turn();
+    fetch_w(w[1], tile(t + 1));
+    store_x(lx + kTileBytes, tile(t + 1));
+    fetch_x(tile(t + 2));
+    if (place(t) < own) use(w[0], lx, tile(t));
+    turn();
+    fetch_w(w[0], tile(t + 2));
+    store_x(lx, tile(t + 2));
+    fetch_x(tile(t + 3));
+    if (t + 1 < steps && place(t + 1) < own) use(w[1], lx + kTileBytes, tile(t + 1));
+  }
+  if constexpr (S > 1) {
+    f32x4* sums = (f32x4*)lds + lane;
+    __syncthreads();
+    if (slice > 0) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          sums[(((slice - 1) * R + set) * NI * NJ + i * NJ + j) * 64] = acc[i][j];
+    }
+    __syncthreads();
+    if (slice > 0) return;
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s)
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] += sums[((s * R + set) * NI * NJ + i * NJ + j) * 64];
+  }
+  if constexpr (PAIR) {
+    with_act(a.act, [&](auto act) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        leave_pair<T>(a, act, acc[0][j], acc[1][j], 16 * j + q, r0 + 4 * g);
+    });
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int32_t t = 16 * j + q, r = r0 + 16 * i + 4 * g;
+        if (t >= a.tokens || r >= a.rows) continue;
+        if (a.split > 1)
+          *(f32x4*)(a.acc + ((int64_t)part * a.tokens + t) * a.pad + r) = acc[i][j];
+        else leave4<T>(a.out + t * a.ldo, r, a.rows, acc[i][j]);
+      }
+  }
+}
+
+// The parts' sums, four columns a thread.
+constexpr int kJoinThreads = 64;
+template <typename T>
+__global__ __launch_bounds__(kJoinThreads) void k_ffn_few_join(
+    const float* __restrict__ acc, int32_t split, int32_t tokens, int32_t pad, int32_t rows,
+    uint16_t* __restrict__ out, int64_t ldo) {
+  const int32_t t = blockIdx.y, r = (int32_t)(blockIdx.x * kJoinThreads + threadIdx.x) * 4;
+  if (r >= rows) return;
+  const float* p = acc + (int64_t)t * pad + r;
+  f32x4 s = *(const f32x4*)p;
+#pragma unroll 8
+  for (int32_t n = 1; n < split; ++n) s += *(const f32x4*)(p + (int64_t)n * tokens * pad);
+  leave4<T>(out + t * ldo, r, rows, s);
+}
+
+template <typename T, int NJ, int R, bool PAIR>
+int shared_r(const Few& a, hipStream_t stream) {
+  const int32_t each = PAIR ? 16 * R : 32 * R;
+  hipLaunchKernelGGL((k_ffn_shared<T, NJ, R, PAIR>),
+                     dim3((uint32_t)((a.rows + each - 1) / each * a.split)), dim3(64 * kWaves), 0,
+                     stream, a);
   return (int)hipGetLastError();
 }
 
 template <typename T, int NJ>
-int few_j(const Few& in, const Few& out, hipStream_t stream) {
-  const int e = few_k<T, NJ, 4, true>(in, stream);
-  return e ? e : few_k<T, NJ, 8, false>(out, stream);
+int shared_j(const Few& in, const Few& out, const FfnPlan& p, hipStream_t stream) {
+  int e = p.few_sets_in == 4 ? shared_r<T, NJ, 4, true>(in, stream)
+                             : shared_r<T, NJ, 2, true>(in, stream);
+  if (e) return e;
+  e = p.few_sets_out == 4 ? shared_r<T, NJ, 4, false>(out, stream)
+                          : shared_r<T, NJ, 2, false>(out, stream);
+  if (e || out.split == 1) return e;
+  hipLaunchKernelGGL((k_ffn_few_join<T>),
+                     dim3((uint32_t)((out.rows + 4 * kJoinThreads - 1) / (4 * kJoinThreads)),
+                          (uint32_t)out.tokens),
+                     dim3(kJoinThreads), 0, stream, out.acc, out.split, out.tokens, out.pad,
+                     out.rows, out.out, out.ldo);
+  return (int)hipGetLastError();
+}
+
+template <typename T>
+int direct(const Few& in, const Few& out, hipStream_t stream) {
+  hipLaunchKernelGGL((k_ffn_direct<T, 4, true>), dim3((uint32_t)((in.rows + 15) / 16)), dim3(256),
+                     0, stream, in);
+  ZK_LAUNCHED();
+  hipLaunchKernelGGL((k_ffn_direct<T, 8, false>), dim3((uint32_t)((out.rows + 15) / 16)),
+                     dim3(512), 0, stream, out);
+  return (int)hipGetLastError();
 }
 
 template <typename T>
 int few_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, void* y, int64_t ldy,
           const zero_ffn_saved_t* saved, hipStream_t stream) {
-  uint16_t* h = at<uint16_t>(ws, p.h);
+  const Kept to = kept(p, ws, saved);
   Few in{};
   in.w0 = (const uint16_t*)f->w_gate;
   in.w1 = (const uint16_t*)f->w_up;
@@ -234,27 +438,27 @@ int few_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, void* y, int64_t ldy,
   in.k = (int32_t)f->hidden;
   in.tokens = (int32_t)f->tokens;
   in.act = f->act;
-  in.out = h;
-  in.ldo = p.inner_pad;
+  in.split = 1;
+  in.to = to;
   in.pad = (int32_t)p.inner_pad;
-  if (saved) {
-    in.gate = (uint16_t*)saved->gate;
-    in.up = (uint16_t*)saved->up;
-    in.lds = saved->ld;
-  }
   Few out{};
-  out.w0 = out.w1 = (const uint16_t*)f->w_down;
-  out.ldw0 = out.ldw1 = f->ld_down;
-  out.x = h;
-  out.ldx = p.inner_pad;
+  out.w0 = (const uint16_t*)f->w_down;
+  out.ldw0 = f->ld_down;
+  out.x = to.h;
+  out.ldx = to.ld;
   out.rows = (int32_t)f->hidden;
   out.k = (int32_t)f->inner;
   out.tokens = (int32_t)f->tokens;
+  out.split = p.split_y;
+  out.pad = (int32_t)p.hidden_pad;
   out.out = (uint16_t*)y;
   out.ldo = ldy;
-  if (f->tokens <= 16) return few_j<T, 1>(in, out, stream);
-  if (f->tokens <= 32) return few_j<T, 2>(in, out, stream);
-  return few_j<T, 4>(in, out, stream);
+  out.acc = at<float>(ws, p.acc);
+  if (p.few_sets_in == 1) return direct<T>(in, out, stream);
+  if (f->tokens <= 16) return shared_j<T, 1>(in, out, p, stream);
+  if (f->tokens <= 32) return shared_j<T, 2>(in, out, p, stream);
+  if (f->tokens <= 48) return shared_j<T, 3>(in, out, p, stream);
+  return shared_j<T, 4>(in, out, p, stream);
 }
 
 }  // namespace

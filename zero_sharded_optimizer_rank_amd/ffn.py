@@ -20,10 +20,10 @@ ACTIVATIONS = {"silu": abi.ZERO_ACT_SILU, "gelu": abi.ZERO_ACT_GELU,
 
 
 class FFNSaved(NamedTuple):
-    """What the gradients need of a forward pass: both projections in 16 bits, their columns
-    padded to a multiple of 8."""
-    gate: torch.Tensor
-    up: torch.Tensor
+    """What the gradients need of a forward pass, in 16 bits, columns padded to a multiple of 8."""
+    act: torch.Tensor     # act(x @ w_gate.T)
+    slope: torch.Tensor   # (x @ w_up.T) * act'(x @ w_gate.T)
+    h: torch.Tensor       # act * (x @ w_up.T)
 
 
 class FFNOut(NamedTuple):
@@ -93,11 +93,11 @@ class GatedFFN:
         return need
 
     def new_saved(self, tokens: Optional[int] = None) -> FFNSaved:
-        """Buffers for a forward pass to keep its projections in: one pair a layer whose
+        """Buffers for a forward pass to keep what its gradients need: one set a layer whose
         gradients are still to come."""
         tokens = self.tokens if tokens is None else tokens
         return FFNSaved(*(torch.empty(tokens, self._pad, dtype=self.dtype, device=self.device)
-                          for _ in range(2)))
+                          for _ in range(3)))
 
     def _matrix(self, t, rows, cols, what, types=None):
         if not isinstance(t, torch.Tensor) or t.dim() != 2 or tuple(t.shape) != (rows, cols):
@@ -128,14 +128,14 @@ class GatedFFN:
     def _saved_t(self, saved, t):
         if not isinstance(saved, FFNSaved):
             raise TypeError("saved must be an FFNSaved")
-        lds = []
-        for b, what in ((saved.gate, "gate"), (saved.up, "up")):
+        lds = set()
+        for b, what in zip(saved, saved._fields):
             if not isinstance(b, torch.Tensor) or b.dim() != 2 or b.shape[0] < t:
-                raise ValueError(f"{what} must be a [{t}, {self._pad}] tensor")
-            lds.append(self._matrix(b[:t], t, self._pad, what))
-        if lds[0] != lds[1] and t > 1:
-            raise ValueError("the rows of gate and up lie differently")
-        return abi.zero_ffn_saved_t(saved.gate.data_ptr(), saved.up.data_ptr(), lds[0])
+                raise ValueError(f"saved.{what} must be a [{t}, {self._pad}] tensor")
+            lds.add(self._matrix(b[:t], t, self._pad, "saved." + what))
+        if len(lds) > 1:
+            raise ValueError("the rows of act, slope and h lie differently")
+        return abi.zero_ffn_saved_t(*(b.data_ptr() for b in saved), lds.pop())
 
     def _workspace(self, ffn, grads, stream):
         # rows that do not start on 16-byte boundaries take copies in the workspace
