@@ -20,6 +20,7 @@ struct FfnPlan {
   int64_t hidden_pad, inner_pad;  // row lengths of packed matrices: multiples of 8
   bool few;
   bool pack_x, pack_gate, pack_up, pack_down, pack_dy;  // rows that no 16-byte loads fit
+  bool small_in, small_out, small_back1, small_back2;  // 128 x 128 tiles, else 256 x 256
   int32_t split_y, split_dx;      // ways the contractions over the inner axis are split
   int32_t few_sets_in, few_sets_out;  // few: sets of rows of a workgroup, 2 or 4; 1: x is
                                       // not shared

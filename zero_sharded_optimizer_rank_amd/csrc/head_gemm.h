@@ -98,14 +98,14 @@ struct Operand {
 
 constexpr int kStage = 64;  // contraction indexes of a stage
 
-// R tile rows (columns of memory if COLS) staged by eight waves.  HALF 0 or 1:
+// R tile rows (columns of memory if COLS) staged by WAVES waves.  HALF 0 or 1:
 // R = 128 of the tile's 256 rows, local row r is row r / 64 * 128 + 64 * HALF +
 // r % 64; HALF < 0: all rows.
-template <int R, bool COLS, int HALF>
+template <int R, bool COLS, int HALF, int WAVES = 8>
 struct Part {
   static constexpr int kBytes = R * kStage * 2;
-  static constexpr int kLoads = kBytes / (8 * 1024);  // 1 KiB loads of a wave
-  static_assert(kLoads * 8 * 1024 == kBytes && (HALF < 0 || R == 128), "whole loads");
+  static constexpr int kLoads = kBytes / (WAVES * 1024);  // 1 KiB loads of a wave
+  static_assert(kLoads * WAVES * 1024 == kBytes && (HALF < 0 || R == 128), "whole loads");
 
   // Issue the loads of contraction indexes [k0, k0 + 64) into lds; past the
   // contraction's end they read zero.

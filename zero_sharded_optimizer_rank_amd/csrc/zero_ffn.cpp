@@ -92,23 +92,36 @@ bool ragged(const void* p, int64_t ld, int64_t width) {
 // Workgroups of few tokens' first product that are enough for the 256 CUs.
 constexpr int64_t kFewGroups = 192;
 
-// Ways to split a contraction whose output has few tiles: up to one round of
-// the 256 CUs, of at least four stages each.
-int32_t split_of(int64_t out_tiles, int64_t k) {
-  const int64_t stages = tiles(k, zk::kFfnStep);
-  int64_t s = 256 / (out_tiles > 0 ? out_tiles : 1);
-  if (s > stages / 4) s = stages / 4;
+// A product's tiles and their stages; small tiles share a CU by two.
+struct Work {
+  int64_t count, stages;
+};
+Work work(int64_t rows, int64_t cols, int64_t k, bool small) {
+  const int64_t t = small ? 128 : 256;
+  return {tiles(rows, t) * tiles(cols, t), tiles(k, zk::kFfnStep)};
+}
+int64_t places(bool small) { return small ? 512 : 256; }
+
+// Ways to split a contraction whose output has few tiles: up to three quarters of
+// a round of them, of at least four stages each (more parts cost more in their
+// fp32 sums than idle CUs do: 512 x 4096 x 14336, 32 tiles, in 4 / 6 / 7 / 9 parts 203 /
+// 197 / 200 / 216 us a forward pass; 1024 x 1600 x 6400, 28 tiles, in 3 / 5 / 7 / 9 108 / 99
+// / 98 / 100).
+int32_t split_of(const Work& w, bool small) {
+  int64_t s = places(small) * 3 / 4 / (w.count > 0 ? w.count : 1);
+  if (s > w.stages / 4) s = w.stages / 4;
   return (int32_t)(s < 1 ? 1 : s);
 }
-// Ways where other tiles share the launch: no part longer than three quarters of
-// what a CU gets of the whole (in stages; the others fill up behind), or than
-// split_of has it.
-int32_t split_beside(int64_t out_tiles, int64_t k, int64_t other_stages) {
-  const int64_t stages = tiles(k, zk::kFfnStep);
-  const int64_t each = (out_tiles * stages + other_stages) / 256 * 3 / 4;
-  int64_t s = tiles(stages, each > 4 ? each : 4);
-  const int32_t most = split_of(out_tiles, k);
-  return (int32_t)(s < most ? s : most);
+// Ways where other tiles share the launch and fill up behind: a part is about as
+// long as what a CU gets of the whole (1024 x 1600 x 6400, 200 stages of 44 a CU, in 3 /
+// 4 / 5 / 9 parts 279 / 259 / 266 / 280 us a training pass; 512 x 4096 x 14336, 448 of 112,
+// in 3 / 4 / 5 / 6 593 / 562 / 568 / 591).
+int32_t split_beside(const Work& w, int64_t other_stages, bool small) {
+  const int64_t all = w.count * w.stages + other_stages;
+  int64_t s = w.stages * places(small) / (all > 0 ? all : 1);
+  const int32_t most = split_of(w, small);
+  if (s > most) s = most;
+  return (int32_t)(s < 1 ? 1 : s);
 }
 
 }  // namespace
@@ -128,9 +141,19 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
     p.pack_down = ragged(f->w_down, f->ld_down, F);
     p.pack_dy = g && ragged(g->dy, g->lddy, H);
   }
-  const int64_t out_tiles = tiles(T, kFfnTile) * tiles(H, kFfnTile);
+  // Small tiles where the large ones would leave half of the CUs idle (100 x 4096 x 14336,
+  // 112 tiles, forward 130 -> 107 us; 1024 x 1600 x 6400, 200 tiles, 88 -> 100), in a
+  // backward pass where a CU's share is short, so that a tile's start and end weigh
+  // (300 x 1600 x 6400, training 194 -> 165 us; 512 x 4096 x 14336 563 -> 654), and for y of
+  // up to one small tile's tokens.
+  const Work in = work(2 * F, T, H, false), dh = work(F, T, H, false), dw = work(F, H, T, false);
+  const Work dx = work(T, H, 2 * F, false);
+  p.small_in = in.count < 128;
+  p.small_out = T <= 128;
+  p.small_back1 = dh.count * dh.stages + dw.count * dw.stages < 24 * 256;
+  p.small_back2 = dx.count * dx.stages + 2 * dw.count * dw.stages < 24 * 256;
   p.split_y = p.split_dx = 1;
-  if (!p.few && !g) p.split_y = split_of(out_tiles, F);
+  if (!p.few && !g) p.split_y = split_of(work(T, H, F, p.small_out), p.small_out);
   if (p.few) {
     p.few_sets_in = T <= 8 ? 1 : tiles(F, 64) >= kFewGroups ? 4 : 2;
     p.few_sets_out = T <= 8 ? 1 : H >= 2048 ? 4 : 2;
@@ -143,8 +166,10 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
     }
   }
   if (g) {
-    const int64_t dw = tiles(F, kFfnTile) * tiles(H, kFfnTile) * tiles(T, kFfnStep);
-    p.split_dx = split_beside(out_tiles, 2 * F, (g->dw_gate ? dw : 0) + (g->dw_up ? dw : 0));
+    const Work w = work(F, H, T, p.small_back2);
+    const int64_t each = w.count * w.stages;
+    p.split_dx = split_beside(work(T, H, 2 * F, p.small_back2),
+                              (g->dw_gate ? each : 0) + (g->dw_up ? each : 0), p.small_back2);
   }
   size_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -176,7 +201,7 @@ extern "C" {
 size_t zero_ffn_workspace_bytes(const zero_ffn_t* ffn, const zero_ffn_grads_t* grads) {
   if (!ffn || !good_sizes(ffn) || (grads && !good_ld(grads->lddy, ffn->hidden))) return 0;
   // a batch of fewer tokens, or a call for fewer gradients, may be split more ways: at
-  // most split_of's; the plan changes by the tile
+  // most split_of's; the plan changes by the stage of 64
   zero_ffn_t f = *ffn;
   zero_ffn_grads_t only;
   if (grads) {
@@ -190,7 +215,7 @@ size_t zero_ffn_workspace_bytes(const zero_ffn_t* ffn, const zero_ffn_grads_t* g
     if (n > need) need = n;
   };
   for (int64_t t = 1; t <= zk::kFfnFew; ++t) count(t);
-  for (int64_t t = 0; t < ffn->tokens; t += zk::kFfnTile) count(t + zk::kFfnTile);
+  for (int64_t t = zk::kFfnFew; t < ffn->tokens; t += zk::kFfnStep) count(t + zk::kFfnStep);
   return need;
 }
 

@@ -8,18 +8,19 @@
 //   backward  k_ffn_back1  dh = dy Wd, whose tiles leave as dg and du; dWd = dy^T h
 //             k_ffn_back2  dx = dg Wg + du Wu, one contraction over both; dWg, dWu
 // What does not wait for one another shares a launch, so that the tiles of one
-// fill the CUs that the last round of the other leaves idle.  All products are 256
-// x 256 tiles of head_gemm.h with fp32 sums; every operand is read as it lies.
+// fill the CUs that the last round of the other leaves idle.  All products are the
+// tiles of ffn_gemm.h (SMALL: 128 x 128) with fp32 sums; every operand is read as it
+// lies.
 #include <stddef.h>
 
 #include "ffn_device.h"
+#include "ffn_gemm.h"
 
 namespace zk {
 namespace {
 
 using namespace dev;
 
-constexpr int kGemmThreads = 512;
 constexpr int kPackThreads = 256;
 
 // Rows in whole 16-byte pieces: copies for matrices whose rows lie otherwise.
@@ -63,6 +64,9 @@ __device__ __forceinline__ void store_row(uint16_t* row, int32_t c, int32_t n, u
   }
 }
 
+template <int N>
+__device__ __forceinline__ uint32_t tiles_of(int32_t x) { return (uint32_t)((x + N - 1) / N); }
+
 // --- forward -------------------------------------------------------------------
 struct PairProduct {
   Operand gate, up, B;
@@ -71,22 +75,21 @@ struct PairProduct {
   __device__ __forceinline__ const Operand& b(int32_t&) const { return B; }
 };
 
-// A tile: 128 inner columns of both projections, 256 tokens, so that a lane holds g
-// and u of the same element.  What the gradients need is formed here, from the fp32
+// A tile has the same inner columns of both projections, so that a lane holds g and u
+// of the same element.  What the gradients need is formed here, from the fp32
 // sums, so that the backward pass has two products an element left to do.
-template <typename T, int ACT, bool SAVE>
-__global__ __launch_bounds__(kGemmThreads) void k_ffn_in(Matrix x, Matrix w_gate, Matrix w_up,
-                                                         int32_t tokens, int32_t inner,
-                                                         int32_t inner_pad, Kept to) {
-  using G = Gemm<T, false, false, true>;
-  ZK_GEMM_LDS;
+template <typename T, int ACT, bool SAVE, bool SMALL>
+__global__ __launch_bounds__(SMALL ? 256 : 512) void k_ffn_in(Matrix x, Matrix w_gate, Matrix w_up,
+                                                              int32_t tokens, int32_t inner,
+                                                              int32_t inner_pad, Kept to) {
+  using G = typename TileOf<SMALL, T, false, false, true>::G;
+  const auto lds = G::shared();
   int32_t mt, nt;
-  if (!tile_of(blockIdx.x, (uint32_t)((inner + 127) / 128), (uint32_t)((tokens + 255) / 256), mt,
-               nt))
-    return;
-  const int32_t f0 = mt * 128, t0 = nt * 256;
-  const PairProduct src{by_rows(w_gate, f0, inner, 128), by_rows(w_up, f0, inner, 128),
-                        by_rows(x, t0, tokens, 256)};
+  if (!tile_of(blockIdx.x, tiles_of<G::kRows>(inner), tiles_of<G::kCols>(tokens), mt, nt)) return;
+  const int32_t f0 = mt * G::kRows, t0 = nt * G::kCols;
+  const PairProduct src{by_rows(w_gate, f0, inner, G::kRows), by_rows(w_up, f0, inner, G::kRows),
+                        by_rows(x, t0, tokens, G::kCols)};
+  constexpr int H = G::MI / 2;
   f32x4 acc[G::MI][G::NJ];
   G::run(src, x.width, lds, acc);
   auto leave = [&](uint16_t* out, int region) {
@@ -98,11 +101,11 @@ __global__ __launch_bounds__(kGemmThreads) void k_ffn_in(Matrix x, Matrix w_gate
 #pragma unroll
   for (int j = 0; j < G::NJ; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < H; ++i) {
       f32x4 a, b, h;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float u = acc[4 + i][j][e];
+        const float u = acc[H + i][j][e];
         float slope;
         a[e] = activated(Act<ACT>{}, acc[i][j][e], slope);
         b[e] = u * slope;
@@ -126,7 +129,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_ffn_in(Matrix x, Matrix w_gate
 #pragma unroll
     for (int j = 0; j < G::NJ; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < H; ++i)
         G::put_half(lds, 0, i, j,
                     u32x2{__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1])});
     __syncthreads();
@@ -169,23 +172,24 @@ struct OutArgs {
   int64_t ldo;
 };
 
-template <typename T, bool DX>
-__device__ __forceinline__ void out_tile(uint32_t block, const OutArgs& o, const GemmLds& lds) {
-  using G = Gemm<T, DX, false>;
-  const uint32_t ht = (uint32_t)((o.hidden + 255) / 256);
+template <typename T, bool DX, bool SMALL>
+__device__ __forceinline__ void out_tile(uint32_t block, const OutArgs& o) {
+  using G = typename TileOf<SMALL, T, DX, false>::G;
+  const auto lds = G::shared();
+  const uint32_t ht = tiles_of<G::kRows>(o.hidden);
   int32_t mt, nt;
-  if (!tile_of(block, (uint32_t)((o.tokens + 255) / 256), ht * (uint32_t)o.split, mt, nt)) return;
-  const int32_t h0 = (int32_t)((uint32_t)nt % ht) * 256, t0 = mt * 256;
+  if (!tile_of(block, tiles_of<G::kCols>(o.tokens), ht * (uint32_t)o.split, mt, nt)) return;
+  const int32_t h0 = (int32_t)((uint32_t)nt % ht) * G::kRows, t0 = mt * G::kCols;
   const int32_t part = (int32_t)((uint32_t)nt / ht);
   const int32_t stages = (o.inner + kStage - 1) / kStage, all = DX ? 2 * stages : stages;
   const int32_t s0 = (int32_t)((int64_t)all * part / o.split);
   const int32_t s1 = (int32_t)((int64_t)all * (part + 1) / o.split);
   Products<DX> src;
-  src.A1 = DX ? by_cols(o.a1, h0, o.inner) : by_rows(o.a1, h0, o.hidden, 256);
-  src.B1 = by_rows(o.b1, t0, o.tokens, 256);
+  src.A1 = DX ? by_cols(o.a1, h0, o.inner) : by_rows(o.a1, h0, o.hidden, G::kRows);
+  src.B1 = by_rows(o.b1, t0, o.tokens, G::kCols);
   if constexpr (DX) {
     src.A2 = by_cols(o.a2, h0, o.inner);
-    src.B2 = by_rows(o.b2, t0, o.tokens, 256);
+    src.B2 = by_rows(o.b2, t0, o.tokens, G::kCols);
   }
   src.k0 = s0 * kStage;
   src.k1 = stages * kStage;
@@ -202,19 +206,18 @@ __device__ __forceinline__ void out_tile(uint32_t block, const OutArgs& o, const
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int j = 0; j < G::NJ; ++j) {
-    const int32_t t = t0 + (wave % 4) * 64 + j * 16 + (lane & 15);
+    const int32_t t = t0 + G::col(wave, j) + (lane & 15);
     float* p = o.acc + ((int64_t)part * o.acc_rows + t) * o.acc_ld;
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int i = 0; i < G::MI; ++i)
-      *(f32x4*)(p + h0 + wave / 4 * 128 + 16 * i + 4 * (lane >> 4)) = acc[i][j];
+      *(f32x4*)(p + h0 + G::row(wave, i) + 4 * (lane >> 4)) = acc[i][j];
   }
 }
 
-template <typename T>
-__global__ __launch_bounds__(kGemmThreads) void k_ffn_out(OutArgs o) {
-  ZK_GEMM_LDS;
-  out_tile<T, false>(blockIdx.x, o, lds);
+template <typename T, bool SMALL>
+__global__ __launch_bounds__(SMALL ? 256 : 512) void k_ffn_out(OutArgs o) {
+  out_tile<T, false, SMALL>(blockIdx.x, o);
 }
 
 // The splits' sums, four columns a thread.
@@ -254,24 +257,24 @@ struct DhArgs {
 // A tile of dh: A = Wd by its columns (inner), B = dy by its rows; it leaves as dg =
 // dh (u act'(g)) and du = dh act(g).  Lane by lane those lie as the sums do, eight
 // bytes each; the next column's are on their way while one is multiplied.
-template <typename T>
-__device__ __forceinline__ void dh_tile(uint32_t block, const DhArgs& a, const GemmLds& lds) {
-  using G = Gemm<T, true, false>;
+template <typename T, bool SMALL>
+__device__ __forceinline__ void dh_tile(uint32_t block, const DhArgs& a) {
+  using G = typename TileOf<SMALL, T, true, false>::G;
+  const auto lds = G::shared();
   int32_t mt, nt;
-  if (!tile_of(block, (uint32_t)((a.inner + 255) / 256), (uint32_t)((a.tokens + 255) / 256), mt,
-               nt))
-    return;
-  const int32_t f0 = mt * 256, t0 = nt * 256;
+  if (!tile_of(block, tiles_of<G::kRows>(a.inner), tiles_of<G::kCols>(a.tokens), mt, nt)) return;
+  const int32_t f0 = mt * G::kRows, t0 = nt * G::kCols;
   f32x4 acc[G::MI][G::NJ];
-  G::run(by_cols(a.w_down, f0, a.hidden), by_rows(a.dy, t0, a.tokens, 256), a.hidden, lds, acc);
+  G::run(by_cols(a.w_down, f0, a.hidden), by_rows(a.dy, t0, a.tokens, G::kCols), a.hidden, lds,
+         acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   u32x2 av[2][G::MI], bv[2][G::MI];
   auto fetch = [&](int j) {  // what lies past the operands is not stored
-    const int32_t t = t0 + (wave % 4) * 64 + j * 16 + (lane & 15);
+    const int32_t t = t0 + G::col(wave, j) + (lane & 15);
     const int64_t row = (int64_t)(t < a.tokens ? t : a.tokens - 1) * a.ld;
 #pragma unroll
     for (int i = 0; i < G::MI; ++i) {
-      const int32_t f = f0 + wave / 4 * 128 + 16 * i + 4 * (lane >> 4);
+      const int32_t f = f0 + G::row(wave, i) + 4 * (lane >> 4);
       const int64_t at = row + (f < a.inner_pad ? f : 0);
       av[j & 1][i] = *(const u32x2*)(a.act + at);
       bv[j & 1][i] = *(const u32x2*)(a.slope + at);
@@ -283,7 +286,6 @@ __device__ __forceinline__ void dh_tile(uint32_t block, const DhArgs& a, const G
     if (j + 1 < G::NJ) fetch(j + 1);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    lds_char* p = G::column(lds, j);
 #pragma unroll
     for (int i = 0; i < G::MI; ++i) {
       f32x4 x, y;
@@ -292,7 +294,7 @@ __device__ __forceinline__ void dh_tile(uint32_t block, const DhArgs& a, const G
         x[e] = acc[i][j][e] * widen<T>((bv[j & 1][i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
         y[e] = acc[i][j][e] * widen<T>((av[j & 1][i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
       }
-      G::put(p, i, j, narrow4<T>(x[0], x[1], x[2], x[3]));
+      G::put(lds, i, j, narrow4<T>(x[0], x[1], x[2], x[3]));
       u32x2 v = narrow4<T>(y[0], y[1], y[2], y[3]);
       // narrowed here, into a sum's registers, and not where it leaves
       asm volatile("" : "+v"(v));
@@ -310,12 +312,10 @@ __device__ __forceinline__ void dh_tile(uint32_t block, const DhArgs& a, const G
   leave(a.dg);
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < G::NJ; ++j) {
-    lds_char* p = G::column(lds, j);
+  for (int j = 0; j < G::NJ; ++j)
 #pragma unroll
     for (int i = 0; i < G::MI; ++i)
-      G::put(p, i, j, u32x2{__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1])});
-  }
+      G::put(lds, i, j, u32x2{__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1])});
   leave(a.du);
 }
 
@@ -329,12 +329,13 @@ struct WeightGrad {
   int64_t ld;
 };
 
-template <typename T, bool F32OUT>
-__device__ __forceinline__ void dw_tile(uint32_t block, const WeightGrad& w, const GemmLds& lds) {
-  using G = Gemm<T, true, true>;
+template <typename T, bool F32OUT, bool SMALL>
+__device__ __forceinline__ void dw_tile(uint32_t block, const WeightGrad& w) {
+  using G = typename TileOf<SMALL, T, true, true>::G;
+  const auto lds = G::shared();
   int32_t mt, nt;
-  if (!tile_of(block, (uint32_t)((w.n + 255) / 256), (uint32_t)((w.m + 255) / 256), nt, mt)) return;
-  const int32_t m0 = mt * 256, n0 = nt * 256, accumulate = w.accumulate;
+  if (!tile_of(block, tiles_of<G::kCols>(w.n), tiles_of<G::kRows>(w.m), nt, mt)) return;
+  const int32_t m0 = mt * G::kRows, n0 = nt * G::kCols, accumulate = w.accumulate;
   f32x4 acc[G::MI][G::NJ];
   G::run(by_cols(w.a, m0, w.tokens), by_cols(w.b, n0, w.tokens), w.tokens, lds, acc);
   if (!F32OUT && !accumulate) {
@@ -348,12 +349,12 @@ __device__ __forceinline__ void dw_tile(uint32_t block, const WeightGrad& w, con
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int j = 0; j < G::NJ; ++j) {
-    const int32_t n = n0 + wave % 4 * 64 + j * 16 + (lane & 15);
+    const int32_t n = n0 + G::col(wave, j) + (lane & 15);
     if (n >= w.n) continue;
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int i = 0; i < G::MI; ++i) {
-      const int32_t m = m0 + wave / 4 * 128 + 16 * i + 4 * (lane >> 4);
+      const int32_t m = m0 + G::row(wave, i) + 4 * (lane >> 4);
       const int64_t at = (int64_t)n * w.ld + m;
       f32x4 d = acc[i][j];
       if constexpr (F32OUT) {
@@ -384,23 +385,21 @@ __device__ __forceinline__ void dw_tile(uint32_t block, const WeightGrad& w, con
 
 // Workgroups from w.first on take dWd, those before dh: whichever has the longer
 // contraction comes first.
-template <typename T, bool F32OUT>
-__global__ __launch_bounds__(kGemmThreads) void k_ffn_back1(DhArgs d, uint32_t dh_first,
-                                                            WeightGrad w) {
-  ZK_GEMM_LDS;
+template <typename T, bool F32OUT, bool SMALL>
+__global__ __launch_bounds__(SMALL ? 256 : 512) void k_ffn_back1(DhArgs d, uint32_t dh_first,
+                                                                 WeightGrad w) {
   const bool weight = w.first > dh_first ? blockIdx.x >= w.first : blockIdx.x < dh_first;
-  if (weight) dw_tile<T, F32OUT>(blockIdx.x - w.first, w, lds);
-  else dh_tile<T>(blockIdx.x - dh_first, d, lds);
+  if (weight) dw_tile<T, F32OUT, SMALL>(blockIdx.x - w.first, w);
+  else dh_tile<T, SMALL>(blockIdx.x - dh_first, d);
 }
 
 // dx first, then dWg and dWu.
-template <typename T, bool F32OUT>
-__global__ __launch_bounds__(kGemmThreads) void k_ffn_back2(OutArgs o, WeightGrad g,
-                                                            WeightGrad u) {
-  ZK_GEMM_LDS;
-  if (blockIdx.x < g.first) return out_tile<T, true>(blockIdx.x, o, lds);
+template <typename T, bool F32OUT, bool SMALL>
+__global__ __launch_bounds__(SMALL ? 256 : 512) void k_ffn_back2(OutArgs o, WeightGrad g,
+                                                                 WeightGrad u) {
+  if (blockIdx.x < g.first) return out_tile<T, true, SMALL>(blockIdx.x, o);
   const WeightGrad w = blockIdx.x < u.first ? g : u;
-  dw_tile<T, F32OUT>(blockIdx.x - w.first, w, lds);
+  dw_tile<T, F32OUT, SMALL>(blockIdx.x - w.first, w);
 }
 
 // --- launches ----------------------------------------------------------------------
@@ -427,8 +426,8 @@ OutArgs out_args(const zero_ffn_t* f, const FfnPlan& p, void* ws, Matrix a1, Mat
   return OutArgs{a1, a2, b1, b2, (int32_t)f->tokens, (int32_t)f->hidden, (int32_t)f->inner, split,
                  tt * 256, (int32_t)(ht * 256), at<float>(ws, p.acc), (uint16_t*)out, ldo};
 }
-uint32_t out_blocks(const OutArgs& o) {
-  return tile_grid((o.tokens + 255) / 256, (int64_t)((o.hidden + 255) / 256) * o.split);
+uint32_t grid_of(int64_t rows, int64_t cols, int64_t tile, int64_t times = 1) {
+  return tile_grid((rows + tile - 1) / tile, (cols + tile - 1) / tile * times);
 }
 
 template <typename T>
@@ -446,12 +445,12 @@ int join_t(const OutArgs& o, hipStream_t stream) {
   return (int)hipSuccess;
 }
 
-template <typename T, bool SAVE>
+template <typename T, bool SAVE, bool SMALL>
 auto in_kernel(int32_t act) {
-  return act == ZERO_ACT_SILU        ? k_ffn_in<T, ZERO_ACT_SILU, SAVE>
-         : act == ZERO_ACT_GELU      ? k_ffn_in<T, ZERO_ACT_GELU, SAVE>
-         : act == ZERO_ACT_GELU_TANH ? k_ffn_in<T, ZERO_ACT_GELU_TANH, SAVE>
-                                     : k_ffn_in<T, ZERO_ACT_RELU, SAVE>;
+  return act == ZERO_ACT_SILU        ? k_ffn_in<T, ZERO_ACT_SILU, SAVE, SMALL>
+         : act == ZERO_ACT_GELU      ? k_ffn_in<T, ZERO_ACT_GELU, SAVE, SMALL>
+         : act == ZERO_ACT_GELU_TANH ? k_ffn_in<T, ZERO_ACT_GELU_TANH, SAVE, SMALL>
+                                     : k_ffn_in<T, ZERO_ACT_RELU, SAVE, SMALL>;
 }
 
 template <typename T>
@@ -465,13 +464,21 @@ int forward_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, void* y, int64_t 
   if (!e) e = view(f->w_down, f->ld_down, H, F, p.pack_down, ws, p.w_down, stream, wd);
   if (e) return e;
   const Kept to = kept(p, ws, saved);
-  hipLaunchKernelGGL((saved ? in_kernel<T, true>(f->act) : in_kernel<T, false>(f->act)),
-                     dim3(tile_grid((F + 127) / 128, (T_ + 255) / 256)), dim3(kGemmThreads), 0,
-                     stream, x, wg, wu, (int32_t)T_, (int32_t)F, (int32_t)p.inner_pad, to);
+  const auto in = p.small_in ? (saved ? in_kernel<T, true, true>(f->act)
+                                      : in_kernel<T, false, true>(f->act))
+                             : (saved ? in_kernel<T, true, false>(f->act)
+                                      : in_kernel<T, false, false>(f->act));
+  hipLaunchKernelGGL(in, dim3(grid_of(2 * F, T_, p.small_in ? 128 : 256)),
+                     dim3(p.small_in ? 256 : 512), 0, stream, x, wg, wu, (int32_t)T_, (int32_t)F,
+                     (int32_t)p.inner_pad, to);
   ZK_LAUNCHED();
   const Matrix h{to.h, (int32_t)to.ld, (int32_t)p.inner_pad};
   const OutArgs o = out_args(f, p, ws, wd, wd, h, h, p.split_y, y, ldy);
-  hipLaunchKernelGGL((k_ffn_out<T>), dim3(out_blocks(o)), dim3(kGemmThreads), 0, stream, o);
+  const uint32_t blocks = grid_of(T_, H, p.small_out ? 128 : 256, o.split);
+  if (p.small_out)
+    hipLaunchKernelGGL((k_ffn_out<T, true>), dim3(blocks), dim3(256), 0, stream, o);
+  else
+    hipLaunchKernelGGL((k_ffn_out<T, false>), dim3(blocks), dim3(512), 0, stream, o);
   ZK_LAUNCHED();
   return join_t<T>(o, stream);
 }
@@ -490,7 +497,7 @@ int backward_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, const zero_ffn_s
   const int32_t Fp = (int32_t)p.inner_pad;
   const Matrix h{(const uint16_t*)saved->h, (int32_t)saved->ld, Fp};
   const Matrix dg{at<uint16_t>(ws, p.dg), Fp, Fp}, du{at<uint16_t>(ws, p.du), Fp, Fp};
-  const uint32_t dw_blocks = tile_grid((F + 255) / 256, (H + 255) / 256);
+  const int64_t tile1 = p.small_back1 ? 128 : 256, tile2 = p.small_back2 ? 128 : 256;
   // tokens 0: nothing but weights' gradients to clear
   const bool weights = T_ > 0 || !g->accumulate;
   WeightGrad down{h, dy, (int32_t)F, (int32_t)H, (int32_t)T_, g->accumulate, 0, g->dw_down,
@@ -502,23 +509,31 @@ int backward_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, const zero_ffn_s
   const DhArgs dh{wd, dy, (int32_t)T_, (int32_t)H, (int32_t)F, Fp, (const uint16_t*)saved->act,
                   (const uint16_t*)saved->slope, saved->ld, (uint16_t*)dg.p, (uint16_t*)du.p};
   const bool through = T_ > 0 && (g->dx || g->dw_gate || g->dw_up);
-  const uint32_t dh_blocks = through ? tile_grid((F + 255) / 256, (T_ + 255) / 256) : 0;
-  const uint32_t down_blocks = weights && down.out ? dw_blocks : 0;
+  const uint32_t dh_blocks = through ? grid_of(F, T_, tile1) : 0;
+  const uint32_t down_blocks = weights && down.out ? grid_of(H, F, tile1) : 0;
   if (dh_blocks + down_blocks) {
     const bool dh_first = through && H >= T_;
     down.first = dh_first ? dh_blocks : 0;
-    hipLaunchKernelGGL((k_ffn_back1<T, F32OUT>), dim3(dh_blocks + down_blocks), dim3(kGemmThreads),
-                       0, stream, dh, dh_first ? 0 : down_blocks, down);
+    if (p.small_back1)
+      hipLaunchKernelGGL((k_ffn_back1<T, F32OUT, true>), dim3(dh_blocks + down_blocks), dim3(256),
+                         0, stream, dh, dh_first ? 0 : down_blocks, down);
+    else
+      hipLaunchKernelGGL((k_ffn_back1<T, F32OUT, false>), dim3(dh_blocks + down_blocks), dim3(512),
+                         0, stream, dh, dh_first ? 0 : down_blocks, down);
     ZK_LAUNCHED();
   }
   const OutArgs o = out_args(f, p, ws, wg, wu, dg, du, p.split_dx, g->dx, g->lddx);
   const bool dx = g->dx && T_ > 0;
-  gate.first = dx ? out_blocks(o) : 0;
-  up.first = gate.first + (weights && gate.out ? dw_blocks : 0);
-  const uint32_t blocks = up.first + (weights && up.out ? dw_blocks : 0);
+  gate.first = dx ? grid_of(T_, H, tile2, o.split) : 0;
+  up.first = gate.first + (weights && gate.out ? grid_of(F, H, tile2) : 0);
+  const uint32_t blocks = up.first + (weights && up.out ? grid_of(F, H, tile2) : 0);
   if (blocks) {
-    hipLaunchKernelGGL((k_ffn_back2<T, F32OUT>), dim3(blocks), dim3(kGemmThreads), 0, stream, o,
-                       gate, up);
+    if (p.small_back2)
+      hipLaunchKernelGGL((k_ffn_back2<T, F32OUT, true>), dim3(blocks), dim3(256), 0, stream, o,
+                         gate, up);
+    else
+      hipLaunchKernelGGL((k_ffn_back2<T, F32OUT, false>), dim3(blocks), dim3(512), 0, stream, o,
+                         gate, up);
     ZK_LAUNCHED();
   }
   return dx ? join_t<T>(o, stream) : (int)hipSuccess;
