@@ -895,8 +895,7 @@ int zero_head_loss_grad(const zero_head_t* head, float* token_loss, float* lse,
  *   dh = dy Wd,  du = dh act(g),  dg = dh u act'(g)
  *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h
  * Sums are fp32.  h, dg and du are rounded once to the 16-bit type (the matrix cores
- * multiply it), and so are act(g) and u act'(g), which are kept for the gradients; in
- * fp16 what passes 65504 becomes infinite.  Gradients carry whatever loss scale dy carries.  Equal
+ * multiply it); in fp16 what passes 65504 becomes infinite.  Gradients carry whatever loss scale dy carries.  Equal
  * inputs give equal bits. */
 
 enum zero_act {
@@ -925,12 +924,16 @@ typedef struct zero_ffn {
   int32_t act;                    /* zero_act */
 } zero_ffn_t;
 
-/* What the gradients need of the forward pass, in 16 bits: formed there from the fp32
- * sums, so that the backward pass has two products an element left to do. */
+/* What the gradients need of the forward pass: formed there from the fp32 sums, so that
+ * the backward pass has two products an element left to do.  act(g) and b = u act'(g)
+ * are kept in 24 bits, as fp32 patterns rounded to 15 fraction bits: the upper 16
+ * bits apart, the lower 8 together.  Buffers of T rows of F elements of 16 bits, F
+ * rounded up to 8. */
 typedef struct zero_ffn_saved {
-  void* act;    /* act(g): device [T, F rounded up to 8], 16-byte aligned */
-  void* slope;  /* u act'(g): the same */
-  void* h;      /* the same */
+  void* act;    /* device, 16-byte aligned: upper half of act(g) */
+  void* slope;  /* the same: upper half of b */
+  void* low;    /* the same: the next 8 bits of act(g), and above them b's */
+  void* h;      /* the same: h */
   int64_t ld;   /* elements between rows, a multiple of 8, >= F rounded up to 8 */
 } zero_ffn_saved_t;
 

@@ -13,7 +13,7 @@ a          all slopes are at most 1.2: 1.2 times g's error, and the evaluation: 
 slope      second derivatives are at most 1: g's error, and es = e (1 + |g|) (16 + 8 (|g| + g^2 +
            |g|^3)) (1 + |slope|); relu: wrong by 1 where g is within its error of 0
 h          errors of a and u through the product, one fp32 operation, one rounding
-kept       a and b = u slope with their errors, one rounding each
+kept       a and b = u slope with their errors, rounded to 16 bits of significand (2^-16)
 y          h's error through |Wd|, F e (|h| |Wd|^T), one rounding
 dh         H e (|dy| |Wd|), not rounded
 du, dg     products of dh with the kept a and b, one operation, one rounding
@@ -74,7 +74,7 @@ def reference(x, wg, wu, wd, name, dy=None):
         es = (r <= bg).double()
     b = v * slope
     db = bv * slope.abs() + v.abs() * es + E * b.abs()
-    sa, sb = da + u * (a.abs() + da) + tiny, db + u * (b.abs() + db) + tiny
+    sa, sb = da + 2.0 ** -16 * (a.abs() + da) + 1e-38, db + 2.0 ** -16 * (b.abs() + db) + 1e-38
     Y = dy.double()
     dh = Y @ D
     bdh = H * E * (Y.abs() @ D.abs())

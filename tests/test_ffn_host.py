@@ -5,7 +5,7 @@ import pytest
 from zero_sharded_optimizer_rank_amd import abi
 
 X, WG, WU, WD, Y, DY, DX = (0x1000000 * i for i in range(1, 8))  # never dereferenced
-DG, DU, DD, ACT, SLOPE, MID, WS = (0x1000000 * i for i in range(8, 15))
+DG, DU, DD, ACT, SLOPE, LOW, MID, WS = (0x1000000 * i for i in range(8, 16))
 T, H, F = 100, 64, 96
 
 
@@ -17,7 +17,7 @@ def _ffn(**kw):
 
 
 def _saved(**kw):
-    s = dict(act=ACT, slope=SLOPE, h=MID, ld=F)
+    s = dict(act=ACT, slope=SLOPE, low=LOW, h=MID, ld=F)
     s.update(kw)
     return abi.zero_ffn_saved_t(**s)
 
@@ -74,6 +74,8 @@ def _backward(f=None, saved=None, g=None, ws=WS, n=BIG):
     (lambda: _forward(_ffn(inner=F - 3), saved=_saved(ld=F - 3)), abi.ZERO_EINVAL),
     (lambda: _forward(saved=_saved(act=None)), abi.ZERO_EINVAL),
     (lambda: _forward(saved=_saved(slope=SLOPE + 8)), abi.ZERO_EALIGN),
+    (lambda: _forward(saved=_saved(low=None)), abi.ZERO_EINVAL),
+    (lambda: _forward(saved=_saved(low=LOW + 8)), abi.ZERO_EALIGN),
     (lambda: _forward(saved=_saved(h=ACT + 16)), abi.ZERO_EINVAL),
     (lambda: _forward(saved=_saved(h=WG)), abi.ZERO_EINVAL),
     (lambda: _backward(_ffn(x=None)), abi.ZERO_EINVAL),
@@ -88,7 +90,7 @@ def _backward(f=None, saved=None, g=None, ws=WS, n=BIG):
     (lambda: _backward(g=_grads(dw_dtype=abi.ZERO_F32, dw_up=DU + 2)), abi.ZERO_EALIGN),
     (lambda: _backward(g=_grads(dw_up=DG + 2)), abi.ZERO_EINVAL),
     (lambda: _backward(g=_grads(dx=DY)), abi.ZERO_EINVAL),
-    (lambda: _backward(g=_grads(dw_down=SLOPE)), abi.ZERO_EINVAL),
+    (lambda: _backward(g=_grads(dw_down=LOW)), abi.ZERO_EINVAL),
     (lambda: _backward(g=_grads(dx=WS + 64)), abi.ZERO_EINVAL),
     (lambda: _backward(ws=None), abi.ZERO_EINVAL),
     (lambda: _backward(n=16), abi.ZERO_ENOSPC),

@@ -87,7 +87,9 @@ def _run(T, H, F, dt, act, seed=0, tokens=None, views=None, dw_type=None, extra=
 SHAPES = [(1, 1, 1), (1, 8, 8), (2, 7, 3), (5, 16, 40), (16, 64, 64), (17, 72, 200),
           (33, 131, 77), (48, 264, 264), (63, 136, 1000), (64, 512, 130), (65, 64, 64),
           (100, 131, 77), (130, 8, 500), (255, 256, 256), (256, 256, 256), (257, 264, 520),
-          (300, 1000, 136), (513, 72, 129), (70, 300, 5000), (1, 1600, 640), (64, 1601, 70)]
+          (300, 1000, 136), (513, 72, 129), (70, 300, 5000), (1, 1600, 640), (64, 1601, 70),
+          # few tiles of long contractions: every product in parts
+          (200, 4000, 40), (2000, 24, 40), (5000, 8, 8), (130, 2051, 9), (1030, 515, 260)]
 
 
 @pytest.mark.parametrize("dt", TYPES, ids=["bf16", "f16"])

@@ -136,8 +136,8 @@ class zero_ffn_t(ctypes.Structure):
 
 
 class zero_ffn_saved_t(ctypes.Structure):
-    _fields_ = [("act", ctypes.c_void_p), ("slope", ctypes.c_void_p), ("h", ctypes.c_void_p),
-                ("ld", ctypes.c_int64)]
+    _fields_ = [("act", ctypes.c_void_p), ("slope", ctypes.c_void_p), ("low", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("ld", ctypes.c_int64)]
 
 
 class zero_ffn_grads_t(ctypes.Structure):

@@ -21,7 +21,8 @@ struct FfnPlan {
   bool few;
   bool pack_x, pack_gate, pack_up, pack_down, pack_dy;  // rows that no 16-byte loads fit
   bool small_in, small_out, small_back1, small_back2;  // 128 x 128 tiles, else 256 x 256
-  int32_t split_y, split_dx;      // ways the contractions over the inner axis are split
+  // parts that a product's contraction is cut into; small tiles: any, large: y and dx
+  int32_t split_in, split_y, split_dh, split_dw1, split_dx, split_dw2;
   int32_t few_sets_in, few_sets_out;  // few: sets of rows of a workgroup, 2 or 4; 1: x is
                                       // not shared
   // offsets

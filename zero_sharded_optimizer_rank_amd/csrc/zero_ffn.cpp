@@ -47,11 +47,11 @@ int check_ffn(const zero_ffn_t* f) {
 
 int check_saved(const zero_ffn_t* f, const zero_ffn_saved_t* s) {
   if (s->ld < up(f->inner, 8) || s->ld % 8 || s->ld > ZERO_FFN_MAX_WIDTH)
-    return fail(ZERO_EINVAL, "rows of act, slope and h %lld apart", (long long)s->ld);
-  if (f->tokens > 0 && (!s->act || !s->slope || !s->h))
-    return fail(ZERO_EINVAL, "act, slope or h is NULL");
-  if (!aligned(s->act, 16) || !aligned(s->slope, 16) || !aligned(s->h, 16))
-    return fail(ZERO_EALIGN, "act, slope and h must be 16-byte aligned");
+    return fail(ZERO_EINVAL, "rows of act, slope, low and h %lld apart", (long long)s->ld);
+  if (f->tokens > 0 && (!s->act || !s->slope || !s->low || !s->h))
+    return fail(ZERO_EINVAL, "act, slope, low or h is NULL");
+  if (!aligned(s->act, 16) || !aligned(s->slope, 16) || !aligned(s->low, 16) || !aligned(s->h, 16))
+    return fail(ZERO_EALIGN, "act, slope, low and h must be 16-byte aligned");
   return ZERO_OK;
 }
 
@@ -112,16 +112,28 @@ int32_t split_of(const Work& w, bool small) {
   if (s > w.stages / 4) s = w.stages / 4;
   return (int32_t)(s < 1 ? 1 : s);
 }
-// Ways where other tiles share the launch and fill up behind: a part is about as
+// Parts of dx where other tiles share the launch and fill up behind: a part is about as
 // long as what a CU gets of the whole (1024 x 1600 x 6400, 200 stages of 44 a CU, in 3 /
 // 4 / 5 / 9 parts 279 / 259 / 266 / 280 us a training pass; 512 x 4096 x 14336, 448 of 112,
 // in 3 / 4 / 5 / 6 593 / 562 / 568 / 591).
-int32_t split_beside(const Work& w, int64_t other_stages, bool small) {
+int32_t split_beside(const Work& w, int64_t other_stages) {
   const int64_t all = w.count * w.stages + other_stages;
-  int64_t s = w.stages * places(small) / (all > 0 ? all : 1);
-  const int32_t most = split_of(w, small);
-  if (s > most) s = most;
-  return (int32_t)(s < 1 ? 1 : s);
+  const int64_t s = w.stages * places(false) / (all > 0 ? all : 1);
+  const int32_t most = split_of(w, false);
+  return (int32_t)(s > most ? most : s < 1 ? 1 : s);
+}
+// Parts of the products of one launch of small tiles: about as long as what one of
+// three quarters of the places gets of the whole, and at least four stages.
+int64_t part_length(int64_t all_stages) {
+  const int64_t each = tiles(all_stages, places(true) * 3 / 4);
+  return each > 4 ? each : 4;
+}
+int32_t parts_of(const Work& w, int64_t length) {
+  const int64_t s = w.stages / length;
+  return (int32_t)(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+int64_t sums_bytes(int64_t rows, int64_t cols, int64_t parts) {
+  return parts > 1 ? 4 * parts * up(rows, 256) * up(cols, 256) : 0;
 }
 
 }  // namespace
@@ -143,17 +155,37 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
   }
   // Small tiles where the large ones would leave half of the CUs idle (100 x 4096 x 14336,
   // 112 tiles, forward 130 -> 107 us; 1024 x 1600 x 6400, 200 tiles, 88 -> 100), in a
-  // backward pass where a CU's share is short, so that a tile's start and end weigh
+  // backward pass also where a CU's share is short, so that a tile's start and end weigh
   // (300 x 1600 x 6400, training 194 -> 165 us; 512 x 4096 x 14336 563 -> 654), and for y of
   // up to one small tile's tokens.
-  const Work in = work(2 * F, T, H, false), dh = work(F, T, H, false), dw = work(F, H, T, false);
-  const Work dx = work(T, H, 2 * F, false);
+  const auto all = [](const Work& w) { return w.count * w.stages; };
+  Work in = work(2 * F, T, H, false), dh = work(F, T, H, false), dw = work(F, H, T, false);
+  Work dx = work(T, H, 2 * F, false);
   p.small_in = in.count < 128;
   p.small_out = T <= 128;
-  p.small_back1 = dh.count * dh.stages + dw.count * dw.stages < 24 * 256;
-  p.small_back2 = dx.count * dx.stages + 2 * dw.count * dw.stages < 24 * 256;
-  p.split_y = p.split_dx = 1;
-  if (!p.few && !g) p.split_y = split_of(work(T, H, F, p.small_out), p.small_out);
+  p.small_back1 = dh.count + dw.count < 128 || all(dh) + all(dw) < 24 * 256;
+  p.small_back2 = dx.count + 2 * dw.count < 128 || all(dx) + 2 * all(dw) < 24 * 256;
+  p.split_in = p.split_y = p.split_dh = p.split_dw1 = p.split_dx = p.split_dw2 = 1;
+  if (!p.few && !g) {
+    p.split_y = split_of(work(T, H, F, p.small_out), p.small_out);
+    in = work(2 * F, T, H, true);
+    if (p.small_in) p.split_in = parts_of(in, part_length(all(in)));
+  }
+  // (what a call does not want is counted all the same: the plan does not depend on it)
+  if (g && p.small_back1) {
+    const Work d = work(F, T, H, true), w = work(F, H, T, true);
+    const int64_t length = part_length(all(d) + all(w));
+    p.split_dh = parts_of(d, length);
+    p.split_dw1 = parts_of(w, length);
+  }
+  if (g && p.small_back2) {
+    const Work d = work(T, H, 2 * F, true), w = work(F, H, T, true);
+    const int64_t length = part_length(all(d) + 2 * all(w));
+    p.split_dx = parts_of(d, length);
+    p.split_dw2 = parts_of(w, length);
+  } else if (g) {
+    p.split_dx = split_beside(dx, 2 * all(dw));
+  }
   if (p.few) {
     p.few_sets_in = T <= 8 ? 1 : tiles(F, 64) >= kFewGroups ? 4 : 2;
     p.few_sets_out = T <= 8 ? 1 : H >= 2048 ? 4 : 2;
@@ -164,12 +196,6 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
       if (s > most) s = most;
       p.split_y = (int32_t)(s < 1 ? 1 : s);
     }
-  }
-  if (g) {
-    const Work w = work(F, H, T, p.small_back2);
-    const int64_t each = w.count * w.stages;
-    p.split_dx = split_beside(work(T, H, 2 * F, p.small_back2),
-                              (g->dw_gate ? each : 0) + (g->dw_up ? each : 0), p.small_back2);
   }
   size_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -187,9 +213,19 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
     p.dg = take(2 * T * p.inner_pad);
     p.du = take(2 * T * p.inner_pad);
   }
-  const int32_t split = g ? p.split_dx : p.split_y;
-  const int64_t row = p.few ? 1 : kFfnTile, col = p.few ? 8 : kFfnTile;
-  p.acc = take(split > 1 ? 4 * split * up(T, row) * up(H, col) : 0);
+  // the launches' sums, one launch's after the other's
+  int64_t sums;
+  if (p.few) {
+    sums = p.split_y > 1 ? 4 * p.split_y * T * p.hidden_pad : 0;
+  } else if (!g) {
+    const int64_t one = 2 * sums_bytes(F, T, p.split_in), two = sums_bytes(H, T, p.split_y);
+    sums = one > two ? one : two;
+  } else {
+    const int64_t one = sums_bytes(F, T, p.split_dh) + sums_bytes(F, H, p.split_dw1);
+    const int64_t two = sums_bytes(H, T, p.split_dx) + 2 * sums_bytes(F, H, p.split_dw2);
+    sums = one > two ? one : two;
+  }
+  p.acc = take(sums);
   p.total = at > 0 ? at : 256;
   return p;
 }
@@ -200,18 +236,13 @@ extern "C" {
 
 size_t zero_ffn_workspace_bytes(const zero_ffn_t* ffn, const zero_ffn_grads_t* grads) {
   if (!ffn || !good_sizes(ffn) || (grads && !good_ld(grads->lddy, ffn->hidden))) return 0;
-  // a batch of fewer tokens, or a call for fewer gradients, may be split more ways: at
-  // most split_of's; the plan changes by the stage of 64
+  // a batch of fewer tokens may be cut into more parts; the plan changes by the stage
+  // of 64
   zero_ffn_t f = *ffn;
-  zero_ffn_grads_t only;
-  if (grads) {
-    only = *grads;
-    only.dw_gate = only.dw_up = nullptr;
-  }
   size_t need = 0;
   const auto count = [&](int64_t tokens) {
     f.tokens = tokens < ffn->tokens ? tokens : ffn->tokens;
-    const size_t n = zk::ffn_plan(&f, grads ? &only : nullptr).total;
+    const size_t n = zk::ffn_plan(&f, grads).total;
     if (n > need) need = n;
   };
   for (int64_t t = 1; t <= zk::kFfnFew; ++t) count(t);
@@ -234,15 +265,16 @@ int zero_ffn_forward(const zero_ffn_t* ffn, void* y, int64_t ldy, const zero_ffn
   rc = check_workspace(p.total, workspace, ws_bytes);
   if (rc) return rc;
   const int64_t Fp = p.inner_pad;
-  const zero_ffn_saved_t none = {nullptr, nullptr, nullptr, 0}, *s = saved ? saved : &none;
-  const Range out[5] = {matrix(y, T, ldy, H, 2, "y"), matrix(s->act, T, s->ld, Fp, 2, "act"),
+  const zero_ffn_saved_t none = {nullptr, nullptr, nullptr, nullptr, 0}, *s = saved ? saved : &none;
+  const Range out[6] = {matrix(y, T, ldy, H, 2, "y"), matrix(s->act, T, s->ld, Fp, 2, "act"),
                         matrix(s->slope, T, s->ld, Fp, 2, "slope"),
+                        matrix(s->low, T, s->ld, Fp, 2, "low"),
                         matrix(s->h, T, s->ld, Fp, 2, "h"), {workspace, p.total, "workspace"}};
   const Range in[4] = {matrix(ffn->x, T, ffn->ldx, H, 2, "x"),
                        matrix(ffn->w_gate, F, ffn->ld_gate, H, 2, "w_gate"),
                        matrix(ffn->w_up, F, ffn->ld_up, H, 2, "w_up"),
                        matrix(ffn->w_down, H, ffn->ld_down, F, 2, "w_down")};
-  rc = check_apart(out, 5, in, 4);
+  rc = check_apart(out, 6, in, 4);
   if (rc || T == 0) return rc;
   const int e = p.few ? zk::launch_ffn_few(ffn, p, workspace, y, ldy, saved, stream)
                       : zk::launch_ffn_forward(ffn, p, workspace, y, ldy, saved, stream);
@@ -281,15 +313,16 @@ int zero_ffn_backward(const zero_ffn_t* ffn, const zero_ffn_saved_t* saved,
                         matrix(g->dw_up, F, g->lddw_up, H, ew, "dw_up"),
                         matrix(g->dw_down, H, g->lddw_down, F, ew, "dw_down"),
                         {workspace, p.total, "workspace"}};
-  const Range in[8] = {matrix(ffn->x, T, ffn->ldx, H, 2, "x"),
+  const Range in[9] = {matrix(ffn->x, T, ffn->ldx, H, 2, "x"),
                        matrix(ffn->w_gate, F, ffn->ld_gate, H, 2, "w_gate"),
                        matrix(ffn->w_up, F, ffn->ld_up, H, 2, "w_up"),
                        matrix(ffn->w_down, H, ffn->ld_down, F, 2, "w_down"),
                        matrix(g->dy, T, g->lddy, H, 2, "dy"),
                        matrix(saved->act, T, saved->ld, Fp, 2, "act"),
                        matrix(saved->slope, T, saved->ld, Fp, 2, "slope"),
+                       matrix(saved->low, T, saved->ld, Fp, 2, "low"),
                        matrix(saved->h, T, saved->ld, Fp, 2, "h")};
-  rc = check_apart(out, 5, in, 8);
+  rc = check_apart(out, 5, in, 9);
   if (rc) return rc;
   return hip_status(zk::launch_ffn_backward(ffn, p, workspace, saved, g, stream),
                     "ffn_backward launch");

@@ -67,6 +67,75 @@ __device__ __forceinline__ void store_row(uint16_t* row, int32_t c, int32_t n, u
 template <int N>
 __device__ __forceinline__ uint32_t tiles_of(int32_t x) { return (uint32_t)((x + N - 1) / N); }
 
+// --- contractions in parts -------------------------------------------------------
+// Where a product leaves few tiles its contraction is cut into parts, whose fp32 sums
+// are joined by a launch of their own: part i of a tile's element (row, col) lies at
+// acc[(i * rows + col) * ld + row].
+struct Parts {
+  int32_t count;
+  int32_t ld;
+  int64_t rows;
+  float* acc;
+};
+
+// A source from contraction index k0 to `end`: nothing is loaded past it.
+template <typename S>
+struct Ranged {
+  S src;
+  int32_t k0, end;
+  __device__ __forceinline__ int32_t in(int32_t k) const {
+    k += k0;
+    return k < end ? k : 0x40000000;  // past every operand
+  }
+  __device__ __forceinline__ const Operand& a0(int32_t& k) const {
+    k = in(k);
+    return src.a0(k);
+  }
+  __device__ __forceinline__ const Operand& a1(int32_t& k) const {
+    k = in(k);
+    return src.a1(k);
+  }
+  __device__ __forceinline__ const Operand& b(int32_t& k) const {
+    k = in(k);
+    return src.b(k);
+  }
+};
+
+// acc = part `part` of the source's `stages` stages.
+template <typename G, typename S>
+__device__ __forceinline__ void run_part(const S& src, int32_t stages, int32_t part,
+                                         int32_t parts, const typename G::Lds& lds,
+                                         f32x4 (&acc)[G::MI][G::NJ]) {
+  const int32_t s0 = (int32_t)((int64_t)stages * part / parts);
+  const int32_t s1 = (int32_t)((int64_t)stages * (part + 1) / parts);
+  G::run(Ranged<S>{src, s0 * kStage, s1 * kStage}, (s1 - s0) * kStage, lds, acc);
+}
+
+// Blocks [i0, i1) of the tile's rows as a part's sums; r0, c0: the tile's place.
+template <typename G>
+__device__ __forceinline__ void leave_part(const Parts& p, int32_t part, int32_t r0, int32_t c0,
+                                           int i0, int i1, const f32x4 (&acc)[G::MI][G::NJ]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int j = 0; j < G::NJ; ++j) {
+    float* o = p.acc + ((int64_t)part * p.rows + c0 + G::col(wave, j) + (lane & 15)) * p.ld;
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < G::MI; ++i)
+      if (i >= i0 && i < i1)
+        *(f32x4*)(o + r0 + G::row(wave, i - i0) + 4 * (lane >> 4)) = acc[i][j];
+  }
+}
+// Four sums, of the row that starts at `at`.
+__device__ __forceinline__ f32x4 joined(const Parts& p, int64_t row, int32_t c) {
+  const float* q = p.acc + row * p.ld + c;
+  f32x4 s = *(const f32x4*)q;
+#pragma unroll 4
+  for (int32_t i = 1; i < p.count; ++i) s += *(const f32x4*)(q + (int64_t)i * p.rows * p.ld);
+  return s;
+}
+__device__ __forceinline__ int32_t stages_of(int32_t k) { return (k + kStage - 1) / kStage; }
+
 // --- forward -------------------------------------------------------------------
 struct PairProduct {
   Operand gate, up, B;
@@ -75,22 +144,44 @@ struct PairProduct {
   __device__ __forceinline__ const Operand& b(int32_t&) const { return B; }
 };
 
+// What both projections' sums become: h, and what the gradients need.
+template <int ACT>
+__device__ __forceinline__ void gated(f32x4 g, f32x4 u, f32x4& h, f32x4& a, f32x4& b) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float slope;
+    a[e] = activated(Act<ACT>{}, g[e], slope);
+    b[e] = u[e] * slope;
+    h[e] = a[e] * u[e];
+  }
+}
+
 // A tile has the same inner columns of both projections, so that a lane holds g and u
 // of the same element.  What the gradients need is formed here, from the fp32
 // sums, so that the backward pass has two products an element left to do.
 template <typename T, int ACT, bool SAVE, bool SMALL>
 __global__ __launch_bounds__(SMALL ? 256 : 512) void k_ffn_in(Matrix x, Matrix w_gate, Matrix w_up,
                                                               int32_t tokens, int32_t inner,
-                                                              int32_t inner_pad, Kept to) {
+                                                              int32_t inner_pad, Kept to,
+                                                              Parts parts) {
   using G = typename TileOf<SMALL, T, false, false, true>::G;
   const auto lds = G::shared();
+  const uint32_t tt = tiles_of<G::kCols>(tokens);
   int32_t mt, nt;
-  if (!tile_of(blockIdx.x, tiles_of<G::kRows>(inner), tiles_of<G::kCols>(tokens), mt, nt)) return;
-  const int32_t f0 = mt * G::kRows, t0 = nt * G::kCols;
+  if (!tile_of(blockIdx.x, tiles_of<G::kRows>(inner), tt * (uint32_t)parts.count, mt, nt)) return;
+  const int32_t f0 = mt * G::kRows, t0 = (int32_t)((uint32_t)nt % tt) * G::kCols;
   const PairProduct src{by_rows(w_gate, f0, inner, G::kRows), by_rows(w_up, f0, inner, G::kRows),
                         by_rows(x, t0, tokens, G::kCols)};
   constexpr int H = G::MI / 2;
   f32x4 acc[G::MI][G::NJ];
+  if (SMALL && parts.count > 1) {
+    const int32_t part = (int32_t)((uint32_t)nt / tt);
+    run_part<G>(src, stages_of(x.width), part, parts.count, lds, acc);
+    // both projections' sums side by side
+    leave_part<G>(parts, part, f0, t0, 0, H, acc);
+    leave_part<G>(parts, part, parts.ld / 2 + f0, t0, H, G::MI, acc);
+    return;
+  }
   G::run(src, x.width, lds, acc);
   auto leave = [&](uint16_t* out, int region) {
     G::take_half(lds, region, [&](int col, int row, u32x4 v) {
@@ -103,22 +194,15 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void k_ffn_in(Matrix x, Matrix w
 #pragma unroll
     for (int i = 0; i < H; ++i) {
       f32x4 a, b, h;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float u = acc[H + i][j][e];
-        float slope;
-        a[e] = activated(Act<ACT>{}, acc[i][j][e], slope);
-        b[e] = u * slope;
-        h[e] = a[e] * u;
-      }
+      gated<ACT>(acc[i][j], acc[H + i][j], h, a, b);
       G::put_half(lds, 0, i, j, narrow4<T>(h[0], h[1], h[2], h[3]));
       if constexpr (SAVE) {
-        G::put_half(lds, 1, i, j, narrow4<T>(a[0], a[1], a[2], a[3]));
-        u32x2 v = narrow4<T>(b[0], b[1], b[2], b[3]);
-        // narrowed here, into a sum's registers, and not where it leaves
-        asm volatile("" : "+v"(v));
-        acc[i][j][0] = __uint_as_float(v[0]);
-        acc[i][j][1] = __uint_as_float(v[1]);
+        Kept4 k = keep4(a, b);
+        G::put_half(lds, 1, i, j, k.act);
+        // formed here, into the sums' registers, and not where they leave
+        asm volatile("" : "+v"(k.slope), "+v"(k.low));
+        acc[i][j] = f32x4{__uint_as_float(k.slope[0]), __uint_as_float(k.slope[1]),
+                          __uint_as_float(k.low[0]), __uint_as_float(k.low[1])};
       }
     }
   __syncthreads();
@@ -129,30 +213,45 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void k_ffn_in(Matrix x, Matrix w
 #pragma unroll
     for (int j = 0; j < G::NJ; ++j)
 #pragma unroll
-      for (int i = 0; i < H; ++i)
-        G::put_half(lds, 0, i, j,
-                    u32x2{__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1])});
+      for (int i = 0; i < H; ++i) {
+        const f32x4 v = acc[i][j];
+        G::put_half(lds, 0, i, j, u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])});
+        G::put_half(lds, 1, i, j, u32x2{__float_as_uint(v[2]), __float_as_uint(v[3])});
+      }
     __syncthreads();
     leave(to.slope, 0);
+    leave(to.low, 1);
   }
+}
+
+// The same from the parts' sums, four columns a thread.
+template <typename T, int ACT>
+__global__ __launch_bounds__(kPackThreads) void k_ffn_in_join(Parts parts, int32_t tokens,
+                                                              int32_t inner_pad, Kept to) {
+  const int64_t q = (int64_t)blockIdx.x * kPackThreads + threadIdx.x;
+  const int64_t t = q / (inner_pad / 4);
+  const int32_t f = (int32_t)(q % (inner_pad / 4)) * 4;
+  if (t >= tokens) return;
+  f32x4 h, a, b;
+  gated<ACT>(joined(parts, t, f), joined(parts, t, parts.ld / 2 + f), h, a, b);
+  const int64_t at = t * to.ld + f;
+  *(u32x2*)(to.h + at) = narrow4<T>(h[0], h[1], h[2], h[3]);
+  if (!to.act) return;
+  const Kept4 k = keep4(a, b);
+  *(u32x2*)(to.act + at) = k.act;
+  *(u32x2*)(to.slope + at) = k.slope;
+  *(u32x2*)(to.low + at) = k.low;
 }
 
 // --- y and dx --------------------------------------------------------------------
 // out [tokens, hidden] = B1 A1^T (+ B2 A2^T): A's rows are hidden columns (y: Wd by
 // its rows; dx: Wg, Wu by their columns), B is h, dg, du by its rows.  The second
-// product follows the first in one contraction.  Where that leaves few tiles it
-// is split; the splits' fp32 sums are joined by k_ffn_join.
-template <bool TWO>
-struct Products {
+// product follows the first in one contraction.
+struct TwoProducts {
   Operand A1, A2, B1, B2;
-  int32_t k0;       // first contraction index of this workgroup's part
-  int32_t k1;       // where the second product starts (a multiple of a stage)
-  int32_t end;      // of this part: nothing is loaded past it
+  int32_t k1;  // where the second product starts (a multiple of a stage)
   __device__ __forceinline__ const Operand& pick(int32_t& k, const Operand& p,
                                                  const Operand& q) const {
-    k += k0;
-    if (k >= end) k = 0x40000000;  // past every operand
-    if constexpr (!TWO) return p;
     if (k < k1) return p;
     k -= k1;
     return q;
@@ -164,11 +263,9 @@ struct Products {
 
 struct OutArgs {
   Matrix a1, a2, b1, b2;
-  int32_t tokens, hidden, inner, split;
-  int64_t acc_rows;   // of a split's sums
-  int32_t acc_ld;
-  float* acc;         // split > 1
-  uint16_t* out;      // split = 1
+  int32_t tokens, hidden, inner;
+  Parts parts;
+  uint16_t* out;
   int64_t ldo;
 };
 
@@ -178,41 +275,25 @@ __device__ __forceinline__ void out_tile(uint32_t block, const OutArgs& o) {
   const auto lds = G::shared();
   const uint32_t ht = tiles_of<G::kRows>(o.hidden);
   int32_t mt, nt;
-  if (!tile_of(block, tiles_of<G::kCols>(o.tokens), ht * (uint32_t)o.split, mt, nt)) return;
+  if (!tile_of(block, tiles_of<G::kCols>(o.tokens), ht * (uint32_t)o.parts.count, mt, nt)) return;
   const int32_t h0 = (int32_t)((uint32_t)nt % ht) * G::kRows, t0 = mt * G::kCols;
-  const int32_t part = (int32_t)((uint32_t)nt / ht);
-  const int32_t stages = (o.inner + kStage - 1) / kStage, all = DX ? 2 * stages : stages;
-  const int32_t s0 = (int32_t)((int64_t)all * part / o.split);
-  const int32_t s1 = (int32_t)((int64_t)all * (part + 1) / o.split);
-  Products<DX> src;
-  src.A1 = DX ? by_cols(o.a1, h0, o.inner) : by_rows(o.a1, h0, o.hidden, G::kRows);
-  src.B1 = by_rows(o.b1, t0, o.tokens, G::kCols);
-  if constexpr (DX) {
-    src.A2 = by_cols(o.a2, h0, o.inner);
-    src.B2 = by_rows(o.b2, t0, o.tokens, G::kCols);
-  }
-  src.k0 = s0 * kStage;
-  src.k1 = stages * kStage;
-  src.end = s1 * kStage;
+  const int32_t part = (int32_t)((uint32_t)nt / ht), stages = stages_of(o.inner);
   f32x4 acc[G::MI][G::NJ];
-  G::run(src, (s1 - s0) * kStage, lds, acc);
-  if (o.split == 1) {
-    G::transposed(lds, acc, narrow4<T>, [&](int col, int row, u32x4 v) {
-      const int32_t t = t0 + col, c = h0 + row;
-      if (t < o.tokens && c < o.hidden) store_row(o.out + (int64_t)t * o.ldo, c, o.hidden, v);
-    });
-    return;
+  if constexpr (DX) {
+    const TwoProducts src{by_cols(o.a1, h0, o.inner), by_cols(o.a2, h0, o.inner),
+                          by_rows(o.b1, t0, o.tokens, G::kCols),
+                          by_rows(o.b2, t0, o.tokens, G::kCols), stages * kStage};
+    run_part<G>(src, 2 * stages, part, o.parts.count, lds, acc);
+  } else {
+    const OneProduct src{by_rows(o.a1, h0, o.hidden, G::kRows),
+                         by_rows(o.b1, t0, o.tokens, G::kCols)};
+    run_part<G>(src, stages, part, o.parts.count, lds, acc);
   }
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int j = 0; j < G::NJ; ++j) {
-    const int32_t t = t0 + G::col(wave, j) + (lane & 15);
-    float* p = o.acc + ((int64_t)part * o.acc_rows + t) * o.acc_ld;
-    asm volatile("" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < G::MI; ++i)
-      *(f32x4*)(p + h0 + G::row(wave, i) + 4 * (lane >> 4)) = acc[i][j];
-  }
+  if (o.parts.count > 1) return leave_part<G>(o.parts, part, h0, t0, 0, G::MI, acc);
+  G::transposed(lds, acc, narrow4<T>, [&](int col, int row, u32x4 v) {
+    const int32_t t = t0 + col, c = h0 + row;
+    if (t < o.tokens && c < o.hidden) store_row(o.out + (int64_t)t * o.ldo, c, o.hidden, v);
+  });
 }
 
 template <typename T, bool SMALL>
@@ -220,20 +301,17 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void k_ffn_out(OutArgs o) {
   out_tile<T, false, SMALL>(blockIdx.x, o);
 }
 
-// The splits' sums, four columns a thread.
+// y or dx from the parts' sums, four columns a thread.
 template <typename T>
-__global__ __launch_bounds__(kPackThreads) void k_ffn_join(const float* __restrict__ acc,
-                                                           int32_t split, int64_t acc_rows,
-                                                           int32_t acc_ld, int32_t hidden,
-                                                           uint16_t* __restrict__ out,
-                                                           int64_t ldo) {
-  const int64_t t = blockIdx.y;
-  const int32_t c = (int32_t)(blockIdx.x * kPackThreads + threadIdx.x) * 4;
-  if (c >= hidden) return;
-  const float* p = acc + t * acc_ld + c;
-  f32x4 s = *(const f32x4*)p;
-#pragma unroll 4
-  for (int32_t k = 1; k < split; ++k) s += *(const f32x4*)(p + (int64_t)k * acc_rows * acc_ld);
+__global__ __launch_bounds__(kPackThreads) void k_ffn_out_join(Parts parts, int32_t tokens,
+                                                               int32_t hidden,
+                                                               uint16_t* __restrict__ out,
+                                                               int64_t ldo) {
+  const int32_t quads = (hidden + 3) / 4;
+  const int64_t q = (int64_t)blockIdx.x * kPackThreads + threadIdx.x, t = q / quads;
+  const int32_t c = (int32_t)(q % quads) * 4;
+  if (t >= tokens) return;
+  const f32x4 s = joined(parts, t, c);
   uint16_t* o = out + t * ldo + c;
   const u32x2 v = narrow4<T>(s[0], s[1], s[2], s[3]);
   if (c + 4 <= hidden) {
@@ -249,57 +327,77 @@ __global__ __launch_bounds__(kPackThreads) void k_ffn_join(const float* __restri
 struct DhArgs {
   Matrix w_down, dy;
   int32_t tokens, hidden, inner, inner_pad;
-  const uint16_t *act, *slope;  // rows ld apart
+  const uint16_t *act, *slope, *low;  // rows ld apart
   int64_t ld;
-  uint16_t *dg, *du;            // rows inner_pad apart
+  uint16_t *dg, *du;                  // rows inner_pad apart
+  Parts parts;
 };
+
+// dh of four elements becomes dg and du.
+template <typename T>
+__device__ __forceinline__ void gradients(f32x4 dh, u32x2 act, u32x2 slope, u32x2 low, u32x2& dg,
+                                          u32x2& du) {
+  f32x4 x, y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[e] = dh[e] * kept_at<1>(slope, low, e);
+    y[e] = dh[e] * kept_at<0>(act, low, e);
+  }
+  dg = narrow4<T>(x[0], x[1], x[2], x[3]);
+  du = narrow4<T>(y[0], y[1], y[2], y[3]);
+}
 
 // A tile of dh: A = Wd by its columns (inner), B = dy by its rows; it leaves as dg =
 // dh (u act'(g)) and du = dh act(g).  Lane by lane those lie as the sums do, eight
-// bytes each; the next column's are on their way while one is multiplied.
+// bytes each; the next few blocks' are on their way while some are multiplied.
 template <typename T, bool SMALL>
 __device__ __forceinline__ void dh_tile(uint32_t block, const DhArgs& a) {
   using G = typename TileOf<SMALL, T, true, false>::G;
   const auto lds = G::shared();
+  const uint32_t tt = tiles_of<G::kCols>(a.tokens);
   int32_t mt, nt;
-  if (!tile_of(block, tiles_of<G::kRows>(a.inner), tiles_of<G::kCols>(a.tokens), mt, nt)) return;
-  const int32_t f0 = mt * G::kRows, t0 = nt * G::kCols;
+  if (!tile_of(block, tiles_of<G::kRows>(a.inner), tt * (uint32_t)a.parts.count, mt, nt)) return;
+  const int32_t f0 = mt * G::kRows, t0 = (int32_t)((uint32_t)nt % tt) * G::kCols;
+  const OneProduct src{by_cols(a.w_down, f0, a.hidden), by_rows(a.dy, t0, a.tokens, G::kCols)};
   f32x4 acc[G::MI][G::NJ];
-  G::run(by_cols(a.w_down, f0, a.hidden), by_rows(a.dy, t0, a.tokens, G::kCols), a.hidden, lds,
-         acc);
+  if (SMALL && a.parts.count > 1) {
+    const int32_t part = (int32_t)((uint32_t)nt / tt);
+    run_part<G>(src, stages_of(a.hidden), part, a.parts.count, lds, acc);
+    return leave_part<G>(a.parts, part, f0, t0, 0, G::MI, acc);
+  }
+  G::run(src, a.hidden, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  u32x2 av[2][G::MI], bv[2][G::MI];
-  auto fetch = [&](int j) {  // what lies past the operands is not stored
+  constexpr int N = 4, kSets = G::MI * G::NJ / N;  // blocks of a set
+  u32x2 av[2][N], bv[2][N], lv[2][N];
+  auto fetch = [&](int set) {  // what lies past the operands is not stored
+    const int j = set * N / G::MI;
     const int32_t t = t0 + G::col(wave, j) + (lane & 15);
     const int64_t row = (int64_t)(t < a.tokens ? t : a.tokens - 1) * a.ld;
 #pragma unroll
-    for (int i = 0; i < G::MI; ++i) {
-      const int32_t f = f0 + G::row(wave, i) + 4 * (lane >> 4);
+    for (int n = 0; n < N; ++n) {
+      const int32_t f = f0 + G::row(wave, set * N % G::MI + n) + 4 * (lane >> 4);
       const int64_t at = row + (f < a.inner_pad ? f : 0);
-      av[j & 1][i] = *(const u32x2*)(a.act + at);
-      bv[j & 1][i] = *(const u32x2*)(a.slope + at);
+      av[set & 1][n] = *(const u32x2*)(a.act + at);
+      bv[set & 1][n] = *(const u32x2*)(a.slope + at);
+      lv[set & 1][n] = *(const u32x2*)(a.low + at);
     }
   };
   fetch(0);
 #pragma unroll
-  for (int j = 0; j < G::NJ; ++j) {
-    if (j + 1 < G::NJ) fetch(j + 1);
+  for (int set = 0; set < kSets; ++set) {
+    if (set + 1 < kSets) fetch(set + 1);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < G::MI; ++i) {
-      f32x4 x, y;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = acc[i][j][e] * widen<T>((bv[j & 1][i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-        y[e] = acc[i][j][e] * widen<T>((av[j & 1][i][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-      }
-      G::put(lds, i, j, narrow4<T>(x[0], x[1], x[2], x[3]));
-      u32x2 v = narrow4<T>(y[0], y[1], y[2], y[3]);
+    for (int n = 0; n < N; ++n) {
+      const int j = set * N / G::MI, i = set * N % G::MI + n;
+      u32x2 x, y;
+      gradients<T>(acc[i][j], av[set & 1][n], bv[set & 1][n], lv[set & 1][n], x, y);
+      G::put(lds, i, j, x);
       // narrowed here, into a sum's registers, and not where it leaves
-      asm volatile("" : "+v"(v));
-      acc[i][j][0] = __uint_as_float(v[0]);
-      acc[i][j][1] = __uint_as_float(v[1]);
+      asm volatile("" : "+v"(y));
+      acc[i][j][0] = __uint_as_float(y[0]);
+      acc[i][j][1] = __uint_as_float(y[1]);
     }
   }
   auto leave = [&](uint16_t* out) {
@@ -319,6 +417,21 @@ __device__ __forceinline__ void dh_tile(uint32_t block, const DhArgs& a) {
   leave(a.du);
 }
 
+// The same from the parts' sums, four columns a thread.
+template <typename T>
+__global__ __launch_bounds__(kPackThreads) void k_ffn_dh_join(DhArgs a) {
+  const int64_t q = (int64_t)blockIdx.x * kPackThreads + threadIdx.x;
+  const int64_t t = q / (a.inner_pad / 4);
+  const int32_t f = (int32_t)(q % (a.inner_pad / 4)) * 4;
+  if (t >= a.tokens) return;
+  const int64_t at = t * a.ld + f, to = t * a.inner_pad + f;
+  u32x2 x, y;
+  gradients<T>(joined(a.parts, t, f), *(const u32x2*)(a.act + at), *(const u32x2*)(a.slope + at),
+               *(const u32x2*)(a.low + at), x, y);
+  *(u32x2*)(a.dg + to) = x;
+  *(u32x2*)(a.du + to) = y;
+}
+
 // One weight's gradient [n, m] = B^T A: row j is column j of B against the columns
 // of A, over the tokens.
 struct WeightGrad {
@@ -327,18 +440,58 @@ struct WeightGrad {
   uint32_t first;  // its first workgroup
   void* out;
   int64_t ld;
+  Parts parts;
 };
+
+// Four sums of row n from column m on, into their place.
+template <typename T, bool F32OUT>
+__device__ __forceinline__ void leave_dw(const WeightGrad& w, int32_t n, int32_t m, f32x4 d) {
+  const int64_t at = (int64_t)n * w.ld + m;
+  if constexpr (F32OUT) {
+    float* o = (float*)w.out + at;
+    if (m + 4 <= w.m) {
+      if (w.accumulate) d = *(const f32x4_a4*)o + d;
+      *(f32x4_a4*)o = d;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (m + e < w.m) o[e] = w.accumulate ? o[e] + d[e] : d[e];
+    }
+  } else {
+    uint16_t* o = (uint16_t*)w.out + at;
+    if (m + 4 <= w.m) {
+      if (w.accumulate) {
+        const u32x2 q = *(const u32x2_a2*)o;
+        d += f32x4{widen<T>(q[0] & 0xFFFFu), widen<T>(q[0] >> 16), widen<T>(q[1] & 0xFFFFu),
+                   widen<T>(q[1] >> 16)};
+      }
+      *(u32x2_a2*)o = narrow4<T>(d[0], d[1], d[2], d[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (m + e < w.m)
+          o[e] = (uint16_t)narrow<T>(w.accumulate ? widen<T>(o[e]) + d[e] : d[e]);
+    }
+  }
+}
 
 template <typename T, bool F32OUT, bool SMALL>
 __device__ __forceinline__ void dw_tile(uint32_t block, const WeightGrad& w) {
   using G = typename TileOf<SMALL, T, true, true>::G;
   const auto lds = G::shared();
+  const uint32_t rows = tiles_of<G::kRows>(w.m);
   int32_t mt, nt;
-  if (!tile_of(block, tiles_of<G::kCols>(w.n), tiles_of<G::kRows>(w.m), nt, mt)) return;
-  const int32_t m0 = mt * G::kRows, n0 = nt * G::kCols, accumulate = w.accumulate;
+  if (!tile_of(block, tiles_of<G::kCols>(w.n), rows * (uint32_t)w.parts.count, nt, mt)) return;
+  const int32_t m0 = (int32_t)((uint32_t)mt % rows) * G::kRows, n0 = nt * G::kCols;
+  const OneProduct src{by_cols(w.a, m0, w.tokens), by_cols(w.b, n0, w.tokens)};
   f32x4 acc[G::MI][G::NJ];
-  G::run(by_cols(w.a, m0, w.tokens), by_cols(w.b, n0, w.tokens), w.tokens, lds, acc);
-  if (!F32OUT && !accumulate) {
+  if (SMALL && w.parts.count > 1) {
+    const int32_t part = (int32_t)((uint32_t)mt / rows);
+    run_part<G>(src, stages_of(w.tokens), part, w.parts.count, lds, acc);
+    return leave_part<G>(w.parts, part, m0, n0, 0, G::MI, acc);
+  }
+  G::run(src, w.tokens, lds, acc);
+  if (!F32OUT && !w.accumulate) {
     uint16_t* out = (uint16_t*)w.out;
     G::transposed(lds, acc, narrow4<T>, [&](int col, int row, u32x4 v) {
       const int32_t n = n0 + col, m = m0 + row;
@@ -353,34 +506,22 @@ __device__ __forceinline__ void dw_tile(uint32_t block, const WeightGrad& w) {
     if (n >= w.n) continue;
     asm volatile("" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < G::MI; ++i) {
-      const int32_t m = m0 + G::row(wave, i) + 4 * (lane >> 4);
-      const int64_t at = (int64_t)n * w.ld + m;
-      f32x4 d = acc[i][j];
-      if constexpr (F32OUT) {
-        float* o = (float*)w.out + at;
-        if (m + 4 <= w.m) {
-          if (accumulate) d = *(const f32x4_a4*)o + d;
-          *(f32x4_a4*)o = d;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (m + e < w.m) o[e] = accumulate ? o[e] + d[e] : d[e];
-        }
-      } else {
-        uint16_t* o = (uint16_t*)w.out + at;
-        if (m + 4 <= w.m) {
-          const u32x2 q = *(const u32x2_a2*)o;
-          *(u32x2_a2*)o = narrow4<T>(widen<T>(q[0] & 0xFFFFu) + d[0], widen<T>(q[0] >> 16) + d[1],
-                                     widen<T>(q[1] & 0xFFFFu) + d[2], widen<T>(q[1] >> 16) + d[3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (m + e < w.m) o[e] = (uint16_t)narrow<T>(widen<T>(o[e]) + d[e]);
-        }
-      }
-    }
+    for (int i = 0; i < G::MI; ++i)
+      leave_dw<T, F32OUT>(w, n, m0 + G::row(wave, i) + 4 * (lane >> 4), acc[i][j]);
   }
+}
+
+// The same from the parts' sums, four columns a thread; the second weight's
+// workgroups, if it has any, start at b.first.
+template <typename T, bool F32OUT>
+__global__ __launch_bounds__(kPackThreads) void k_ffn_dw_join(WeightGrad a, WeightGrad b) {
+  const bool second = blockIdx.x >= b.first;
+  const WeightGrad w = second ? b : a;
+  const int32_t quads = (w.m + 3) / 4;
+  const int64_t q = (int64_t)(blockIdx.x - (second ? b.first : 0u)) * kPackThreads + threadIdx.x;
+  const int64_t n = q / quads;
+  const int32_t m = (int32_t)(q % quads) * 4;
+  if (n < w.n) leave_dw<T, F32OUT>(w, (int32_t)n, m, joined(w.parts, n, m));
 }
 
 // Workgroups from w.first on take dWd, those before dh: whichever has the longer
@@ -420,29 +561,29 @@ int view(const void* src, int64_t ld, int64_t rows, int64_t cols, bool pack, voi
   return (int)hipGetLastError();
 }
 
-OutArgs out_args(const zero_ffn_t* f, const FfnPlan& p, void* ws, Matrix a1, Matrix a2, Matrix b1,
-                 Matrix b2, int32_t split, void* out, int64_t ldo) {
-  const int64_t ht = (f->hidden + 255) / 256, tt = (f->tokens + 255) / 256;
-  return OutArgs{a1, a2, b1, b2, (int32_t)f->tokens, (int32_t)f->hidden, (int32_t)f->inner, split,
-                 tt * 256, (int32_t)(ht * 256), at<float>(ws, p.acc), (uint16_t*)out, ldo};
-}
 uint32_t grid_of(int64_t rows, int64_t cols, int64_t tile, int64_t times = 1) {
   return tile_grid((rows + tile - 1) / tile, (cols + tile - 1) / tile * times);
 }
+uint32_t quads_grid(int64_t rows, int64_t cols) {
+  return (uint32_t)((rows * ((cols + 3) / 4) + kPackThreads - 1) / kPackThreads);
+}
+// Sums of `parts` parts of cols rows of `rows` columns, at *next floats into acc.
+Parts parts_at(void* ws, const FfnPlan& p, int64_t rows, int64_t cols, int32_t parts,
+               int64_t* next) {
+  Parts q{parts, (int32_t)((rows + 255) / 256 * 256), (cols + 255) / 256 * 256, nullptr};
+  if (parts > 1) {
+    q.acc = at<float>(ws, p.acc) + *next;
+    *next += q.ld * q.rows * parts;
+  }
+  return q;
+}
 
 template <typename T>
-int join_t(const OutArgs& o, hipStream_t stream) {
-  if (o.split == 1) return (int)hipSuccess;
-  const int64_t cols = 4 * kPackThreads, most = 65535;
-  for (int64_t t0 = 0; t0 < o.tokens; t0 += most) {
-    const int64_t n = o.tokens - t0 < most ? o.tokens - t0 : most;
-    hipLaunchKernelGGL((k_ffn_join<T>),
-                       dim3((uint32_t)((o.hidden + cols - 1) / cols), (uint32_t)n),
-                       dim3(kPackThreads), 0, stream, o.acc + t0 * o.acc_ld, o.split, o.acc_rows,
-                       o.acc_ld, o.hidden, o.out + t0 * o.ldo, o.ldo);
-    ZK_LAUNCHED();
-  }
-  return (int)hipSuccess;
+int out_join(const OutArgs& o, hipStream_t stream) {
+  if (o.parts.count == 1) return (int)hipSuccess;
+  hipLaunchKernelGGL((k_ffn_out_join<T>), dim3(quads_grid(o.tokens, o.hidden)),
+                     dim3(kPackThreads), 0, stream, o.parts, o.tokens, o.hidden, o.out, o.ldo);
+  return (int)hipGetLastError();
 }
 
 template <typename T, bool SAVE, bool SMALL>
@@ -451,6 +592,13 @@ auto in_kernel(int32_t act) {
          : act == ZERO_ACT_GELU      ? k_ffn_in<T, ZERO_ACT_GELU, SAVE, SMALL>
          : act == ZERO_ACT_GELU_TANH ? k_ffn_in<T, ZERO_ACT_GELU_TANH, SAVE, SMALL>
                                      : k_ffn_in<T, ZERO_ACT_RELU, SAVE, SMALL>;
+}
+template <typename T>
+auto in_join_kernel(int32_t act) {
+  return act == ZERO_ACT_SILU        ? k_ffn_in_join<T, ZERO_ACT_SILU>
+         : act == ZERO_ACT_GELU      ? k_ffn_in_join<T, ZERO_ACT_GELU>
+         : act == ZERO_ACT_GELU_TANH ? k_ffn_in_join<T, ZERO_ACT_GELU_TANH>
+                                     : k_ffn_in_join<T, ZERO_ACT_RELU>;
 }
 
 template <typename T>
@@ -464,23 +612,39 @@ int forward_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, void* y, int64_t 
   if (!e) e = view(f->w_down, f->ld_down, H, F, p.pack_down, ws, p.w_down, stream, wd);
   if (e) return e;
   const Kept to = kept(p, ws, saved);
+  int64_t next = 0;
+  Parts parts = parts_at(ws, p, F, T_, p.split_in, &next);
+  if (parts.count > 1) {  // both projections
+    parts.ld *= 2;
+    next *= 2;
+  }
   const auto in = p.small_in ? (saved ? in_kernel<T, true, true>(f->act)
                                       : in_kernel<T, false, true>(f->act))
                              : (saved ? in_kernel<T, true, false>(f->act)
                                       : in_kernel<T, false, false>(f->act));
-  hipLaunchKernelGGL(in, dim3(grid_of(2 * F, T_, p.small_in ? 128 : 256)),
+  const int64_t rows = p.small_in ? 64 : 128;  // of each projection
+  hipLaunchKernelGGL(in, dim3(tile_grid((F + rows - 1) / rows,
+                                        (T_ + 2 * rows - 1) / (2 * rows) * parts.count)),
                      dim3(p.small_in ? 256 : 512), 0, stream, x, wg, wu, (int32_t)T_, (int32_t)F,
-                     (int32_t)p.inner_pad, to);
+                     (int32_t)p.inner_pad, to, parts);
   ZK_LAUNCHED();
+  if (parts.count > 1) {
+    hipLaunchKernelGGL(in_join_kernel<T>(f->act), dim3(quads_grid(T_, p.inner_pad)),
+                       dim3(kPackThreads), 0, stream, parts, (int32_t)T_, (int32_t)p.inner_pad,
+                       to);
+    ZK_LAUNCHED();
+  }
   const Matrix h{to.h, (int32_t)to.ld, (int32_t)p.inner_pad};
-  const OutArgs o = out_args(f, p, ws, wd, wd, h, h, p.split_y, y, ldy);
-  const uint32_t blocks = grid_of(T_, H, p.small_out ? 128 : 256, o.split);
+  next = 0;  // the sums before have been read by then
+  const OutArgs o{wd, wd, h, h, (int32_t)T_, (int32_t)H, (int32_t)F,
+                  parts_at(ws, p, H, T_, p.split_y, &next), (uint16_t*)y, ldy};
+  const uint32_t blocks = grid_of(T_, H, p.small_out ? 128 : 256, o.parts.count);
   if (p.small_out)
     hipLaunchKernelGGL((k_ffn_out<T, true>), dim3(blocks), dim3(256), 0, stream, o);
   else
     hipLaunchKernelGGL((k_ffn_out<T, false>), dim3(blocks), dim3(512), 0, stream, o);
   ZK_LAUNCHED();
-  return join_t<T>(o, stream);
+  return out_join<T>(o, stream);
 }
 
 template <typename T, bool F32OUT>
@@ -500,17 +664,25 @@ int backward_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, const zero_ffn_s
   const int64_t tile1 = p.small_back1 ? 128 : 256, tile2 = p.small_back2 ? 128 : 256;
   // tokens 0: nothing but weights' gradients to clear
   const bool weights = T_ > 0 || !g->accumulate;
-  WeightGrad down{h, dy, (int32_t)F, (int32_t)H, (int32_t)T_, g->accumulate, 0, g->dw_down,
-                  g->lddw_down};
-  WeightGrad gate{x, dg, (int32_t)H, (int32_t)F, (int32_t)T_, g->accumulate, 0, g->dw_gate,
-                  g->lddw_gate};
-  WeightGrad up{x, du, (int32_t)H, (int32_t)F, (int32_t)T_, g->accumulate, 0, g->dw_up,
-                g->lddw_up};
-  const DhArgs dh{wd, dy, (int32_t)T_, (int32_t)H, (int32_t)F, Fp, (const uint16_t*)saved->act,
-                  (const uint16_t*)saved->slope, saved->ld, (uint16_t*)dg.p, (uint16_t*)du.p};
+  const auto weight = [&](const Matrix& a, const Matrix& b, int64_t m, int64_t n, void* out,
+                          int64_t ld, int32_t parts, int64_t* next) {
+    return WeightGrad{a, b, (int32_t)m, (int32_t)n, (int32_t)T_, g->accumulate, 0,
+                      weights ? out : nullptr, ld,
+                      parts_at(ws, p, m, n, weights && out ? parts : 1, next)};
+  };
+  const auto dw_grid = [&](const WeightGrad& w, int64_t tile) {
+    return w.out ? grid_of(w.n, w.m, tile, w.parts.count) : 0u;
+  };
+
   const bool through = T_ > 0 && (g->dx || g->dw_gate || g->dw_up);
-  const uint32_t dh_blocks = through ? grid_of(F, T_, tile1) : 0;
-  const uint32_t down_blocks = weights && down.out ? grid_of(H, F, tile1) : 0;
+  int64_t next = 0;
+  const DhArgs dh{wd, dy, (int32_t)T_, (int32_t)H, (int32_t)F, Fp, (const uint16_t*)saved->act,
+                  (const uint16_t*)saved->slope, (const uint16_t*)saved->low, saved->ld,
+                  (uint16_t*)dg.p, (uint16_t*)du.p,
+                  parts_at(ws, p, F, T_, through ? p.split_dh : 1, &next)};
+  WeightGrad down = weight(h, dy, F, H, g->dw_down, g->lddw_down, p.split_dw1, &next);
+  const uint32_t dh_blocks = through ? grid_of(F, T_, tile1, dh.parts.count) : 0;
+  const uint32_t down_blocks = dw_grid(down, tile1);
   if (dh_blocks + down_blocks) {
     const bool dh_first = through && H >= T_;
     down.first = dh_first ? dh_blocks : 0;
@@ -522,11 +694,35 @@ int backward_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, const zero_ffn_s
                          0, stream, dh, dh_first ? 0 : down_blocks, down);
     ZK_LAUNCHED();
   }
-  const OutArgs o = out_args(f, p, ws, wg, wu, dg, du, p.split_dx, g->dx, g->lddx);
+  if (dh.parts.count > 1) {
+    hipLaunchKernelGGL((k_ffn_dh_join<T>), dim3(quads_grid(T_, Fp)), dim3(kPackThreads), 0, stream,
+                       dh);
+    ZK_LAUNCHED();
+  }
+  const auto dw_join = [&](const WeightGrad& a, const WeightGrad& b) {
+    const WeightGrad& one = a.parts.count > 1 ? a : b;
+    WeightGrad two = b;
+    two.first = quads_grid(one.n, one.m);
+    const bool both = a.parts.count > 1 && b.parts.count > 1;
+    hipLaunchKernelGGL((k_ffn_dw_join<T, F32OUT>),
+                       dim3(two.first + (both ? quads_grid(two.n, two.m) : 0u)),
+                       dim3(kPackThreads), 0, stream, one, two);
+    return (int)hipGetLastError();
+  };
+  if (down.parts.count > 1) {
+    e = dw_join(down, WeightGrad{});
+    if (e) return e;
+  }
+
+  next = 0;  // the sums before have been read by then
   const bool dx = g->dx && T_ > 0;
-  gate.first = dx ? grid_of(T_, H, tile2, o.split) : 0;
-  up.first = gate.first + (weights && gate.out ? grid_of(F, H, tile2) : 0);
-  const uint32_t blocks = up.first + (weights && up.out ? grid_of(F, H, tile2) : 0);
+  const OutArgs o{wg, wu, dg, du, (int32_t)T_, (int32_t)H, (int32_t)F,
+                  parts_at(ws, p, H, T_, dx ? p.split_dx : 1, &next), (uint16_t*)g->dx, g->lddx};
+  WeightGrad gate = weight(x, dg, H, F, g->dw_gate, g->lddw_gate, p.split_dw2, &next);
+  WeightGrad up = weight(x, du, H, F, g->dw_up, g->lddw_up, p.split_dw2, &next);
+  gate.first = dx ? grid_of(T_, H, tile2, o.parts.count) : 0;
+  up.first = gate.first + dw_grid(gate, tile2);
+  const uint32_t blocks = up.first + dw_grid(up, tile2);
   if (blocks) {
     if (p.small_back2)
       hipLaunchKernelGGL((k_ffn_back2<T, F32OUT, true>), dim3(blocks), dim3(256), 0, stream, o,
@@ -536,7 +732,11 @@ int backward_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, const zero_ffn_s
                          gate, up);
     ZK_LAUNCHED();
   }
-  return dx ? join_t<T>(o, stream) : (int)hipSuccess;
+  if (gate.parts.count > 1 || up.parts.count > 1) {
+    e = dw_join(gate, up);
+    if (e) return e;
+  }
+  return dx ? out_join<T>(o, stream) : (int)hipSuccess;
 }
 
 template <typename T>

@@ -86,8 +86,10 @@ __device__ __forceinline__ void leave_pair(const Few& a, A act, f32x4 g, f32x4 u
   const int64_t at = t * a.to.ld + r;
   *(u32x2*)(a.to.h + at) = narrow4<T>(h[0], h[1], h[2], h[3]);
   if (a.to.act) {
-    *(u32x2*)(a.to.act + at) = narrow4<T>(v[0], v[1], v[2], v[3]);
-    *(u32x2*)(a.to.slope + at) = narrow4<T>(b[0], b[1], b[2], b[3]);
+    const Kept4 k = keep4(v, b);
+    *(u32x2*)(a.to.act + at) = k.act;
+    *(u32x2*)(a.to.slope + at) = k.slope;
+    *(u32x2*)(a.to.low + at) = k.low;
   }
 }
 // Four columns of an output row that holds n.

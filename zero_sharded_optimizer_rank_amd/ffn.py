@@ -20,10 +20,13 @@ ACTIVATIONS = {"silu": abi.ZERO_ACT_SILU, "gelu": abi.ZERO_ACT_GELU,
 
 
 class FFNSaved(NamedTuple):
-    """What the gradients need of a forward pass, in 16 bits, columns padded to a multiple of 8."""
+    """What the gradients need of a forward pass, columns padded to a multiple of 8.  act and
+    slope hold the upper 16 bits of fp32 values (bfloat16 patterns, whatever the block's type),
+    low the next 8 of both: 24 bits each."""
     act: torch.Tensor     # act(x @ w_gate.T)
     slope: torch.Tensor   # (x @ w_up.T) * act'(x @ w_gate.T)
-    h: torch.Tensor       # act * (x @ w_up.T)
+    low: torch.Tensor
+    h: torch.Tensor       # act * (x @ w_up.T), in the block's type
 
 
 class FFNOut(NamedTuple):
@@ -97,7 +100,7 @@ class GatedFFN:
         gradients are still to come."""
         tokens = self.tokens if tokens is None else tokens
         return FFNSaved(*(torch.empty(tokens, self._pad, dtype=self.dtype, device=self.device)
-                          for _ in range(3)))
+                          for _ in range(4)))
 
     def _matrix(self, t, rows, cols, what, types=None):
         if not isinstance(t, torch.Tensor) or t.dim() != 2 or tuple(t.shape) != (rows, cols):
@@ -134,7 +137,7 @@ class GatedFFN:
                 raise ValueError(f"saved.{what} must be a [{t}, {self._pad}] tensor")
             lds.add(self._matrix(b[:t], t, self._pad, "saved." + what))
         if len(lds) > 1:
-            raise ValueError("the rows of act, slope and h lie differently")
+            raise ValueError("the rows of act, slope, low and h lie differently")
         return abi.zero_ffn_saved_t(*(b.data_ptr() for b in saved), lds.pop())
 
     def _workspace(self, ffn, grads, stream):
