@@ -895,8 +895,10 @@ int zero_head_loss_grad(const zero_head_t* head, float* token_loss, float* lse,
  *   dh = dy Wd,  du = dh act(g),  dg = dh u act'(g)
  *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h
  * Sums are fp32.  h, dg and du are rounded once to the 16-bit type (the matrix cores
- * multiply it); in fp16 what passes 65504 becomes infinite.  Gradients carry whatever loss scale dy carries.  Equal
- * inputs give equal bits. */
+ * multiply it); in fp16 what passes 65504 becomes infinite.  For up to 16 tokens (and
+ * hidden, inner >= 8) the forward pass multiplies h in two 16-bit parts, so that its
+ * rounding does not reach y.  Gradients carry whatever loss scale dy carries.  Equal
+ * inputs give equal bits; a token's y may depend on how many tokens share the call. */
 
 enum zero_act {
   ZERO_ACT_SILU = 0,      /* g / (1 + e^-g) */

@@ -95,6 +95,27 @@ def reference(x, wg, wu, wd, name, dy=None):
     return out
 
 
+def few_bound(x, wg, wu, wd, name):
+    """y, and the bound where h is held in two 16-bit parts: the second is off by u of itself, so h
+    by u^2 (and the type's smallest step), and the contraction is over both parts."""
+    dt = x.dtype
+    u = torch.finfo(dt).eps / 2
+    tiny = torch.finfo(dt).smallest_normal * torch.finfo(dt).eps / 2
+    H, F = x.shape[1], wg.shape[0]
+    X, G, U, D = (t.double() for t in (x, wg, wu, wd))
+    g, v = X @ G.t(), X @ U.t()
+    bg, bv = H * E * (X.abs() @ G.abs().t()), H * E * (X.abs() @ U.abs().t())
+    a = act(name, g)[0]
+    r = g.abs()
+    da = 1.2 * bg + a.abs() * E * (16 + 8 * (r + r ** 2 + r ** 3)) + 1e-30
+    h = a * v
+    bh = da * v.abs() + a.abs() * bv + E * h.abs()
+    bh = bh + u * u * (h.abs() + bh) + tiny
+    y = h @ D.t()
+    by = bh @ D.abs().t() + 2 * F * E * ((1 + u) * (h.abs() + bh) @ D.abs().t())
+    return h, y, 1.05 * (by + u * y.abs()) + tiny
+
+
 def check(got, want, bound, name):
     got = got.double()
     err = (got - want).abs()

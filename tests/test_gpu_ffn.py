@@ -118,6 +118,45 @@ def test_tokens(T):
     assert (f._y[T:] == 3).all() and (f._dx[T:] == 3).all()
 
 
+@pytest.mark.parametrize("dt", TYPES, ids=["bf16", "f16"])
+@pytest.mark.parametrize("T,H,F", [(1, 24, 4000), (4, 40, 1001), (7, 16, 2048), (8, 2056, 8200),
+                                   (9, 24, 2000), (13, 67, 515), (16, 40, 8200)])
+def test_few_tokens_round_once(T, H, F, dt):
+    """Up to 16 tokens h's own rounding does not reach y."""
+    x, wg, wu, wd, _ = _inputs(T, H, F, dt, seed=24)
+    h, want, bound = fu.few_bound(x, wg, wu, wd, "gelu")
+    f = _ffn(T, H, F, dt, act="gelu")
+    saved = f.new_saved()
+    for t in saved:
+        t.fill_(float("nan"))
+    _dirty(f)
+    r = f.forward(x, wg, wu, wd, save=saved)
+    fu.check(r.y, want, bound, "y")
+    # |round(y + d) - y| <= |round(y) - y| + 2 |d|: d are fp32 sums' errors, which add up as a
+    # random walk does, to a relative (sqrt F + sqrt H + 16) E at twice their size
+    limit = (want.to(dt).double() - want).norm() / want.norm()
+    limit = float(limit) + 2 * 2 * (F ** 0.5 + H ** 0.5 + 16) * fu.E
+    fu.check_norm(r.y, want, limit, "y")
+    if dt == torch.bfloat16 and T * H >= 200:  # it tells: h rounded once more is outside
+        once = (h.to(dt).double() @ wd.double().t()).to(dt).double()
+        assert float((once - want).norm() / want.norm()) > limit
+
+
+@pytest.mark.parametrize("T", [5, 12])
+def test_few_tokens_past_16_bits(T):
+    """Where h passes fp16's range y is what infinities give, as for more tokens."""
+    H, F, dt = 64, 64, torch.float16
+    x, wg, wu = (torch.zeros(r, H, dtype=dt, device="cuda") for r in (T, F, F))
+    x[:, 0] = 300.0
+    wg[3, 0] = wu[3, 0] = 1.0  # h = 90000 in one column
+    wd = torch.eye(H, F, device="cuda").to(dt)
+    y = _ffn(T, H, F, dt, act="relu").forward(x, wg, wu, wd).y
+    many = _ffn(40, H, F, dt, act="relu").forward(x.repeat(40, 1)[:40], wg, wu, wd).y
+    assert torch.isinf(y[:, 3]).all()
+    assert torch.equal(torch.isnan(y), torch.isnan(many[:T]))
+    assert torch.equal(y.nan_to_num(nan=7.0), many[:T].nan_to_num(nan=7.0))
+
+
 def _strided(t):
     b = torch.full((t.shape[0], t.shape[1] + 24), float("nan"), dtype=t.dtype, device=t.device)
     b[:, 8:8 + t.shape[1]] = t

@@ -13,20 +13,21 @@ namespace zk {
 constexpr int64_t kFfnTile = 256;
 constexpr int64_t kFfnStep = 64;   // contraction elements a step stages
 constexpr int32_t kFfnFew = 64;    // most tokens of the form that streams the weights
+constexpr int32_t kFfnLow = 16;    // most tokens whose h is kept in two parts there
 constexpr int kFewTile = 128;      // columns of a wave's step there: two lines of a row
 
 // Where things lie in the workspace (byte offsets), and how the work is cut.
 struct FfnPlan {
   int64_t hidden_pad, inner_pad;  // row lengths of packed matrices: multiples of 8
-  bool few;
+  bool few, low;
   bool pack_x, pack_gate, pack_up, pack_down, pack_dy;  // rows that no 16-byte loads fit
   bool small_in, small_out, small_back1, small_back2;  // 128 x 128 tiles, else 256 x 256
   // parts that a product's contraction is cut into; small tiles: any, large: y and dx
   int32_t split_in, split_y, split_dh, split_dw1, split_dx, split_dw2;
-  int32_t few_sets_in, few_sets_out;  // few: sets of rows of a workgroup, 2 or 4; 1: x is
+  int32_t few_sets_in, few_sets_out;  // few: sets of rows of a workgroup, 2 or 4; both 1: x is
                                       // not shared
   // offsets
-  size_t x, w_gate, w_up, w_down, dy, h, dg, du, acc, total;
+  size_t x, w_gate, w_up, w_down, dy, h, h_low, dg, du, acc, total;
 };
 FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g);
 

@@ -89,9 +89,6 @@ bool ragged(const void* p, int64_t ld, int64_t width) {
   return width % 8 != 0 || ld % 8 != 0 || !aligned(p, 16);
 }
 
-// Workgroups of few tokens' first product that are enough for the 256 CUs.
-constexpr int64_t kFewGroups = 192;
-
 // A product's tiles and their stages; small tiles share a CU by two.
 struct Work {
   int64_t count, stages;
@@ -146,6 +143,7 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
   p.hidden_pad = up(H, 8);
   p.inner_pad = up(F, 8);
   p.few = !g && T <= kFfnFew && H >= 8 && F >= 8;  // whole 16-byte loads
+  p.low = p.few && T <= kFfnLow;
   if (!p.few) {
     p.pack_x = ragged(f->x, f->ldx, H);
     p.pack_gate = ragged(f->w_gate, f->ld_gate, H);
@@ -187,8 +185,18 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
     p.split_dx = split_beside(dx, 2 * all(dw));
   }
   if (p.few) {
-    p.few_sets_in = T <= 8 ? 1 : tiles(F, 64) >= kFewGroups ? 4 : 2;
-    p.few_sets_out = T <= 8 ? 1 : H >= 2048 ? 4 : 2;
+    // Sets of the first product by the rounds that its workgroups take on the 256 CUs, one a
+    // CU; at a tie four, which fetch x half as often (12 tokens, two and four sets: 2048 x
+    // 8192 32 and 39 us a forward pass, 4096 x 11008 81 and 63, 8192 x 22016 208 and 232).
+    const auto rounds = [&](int64_t sets) { return tiles(tiles(F, 16 * sets), 256) * sets; };
+    p.few_sets_in = rounds(2) < rounds(4) ? 2 : 4;
+    p.few_sets_out = H >= 2048 ? 4 : 2;
+    // Up to 8 tokens' x and h come from the L2 as fast, and the waves need not wait for one
+    // another, unless the products are large and the tokens more than 4 (8 tokens, not
+    // shared and shared: 768 x 2048 13 and 20 us, 4096 x 8192 48 and 60, 4096 x 14336 78 and
+    // 69, 8192 x 28672 288 and 260; 4 tokens there 75 and 73, 265 and 261).
+    if (T <= 4 || (T <= 8 && (H < 2048 || F <= 8192)))
+      p.few_sets_in = p.few_sets_out = 1;
     if (p.few_sets_out > 1) {
       const int64_t blocks = tiles(H, 32 * p.few_sets_out), steps = tiles(F, kFewTile);
       const int64_t most = steps * p.few_sets_out / (2 * 8);  // two steps a slice at least
@@ -209,6 +217,7 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
   p.w_down = take(p.pack_down ? 2 * H * p.inner_pad : 0);
   p.dy = take(p.pack_dy ? 2 * T * p.hidden_pad : 0);
   p.h = take(g ? 0 : 2 * T * p.inner_pad);
+  p.h_low = take(p.low ? 2 * T * p.inner_pad : 0);
   if (g) {
     p.dg = take(2 * T * p.inner_pad);
     p.du = take(2 * T * p.inner_pad);

@@ -5,15 +5,25 @@
 // weight at 64 tokens.  So no weight is staged: a wave takes 32 rows' pieces (16
 // of each projection) from memory straight into fragments, 128 columns at a time,
 // the next ones on their way while the last are multiplied.  Rows may start anywhere.
-//   up to 8 tokens  k_ffn_direct  the waves of a workgroup share the contraction
-//   more            k_ffn_shared  x (and h) go through LDS, and waves of the same columns
-//                                 share them: fetched by each wave from the L2 they
-//                                 would be twice the weights' bytes at 64 tokens (4096
-//                                 x 14336: 184 us a pass, so 87).  Eight waves are R
-//                                 sets of rows by 8 / R slices of the contraction,
-//                                 joined through LDS in a fixed order; the second
-//                                 product's, whose rows are few, is also split over
-//                                 workgroups (k_ffn_few_join)
+//   up to 4 or 8 tokens  k_ffn_direct  the waves of a workgroup share the contraction
+//   more                 k_ffn_shared  x (and h) go through LDS, and waves of the same
+//                                      columns share them: fetched by each wave from the
+//                                      L2 they would be twice the weights' bytes at 64
+//                                      tokens (4096 x 14336: 184 us a pass, so 87).
+//                                      Eight waves are R sets of rows by 8 / R slices of
+//                                      the contraction, joined through LDS in a fixed
+//                                      order; the second product's, whose rows are few,
+//                                      is also split over workgroups (k_ffn_few_join)
+// One token of 4096 x 14336 in bf16 takes 66 us (352 MB of weights, 5.3 TB/s), 37 tokens of
+// 1600 x 6400 in fp16 30 (61 MB; about 20 of them are the launches' start and end), 22 of
+// 8192 x 28672 259 (5.4 TB/s).
+//
+// With few tokens the outputs are few, and a second rounding on the way to them shows (y
+// is off by 2.3e-3 in bf16 where its own rounding alone is 1.7e-3).  Up to 16 tokens h
+// therefore is kept in two 16-bit parts, the second what the first one's rounding left:
+// without more products up to 8 tokens, whose second parts are the columns that have
+// no token, with twice as many of the second product for more, which still wait for the
+// weights (16 tokens, 1600 x 6400: 30.4 -> 31.9 us).  From 24 on it would cost 8%.
 #include <stddef.h>
 
 #include "ffn_device.h"
@@ -30,8 +40,11 @@ struct Few {
   int64_t ldw0, ldw1;
   const uint16_t* x;        // [tokens, k]
   int64_t ldx;
+  const uint16_t* x_low;    // else: what x's rounding left, or NULL; rows ldx_low apart
+  int64_t ldx_low;
   int32_t rows, k, tokens, act, split;
   Kept to;                  // PAIR
+  uint16_t* h_low;          // PAIR: what h's rounding leaves, rows pad apart, or NULL
   int32_t pad;              // PAIR: columns of h; those past the rows are zero
   uint16_t* out;            // else, split = 1: [tokens, rows], rows ldo apart
   int64_t ldo;
@@ -84,7 +97,17 @@ __device__ __forceinline__ void leave_pair(const Few& a, A act, f32x4 g, f32x4 u
   }
   if (t >= a.tokens || r >= a.pad) return;
   const int64_t at = t * a.to.ld + r;
-  *(u32x2*)(a.to.h + at) = narrow4<T>(h[0], h[1], h[2], h[3]);
+  const u32x2 h16 = narrow4<T>(h[0], h[1], h[2], h[3]);
+  *(u32x2*)(a.to.h + at) = h16;
+  if (a.h_low) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float rest = h[e] - widen<T>(h16[e >> 1] >> (16 * (e & 1)) & 0xFFFFu);
+      // infinity and NaN are h's to hand on
+      h[e] = __builtin_fabsf(rest) < __builtin_inff() ? rest : 0.0f;
+    }
+    *(u32x2*)(a.h_low + (int64_t)t * a.pad + r) = narrow4<T>(h[0], h[1], h[2], h[3]);
+  }
   if (a.to.act) {
     const Kept4 k = keep4(v, b);
     *(u32x2*)(a.to.act + at) = k.act;
@@ -126,7 +149,10 @@ k_ffn_direct(const Few a) {
       const int64_t at = r < a.rows ? r : a.rows - 1;
       wr[i][h] = i ? a.w1 + at * a.ldw1 : a.w0 + at * a.ldw0;
     }
-  const uint16_t* xr = a.x + (int64_t)(q < a.tokens ? q : a.tokens - 1) * a.ldx;
+  // columns 8 to 15 of the product have no token: they take what h's rounding left
+  const bool low = !PAIR && q >= 8;
+  const int32_t token = (PAIR ? q : q & 7) < a.tokens ? (PAIR ? q : q & 7) : a.tokens - 1;
+  const uint16_t* xr = low ? a.x_low + token * a.ldx_low : a.x + token * a.ldx;
   const int32_t wk = 8 * (4 * (q >> 3) + g);
   const int beyond = (8 - k % 8) % 8;
   f32x4 acc[NI];
@@ -201,17 +227,22 @@ k_ffn_direct(const Few a) {
   const int32_t r = r0 + 4 * g;
   if constexpr (PAIR) {
     with_act(a.act, [&](auto act) { leave_pair<T>(a, act, acc[0], acc[1], q, r); });
-  } else if (q < a.tokens && r < a.rows) {
-    leave4<T>(a.out + q * a.ldo, r, a.rows, acc[0]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)  // lane q + 8's
+      acc[0][e] += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+          0, (int)__float_as_uint(acc[0][e]), 0x128, 0xF, 0xF, false));
+    if (q < a.tokens && r < a.rows) leave4<T>(a.out + q * a.ldo, r, a.rows, acc[0]);
   }
 }
 
 // More tokens: x goes through LDS.
-template <typename T, int NJ, int R, bool PAIR>
+template <typename T, int NJ, int R, bool PAIR, bool LOW>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))) void
 k_ffn_shared(const Few a) {
-  constexpr int NI = 2, S = kWaves / R, XLOADS = 4 * NJ / R > 0 ? 4 * NJ / R : 1;
-  constexpr int kTileBytes = 16 * NJ * 2 * kFewTile, kSums = kWaves * NI * NJ * 1024;
+  constexpr int NI = 2, S = kWaves / R, XROWS = 16 * NJ * (LOW ? 2 : 1);
+  constexpr int XLOADS = XROWS > 4 * R ? XROWS / (4 * R) : 1;
+  constexpr int kTileBytes = XROWS * 2 * kFewTile, kSums = kWaves * NI * NJ * 1024;
   constexpr int kLds = 2 * S * kTileBytes > kSums ? 2 * S * kTileBytes : kSums;
   __shared__ __attribute__((aligned(1024))) char lds[kLds];
   const int lane = threadIdx.x & 63, g = lane >> 4, q = lane & 15;
@@ -237,9 +268,9 @@ k_ffn_shared(const Few a) {
 #pragma unroll
   for (int n = 0; n < XLOADS; ++n) {
     const int32_t t = (xt >> 4) + 4 * R * n;
-    xr[n] = a.x + (int64_t)(t < a.tokens ? t : a.tokens - 1) * a.ldx;
+    const int32_t own = t % (16 * NJ) < a.tokens ? t % (16 * NJ) : a.tokens - 1;
+    xr[n] = LOW && t >= 16 * NJ ? a.x_low + own * a.ldx_low : a.x + own * a.ldx;
   }
-  const bool stores_x = 4 * R <= 16 * NJ || (xt >> 4) < 16 * NJ;
   char* const lx = lds + slice * 2 * kTileBytes;
   const int beyond = (8 - k % 8) % 8;
   auto load = [&](const uint16_t* row, int32_t c) { return row8(row, c, k); };
@@ -271,7 +302,7 @@ k_ffn_shared(const Few a) {
 #pragma unroll
     for (int n = 0; n < XLOADS; ++n) {
       const int row = (xt >> 4) + 4 * R * n;
-      if (stores_x) *(s16x8*)(d + row * 256 + ((xc ^ (row & 15)) << 4)) = xs[n];
+      *(s16x8*)(d + row * 256 + ((xc ^ (row & 15)) << 4)) = xs[n];
     }
   };
   auto use = [&](s16x8 (&d)[NI][2][2], const char* l, int32_t tile) {
@@ -293,10 +324,13 @@ k_ffn_shared(const Few a) {
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          const s16x8 b =
-              *(const s16x8*)(l + (16 * j + q) * 256 + (((8 * n + 4 * s + g) ^ q) << 4));
 #pragma unroll
-          for (int i = 0; i < NI; ++i) acc[i][j] = mfma(T{}, f[i][s], b, acc[i][j]);
+          for (int rows = 0; rows < XROWS; rows += 16 * NJ) {
+            const s16x8 b =
+                *(const s16x8*)(l + (rows + 16 * j + q) * 256 + (((8 * n + 4 * s + g) ^ q) << 4));
+#pragma unroll
+            for (int i = 0; i < NI; ++i) acc[i][j] = mfma(T{}, f[i][s], b, acc[i][j]);
+          }
         }
     }
   };
@@ -388,10 +422,10 @@ __global__ __launch_bounds__(kJoinThreads) void k_ffn_few_join(
   leave4<T>(out + t * ldo, r, rows, s);
 }
 
-template <typename T, int NJ, int R, bool PAIR>
+template <typename T, int NJ, int R, bool PAIR, bool LOW>
 int shared_r(const Few& a, hipStream_t stream) {
   const int32_t each = PAIR ? 16 * R : 32 * R;
-  hipLaunchKernelGGL((k_ffn_shared<T, NJ, R, PAIR>),
+  hipLaunchKernelGGL((k_ffn_shared<T, NJ, R, PAIR, LOW>),
                      dim3((uint32_t)((a.rows + each - 1) / each * a.split)), dim3(64 * kWaves), 0,
                      stream, a);
   return (int)hipGetLastError();
@@ -399,11 +433,12 @@ int shared_r(const Few& a, hipStream_t stream) {
 
 template <typename T, int NJ>
 int shared_j(const Few& in, const Few& out, const FfnPlan& p, hipStream_t stream) {
-  int e = p.few_sets_in == 4 ? shared_r<T, NJ, 4, true>(in, stream)
-                             : shared_r<T, NJ, 2, true>(in, stream);
+  constexpr bool LOW = 16 * NJ <= kFfnLow;
+  int e = p.few_sets_in == 4 ? shared_r<T, NJ, 4, true, false>(in, stream)
+                             : shared_r<T, NJ, 2, true, false>(in, stream);
   if (e) return e;
-  e = p.few_sets_out == 4 ? shared_r<T, NJ, 4, false>(out, stream)
-                          : shared_r<T, NJ, 2, false>(out, stream);
+  e = p.few_sets_out == 4 ? shared_r<T, NJ, 4, false, LOW>(out, stream)
+                          : shared_r<T, NJ, 2, false, LOW>(out, stream);
   if (e || out.split == 1) return e;
   hipLaunchKernelGGL((k_ffn_few_join<T>),
                      dim3((uint32_t)((out.rows + 4 * kJoinThreads - 1) / (4 * kJoinThreads)),
@@ -441,11 +476,14 @@ int few_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, void* y, int64_t ldy,
   in.split = 1;
   in.to = to;
   in.pad = (int32_t)p.inner_pad;
+  in.h_low = p.low ? at<uint16_t>(ws, p.h_low) : nullptr;
   Few out{};
   out.w0 = (const uint16_t*)f->w_down;
   out.ldw0 = f->ld_down;
   out.x = to.h;
   out.ldx = to.ld;
+  out.x_low = in.h_low;
+  out.ldx_low = p.inner_pad;
   out.rows = (int32_t)f->hidden;
   out.k = (int32_t)f->inner;
   out.tokens = (int32_t)f->tokens;
