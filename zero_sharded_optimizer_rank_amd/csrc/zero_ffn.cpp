@@ -154,15 +154,16 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
   // Small tiles where the large ones would leave half of the CUs idle (100 x 4096 x 14336,
   // 112 tiles, forward 130 -> 107 us; 1024 x 1600 x 6400, 200 tiles, 88 -> 100), in a
   // backward pass also where a CU's share is short, so that a tile's start and end weigh
-  // (300 x 1600 x 6400, training 194 -> 165 us; 512 x 4096 x 14336 563 -> 654), and for y of
-  // up to one small tile's tokens.
+  // (300 x 1600 x 6400, training 194 -> 165 us; 512 x 4096 x 14336 563 -> 654), and for y and
+  // the second backward launch of up to one small tile's tokens (100 x 4096 x 14336, training
+  // 318 -> 304 us, 200 x 4096 x 14336 422 -> 464; 64 x 8192 x 28672 1013 -> 1011).
   const auto all = [](const Work& w) { return w.count * w.stages; };
   Work in = work(2 * F, T, H, false), dh = work(F, T, H, false), dw = work(F, H, T, false);
   Work dx = work(T, H, 2 * F, false);
   p.small_in = in.count < 128;
   p.small_out = T <= 128;
   p.small_back1 = dh.count + dw.count < 128 || all(dh) + all(dw) < 24 * 256;
-  p.small_back2 = dx.count + 2 * dw.count < 128 || all(dx) + 2 * all(dw) < 24 * 256;
+  p.small_back2 = T <= 128 || dx.count + 2 * dw.count < 128 || all(dx) + 2 * all(dw) < 24 * 256;
   p.split_in = p.split_y = p.split_dh = p.split_dw1 = p.split_dx = p.split_dw2 = 1;
   if (!p.few && !g) {
     p.split_y = split_of(work(T, H, F, p.small_out), p.small_out);
