@@ -49,7 +49,7 @@ struct AdamEntry {
 
 struct ListScalars {
   float b1, omb1, b2, omb2, eps, sqrt_bc2;
-  float inv_root;    // 2^-12 / sqrt(1 - b2^t)
+  float inv_root, inv_root_low;  // 1 / sqrt(1 - b2^t), and 2^-12 of it
   float scale;       // 1 / loss_scale
   uint32_t key;      // the seed, mixed once
   double step_size;  // lr / (1 - b1^t); a tensor's factor follows

@@ -118,7 +118,8 @@ int zero_tensors_adam(const zero_adam_list_t* list, const zero_step_args_t* args
   s.omb2 = (float)(1.0 - args->beta2);
   s.eps = (float)args->eps;
   s.sqrt_bc2 = (float)sqrt(c2);
-  s.inv_root = (float)(0x1p-12 / sqrt(c2));
+  s.inv_root = (float)(1.0 / sqrt(c2));
+  s.inv_root_low = 0x1p-12f * s.inv_root;
   s.scale = scale;
   s.key = seed;
   s.step_size = args->lr / c1;

@@ -254,8 +254,11 @@ __device__ __forceinline__ void update_chunk(const AdamEntry& t, int64_t at, int
       vv = sc.b2 * vv + sc.omb2 * (gc * gc);
       float u;
       if constexpr (SMALL) {
-        // 2^24: the instruction's root of what fp32 holds with fewer bits is zero
-        const float den = __builtin_amdgcn_sqrtf(vv * 0x1p24f) * sc.inv_root + sc.eps;
+        // the instruction's root of what fp32 holds with fewer bits is zero, so small
+        // ones are raised by 2^24; large ones would pass fp32's range
+        const bool low = vv < 1.0f;
+        const float den = __builtin_amdgcn_sqrtf(low ? vv * 0x1p24f : vv) *
+                              (low ? sc.inv_root_low : sc.inv_root) + sc.eps;
         u = mm * __builtin_amdgcn_rcpf(den);
       } else {
         u = mm / (__builtin_sqrtf(vv) / sc.sqrt_bc2 + sc.eps);
