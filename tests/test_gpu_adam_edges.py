@@ -54,3 +54,40 @@ def test_large_gradients_within_the_roundings(bits, gt):
         p = w.cpu().numpy()
         assert (np.abs(p.astype(np.float64) - want[0]) <= far[0]).all()
         m, v = (t[:mags.size].float().cpu().numpy() for t in lst.moments())
+
+
+NANS = [("f32", 0xFFFFFFFF), ("f32", 0xFFC00000), ("f32", 0x7FFFFFFF), ("f32", 0x7F800001),
+        ("f16", 0xFFFF), ("f16", 0xFE00), ("f16", 0x7FFF), ("bf16", 0xFFFF), ("bf16", 0xFFC0),
+        ("bf16", 0x7FFF), ("bf16", 0x7F81)]
+
+
+@pytest.mark.parametrize("dt,pattern", NANS, ids=[f"{d}-{p:X}" for d, p in NANS])
+def test_a_nan_stays_one(dt, pattern):
+    """Whatever the NaN's sign and payload and the random bits: the element's m, v and weight are
+    NaN, its block's exponents the largest, and the blocks beside it have the codes of a step
+    without it."""
+    n, at = 3 * au.BLOCK, au.BLOCK + 5
+    wide = dt == "f32"
+    bits = np.full(n, pattern, dtype=np.uint32 if wide else np.uint16)
+    t = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dt]
+    nans = torch.from_numpy(bits.view(np.int32 if wide else np.int16)).view(t).cuda()
+    for seed in range(20):
+        sound = torch.full((n,), 2.0 ** -9, dtype=t, device="cuda")
+        g = sound.clone()
+        g[at] = nans[at]
+        assert torch.isnan(g[at])
+        states = []
+        for grad in (sound, g):
+            w = torch.ones(n, device="cuda")
+            lst = _list(grad, w, 8)
+            lst.step(lr=1e-3, step=1, seed=seed)
+            m, v = lst.moments()
+            states.append((lst.state, w, m, v))
+        (a, _, _, _), (b, w, m, v) = states
+        assert torch.nonzero(torch.isnan(w))[:, 0].tolist() == [at]
+        assert torch.nonzero(torch.isnan(m))[:, 0].tolist() == [at]
+        assert torch.nonzero(torch.isnan(v))[:, 0].tolist() == [at]
+        assert b.m_exp.tolist()[1] == 255 and b.v_exp.tolist()[1] == 255
+        for x, y in ((a.m, b.m), (a.v, b.v)):
+            assert torch.equal(x[:au.BLOCK], y[:au.BLOCK])
+            assert torch.equal(x[2 * au.BLOCK:], y[2 * au.BLOCK:])

@@ -161,9 +161,11 @@ __device__ __forceinline__ float decode_v(uint32_t codes, int e, uint32_t base) 
   const uint32_t a = codes >> (8 * e) & 0xFFu;
   return __uint_as_float(a ? (a << 20) + base : 0u);
 }
-// fp32's pattern (without sign) with 3 fraction bits, rounded up where the bits
-// below and the random ones (bits 4 to 19) overflow.  A NaN stays one.
-__device__ __forceinline__ uint32_t cut(uint32_t pattern, uint32_t random) {
+// fp32's pattern without sign, with 3 fraction bits, rounded up where the bits
+// below and the random ones (bits 4 to 19) overflow.  A NaN stays one, whatever its
+// sign and payload: without the sign the addition cannot pass 32 bits.
+__device__ __forceinline__ uint32_t cut(float x, uint32_t random) {
+  const uint32_t pattern = __float_as_uint(x) & 0x7FFFFFFFu;
   const uint32_t p = (pattern + ((random & 0xFFFF0u) | 8u)) >> 20;
   return p < 0x7FFu ? p : 0x7FFu;
 }
@@ -270,8 +272,8 @@ __device__ __forceinline__ void update_chunk(const AdamEntry& t, int64_t at, int
       v[k][e] = vv;
       if constexpr (SMALL) {
         const uint32_t random = mix(count + (uint32_t)e);
-        pm[e] = cut(__float_as_uint(mm) & 0x7FFFFFFFu, random << 4);
-        pv[e] = cut(__float_as_uint(vv), random >> 12);  // no sign: v >= 0
+        pm[e] = cut(mm, random << 4);
+        pv[e] = cut(vv, random >> 12);
         if (FULL || e < n) top = max2(top, pm[e] | pv[e] << 16);
       }
     }
