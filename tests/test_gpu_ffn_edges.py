@@ -1,0 +1,60 @@
+"""The gated feed-forward block where values leave the ordinary range: NaNs and infinities, huge
+arguments of the activations."""
+import pytest
+
+import ffn_util as fu
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.bfloat16, torch.float16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _ffn(*a, **k):
+    from zero_sharded_optimizer_rank_amd.ffn import GatedFFN
+    return GatedFFN(*a, **k)
+
+
+def _kept(saved):
+    """The fp32 values of act and slope: their upper 16 bits, and the next 8 from low."""
+    high = [t.view(torch.int16).to(torch.int32) << 16 for t in (saved.act, saved.slope)]
+    low = saved.low.view(torch.int16).to(torch.int32)
+    return tuple((h | (b & 0xFF) << 8).view(torch.float32) for h, b in zip(high, (low, low >> 8)))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu"])
+@pytest.mark.parametrize("T", [3, 20, 100])
+def test_huge_arguments(T, act):
+    """Where the activation has reached its line (g, or 0) it stays there up to the largest
+    finite g, and its slope 1 or 0: kept in 24 bits, off by 2^-16 of itself; g = -30 is the only
+    one with a value between, under 1e-9."""
+    H, F, dt = 8, 16, torch.bfloat16
+    x = torch.zeros(T, H, dtype=dt, device="cuda")
+    x[:, 1] = 1.0
+    values = [30.0, 1e4, 1e10, 1e13, 1e19, 4e19, 1e20, 1e30, 3e38]
+    wg = torch.zeros(F, H, dtype=dt, device="cuda")
+    for i in range(F):
+        wg[i, 0] = 1.0 if i % 2 else -1.0
+    wu = torch.zeros_like(wg)
+    wu[:, 1] = 1.0
+    wd = torch.zeros(H, F, dtype=dt, device="cuda")
+    wd[0] = 1.0
+    dy = torch.zeros_like(x)
+    dy[:, 0] = 1.0
+    f = _ffn(T, H, F, dt, act=act)
+    for value in values:
+        x[:, 0] = value
+        r = f.forward(x, wg, wu, wd, save=True)
+        g = x.double() @ wg.double().t()
+        for got, want in zip(_kept(r.saved), fu.act(act, g)):
+            assert ((got.double() - want).abs() <= 2.0 ** -16 * want.abs() + 1e-9).all(), value
+        # dg = slope: dx's first column is its difference over both signs, bf16 rounds it
+        dx = f.backward(dy, x, wg, wu, wd, r.saved).dx
+        assert ((dx[:, 0].double() - F // 2).abs() <= F // 2 * 2.0 ** -8 + 1e-6).all(), value

@@ -101,7 +101,8 @@ __device__ __forceinline__ float activated(Act<A>, float g, float& slope) {
     slope = c + g * density;
     return g * c;
   } else if constexpr (A == ZERO_ACT_GELU_TANH) {
-    const float q = 0.044715f * g * g;
+    // held finite: beyond, s is 0 or 1, and 0 times an infinite slope of z would be NaN
+    const float q = __builtin_fminf(0.044715f * g * g, 0x1p100f);
     const float s = logistic(kGeluTanh * (g + g * q)), a = g * s;
     slope = s + a * (1.0f - s) * (kGeluTanh * (1.0f + 3.0f * q));
     return a;
