@@ -58,3 +58,42 @@ def test_huge_arguments(T, act):
         # dg = slope: dx's first column is its difference over both signs, bf16 rounds it
         dx = f.backward(dy, x, wg, wu, wd, r.saved).dx
         assert ((dx[:, 0].double() - F // 2).abs() <= F // 2 * 2.0 ** -8 + 1e-6).all(), value
+
+
+PADS = [(20, 64, 203), (100, 64, 203), (300, 72, 45), (200, 4000, 43), (130, 2051, 9),
+        (1030, 4104, 4099)]
+
+
+@pytest.mark.parametrize("T,H,F", PADS, ids=["x".join(map(str, p)) for p in PADS])
+def test_infinities_with_ragged_widths(T, H, F):
+    """All values positive, so that one infinity makes a token's sums +inf and none NaN, as in the
+    formulas; columns that only fill the rows up to 8 take no part."""
+    dt = torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(0)
+
+    def positive(rows, cols, s):
+        return (torch.rand(rows, cols, generator=gen, device="cuda") * s + s / 8).to(dt)
+    x, dy = positive(T, H, 1.0), positive(T, H, 0.05)
+    wg, wu, wd = positive(F, H, 1.0 / H), positive(F, H, 1.0 / H), positive(H, F, 1.0 / F)
+    f = _ffn(T, H, F, dt, act="relu")
+    r = f.forward(x, wg, wu, wd, save=True)
+    y, dx = r.y.clone(), f.backward(dy, x, wg, wu, wd, r.saved).dx.clone()
+    assert torch.isfinite(y).all() and torch.isfinite(dx).all()
+    at, keep = 17, torch.arange(T, device="cuda") != 17
+    inf = float("inf")
+    bad = x.clone()
+    bad[at, 5] = inf
+    r = f.forward(bad, wg, wu, wd, save=True)
+    d = f.backward(dy, bad, wg, wu, wd, r.saved)
+    assert torch.equal(r.y[keep], y[keep]) and torch.equal(d.dx[keep], dx[keep])
+    assert (r.y[at] == inf).all() and (d.dx[at] == inf).all()
+    for w in (d.dw_gate, d.dw_up, d.dw_down):
+        assert (w == inf).all()
+    r = f.forward(x, wg, wu, wd, save=True)
+    bad = dy.clone()
+    bad[at, 5] = inf
+    d = f.backward(bad, x, wg, wu, wd, r.saved)
+    assert torch.equal(d.dx[keep], dx[keep]) and (d.dx[at] == inf).all()
+    assert (d.dw_gate == inf).all() and (d.dw_up == inf).all() and (d.dw_down[5] == inf).all()
+    other = torch.arange(H, device="cuda") != 5
+    assert torch.isfinite(d.dw_down[other]).all()

@@ -144,6 +144,33 @@ __device__ __forceinline__ f32x4 joined(const Parts& p, int64_t row, int32_t c) 
 }
 __device__ __forceinline__ int32_t stages_of(int32_t k) { return (k + kStage - 1) / kStage; }
 
+// Rows of blocks [i0, i1) of a tile's sums that lie past the operand's (its row 0 is r0) are
+// zero: an infinity in the other operand makes them NaN, and those that fill h's, dg's and
+// du's rows up to 8 take part in the next contraction.
+template <typename G>
+__device__ __forceinline__ void clear_past(int32_t r0, int32_t rows, int i0, int i1,
+                                           f32x4 (&acc)[G::MI][G::NJ]) {
+  if (r0 + G::kRows <= rows) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = 0; i < G::MI; ++i) {
+    if (i < i0 || i >= i1) continue;
+    const int32_t r = r0 + G::row(wave, i - i0) + 4 * (lane >> 4);
+#pragma unroll
+    for (int j = 0; j < G::NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (r + e >= rows) acc[i][j][e] = 0.0f;
+  }
+}
+// The same of four sums.
+__device__ __forceinline__ f32x4 before(int32_t rows, int32_t r, f32x4 s) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (r + e >= rows) s[e] = 0.0f;
+  return s;
+}
+
 // --- forward -------------------------------------------------------------------
 struct PairProduct {
   Operand gate, up, B;
@@ -192,6 +219,8 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void k_ffn_in(Matrix x, Matrix w
     return;
   }
   G::run(src, x.width, lds, acc);
+  clear_past<G>(f0, inner, 0, H, acc);
+  clear_past<G>(f0, inner, H, G::MI, acc);
   auto leave = [&](uint16_t* out, int region) {
     G::take_half(lds, region, [&](int col, int row, u32x4 v) {
       const int32_t t = t0 + col, f = f0 + row;
@@ -237,13 +266,15 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void k_ffn_in(Matrix x, Matrix w
 // inner columns: 6 us, mostly its launch).
 template <typename T, int ACT>
 __global__ __launch_bounds__(kPackThreads) void k_ffn_in_join(Parts parts, int32_t tokens,
-                                                              int32_t inner_pad, Kept to) {
+                                                              int32_t inner, int32_t inner_pad,
+                                                              Kept to) {
   const int64_t q = (int64_t)blockIdx.x * kPackThreads + threadIdx.x;
   const int64_t t = q / (inner_pad / 4);
   const int32_t f = (int32_t)(q % (inner_pad / 4)) * 4;
   if (t >= tokens) return;
   f32x4 h, a, b;
-  gated<ACT>(joined(parts, t, f), joined(parts, t, parts.ld / 2 + f), h, a, b);
+  gated<ACT>(before(inner, f, joined(parts, t, f)),
+             before(inner, f, joined(parts, t, parts.ld / 2 + f)), h, a, b);
   const int64_t at = t * to.ld + f;
   *(u32x2*)(to.h + at) = narrow4<T>(h[0], h[1], h[2], h[3]);
   if (!to.act) return;
@@ -381,6 +412,7 @@ __device__ __forceinline__ void dh_tile(uint32_t block, const DhArgs& a) {
     return leave_part<G>(a.parts, part, f0, t0, 0, G::MI, acc);
   }
   G::run(src, a.hidden, lds, acc);
+  clear_past<G>(f0, a.inner, 0, G::MI, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   constexpr int N = 4, kSets = G::MI * G::NJ / N;  // blocks of a set
   u32x2 av[2][N], bv[2][N], lv[2][N];
@@ -442,8 +474,8 @@ __global__ __launch_bounds__(kPackThreads) void k_ffn_dh_join(DhArgs a) {
   if (t >= a.tokens) return;
   const int64_t at = t * a.ld + f, to = t * a.inner_pad + f;
   u32x2 x, y;
-  gradients<T>(joined(a.parts, t, f), *(const u32x2*)(a.act + at), *(const u32x2*)(a.slope + at),
-               *(const u32x2*)(a.low + at), x, y);
+  gradients<T>(before(a.inner, f, joined(a.parts, t, f)), *(const u32x2*)(a.act + at),
+               *(const u32x2*)(a.slope + at), *(const u32x2*)(a.low + at), x, y);
   *(u32x2*)(a.dg + to) = x;
   *(u32x2*)(a.du + to) = y;
 }
@@ -648,8 +680,8 @@ int forward_t(const zero_ffn_t* f, const FfnPlan& p, void* ws, void* y, int64_t 
   ZK_LAUNCHED();
   if (parts.count > 1) {
     hipLaunchKernelGGL(in_join_kernel<T>(f->act), dim3(quads_grid(T_, p.inner_pad)),
-                       dim3(kPackThreads), 0, stream, parts, (int32_t)T_, (int32_t)p.inner_pad,
-                       to);
+                       dim3(kPackThreads), 0, stream, parts, (int32_t)T_, (int32_t)F,
+                       (int32_t)p.inner_pad, to);
     ZK_LAUNCHED();
   }
   const Matrix h{to.h, (int32_t)to.ld, (int32_t)p.inner_pad};
