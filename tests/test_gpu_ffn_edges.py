@@ -97,3 +97,26 @@ def test_infinities_with_ragged_widths(T, H, F):
     assert (d.dw_gate == inf).all() and (d.dw_up == inf).all() and (d.dw_down[5] == inf).all()
     other = torch.arange(H, device="cuda") != 5
     assert torch.isfinite(d.dw_down[other]).all()
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=["bf16", "f16"])
+@pytest.mark.parametrize("pattern", [0xFFFF, 0x7FFF, None], ids=["FFFF", "7FFF", "inf-inf"])
+@pytest.mark.parametrize("T", [3, 20, 100, 300])
+def test_nans_are_kept_as_such(T, pattern, dt):
+    """What is kept for the gradients of a token of NaNs is NaN, whatever their payload, whether
+    an input's or made by the sums."""
+    H, F = 72, 136
+    x, wg, wu = (torch.ones(r, H, dtype=dt, device="cuda") for r in (T, F, F))
+    if pattern is None:
+        x[1, 4], x[1, 5] = float("inf"), float("-inf")
+    else:
+        x.view(torch.int16)[1] = pattern - 0x10000 if pattern > 0x7FFF else pattern
+    wd = torch.ones(H, F, dtype=dt, device="cuda")
+    f = _ffn(T, H, F, dt)
+    r = f.forward(x, wg, wu, wd, save=True)
+    for t in (*_kept(r.saved), r.saved.h):
+        assert torch.isnan(t[1]).all() and torch.isfinite(t[0]).all()
+    d = f.backward(torch.ones_like(x), x, wg, wu, wd, r.saved)
+    assert torch.isnan(r.y[1]).all() and torch.isnan(d.dx[1]).all()
+    # (token 0's sums are all positive: in fp16 they pass its range, 136 x 2 x 72^2 and more)
+    assert not torch.isnan(r.y[0]).any() and not torch.isnan(d.dx[0]).any()

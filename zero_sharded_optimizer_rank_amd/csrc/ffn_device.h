@@ -22,7 +22,8 @@ inline Kept kept(const FfnPlan& p, void* ws, const zero_ffn_saved_t* s) {
   return Kept{at<uint16_t>(ws, p.h), nullptr, nullptr, nullptr, p.inner_pad};
 }
 
-// Four elements of act(g) and of b as they are kept.
+// Four elements of act(g) and of b as they are kept.  Rounding could only lose a NaN of all
+// ones: an operand's 16 bits and the instructions' own NaNs leave the lower bits zero.
 struct Kept4 {
   u32x2 act, slope, low;
 };
