@@ -91,3 +91,38 @@ def test_a_nan_stays_one(dt, pattern):
         for x, y in ((a.m, b.m), (a.v, b.v)):
             assert torch.equal(x[:au.BLOCK], y[:au.BLOCK])
             assert torch.equal(x[2 * au.BLOCK:], y[2 * au.BLOCK:])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_state_whose_buffers_were_exchanged(bits):
+    """Refused by the list that holds the old ones, and by a new list if they do not fit; copied
+    into, or with fitting buffers and a new list, the run goes on."""
+    from zero_sharded_optimizer_rank_amd.adam import AdamList, AdamState
+    n = 300
+    g = torch.full((n,), 1e-3, device="cuda")
+    w = torch.zeros(n, device="cuda")
+    state = AdamState([n], bits=bits)
+    lst = AdamList([g], [w], state)
+    lst.step(lr=1e-3, step=1)
+    names = ("m", "v") + (("m_exp", "v_exp") if bits == 8 else ())
+    saved = {k: getattr(state, k).cpu() for k in names}
+    at = w.clone()
+    lst.step(lr=1e-3, step=2)
+    want = w.clone()
+    for k in names:
+        getattr(state, k).copy_(saved[k])
+    w.copy_(at)
+    lst.step(lr=1e-3, step=2)
+    assert torch.equal(w, want)
+    state.m = saved["m"]  # on the host
+    with pytest.raises(RuntimeError, match="exchanged"):
+        lst.step(lr=1e-3, step=3)
+    with pytest.raises(RuntimeError, match="exchanged"):
+        lst.moments()
+    with pytest.raises(ValueError, match="the state's m "):
+        AdamList([g], [w], state)
+    for k in names:
+        setattr(state, k, saved[k].cuda())
+    w.copy_(at)
+    AdamList([g], [w], state).step(lr=1e-3, step=2)
+    assert torch.equal(w, want)

@@ -29,7 +29,8 @@ class AdamState:
 
     bits: 32 (m and v are float32) or 8 (m and v are uint8 codes, m_exp and v_exp the exponents
     that 128 neighbouring elements share).  Tensor i's moments start at element offsets[i], a
-    multiple of 128.  Save and load the buffers to save and resume a run.
+    multiple of 128.  Save the buffers to save a run, and copy into them to resume it: a list made
+    of the state holds them where they lie.
     """
 
     def __init__(self, numels: Sequence[int], bits: int = 32, device=None):
@@ -62,6 +63,26 @@ def _each(value, n, what):
     return [float(v) for v in values]
 
 
+MOMENTS = ("m", "v", "m_exp", "v_exp")
+
+
+def _moments_of(state):
+    """The state's buffers, checked: they may have been exchanged since it was made."""
+    block, small = abi.ZERO_ADAM_BLOCK, state.bits == 8
+    blocks = sum(-(-n // block) for n in state.numels)
+    dtype = torch.uint8 if small else torch.float32
+    buffers = tuple(getattr(state, name) for name in MOMENTS)
+    for t, name, count in zip(buffers, MOMENTS, (block * blocks,) * 2 + (blocks,) * 2):
+        if not small and name.endswith("exp"):
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != count \
+                or not t.is_contiguous():
+            raise ValueError(f"the state's {name} must be {count} contiguous elements of {dtype}")
+        if t.device != state.device:
+            raise ValueError(f"the state's {name} is on {t.device}, the state on {state.device}")
+    return buffers
+
+
 def _check_buffers_apart(spans) -> None:
     reach, owner = 0, ""
     for start, end, what in sorted(spans):
@@ -78,7 +99,8 @@ class AdamList:
     any of the three types that receive the new weights, or None.  weight_decay (decoupled) and
     lr_scale (a factor on the step's lr): one number, or one a tensor.  No two buffers may share
     memory.  The list is made for these tensors where they lie, as a ``GradList`` is: gradients
-    that a step makes anew need a new list.  Calls run on the given stream (default: the current
+    that a step makes anew need a new list, and so does a state whose buffers were exchanged
+    (calls refuse it).  Calls run on the given stream (default: the current
     stream of the list's device), which has to wait for the stream that the list was made on, as
     for any tensor; calls on one list must not overlap.  The list has to outlive their work, and
     the graphs that hold them; a graph replays the scalars of the step that it captured.
@@ -130,8 +152,8 @@ class AdamList:
                                 grad_dtype=DTYPES[g.dtype],
                                 param_dtype=abi.ZERO_F32 if p is None else DTYPES[p.dtype],
                                 moment_bits=state.bits))
-        for t, what in ((state.m, "m"), (state.v, "v"), (state.m_exp, "m_exp"),
-                        (state.v_exp, "v_exp")):
+        self._moments = _moments_of(state)
+        for t, what in zip(self._moments, MOMENTS):
             if t is not None:
                 span(t, what)
         _check_buffers_apart(spans)
@@ -145,6 +167,10 @@ class AdamList:
         self._args = abi.step_args(lr=0.0, beta1=0.0, beta2=0.0, eps=0.0, weight_decay=0.0,
                                    max_grad_norm=0.0, loss_scale=1.0, step=1)
 
+    def _check_state(self):
+        if any(getattr(self.state, name) is not t for name, t in zip(MOMENTS, self._moments)):
+            raise RuntimeError("the state's buffers were exchanged: make a new list")
+
     def step(self, *, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
              step: int, loss_scale: float = 1.0, norm: Optional[GradList] = None,
              seed: Optional[int] = None, stream=None) -> None:
@@ -153,6 +179,7 @@ class AdamList:
         norm: the GradList whose last norm gives the clip coefficient, and the skip (nothing is
         written then; the next step has the same number).  seed: 32 bits for the rounding of
         8-bit moments, default the step's number."""
+        self._check_state()
         result = None
         if norm is not None:
             if norm.device != self.device:
@@ -171,6 +198,7 @@ class AdamList:
     def moments(self, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """The values of m and v, flat as in the state: the state's own buffers for 32 bits, for 8
         bits bfloat16 buffers of the list (exact), written again by the next call."""
+        self._check_state()
         if self.state.bits == 32:
             return self.state.m, self.state.v
         handle = stream_of(self.device, stream)
