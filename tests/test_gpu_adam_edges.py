@@ -126,3 +126,30 @@ def test_a_state_whose_buffers_were_exchanged(bits):
     w.copy_(at)
     AdamList([g], [w], state).step(lr=1e-3, step=2)
     assert torch.equal(w, want)
+
+
+def test_moments_first_read_in_a_capture():
+    """The buffers that the captured call makes are not cleared before a replay: an eager call
+    before it finds them as they are, and leaves zeros between the tensors all the same."""
+    from zero_sharded_optimizer_rank_amd.adam import AdamList, AdamState
+    sizes = [130, 5]
+    g = [torch.full((n,), 1e-3, device="cuda") for n in sizes]
+    state = AdamState(sizes, bits=8)
+    lst = AdamList(g, [torch.zeros_like(t) for t in g], state)
+    lst.step(lr=1e-3, step=1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a = lst.moments()
+    for t in a:
+        t.fill_(7.0)
+    want = AdamList(g, [torch.zeros_like(t) for t in g], state).moments()
+    b = lst.moments()
+    for t, w in zip(b, want):
+        assert torch.equal(t, w) and (t[130:256] == 0).all() and (t[261:] == 0).all()
+    for _ in range(2):
+        for t in a:
+            t.fill_(7.0)
+        graph.replay()
+        for t, w in zip(a, want):
+            assert torch.equal(t, w)

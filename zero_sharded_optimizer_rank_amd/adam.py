@@ -162,7 +162,7 @@ class AdamList:
         with on_device(device):
             self.list = abi.zero_tensors_adam_prepare(abi.adam_table(entries), n, self.table, size,
                                                       stream_of(device, None))
-        self._read = None
+        self._read, self._cleared = None, False
         # filled by each step: making it anew would take a third of a short list's time
         self._args = abi.step_args(lr=0.0, beta1=0.0, beta2=0.0, eps=0.0, weight_decay=0.0,
                                    max_grad_norm=0.0, loss_scale=1.0, step=1)
@@ -196,18 +196,23 @@ class AdamList:
             abi.zero_tensors_adam(self.list, args, seed, result, handle)
 
     def moments(self, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
-        """The values of m and v, flat as in the state: the state's own buffers for 32 bits, for 8
-        bits bfloat16 buffers of the list (exact), written again by the next call."""
+        """The values of m and v, flat as in the state, zero between the tensors: the state's own
+        buffers for 32 bits, for 8 bits bfloat16 buffers of the list (exact), written again by the
+        next call."""
         self._check_state()
         if self.state.bits == 32:
             return self.state.m, self.state.v
         handle = stream_of(self.device, stream)
         with on_device(self.device):
-            if self._read is None:
-                # zero between the tensors; the memory is the call's stream's from the start
+            if not self._cleared:
                 with torch.cuda.stream(stream):
-                    self._read = tuple(torch.zeros(self.state.elements, dtype=torch.bfloat16,
-                                                   device=self.device) for _ in range(2))
+                    if self._read is None:  # the memory is the call's stream's from the start
+                        self._read = tuple(torch.empty(self.state.elements, dtype=torch.bfloat16,
+                                                       device=self.device) for _ in range(2))
+                    for t in self._read:
+                        t.zero_()
+                    # (a call that is captured clears them when it is replayed)
+                    self._cleared = not torch.cuda.is_current_stream_capturing()
             m, v = self._read
             abi.zero_tensors_adam_moments(self.list, m, v, abi.ZERO_BF16, handle)
         return m, v
