@@ -120,3 +120,40 @@ def test_nans_are_kept_as_such(T, pattern, dt):
     assert torch.isnan(r.y[1]).all() and torch.isnan(d.dx[1]).all()
     # (token 0's sums are all positive: in fp16 they pass its range, 136 x 2 x 72^2 and more)
     assert not torch.isnan(r.y[0]).any() and not torch.isnan(d.dx[0]).any()
+
+
+@pytest.mark.parametrize("H,F", [(64, 72), (67, 75)])
+def test_a_workspace_is_sized_once(H, F, monkeypatch):
+    """Rows between 16-byte boundaries: the plans of all smaller batches are looked at by the
+    first call for matrices that lie so, not by every call; other matrices' are looked at again."""
+    from zero_sharded_optimizer_rank_amd import abi
+    T, dt = 150, torch.float16
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def odd(r, c, s):
+        return (torch.randn(r, c + 5, generator=g, device="cuda") * s).to(dt)[:, 3:3 + c]
+    x, dy = odd(T, H, 1.0), odd(T, H, 0.05)
+    wg, wu, wd = odd(F, H, H ** -0.5), odd(F, H, H ** -0.5), odd(H, F, F ** -0.5)
+    f = _ffn(T, H, F, dt)
+    calls, real = [], abi.zero_ffn_workspace_bytes
+
+    def counted(*a):
+        calls.append(a)
+        return real(*a)
+    monkeypatch.setattr(abi, "zero_ffn_workspace_bytes", counted)
+    outs = []
+    for t in (150, 30, 150):
+        before = len(calls)
+        r = f.forward(x[:t], wg, wu, wd, save=True)
+        d = f.backward(dy[:t], x[:t], wg, wu, wd, r.saved)
+        outs.append([a.clone() for a in (r.y, *d)])
+        assert (len(calls) > before) == (len(outs) == 1)
+    for a, b in zip(outs[0], outs[2]):
+        assert torch.equal(a, b)
+    before = len(calls)
+    whole = torch.zeros(T, (H + 7) // 8 * 8, dtype=dt, device="cuda")[:, :H]
+    whole.copy_(x)
+    y = f.forward(whole, wg, wu, wd).y
+    assert len(calls) > before and torch.equal(y, outs[0][0])
+    ref = fu.reference(x, wg, wu, wd, "silu", dy)
+    fu.check(y, *ref["y"], "y")

@@ -78,6 +78,7 @@ class GatedFFN:
         self._saved = self.new_saved() if grad else None
         self._dx = torch.empty(tokens, hidden, dtype=dtype, device=dev) if grad else None
         self._dw = {}  # made by the first backward that is not given one
+        self._needs = {}  # workspace by the matrices whose rows lie between 16-byte boundaries
 
     def _sizes(self, tokens):
         h, f = self.hidden, self.inner
@@ -142,16 +143,20 @@ class GatedFFN:
 
     def _workspace(self, ffn, grads, stream):
         # rows that do not start on 16-byte boundaries take copies in the workspace
-        parts = [ffn.x, ffn.w_gate, ffn.w_up, ffn.w_down, 2 * ffn.ldx, 2 * ffn.ld_gate,
-                 2 * ffn.ld_up, 2 * ffn.ld_down, 2 * self.hidden, 2 * self.inner]
+        rows = [(ffn.x, ffn.ldx), (ffn.w_gate, ffn.ld_gate), (ffn.w_up, ffn.ld_up),
+                (ffn.w_down, ffn.ld_down)]
         if grads is not None:
-            parts += [grads.dy, 2 * grads.lddy]
-        if any((p or 0) % 16 for p in parts):  # (an empty batch has no address)
+            rows.append((grads.dy, grads.lddy))
+        # (an empty batch has no address)
+        lies = tuple([((p or 0) | 2 * ld) % 16 != 0 for p, ld in rows])
+        if any(lies):
             # grown for every later batch that lies so; graphs captured before hold the old
             # one's address, so that stays too
-            full = abi.zero_ffn_t.from_buffer_copy(ffn)
-            full.tokens = self.tokens
-            need = self._need(full, grads is not None, grads)
+            need = self._needs.get(lies)
+            if need is None:  # sized once: all smaller batches are looked at
+                full = abi.zero_ffn_t.from_buffer_copy(ffn)
+                full.tokens = self.tokens
+                need = self._needs[lies] = self._need(full, grads is not None, grads)
             if need > self.ws.numel():
                 self._old_ws = getattr(self, "_old_ws", []) + [self.ws]
                 with torch.cuda.stream(stream):  # the memory is the call's stream's from the start
