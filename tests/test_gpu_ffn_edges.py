@@ -157,3 +157,28 @@ def test_a_workspace_is_sized_once(H, F, monkeypatch):
     assert len(calls) > before and torch.equal(y, outs[0][0])
     ref = fu.reference(x, wg, wu, wd, "silu", dy)
     fu.check(y, *ref["y"], "y")
+
+
+def test_kept_values_are_made_when_they_are_asked_for():
+    """A block whose calls bring their own buffers for the kept values makes none; one that is made
+    for gradients keeps them in its own from the first save=True on."""
+    T, H, F, dt = 512, 64, 4096, torch.bfloat16
+    each = 4 * T * F * dt.itemsize
+    x, wg, wu, wd = (torch.full(s, 0.01, dtype=dt, device="cuda")
+                     for s in ((T, H), (F, H), (F, H), (H, F)))
+    before = torch.cuda.memory_allocated()
+    f = _ffn(T, H, F, dt)
+    # without its workspace: y and dx, each 64 KiB
+    assert torch.cuda.memory_allocated() - before - f.ws.numel() < each // 8
+    own = f.new_saved()
+    before = torch.cuda.memory_allocated()
+    f.forward(x, wg, wu, wd)
+    assert f.forward(x, wg, wu, wd, save=own).saved is own
+    assert torch.cuda.memory_allocated() == before
+    a = f.forward(x, wg, wu, wd, save=True).saved
+    b = f.forward(x[:9], wg, wu, wd, save=True).saved
+    assert torch.cuda.memory_allocated() == before + each
+    for s, t, o in zip(a, b, own):
+        assert s.data_ptr() == t.data_ptr() != o.data_ptr() and t.shape[0] == 9
+    with pytest.raises(ValueError, match="grad=False"):
+        _ffn(T, H, F, dt, grad=False).forward(x, wg, wu, wd, save=True)

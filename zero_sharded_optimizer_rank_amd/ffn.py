@@ -75,7 +75,7 @@ class GatedFFN:
         dev = self.device
         self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
         self._y = torch.empty(tokens, hidden, dtype=dtype, device=dev)
-        self._saved = self.new_saved() if grad else None
+        self._saved = None  # made by the first save=True: 8 bytes an element of tokens x inner
         self._dx = torch.empty(tokens, hidden, dtype=dtype, device=dev) if grad else None
         self._dw = {}  # made by the first backward that is not given one
         self._needs = {}  # workspace by the matrices whose rows lie between 16-byte boundaries
@@ -169,13 +169,16 @@ class GatedFFN:
         t = ffn.tokens
         y = self._y[:t] if y is None else y
         ldy = self._matrix(y, t, self.hidden, "y")
+        handle = stream_of(self.device, stream)
         saved = saved_t = None
         if save is not False and save is not None:
-            if save is True and self._saved is None:
+            if save is True and not self.has_grad:
                 raise ValueError("the block was made with grad=False")
+            if save is True and self._saved is None:
+                with torch.cuda.stream(stream):  # as a grown workspace
+                    self._saved = self.new_saved()
             saved = FFNSaved(*(b[:t] for b in self._saved)) if save is True else save
             saved_t = self._saved_t(saved, t)
-        handle = stream_of(self.device, stream)
         with on_device(self.device):
             ws = self._workspace(ffn, None, stream)
             abi.zero_ffn_forward(ffn, y, ldy, saved_t, ws, ws.numel(), handle)
