@@ -1,5 +1,7 @@
 """The gated feed-forward block where values leave the ordinary range: NaNs and infinities, huge
 arguments of the activations."""
+import warnings
+
 import pytest
 
 import ffn_util as fu
@@ -182,3 +184,25 @@ def test_kept_values_are_made_when_they_are_asked_for():
         assert s.data_ptr() == t.data_ptr() != o.data_ptr() and t.shape[0] == 9
     with pytest.raises(ValueError, match="grad=False"):
         _ffn(T, H, F, dt, grad=False).forward(x, wg, wu, wd, save=True)
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_inputs_that_require_gradients(which):
+    """The outputs carry no graph, and where autograd would have made one that is said."""
+    T, H, F, dt = 5, 64, 72, torch.bfloat16
+    t = [torch.full(s, 0.1, dtype=dt, device="cuda") for s in ((T, H), (F, H), (F, H), (H, F))]
+    f = _ffn(T, H, F, dt)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        want = f.forward(*t, save=True)
+        y = want.y.clone()
+        t[which].requires_grad_()
+        with torch.no_grad():
+            assert torch.equal(f.forward(*t, save=True).y, y)
+    with pytest.warns(UserWarning, match="autograd does not record"):
+        r = f.forward(*t, save=True)
+    assert torch.equal(r.y, y) and not r.y.requires_grad
+    with warnings.catch_warnings():  # the call for the gradients says nothing
+        warnings.simplefilter("error")
+        d = f.backward(torch.ones(T, H, dtype=dt, device="cuda"), *t, r.saved)
+    assert not any(a.requires_grad for a in d)

@@ -7,6 +7,7 @@ caller's, so that one serves all layers.
 """
 from __future__ import annotations
 
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -51,7 +52,9 @@ class GatedFFN:
     buffers, which the next call writes again.  Calls run on the given stream (default: the
     current stream of the device), which has to wait for the stream that the block was made on, as
     for any tensor, and must not overlap on one block.  The block has to outlive the work of its
-    calls, and the graphs that hold them.
+    calls, and the graphs that hold them.  Outputs carry no autograd graph: the gradients are what
+    ``backward`` returns, and a forward pass of inputs that require gradients warns where autograd
+    is on.
     """
 
     def __init__(self, tokens: int, hidden: int, inner: int, dtype: torch.dtype,
@@ -166,6 +169,10 @@ class GatedFFN:
     def forward(self, x, w_gate, w_up, w_down, y=None, save=False, stream=None) -> FFNOut:
         """The block's output; save=True, or an FFNSaved, keeps what ``backward`` needs."""
         ffn = self._ffn(x, w_gate, w_up, w_down)
+        if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad
+                                        or w_up.requires_grad or w_down.requires_grad):
+            warnings.warn("autograd does not record the block: call its backward (under "
+                          "torch.no_grad() this is not said)", stacklevel=2)
         t = ffn.tokens
         y = self._y[:t] if y is None else y
         ldy = self._matrix(y, t, self.hidden, "y")
