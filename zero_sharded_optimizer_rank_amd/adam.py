@@ -168,7 +168,8 @@ class AdamList:
                                    max_grad_norm=0.0, loss_scale=1.0, step=1)
 
     def _check_state(self):
-        if any(getattr(self.state, name) is not t for name, t in zip(MOMENTS, self._moments)):
+        s, (m, v, m_exp, v_exp) = self.state, self._moments
+        if s.m is not m or s.v is not v or s.m_exp is not m_exp or s.v_exp is not v_exp:
             raise RuntimeError("the state's buffers were exchanged: make a new list")
 
     def step(self, *, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
