@@ -759,6 +759,8 @@ int zero_tensors_adam_prepare(const zero_adam_tensor_t* tensors, int32_t n_tenso
  *   r = mix(mix(mix(mix(seed) + t) + (i >> 12)) + (i & 4095)), u = r & 0xFFFF for m,
  *   r >> 16 for v;
  *   mix(x): x ^= x >> 16; x *= 0x7FEB352D; x ^= x >> 15; x *= 0x846CA68B; x ^= x >> 16
+ * A captured call repeats its args and its seed at every replay: the bias correction of
+ * one step, and the same random bits for every element.
  * The parameter is updated from the moments before they are rounded; there, where the
  * moments keep 3 bits, the root and the two quotients are those of the instructions (one
  * unit in the last place each, the first quotient as a product with the reciprocal).
@@ -895,10 +897,11 @@ int zero_head_loss_grad(const zero_head_t* head, float* token_loss, float* lse,
  *   dh = dy Wd,  du = dh act(g),  dg = dh u act'(g)
  *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h
  * Sums are fp32.  h, dg and du are rounded once to the 16-bit type (the matrix cores
- * multiply it); in fp16 what passes 65504 becomes infinite.  For up to 16 tokens (and
- * hidden, inner >= 8) the forward pass multiplies h in two 16-bit parts, so that its
- * rounding does not reach y.  Gradients carry whatever loss scale dy carries.  Equal
- * inputs give equal bits; a token's y may depend on how many tokens share the call. */
+ * multiply it); in fp16 what passes 65504 becomes infinite, and what lies below 2^-14
+ * keeps steps of 2^-24.  For up to 16 tokens (and hidden, inner >= 8) the forward pass
+ * multiplies h in two 16-bit parts, so that its rounding does not reach y.  Gradients
+ * carry whatever loss scale dy carries; in fp16 it has to hold dg and du in that range.
+ * Equal inputs give equal bits; a token's y may depend on how many tokens share the call. */
 
 enum zero_act {
   ZERO_ACT_SILU = 0,      /* g / (1 + e^-g) */

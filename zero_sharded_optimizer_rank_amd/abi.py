@@ -105,8 +105,8 @@ class zero_adam_tensor_t(ctypes.Structure):
 
 class zero_adam_list_t(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("blocks32", ctypes.c_int64),
-                ("blocks8", ctypes.c_int64), ("elements", ctypes.c_int64), ("n_tensors", ctypes.c_int32),
-                ("reserved", ctypes.c_int32)]
+                ("blocks8", ctypes.c_int64), ("elements", ctypes.c_int64),
+                ("n_tensors", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class zero_head_t(ctypes.Structure):

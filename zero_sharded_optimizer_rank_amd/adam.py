@@ -103,7 +103,9 @@ class AdamList:
     (calls refuse it).  Calls run on the given stream (default: the current
     stream of the list's device), which has to wait for the stream that the list was made on, as
     for any tensor; calls on one list must not overlap.  The list has to outlive their work, and
-    the graphs that hold them; a graph replays the scalars of the step that it captured.
+    the graphs that hold them.  A graph replays the scalars of the step that it captured, its bias
+    correction, rate and seed: 8-bit moments are rounded by the same random bits each time, so a
+    run of many steps calls ``step`` and does not replay one.
     """
 
     def __init__(self, grads: Sequence[torch.Tensor], masters: Sequence[torch.Tensor],

@@ -154,9 +154,10 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
   // Small tiles where the large ones would leave half of the CUs idle (100 x 4096 x 14336,
   // 112 tiles, forward 130 -> 107 us; 1024 x 1600 x 6400, 200 tiles, 88 -> 100), in a
   // backward pass also where a CU's share is short, so that a tile's start and end weigh
-  // (300 x 1600 x 6400, training 194 -> 165 us; 512 x 4096 x 14336 563 -> 654), and for y and
-  // the second backward launch of up to one small tile's tokens (100 x 4096 x 14336, training
-  // 318 -> 304 us, 200 x 4096 x 14336 422 -> 464; 64 x 8192 x 28672 1013 -> 1011).
+  // (300 x 1600 x 6400, training, first launch 168 -> 145 us, second 149 -> 144; 512 x 4096 x
+  // 14336 587 -> 607 and 588 -> 706), and for y and the second backward launch of up to one
+  // small tile's tokens (y: 100 x 4096 x 14336, forward 111 -> 107, 200 x 4096 x 14336 135 ->
+  // 143; training 318 -> 304 and 426 -> 470; 64 x 8192 x 28672 1005 -> 1007).
   const auto all = [](const Work& w) { return w.count * w.stages; };
   Work in = work(2 * F, T, H, false), dh = work(F, T, H, false), dw = work(F, H, T, false);
   Work dx = work(T, H, 2 * F, false);
@@ -191,11 +192,18 @@ FfnPlan ffn_plan(const zero_ffn_t* f, const zero_ffn_grads_t* g) {
     // 8192 32 and 39 us a forward pass, 4096 x 11008 81 and 63, 8192 x 22016 208 and 232).
     const auto rounds = [&](int64_t sets) { return tiles(tiles(F, 16 * sets), 256) * sets; };
     p.few_sets_in = rounds(2) < rounds(4) ? 2 : 4;
+    // Sets of the second: four where its rows are many, so that h is fetched half as often (40
+    // and 60 tokens, two and four sets: 8192 x 28672 278 and 270, 303 and 287 us a forward
+    // pass; 4096 x 14336 79 and 79, 87 and 85; 2048 x 8192 37 and 38, 41 and 41); with fewer
+    // rows either is ahead by a few percent (1024 x 4096 23.5 and 24.4, 26.2 and 26.0; 1600 x
+    // 6400 36.2 and 35.4, 39.5 and 38.3; 768 x 2048 22.3 and 22.4, 24.8 and 24.0).
     p.few_sets_out = H >= 2048 ? 4 : 2;
     // Up to 8 tokens' x and h come from the L2 as fast, and the waves need not wait for one
     // another, unless the products are large and the tokens more than 4 (8 tokens, not
-    // shared and shared: 768 x 2048 13 and 20 us, 4096 x 8192 48 and 60, 4096 x 14336 78 and
-    // 69, 8192 x 28672 288 and 260; 4 tokens there 75 and 73, 265 and 261).
+    // shared and shared: 768 x 2048 13 and 20 us, 4096 x 8192 49 and 58, 4096 x 14336 82 and
+    // 72, 8192 x 28672 284 and 258).  Up to 4 tokens never: one token 71 and 72 at 4096 x 14336,
+    // 248 and 259 at 8192 x 28672; at four the 3% of 4096 x 14336 (74.5 and 72.5; 8192 x 28672
+    // 258 and 258, 4096 x 11008 60 and 63) are left for the simpler rule.
     if (T <= 4 || (T <= 8 && (H < 2048 || F <= 8192)))
       p.few_sets_in = p.few_sets_out = 1;
     if (p.few_sets_out > 1) {

@@ -262,8 +262,8 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void k_ffn_in(Matrix x, Matrix w
   }
 }
 
-// The same from the parts' sums, four columns a thread: bound by memory (387 tokens, 272
-// inner columns: 6 us, mostly its launch).
+// The same from the parts' sums, four columns a thread: bound by memory (387 tokens of
+// 4096 x 272, 16 parts: 6.5 us, mostly its launch).
 template <typename T, int ACT>
 __global__ __launch_bounds__(kPackThreads) void k_ffn_in_join(Parts parts, int32_t tokens,
                                                               int32_t inner, int32_t inner_pad,
@@ -338,13 +338,13 @@ __device__ __forceinline__ void out_tile(uint32_t block, const OutArgs& o) {
 }
 
 // y.  One product of T x hidden tiles: few, so its contraction, the longest, is often cut
-// into parts (512 tokens of 4099 x 14339: 32 tiles in 6 parts, 99 us, 0.61 PFLOP/s).
+// into parts (512 tokens of 4099 x 14339: 34 tiles in 5 parts, 101 us, 0.59 PFLOP/s).
 template <typename T, bool SMALL>
 __global__ __launch_bounds__(SMALL ? 256 : 512) void k_ffn_out(OutArgs o) {
   out_tile<T, false, SMALL>(blockIdx.x, o);
 }
 
-// y or dx from the parts' sums, four columns a thread: bound by memory (1024 x 1600, 7 and 4
+// y or dx from the parts' sums, four columns a thread: bound by memory (1024 x 1600, 6 and 4
 // parts: 6.6 us, 5.5 TB/s).
 template <typename T>
 __global__ __launch_bounds__(kPackThreads) void k_ffn_out_join(Parts parts, int32_t tokens,
@@ -464,8 +464,8 @@ __device__ __forceinline__ void dh_tile(uint32_t block, const DhArgs& a) {
   leave(a.du);
 }
 
-// The same from the parts' sums, four columns a thread: bound by memory (64 tokens, 14336
-// inner columns: 5 us).
+// The same from the parts' sums, four columns a thread: bound by memory (64 tokens of
+// 4096 x 14336, 2 parts: 5 us).
 template <typename T>
 __global__ __launch_bounds__(kPackThreads) void k_ffn_dh_join(DhArgs a) {
   const int64_t q = (int64_t)blockIdx.x * kPackThreads + threadIdx.x;
@@ -561,7 +561,8 @@ __device__ __forceinline__ void dw_tile(uint32_t block, const WeightGrad& w) {
 
 // The same from the parts' sums, four columns a thread, bound by memory; the second
 // weight's workgroups, if it has any, start at b.first.  For many tokens of narrow blocks
-// only: their weights' tiles are few and the contraction, the tokens, long.
+// only: their weights' tiles are few and the contraction, the tokens, long (2000 tokens of
+// 24 x 40, 8 parts: 3 us, its launch).
 template <typename T, bool F32OUT>
 __global__ __launch_bounds__(kPackThreads) void k_ffn_dw_join(WeightGrad a, WeightGrad b) {
   const bool second = blockIdx.x >= b.first;

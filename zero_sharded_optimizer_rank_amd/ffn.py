@@ -195,8 +195,10 @@ class GatedFFN:
                  dw_up=None, dw_down=None, accumulate: bool = False, need_dx: bool = True,
                  need_dw: bool = True, stream=None) -> FFNGrads:
         """The gradients, from what ``forward`` kept for the same x and weights.  They carry the
-        loss scale that dy carries.  dw_* may be given, all of one type, the block's or float32
-        (e.g. pieces of a flat contribution row); accumulate adds to them."""
+        loss scale that dy carries; in float16 it has to hold them, and the gradients of both
+        projections, between 2^-14 (below, steps are 2^-24) and 65504.  dw_* may be given, all of
+        one type, the block's or float32 (e.g. pieces of a flat contribution row); accumulate adds
+        to them."""
         if not self.has_grad:
             raise ValueError("the block was made with grad=False")
         ffn = self._ffn(x, w_gate, w_up, w_down)
