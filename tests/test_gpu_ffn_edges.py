@@ -206,3 +206,36 @@ def test_inputs_that_require_gradients(which):
         warnings.simplefilter("error")
         d = f.backward(torch.ones(T, H, dtype=dt, device="cuda"), *t, r.saved)
     assert not any(a.requires_grad for a in d)
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=["bf16", "f16"])
+@pytest.mark.parametrize("T,H,F", [(1, 64, 72), (5, 64, 203), (8, 2056, 8200), (9, 64, 72),
+                                   (12, 72, 4099), (16, 2051, 1003), (17, 64, 72), (100, 64, 203)])
+def test_infinite_down_weights(T, H, F, dt):
+    """One weight of w_down is infinite: its row's outputs are h times it, infinities, whether h
+    takes part in one piece or in two of which the second may be zero; the others stay."""
+    gen = torch.Generator(device="cuda").manual_seed(0)
+
+    def normal(rows, cols, s):
+        return (torch.randn(rows, cols, generator=gen, device="cuda") * s).to(dt)
+    x, wg, wu, wd = (normal(T, H, 1.0), normal(F, H, H ** -0.5), normal(F, H, H ** -0.5),
+                     normal(H, F, F ** -0.5))
+    f0, rows = F - 3, [3, H - 1]
+    wg[f0], wu[f0] = 1.0 / H, 0.0
+    wu[f0, 0] = 1.0
+    x[:, 0] = torch.where(x[:, 0] < 0, -1.0, 1.0).to(dt)  # h[:, f0] is act(g) or its negative
+    x[:, 1:] = x[:, 1:].abs()
+    x[0] = 1.0  # h[0, f0] = act(1): exactly known to neither piece
+    f = _ffn(T, H, F, dt, act="relu")
+    y = f.forward(x, wg, wu, wd).y.clone()
+    for value in (float("inf"), float("-inf")):
+        bad = wd.clone()
+        bad[rows, f0] = value
+        got = f.forward(x, wg, wu, bad).y
+        g = x.double() @ wg[f0].double()
+        h = torch.clamp(g, min=0) * x[:, 0].double()
+        assert (h.abs() > 0.1).all()
+        for r in rows:
+            assert torch.equal(got[:, r].double(), h * value)
+        keep = [r for r in range(H) if r not in rows]
+        assert torch.equal(got[:, keep], y[:, keep])

@@ -115,6 +115,11 @@ __device__ __forceinline__ void leave_pair(const Few& a, A act, f32x4 g, f32x4 u
     *(u32x2*)(a.to.low + at) = k.low;
   }
 }
+// Sums over h's two parts.  Where an infinite weight meets a second part of zero that sum
+// is NaN; the first part's is what h gives there.
+__device__ __forceinline__ float both(float s, float low) {
+  return __builtin_fabsf(s) < __builtin_inff() ? s + low : s;
+}
 // Four columns of an output row that holds n.
 template <typename T>
 __device__ __forceinline__ void leave4(uint16_t* row, int32_t r, int32_t n, f32x4 s) {
@@ -230,8 +235,8 @@ k_ffn_direct(const Few a) {
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)  // lane q + 8's
-      acc[0][e] += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
-          0, (int)__float_as_uint(acc[0][e]), 0x128, 0xF, 0xF, false));
+      acc[0][e] = both(acc[0][e], __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+                                      0, (int)__float_as_uint(acc[0][e]), 0x128, 0xF, 0xF, false)));
     if (q < a.tokens && r < a.rows) leave4<T>(a.out + q * a.ldo, r, a.rows, acc[0]);
   }
 }
@@ -280,6 +285,7 @@ k_ffn_shared(const Few a) {
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{};
+  f32x4 low[LOW ? NI : 1][LOW ? NJ : 1] = {};  // the second part's
   // [rows][line][rows 0-7 or 8-15]
   s16x8 w[2][NI][2][2], x[2][XLOADS];
   auto fetch_w = [&](s16x8 (&d)[NI][2][2], int32_t tile) {
@@ -325,11 +331,14 @@ k_ffn_shared(const Few a) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-          for (int rows = 0; rows < XROWS; rows += 16 * NJ) {
-            const s16x8 b =
-                *(const s16x8*)(l + (rows + 16 * j + q) * 256 + (((8 * n + 4 * s + g) ^ q) << 4));
+          for (int part = 0; part < (LOW ? 2 : 1); ++part) {
+            const int row = 16 * (part * NJ + j) + q;
+            const s16x8 b = *(const s16x8*)(l + row * 256 + (((8 * n + 4 * s + g) ^ q) << 4));
 #pragma unroll
-            for (int i = 0; i < NI; ++i) acc[i][j] = mfma(T{}, f[i][s], b, acc[i][j]);
+            for (int i = 0; i < NI; ++i) {
+              f32x4& sum = part ? low[LOW ? i : 0][LOW ? j : 0] : acc[i][j];
+              sum = mfma(T{}, f[i][s], b, sum);
+            }
           }
         }
     }
@@ -373,6 +382,14 @@ k_ffn_shared(const Few a) {
     store_x(x[0], lx, tile(t + 2));
     fetch_x(x[0], tile(t + 4));
     if (place(t + 1) < own) use(w[1], lx + kTileBytes, tile(t + 1));
+  }
+  if constexpr (LOW) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = both(acc[i][j][e], low[i][j][e]);
   }
   // The slices' sums, in their order; each wave of a set finishes some of its blocks (50
   // tokens, 72 x 200: 17.8 us a forward pass where the first slice did it all, 16.7 so).
